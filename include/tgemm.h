@@ -60,6 +60,13 @@ typedef enum tgemm_op {
     TGEMM_OP_T = 1  /* op(X) = Xᵀ */
 } tgemm_op_t;
 
+/* Element types of the loss operators' operands. */
+typedef enum tgemm_dtype {
+    TGEMM_F32 = 0,
+    TGEMM_BF16 = 1,
+    TGEMM_F16 = 2
+} tgemm_dtype_t;
+
 typedef enum tgemm_status {
     TGEMM_SUCCESS = 0,
     TGEMM_ERROR_INVALID_VALUE = 1, /* bad size, leading dimension, pointer or overlap, or an
@@ -340,6 +347,113 @@ tgemm_status_t tgemm_sgemm_host(int64_t M, int64_t N, int64_t K,
 /* Device workspace bytes tgemm_sgemm_host needs; 0 if it needs none (M, N or
  * K zero); -1 for invalid sizes or a negative panel_rows. */
 int64_t tgemm_sgemm_host_workspace_size(int64_t M, int64_t N, int64_t K, int64_t panel_rows);
+
+/*
+ * Losses on the product Z = X·Wᵀ of an output head, without Z
+ * -----------------------------------------------------------
+ * X is T×D (a row a token's hidden state), W is V×D (a row a word of the
+ * vocabulary), both row-major with leading dimensions ldx, ldw >= D in
+ * elements, of type `dtype` (both the same).  Z is T×V and read by nothing but
+ * the loss; it is formed tile by tile in registers, reduced there to a maximum
+ * and a sum of exponentials a row, and formed again in the backward pass, a
+ * piece of the vocabulary at a time.
+ *
+ * Types       dtype float32, bf16 or fp16: the type of X, W and their
+ *             gradients.  Products of 16-bit values are exact and summed in
+ *             float32.  A float32 operand is split into three bf16 planes (24
+ *             bits) and the six products of planes that reach 2^-24 of the
+ *             largest are summed in float32; in X and W an infinity gives NaN
+ *             there.  Row statistics, losses and the sums over pieces are
+ *             float32.  The logits' gradient is rounded to the operands' type
+ *             (float32: to three planes) before the two gradient products.
+ * Sizes       0 <= T < 2^24, 1 <= V <= 2^24, 1 <= D <= 2^22, 1 <= K <= 1024,
+ *             leading dimensions up to 2^40; larger ones, and an unknown
+ *             dtype: TGEMM_ERROR_NOT_SUPPORTED.  T = 0: nothing but `summary`
+ *             and a zero dW is written.
+ * Workspace   Device memory of the caller, 16-byte aligned, at least
+ *             tgemm_linear_loss_workspace_size(...) bytes for the same
+ *             arguments, overlapping none of the others.  Its contents on
+ *             entry do not matter and on return are unspecified.  Two calls in
+ *             flight at once need two.
+ * Errors      As above, before anything is queued; also
+ *             TGEMM_ERROR_INVALID_VALUE for a missing, misaligned, overlapping
+ *             or too small workspace, an output that overlaps an input or
+ *             another output, a misaligned or missing array, a negative
+ *             grad_step, a temperature that is not positive and finite.
+ * Indices     An index out of [0, V) is never used as an address: its row's
+ *             loss is NaN, and so are its row of dX and all of dW.
+ * Rows        A row that does not count (its target is ignore_index, or all of
+ *             its teacher logits are -infinity) has the loss 0, a zero row of
+ *             dX and no part in dW, whatever X holds there.
+ * Order       Sums are taken in a fixed order: the same call gives the same
+ *             bits.  Every call can be captured into a graph.
+ *
+ * lse[t] = log sum_v exp(z_tv / temperature) (temperature 1 for cross entropy).
+ * summary (NULL, or three floats): the sum of the losses, their mean over the
+ * rows that count, and 1 / the number of those rows; 0, 0 and 1 if none does.
+ *
+ * Backward: dX (T×D, lddx >= D) and dW (V×D, lddw >= D) = the gradients of
+ * sum_t g_t·loss_t, with g_t = grad_loss[t·grad_step]·grad_weight[0]
+ * (grad_step 0: one value for every row; grad_weight NULL: 1; `summary + 2`
+ * there gives the gradient of the mean).  Either of dX and dW may be NULL and
+ * is then not computed.  lse and student are those of the forward call.
+ */
+
+/* Bytes of workspace of a forward (backward_pass 0) or backward (1) call with
+ * these arguments; teacher_k: K, or 0 for cross entropy.  0 if T is 0 or the
+ * arguments are refused. */
+size_t tgemm_linear_loss_workspace_size(tgemm_dtype_t dtype, int64_t T, int64_t V, int64_t D,
+                                        const void *X, int64_t ldx,
+                                        const void *W, int64_t ldw,
+                                        int64_t teacher_k, int backward_pass);
+
+/* Softmax cross entropy: loss[t] = lse[t] - z_t,target[t]. */
+tgemm_status_t tgemm_linear_ce_forward(tgemm_dtype_t dtype, int64_t T, int64_t V, int64_t D,
+                                       const void *X, int64_t ldx,
+                                       const void *W, int64_t ldw,
+                                       const int64_t *target, int64_t ignore_index,
+                                       float *loss, float *lse, float *summary,
+                                       void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+tgemm_status_t tgemm_linear_ce_backward(tgemm_dtype_t dtype, int64_t T, int64_t V, int64_t D,
+                                        const void *X, int64_t ldx,
+                                        const void *W, int64_t ldw,
+                                        const int64_t *target, int64_t ignore_index,
+                                        const float *lse,
+                                        const float *grad_loss, int64_t grad_step, const float *grad_weight,
+                                        void *dX, int64_t lddx, void *dW, int64_t lddw,
+                                        void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Distillation from a teacher's top logits.  teacher_ids (T×K, leading
+ * dimension ld_ids >= K) and teacher_logits (T×K of teacher_dtype, ld_logits
+ * >= K) hold a row's K words and the teacher's logits of them; an entry with
+ * the logit -infinity is absent, whatever its id.  With q_t the softmax of the
+ * row's logits / temperature over its entries (an id that comes twice holds
+ * the sum of both), and z the student's logits / temperature,
+ *   loss[t] = temperature²·sum_k q_tk·(log q_tk - (z_t,id - lse[t])),
+ * the Kullback-Leibler divergence from the student's whole vocabulary to q.
+ * student[t·K + k] receives z_t,id (0 for an absent entry).
+ */
+tgemm_status_t tgemm_linear_kd_forward(tgemm_dtype_t dtype, int64_t T, int64_t V, int64_t D,
+                                       const void *X, int64_t ldx,
+                                       const void *W, int64_t ldw,
+                                       int64_t K, const int64_t *teacher_ids, int64_t ld_ids,
+                                       tgemm_dtype_t teacher_dtype, const void *teacher_logits, int64_t ld_logits,
+                                       float temperature,
+                                       float *loss, float *lse, float *student, float *summary,
+                                       void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+tgemm_status_t tgemm_linear_kd_backward(tgemm_dtype_t dtype, int64_t T, int64_t V, int64_t D,
+                                        const void *X, int64_t ldx,
+                                        const void *W, int64_t ldw,
+                                        int64_t K, const int64_t *teacher_ids, int64_t ld_ids,
+                                        tgemm_dtype_t teacher_dtype, const void *teacher_logits, int64_t ld_logits,
+                                        float temperature,
+                                        const float *lse, const float *student,
+                                        const float *grad_loss, int64_t grad_step, const float *grad_weight,
+                                        void *dX, int64_t lddx, void *dW, int64_t lddw,
+                                        void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* Static, human-readable text for a status code. */
 const char *tgemm_status_string(tgemm_status_t status);

@@ -37,6 +37,14 @@ from ._lib import (  # noqa: F401
     tgemm_sgemm_simt,
     tgemm_sgemm_host,
     tgemm_sgemm_host_workspace_size,
+    tgemm_linear_ce_backward,
+    tgemm_linear_ce_forward,
+    tgemm_linear_kd_backward,
+    tgemm_linear_kd_forward,
+    tgemm_linear_loss_workspace_size,
+    TGEMM_BF16,
+    TGEMM_F16,
+    TGEMM_F32,
     tgemm_sgemm_splitk,
     tgemm_sgemm_splitk_ex,
     tgemm_sgemm_splitk_choose,
@@ -47,6 +55,15 @@ from ._lib import (  # noqa: F401
     tgemm_status_string,
     tgemm_transpose,
     tgemm_version,
+)
+
+from .linear_loss import (  # noqa: F401
+    linear_cross_entropy,
+    linear_cross_entropy_backward,
+    linear_cross_entropy_forward,
+    linear_distillation,
+    linear_distillation_backward,
+    linear_distillation_forward,
 )
 
 KERNELS = ("auto", "mfma", "naive", "lds", "simt")

@@ -32,6 +32,15 @@ TGEMM_TRANSPOSE_BLOCKED = 0
 TGEMM_TRANSPOSE_NAIVE = 1
 TGEMM_TRANSPOSE_TILED = 2
 TGEMM_TRANSPOSE_TILED_PADDED = 3
+# tgemm_dtype_t values
+TGEMM_F32 = 0
+TGEMM_BF16 = 1
+TGEMM_F16 = 2
+
+_HEAD = [ctypes.c_int, _i64, _i64, _i64, _ptr, _i64, _ptr, _i64]  # dtype, T, V, D, X, ldx, W, ldw
+_TEACHER = [_i64, _ptr, _i64, ctypes.c_int, _ptr, _i64, ctypes.c_float]
+_GRADS = [_ptr, _i64, _ptr, _ptr, _i64, _ptr, _i64]  # grad_loss, grad_step, grad_weight, dX, lddx, dW, lddw
+_ROOM = [_ptr, ctypes.c_size_t, _ptr]  # workspace, its bytes, stream
 
 SIGNATURES = {
     "tgemm_sgemm": (ctypes.c_int, _GEMM + [_ptr]),
@@ -54,6 +63,11 @@ SIGNATURES = {
     "tgemm_sgemm_splitk_noalloc": (ctypes.c_int, [ctypes.c_int, ctypes.c_int] + _GEMM + [ctypes.c_int, _ptr]),
     "tgemm_sgemm_splitk_workspace_size": (ctypes.c_size_t, [_i64, _i64, _i64, ctypes.c_int]),
     "tgemm_sgemm_splitk_choose": (ctypes.c_int, [_i64, _i64, _i64]),
+    "tgemm_linear_loss_workspace_size": (ctypes.c_size_t, _HEAD + [_i64, ctypes.c_int]),
+    "tgemm_linear_ce_forward": (ctypes.c_int, _HEAD + [_ptr, _i64] + [_ptr] * 3 + _ROOM),
+    "tgemm_linear_ce_backward": (ctypes.c_int, _HEAD + [_ptr, _i64, _ptr] + _GRADS + _ROOM),
+    "tgemm_linear_kd_forward": (ctypes.c_int, _HEAD + _TEACHER + [_ptr] * 4 + _ROOM),
+    "tgemm_linear_kd_backward": (ctypes.c_int, _HEAD + _TEACHER + [_ptr] * 2 + _GRADS + _ROOM),
     "tgemm_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "tgemm_version": (ctypes.c_int, []),
 }
@@ -153,6 +167,40 @@ def tgemm_sgemm_splitk_workspace_size(M, N, K, splits) -> int:
 
 def tgemm_sgemm_splitk_choose(M, N, K) -> int:
     return library().tgemm_sgemm_splitk_choose(M, N, K)
+
+
+def tgemm_linear_loss_workspace_size(dtype, T, V, D, X, ldx, W, ldw, teacher_k=0, backward_pass=0) -> int:
+    return library().tgemm_linear_loss_workspace_size(dtype, T, V, D, X, ldx, W, ldw, teacher_k, backward_pass)
+
+
+def tgemm_linear_ce_forward(dtype, T, V, D, X, ldx, W, ldw, target, ignore_index, loss, lse, summary, workspace,
+                            workspace_bytes, stream=None) -> int:
+    return library().tgemm_linear_ce_forward(dtype, T, V, D, X, ldx, W, ldw, target, ignore_index, loss, lse, summary,
+                                             workspace, workspace_bytes, stream)
+
+
+def tgemm_linear_ce_backward(dtype, T, V, D, X, ldx, W, ldw, target, ignore_index, lse, grad_loss, grad_step,
+                             grad_weight, dX, lddx, dW, lddw, workspace, workspace_bytes, stream=None) -> int:
+    return library().tgemm_linear_ce_backward(dtype, T, V, D, X, ldx, W, ldw, target, ignore_index, lse, grad_loss,
+                                              grad_step, grad_weight, dX, lddx, dW, lddw, workspace, workspace_bytes,
+                                              stream)
+
+
+def tgemm_linear_kd_forward(dtype, T, V, D, X, ldx, W, ldw, K, teacher_ids, ld_ids, teacher_dtype, teacher_logits,
+                            ld_logits, temperature, loss, lse, student, summary, workspace, workspace_bytes,
+                            stream=None) -> int:
+    return library().tgemm_linear_kd_forward(dtype, T, V, D, X, ldx, W, ldw, K, teacher_ids, ld_ids, teacher_dtype,
+                                             teacher_logits, ld_logits, temperature, loss, lse, student, summary,
+                                             workspace, workspace_bytes, stream)
+
+
+def tgemm_linear_kd_backward(dtype, T, V, D, X, ldx, W, ldw, K, teacher_ids, ld_ids, teacher_dtype, teacher_logits,
+                             ld_logits, temperature, lse, student, grad_loss, grad_step, grad_weight, dX, lddx, dW,
+                             lddw, workspace, workspace_bytes, stream=None) -> int:
+    return library().tgemm_linear_kd_backward(dtype, T, V, D, X, ldx, W, ldw, K, teacher_ids, ld_ids, teacher_dtype,
+                                              teacher_logits, ld_logits, temperature, lse, student, grad_loss,
+                                              grad_step, grad_weight, dX, lddx, dW, lddw, workspace, workspace_bytes,
+                                              stream)
 
 
 def tgemm_mfma_variant_count() -> int:

@@ -1,0 +1,187 @@
+// Internal interface of the loss operators on an output head's product
+// (linear_loss.cpp: entry points; linear_loss_product.hip: the products;
+// linear_loss_rows.hip: passes over rows).  Every launcher takes validated
+// arguments and returns the launch's hipError_t.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "mfma16.h"
+#include "tgemm.h"
+
+namespace tgemm {
+namespace loss {
+
+// A fp16 gradient piece holds 2^15 times its value over the row's power of
+// two (bf16 and float32 have the range to hold the value itself).
+constexpr int kHalfShift = 15;
+
+// ---- the products ----------------------------------------------------------
+
+// Tile configurations, by index (linear_loss_product.hip).
+struct TileShape {
+    int bm, bn;
+    int wg_per_cu;
+    int stat_columns;  // columns a wavefront's partial (maximum, sum) covers
+};
+int tile_count();
+const TileShape &tile_shape(int index);
+
+// Partial softmax statistics of s·X·Wᵀ: part[t][g] = (maximum, sum of
+// exp2(· - maximum)) of row t's columns of group g, in units of log2;
+// picked[t] = the scaled logit at target[t] (rows whose target is in [0, V)).
+struct StatsArgs {
+    m16::Operands op;
+    float scale;
+    float2 *part;
+    int groups;
+    const int64_t *target;  // or NULL
+    float *picked;
+};
+hipError_t launch_stats(bool half, int tile, const StatsArgs &a, hipStream_t stream);
+
+// A piece of the logits' gradient: G[t][v - v0] = coef[t]·(exp(s·z - lse[t]) -
+// [v = target[t]]), zero past the ends, 16-bit or three bf16 planes.
+struct GradArgs {
+    m16::Operands op;
+    float scale;
+    const float *lse, *coef;
+    const int64_t *target;  // or NULL
+    int64_t v0;
+    int rows;               // rows to write (T rounded up to 64)
+    void *G;
+    int64_t ldg, plane;     // elements
+    int planes;
+};
+hipError_t launch_grad(bool half, int tile, const GradArgs &a, hipStream_t stream);
+
+// C = A·B with A = G as stored (dX) or transposed (dW), B MN-contiguous.
+struct OutArgs {
+    m16::Operands op;
+    void *out;
+    int64_t ldo;
+    tgemm_dtype_t dtype;
+    bool vec;                // out and its rows 16-byte aligned
+    bool add;                // float32 out: add to what is there
+    int64_t split_stride;    // elements between the outputs of blockIdx.y
+    int splits;
+    const float *row_scale;  // or NULL
+    const float *all_scale;  // or NULL
+};
+hipError_t launch_dx(bool half, int tile, const OutArgs &a, hipStream_t stream);
+hipError_t launch_dw(bool half, int tile, const OutArgs &a, hipStream_t stream);
+
+// ---- passes over rows ------------------------------------------------------
+
+// dst (planes of rows_out×ld_out 16-bit elements, zero past the ends) = src
+// (rows×cols).  coef: rows with coef 0 become zero.  exps: row t is scaled by
+// 2^(exps[t] - the largest of block_max), and all_scale receives
+// 2^(that - kHalfShift).
+struct CopyArgs {
+    const void *src;
+    int64_t ld;
+    tgemm_dtype_t dtype;
+    int64_t rows, cols;
+    void *dst;
+    int64_t rows_out, ld_out, plane;
+    int planes;
+    bool vec;  // 16-byte loads
+    const float *coef;
+    const int *exps, *block_max;
+    int blocks;
+    float *all_scale;
+};
+hipError_t launch_copy(const CopyArgs &a, hipStream_t stream);
+
+// The teacher's part of a row, as both passes read it.
+struct Teacher {
+    int K;
+    const int64_t *ids;
+    int64_t ld_ids;
+    const void *logits;
+    int64_t ld_logits;
+    tgemm_dtype_t dtype;
+    float scale;  // 1 / temperature
+};
+
+struct JoinArgs {
+    int64_t T, V;
+    int groups;
+    const float2 *part;
+    const int64_t *target;
+    int64_t ignore;
+    const float *picked;
+    const Teacher *teacher;  // host pointer; NULL for cross entropy
+    const float *student;
+    float *loss, *lse;
+    int *counted;  // or NULL: receives whether a row counts
+};
+hipError_t launch_join(const JoinArgs &a, hipStream_t stream);
+
+// summary = {sum of loss, the mean over the rows that count, 1 / their number}
+// (1 / 1 where none does).
+hipError_t launch_summary(int64_t T, const float *loss, const int *counted, float *summary, hipStream_t stream);
+
+// student[t][k] = s·x_t·w_{id}: 0 where the entry is absent, NaN where its id is out of range.
+struct PickArgs {
+    int64_t T, V, D;
+    const void *X;
+    int64_t ldx;
+    const void *W;
+    int64_t ldw;
+    tgemm_dtype_t dtype;
+    Teacher teacher;
+    float *student;
+};
+hipError_t launch_pick(const PickArgs &a, hipStream_t stream);
+
+// The factor of a row's gradient, coef[t] = grad[t·grad_step]·factor·*weight, 0 for rows that do
+// not count, NaN for rows with an index out of range; for fp16 its fraction
+// times 2^kHalfShift, with row_scale[t] = 2^(exponent - kHalfShift), exps[t]
+// the exponent, and block_max[b] the largest of rows 256·b ... 256·b + 255.
+struct CoefArgs {
+    int64_t T, V;
+    const float *grad;
+    int64_t grad_step;
+    float factor;
+    const float *weight;  // or NULL
+    const int64_t *target;
+    int64_t ignore;
+    const Teacher *teacher;
+    bool half;
+    float *coef, *row_scale;
+    int *exps, *block_max;
+};
+hipError_t launch_coef(const CoefArgs &a, hipStream_t stream);
+
+// G[t][id - v0] = coef[t]·(exp(student - lse) - the teacher's probability of id) for the ids in [v0, v0 + cols).
+struct ScatterArgs {
+    int64_t T, v0, cols;
+    Teacher teacher;
+    const float *student, *lse, *coef;
+    void *G;
+    int64_t ldg, plane;
+    int planes;
+    bool half;
+};
+hipError_t launch_scatter(const ScatterArgs &a, hipStream_t stream);
+
+// out[t][d] = row_scale[t]·(part_0 + part_1 + ...)[t][d], part_s at part + s·stride.
+struct SumArgs {
+    int64_t T, D;
+    const float *part;
+    int64_t ld, stride;
+    int count;
+    const float *row_scale;
+    void *out;
+    int64_t ldo;
+    tgemm_dtype_t dtype;
+};
+hipError_t launch_sum(const SumArgs &a, hipStream_t stream);
+
+// rows×cols elements of out = 0
+hipError_t launch_zero(void *out, int64_t ldo, tgemm_dtype_t dtype, int64_t rows, int64_t cols, hipStream_t stream);
+
+}  // namespace loss
+}  // namespace tgemm

@@ -1,0 +1,311 @@
+"""Losses on an output head's product X·Wᵀ, for torch tensors, without the product.
+
+X (T×D) holds the tokens' hidden states and W (V×D) the head's weight, both
+float32, bfloat16 or float16 on one GPU, row-major with any leading dimension.
+
+* ``linear_cross_entropy`` and ``linear_distillation`` are differentiable in X
+  and W and reduce over the rows;
+* ``..._forward`` gives the losses of the rows and what the backward pass
+  needs, ``..._backward`` the gradients of sum_t grad_loss_t·loss_t: the same
+  calls without torch's autograd, for programs that keep their own buffers or
+  capture them into a graph.
+
+All are queued on `stream` (default: torch's current stream of X's device) and
+return without waiting.  include/tgemm.h states the arithmetic.
+"""
+
+from __future__ import annotations
+
+import functools
+
+from . import _lib
+from ._lib import TgemmError
+
+REDUCTIONS = ("mean", "sum", "none")
+
+
+def _dtype(t):
+    import torch
+
+    return {torch.float32: _lib.TGEMM_F32, torch.bfloat16: _lib.TGEMM_BF16, torch.float16: _lib.TGEMM_F16}.get(t.dtype)
+
+
+def _rows(t, name, shape=None, device=None, like=None):
+    """A row-major matrix of a supported type, and its leading dimension."""
+    import torch
+
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or _dtype(t) is None:
+        raise TypeError(f"{name} must be a 2-D float32, bfloat16 or float16 torch tensor")
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise TypeError(f"{name} must live on {'a GPU' if device is None else device}")
+    if like is not None and t.dtype != like:
+        raise TypeError(f"{name} must be {like}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {shape[0]}x{shape[1]}")
+    rows, cols = t.shape
+    if cols > 1 and rows > 0 and t.stride(1) != 1 or rows > 1 and t.stride(0) < cols:
+        raise ValueError(f"{name} must be row-major")
+    return max(t.stride(0), cols, 1) if rows > 1 else max(cols, 1)
+
+
+def _ids(t, name, shape, device):
+    import torch
+
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int64 or tuple(t.shape) != shape:
+        raise TypeError(f"{name} must be an int64 torch tensor of {'x'.join(map(str, shape))}")
+    if t.device != device:
+        raise TypeError(f"{name} must live on {device}")
+    return t.contiguous() if t.dim() == 1 else t
+
+
+def _floats(t, name, shape, device):
+    import torch
+
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or tuple(t.shape) != shape:
+        raise TypeError(f"{name} must be a float32 torch tensor of {'x'.join(map(str, shape))}")
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and live on {device}")
+    return t
+
+
+class _Call:
+    """The arguments shared by the four calls, and what they allocate."""
+
+    def __init__(self, X, W, stream):
+        import torch
+
+        ldx = _rows(X, "X")
+        ldw = _rows(W, "W", device=X.device, like=X.dtype)
+        if X.shape[1] != W.shape[1]:
+            raise ValueError(f"inner sizes differ: X is {tuple(X.shape)}, W is {tuple(W.shape)}")
+        if W.shape[0] < 1 or W.shape[1] < 1:
+            raise ValueError("W must have a row and a column")
+        self.device, self.dtype = X.device, X.dtype
+        self.T, self.D = X.shape
+        self.V = W.shape[0]
+        self.head = (_dtype(X), self.T, self.V, self.D, X.data_ptr(), ldx, W.data_ptr(), ldw)
+        self.stream = torch.cuda.current_stream(X.device).cuda_stream if stream is None else stream
+        self.made = []
+
+    def teacher(self, ids, logits, temperature):
+        import torch
+
+        if not isinstance(ids, torch.Tensor) or ids.dim() != 2 or ids.shape[0] != self.T or ids.shape[1] < 1:
+            raise TypeError(f"teacher_ids must be an int64 torch tensor of {self.T} rows")
+        self.K = ids.shape[1]
+        ids = _ids(ids, "teacher_ids", (self.T, self.K), self.device)
+        if self.T and (self.K > 1 and ids.stride(1) != 1 or self.T > 1 and ids.stride(0) < self.K):
+            raise ValueError("teacher_ids must be row-major")
+        ld = _rows(logits, "teacher_logits", (self.T, self.K), self.device)
+        ld_ids = max(ids.stride(0), self.K) if self.T > 1 else self.K
+        return (self.K, ids.data_ptr(), ld_ids, _dtype(logits), logits.data_ptr(), ld, float(temperature))
+
+    def new(self, shape, dtype):
+        import torch
+
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        self.made.append(t)
+        return t
+
+    def floats(self, t, name, shape):
+        import torch
+
+        return self.new(shape, torch.float32) if t is None else _floats(t, name, shape, self.device)
+
+    def gradient(self, t, name, shape):
+        if t is None:
+            t = self.new(shape, self.dtype)
+        return t, _rows(t, name, shape, self.device, self.dtype)
+
+    def room(self, workspace, k, backward):
+        import torch
+
+        need = _lib.tgemm_linear_loss_workspace_size(*self.head, k, backward)
+        if workspace is None:
+            workspace = self.new(max(need, 1), torch.uint8)
+        elif not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8:
+            raise TypeError("workspace must be a CUDA uint8 tensor")
+        elif workspace.device != self.device or not workspace.is_contiguous():
+            raise TypeError(f"workspace must be contiguous and live on {self.device}")
+        return workspace.data_ptr(), workspace.numel()
+
+    def queue(self, entry, *args):
+        import torch
+
+        from . import _hold_for_stream
+
+        with torch.cuda.device(self.device):
+            _hold_for_stream(self.stream, self.device, *self.made)
+            st = getattr(_lib, entry)(*self.head, *args, self.stream)
+        if st != _lib.TGEMM_SUCCESS:
+            raise TgemmError(st, entry)
+
+
+def _ptr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _ce_forward(X, W, target, ignore_index, loss, lse, summary, workspace, stream):
+    c = _Call(X, W, stream)
+    target = _ids(target, "target", (c.T,), c.device)
+    loss, lse = c.floats(loss, "loss", (c.T,)), c.floats(lse, "lse", (c.T,))
+    if summary:
+        summary = c.floats(None, "summary", (3,))
+    c.queue("tgemm_linear_ce_forward", target.data_ptr(), int(ignore_index), loss.data_ptr(), lse.data_ptr(),
+            _ptr(summary) if summary is not False else 0, *c.room(workspace, 0, 0))
+    return loss, lse, summary
+
+
+def linear_cross_entropy_forward(X, W, target, *, ignore_index=-100, loss=None, lse=None, workspace=None, stream=None):
+    """(loss, lse) of the rows (tgemm_linear_ce_forward): lse_t = log sum_v exp(x_t·w_v), loss_t = lse_t - x_t·w_y
+    with y = target_t (int64), 0 where y is ignore_index and NaN where y is outside the vocabulary otherwise.  loss
+    and lse: float32 tensors of T to write to; workspace: a CUDA uint8 tensor of at least
+    tgemm_linear_loss_workspace_size bytes (allocated if omitted; two calls in flight at once need two)."""
+    return _ce_forward(X, W, target, ignore_index, loss, lse, False, workspace, stream)[:2]
+
+
+def _gradients(c, X, W, dX, dW, need):
+    dX, lddx = c.gradient(dX, "dX", (c.T, c.D)) if need[0] else (None, c.D)
+    dW, lddw = c.gradient(dW, "dW", (c.V, c.D)) if need[1] else (None, c.D)
+    return dX, dW, (_ptr(dX), lddx, _ptr(dW), lddw)
+
+
+def _grad_loss(c, grad):
+    """grad_loss: one value a row, or one for all."""
+    import torch
+
+    if not isinstance(grad, torch.Tensor) or grad.dtype != torch.float32 or tuple(grad.shape) not in ((c.T,), ()):
+        raise TypeError(f"grad_loss must be a float32 torch tensor of {c.T}, or of no dimension")
+    if grad.device != c.device:
+        raise TypeError(f"grad_loss must live on {c.device}")
+    return grad.data_ptr(), grad.stride(0) if grad.dim() and c.T > 1 else 0
+
+
+def _ce_backward(grad_loss, weight, X, W, target, lse, ignore_index, dX, dW, need, workspace, stream):
+    c = _Call(X, W, stream)
+    target = _ids(target, "target", (c.T,), c.device)
+    lse = _floats(lse, "lse", (c.T,), c.device)
+    dX, dW, outs = _gradients(c, X, W, dX, dW, need)
+    c.queue("tgemm_linear_ce_backward", target.data_ptr(), int(ignore_index), lse.data_ptr(), *_grad_loss(c, grad_loss),
+            _ptr(weight), *outs, *c.room(workspace, 0, 1))
+    return dX, dW
+
+
+def linear_cross_entropy_backward(grad_loss, X, W, target, lse, *, ignore_index=-100, dX=None, dW=None,
+                                  need=(True, True), workspace=None, stream=None):
+    """(dX, dW) = the gradients of sum_t grad_loss_t·loss_t (tgemm_linear_ce_backward).  grad_loss: float32, one
+    value a row or one of no dimension for all; lse as linear_cross_entropy_forward gave it.  dX, dW: row-major
+    tensors to write to; need: which of the two are computed (None is returned for the other)."""
+    return _ce_backward(grad_loss, None, X, W, target, lse, ignore_index, dX, dW, need, workspace, stream)
+
+
+def _kd_forward(X, W, teacher_ids, teacher_logits, temperature, loss, lse, student, summary, workspace, stream):
+    c = _Call(X, W, stream)
+    teacher = c.teacher(teacher_ids, teacher_logits, temperature)
+    loss, lse = c.floats(loss, "loss", (c.T,)), c.floats(lse, "lse", (c.T,))
+    student = c.floats(student, "student", (c.T, c.K))
+    if summary:
+        summary = c.floats(None, "summary", (3,))
+    c.queue("tgemm_linear_kd_forward", *teacher, loss.data_ptr(), lse.data_ptr(), student.data_ptr(),
+            _ptr(summary) if summary is not False else 0, *c.room(workspace, c.K, 0))
+    return loss, lse, student, summary
+
+
+def linear_distillation_forward(X, W, teacher_ids, teacher_logits, *, temperature=1.0, loss=None, lse=None,
+                                student=None, workspace=None, stream=None):
+    """(loss, lse, student) of the rows (tgemm_linear_kd_forward) for a teacher's top logits: teacher_ids (T×K,
+    int64) the words and teacher_logits (T×K, float32, bfloat16 or float16) their logits; an entry with the logit
+    -inf is absent.  With q the softmax of a row's logits / temperature over its entries and z the student's logits
+    / temperature, loss_t = temperature²·sum_k q_k·(log q_k - (z_k - lse_t)), 0 for a row without entries and NaN
+    where an entry's id is outside the vocabulary.  student: z at the teacher's ids (0 where absent)."""
+    return _kd_forward(X, W, teacher_ids, teacher_logits, temperature, loss, lse, student, False, workspace, stream)[:3]
+
+
+def _kd_backward(grad_loss, weight, X, W, teacher_ids, teacher_logits, lse, student, temperature, dX, dW, need,
+                 workspace, stream):
+    c = _Call(X, W, stream)
+    teacher = c.teacher(teacher_ids, teacher_logits, temperature)
+    lse = _floats(lse, "lse", (c.T,), c.device)
+    student = _floats(student, "student", (c.T, c.K), c.device)
+    dX, dW, outs = _gradients(c, X, W, dX, dW, need)
+    c.queue("tgemm_linear_kd_backward", *teacher, lse.data_ptr(), student.data_ptr(), *_grad_loss(c, grad_loss),
+            _ptr(weight), *outs, *c.room(workspace, c.K, 1))
+    return dX, dW
+
+
+def linear_distillation_backward(grad_loss, X, W, teacher_ids, teacher_logits, lse, student, *, temperature=1.0,
+                                 dX=None, dW=None, need=(True, True), workspace=None, stream=None):
+    """(dX, dW) = the gradients of sum_t grad_loss_t·loss_t (tgemm_linear_kd_backward); lse and student as
+    linear_distillation_forward gave them, the rest as linear_cross_entropy_backward."""
+    return _kd_backward(grad_loss, None, X, W, teacher_ids, teacher_logits, lse, student, temperature, dX, dW, need,
+                        workspace, stream)
+
+
+@functools.lru_cache(maxsize=None)
+def _functions():
+    """The differentiable forms.  One backward pass per forward pass through each; there is no second derivative."""
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    def reduced(reduction, loss, summary):
+        # a copy of one element: an output that is a view could not be changed in place by the caller
+        return loss if reduction == "none" else summary[0 if reduction == "sum" else 1].clone()
+
+    class CrossEntropy(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, X, W, target, ignore_index, reduction):
+            loss, lse, summary = _ce_forward(X, W, target, ignore_index, None, None, reduction != "none", None, None)
+            ctx.save_for_backward(X, W, target, lse, summary if reduction == "mean" else None)
+            ctx.ignore_index = ignore_index
+            return reduced(reduction, loss, summary)
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, grad):
+            X, W, target, lse, summary = ctx.saved_tensors
+            weight = None if summary is None else summary[2:]
+            dX, dW = _ce_backward(grad, weight, X, W, target, lse, ctx.ignore_index, None, None,
+                                  ctx.needs_input_grad[:2], None, None)
+            return dX, dW, None, None, None
+
+    class Distillation(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, X, W, teacher_ids, teacher_logits, temperature, reduction):
+            loss, lse, student, summary = _kd_forward(X, W, teacher_ids, teacher_logits, temperature, None, None, None,
+                                                      reduction != "none", None, None)
+            ctx.save_for_backward(X, W, teacher_ids, teacher_logits, lse, student,
+                                  summary if reduction == "mean" else None)
+            ctx.temperature = temperature
+            return reduced(reduction, loss, summary)
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, grad):
+            X, W, ids, logits, lse, student, summary = ctx.saved_tensors
+            weight = None if summary is None else summary[2:]
+            dX, dW = _kd_backward(grad, weight, X, W, ids, logits, lse, student, ctx.temperature, None, None,
+                                  ctx.needs_input_grad[:2], None, None)
+            return dX, dW, None, None, None, None
+
+    return CrossEntropy, Distillation
+
+
+def _check_reduction(reduction):
+    if reduction not in REDUCTIONS:
+        raise ValueError(f"reduction must be one of {REDUCTIONS}")
+
+
+def linear_cross_entropy(X, W, target, *, ignore_index=-100, reduction="mean"):
+    """The softmax cross entropy of the logits X·Wᵀ against `target`, differentiable in X and W; the logits are never
+    held.  reduction: "mean" over the rows whose target is not ignore_index (0 if there is none), "sum", or "none"
+    for the losses of the rows.  Losses are float32; gradients have the type of X and W."""
+    _check_reduction(reduction)
+    return _functions()[0].apply(X, W, target, ignore_index, reduction)
+
+
+def linear_distillation(X, W, teacher_ids, teacher_logits, *, temperature=1.0, reduction="mean"):
+    """The distillation loss of the logits X·Wᵀ against a teacher's top logits (linear_distillation_forward),
+    differentiable in X and W (the teacher's logits get no gradient).  reduction: "mean" over the rows that have an
+    entry (0 if none has), "sum" or "none"."""
+    _check_reduction(reduction)
+    return _functions()[1].apply(X, W, teacher_ids, teacher_logits, temperature, reduction)
