@@ -95,22 +95,31 @@ bool as_stored(const void *p, int64_t ld, const Head &h)
            reinterpret_cast<uintptr_t>(p) % 16 == 0;
 }
 
-// The tile for an M×N product of `steps` steps: least time by its rounds over
-// the 256 compute units, a tile's time being its area over the rate that its
-// shape sustains, and a fixed cost for filling and draining it.
-int choose_tile(int64_t M, int64_t N, int64_t steps)
+// The tile for an M×N product of `steps` steps, and into how many parts its
+// sum is split (1 where `split` is false): least time by its rounds over the
+// 256 compute units, a tile's time being its area over the rate that its shape
+// sustains, with a fixed cost for filling and draining it, and the writing and
+// reading of the parts.  The unit is a 256×256 tile's step, 1.5 µs.
+struct Choice {
+    int tile = 0, splits = 1;
+};
+Choice choose_tile(int64_t M, int64_t N, int64_t steps, bool split = false)
 {
     static const double rate[] = {1.0, 0.7, 0.25};
-    int best = 0;
-    double least = 0;
+    Choice best;
+    double least = -1;
     for (int i = 0; i < tile_count(); ++i) {
         const TileShape &s = tile_shape(i);
         const int64_t tiles = ceil_div(M, s.bm) * ceil_div(N, s.bn);
-        const double rounds = (double)ceil_div(tiles, (int64_t)256 * s.wg_per_cu) * s.wg_per_cu;
-        const double time = rounds * ((double)s.bm * s.bn / 65536.0 / rate[i] * (double)steps + 3.0);
-        if (i == 0 || time < least) {
-            least = time;
-            best = i;
+        for (int64_t parts = 1; parts == 1 || (split && parts <= 64 && steps / parts >= 4); parts *= 2) {
+            const double rounds = (double)ceil_div(tiles * parts, (int64_t)256 * s.wg_per_cu) * s.wg_per_cu;
+            double time = rounds * ((double)s.bm * s.bn / 65536.0 / rate[i] * (double)ceil_div(steps, parts) + 3.0);
+            if (parts > 1) time += 4.0 + (double)M * (double)N * 8.0 * (double)parts / 5e12 / 1.5e-6;
+            if (least < 0 || time < least) {
+                least = time;
+                best.tile = i;
+                best.splits = (int)parts;
+            }
         }
     }
     return best;
@@ -167,7 +176,7 @@ bool fits(int64_t M, int64_t N, int tile, int64_t splits)
 bool plan_forward(Plan &p, const Head &h, bool distill)
 {
     plan_operands(p, h, false);
-    p.stat_tile = choose_tile(h.T, h.V, p.Dp / kStepK * p.segments);
+    p.stat_tile = choose_tile(h.T, h.V, p.Dp / kStepK * p.segments).tile;
     p.groups = (int)ceil_div(h.V, tile_shape(p.stat_tile).stat_columns);
     p.part = p.take(h.T * p.groups * 8);
     if (!distill) p.picked = p.take(h.T * 4);
@@ -184,15 +193,11 @@ bool plan_backward(Plan &p, const Head &h)
     p.piece = round_up(ceil_div(h.V, p.pieces), 256);
     p.pieces = ceil_div(h.V, p.piece);
     const int64_t seg = p.segments;
-    p.grad_tile = choose_tile(p.Tp, p.piece, p.Dp / kStepK * seg);
-    p.dw_tile = choose_tile(p.piece, h.D, p.Tp / kStepK * seg);
-    const int64_t dx_steps = p.piece / kStepK;
-    p.dx_tile = choose_tile(h.T, h.D, dx_steps * seg);
-    const TileShape &s = tile_shape(p.dx_tile);
-    const int64_t tiles = ceil_div(h.T, s.bm) * ceil_div(h.D, s.bn), room = (int64_t)256 * s.wg_per_cu;
-    int64_t splits = room / tiles;  // few tiles: the sum over the vocabulary is split
-    if (splits > dx_steps / 4) splits = dx_steps / 4;
-    p.dx_splits = (int)(splits < 1 ? 1 : splits > 64 ? 64 : splits);
+    p.grad_tile = choose_tile(p.Tp, p.piece, p.Dp / kStepK * seg).tile;
+    p.dw_tile = choose_tile(p.piece, h.D, p.Tp / kStepK * seg).tile;
+    const Choice dx = choose_tile(h.T, h.D, p.piece / kStepK * seg, true);
+    p.dx_tile = dx.tile;
+    p.dx_splits = dx.splits;
     p.dx_direct = p.pieces == 1 && p.dx_splits == 1;
     p.coef = p.take(h.T * 4);
     if (p.half) {

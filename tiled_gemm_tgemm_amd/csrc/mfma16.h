@@ -8,7 +8,7 @@
 //   a lane and its partner, and a row's values leave in 16-byte pieces.
 // * K runs in steps of 64.  A step's slices of A and B go from device memory
 //   straight into LDS, 16 bytes a lane, into one of two stages; the loads of
-//   step p+1 are under way while step p is multiplied.
+//   the next step are under way while a step is multiplied.
 // * The order of the 32 columns of a block is free as long as the reader of C
 //   knows it: column 16·h + 4·q + r of C sits at index 8·q + 4·h + r of the
 //   instruction, which is what gives lane half h the 16 adjacent columns
@@ -121,8 +121,12 @@ struct Loader {
     __device__ __forceinline__ void issue(const char *base, lds_char *stage, int wave) const
     {
 #pragma unroll
-        for (int r = 0; r < kRounds; ++r)
-            __builtin_amdgcn_global_load_lds((global_char *)(base + off[r]), stage + (r * THREADS + wave * 64) * 16, 16, 0, 0);
+        for (int r = 0; r < kRounds; ++r) {
+            // kept as 32 bits in the loop: the load then adds it to the scalar base by itself
+            uint32_t o = off[r];
+            asm volatile("" : "+v"(o));
+            __builtin_amdgcn_global_load_lds((global_char *)(base + o), stage + (r * THREADS + wave * 64) * 16, 16, 0, 0);
+        }
     }
 };
 
@@ -164,6 +168,32 @@ struct Reader {
         }
     }
 };
+
+// The work-group's loads into LDS have arrived, and its reads of LDS are done.
+// A barrier's fence does not by itself wait for loads that write LDS.
+__device__ __forceinline__ void arrive()
+{
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+    __syncthreads();
+}
+
+struct Yes { static constexpr bool value = true; };
+struct No { static constexpr bool value = false; };
+
+// Scheduling hints: READS LDS reads and LOADS loads spread evenly among MFMAS
+// matrix instructions.
+template <int MFMAS, int READS, int LOADS, int I = 0>
+__device__ __forceinline__ void spread()
+{
+    if constexpr (I < MFMAS) {
+        constexpr int reads = (I + 1) * READS / MFMAS - I * READS / MFMAS;
+        constexpr int loads = (I + 1) * LOADS / MFMAS - I * LOADS / MFMAS;
+        if constexpr (reads > 0) __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);
+        if constexpr (loads > 0) __builtin_amdgcn_sched_group_barrier(0x020, loads, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        spread<MFMAS, READS, LOADS, I + 1>();
+    }
+}
 
 // A tile of C.  After run(), lane (l32 = lane & 31, half = lane >> 5) holds in
 // acc[i][j][r] row row0 + i·32 + l32, column col0 + j·32 + 16·half + r.
@@ -212,46 +242,90 @@ struct TileProduct {
         const int64_t step_a = (A_MC ? (int64_t)kStepK * p.lda : (int64_t)kStepK) * 2;
         const int64_t step_b = (B_MC ? (int64_t)kStepK * p.ldb : (int64_t)kStepK) * 2;
 
-        auto issue = [&](int seg, int k, int stage) {
-            const int pa = (kPairsA >> (2 * seg)) & 3, pb = (kPairsB >> (2 * seg)) & 3;
-            const char *a = A + k * step_a, *b = B + k * step_b;
+        // where the next loads come from
+        int seg = 0, k = first;
+        const char *from_a = nullptr, *from_b = nullptr;
+        auto seek = [&]() {
+            from_a = A + k * step_a;
+            from_b = B + k * step_b;
             if (p.segments > 1) {
-                a += pa * p.plane_a * 2;
-                b += pb * p.plane_b * 2;
+                from_a += ((kPairsA >> (2 * seg)) & 3) * p.plane_a * 2;
+                from_b += ((kPairsB >> (2 * seg)) & 3) * p.plane_b * 2;
             }
             // the last rows of an MC operand, and back to whole steps for the next segment
-            if (A_MC && ((k + 1) * kStepK > p.k_a || p.segments > 1)) la.place(p.lda, a_last, p.k_a - 1 - k * kStepK);
-            if (B_MC && ((k + 1) * kStepK > p.k_b || p.segments > 1)) lb.place(p.ldb, b_last, p.k_b - 1 - k * kStepK);
-            la.issue(a, lds + stage * kStage, wave);
-            lb.issue(b, lds + stage * kStage + BM * kStepK * 2, wave);
-        };
-
-        int seg = 0, k = first, stage = 0;
-        issue(seg, k, 0);
-        while (true) {
-            __syncthreads();  // this step's slices are in LDS; the other stage is read no more
+            if (A_MC && ((k + 1) * kStepK > p.k_a || (p.segments > 1 && k == first)))
+                la.place(p.lda, a_last, p.k_a - 1 - k * kStepK);
+            if (B_MC && ((k + 1) * kStepK > p.k_b || (p.segments > 1 && k == first)))
+                lb.place(p.ldb, b_last, p.k_b - 1 - k * kStepK);
             if (++k == last) {
                 k = first;
                 ++seg;
             }
-            const bool more = seg < p.segments;
-            if (more) issue(seg, k, stage ^ 1);
+        };
+        auto issue = [&](int stage) {
+            la.issue(from_a, lds + stage * kStage, wave);
+            lb.issue(from_b, lds + stage * kStage + BM * kStepK * 2, wave);
+        };
+
+        // Two sets of fragments: those of the next 16 values of k are read
+        // while these are multiplied.
+        typename Frag<E>::type a[2][FM], b[2][FN];
+        auto read = [&](int stage, int s) {
             lds_char *as = lds + stage * kStage, *bs = as + BM * kStepK * 2;
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                typename Frag<E>::type a[FM], b[FN];
+            for (int j = 0; j < FN; ++j) b[s & 1][j] = rb.template read<E>(bs, j, s);
 #pragma unroll
-                for (int i = 0; i < FM; ++i) a[i] = ra.template read<E>(as, i, s);
+            for (int i = 0; i < FM; ++i) a[s & 1][i] = ra.template read<E>(as, i, s);
+        };
+        auto multiply = [&](int s) {
 #pragma unroll
-                for (int j = 0; j < FN; ++j) b[j] = rb.template read<E>(bs, j, s);
+            for (int i = 0; i < FM; ++i)
 #pragma unroll
-                for (int i = 0; i < FM; ++i)
+                for (int j = 0; j < FN; ++j) acc[i][j] = Frag<E>::mfma(b[s & 1][j], a[s & 1][i], acc[i][j]);
+        };
+        constexpr int kReads = FM * (A_MC ? 2 : 1) + FN * (B_MC ? 2 : 1);
+        constexpr int kLoads = decltype(la)::kRounds + decltype(lb)::kRounds;
+
+        // A step on the slices of `stage`, its first fragments read.  The
+        // barrier stands before the last quarter, whose fragments are in
+        // registers by then: this stage is read no more, so the loads of the
+        // step after next go there, and the next step's slices have arrived,
+        // so its first fragments are read under the last quarter's products.
+        auto step = [&](int stage, auto load, auto next) {
 #pragma unroll
-                    for (int j = 0; j < FN; ++j) acc[i][j] = Frag<E>::mfma(b[j], a[i], acc[i][j]);
+            for (int s = 0; s < 3; ++s) {
+                read(stage, s + 1);
+                multiply(s);
+                spread<FM * FN, kReads, 0>();
             }
-            if (!more) break;
-            stage ^= 1;
+            if constexpr (decltype(next)::value) {
+                arrive();
+                if constexpr (decltype(load)::value) issue(stage);
+                read(stage ^ 1, 0);
+            }
+            multiply(3);
+            spread<FM * FN, decltype(next)::value ? kReads : 0, decltype(load)::value ? kLoads : 0>();
+        };
+
+        const int total = (last - first) * p.segments;
+        seek();
+        issue(0);
+        if (total > 1) {
+            seek();
+            issue(1);
         }
+        arrive();
+        read(0, 0);
+        int n = 0;
+        for (; n + 2 < total; ++n) {
+            seek();
+            step(n & 1, Yes{}, Yes{});
+        }
+        if (n + 1 < total) {
+            step(n & 1, No{}, Yes{});
+            ++n;
+        }
+        step(n & 1, No{}, No{});
     }
 };
 
