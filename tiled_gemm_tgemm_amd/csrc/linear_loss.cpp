@@ -32,6 +32,12 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t size_of(tgemm_dtype_t t) { return t == TGEMM_F32 ? 4 : 2; }
 bool known(tgemm_dtype_t t) { return t == TGEMM_F32 || t == TGEMM_BF16 || t == TGEMM_F16; }
 
+// Rows start 16-byte aligned.
+bool rows16(const void *p, int64_t ld, tgemm_dtype_t dtype)
+{
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * (int64_t)size_of(dtype) % 16 == 0;
+}
+
 tgemm_status_t from_hip(hipError_t e) { return e == hipSuccess ? TGEMM_SUCCESS : TGEMM_ERROR_HIP; }
 
 // A byte range that a call reads or writes.
@@ -137,7 +143,7 @@ struct Plan {
     int stat_tile = 0, groups = 0;
     int64_t part = -1, picked = -1, counted = -1;
     // backward
-    int64_t piece = 0, pieces = 0;
+    int64_t piece = 0, pieces = 0, ldg = 0;
     int grad_tile = 0, dx_tile = 0, dw_tile = 0, dx_splits = 1;
     bool dx_direct = false;
     int64_t coef = -1, row_scale = -1, exps = -1, block_max = -1, all_scale = -1, g = -1, dx_part = -1;
@@ -192,6 +198,7 @@ bool plan_backward(Plan &p, const Head &h)
     p.pieces = ceil_div(h.V, cols);
     p.piece = round_up(ceil_div(h.V, p.pieces), 256);
     p.pieces = ceil_div(h.V, p.piece);
+    p.ldg = p.piece + 128;
     const int64_t seg = p.segments;
     p.grad_tile = choose_tile(p.Tp, p.piece, p.Dp / kStepK * seg).tile;
     p.dw_tile = choose_tile(p.piece, h.D, p.Tp / kStepK * seg).tile;
@@ -203,10 +210,10 @@ bool plan_backward(Plan &p, const Head &h)
     if (p.half) {
         p.row_scale = p.take(h.T * 4);
         p.exps = p.take(h.T * 4);
-        p.block_max = p.take(ceil_div(h.T, 256) * 4);
+        p.block_max = p.take(coef_blocks(h.T, true) * 4);
         p.all_scale = p.take(4);
     }
-    p.g = p.take(p.Tp * p.piece * 2 * p.planes);
+    p.g = p.take(p.Tp * p.ldg * 2 * p.planes);
     if (!p.dx_direct) p.dx_part = p.take(p.dx_splits * h.T * p.Dp * 4);
     return fits(p.Tp, p.piece, p.grad_tile, 1) && fits(p.piece, h.D, p.dw_tile, 1) &&
            fits(h.T, h.D, p.dx_tile, p.dx_splits);
@@ -241,7 +248,7 @@ T *in(void *workspace, int64_t offset) { return offset < 0 ? nullptr : (T *)((ch
 
 // Lays out `rows` rows of an operand at dst.
 hipError_t copy_in(const Plan &p, const Head &h, const void *src, int64_t ld, int64_t rows, void *dst, int64_t rows_out,
-                   hipStream_t stream, const float *coef = nullptr, void *workspace = nullptr)
+                   hipStream_t stream, const float *coef = nullptr, void *workspace = nullptr, int blocks = 0)
 {
     CopyArgs c{};
     c.src = src;
@@ -254,12 +261,12 @@ hipError_t copy_in(const Plan &p, const Head &h, const void *src, int64_t ld, in
     c.ld_out = p.Dp;
     c.plane = rows_out * p.Dp;
     c.planes = p.planes;
-    c.vec = reinterpret_cast<uintptr_t>(src) % 16 == 0 && ld % 8 == 0;
+    c.vec = rows16(src, ld, h.dtype);
     c.coef = coef;
     if (coef != nullptr && p.half) {
         c.exps = in<int>(workspace, p.exps);
         c.block_max = in<int>(workspace, p.block_max);
-        c.blocks = (int)ceil_div(h.T, 256);
+        c.blocks = blocks;
         c.all_scale = in<float>(workspace, p.all_scale);
     }
     return launch_copy(c, stream);
@@ -310,7 +317,8 @@ tgemm_status_t forward(const Plan &p, const Head &h, const Labels &l, float *los
     e = launch_stats(p.half, p.stat_tile, s, stream);
     if (e != hipSuccess) return from_hip(e);
     if (l.teacher != nullptr) {
-        PickArgs k{h.T, h.V, h.D, h.X, h.ldx, h.W, h.ldw, h.dtype, *l.teacher, student};
+        PickArgs k{h.T, h.V, h.D, h.X, h.ldx, h.W, h.ldw, h.dtype, rows16(h.X, h.ldx, h.dtype) && rows16(h.W, h.ldw, h.dtype),
+                   *l.teacher, student};
         e = launch_pick(k, stream);
         if (e != hipSuccess) return from_hip(e);
     }
@@ -348,7 +356,8 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
     // Rows that do not count may hold anything: they are cleared where they
     // would meet a zero of the logits' gradient.
     void *xs = in<void>(ws, p.xs);
-    e = copy_in(p, h, h.X, h.ldx, h.T, xs, p.Tp, stream, c.coef, ws);
+    e = copy_in(p, h, h.X, h.ldx, h.T, xs, p.Tp, stream, c.coef, ws,
+                (int)coef_blocks(h.T, l.teacher != nullptr));
     if (e != hipSuccess) return from_hip(e);
     const Stored cleared{xs, p.Dp, p.Tp * p.Dp};
     Stored x = cleared, w{h.W, h.ldw, 0};
@@ -365,7 +374,7 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
     }
 
     void *g = in<void>(ws, p.g);
-    const int64_t plane_g = p.Tp * p.piece;
+    const int64_t plane_g = p.Tp * p.ldg;
     const int64_t dx_stride = h.T * p.Dp;
     for (int64_t n = 0; n < p.pieces; ++n) {
         const int64_t v0 = n * p.piece, cols = h.V - v0 < p.piece ? h.V - v0 : p.piece;
@@ -390,13 +399,13 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
         a.v0 = v0;
         a.rows = (int)p.Tp;
         a.G = g;
-        a.ldg = p.piece;
+        a.ldg = p.ldg;
         a.plane = plane_g;
         a.planes = p.planes;
         e = launch_grad(p.half, p.grad_tile, a, stream);
         if (e != hipSuccess) return from_hip(e);
         if (l.teacher != nullptr) {
-            ScatterArgs s{h.T, v0, cols, *l.teacher, student, lse, c.coef, g, p.piece, plane_g, p.planes, p.half};
+            ScatterArgs s{h.T, v0, cols, *l.teacher, student, lse, c.coef, g, p.ldg, plane_g, p.planes, p.half};
             e = launch_scatter(s, stream);
             if (e != hipSuccess) return from_hip(e);
         }
@@ -405,7 +414,7 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
             o.op = operands(p, h.T, h.D, cols_steps, p.dx_tile);
             o.op.steps_per_split = (int)ceil_div(cols_steps, p.dx_splits);
             o.op.A = g;
-            o.op.lda = p.piece;
+            o.op.lda = p.ldg;
             o.op.plane_a = plane_g;
             o.op.mn_a = (int)p.Tp;
             o.op.B = wn;
@@ -418,7 +427,7 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
                 o.out = dX;
                 o.ldo = lddx;
                 o.dtype = h.dtype;
-                o.vec = reinterpret_cast<uintptr_t>(dX) % 16 == 0 && lddx * size_of(h.dtype) % 16 == 0;
+                o.vec = rows16(dX, lddx, h.dtype);
                 o.row_scale = in<float>(ws, p.row_scale);
             } else {
                 o.out = in<float>(ws, p.dx_part);
@@ -435,7 +444,7 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
             OutArgs o{};
             o.op = operands(p, cols, h.D, p.Tp / kStepK, p.dw_tile);
             o.op.A = g;
-            o.op.lda = p.piece;
+            o.op.lda = p.ldg;
             o.op.plane_a = plane_g;
             o.op.mn_a = (int)p.piece;
             o.op.k_a = (int)p.Tp;
@@ -447,7 +456,7 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
             o.out = (char *)dW + v0 * lddw * (int64_t)size_of(h.dtype);
             o.ldo = lddw;
             o.dtype = h.dtype;
-            o.vec = reinterpret_cast<uintptr_t>(dW) % 16 == 0 && lddw * size_of(h.dtype) % 16 == 0;
+            o.vec = rows16(dW, lddw, h.dtype);
             o.splits = 1;
             o.all_scale = in<float>(ws, p.all_scale);
             e = launch_dw(p.half, p.dw_tile, o, stream);
@@ -456,7 +465,7 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
     }
     if (dX != nullptr && !p.dx_direct) {
         SumArgs s{h.T, h.D, in<float>(ws, p.dx_part), p.Dp, dx_stride, p.dx_splits, in<float>(ws, p.row_scale),
-                  dX, lddx, h.dtype};
+                  dX, lddx, h.dtype, rows16(dX, lddx, h.dtype)};
         e = launch_sum(s, stream);
         if (e != hipSuccess) return from_hip(e);
     }

@@ -64,7 +64,7 @@ struct OutArgs {
     tgemm_dtype_t dtype;
     bool vec;                // out and its rows 16-byte aligned
     bool add;                // float32 out: add to what is there
-    int64_t split_stride;    // elements between the outputs of blockIdx.y
+    int64_t split_stride;    // elements between the outputs of the sum's parts
     int splits;
     const float *row_scale;  // or NULL
     const float *all_scale;  // or NULL
@@ -131,6 +131,7 @@ struct PickArgs {
     const void *W;
     int64_t ldw;
     tgemm_dtype_t dtype;
+    bool vec;  // 16-byte loads
     Teacher teacher;
     float *student;
 };
@@ -139,7 +140,9 @@ hipError_t launch_pick(const PickArgs &a, hipStream_t stream);
 // The factor of a row's gradient, coef[t] = grad[t·grad_step]·factor·*weight, 0 for rows that do
 // not count, NaN for rows with an index out of range; for fp16 its fraction
 // times 2^kHalfShift, with row_scale[t] = 2^(exponent - kHalfShift), exps[t]
-// the exponent, and block_max[b] the largest of rows 256·b ... 256·b + 255.
+// the exponent, and block_max[b] the largest of a work-group's rows (256, or
+// 16 where each has a teacher's entries).
+inline int64_t coef_blocks(int64_t T, bool teacher) { return teacher ? (T + 15) / 16 : (T + 255) / 256; }
 struct CoefArgs {
     int64_t T, V;
     const float *grad;
@@ -177,6 +180,7 @@ struct SumArgs {
     void *out;
     int64_t ldo;
     tgemm_dtype_t dtype;
+    bool vec;  // out and its rows 16-byte aligned
 };
 hipError_t launch_sum(const SumArgs &a, hipStream_t stream);
 

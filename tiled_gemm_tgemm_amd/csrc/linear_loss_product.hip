@@ -21,7 +21,7 @@ constexpr float kLog2e = 1.44269504088896340736f;
 template <class E, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void linear_stats_kernel(StatsArgs a)
 {
-    typedef TileProduct<E, BM, BN, WM, WN, false, false> Tile;
+    typedef TileProduct<E, BM, BN, WM, WN, false, false, 64, 2> Tile;
     __shared__ __align__(1024) char lds[Tile::kLds];
     Tile t;
     t.run(a.op, (lds_char *)lds);
@@ -90,7 +90,7 @@ __device__ __forceinline__ void store16(E *to, const float (&v)[16])
 template <class E, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void linear_grad_kernel(GradArgs a)
 {
-    typedef TileProduct<E, BM, BN, WM, WN, false, false> Tile;
+    typedef TileProduct<E, BM, BN, WM, WN, false, false, 64, 2> Tile;
     __shared__ __align__(1024) char lds[Tile::kLds];
     Tile t;
     t.run(a.op, (lds_char *)lds);
@@ -158,7 +158,7 @@ __device__ __forceinline__ void store_row(T *to, const float (&v)[16], int left,
 template <class E, int BM, int BN, int WM, int WN, bool A_MC>
 __global__ __launch_bounds__(64 * WM * WN) void linear_out_kernel(OutArgs a)
 {
-    typedef TileProduct<E, BM, BN, WM, WN, A_MC, true> Tile;
+    typedef TileProduct<E, BM, BN, WM, WN, A_MC, true, BM >= 128 ? 32 : 64, BM >= 128 ? 4 : 2> Tile;
     __shared__ __align__(1024) char lds[Tile::kLds];
     Tile t;
     t.run(a.op, (lds_char *)lds);
@@ -178,7 +178,7 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_out_kernel(OutArgs a)
             float v[16];
 #pragma unroll
             for (int r = 0; r < 16; ++r) v[r] = t.acc[i][j][r] * s;
-            const int64_t at = (int64_t)row * a.ldo + col + (int64_t)blockIdx.y * a.split_stride;
+            const int64_t at = (int64_t)row * a.ldo + col + (int64_t)t.split * a.split_stride;
             if (a.dtype == TGEMM_F32) {
                 float *to = (float *)a.out + at;
                 if (a.add) {
@@ -203,7 +203,7 @@ constexpr TileShape kTiles[] = {
 #define TGEMM_TILES(X) X(0, 256, 256, 2, 4) X(1, 128, 128, 2, 2) X(2, 32, 128, 1, 4)
 
 template <class Args>
-dim3 grid_of(const Args &a, int splits) { return dim3((unsigned)(a.op.tiles_m * a.op.tiles_n), (unsigned)splits); }
+unsigned grid_of(const Args &a, int splits) { return (unsigned)(a.op.tiles_m * a.op.tiles_n) * (unsigned)splits; }
 
 }  // namespace
 

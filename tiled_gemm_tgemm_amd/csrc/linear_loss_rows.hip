@@ -220,23 +220,64 @@ __global__ __launch_bounds__(1024) void linear_summary_kernel(int64_t T, const f
     }
 }
 
+// Eight adjacent values of a row, `left` of which are there.
+__device__ __forceinline__ void load8(const void *p, int64_t at, tgemm_dtype_t dtype, bool vec, int64_t left,
+                                      float (&v)[8])
+{
+    if (vec && left >= 8) {
+        if (dtype == TGEMM_F32) {
+            const m16::f32x4 *q = (const m16::f32x4 *)((const float *)p + at);
+            const m16::f32x4 lo = q[0], hi = q[1];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = e < 4 ? lo[e & 3] : hi[e & 3];
+        } else {
+            const u16x8 w = *(const u16x8 *)((const uint16_t *)p + at);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                v[e] = dtype == TGEMM_BF16 ? (float)__builtin_bit_cast(__bf16, (uint16_t)w[e])
+                                           : (float)__builtin_bit_cast(_Float16, (uint16_t)w[e]);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = e < left ? load_as_float(p, at + e, dtype) : 0.0f;
+    }
+}
+
+// A wavefront takes kTogether entries of a row at a time, so that as many
+// rows of W are on their way.
 __global__ __launch_bounds__(256) void linear_pick_kernel(PickArgs a)
 {
+    constexpr int kTogether = 8;
     const int64_t row = blockIdx.x;
     const int lane = threadIdx.x & 63, K = a.teacher.K;
-    for (int k = threadIdx.x >> 6; k < K; k += 4) {
-        const float v = load_as_float(a.teacher.logits, row * a.teacher.ld_logits + k, a.teacher.dtype);
-        const int64_t id = a.teacher.ids[row * a.teacher.ld_ids + k];
-        float sum = 0.0f;
-        if (v == -INFINITY) {
-        } else if (id < 0 || id >= a.V) {
-            sum = NAN;
-        } else {
-            for (int64_t d = lane; d < a.D; d += 64)
-                sum += load_as_float(a.X, row * a.ldx + d, a.dtype) * load_as_float(a.W, id * a.ldw + d, a.dtype);
-            sum = wave_sum(sum) * a.teacher.scale;
+    for (int k0 = (threadIdx.x >> 6) * kTogether; k0 < K; k0 += 4 * kTogether) {
+        int64_t id[kTogether];
+        float sum[kTogether];
+#pragma unroll
+        for (int j = 0; j < kTogether; ++j) {
+            const int k = min(k0 + j, K - 1);
+            const float v = load_as_float(a.teacher.logits, row * a.teacher.ld_logits + k, a.teacher.dtype);
+            id[j] = a.teacher.ids[row * a.teacher.ld_ids + k];
+            sum[j] = v == -INFINITY ? 0.0f : id[j] < 0 || id[j] >= a.V ? NAN : 0.0f;
+            // an entry that is absent or out of range adds nothing: row 0 stands in for it
+            if (v == -INFINITY || id[j] < 0 || id[j] >= a.V) id[j] = -1;
         }
-        if (lane == 0) a.student[row * K + k] = sum;
+        for (int64_t d = lane * 8; d < a.D; d += 512) {
+            float x[8];
+            load8(a.X, row * a.ldx + d, a.dtype, a.vec, a.D - d, x);
+            float w[kTogether][8];
+#pragma unroll
+            for (int j = 0; j < kTogether; ++j) load8(a.W, max(id[j], (int64_t)0) * a.ldw + d, a.dtype, a.vec, a.D - d, w[j]);
+#pragma unroll
+            for (int j = 0; j < kTogether; ++j)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum[j] = id[j] < 0 ? sum[j] : fmaf(x[e], w[j][e], sum[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kTogether; ++j) {
+            sum[j] = wave_sum(sum[j]) * a.teacher.scale;
+            if (lane == j && k0 + j < K) a.student[row * K + k0 + j] = sum[j];
+        }
     }
 }
 
@@ -261,15 +302,19 @@ __device__ __forceinline__ void put_coef(const CoefArgs &a, int64_t row, float c
     a.coef[row] = c;
 }
 
+template <int WAVES>
 __device__ __forceinline__ void put_block_max(const CoefArgs &a, int64_t block, int exponent)
 {
     if (!a.half) return;
-    __shared__ int best[4];
+    __shared__ int best[WAVES];
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) exponent = max(exponent, __shfl_xor(exponent, d));
     if ((threadIdx.x & 63) == 0) best[threadIdx.x >> 6] = exponent;
     __syncthreads();
-    if (threadIdx.x == 0) a.block_max[block] = max(max(best[0], best[1]), max(best[2], best[3]));
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < WAVES; ++w) exponent = max(exponent, best[w]);
+        a.block_max[block] = exponent;
+    }
 }
 
 __global__ __launch_bounds__(256) void linear_ce_coef_kernel(CoefArgs a)
@@ -280,31 +325,28 @@ __global__ __launch_bounds__(256) void linear_ce_coef_kernel(CoefArgs a)
         const int64_t y = a.target[row];
         put_coef(a, row, y == a.ignore ? 0.0f : y < 0 || y >= a.V ? NAN : grad_of(a, row), exponent);
     }
-    put_block_max(a, blockIdx.x, exponent);
+    put_block_max<4>(a, blockIdx.x, exponent);
 }
 
-// 256 rows a work-group, a wavefront a row at a time.
-__global__ __launch_bounds__(256) void linear_kd_coef_kernel(CoefArgs a, Teacher t)
+// A wavefront a row.
+__global__ __launch_bounds__(1024) void linear_kd_coef_kernel(CoefArgs a, Teacher t)
 {
+    const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
-    int best = kNoExponent;
-    for (int i = threadIdx.x >> 6; i < 256; i += 4) {
-        const int64_t row = (int64_t)blockIdx.x * 256 + i;
-        if (row >= a.T) break;
+    int exponent = kNoExponent;
+    if (row < a.T) {
         bool any = false, bad = false;
         for (int k = lane; k < t.K; k += 64) {
-            if (load_as_float(t.logits, row * t.ld_logits + k, t.dtype) == -INFINITY) continue;
             const int64_t id = t.ids[row * t.ld_ids + k];
+            if (load_as_float(t.logits, row * t.ld_logits + k, t.dtype) == -INFINITY) continue;
             any = true;
             bad |= id < 0 || id >= a.V;
         }
         any = __any(any);
         bad = __any(bad);
-        int exponent = kNoExponent;
         if (lane == 0) put_coef(a, row, !any ? 0.0f : bad ? NAN : grad_of(a, row), exponent);
-        best = max(best, exponent);
     }
-    put_block_max(a, blockIdx.x, best);
+    put_block_max<16>(a, blockIdx.x, exponent);
 }
 
 // A wavefront a row.  An id that comes twice holds the sum of its entries in
@@ -353,15 +395,31 @@ __device__ __forceinline__ void store_as(void *p, int64_t at, tgemm_dtype_t dtyp
     else ((_Float16 *)p)[at] = (_Float16)v;
 }
 
+// Four columns a thread; the parts' rows are padded to a multiple of 64.
 __global__ __launch_bounds__(256) void linear_sum_kernel(SumArgs a)
 {
-    const int64_t total = a.T * a.D;
+    const int64_t per_row = (a.D + 3) / 4, total = a.T * per_row;
     for (int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x; p < total; p += (int64_t)gridDim.x * 256) {
-        const int64_t row = p / a.D, col = p - row * a.D;
-        float v = 0.0f;
-        for (int s = 0; s < a.count; ++s) v += a.part[s * a.stride + row * a.ld + col];
+        const int64_t row = p / per_row, col = (p - row * per_row) * 4;
+        const float *part = a.part + row * a.ld + col;
+        m16::f32x4 v = *(const m16::f32x4 *)part;
+        for (int s = 1; s < a.count; ++s) v += *(const m16::f32x4 *)(part + s * a.stride);
         if (a.row_scale != nullptr) v *= a.row_scale[row];
-        store_as(a.out, row * a.ldo + col, a.dtype, v);
+        const int64_t at = row * a.ldo + col;
+        if (a.vec && col + 4 <= a.D) {
+            if (a.dtype == TGEMM_F32) {
+                *(m16::f32x4 *)((float *)a.out + at) = v;
+            } else {
+                uint16_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = a.dtype == TGEMM_BF16 ? bits((__bf16)v[e]) : bits((_Float16)v[e]);
+                *(uint2 *)((uint16_t *)a.out + at) = make_uint2(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (col + e < a.D) store_as(a.out, at + e, a.dtype, v[e]);
+        }
     }
 }
 
@@ -410,9 +468,9 @@ hipError_t launch_pick(const PickArgs &a, hipStream_t stream)
 
 hipError_t launch_coef(const CoefArgs &a, hipStream_t stream)
 {
-    const unsigned blocks = (unsigned)((a.T + 255) / 256);
+    const unsigned blocks = (unsigned)coef_blocks(a.T, a.teacher != nullptr);
     if (a.teacher == nullptr) linear_ce_coef_kernel<<<blocks, 256, 0, stream>>>(a);
-    else linear_kd_coef_kernel<<<blocks, 256, 0, stream>>>(a, *a.teacher);
+    else linear_kd_coef_kernel<<<blocks, 1024, 0, stream>>>(a, *a.teacher);
     return hipGetLastError();
 }
 
@@ -424,7 +482,7 @@ hipError_t launch_scatter(const ScatterArgs &a, hipStream_t stream)
 
 hipError_t launch_sum(const SumArgs &a, hipStream_t stream)
 {
-    linear_sum_kernel<<<blocks_for(a.T * a.D), 256, 0, stream>>>(a);
+    linear_sum_kernel<<<blocks_for(a.T * ((a.D + 3) / 4)), 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 

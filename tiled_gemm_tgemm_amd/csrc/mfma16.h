@@ -6,9 +6,9 @@
 //   formed transposed (B's fragment is the instruction's first operand), so a
 //   lane holds 16 columns of one row of C: sums along a row of C stay within
 //   a lane and its partner, and a row's values leave in 16-byte pieces.
-// * K runs in steps of 64.  A step's slices of A and B go from device memory
-//   straight into LDS, 16 bytes a lane, into one of two stages; the loads of
-//   the next step are under way while a step is multiplied.
+// * K runs in steps of BK.  A step's slices of A and B go from device memory
+//   straight into LDS, 16 bytes a lane, into one of STAGES stages; the loads of
+//   the next steps are under way while a step is multiplied.
 // * The order of the 32 columns of a block is free as long as the reader of C
 //   knows it: column 16·h + 4·q + r of C sits at index 8·q + 4·h + r of the
 //   instruction, which is what gives lane half h the 16 adjacent columns
@@ -20,7 +20,7 @@
 // which the transposing LDS read gathers four values of k a lane.  The loads
 // into LDS write 16-byte pieces in lane order, so the pieces are permuted on
 // the reading side of device memory, within a cache line: piece c of a KC row
-// goes to c ^ (row & 7), and the 64-byte quarter-lines of an MC row are
+// goes to c ^ (row / 2 & 7), and the 64-byte quarter-lines of an MC row are
 // exchanged by the row's k.  Without that the 32 rows of a KC fragment would
 // start in the same banks, as would the four rows of a transposing read.
 #pragma once
@@ -51,7 +51,7 @@ struct Operands {
     int segments;              // 1, or 6: the plane pairs of kPairs
     int M, N;
     int steps;                 // steps of 64 along K
-    int steps_per_split;       // blockIdx.y takes steps [y·this, (y+1)·this)
+    int steps_per_split;       // part y of the sum takes steps [y·this, (y+1)·this)
     int mn_a, mn_b;            // KC: rows of A / B; MC: columns that may be read, a multiple of 8
     int k_a, k_b;              // MC: rows (values of k) of A / B
     int tiles_m, tiles_n;
@@ -83,16 +83,39 @@ struct Frag<_Float16> {
     }
 };
 
+// A 16-byte read of a KC fragment takes 16 rows at a time, which span 16·2·BK
+// bytes; each of them finds its piece in another 16 bytes of the 256 that the
+// banks are wide.
+template <int BK>
+__device__ __forceinline__ constexpr int swizzle(int row) { return BK == 64 ? (row >> 1) & 7 : (row >> 2) & 3; }
+
 typedef __attribute__((address_space(3))) char lds_char;
-typedef const __attribute__((address_space(1))) char global_char;
+
+// 16 bytes a lane from base + offset to 16 adjacent bytes a lane from `to` (the
+// same in all lanes).  The builtin for this makes the compiler wait for all
+// such loads before the next LDS read that it cannot tell apart, which every
+// transposing read is; arrive() does the waiting here.  Nothing is returned in
+// a register.  m0 is reserved, which the compiler warns about where it is named
+// as overwritten; it keeps nothing there.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void load_lds(const char *base, uint32_t offset, lds_char *to)
+{
+    const uint32_t at = (uint32_t)(uintptr_t)to;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(offset), "s"(base)
+                 : "memory", "m0");
+}
+#pragma clang diagnostic pop
 
 // One operand's slices: where this thread's 16-byte pieces come from.
-template <int MN, int THREADS, bool MC, bool PERMUTE>
+template <int MN, int BK, int THREADS, bool MC, bool PERMUTE>
 struct Loader {
-    static constexpr int kBytes = MN * kStepK * 2;
+    static constexpr int kBytes = MN * BK * 2;
     static constexpr int kRounds = kBytes / 16 / THREADS;
     static_assert(kRounds * 16 * THREADS == kBytes, "whole rounds");
-    static constexpr int kRowPieces = MC ? MN / 8 : 8;
+    static constexpr int kRowPieces = MC ? MN / 8 : BK / 8;
     uint32_t off[kRounds];
 
     static __device__ __forceinline__ int piece(int r) { return r * THREADS + (int)threadIdx.x; }
@@ -113,27 +136,21 @@ struct Loader {
             } else {
                 int mn = row;
                 if constexpr (PERMUTE) mn = (row & ~31) | ((row & 4) << 2) | ((row & 24) >> 1) | (row & 3);
-                off[r] = ((uint32_t)min(mn, mn_last) * (uint32_t)ld + (uint32_t)((slot ^ (row & 7)) * 8)) * 2u;
+                off[r] = ((uint32_t)min(mn, mn_last) * (uint32_t)ld + (uint32_t)((slot ^ swizzle<BK>(row)) * 8)) * 2u;
             }
         }
     }
 
-    __device__ __forceinline__ void issue(const char *base, lds_char *stage, int wave) const
+    __device__ __forceinline__ void issue_one(const char *base, lds_char *stage, int wave, int r) const
     {
-#pragma unroll
-        for (int r = 0; r < kRounds; ++r) {
-            // kept as 32 bits in the loop: the load then adds it to the scalar base by itself
-            uint32_t o = off[r];
-            asm volatile("" : "+v"(o));
-            __builtin_amdgcn_global_load_lds((global_char *)(base + o), stage + (r * THREADS + wave * 64) * 16, 16, 0, 0);
-        }
+        load_lds(base, off[r], stage + (r * THREADS + wave * 64) * 16);
     }
 };
 
 // Byte offsets of a wavefront's fragments in a slice.
-template <int MN, int F, bool MC, bool PERMUTE>
+template <int MN, int BK, int F, bool MC, bool PERMUTE>
 struct Reader {
-    int at[MC ? F : 4];
+    int at[MC ? F : BK / 16];
 
     // mn: the wavefront's first row or column in the tile
     __device__ __forceinline__ void place(int mn, int lane)
@@ -148,7 +165,7 @@ struct Reader {
         } else {
             const int l32 = lane & 31, half = lane >> 5;
 #pragma unroll
-            for (int s = 0; s < 4; ++s) at[s] = (mn + l32) * 128 + (((2 * s + half) ^ (l32 & 7)) * 16);
+            for (int s = 0; s < BK / 16; ++s) at[s] = (mn + l32) * (2 * BK) + (((2 * s + half) ^ swizzle<BK>(l32)) * 16);
         }
     }
 
@@ -164,55 +181,74 @@ struct Reader {
             return __builtin_bit_cast(V, v);
         } else {
             typedef __attribute__((address_space(3))) V ldsv;
-            return *(ldsv *)(slice + at[s] + f * 32 * 128);
+            return *(ldsv *)(slice + at[s] + f * 32 * (2 * BK));
         }
     }
 };
 
-// The work-group's loads into LDS have arrived, and its reads of LDS are done.
-// A barrier's fence does not by itself wait for loads that write LDS.
+// The work-group's loads into LDS have arrived but for the last FLYING of each
+// thread, and its reads of LDS are done.  The compiler's own barrier would not
+// wait for loads that write LDS.
+template <int FLYING>
 __device__ __forceinline__ void arrive()
 {
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+    __builtin_amdgcn_s_waitcnt((FLYING & 15) | (FLYING >> 4) << 14 | 7 << 4);  // vmcnt(FLYING) lgkmcnt(0)
     __syncthreads();
+}
+
+// The hardware deals work-groups round-robin to eight XCDs with an L2 each;
+// XCD x takes the x-th run of logical ids, as in mfma::tile_of.  Ids walk the
+// tiles of one part of the sum, then those of the next (parts share nothing),
+// and within a part groups of 8 tile rows column by column, so that the
+// work-groups of an XCD share rows of A and columns of B.
+__device__ __forceinline__ void place_tile(int tiles_m, int tiles_n, int &tm, int &tn, int &split)
+{
+    const int groups = gridDim.x, q = groups / mfma::kXcds, r = groups % mfma::kXcds;
+    const int x = blockIdx.x % mfma::kXcds;
+    const int logical = blockIdx.x / mfma::kXcds + x * q + min(x, r);
+    const int tiles = tiles_m * tiles_n;
+    split = logical / tiles;
+    const int tile = logical - split * tiles, per_group = 8 * tiles_n;
+    const int group = tile / per_group, in_group = tile - group * per_group;
+    const int rows = min(tiles_m - group * 8, 8);
+    tm = group * 8 + in_group % rows;
+    tn = in_group / rows;
 }
 
 struct Yes { static constexpr bool value = true; };
 struct No { static constexpr bool value = false; };
 
-// Scheduling hints: READS LDS reads and LOADS loads spread evenly among MFMAS
-// matrix instructions.
-template <int MFMAS, int READS, int LOADS, int I = 0>
+// Scheduling hints: READS LDS reads spread evenly among MFMAS matrix
+// instructions.
+template <int MFMAS, int READS, int I = 0>
 __device__ __forceinline__ void spread()
 {
     if constexpr (I < MFMAS) {
         constexpr int reads = (I + 1) * READS / MFMAS - I * READS / MFMAS;
-        constexpr int loads = (I + 1) * LOADS / MFMAS - I * LOADS / MFMAS;
         if constexpr (reads > 0) __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);
-        if constexpr (loads > 0) __builtin_amdgcn_sched_group_barrier(0x020, loads, 0);
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        spread<MFMAS, READS, LOADS, I + 1>();
+        spread<MFMAS, READS, I + 1>();
     }
 }
 
 // A tile of C.  After run(), lane (l32 = lane & 31, half = lane >> 5) holds in
 // acc[i][j][r] row row0 + i·32 + l32, column col0 + j·32 + 16·half + r.
-template <class E, int BM, int BN, int WM, int WN, bool A_MC, bool B_MC>
+template <class E, int BM, int BN, int WM, int WN, bool A_MC, bool B_MC, int BK, int STAGES>
 struct TileProduct {
     static constexpr int kThreads = 64 * WM * WN;
     static constexpr int FM = BM / WM / 32, FN = BN / WN / 32;
-    static constexpr int kStage = (BM + BN) * kStepK * 2;
-    static constexpr int kLds = 2 * kStage;
+    static constexpr int kStage = (BM + BN) * BK * 2;
+    static constexpr int kLds = STAGES * kStage;
 
     f32x16 acc[FM][FN];
-    int row0, col0;
+    int row0, col0, split;
 
     __device__ __forceinline__ void run(const Operands &p, lds_char *lds)
     {
         const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
         const int wm = wave / WN, wn = wave % WN;
         int tm, tn;
-        mfma::tile_of(p.tiles_m, p.tiles_n, 8, tm, tn);
+        place_tile(p.tiles_m, p.tiles_n, tm, tn, split);
         const int m0 = tm * BM, n0 = tn * BN;
         row0 = m0 + wm * (FM * 32);
         col0 = n0 + wn * (FN * 32);
@@ -223,55 +259,61 @@ struct TileProduct {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
-        const int first = blockIdx.y * p.steps_per_split;
-        const int last = min(p.steps, first + p.steps_per_split);
+        const int first = split * p.steps_per_split * (kStepK / BK);
+        const int last = min(p.steps * (kStepK / BK), first + p.steps_per_split * (kStepK / BK));
         if (first >= last) return;
 
-        Loader<BM, kThreads, A_MC, false> la;
-        Loader<BN, kThreads, B_MC, true> lb;
-        Reader<BM, FM, A_MC, false> ra;
-        Reader<BN, FN, B_MC, true> rb;
+        Loader<BM, BK, kThreads, A_MC, false> la;
+        Loader<BN, BK, kThreads, B_MC, true> lb;
+        Reader<BM, BK, FM, A_MC, false> ra;
+        Reader<BN, BK, FN, B_MC, true> rb;
         ra.place(wm * (FM * 32), lane);
         rb.place(wn * (FN * 32), lane);
         const int a_last = A_MC ? p.mn_a - 8 - m0 : p.mn_a - 1 - m0;
         const int b_last = B_MC ? p.mn_b - 8 - n0 : p.mn_b - 1 - n0;
-        la.place(p.lda, a_last, A_MC ? p.k_a - 1 - first * kStepK : 0);
-        lb.place(p.ldb, b_last, B_MC ? p.k_b - 1 - first * kStepK : 0);
+        // An MC operand may end inside a step or before its last ones (K is
+        // padded to 64): such a step starts at the last row at the latest.
+        auto start = [](int k, int rows) { return min(k * BK, rows - 1); };
+        if constexpr (A_MC) la.place(p.lda, a_last, p.k_a - 1 - start(first, p.k_a));
+        else la.place(p.lda, a_last, 0);
+        if constexpr (B_MC) lb.place(p.ldb, b_last, p.k_b - 1 - start(first, p.k_b));
+        else lb.place(p.ldb, b_last, 0);
         const char *A = (const char *)p.A + (A_MC ? (int64_t)m0 : (int64_t)m0 * p.lda) * 2;
         const char *B = (const char *)p.B + (B_MC ? (int64_t)n0 : (int64_t)n0 * p.ldb) * 2;
-        const int64_t step_a = (A_MC ? (int64_t)kStepK * p.lda : (int64_t)kStepK) * 2;
-        const int64_t step_b = (B_MC ? (int64_t)kStepK * p.ldb : (int64_t)kStepK) * 2;
-
         // where the next loads come from
         int seg = 0, k = first;
         const char *from_a = nullptr, *from_b = nullptr;
         auto seek = [&]() {
-            from_a = A + k * step_a;
-            from_b = B + k * step_b;
+            const int start_a = A_MC ? start(k, p.k_a) : k * BK, start_b = B_MC ? start(k, p.k_b) : k * BK;
+            from_a = A + (A_MC ? start_a * p.lda : (int64_t)start_a) * 2;
+            from_b = B + (B_MC ? start_b * p.ldb : (int64_t)start_b) * 2;
             if (p.segments > 1) {
                 from_a += ((kPairsA >> (2 * seg)) & 3) * p.plane_a * 2;
                 from_b += ((kPairsB >> (2 * seg)) & 3) * p.plane_b * 2;
             }
             // the last rows of an MC operand, and back to whole steps for the next segment
-            if (A_MC && ((k + 1) * kStepK > p.k_a || (p.segments > 1 && k == first)))
-                la.place(p.lda, a_last, p.k_a - 1 - k * kStepK);
-            if (B_MC && ((k + 1) * kStepK > p.k_b || (p.segments > 1 && k == first)))
-                lb.place(p.ldb, b_last, p.k_b - 1 - k * kStepK);
+            if (A_MC && ((k + 1) * BK > p.k_a || (p.segments > 1 && k == first))) la.place(p.lda, a_last, p.k_a - 1 - start_a);
+            if (B_MC && ((k + 1) * BK > p.k_b || (p.segments > 1 && k == first))) lb.place(p.ldb, b_last, p.k_b - 1 - start_b);
             if (++k == last) {
                 k = first;
                 ++seg;
             }
         };
-        auto issue = [&](int stage) {
-            la.issue(from_a, lds + stage * kStage, wave);
-            lb.issue(from_b, lds + stage * kStage + BM * kStepK * 2, wave);
+        constexpr int kLoadsA = decltype(la)::kRounds, kLoads = kLoadsA + decltype(lb)::kRounds;
+        auto issue = [&](int stage, int lo, int hi) {
+#pragma unroll
+            for (int r = 0; r < kLoads; ++r) {
+                if (r < lo || r >= hi) continue;
+                if (r < kLoadsA) la.issue_one(from_a, lds + stage * kStage, wave, r);
+                else lb.issue_one(from_b, lds + stage * kStage + BM * BK * 2, wave, r - kLoadsA);
+            }
         };
 
         // Two sets of fragments: those of the next 16 values of k are read
         // while these are multiplied.
         typename Frag<E>::type a[2][FM], b[2][FN];
         auto read = [&](int stage, int s) {
-            lds_char *as = lds + stage * kStage, *bs = as + BM * kStepK * 2;
+            lds_char *as = lds + stage * kStage, *bs = as + BM * BK * 2;
 #pragma unroll
             for (int j = 0; j < FN; ++j) b[s & 1][j] = rb.template read<E>(bs, j, s);
 #pragma unroll
@@ -284,48 +326,53 @@ struct TileProduct {
                 for (int j = 0; j < FN; ++j) acc[i][j] = Frag<E>::mfma(b[s & 1][j], a[s & 1][i], acc[i][j]);
         };
         constexpr int kReads = FM * (A_MC ? 2 : 1) + FN * (B_MC ? 2 : 1);
-        constexpr int kLoads = decltype(la)::kRounds + decltype(lb)::kRounds;
 
         // A step on the slices of `stage`, its first fragments read.  The
-        // barrier stands before the last quarter, whose fragments are in
-        // registers by then: this stage is read no more, so the loads of the
-        // step after next go there, and the next step's slices have arrived,
-        // so its first fragments are read under the last quarter's products.
-        auto step = [&](int stage, auto load, auto next) {
+        // barrier stands before the last 16 values of k, whose fragments are
+        // in registers by then: this stage is read no more, so the loads of
+        // the step STAGES further on go there, and the next step's slices
+        // have arrived, so its first fragments are read under these products.
+        constexpr int kSubs = BK / 16;
+        auto step = [&](int stage, int after, auto load, auto next) {
 #pragma unroll
-            for (int s = 0; s < 3; ++s) {
+            for (int s = 0; s < kSubs - 1; ++s) {
                 read(stage, s + 1);
                 multiply(s);
-                spread<FM * FN, kReads, 0>();
+                spread<FM * FN, kReads>();
             }
             if constexpr (decltype(next)::value) {
-                arrive();
-                if constexpr (decltype(load)::value) issue(stage);
-                read(stage ^ 1, 0);
+                if constexpr (decltype(load)::value) arrive<(STAGES - 2) * kLoads>();
+                else arrive<0>();
+                read(after, 0);
             }
-            multiply(3);
-            spread<FM * FN, decltype(next)::value ? kReads : 0, decltype(load)::value ? kLoads : 0>();
+#pragma unroll
+            for (int m = 0; m < FM * FN; ++m) {
+                if constexpr (decltype(load)::value) issue(stage, m * kLoads / (FM * FN), (m + 1) * kLoads / (FM * FN));
+                const int i = m / FN, j = m % FN, s = (kSubs - 1) & 1;
+                acc[i][j] = Frag<E>::mfma(b[s][j], a[s][i], acc[i][j]);
+            }
         };
 
         const int total = (last - first) * p.segments;
-        seek();
-        issue(0);
-        if (total > 1) {
+        int ahead = 0;
+        for (; ahead < STAGES && ahead < total; ++ahead) {
             seek();
-            issue(1);
+            issue(ahead, 0, kLoads);
         }
-        arrive();
+        arrive<0>();
         read(0, 0);
-        int n = 0;
-        for (; n + 2 < total; ++n) {
+        int n = 0, stage = 0;
+        auto following = [](int st) { return st + 1 == STAGES ? 0 : st + 1; };
+        for (; n + STAGES < total; ++n) {
             seek();
-            step(n & 1, Yes{}, Yes{});
+            step(stage, following(stage), Yes{}, Yes{});
+            stage = following(stage);
         }
-        if (n + 1 < total) {
-            step(n & 1, No{}, Yes{});
-            ++n;
+        for (; n + 1 < total; ++n) {
+            step(stage, following(stage), No{}, Yes{});
+            stage = following(stage);
         }
-        step(n & 1, No{}, No{});
+        step(stage, stage, No{}, No{});
     }
 };
 
