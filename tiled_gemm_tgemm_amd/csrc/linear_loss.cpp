@@ -131,6 +131,9 @@ Choice choose_tile(int64_t M, int64_t N, int64_t steps, bool split = false)
     return best;
 }
 
+// The parts of a sum of `steps` steps, at most `most`, none of them empty.
+int parts_of(int64_t steps, int64_t most) { return (int)ceil_div(steps, ceil_div(steps, most)); }
+
 // Where a call's buffers lie in its workspace.
 struct Plan {
     bool half = false;
@@ -204,7 +207,7 @@ bool plan_backward(Plan &p, const Head &h)
     p.dw_tile = choose_tile(p.piece, h.D, p.Tp / kStepK * seg).tile;
     const Choice dx = choose_tile(h.T, h.D, p.piece / kStepK * seg, true);
     p.dx_tile = dx.tile;
-    p.dx_splits = dx.splits;
+    p.dx_splits = parts_of(ceil_div(h.V < p.piece ? h.V : p.piece, kStepK), dx.splits);
     p.dx_direct = p.pieces == 1 && p.dx_splits == 1;
     p.coef = p.take(h.T * 4);
     if (p.half) {
@@ -229,6 +232,7 @@ Operands operands(const Plan &p, int64_t M, int64_t N, int64_t steps, int tile)
     o.steps = o.steps_per_split = (int)steps;
     o.tiles_m = (int)ceil_div(M, s.bm);
     o.tiles_n = (int)ceil_div(N, s.bn);
+    o.splits = 1;
     return o;
 }
 
@@ -412,7 +416,9 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
         if (dX != nullptr) {
             OutArgs o{};
             o.op = operands(p, h.T, h.D, cols_steps, p.dx_tile);
-            o.op.steps_per_split = (int)ceil_div(cols_steps, p.dx_splits);
+            // the last piece may take fewer parts; the others' sums stand
+            o.op.splits = parts_of(cols_steps, p.dx_splits);
+            o.op.steps_per_split = (int)ceil_div(cols_steps, o.op.splits);
             o.op.A = g;
             o.op.lda = p.ldg;
             o.op.plane_a = plane_g;
@@ -422,7 +428,6 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
             o.op.plane_b = w.plane;
             o.op.mn_b = (int)p.Dp;
             o.op.k_b = (int)(h.V - v0);
-            o.splits = p.dx_splits;
             if (p.dx_direct) {
                 o.out = dX;
                 o.ldo = lddx;
@@ -457,7 +462,6 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
             o.ldo = lddw;
             o.dtype = h.dtype;
             o.vec = rows16(dW, lddw, h.dtype);
-            o.splits = 1;
             o.all_scale = in<float>(ws, p.all_scale);
             e = launch_dw(p.half, p.dw_tile, o, stream);
             if (e != hipSuccess) return from_hip(e);

@@ -65,7 +65,6 @@ struct OutArgs {
     bool vec;                // out and its rows 16-byte aligned
     bool add;                // float32 out: add to what is there
     int64_t split_stride;    // elements between the outputs of the sum's parts
-    int splits;
     const float *row_scale;  // or NULL
     const float *all_scale;  // or NULL
 };

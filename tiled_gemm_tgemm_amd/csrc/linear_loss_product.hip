@@ -7,7 +7,6 @@ namespace tgemm {
 namespace loss {
 namespace {
 
-using m16::f32x16;
 using m16::f32x4;
 using m16::lds_char;
 using m16::Operands;
@@ -15,56 +14,83 @@ using m16::TileProduct;
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// Columns past the last of the vocabulary do not count; a wavefront's
-// columns are 16 per lane and block, so a row's maximum and sum take the
-// lane's own values and one exchange with the lane of the other half.
+// a·b, where 0 times anything, NaN and infinity too, is 0.
+__device__ __forceinline__ float mul_zero(float a, float b)
+{
+    float r;
+    asm("v_mul_legacy_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+
+// A row's adjacent columns that a lane holds.
+template <class Tile>
+constexpr int kHeld = 4 * Tile::FN;
+
+// Columns past the last of the vocabulary do not count.  A row's maximum and
+// sum take the lane's own values and two exchanges with the three lanes that
+// hold the rest of the row.
 template <class E, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void linear_stats_kernel(StatsArgs a)
 {
-    typedef TileProduct<E, BM, BN, WM, WN, false, false, 64, 2> Tile;
+    typedef TileProduct<E, BM, BN, WM, WN, false, false> Tile;
+    constexpr int H = kHeld<Tile>;
     __shared__ __align__(1024) char lds[Tile::kLds];
-    Tile t;
-    t.run(a.op, (lds_char *)lds);
-
-    const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5;
     const float scale2 = a.scale * kLog2e;
-    const int group = t.col0 / (Tile::FN * 32);
+    Tile::run(a.op, (lds_char *)lds, [&](typename Tile::Acc &acc, int row0, int col0, int) {
+        const int lane = m16::thread_anew() & 63, l16 = lane & 15, quarter = lane >> 4;
+        const int left = a.op.N - (col0 + H * quarter);  // this lane's columns that exist
+        if (a.op.N - col0 < Tile::FN * 16) {
 #pragma unroll
-    for (int i = 0; i < Tile::FM; ++i) {
-        const int row = t.row0 + i * 32 + l32;
-        if (a.target != nullptr && row < a.op.M) {
-            const int64_t want = a.target[row] - (t.col0 + 16 * half);
+            for (int i = 0; i < Tile::FM; ++i)
 #pragma unroll
-            for (int j = 0; j < Tile::FN; ++j) {
-                const int64_t r = want - j * 32;
-                if (r >= 0 && r < 16 && want + t.col0 + 16 * half < a.op.N) {
-                    float z = 0.0f;
+                for (int e = 0; e < H; ++e)
+                    if (e >= left) acc[i][e / 4][e % 4] = -INFINITY;
+        }
+        if (a.target != nullptr) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) z = r == e ? t.acc[i][j][e] : z;
-                    a.picked[row] = z * a.scale;
-                }
+            for (int i = 0; i < Tile::FM; ++i) {
+                const int row = row0 + i * 16 + l16;
+                if (row >= a.op.M) continue;
+                const int64_t want = a.target[row] - (col0 + H * quarter);
+                if (want < 0 || want >= min(left, H)) continue;
+                float z = 0.0f;
+#pragma unroll
+                for (int e = 0; e < H; ++e) z = want == e ? acc[i][e / 4][e % 4] : z;
+                a.picked[row] = z * a.scale;
             }
         }
-        float high = -INFINITY;
+        // the scale is positive, so the largest product is the largest logit
+        float high[Tile::FM], sum[Tile::FM];
 #pragma unroll
-        for (int j = 0; j < Tile::FN; ++j)
+        for (int i = 0; i < Tile::FM; ++i) {
+            high[i] = acc[i][0][0];
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const float z = t.col0 + j * 32 + 16 * half + r < a.op.N ? t.acc[i][j][r] * scale2 : -INFINITY;
-                t.acc[i][j][r] = z;
-                high = fmaxf(high, z);
+            for (int e = 1; e < H; ++e) high[i] = fmaxf(high[i], acc[i][e / 4][e % 4]);
+        }
+#pragma unroll
+        for (int i = 0; i < Tile::FM; ++i) high[i] = fmaxf(high[i], __shfl_xor(high[i], 16));
+#pragma unroll
+        for (int i = 0; i < Tile::FM; ++i) high[i] = fmaxf(high[i], __shfl_xor(high[i], 32)) * scale2;
+#pragma unroll
+        for (int i = 0; i < Tile::FM; ++i) {
+            const float from = high[i] == -INFINITY ? 0.0f : high[i];
+            sum[i] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < H; ++e) sum[i] += __builtin_amdgcn_exp2f(fmaf(acc[i][e / 4][e % 4], scale2, -from));
+        }
+#pragma unroll
+        for (int i = 0; i < Tile::FM; ++i) sum[i] += __shfl_xor(sum[i], 16);
+#pragma unroll
+        for (int i = 0; i < Tile::FM; ++i) sum[i] += __shfl_xor(sum[i], 32);
+        const int group = col0 / (Tile::FN * 16);
+        if (quarter == 0 && group < a.groups) {
+#pragma unroll
+            for (int i = 0; i < Tile::FM; ++i) {
+                const int row = row0 + i * 16 + l16;
+                if (row < a.op.M) a.part[(int64_t)row * a.groups + group] = make_float2(high[i], sum[i]);
             }
-        high = fmaxf(high, __shfl_xor(high, 32));
-        const float from = high == -INFINITY ? 0.0f : high;
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < Tile::FN; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) sum += __builtin_amdgcn_exp2f(t.acc[i][j][r] - from);
-        sum += __shfl_xor(sum, 32);
-        if (half == 0 && row < a.op.M && group < a.groups)
-            a.part[(int64_t)row * a.groups + group] = make_float2(high, sum);
-    }
+        }
+    });
 }
 
 __device__ __forceinline__ uint32_t pack(__bf16 a, __bf16 b)
@@ -76,72 +102,84 @@ __device__ __forceinline__ uint32_t pack(_Float16 a, _Float16 b)
     return (uint32_t)__builtin_bit_cast(uint16_t, a) | (uint32_t)__builtin_bit_cast(uint16_t, b) << 16;
 }
 
-template <class E>
-__device__ __forceinline__ void store16(E *to, const float (&v)[16])
+// N (a multiple of 8) adjacent values as 16-bit numbers, 16-byte aligned.
+template <class E, int N>
+__device__ __forceinline__ void store_packed(E *to, const float (&v)[N])
 {
-    uint32_t w[8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) w[q] = pack((E)v[2 * q], (E)v[2 * q + 1]);
-    uint4 *p = reinterpret_cast<uint4 *>(to);
-    p[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    p[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    for (int q = 0; q < N / 8; ++q) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = pack((E)v[8 * q + 2 * e], (E)v[8 * q + 2 * e + 1]);
+        reinterpret_cast<uint4 *>(to)[q] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
 }
 
 template <class E, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void linear_grad_kernel(GradArgs a)
 {
-    typedef TileProduct<E, BM, BN, WM, WN, false, false, 64, 2> Tile;
+    typedef TileProduct<E, BM, BN, WM, WN, false, false> Tile;
+    constexpr int H = kHeld<Tile>;
     __shared__ __align__(1024) char lds[Tile::kLds];
-    Tile t;
-    t.run(a.op, (lds_char *)lds);
-
-    const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5;
+    Tile::run(a.op, (lds_char *)lds, [&](typename Tile::Acc &acc, int row0, int col0, int) {
+        const int lane = m16::thread_anew() & 63, l16 = lane & 15, quarter = lane >> 4;
+        const int col = col0 + H * quarter;
+        if (col >= a.ldg) return;
 #pragma unroll
-    for (int i = 0; i < Tile::FM; ++i) {
-        const int row = t.row0 + i * 32 + l32;
-        if (row >= a.rows) continue;
-        const bool real = row < a.op.M;
-        const float c = real ? a.coef[row] : 0.0f;
-        const float lse = real ? a.lse[row] : 0.0f;
-        const int64_t want = real && a.target != nullptr ? a.target[row] - a.v0 : -1;
+        for (int i = 0; i < Tile::FM; ++i) {
+            const int row = row0 + i * 16 + l16;
+            if (row >= a.rows) continue;
+            const bool real = row < a.op.M;
+            const float c = real ? a.coef[row] : 0.0f;
+            const float lse = !real ? 0.0f : c == c ? a.lse[row] : c;
+            const int64_t want = real && a.target != nullptr ? a.target[row] - a.v0 - col : -1;
+            float g[H];
+            // in 16 bits the exponent's argument may be rounded once more
+            if (a.planes == 1) {
+                const float scale2 = a.scale * kLog2e, lse2 = lse * kLog2e;
 #pragma unroll
-        for (int j = 0; j < Tile::FN; ++j) {
-            const int col = t.col0 + j * 32 + 16 * half;
-            if (col >= a.ldg) continue;
-            float g[16];
+                for (int e = 0; e < H; ++e) g[e] = __builtin_amdgcn_exp2f(fmaf(acc[i][e / 4][e % 4], scale2, -lse2));
+            } else {
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const float p = __builtin_amdgcn_exp2f(fmaf(t.acc[i][j][r], a.scale, -lse) * kLog2e);
-                // a row that does not count is zero whatever its logits are
-                g[r] = c != 0.0f && col + r < a.op.N ? c * (col + r == want ? p - 1.0f : p) : 0.0f;
+                for (int e = 0; e < H; ++e) g[e] = __builtin_amdgcn_exp2f(fmaf(acc[i][e / 4][e % 4], a.scale, -lse) * kLog2e);
             }
+            if (want >= 0 && want < H) {
+#pragma unroll
+                for (int e = 0; e < H; ++e) g[e] = want == e ? g[e] - 1.0f : g[e];
+            }
+            if (col + H > a.op.N) {
+#pragma unroll
+                for (int e = 0; e < H; ++e) g[e] = col + e < a.op.N ? g[e] : 0.0f;
+            }
+            // 0 times anything is 0 here: a row that does not count is zero
+            // whatever its logits are
+#pragma unroll
+            for (int e = 0; e < H; ++e) g[e] = mul_zero(c, g[e]);
             E *to = (E *)a.G + (int64_t)row * a.ldg + col;
-            if constexpr (sizeof(E) == 2) {
-                if (a.planes == 1) {
-                    store16<E>(to, g);
-                } else {
+            if (a.planes == 1) {
+                store_packed<E, H>(to, g);
+            } else {
 #pragma unroll
-                    for (int q = 0; q < 3; ++q) {
-                        store16<E>(to + q * a.plane, g);
+                for (int q = 0; q < 3; ++q) {
+                    store_packed<E, H>(to + q * a.plane, g);
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) g[r] -= (float)(E)g[r];
-                    }
+                    for (int e = 0; e < H; ++e) g[e] -= (float)(E)g[e];
                 }
             }
         }
-    }
+    });
 }
 
-// 16 adjacent values of a row of the result, `left` of them inside it.
-template <class T>
-__device__ __forceinline__ void store_row(T *to, const float (&v)[16], int left, bool vec)
+// N adjacent values of a row of the result, `left` of them inside it.
+template <class T, int N>
+__device__ __forceinline__ void store_row(T *to, const float (&v)[N], int left, bool vec)
 {
-    if (vec && left >= 16) {
+    if (vec && left >= N) {
         if constexpr (sizeof(T) == 2) {
-            store16<T>(to, v);
+            store_packed<T, N>(to, v);
         } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < N / 4; ++q) {
                 f32x4 w;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w[e] = v[4 * q + e];
@@ -150,48 +188,44 @@ __device__ __forceinline__ void store_row(T *to, const float (&v)[16], int left,
         }
     } else {
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-            if (r < left) to[r] = (T)v[r];
+        for (int e = 0; e < N; ++e)
+            if (e < left) to[e] = (T)v[e];
     }
 }
 
 template <class E, int BM, int BN, int WM, int WN, bool A_MC>
 __global__ __launch_bounds__(64 * WM * WN) void linear_out_kernel(OutArgs a)
 {
-    typedef TileProduct<E, BM, BN, WM, WN, A_MC, true, BM >= 128 ? 32 : 64, BM >= 128 ? 4 : 2> Tile;
+    typedef TileProduct<E, BM, BN, WM, WN, A_MC, true> Tile;
+    constexpr int H = kHeld<Tile>;
     __shared__ __align__(1024) char lds[Tile::kLds];
-    Tile t;
-    t.run(a.op, (lds_char *)lds);
-
-    const int lane = threadIdx.x & 63, l32 = lane & 31, half = lane >> 5;
     const float all = a.all_scale != nullptr ? *a.all_scale : 1.0f;
+    Tile::run(a.op, (lds_char *)lds, [&](typename Tile::Acc &acc, int row0, int col0, int split) {
+        const int lane = m16::thread_anew() & 63, l16 = lane & 15, quarter = lane >> 4;
+        const int col = col0 + H * quarter, left = a.op.N - col;
+        if (left <= 0) return;
 #pragma unroll
-    for (int i = 0; i < Tile::FM; ++i) {
-        const int row = t.row0 + i * 32 + l32;
-        if (row >= a.op.M) continue;
-        const float s = a.row_scale != nullptr ? a.row_scale[row] * all : all;
+        for (int i = 0; i < Tile::FM; ++i) {
+            const int row = row0 + i * 16 + l16;
+            if (row >= a.op.M) continue;
+            const float s = a.row_scale != nullptr ? a.row_scale[row] * all : all;
+            float v[H];
 #pragma unroll
-        for (int j = 0; j < Tile::FN; ++j) {
-            const int col = t.col0 + j * 32 + 16 * half;
-            const int left = a.op.N - col;
-            if (left <= 0) continue;
-            float v[16];
-#pragma unroll
-            for (int r = 0; r < 16; ++r) v[r] = t.acc[i][j][r] * s;
-            const int64_t at = (int64_t)row * a.ldo + col + (int64_t)t.split * a.split_stride;
+            for (int e = 0; e < H; ++e) v[e] = acc[i][e / 4][e % 4] * s;
+            const int64_t at = (int64_t)row * a.ldo + col + (int64_t)split * a.split_stride;
             if (a.dtype == TGEMM_F32) {
                 float *to = (float *)a.out + at;
                 if (a.add) {
 #pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (r < left) v[r] += to[r];
+                    for (int e = 0; e < H; ++e)
+                        if (e < left) v[e] += to[e];
                 }
-                store_row<float>(to, v, left, a.vec);
+                store_row<float, H>(to, v, left, a.vec);
             } else {
-                store_row<E>((E *)a.out + at, v, left, a.vec);
+                store_row<E, H>((E *)a.out + at, v, left, a.vec);
             }
         }
-    }
+    });
 }
 
 constexpr TileShape kTiles[] = {
@@ -202,8 +236,15 @@ constexpr TileShape kTiles[] = {
 
 #define TGEMM_TILES(X) X(0, 256, 256, 2, 4) X(1, 128, 128, 2, 2) X(2, 32, 128, 1, 4)
 
+// As many work-groups as the GPU holds at once (a multiple of 8, so that a
+// work-group's tiles stay on its XCD).
 template <class Args>
-unsigned grid_of(const Args &a, int splits) { return (unsigned)(a.op.tiles_m * a.op.tiles_n) * (unsigned)splits; }
+unsigned grid_of(const Args &a, int tile)
+{
+    const int64_t tiles = (int64_t)a.op.tiles_m * a.op.tiles_n * a.op.splits;
+    const int64_t most = (int64_t)256 * kTiles[tile].wg_per_cu;
+    return (unsigned)(tiles < most ? tiles : most);
+}
 
 }  // namespace
 
@@ -215,8 +256,8 @@ hipError_t launch_stats(bool half, int tile, const StatsArgs &a, hipStream_t str
     switch (tile) {
 #define X(I, BM, BN, WM, WN)                                                                            \
     case I:                                                                                             \
-        if (half) linear_stats_kernel<_Float16, BM, BN, WM, WN><<<grid_of(a, 1), 64 * WM * WN, 0, stream>>>(a); \
-        else linear_stats_kernel<__bf16, BM, BN, WM, WN><<<grid_of(a, 1), 64 * WM * WN, 0, stream>>>(a);        \
+        if (half) linear_stats_kernel<_Float16, BM, BN, WM, WN><<<grid_of(a, I), 64 * WM * WN, 0, stream>>>(a); \
+        else linear_stats_kernel<__bf16, BM, BN, WM, WN><<<grid_of(a, I), 64 * WM * WN, 0, stream>>>(a);        \
         break;
         TGEMM_TILES(X)
 #undef X
@@ -229,8 +270,8 @@ hipError_t launch_grad(bool half, int tile, const GradArgs &a, hipStream_t strea
     switch (tile) {
 #define X(I, BM, BN, WM, WN)                                                                            \
     case I:                                                                                             \
-        if (half) linear_grad_kernel<_Float16, BM, BN, WM, WN><<<grid_of(a, 1), 64 * WM * WN, 0, stream>>>(a); \
-        else linear_grad_kernel<__bf16, BM, BN, WM, WN><<<grid_of(a, 1), 64 * WM * WN, 0, stream>>>(a);        \
+        if (half) linear_grad_kernel<_Float16, BM, BN, WM, WN><<<grid_of(a, I), 64 * WM * WN, 0, stream>>>(a); \
+        else linear_grad_kernel<__bf16, BM, BN, WM, WN><<<grid_of(a, I), 64 * WM * WN, 0, stream>>>(a);        \
         break;
         TGEMM_TILES(X)
 #undef X
@@ -243,8 +284,8 @@ hipError_t launch_dx(bool half, int tile, const OutArgs &a, hipStream_t stream)
     switch (tile) {
 #define X(I, BM, BN, WM, WN)                                                                                     \
     case I:                                                                                                      \
-        if (half) linear_out_kernel<_Float16, BM, BN, WM, WN, false><<<grid_of(a, a.splits), 64 * WM * WN, 0, stream>>>(a); \
-        else linear_out_kernel<__bf16, BM, BN, WM, WN, false><<<grid_of(a, a.splits), 64 * WM * WN, 0, stream>>>(a);        \
+        if (half) linear_out_kernel<_Float16, BM, BN, WM, WN, false><<<grid_of(a, I), 64 * WM * WN, 0, stream>>>(a); \
+        else linear_out_kernel<__bf16, BM, BN, WM, WN, false><<<grid_of(a, I), 64 * WM * WN, 0, stream>>>(a);        \
         break;
         TGEMM_TILES(X)
 #undef X
@@ -257,8 +298,8 @@ hipError_t launch_dw(bool half, int tile, const OutArgs &a, hipStream_t stream)
     switch (tile) {
 #define X(I, BM, BN, WM, WN)                                                                                    \
     case I:                                                                                                     \
-        if (half) linear_out_kernel<_Float16, BM, BN, WM, WN, true><<<grid_of(a, a.splits), 64 * WM * WN, 0, stream>>>(a); \
-        else linear_out_kernel<__bf16, BM, BN, WM, WN, true><<<grid_of(a, a.splits), 64 * WM * WN, 0, stream>>>(a);        \
+        if (half) linear_out_kernel<_Float16, BM, BN, WM, WN, true><<<grid_of(a, I), 64 * WM * WN, 0, stream>>>(a); \
+        else linear_out_kernel<__bf16, BM, BN, WM, WN, true><<<grid_of(a, I), 64 * WM * WN, 0, stream>>>(a);        \
         break;
         TGEMM_TILES(X)
 #undef X

@@ -1,28 +1,30 @@
 // Tiles of 16-bit products on the matrix cores: C = A·B with A M×K and B K×N
 // of bf16 or fp16 values, summed in fp32 registers.
 //
-// * A work-group of WM×WN wavefronts holds a BM×BN tile of C in registers, a
-//   wavefront FM×FN blocks of 32×32 (v_mfma_f32_32x32x16).  The blocks are
-//   formed transposed (B's fragment is the instruction's first operand), so a
-//   lane holds 16 columns of one row of C: sums along a row of C stay within
-//   a lane and its partner, and a row's values leave in 16-byte pieces.
-// * K runs in steps of BK.  A step's slices of A and B go from device memory
-//   straight into LDS, 16 bytes a lane, into one of STAGES stages; the loads of
-//   the next steps are under way while a step is multiplied.
-// * The order of the 32 columns of a block is free as long as the reader of C
-//   knows it: column 16·h + 4·q + r of C sits at index 8·q + 4·h + r of the
-//   instruction, which is what gives lane half h the 16 adjacent columns
-//   16·h ... 16·h + 15 in accumulator order.
+// * A work-group of WM×WN wavefronts computes BM×BN tiles of C, a wavefront
+//   FM×FN blocks of 16×16 (v_mfma_f32_16x16x32).  The GPU runs these products
+//   at the clock that its power allows, and this instruction needs less of it
+//   than v_mfma_f32_32x32x16, which moves twice the accumulators for the same
+//   work (from registers alone, random bf16: 2054 against 1834 TFLOP/s).
+// * The blocks are formed transposed (B's fragment is the instruction's first
+//   operand), so a lane holds values of one row of C: sums along a row stay
+//   within a lane and the three that share its row, and a row's values leave
+//   in 16-byte pieces.  The order of a wavefront's columns is free as long as
+//   the reader of C knows it: column 4·FN·q + 4·b + r sits at index 4·q + r of
+//   block b, which gives the lanes of quarter q 4·FN adjacent columns.
+// * K runs in steps of 64.  A step's slices of A and B go from device memory
+//   straight into LDS, 16 bytes a lane, into one of two stages; the loads of
+//   the next step are under way while a step is multiplied.
 //
 // An operand is K-contiguous ("KC": element (mn, k) at mn·ld + k) or
 // MN-contiguous ("MC": at k·ld + mn).  A KC slice lies in LDS as mn rows of
 // 128 bytes, an MC slice as 64 rows (one a k) of 2·BM or 2·BN bytes, from
 // which the transposing LDS read gathers four values of k a lane.  The loads
 // into LDS write 16-byte pieces in lane order, so the pieces are permuted on
-// the reading side of device memory, within a cache line: piece c of a KC row
-// goes to c ^ (row / 2 & 7), and the 64-byte quarter-lines of an MC row are
-// exchanged by the row's k.  Without that the 32 rows of a KC fragment would
-// start in the same banks, as would the four rows of a transposing read.
+// the reading side of device memory, within a row: piece c of a KC row goes to
+// c ^ (row / 2 & 7), piece c of an MC row to c ^ flip(k).  Without that the 16
+// rows of a KC fragment would start in the same banks, as would the rows of a
+// transposing read.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -34,7 +36,6 @@ namespace tgemm {
 namespace m16 {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -54,7 +55,7 @@ struct Operands {
     int steps_per_split;       // part y of the sum takes steps [y·this, (y+1)·this)
     int mn_a, mn_b;            // KC: rows of A / B; MC: columns that may be read, a multiple of 8
     int k_a, k_b;              // MC: rows (values of k) of A / B
-    int tiles_m, tiles_n;
+    int tiles_m, tiles_n, splits;
 };
 
 // A float32 operand is the sum of three bf16 planes (high, middle, low: 24
@@ -69,25 +70,33 @@ struct Frag;
 template <>
 struct Frag<__bf16> {
     typedef bf16x8 type;
-    static __device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c)
+    static __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c)
     {
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
     }
 };
 template <>
 struct Frag<_Float16> {
     typedef f16x8 type;
-    static __device__ __forceinline__ f32x16 mfma(f16x8 a, f16x8 b, f32x16 c)
+    static __device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c)
     {
-        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
     }
 };
 
-// A 16-byte read of a KC fragment takes 16 rows at a time, which span 16·2·BK
-// bytes; each of them finds its piece in another 16 bytes of the 256 that the
-// banks are wide.
-template <int BK>
-__device__ __forceinline__ constexpr int swizzle(int row) { return BK == 64 ? (row >> 1) & 7 : (row >> 2) & 3; }
+// The exchange of 16-byte pieces in LDS.  A KC read takes 16 rows at a time,
+// which lie 128 bytes apart: two rows share a position in the 256 bytes that
+// the banks are wide, eight pairs are told apart by their pieces.  An MC read
+// takes four (two times four) rows of 2·MN bytes at a time: 32 adjacent bytes
+// of each, or, where a block's columns are 4·F apart (PERMUTE), four pieces.
+__device__ __forceinline__ constexpr int swizzle(int row) { return (row >> 1) & 7; }
+template <int MN, int F, bool PERMUTE>
+__device__ __forceinline__ constexpr int flip(int k)
+{
+    const int j = k & 3, h = (k >> 3) & 1;
+    if (PERMUTE) return F == 4 ? (j & 1) | (j >> 1) << 3 : 4 * j;
+    return MN >= 128 ? 2 * j + 8 * h : 0;
+}
 
 typedef __attribute__((address_space(3))) char lds_char;
 
@@ -109,34 +118,44 @@ __device__ __forceinline__ void load_lds(const char *base, uint32_t offset, lds_
 }
 #pragma clang diagnostic pop
 
-// One operand's slices: where this thread's 16-byte pieces come from.
-template <int MN, int BK, int THREADS, bool MC, bool PERMUTE>
+// threadIdx.x, of which nothing that is worked out from it is kept over a tile's
+// products: it would cost registers there.
+__device__ __forceinline__ int thread_anew()
+{
+    int thread = threadIdx.x;
+    asm volatile("" : "+v"(thread));
+    return thread;
+}
+
+// One operand's slices: where this thread's 16-byte pieces come from.  F: the
+// blocks of 16 that a wavefront takes.
+template <int MN, int F, int THREADS, bool MC, bool PERMUTE>
 struct Loader {
-    static constexpr int kBytes = MN * BK * 2;
+    static constexpr int kBytes = MN * kStepK * 2;
     static constexpr int kRounds = kBytes / 16 / THREADS;
     static_assert(kRounds * 16 * THREADS == kBytes, "whole rounds");
-    static constexpr int kRowPieces = MC ? MN / 8 : BK / 8;
+    static constexpr int kRowPieces = MC ? MN / 8 : kStepK / 8;
     uint32_t off[kRounds];
-
-    static __device__ __forceinline__ int piece(int r) { return r * THREADS + (int)threadIdx.x; }
 
     // mn_last: the last row (KC) or the last 8-aligned column (MC) of the
     // operand, relative to the tile; k_last: the last row of an MC operand,
     // relative to the step.
     __device__ __forceinline__ void place(int64_t ld, int mn_last, int k_last)
     {
+        const int thread = thread_anew();
 #pragma unroll
         for (int r = 0; r < kRounds; ++r) {
-            const int row = piece(r) / kRowPieces, slot = piece(r) % kRowPieces;
+            const int piece = r * THREADS + thread, row = piece / kRowPieces, slot = piece % kRowPieces;
             if constexpr (MC) {
-                constexpr int mask = MN / 32 - 1;
-                const int quarter = (slot / 4) ^ (((row & 3) | ((row >> 1) & 4)) & mask);
-                const int mn = min(quarter * 32 + (slot % 4) * 8, mn_last);
+                const int mn = min((slot ^ flip<MN, F, PERMUTE>(row)) * 8, mn_last);
                 off[r] = ((uint32_t)min(row, k_last) * (uint32_t)ld + (uint32_t)mn) * 2u;
             } else {
                 int mn = row;
-                if constexpr (PERMUTE) mn = (row & ~31) | ((row & 4) << 2) | ((row & 24) >> 1) | (row & 3);
-                off[r] = ((uint32_t)min(mn, mn_last) * (uint32_t)ld + (uint32_t)((slot ^ swizzle<BK>(row)) * 8)) * 2u;
+                if constexpr (PERMUTE) {
+                    const int in = row % (16 * F), b = in / 16, q = in / 4 % 4;
+                    mn = row - in + 4 * F * q + 4 * b + in % 4;
+                }
+                off[r] = ((uint32_t)min(mn, mn_last) * (uint32_t)ld + (uint32_t)((slot ^ swizzle(row)) * 8)) * 2u;
             }
         }
     }
@@ -147,25 +166,24 @@ struct Loader {
     }
 };
 
-// Byte offsets of a wavefront's fragments in a slice.
-template <int MN, int BK, int F, bool MC, bool PERMUTE>
+// Byte offsets of a wavefront's F fragments in a slice (which starts at a
+// multiple of 1024 bytes).  In an MC slice a block further on is another value
+// of bits that nothing else of the offset uses, so one register serves all.
+template <int MN, int F, bool MC, bool PERMUTE>
 struct Reader {
-    int at[MC ? F : BK / 16];
+    int at[MC ? 1 : 2];
 
     // mn: the wavefront's first row or column in the tile
     __device__ __forceinline__ void place(int mn, int lane)
     {
+        const int l16 = lane & 15, quarter = lane >> 4;
         if constexpr (MC) {
-            constexpr int mask = MN / 32 - 1;
-            const int i = lane & 15, row = i >> 2, piece = i & 3, right = (lane >> 4) & 1, half = lane >> 5;
-            const int in = PERMUTE ? 32 * (piece & 1) + 16 * right + 8 * (piece >> 1) : 32 * right + 8 * piece;
-#pragma unroll
-            for (int f = 0; f < F; ++f)
-                at[f] = (8 * half + row) * (2 * MN) + (((mn / 32 + f) ^ ((row | (half << 2)) & mask)) * 64) + in;
+            const int k = 8 * quarter + (l16 >> 2), q = l16 & 3;
+            const int col = mn + (PERMUTE ? 4 * F * q : 4 * q);
+            at[0] = k * (2 * MN) + ((col / 8) ^ flip<MN, F, PERMUTE>(k)) * 16 + (col & 4) * 2;
         } else {
-            const int l32 = lane & 31, half = lane >> 5;
 #pragma unroll
-            for (int s = 0; s < BK / 16; ++s) at[s] = (mn + l32) * (2 * BK) + (((2 * s + half) ^ swizzle<BK>(l32)) * 16);
+            for (int s = 0; s < 2; ++s) at[s] = (mn + l16) * 128 + (((4 * s + quarter) ^ swizzle(l16)) * 16);
         }
     }
 
@@ -175,37 +193,36 @@ struct Reader {
         typedef typename Frag<E>::type V;
         if constexpr (MC) {
             typedef __attribute__((address_space(3))) s16x4 lds4;
-            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(slice + at[f] + (16 * s) * (2 * MN)));
-            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(slice + at[f] + (16 * s + 4) * (2 * MN)));
+            const uint32_t from = ((uint32_t)(uintptr_t)slice + (uint32_t)at[0]) ^ (uint32_t)(f << (PERMUTE ? 3 : 5));
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(uintptr_t)(from + (32 * s) * (2 * MN)));
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(uintptr_t)(from + (32 * s + 4) * (2 * MN)));
             const s16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
             return __builtin_bit_cast(V, v);
         } else {
             typedef __attribute__((address_space(3))) V ldsv;
-            return *(ldsv *)(slice + at[s] + f * 32 * (2 * BK));
+            return *(ldsv *)(slice + at[s] + f * 16 * 128);
         }
     }
 };
 
-// The work-group's loads into LDS have arrived but for the last FLYING of each
-// thread, and its reads of LDS are done.  The compiler's own barrier would not
-// wait for loads that write LDS.
-template <int FLYING>
+// The work-group's loads into LDS have arrived, and its reads of LDS are done.
+// The compiler's own barrier would not wait for loads that write LDS.
 __device__ __forceinline__ void arrive()
 {
-    __builtin_amdgcn_s_waitcnt((FLYING & 15) | (FLYING >> 4) << 14 | 7 << 4);  // vmcnt(FLYING) lgkmcnt(0)
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
     __syncthreads();
 }
 
-// The hardware deals work-groups round-robin to eight XCDs with an L2 each;
-// XCD x takes the x-th run of logical ids, as in mfma::tile_of.  Ids walk the
+// Tile `id` of `ids`.  The hardware deals work-groups, and a grid that is a
+// multiple of 8 its tiles, round-robin to eight XCDs with an L2 each; XCD x takes the x-th run of logical ids, as in mfma::tile_of.  Ids walk the
 // tiles of one part of the sum, then those of the next (parts share nothing),
 // and within a part groups of 8 tile rows column by column, so that the
 // work-groups of an XCD share rows of A and columns of B.
-__device__ __forceinline__ void place_tile(int tiles_m, int tiles_n, int &tm, int &tn, int &split)
+__device__ __forceinline__ void place_tile(int id, int ids, int tiles_m, int tiles_n, int &tm, int &tn, int &split)
 {
-    const int groups = gridDim.x, q = groups / mfma::kXcds, r = groups % mfma::kXcds;
-    const int x = blockIdx.x % mfma::kXcds;
-    const int logical = blockIdx.x / mfma::kXcds + x * q + min(x, r);
+    const int q = ids / mfma::kXcds, r = ids % mfma::kXcds;
+    const int x = id % mfma::kXcds;
+    const int logical = id / mfma::kXcds + x * q + min(x, r);
     const int tiles = tiles_m * tiles_n;
     split = logical / tiles;
     const int tile = logical - split * tiles, per_group = 8 * tiles_n;
@@ -214,9 +231,6 @@ __device__ __forceinline__ void place_tile(int tiles_m, int tiles_n, int &tm, in
     tm = group * 8 + in_group % rows;
     tn = in_group / rows;
 }
-
-struct Yes { static constexpr bool value = true; };
-struct No { static constexpr bool value = false; };
 
 // Scheduling hints: READS LDS reads spread evenly among MFMAS matrix
 // instructions.
@@ -231,59 +245,73 @@ __device__ __forceinline__ void spread()
     }
 }
 
-// A tile of C.  After run(), lane (l32 = lane & 31, half = lane >> 5) holds in
-// acc[i][j][r] row row0 + i·32 + l32, column col0 + j·32 + 16·half + r.
-template <class E, int BM, int BN, int WM, int WN, bool A_MC, bool B_MC, int BK, int STAGES>
+// The tiles of C that a work-group computes: blockIdx.x, blockIdx.x +
+// gridDim.x, ...  For each, `epilogue(acc, row0, col0, split)` is called when
+// the lane holds in acc[i][j][r] row row0 + 16·i + lane % 16, column col0 +
+// 4·FN·(lane / 16) + 4·j + r.  The loads run two steps ahead without regard to
+// where a tile ends, so the next tile's are under way by then.
+template <class E, int BM, int BN, int WM, int WN, bool A_MC, bool B_MC>
 struct TileProduct {
     static constexpr int kThreads = 64 * WM * WN;
-    static constexpr int FM = BM / WM / 32, FN = BN / WN / 32;
+    static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
+    static constexpr int BK = kStepK;
     static constexpr int kStage = (BM + BN) * BK * 2;
-    static constexpr int kLds = STAGES * kStage;
+    static constexpr int kLds = 2 * kStage;
+    typedef f32x4 Acc[FM][FN];
 
-    f32x16 acc[FM][FN];
-    int row0, col0, split;
-
-    __device__ __forceinline__ void run(const Operands &p, lds_char *lds)
+    template <class Epilogue>
+    static __device__ __forceinline__ void run(const Operands &p, lds_char *lds, Epilogue epilogue)
     {
         const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
         const int wm = wave / WN, wn = wave % WN;
-        int tm, tn;
-        place_tile(p.tiles_m, p.tiles_n, tm, tn, split);
-        const int m0 = tm * BM, n0 = tn * BN;
-        row0 = m0 + wm * (FM * 32);
-        col0 = n0 + wn * (FN * 32);
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-            for (int j = 0; j < FN; ++j)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+        const int tiles = p.tiles_m * p.tiles_n * p.splits;
+        Loader<BM, FM, kThreads, A_MC, false> la;
+        Loader<BN, FN, kThreads, B_MC, true> lb;
+        Reader<BM, FM, A_MC, false> ra;
+        Reader<BN, FN, B_MC, true> rb;
+        ra.place(wm * (FM * 16), lane);
+        rb.place(wn * (FN * 16), lane);
+        constexpr int kLoadsA = decltype(la)::kRounds, kLoads = kLoadsA + decltype(lb)::kRounds;
+        constexpr int kReadsA = FM / 2 * (A_MC ? 2 : 1), kReadsB = FN * (B_MC ? 2 : 1);
 
-        const int first = split * p.steps_per_split * (kStepK / BK);
-        const int last = min(p.steps * (kStepK / BK), first + p.steps_per_split * (kStepK / BK));
-        if (first >= last) return;
+        // A tile's place and its steps.
+        auto steps_of = [&](int split, int &first, int &last) {
+            first = split * p.steps_per_split;
+            last = min(p.steps, first + p.steps_per_split);
+        };
+        auto place = [&](int id, int &m0, int &n0, int &split) {
+            int tm, tn;
+            place_tile(id, tiles, p.tiles_m, p.tiles_n, tm, tn, split);
+            m0 = tm * BM;
+            n0 = tn * BN;
+        };
 
-        Loader<BM, BK, kThreads, A_MC, false> la;
-        Loader<BN, BK, kThreads, B_MC, true> lb;
-        Reader<BM, BK, FM, A_MC, false> ra;
-        Reader<BN, BK, FN, B_MC, true> rb;
-        ra.place(wm * (FM * 32), lane);
-        rb.place(wn * (FN * 32), lane);
-        const int a_last = A_MC ? p.mn_a - 8 - m0 : p.mn_a - 1 - m0;
-        const int b_last = B_MC ? p.mn_b - 8 - n0 : p.mn_b - 1 - n0;
-        // An MC operand may end inside a step or before its last ones (K is
-        // padded to 64): such a step starts at the last row at the latest.
-        auto start = [](int k, int rows) { return min(k * BK, rows - 1); };
-        if constexpr (A_MC) la.place(p.lda, a_last, p.k_a - 1 - start(first, p.k_a));
-        else la.place(p.lda, a_last, 0);
-        if constexpr (B_MC) lb.place(p.ldb, b_last, p.k_b - 1 - start(first, p.k_b));
-        else lb.place(p.ldb, b_last, 0);
-        const char *A = (const char *)p.A + (A_MC ? (int64_t)m0 : (int64_t)m0 * p.lda) * 2;
-        const char *B = (const char *)p.B + (B_MC ? (int64_t)n0 : (int64_t)n0 * p.ldb) * 2;
-        // where the next loads come from
-        int seg = 0, k = first;
-        const char *from_a = nullptr, *from_b = nullptr;
+        // The loads: which tile, segment and step they are at.
+        int at_id = blockIdx.x, seg, k, first, last, a_last, b_last;
+        const char *A, *B, *from_a, *from_b;
+        auto start = [](int step, int rows) { return min(step * BK, rows - 1); };
+        auto open = [&]() {
+            int m0, n0, split;
+            place(at_id, m0, n0, split);
+            steps_of(split, first, last);
+            a_last = A_MC ? p.mn_a - 8 - m0 : p.mn_a - 1 - m0;
+            b_last = B_MC ? p.mn_b - 8 - n0 : p.mn_b - 1 - n0;
+            la.place(p.lda, a_last, A_MC ? p.k_a - 1 - start(first, p.k_a) : 0);
+            lb.place(p.ldb, b_last, B_MC ? p.k_b - 1 - start(first, p.k_b) : 0);
+            A = (const char *)p.A + (A_MC ? (int64_t)m0 : (int64_t)m0 * p.lda) * 2;
+            B = (const char *)p.B + (B_MC ? (int64_t)n0 : (int64_t)n0 * p.ldb) * 2;
+            seg = 0;
+            k = first;
+        };
         auto seek = [&]() {
+            if (k == last) {
+                k = first;
+                if (++seg == p.segments) {
+                    // after the last tile its first steps are loaded again, for nobody
+                    if (at_id + (int)gridDim.x < tiles) at_id += gridDim.x;
+                    open();
+                }
+            }
             const int start_a = A_MC ? start(k, p.k_a) : k * BK, start_b = B_MC ? start(k, p.k_b) : k * BK;
             from_a = A + (A_MC ? start_a * p.lda : (int64_t)start_a) * 2;
             from_b = B + (B_MC ? start_b * p.ldb : (int64_t)start_b) * 2;
@@ -291,15 +319,11 @@ struct TileProduct {
                 from_a += ((kPairsA >> (2 * seg)) & 3) * p.plane_a * 2;
                 from_b += ((kPairsB >> (2 * seg)) & 3) * p.plane_b * 2;
             }
-            // the last rows of an MC operand, and back to whole steps for the next segment
+            // an MC operand may end inside its last step; the next segment has whole ones again
             if (A_MC && ((k + 1) * BK > p.k_a || (p.segments > 1 && k == first))) la.place(p.lda, a_last, p.k_a - 1 - start_a);
             if (B_MC && ((k + 1) * BK > p.k_b || (p.segments > 1 && k == first))) lb.place(p.ldb, b_last, p.k_b - 1 - start_b);
-            if (++k == last) {
-                k = first;
-                ++seg;
-            }
+            ++k;
         };
-        constexpr int kLoadsA = decltype(la)::kRounds, kLoads = kLoadsA + decltype(lb)::kRounds;
         auto issue = [&](int stage, int lo, int hi) {
 #pragma unroll
             for (int r = 0; r < kLoads; ++r) {
@@ -309,70 +333,74 @@ struct TileProduct {
             }
         };
 
-        // Two sets of fragments: those of the next 16 values of k are read
-        // while these are multiplied.
-        typename Frag<E>::type a[2][FM], b[2][FN];
-        auto read = [&](int stage, int s) {
+        Acc acc;
+        // A step has four phases: each half of the wavefront's rows with each
+        // half of the step's 64 values of k.  Two sets of fragments: those of
+        // the next phase are read while these are multiplied.
+        typename Frag<E>::type a[2][FM / 2], b[2][FN];
+        auto read = [&](int stage, int phase) {
             lds_char *as = lds + stage * kStage, *bs = as + BM * BK * 2;
+            const int s = phase >> 1, h = phase & 1;
+            if (h == 0) {
 #pragma unroll
-            for (int j = 0; j < FN; ++j) b[s & 1][j] = rb.template read<E>(bs, j, s);
+                for (int j = 0; j < FN; ++j) b[s][j] = rb.template read<E>(bs, j, s);
+            }
 #pragma unroll
-            for (int i = 0; i < FM; ++i) a[s & 1][i] = ra.template read<E>(as, i, s);
+            for (int i = 0; i < FM / 2; ++i) a[h][i] = ra.template read<E>(as, h * (FM / 2) + i, s);
         };
-        auto multiply = [&](int s) {
+        auto multiply = [&](int phase, int m) {
+            const int s = phase >> 1, h = phase & 1, i = m / FN, j = m % FN;
+            acc[h * (FM / 2) + i][j] = Frag<E>::mfma(b[s][j], a[h][i], acc[h * (FM / 2) + i][j]);
+        };
+
+        at_id = blockIdx.x;
+        open();
+        seek();
+        issue(0, 0, kLoads);
+        seek();
+        issue(1, 0, kLoads);
+        arrive();
+        read(0, 0);
+        int stage = 0;
+        for (int id = blockIdx.x; id < tiles; id += gridDim.x) {
 #pragma unroll
             for (int i = 0; i < FM; ++i)
 #pragma unroll
-                for (int j = 0; j < FN; ++j) acc[i][j] = Frag<E>::mfma(b[s & 1][j], a[s & 1][i], acc[i][j]);
-        };
-        constexpr int kReads = FM * (A_MC ? 2 : 1) + FN * (B_MC ? 2 : 1);
-
-        // A step on the slices of `stage`, its first fragments read.  The
-        // barrier stands before the last 16 values of k, whose fragments are
-        // in registers by then: this stage is read no more, so the loads of
-        // the step STAGES further on go there, and the next step's slices
-        // have arrived, so its first fragments are read under these products.
-        constexpr int kSubs = BK / 16;
-        auto step = [&](int stage, int after, auto load, auto next) {
+                for (int j = 0; j < FN; ++j)
 #pragma unroll
-            for (int s = 0; s < kSubs - 1; ++s) {
-                read(stage, s + 1);
-                multiply(s);
-                spread<FM * FN, kReads>();
-            }
-            if constexpr (decltype(next)::value) {
-                if constexpr (decltype(load)::value) arrive<(STAGES - 2) * kLoads>();
-                else arrive<0>();
-                read(after, 0);
-            }
+                    for (int r = 0; r < 4; ++r) acc[i][j][r] = 0.0f;
+            int m0, n0, split, from, to;
+            place(id, m0, n0, split);
+            steps_of(split, from, to);
+            for (int n = (to - from) * p.segments; n > 0; --n) {
+                // A step on the slices of `stage`, its first fragments read.
+                // The barrier stands before the last phase, whose fragments
+                // are in registers by then: this stage is read no more, so the
+                // loads of the step after next go there, and the next step's
+                // slices have arrived, so its first fragments are read under
+                // these products.
+                constexpr int kProducts = FM / 2 * FN;
+                seek();
 #pragma unroll
-            for (int m = 0; m < FM * FN; ++m) {
-                if constexpr (decltype(load)::value) issue(stage, m * kLoads / (FM * FN), (m + 1) * kLoads / (FM * FN));
-                const int i = m / FN, j = m % FN, s = (kSubs - 1) & 1;
-                acc[i][j] = Frag<E>::mfma(b[s][j], a[s][i], acc[i][j]);
+                for (int phase = 0; phase < 3; ++phase) {
+                    read(stage, phase + 1);
+#pragma unroll
+                    for (int m = 0; m < kProducts; ++m) multiply(phase, m);
+                    if (phase == 1) spread<kProducts, kReadsA + kReadsB>();
+                    else spread<kProducts, kReadsA>();
+                }
+                arrive();
+                read(stage ^ 1, 0);
+#pragma unroll
+                for (int m = 0; m < kProducts; ++m) {
+                    issue(stage, m * kLoads / kProducts, (m + 1) * kLoads / kProducts);
+                    multiply(3, m);
+                }
+                stage ^= 1;
             }
-        };
-
-        const int total = (last - first) * p.segments;
-        int ahead = 0;
-        for (; ahead < STAGES && ahead < total; ++ahead) {
-            seek();
-            issue(ahead, 0, kLoads);
+            epilogue(acc, m0 + wm * (FM * 16), n0 + wn * (FN * 16), split);
         }
-        arrive<0>();
-        read(0, 0);
-        int n = 0, stage = 0;
-        auto following = [](int st) { return st + 1 == STAGES ? 0 : st + 1; };
-        for (; n + STAGES < total; ++n) {
-            seek();
-            step(stage, following(stage), Yes{}, Yes{});
-            stage = following(stage);
-        }
-        for (; n + 1 < total; ++n) {
-            step(stage, following(stage), No{}, Yes{});
-            stage = following(stage);
-        }
-        step(stage, stage, No{}, No{});
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no load into LDS outlives the work-group
     }
 };
 
