@@ -117,7 +117,7 @@ Choice choose_tile(int64_t M, int64_t N, int64_t steps, bool split = false)
     for (int i = 0; i < tile_count(); ++i) {
         const TileShape &s = tile_shape(i);
         const int64_t tiles = ceil_div(M, s.bm) * ceil_div(N, s.bn);
-        for (int64_t parts = 1; parts == 1 || (split && parts <= 64 && steps / parts >= 4); parts *= 2) {
+        for (int64_t parts = 1; parts == 1 || (split && parts <= 64 && steps / parts >= 4); ++parts) {
             const double rounds = (double)ceil_div(tiles * parts, (int64_t)256 * s.wg_per_cu) * s.wg_per_cu;
             double time = rounds * ((double)s.bm * s.bn / 65536.0 / rate[i] * (double)ceil_div(steps, parts) + 3.0);
             if (parts > 1) time += 4.0 + (double)M * (double)N * 8.0 * (double)parts / 5e12 / 1.5e-6;
@@ -144,12 +144,12 @@ struct Plan {
     int64_t x = -1, w = -1, xs = -1;  // operands laid out for the matrix cores
     // forward
     int stat_tile = 0, groups = 0;
-    int64_t part = -1, picked = -1, counted = -1;
+    int64_t part = -1, picked = -1, counted = -1, starts = -1, list = -1;
     // backward
     int64_t piece = 0, pieces = 0, ldg = 0;
-    int grad_tile = 0, dx_tile = 0, dw_tile = 0, dx_splits = 1;
+    int grad_tile = 0, dx_tile = 0, dw_tile = 0, dx_splits = 1, dw_splits = 1;
     bool dx_direct = false;
-    int64_t coef = -1, row_scale = -1, exps = -1, block_max = -1, all_scale = -1, g = -1, dx_part = -1;
+    int64_t coef = -1, row_scale = -1, exps = -1, block_max = -1, all_scale = -1, g = -1, dx_part = -1, dw_part = -1;
 
     int64_t take(int64_t bytes)
     {
@@ -182,13 +182,18 @@ bool fits(int64_t M, int64_t N, int tile, int64_t splits)
     return ceil_div(M, s.bm) * ceil_div(N, s.bn) * 512 <= kMaxThreads / splits;
 }
 
-bool plan_forward(Plan &p, const Head &h, bool distill)
+bool plan_forward(Plan &p, const Head &h, int64_t teacher_k)
 {
     plan_operands(p, h, false);
     p.stat_tile = choose_tile(h.T, h.V, p.Dp / kStepK * p.segments).tile;
     p.groups = (int)ceil_div(h.V, tile_shape(p.stat_tile).stat_columns);
     p.part = p.take(h.T * p.groups * 8);
-    if (!distill) p.picked = p.take(h.T * 4);
+    if (teacher_k > 0) {
+        p.starts = p.take(h.T * (p.groups + 1) * 2);
+        p.list = p.take(h.T * teacher_k * 4);
+    } else {
+        p.picked = p.take(h.T * 4);
+    }
     p.counted = p.take(h.T * 4);
     return fits(h.T, h.V, p.stat_tile, 1);
 }
@@ -204,7 +209,9 @@ bool plan_backward(Plan &p, const Head &h)
     p.ldg = p.piece + 128;
     const int64_t seg = p.segments;
     p.grad_tile = choose_tile(p.Tp, p.piece, p.Dp / kStepK * seg).tile;
-    p.dw_tile = choose_tile(p.piece, h.D, p.Tp / kStepK * seg).tile;
+    const Choice dw = choose_tile(p.piece, h.D, p.Tp / kStepK * seg, true);
+    p.dw_tile = dw.tile;
+    p.dw_splits = parts_of(p.Tp / kStepK, dw.splits);
     const Choice dx = choose_tile(h.T, h.D, p.piece / kStepK * seg, true);
     p.dx_tile = dx.tile;
     p.dx_splits = parts_of(ceil_div(h.V < p.piece ? h.V : p.piece, kStepK), dx.splits);
@@ -218,7 +225,8 @@ bool plan_backward(Plan &p, const Head &h)
     }
     p.g = p.take(p.Tp * p.ldg * 2 * p.planes);
     if (!p.dx_direct) p.dx_part = p.take(p.dx_splits * h.T * p.Dp * 4);
-    return fits(p.Tp, p.piece, p.grad_tile, 1) && fits(p.piece, h.D, p.dw_tile, 1) &&
+    if (p.dw_splits > 1) p.dw_part = p.take(p.dw_splits * p.piece * p.Dp * 4);
+    return fits(p.Tp, p.piece, p.grad_tile, 1) && fits(p.piece, h.D, p.dw_tile, p.dw_splits) &&
            fits(h.T, h.D, p.dx_tile, p.dx_splits);
 }
 
@@ -251,8 +259,7 @@ template <class T>
 T *in(void *workspace, int64_t offset) { return offset < 0 ? nullptr : (T *)((char *)workspace + offset); }
 
 // Lays out `rows` rows of an operand at dst.
-hipError_t copy_in(const Plan &p, const Head &h, const void *src, int64_t ld, int64_t rows, void *dst, int64_t rows_out,
-                   hipStream_t stream, const float *coef = nullptr, void *workspace = nullptr, int blocks = 0)
+CopyArgs copy_of(const Plan &p, const Head &h, const void *src, int64_t ld, int64_t rows, void *dst, int64_t rows_out)
 {
     CopyArgs c{};
     c.src = src;
@@ -266,14 +273,7 @@ hipError_t copy_in(const Plan &p, const Head &h, const void *src, int64_t ld, in
     c.plane = rows_out * p.Dp;
     c.planes = p.planes;
     c.vec = rows16(src, ld, h.dtype);
-    c.coef = coef;
-    if (coef != nullptr && p.half) {
-        c.exps = in<int>(workspace, p.exps);
-        c.block_max = in<int>(workspace, p.block_max);
-        c.blocks = blocks;
-        c.all_scale = in<float>(workspace, p.all_scale);
-    }
-    return launch_copy(c, stream);
+    return c;
 }
 
 struct Labels {
@@ -295,12 +295,12 @@ tgemm_status_t forward(const Plan &p, const Head &h, const Labels &l, float *los
     Stored x{h.X, h.ldx, 0}, w{h.W, h.ldw, 0};
     if (p.copy_x) {
         x = Stored{in<void>(ws, p.x), p.Dp, h.T * p.Dp};
-        e = copy_in(p, h, h.X, h.ldx, h.T, in<void>(ws, p.x), h.T, stream);
+        e = launch_copy(copy_of(p, h, h.X, h.ldx, h.T, in<void>(ws, p.x), h.T), stream);
         if (e != hipSuccess) return from_hip(e);
     }
     if (p.copy_w) {
         w = Stored{in<void>(ws, p.w), p.Dp, h.V * p.Dp};
-        e = copy_in(p, h, h.W, h.ldw, h.V, in<void>(ws, p.w), h.V, stream);
+        e = launch_copy(copy_of(p, h, h.W, h.ldw, h.V, in<void>(ws, p.w), h.V), stream);
         if (e != hipSuccess) return from_hip(e);
     }
     StatsArgs s{};
@@ -318,19 +318,21 @@ tgemm_status_t forward(const Plan &p, const Head &h, const Labels &l, float *los
     s.groups = p.groups;
     s.target = l.target;
     s.picked = in<float>(ws, p.picked);
+    if (l.teacher != nullptr) {
+        const SortArgs k{h.T, h.V, p.groups, tile_shape(p.stat_tile).stat_columns, *l.teacher, in<uint16_t>(ws, p.starts),
+                         in<uint32_t>(ws, p.list), student};
+        e = launch_sort(k, stream);
+        if (e != hipSuccess) return from_hip(e);
+        s.starts = k.starts;
+        s.list = k.list;
+        s.K = l.teacher->K;
+        s.student = student;
+    }
     e = launch_stats(p.half, p.stat_tile, s, stream);
     if (e != hipSuccess) return from_hip(e);
-    if (l.teacher != nullptr) {
-        PickArgs k{h.T, h.V, h.D, h.X, h.ldx, h.W, h.ldw, h.dtype, rows16(h.X, h.ldx, h.dtype) && rows16(h.W, h.ldw, h.dtype),
-                   *l.teacher, student};
-        e = launch_pick(k, stream);
-        if (e != hipSuccess) return from_hip(e);
-    }
-    JoinArgs j{h.T, h.V, p.groups, s.part, l.target, l.ignore, s.picked, l.teacher, student, loss, lse,
-               summary ? in<int>(ws, p.counted) : nullptr};
-    e = launch_join(j, stream);
-    if (e == hipSuccess && summary != nullptr) e = launch_summary(h.T, loss, j.counted, summary, stream);
-    return from_hip(e);
+    JoinArgs j{h.T, h.V, p.groups, s.part, l.target, l.ignore, s.picked, l.teacher, student, loss, lse, summary,
+               in<int>(ws, p.counted)};
+    return from_hip(launch_join(j, stream));
 }
 
 tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const float *grad, int64_t grad_step,
@@ -354,26 +356,35 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
     c.row_scale = in<float>(ws, p.row_scale);
     c.exps = in<int>(ws, p.exps);
     c.block_max = in<int>(ws, p.block_max);
-    hipError_t e = launch_coef(c, stream);
+    hipError_t e = coef_in_copy(c) ? hipSuccess : launch_coef(c, stream);
     if (e != hipSuccess) return from_hip(e);
 
     // Rows that do not count may hold anything: they are cleared where they
     // would meet a zero of the logits' gradient.
     void *xs = in<void>(ws, p.xs);
-    e = copy_in(p, h, h.X, h.ldx, h.T, xs, p.Tp, stream, c.coef, ws,
-                (int)coef_blocks(h.T, l.teacher != nullptr));
+    CopyArgs clear = copy_of(p, h, h.X, h.ldx, h.T, xs, p.Tp);
+    clear.all_scale = in<float>(ws, p.all_scale);
+    if (coef_in_copy(c)) {
+        clear.make = &c;
+    } else {
+        clear.coef = c.coef;
+        clear.exps = c.exps;
+        clear.block_max = c.block_max;
+        clear.blocks = (int)coef_blocks(h.T, l.teacher != nullptr);
+    }
+    e = launch_copy(clear, stream);
     if (e != hipSuccess) return from_hip(e);
     const Stored cleared{xs, p.Dp, p.Tp * p.Dp};
     Stored x = cleared, w{h.W, h.ldw, 0};
     if (p.half) x = Stored{h.X, h.ldx, 0};
     if (p.copy_x) {
         x = Stored{in<void>(ws, p.x), p.Dp, h.T * p.Dp};
-        e = copy_in(p, h, h.X, h.ldx, h.T, in<void>(ws, p.x), h.T, stream);
+        e = launch_copy(copy_of(p, h, h.X, h.ldx, h.T, in<void>(ws, p.x), h.T), stream);
         if (e != hipSuccess) return from_hip(e);
     }
     if (p.copy_w) {
         w = Stored{in<void>(ws, p.w), p.Dp, h.V * p.Dp};
-        e = copy_in(p, h, h.W, h.ldw, h.V, in<void>(ws, p.w), h.V, stream);
+        e = launch_copy(copy_of(p, h, h.W, h.ldw, h.V, in<void>(ws, p.w), h.V), stream);
         if (e != hipSuccess) return from_hip(e);
     }
 
@@ -458,17 +469,34 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
             o.op.plane_b = cleared.plane;
             o.op.mn_b = (int)p.Dp;
             o.op.k_b = (int)p.Tp;
-            o.out = (char *)dW + v0 * lddw * (int64_t)size_of(h.dtype);
-            o.ldo = lddw;
-            o.dtype = h.dtype;
-            o.vec = rows16(dW, lddw, h.dtype);
-            o.all_scale = in<float>(ws, p.all_scale);
+            void *to = (char *)dW + v0 * lddw * (int64_t)size_of(h.dtype);
+            if (p.dw_splits == 1) {
+                o.out = to;
+                o.ldo = lddw;
+                o.dtype = h.dtype;
+                o.vec = rows16(dW, lddw, h.dtype);
+                o.all_scale = in<float>(ws, p.all_scale);
+            } else {
+                o.op.splits = p.dw_splits;
+                o.op.steps_per_split = (int)ceil_div(p.Tp / kStepK, p.dw_splits);
+                o.out = in<float>(ws, p.dw_part);
+                o.ldo = p.Dp;
+                o.dtype = TGEMM_F32;
+                o.vec = true;
+                o.split_stride = p.piece * p.Dp;
+            }
             e = launch_dw(p.half, p.dw_tile, o, stream);
             if (e != hipSuccess) return from_hip(e);
+            if (p.dw_splits > 1) {
+                SumArgs s{cols, h.D, in<float>(ws, p.dw_part), p.Dp, o.split_stride, p.dw_splits, nullptr,
+                          in<float>(ws, p.all_scale), to, lddw, h.dtype, rows16(dW, lddw, h.dtype)};
+                e = launch_sum(s, stream);
+                if (e != hipSuccess) return from_hip(e);
+            }
         }
     }
     if (dX != nullptr && !p.dx_direct) {
-        SumArgs s{h.T, h.D, in<float>(ws, p.dx_part), p.Dp, dx_stride, p.dx_splits, in<float>(ws, p.row_scale),
+        SumArgs s{h.T, h.D, in<float>(ws, p.dx_part), p.Dp, dx_stride, p.dx_splits, in<float>(ws, p.row_scale), nullptr,
                   dX, lddx, h.dtype, rows16(dX, lddx, h.dtype)};
         e = launch_sum(s, stream);
         if (e != hipSuccess) return from_hip(e);
@@ -480,7 +508,7 @@ tgemm_status_t no_rows(float *summary, hipStream_t stream)
 {
     Range r;
     if (!at(summary, summary ? 1 : 0, 3, 3, 4, r)) return TGEMM_ERROR_INVALID_VALUE;
-    return summary ? from_hip(launch_summary(0, nullptr, nullptr, summary, stream)) : TGEMM_SUCCESS;
+    return summary ? from_hip(launch_summary_none(summary, stream)) : TGEMM_SUCCESS;
 }
 
 tgemm_status_t check_teacher(const Head &h, int64_t K, int64_t ld_ids, tgemm_dtype_t dtype, int64_t ld_logits,
@@ -501,9 +529,9 @@ size_t tgemm_linear_loss_workspace_size(tgemm_dtype_t dtype, int64_t T, int64_t 
                                         const void *W, int64_t ldw, int64_t teacher_k, int backward_pass)
 {
     const Head h{dtype, T, V, D, X, ldx, W, ldw};
-    if (check_head(h) != TGEMM_SUCCESS || T == 0) return 0;
+    if (check_head(h) != TGEMM_SUCCESS || T == 0 || teacher_k < 0 || teacher_k > kMaxK) return 0;
     Plan p;
-    if (!(backward_pass ? plan_backward(p, h) : plan_forward(p, h, teacher_k > 0))) return 0;
+    if (!(backward_pass ? plan_backward(p, h) : plan_forward(p, h, teacher_k))) return 0;
     return (size_t)p.total;
 }
 
@@ -517,7 +545,7 @@ tgemm_status_t tgemm_linear_ce_forward(tgemm_dtype_t dtype, int64_t T, int64_t V
     if (st != TGEMM_SUCCESS) return st;
     if (T == 0) return no_rows(summary, stream);
     Plan p;
-    if (!plan_forward(p, h, false)) return TGEMM_ERROR_NOT_SUPPORTED;
+    if (!plan_forward(p, h, 0)) return TGEMM_ERROR_NOT_SUPPORTED;
     Range r[3], w[4];
     if (!at(X, T, D, ldx, size_of(dtype), r[0]) || !at(W, V, D, ldw, size_of(dtype), r[1]) ||
         !at(target, T, 1, 1, 8, r[2]) || !at(loss, T, 1, 1, 4, w[0]) || !at(lse, T, 1, 1, 4, w[1]) ||
@@ -562,7 +590,7 @@ tgemm_status_t tgemm_linear_kd_forward(tgemm_dtype_t dtype, int64_t T, int64_t V
     if (st != TGEMM_SUCCESS) return st;
     if (T == 0) return no_rows(summary, stream);
     Plan p;
-    if (!plan_forward(p, h, true)) return TGEMM_ERROR_NOT_SUPPORTED;
+    if (!plan_forward(p, h, K)) return TGEMM_ERROR_NOT_SUPPORTED;
     Range r[4], w[5];
     if (!at(X, T, D, ldx, size_of(dtype), r[0]) || !at(W, V, D, ldw, size_of(dtype), r[1]) ||
         !at(teacher_ids, T, K, ld_ids, 8, r[2]) || !at(teacher_logits, T, K, ld_logits, size_of(teacher_dtype), r[3]) ||

@@ -38,6 +38,14 @@ struct StatsArgs {
     int groups;
     const int64_t *target;  // or NULL
     float *picked;
+    // a teacher's entries (linear_sort_kernel), or NULL: row t's entries in
+    // column group g are list[t·K + starts[t·(groups + 1) + g]] ... up to
+    // those of g + 1, each the column in its group and 256·k; student[t·K + k]
+    // receives the scaled logit
+    const uint16_t *starts;
+    const uint32_t *list;
+    int K;
+    float *student;
 };
 hipError_t launch_stats(bool half, int tile, const StatsArgs &a, hipStream_t stream);
 
@@ -73,26 +81,6 @@ hipError_t launch_dw(bool half, int tile, const OutArgs &a, hipStream_t stream);
 
 // ---- passes over rows ------------------------------------------------------
 
-// dst (planes of rows_out×ld_out 16-bit elements, zero past the ends) = src
-// (rows×cols).  coef: rows with coef 0 become zero.  exps: row t is scaled by
-// 2^(exps[t] - the largest of block_max), and all_scale receives
-// 2^(that - kHalfShift).
-struct CopyArgs {
-    const void *src;
-    int64_t ld;
-    tgemm_dtype_t dtype;
-    int64_t rows, cols;
-    void *dst;
-    int64_t rows_out, ld_out, plane;
-    int planes;
-    bool vec;  // 16-byte loads
-    const float *coef;
-    const int *exps, *block_max;
-    int blocks;
-    float *all_scale;
-};
-hipError_t launch_copy(const CopyArgs &a, hipStream_t stream);
-
 // The teacher's part of a row, as both passes read it.
 struct Teacher {
     int K;
@@ -104,6 +92,20 @@ struct Teacher {
     float scale;  // 1 / temperature
 };
 
+// Sorts each row's entries by column for launch_stats, and sets student to 0
+// where an entry is absent and NaN where its id is out of range.
+struct SortArgs {
+    int64_t T, V;
+    int groups, columns;  // column groups, and the columns of one
+    Teacher teacher;
+    uint16_t *starts;
+    uint32_t *list;
+    float *student;
+};
+hipError_t launch_sort(const SortArgs &a, hipStream_t stream);
+
+// summary (or NULL) = {sum of loss, the mean over the rows that count, 1 /
+// their number} (1 / 1 where none does); `counted` is room for a flag a row.
 struct JoinArgs {
     int64_t T, V;
     int groups;
@@ -113,28 +115,12 @@ struct JoinArgs {
     const float *picked;
     const Teacher *teacher;  // host pointer; NULL for cross entropy
     const float *student;
-    float *loss, *lse;
-    int *counted;  // or NULL: receives whether a row counts
+    float *loss, *lse, *summary;
+    int *counted;
 };
 hipError_t launch_join(const JoinArgs &a, hipStream_t stream);
-
-// summary = {sum of loss, the mean over the rows that count, 1 / their number}
-// (1 / 1 where none does).
-hipError_t launch_summary(int64_t T, const float *loss, const int *counted, float *summary, hipStream_t stream);
-
-// student[t][k] = s·x_t·w_{id}: 0 where the entry is absent, NaN where its id is out of range.
-struct PickArgs {
-    int64_t T, V, D;
-    const void *X;
-    int64_t ldx;
-    const void *W;
-    int64_t ldw;
-    tgemm_dtype_t dtype;
-    bool vec;  // 16-byte loads
-    Teacher teacher;
-    float *student;
-};
-hipError_t launch_pick(const PickArgs &a, hipStream_t stream);
+// The summary of no rows.
+hipError_t launch_summary_none(float *summary, hipStream_t stream);
 
 // The factor of a row's gradient, coef[t] = grad[t·grad_step]·factor·*weight, 0 for rows that do
 // not count, NaN for rows with an index out of range; for fp16 its fraction
@@ -157,6 +143,31 @@ struct CoefArgs {
 };
 hipError_t launch_coef(const CoefArgs &a, hipStream_t stream);
 
+// Cross entropy's factors need no pass of their own where a row's power of two
+// is known without the others': in fp16, where one value serves all rows.
+inline bool coef_in_copy(const CoefArgs &a) { return a.teacher == nullptr && (!a.half || a.grad_step == 0); }
+
+// dst (planes of rows_out×ld_out 16-bit elements, zero past the ends) = src
+// (rows×cols).  coef: rows with coef 0 become zero.  exps: row t is scaled by
+// 2^(exps[t] - the largest of block_max), and all_scale receives
+// 2^(that - kHalfShift).
+struct CopyArgs {
+    const void *src;
+    int64_t ld;
+    tgemm_dtype_t dtype;
+    int64_t rows, cols;
+    void *dst;
+    int64_t rows_out, ld_out, plane;
+    int planes;
+    bool vec;  // 16-byte loads
+    const float *coef;
+    const int *exps, *block_max;
+    int blocks;
+    float *all_scale;
+    const struct CoefArgs *make;  // host pointer, or NULL: also does launch_coef's work (coef_in_copy)
+};
+hipError_t launch_copy(const CopyArgs &a, hipStream_t stream);
+
 // G[t][id - v0] = coef[t]·(exp(student - lse) - the teacher's probability of id) for the ids in [v0, v0 + cols).
 struct ScatterArgs {
     int64_t T, v0, cols;
@@ -169,13 +180,14 @@ struct ScatterArgs {
 };
 hipError_t launch_scatter(const ScatterArgs &a, hipStream_t stream);
 
-// out[t][d] = row_scale[t]·(part_0 + part_1 + ...)[t][d], part_s at part + s·stride.
+// out[t][d] = row_scale[t]·all_scale·(part_0 + part_1 + ...)[t][d], part_s at
+// part + s·stride; either scale may be NULL.
 struct SumArgs {
     int64_t T, D;
     const float *part;
     int64_t ld, stride;
     int count;
-    const float *row_scale;
+    const float *row_scale, *all_scale;
     void *out;
     int64_t ldo;
     tgemm_dtype_t dtype;

@@ -59,6 +59,39 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_stats_kernel(StatsArgs a)
                 a.picked[row] = z * a.scale;
             }
         }
+        const int group = col0 / (Tile::FN * 16);
+        if (a.starts != nullptr && group < a.groups) {
+            // a row's first entry here, for all rows at once: most have one or none
+            int at[Tile::FM], n[Tile::FM];
+            uint32_t entry[Tile::FM];
+#pragma unroll
+            for (int i = 0; i < Tile::FM; ++i) {
+                const int64_t row = min(row0 + i * 16 + l16, a.op.M - 1);
+                const uint16_t *from = a.starts + row * (a.groups + 1) + group;
+                at[i] = from[0];
+                n[i] = from[1];
+            }
+#pragma unroll
+            for (int i = 0; i < Tile::FM; ++i) {
+                const int row = row0 + i * 16 + l16;
+                n[i] = row < a.op.M ? n[i] - at[i] : 0;
+                entry[i] = 0;
+                if (n[i] > 0) entry[i] = a.list[(int64_t)row * a.K + at[i]];
+            }
+#pragma unroll
+            for (int i = 0; i < Tile::FM; ++i) {
+                const int64_t base = (int64_t)(row0 + i * 16 + l16) * a.K;
+                for (int c = 0; c < n[i]; ++c) {
+                    const uint32_t what = c == 0 ? entry[i] : a.list[base + at[i] + c];
+                    const int e = (int)(what & 255) - H * quarter;
+                    if (e < 0 || e >= H) continue;
+                    float z = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < H; ++j) z = e == j ? acc[i][j / 4][j % 4] : z;
+                    a.student[base + (what >> 8)] = z * a.scale;
+                }
+            }
+        }
         // the scale is positive, so the largest product is the largest logit
         float high[Tile::FM], sum[Tile::FM];
 #pragma unroll
@@ -82,7 +115,6 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_stats_kernel(StatsArgs a)
         for (int i = 0; i < Tile::FM; ++i) sum[i] += __shfl_xor(sum[i], 16);
 #pragma unroll
         for (int i = 0; i < Tile::FM; ++i) sum[i] += __shfl_xor(sum[i], 32);
-        const int group = col0 / (Tile::FN * 16);
         if (quarter == 0 && group < a.groups) {
 #pragma unroll
             for (int i = 0; i < Tile::FM; ++i) {

@@ -47,9 +47,42 @@ __device__ __forceinline__ __bf16 plane_of(float x)
 __device__ __forceinline__ uint16_t bits(__bf16 v) { return __builtin_bit_cast(uint16_t, v); }
 __device__ __forceinline__ uint16_t bits(_Float16 v) { return __builtin_bit_cast(uint16_t, v); }
 
-__global__ __launch_bounds__(256) void linear_copy_kernel(CopyArgs a)
+__device__ __forceinline__ float grad_of(const CoefArgs &a, int64_t row)
+{
+    const float g = a.grad[row * a.grad_step] * a.factor;
+    return a.weight != nullptr ? g * *a.weight : g;
+}
+
+__device__ __forceinline__ void put_coef(const CoefArgs &a, int64_t row, float c, int &exponent)
+{
+    exponent = kNoExponent;
+    if (a.half) {
+        int e = 0;
+        if (c != 0.0f && !__builtin_isinf(c) && !__builtin_isnan(c)) {
+            c = ldexpf(frexpf(c, &e), kHalfShift);
+            exponent = e;
+        }
+        a.row_scale[row] = ldexpf(1.0f, e - kHalfShift);
+        a.exps[row] = e;
+    }
+    a.coef[row] = c;
+}
+
+__device__ __forceinline__ float ce_factor(const CoefArgs &a, int64_t row)
+{
+    const int64_t y = a.target[row];
+    return y == a.ignore ? 0.0f : y < 0 || y >= a.V ? NAN : grad_of(a, row);
+}
+
+__global__ __launch_bounds__(256) void linear_copy_kernel(CopyArgs a, CoefArgs make, bool making)
 {
     int top = 0;
+    if (making && make.half) {
+        // every row that counts has the same factor: its power of two is the largest
+        const float c = grad_of(make, 0);
+        if (c != 0.0f && !__builtin_isinf(c) && !__builtin_isnan(c)) frexpf(c, &top);
+        if (blockIdx.x == 0 && threadIdx.x == 0) *a.all_scale = ldexpf(1.0f, top - kHalfShift);
+    }
     if (a.exps != nullptr) {
         __shared__ int best[4];
         int m = kNoExponent;
@@ -67,7 +100,15 @@ __global__ __launch_bounds__(256) void linear_copy_kernel(CopyArgs a)
         const int64_t row = p / per_row, col = (p - row * per_row) * 8;
         const int left = row < a.rows ? (int)min((int64_t)8, a.cols - col) : 0;
         uint16_t *to = (uint16_t *)a.dst + row * a.ld_out + col;
-        const bool counts = left > 0 && (a.coef == nullptr || a.coef[row] != 0.0f);
+        bool counts = left > 0;
+        if (making && row < a.rows) {
+            const float c = ce_factor(make, row);
+            int exponent;
+            if (col == 0) put_coef(make, row, c, exponent);
+            counts = counts && c != 0.0f;
+        } else if (a.coef != nullptr && row < a.rows) {
+            counts = counts && a.coef[row] != 0.0f;
+        }
         u16x8 v[3] = {};
         if (counts && a.dtype == TGEMM_F32) {
             const float *from = (const float *)a.src + row * a.ld + col;
@@ -140,63 +181,67 @@ __device__ __forceinline__ TeacherRow read_teacher(const Teacher &t, int64_t row
     return r;
 }
 
-// A wavefront a row: the pairs (maximum, sum) of its column groups joined,
-// then the row's loss.
-__global__ __launch_bounds__(256) void linear_join_kernel(JoinArgs a, Teacher t, bool distill)
+// A wavefront a row: its entries' ids are sorted in LDS (a bitonic network over
+// a power of two of them), then each column group's first one is looked up.
+__global__ __launch_bounds__(64) void linear_sort_kernel(SortArgs a, int room)
 {
-    const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int lane = threadIdx.x & 63;
-    if (row >= a.T) return;
-    const float2 *part = a.part + row * a.groups;
-    float high = -INFINITY, sum = 0.0f;
-    for (int g = lane; g < a.groups; g += 64) {
-        const float2 p = part[g];
-        const float to = fmaxf(high, p.x);
-        if (to != -INFINITY) sum = sum * __builtin_amdgcn_exp2f(high - to) + p.y * __builtin_amdgcn_exp2f(p.x - to);
-        else sum += p.y;  // nothing yet, or a NaN
-        high = to;
-    }
-    const float top = wave_max(high);
-    sum = wave_sum(top == -INFINITY ? sum : sum * __builtin_amdgcn_exp2f(high - top));
-    const float lse = fmaf(top, 0.693147180559945309417f, logf(sum));
-    if (lane == 0) a.lse[row] = lse;
-    if (!distill) {
-        if (lane == 0) {
-            const int64_t y = a.target[row];
-            a.loss[row] = y == a.ignore ? 0.0f : y < 0 || y >= a.V ? NAN : lse - a.picked[row];
-            if (a.counted != nullptr) a.counted[row] = y != a.ignore;
+    extern __shared__ uint64_t keys[];
+    const Teacher &t = a.teacher;
+    const int64_t row = blockIdx.x;
+    const int lane = threadIdx.x;
+    for (int k = lane; k < room; k += 64) {
+        uint64_t key = ~(uint64_t)0;
+        if (k < t.K) {
+            const float v = load_as_float(t.logits, row * t.ld_logits + k, t.dtype);
+            const int64_t id = t.ids[row * t.ld_ids + k];
+            if (v == -INFINITY) a.student[row * t.K + k] = 0.0f;
+            else if (id < 0 || id >= a.V) a.student[row * t.K + k] = NAN;
+            else key = (uint64_t)id << 16 | (uint32_t)k;
         }
-        return;
+        keys[k] = key;
     }
-    const TeacherRow r = read_teacher(t, row, a.V, lane);
-    const float log_sum = logf(r.sum);
-    float loss = 0.0f;
+    for (int size = 2; size <= room; size *= 2)
+        for (int apart = size / 2; apart > 0; apart /= 2) {
+            __syncthreads();
+            for (int p = lane; p < room / 2; p += 64) {
+                const int i = 2 * p - (p & (apart - 1)), j = i + apart;
+                const uint64_t x = keys[i], y = keys[j];
+                if ((x > y) == ((i & size) == 0)) {
+                    keys[i] = y;
+                    keys[j] = x;
+                }
+            }
+        }
+    __syncthreads();
     for (int k = lane; k < t.K; k += 64) {
-        const float v = load_as_float(t.logits, row * t.ld_logits + k, t.dtype);
-        if (v == -INFINITY) continue;
-        const float d = (v - r.high) * t.scale;
-        const float q = expf(d) / r.sum;
-        // an entry whose probability is below the least float32 adds nothing
-        if (q != 0.0f) loss += q * (d - log_sum - (a.student[row * t.K + k] - lse));
+        const uint64_t key = keys[k];
+        if (key != ~(uint64_t)0)
+            a.list[row * t.K + k] = (uint32_t)((int)(key >> 16) % a.columns) | (uint32_t)(key & 0xFFFF) << 8;
     }
-    loss = wave_sum(loss) / (t.scale * t.scale);
-    if (lane == 0) {
-        a.loss[row] = !r.any ? 0.0f : r.bad ? NAN : loss;
-        if (a.counted != nullptr) a.counted[row] = r.any;
+    for (int g = lane; g <= a.groups; g += 64) {
+        const uint64_t from = (uint64_t)g * (uint32_t)a.columns << 16;
+        int lo = 0, hi = room;  // the first key that is not below `from`; the last group ends before the absent ones
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (keys[mid] < from) lo = mid + 1;
+            else hi = mid;
+        }
+        a.starts[row * (a.groups + 1) + g] = (uint16_t)lo;
     }
 }
 
-// One work-group: the order of the sum does not depend on timing.
-__global__ __launch_bounds__(1024) void linear_summary_kernel(int64_t T, const float *loss, const int *counted,
-                                                              float *summary)
+// The sum of the losses and the number of rows that count, by one work-group:
+// their order does not depend on timing.
+template <int WAVES>
+__device__ __forceinline__ void write_summary(int64_t T, const float *loss, const int *counted, float *summary)
 {
-    __shared__ double sums[16];
-    __shared__ int counts[16];
+    __shared__ double sums[WAVES];
+    __shared__ int counts[WAVES];
     double sum = 0.0;
     int count = 0;
-    for (int64_t t = threadIdx.x; t < T; t += 1024) {
-        sum += (double)loss[t];
-        count += counted[t];
+    for (int64_t i = threadIdx.x; i < T; i += 64 * WAVES) {
+        sum += (double)loss[i];
+        count += counted[i];
     }
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) {
@@ -209,7 +254,7 @@ __global__ __launch_bounds__(1024) void linear_summary_kernel(int64_t T, const f
     }
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int w = 1; w < 16; ++w) {
+        for (int w = 1; w < WAVES; ++w) {
             sum += sums[w];
             count += counts[w];
         }
@@ -220,86 +265,64 @@ __global__ __launch_bounds__(1024) void linear_summary_kernel(int64_t T, const f
     }
 }
 
-// Eight adjacent values of a row, `left` of which are there.
-__device__ __forceinline__ void load8(const void *p, int64_t at, tgemm_dtype_t dtype, bool vec, int64_t left,
-                                      float (&v)[8])
+// A wavefront a row: the pairs (maximum, sum) of its column groups joined,
+// then the row's loss.  SUMMARY: one work-group takes all rows, and the summary.
+template <int WAVES, bool SUMMARY>
+__global__ __launch_bounds__(64 * WAVES) void linear_join_kernel(JoinArgs a, Teacher t, bool distill)
 {
-    if (vec && left >= 8) {
-        if (dtype == TGEMM_F32) {
-            const m16::f32x4 *q = (const m16::f32x4 *)((const float *)p + at);
-            const m16::f32x4 lo = q[0], hi = q[1];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = e < 4 ? lo[e & 3] : hi[e & 3];
+    const int lane = threadIdx.x & 63;
+    for (int64_t row = (int64_t)blockIdx.x * WAVES + (threadIdx.x >> 6); row < a.T; row += (int64_t)gridDim.x * WAVES) {
+        const float2 *part = a.part + row * a.groups;
+        float high = -INFINITY, sum = 0.0f;
+        for (int g = lane; g < a.groups; g += 64) {
+            const float2 p = part[g];
+            const float to = fmaxf(high, p.x);
+            if (to != -INFINITY) sum = sum * __builtin_amdgcn_exp2f(high - to) + p.y * __builtin_amdgcn_exp2f(p.x - to);
+            else sum += p.y;  // nothing yet, or a NaN
+            high = to;
+        }
+        const float top = wave_max(high);
+        sum = wave_sum(top == -INFINITY ? sum : sum * __builtin_amdgcn_exp2f(high - top));
+        const float lse = fmaf(top, 0.693147180559945309417f, logf(sum));
+        float loss;
+        bool counts;
+        if (!distill) {
+            const int64_t y = a.target[row];
+            counts = y != a.ignore;
+            loss = !counts ? 0.0f : y < 0 || y >= a.V ? NAN : lse - a.picked[row];
         } else {
-            const u16x8 w = *(const u16x8 *)((const uint16_t *)p + at);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[e] = dtype == TGEMM_BF16 ? (float)__builtin_bit_cast(__bf16, (uint16_t)w[e])
-                                           : (float)__builtin_bit_cast(_Float16, (uint16_t)w[e]);
+            const TeacherRow r = read_teacher(t, row, a.V, lane);
+            const float log_sum = logf(r.sum);
+            loss = 0.0f;
+            for (int k = lane; k < t.K; k += 64) {
+                const float v = load_as_float(t.logits, row * t.ld_logits + k, t.dtype);
+                if (v == -INFINITY) continue;
+                const float d = (v - r.high) * t.scale;
+                const float q = expf(d) / r.sum;
+                // an entry whose probability is below the least float32 adds nothing
+                if (q != 0.0f) loss += q * (d - log_sum - (a.student[row * t.K + k] - lse));
+            }
+            loss = wave_sum(loss) / (t.scale * t.scale);
+            counts = r.any;
+            loss = !counts ? 0.0f : r.bad ? NAN : loss;
         }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = e < left ? load_as_float(p, at + e, dtype) : 0.0f;
-    }
-}
-
-// A wavefront takes kTogether entries of a row at a time, so that as many
-// rows of W are on their way.
-__global__ __launch_bounds__(256) void linear_pick_kernel(PickArgs a)
-{
-    constexpr int kTogether = 8;
-    const int64_t row = blockIdx.x;
-    const int lane = threadIdx.x & 63, K = a.teacher.K;
-    for (int k0 = (threadIdx.x >> 6) * kTogether; k0 < K; k0 += 4 * kTogether) {
-        int64_t id[kTogether];
-        float sum[kTogether];
-#pragma unroll
-        for (int j = 0; j < kTogether; ++j) {
-            const int k = min(k0 + j, K - 1);
-            const float v = load_as_float(a.teacher.logits, row * a.teacher.ld_logits + k, a.teacher.dtype);
-            id[j] = a.teacher.ids[row * a.teacher.ld_ids + k];
-            sum[j] = v == -INFINITY ? 0.0f : id[j] < 0 || id[j] >= a.V ? NAN : 0.0f;
-            // an entry that is absent or out of range adds nothing: row 0 stands in for it
-            if (v == -INFINITY || id[j] < 0 || id[j] >= a.V) id[j] = -1;
-        }
-        for (int64_t d = lane * 8; d < a.D; d += 512) {
-            float x[8];
-            load8(a.X, row * a.ldx + d, a.dtype, a.vec, a.D - d, x);
-            float w[kTogether][8];
-#pragma unroll
-            for (int j = 0; j < kTogether; ++j) load8(a.W, max(id[j], (int64_t)0) * a.ldw + d, a.dtype, a.vec, a.D - d, w[j]);
-#pragma unroll
-            for (int j = 0; j < kTogether; ++j)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sum[j] = id[j] < 0 ? sum[j] : fmaf(x[e], w[j][e], sum[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < kTogether; ++j) {
-            sum[j] = wave_sum(sum[j]) * a.teacher.scale;
-            if (lane == j && k0 + j < K) a.student[row * K + k0 + j] = sum[j];
+        if (lane == 0) {
+            a.lse[row] = lse;
+            a.loss[row] = loss;
+            if (a.summary != nullptr) a.counted[row] = counts;
         }
     }
+    if (!SUMMARY) return;
+
+    // the whole batch is in this work-group
+    __syncthreads();
+    write_summary<WAVES>(a.T, a.loss, a.counted, a.summary);
 }
 
-__device__ __forceinline__ float grad_of(const CoefArgs &a, int64_t row)
+__global__ __launch_bounds__(1024) void linear_summary_kernel(int64_t T, const float *loss, const int *counted,
+                                                              float *summary)
 {
-    const float g = a.grad[row * a.grad_step] * a.factor;
-    return a.weight != nullptr ? g * *a.weight : g;
-}
-
-__device__ __forceinline__ void put_coef(const CoefArgs &a, int64_t row, float c, int &exponent)
-{
-    exponent = kNoExponent;
-    if (a.half) {
-        int e = 0;
-        if (c != 0.0f && !__builtin_isinf(c) && !__builtin_isnan(c)) {
-            c = ldexpf(frexpf(c, &e), kHalfShift);
-            exponent = e;
-        }
-        a.row_scale[row] = ldexpf(1.0f, e - kHalfShift);
-        a.exps[row] = e;
-    }
-    a.coef[row] = c;
+    write_summary<16>(T, loss, counted, summary);
 }
 
 template <int WAVES>
@@ -322,8 +345,7 @@ __global__ __launch_bounds__(256) void linear_ce_coef_kernel(CoefArgs a)
     const int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x;
     int exponent = kNoExponent;
     if (row < a.T) {
-        const int64_t y = a.target[row];
-        put_coef(a, row, y == a.ignore ? 0.0f : y < 0 || y >= a.V ? NAN : grad_of(a, row), exponent);
+        put_coef(a, row, ce_factor(a, row), exponent);
     }
     put_block_max<4>(a, blockIdx.x, exponent);
 }
@@ -404,7 +426,9 @@ __global__ __launch_bounds__(256) void linear_sum_kernel(SumArgs a)
         const float *part = a.part + row * a.ld + col;
         m16::f32x4 v = *(const m16::f32x4 *)part;
         for (int s = 1; s < a.count; ++s) v += *(const m16::f32x4 *)(part + s * a.stride);
-        if (a.row_scale != nullptr) v *= a.row_scale[row];
+        float scale = a.row_scale != nullptr ? a.row_scale[row] : 1.0f;
+        if (a.all_scale != nullptr) scale *= *a.all_scale;
+        v *= scale;
         const int64_t at = row * a.ldo + col;
         if (a.vec && col + 4 <= a.D) {
             if (a.dtype == TGEMM_F32) {
@@ -443,26 +467,43 @@ unsigned blocks_for(int64_t items)
 
 hipError_t launch_copy(const CopyArgs &a, hipStream_t stream)
 {
-    linear_copy_kernel<<<blocks_for(a.rows_out * (a.ld_out / 8)), 256, 0, stream>>>(a);
+    linear_copy_kernel<<<blocks_for(a.rows_out * (a.ld_out / 8)), 256, 0, stream>>>(a, a.make ? *a.make : CoefArgs{},
+                                                                                     a.make != nullptr);
     return hipGetLastError();
 }
+
+// Up to this many rows one work-group joins the statistics and writes the
+// summary too: 6 µs for 33 rows against 4.6 and 4.8 µs and a launch between.
+// (A counter by which the last of many work-groups finds itself needs fences
+// that cost more than the launch: 57 against 13 µs for 3000 rows.)
+constexpr int64_t kSoloRows = 64;
 
 hipError_t launch_join(const JoinArgs &a, hipStream_t stream)
 {
-    linear_join_kernel<<<(unsigned)((a.T + 3) / 4), 256, 0, stream>>>(a, a.teacher ? *a.teacher : Teacher{},
-                                                                      a.teacher != nullptr);
+    const Teacher t = a.teacher ? *a.teacher : Teacher{};
+    const bool distill = a.teacher != nullptr;
+    if (a.summary != nullptr && a.T <= kSoloRows) {
+        linear_join_kernel<16, true><<<1, 1024, 0, stream>>>(a, t, distill);
+        return hipGetLastError();
+    }
+    linear_join_kernel<4, false><<<(unsigned)((a.T + 3) / 4), 256, 0, stream>>>(a, t, distill);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.summary == nullptr) return e;
+    linear_summary_kernel<<<1, 1024, 0, stream>>>(a.T, a.loss, a.counted, a.summary);
     return hipGetLastError();
 }
 
-hipError_t launch_summary(int64_t T, const float *loss, const int *counted, float *summary, hipStream_t stream)
+hipError_t launch_summary_none(float *summary, hipStream_t stream)
 {
-    linear_summary_kernel<<<1, 1024, 0, stream>>>(T, loss, counted, summary);
+    linear_summary_kernel<<<1, 1024, 0, stream>>>(0, nullptr, nullptr, summary);
     return hipGetLastError();
 }
 
-hipError_t launch_pick(const PickArgs &a, hipStream_t stream)
+hipError_t launch_sort(const SortArgs &a, hipStream_t stream)
 {
-    linear_pick_kernel<<<(unsigned)a.T, 256, 0, stream>>>(a);
+    int room = 2;
+    while (room < a.teacher.K) room *= 2;
+    linear_sort_kernel<<<(unsigned)a.T, 64, (size_t)room * 8, stream>>>(a, room);
     return hipGetLastError();
 }
 

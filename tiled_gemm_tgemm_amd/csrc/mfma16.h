@@ -294,12 +294,15 @@ struct TileProduct {
             int m0, n0, split;
             place(at_id, m0, n0, split);
             steps_of(split, first, last);
-            a_last = A_MC ? p.mn_a - 8 - m0 : p.mn_a - 1 - m0;
-            b_last = B_MC ? p.mn_b - 8 - n0 : p.mn_b - 1 - n0;
+            // a tile may lie past an operand's last row: it takes that one
+            const int a_end = p.mn_a - (A_MC ? 8 : 1), b_end = p.mn_b - (B_MC ? 8 : 1);
+            const int a0 = min(m0, a_end), b0 = min(n0, b_end);
+            a_last = a_end - a0;
+            b_last = b_end - b0;
             la.place(p.lda, a_last, A_MC ? p.k_a - 1 - start(first, p.k_a) : 0);
             lb.place(p.ldb, b_last, B_MC ? p.k_b - 1 - start(first, p.k_b) : 0);
-            A = (const char *)p.A + (A_MC ? (int64_t)m0 : (int64_t)m0 * p.lda) * 2;
-            B = (const char *)p.B + (B_MC ? (int64_t)n0 : (int64_t)n0 * p.ldb) * 2;
+            A = (const char *)p.A + (A_MC ? (int64_t)a0 : (int64_t)a0 * p.lda) * 2;
+            B = (const char *)p.B + (B_MC ? (int64_t)b0 : (int64_t)b0 * p.ldb) * 2;
             seg = 0;
             k = first;
         };
