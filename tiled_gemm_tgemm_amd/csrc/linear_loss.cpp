@@ -102,25 +102,34 @@ bool as_stored(const void *p, int64_t ld, const Head &h)
 }
 
 // The tile for an M×N product of `steps` steps, and into how many parts its
-// sum is split (1 where `split` is false): least time by its rounds over the
-// 256 compute units, a tile's time being its area over the rate that its shape
-// sustains, with a fixed cost for filling and draining it, and the writing and
-// reading of the parts.  The unit is a 256×256 tile's step, 1.5 µs.
+// sum is split (1 where `split` is false): the least estimated time, in µs.  A
+// compute unit holds up to wg_per_cu tiles at once; their step takes as long
+// as their area at the rate that the shape sustains (a 256×256 tile 1.5 µs,
+// 1.37 PFLOP/s on 256 compute units), but not less than the loads' way there
+// and back, and a tile takes 4 µs to begin and to end.  Measured at 32 steps
+// with 256, 128 and 32 rows a tile: 512×16384 40, 29 and 58 µs; 64×32000 43,
+// 23 and 22; 4096×32768 with 8 steps 127, 162 and 275.
 struct Choice {
     int tile = 0, splits = 1;
 };
 Choice choose_tile(int64_t M, int64_t N, int64_t steps, bool split = false)
 {
-    static const double rate[] = {1.0, 0.7, 0.25};
+    static const double rate[] = {1.0, 0.83, 0.375};
     Choice best;
     double least = -1;
     for (int i = 0; i < tile_count(); ++i) {
         const TileShape &s = tile_shape(i);
         const int64_t tiles = ceil_div(M, s.bm) * ceil_div(N, s.bn);
         for (int64_t parts = 1; parts == 1 || (split && parts <= 64 && steps / parts >= 4); ++parts) {
-            const double rounds = (double)ceil_div(tiles * parts, (int64_t)256 * s.wg_per_cu) * s.wg_per_cu;
-            double time = rounds * ((double)s.bm * s.bn / 65536.0 / rate[i] * (double)ceil_div(steps, parts) + 3.0);
-            if (parts > 1) time += 4.0 + (double)M * (double)N * 8.0 * (double)parts / 5e12 / 1.5e-6;
+            const int64_t on_one = ceil_div(tiles * parts, 256);
+            auto round = [&](int64_t held) {
+                const double step = (double)held * s.bm * s.bn / 65536.0 / rate[i] * 1.5;
+                return (double)ceil_div(steps, parts) * (step > 0.75 ? step : 0.75) + 4.0;
+            };
+            double time = (double)(on_one / s.wg_per_cu) * round(s.wg_per_cu);
+            if (on_one % s.wg_per_cu != 0) time += round(on_one % s.wg_per_cu);
+            // the parts are written and read once more, by another launch
+            if (parts > 1) time += 6.0 + (double)M * (double)N * 8.0 * (double)parts / 5e6;
             if (least < 0 || time < least) {
                 least = time;
                 best.tile = i;
