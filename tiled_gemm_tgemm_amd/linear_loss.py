@@ -16,6 +16,7 @@ return without waiting.  include/tgemm.h states the arithmetic.
 
 from __future__ import annotations
 
+import copy
 import functools
 
 from . import _lib
@@ -87,6 +88,15 @@ class _Call:
         self.stream = torch.cuda.current_stream(X.device).cuda_stream if stream is None else stream
         self.made = []
 
+    def again(self, X, W):
+        """This call for the backward pass: the same tensors (checked before), wherever they are now."""
+        import torch
+
+        c = copy.copy(self)
+        c.head = (*self.head[:4], X.data_ptr(), self.head[5], W.data_ptr(), self.head[7])
+        c.stream = torch.cuda.current_stream(self.device).cuda_stream
+        return c
+
     def teacher(self, ids, logits, temperature):
         import torch
 
@@ -114,7 +124,7 @@ class _Call:
 
     def gradient(self, t, name, shape):
         if t is None:
-            t = self.new(shape, self.dtype)
+            return self.new(shape, self.dtype), shape[1]
         return t, _rows(t, name, shape, self.device, self.dtype)
 
     def room(self, workspace, k, backward):
@@ -134,9 +144,13 @@ class _Call:
 
         from . import _hold_for_stream
 
-        with torch.cuda.device(self.device):
-            _hold_for_stream(self.stream, self.device, *self.made)
+        _hold_for_stream(self.stream, self.device, *self.made)
+        self.made = []  # the call may be kept for the backward pass, its workspace not
+        if torch.cuda.current_device() == self.device.index:
             st = getattr(_lib, entry)(*self.head, *args, self.stream)
+        else:
+            with torch.cuda.device(self.device):
+                st = getattr(_lib, entry)(*self.head, *args, self.stream)
         if st != _lib.TGEMM_SUCCESS:
             raise TgemmError(st, entry)
 
@@ -145,14 +159,12 @@ def _ptr(t):
     return 0 if t is None else t.data_ptr()
 
 
-def _ce_forward(X, W, target, ignore_index, loss, lse, summary, workspace, stream):
-    c = _Call(X, W, stream)
-    target = _ids(target, "target", (c.T,), c.device)
+def _ce_forward(c, target, ignore_index, loss, lse, summary, workspace):
+    """(loss, lse, summary or None); target checked."""
     loss, lse = c.floats(loss, "loss", (c.T,)), c.floats(lse, "lse", (c.T,))
-    if summary:
-        summary = c.floats(None, "summary", (3,))
+    summary = c.floats(None, "summary", (3,)) if summary else None
     c.queue("tgemm_linear_ce_forward", target.data_ptr(), int(ignore_index), loss.data_ptr(), lse.data_ptr(),
-            _ptr(summary) if summary is not False else 0, *c.room(workspace, 0, 0))
+            _ptr(summary), *c.room(workspace, 0, 0))
     return loss, lse, summary
 
 
@@ -161,10 +173,11 @@ def linear_cross_entropy_forward(X, W, target, *, ignore_index=-100, loss=None, 
     with y = target_t (int64), 0 where y is ignore_index and NaN where y is outside the vocabulary otherwise.  loss
     and lse: float32 tensors of T to write to; workspace: a CUDA uint8 tensor of at least
     tgemm_linear_loss_workspace_size bytes (allocated if omitted; two calls in flight at once need two)."""
-    return _ce_forward(X, W, target, ignore_index, loss, lse, False, workspace, stream)[:2]
+    c = _Call(X, W, stream)
+    return _ce_forward(c, _ids(target, "target", (c.T,), c.device), ignore_index, loss, lse, False, workspace)[:2]
 
 
-def _gradients(c, X, W, dX, dW, need):
+def _gradients(c, dX, dW, need):
     dX, lddx = c.gradient(dX, "dX", (c.T, c.D)) if need[0] else (None, c.D)
     dW, lddw = c.gradient(dW, "dW", (c.V, c.D)) if need[1] else (None, c.D)
     return dX, dW, (_ptr(dX), lddx, _ptr(dW), lddw)
@@ -181,11 +194,9 @@ def _grad_loss(c, grad):
     return grad.data_ptr(), grad.stride(0) if grad.dim() and c.T > 1 else 0
 
 
-def _ce_backward(grad_loss, weight, X, W, target, lse, ignore_index, dX, dW, need, workspace, stream):
-    c = _Call(X, W, stream)
-    target = _ids(target, "target", (c.T,), c.device)
-    lse = _floats(lse, "lse", (c.T,), c.device)
-    dX, dW, outs = _gradients(c, X, W, dX, dW, need)
+def _ce_backward(c, grad_loss, weight, target, lse, ignore_index, dX, dW, need, workspace):
+    """target and lse checked"""
+    dX, dW, outs = _gradients(c, dX, dW, need)
     c.queue("tgemm_linear_ce_backward", target.data_ptr(), int(ignore_index), lse.data_ptr(), *_grad_loss(c, grad_loss),
             _ptr(weight), *outs, *c.room(workspace, 0, 1))
     return dX, dW
@@ -196,18 +207,19 @@ def linear_cross_entropy_backward(grad_loss, X, W, target, lse, *, ignore_index=
     """(dX, dW) = the gradients of sum_t grad_loss_t·loss_t (tgemm_linear_ce_backward).  grad_loss: float32, one
     value a row or one of no dimension for all; lse as linear_cross_entropy_forward gave it.  dX, dW: row-major
     tensors to write to; need: which of the two are computed (None is returned for the other)."""
-    return _ce_backward(grad_loss, None, X, W, target, lse, ignore_index, dX, dW, need, workspace, stream)
-
-
-def _kd_forward(X, W, teacher_ids, teacher_logits, temperature, loss, lse, student, summary, workspace, stream):
     c = _Call(X, W, stream)
-    teacher = c.teacher(teacher_ids, teacher_logits, temperature)
+    target = _ids(target, "target", (c.T,), c.device)
+    return _ce_backward(c, grad_loss, None, target, _floats(lse, "lse", (c.T,), c.device), ignore_index, dX, dW, need,
+                        workspace)
+
+
+def _kd_forward(c, teacher, loss, lse, student, summary, workspace):
+    """(loss, lse, student, summary or None); teacher as _Call.teacher gave it"""
     loss, lse = c.floats(loss, "loss", (c.T,)), c.floats(lse, "lse", (c.T,))
     student = c.floats(student, "student", (c.T, c.K))
-    if summary:
-        summary = c.floats(None, "summary", (3,))
-    c.queue("tgemm_linear_kd_forward", *teacher, loss.data_ptr(), lse.data_ptr(), student.data_ptr(),
-            _ptr(summary) if summary is not False else 0, *c.room(workspace, c.K, 0))
+    summary = c.floats(None, "summary", (3,)) if summary else None
+    c.queue("tgemm_linear_kd_forward", *teacher, loss.data_ptr(), lse.data_ptr(), student.data_ptr(), _ptr(summary),
+            *c.room(workspace, c.K, 0))
     return loss, lse, student, summary
 
 
@@ -218,16 +230,14 @@ def linear_distillation_forward(X, W, teacher_ids, teacher_logits, *, temperatur
     -inf is absent.  With q the softmax of a row's logits / temperature over its entries and z the student's logits
     / temperature, loss_t = temperature²·sum_k q_k·(log q_k - (z_k - lse_t)), 0 for a row without entries and NaN
     where an entry's id is outside the vocabulary.  student: z at the teacher's ids (0 where absent)."""
-    return _kd_forward(X, W, teacher_ids, teacher_logits, temperature, loss, lse, student, False, workspace, stream)[:3]
-
-
-def _kd_backward(grad_loss, weight, X, W, teacher_ids, teacher_logits, lse, student, temperature, dX, dW, need,
-                 workspace, stream):
     c = _Call(X, W, stream)
     teacher = c.teacher(teacher_ids, teacher_logits, temperature)
-    lse = _floats(lse, "lse", (c.T,), c.device)
-    student = _floats(student, "student", (c.T, c.K), c.device)
-    dX, dW, outs = _gradients(c, X, W, dX, dW, need)
+    return _kd_forward(c, teacher, loss, lse, student, False, workspace)[:3]
+
+
+def _kd_backward(c, grad_loss, weight, teacher, lse, student, dX, dW, need, workspace):
+    """teacher as _Call.teacher gave it; lse and student checked"""
+    dX, dW, outs = _gradients(c, dX, dW, need)
     c.queue("tgemm_linear_kd_backward", *teacher, lse.data_ptr(), student.data_ptr(), *_grad_loss(c, grad_loss),
             _ptr(weight), *outs, *c.room(workspace, c.K, 1))
     return dX, dW
@@ -237,8 +247,11 @@ def linear_distillation_backward(grad_loss, X, W, teacher_ids, teacher_logits, l
                                  dX=None, dW=None, need=(True, True), workspace=None, stream=None):
     """(dX, dW) = the gradients of sum_t grad_loss_t·loss_t (tgemm_linear_kd_backward); lse and student as
     linear_distillation_forward gave them, the rest as linear_cross_entropy_backward."""
-    return _kd_backward(grad_loss, None, X, W, teacher_ids, teacher_logits, lse, student, temperature, dX, dW, need,
-                        workspace, stream)
+    c = _Call(X, W, stream)
+    teacher = c.teacher(teacher_ids, teacher_logits, temperature)
+    lse = _floats(lse, "lse", (c.T,), c.device)
+    student = _floats(student, "student", (c.T, c.K), c.device)
+    return _kd_backward(c, grad_loss, None, teacher, lse, student, dX, dW, need, workspace)
 
 
 @functools.lru_cache(maxsize=None)
@@ -254,37 +267,40 @@ def _functions():
     class CrossEntropy(torch.autograd.Function):
         @staticmethod
         def forward(ctx, X, W, target, ignore_index, reduction):
-            loss, lse, summary = _ce_forward(X, W, target, ignore_index, None, None, reduction != "none", None, None)
+            c = _Call(X, W, None)
+            target = _ids(target, "target", (c.T,), c.device)
+            loss, lse, summary = _ce_forward(c, target, ignore_index, None, None, reduction != "none", None)
             ctx.save_for_backward(X, W, target, lse, summary if reduction == "mean" else None)
-            ctx.ignore_index = ignore_index
+            ctx.call, ctx.ignore_index = c, ignore_index
             return reduced(reduction, loss, summary)
 
         @staticmethod
         @once_differentiable
         def backward(ctx, grad):
             X, W, target, lse, summary = ctx.saved_tensors
-            weight = None if summary is None else summary[2:]
-            dX, dW = _ce_backward(grad, weight, X, W, target, lse, ctx.ignore_index, None, None,
-                                  ctx.needs_input_grad[:2], None, None)
+            dX, dW = _ce_backward(ctx.call.again(X, W), grad, None if summary is None else summary[2:], target, lse,
+                                  ctx.ignore_index, None, None, ctx.needs_input_grad, None)
             return dX, dW, None, None, None
 
     class Distillation(torch.autograd.Function):
         @staticmethod
         def forward(ctx, X, W, teacher_ids, teacher_logits, temperature, reduction):
-            loss, lse, student, summary = _kd_forward(X, W, teacher_ids, teacher_logits, temperature, None, None, None,
-                                                      reduction != "none", None, None)
+            c = _Call(X, W, None)
+            teacher = c.teacher(teacher_ids, teacher_logits, temperature)
+            loss, lse, student, summary = _kd_forward(c, teacher, None, None, None, reduction != "none", None)
             ctx.save_for_backward(X, W, teacher_ids, teacher_logits, lse, student,
                                   summary if reduction == "mean" else None)
-            ctx.temperature = temperature
+            ctx.call, ctx.temperature = c, temperature
             return reduced(reduction, loss, summary)
 
         @staticmethod
         @once_differentiable
         def backward(ctx, grad):
             X, W, ids, logits, lse, student, summary = ctx.saved_tensors
-            weight = None if summary is None else summary[2:]
-            dX, dW = _kd_backward(grad, weight, X, W, ids, logits, lse, student, ctx.temperature, None, None,
-                                  ctx.needs_input_grad[:2], None, None)
+            c = ctx.call.again(X, W)
+            dX, dW = _kd_backward(c, grad, None if summary is None else summary[2:],
+                                  c.teacher(ids, logits, ctx.temperature), lse, student, None, None,
+                                  ctx.needs_input_grad, None)
             return dX, dW, None, None, None, None
 
     return CrossEntropy, Distillation
