@@ -205,11 +205,14 @@ struct Reader {
     }
 };
 
-// The work-group's loads into LDS have arrived, and its reads of LDS are done.
-// The compiler's own barrier would not wait for loads that write LDS.
+// The work-group's loads into LDS have arrived but for the last FLYING of each
+// thread, and its reads of LDS are done.  The compiler's own barrier would not
+// wait for loads that write LDS.
+template <int FLYING>
 __device__ __forceinline__ void arrive()
 {
-    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+    static_assert(FLYING < 16, "four bits");
+    __builtin_amdgcn_s_waitcnt(0x0070 | FLYING);  // vmcnt(FLYING) lgkmcnt(0)
     __syncthreads();
 }
 
@@ -327,42 +330,49 @@ struct TileProduct {
             if (B_MC && ((k + 1) * BK > p.k_b || (p.segments > 1 && k == first))) lb.place(p.ldb, b_last, p.k_b - 1 - start_b);
             ++k;
         };
-        auto issue = [&](int stage, int lo, int hi) {
+        // A round of a KC operand may be just the rows that the wavefronts'
+        // first (or second) halves are made of.  Early loads: B and those of A.
+        constexpr bool kHalves = !A_MC && kThreads / 8 == FM / 2 * 16;
+        constexpr int kEarlyA = kHalves ? kLoadsA / 2 : 0, kEarly = kLoads - kLoadsA + kEarlyA;
+        auto issue = [&](int stage, int n) {  // the n-th load, early ones first
+            lds_char *to = lds + stage * kStage;
+            if (n < kEarlyA) la.issue_one(from_a, to, wave, 2 * n);
+            else if (n < kEarly) lb.issue_one(from_b, to + BM * BK * 2, wave, n - kEarlyA);
+            else la.issue_one(from_a, to, wave, kHalves ? 2 * (n - kEarly) + 1 : n - kEarly);
+        };
+        auto issue_all = [&](int stage) {
 #pragma unroll
-            for (int r = 0; r < kLoads; ++r) {
-                if (r < lo || r >= hi) continue;
-                if (r < kLoadsA) la.issue_one(from_a, lds + stage * kStage, wave, r);
-                else lb.issue_one(from_b, lds + stage * kStage + BM * BK * 2, wave, r - kLoadsA);
-            }
+            for (int n = 0; n < kLoads; ++n) issue(stage, n);
         };
 
         Acc acc;
-        // A step has four phases: each half of the wavefront's rows with each
-        // half of the step's 64 values of k.  Two sets of fragments: those of
+        // A step has four phases: each half of the step's 64 values of k with
+        // each half of the wavefront's rows.  Two sets of fragments: those of
         // the next phase are read while these are multiplied.
         typename Frag<E>::type a[2][FM / 2], b[2][FN];
         auto read = [&](int stage, int phase) {
             lds_char *as = lds + stage * kStage, *bs = as + BM * BK * 2;
-            const int s = phase >> 1, h = phase & 1;
+            const int s = phase & 1, h = phase >> 1;
             if (h == 0) {
 #pragma unroll
                 for (int j = 0; j < FN; ++j) b[s][j] = rb.template read<E>(bs, j, s);
             }
 #pragma unroll
-            for (int i = 0; i < FM / 2; ++i) a[h][i] = ra.template read<E>(as, h * (FM / 2) + i, s);
+            for (int i = 0; i < FM / 2; ++i) a[s][i] = ra.template read<E>(as, h * (FM / 2) + i, s);
         };
+        constexpr int kProducts = FM / 2 * FN;
         auto multiply = [&](int phase, int m) {
-            const int s = phase >> 1, h = phase & 1, i = m / FN, j = m % FN;
-            acc[h * (FM / 2) + i][j] = Frag<E>::mfma(b[s][j], a[h][i], acc[h * (FM / 2) + i][j]);
+            const int s = phase & 1, h = phase >> 1, i = m / FN, j = m % FN;
+            acc[h * (FM / 2) + i][j] = Frag<E>::mfma(b[s][j], a[s][i], acc[h * (FM / 2) + i][j]);
         };
 
         at_id = blockIdx.x;
         open();
         seek();
-        issue(0, 0, kLoads);
+        issue_all(0);
         seek();
-        issue(1, 0, kLoads);
-        arrive();
+        issue_all(1);
+        arrive<0>();
         read(0, 0);
         int stage = 0;
         for (int id = blockIdx.x; id < tiles; id += gridDim.x) {
@@ -377,26 +387,36 @@ struct TileProduct {
             steps_of(split, from, to);
             for (int n = (to - from) * p.segments; n > 0; --n) {
                 // A step on the slices of `stage`, its first fragments read.
-                // The barrier stands before the last phase, whose fragments
-                // are in registers by then: this stage is read no more, so the
-                // loads of the step after next go there, and the next step's
-                // slices have arrived, so its first fragments are read under
-                // these products.
-                constexpr int kProducts = FM / 2 * FN;
+                // The first barrier stands after the phases that read B and
+                // the first half of A, the second before the last phase, whose
+                // fragments are in registers by then: what is read no more is
+                // loaded for the step after next.  At the second one the next
+                // step's slices have arrived, so its first fragments are read
+                // under the last products.
                 seek();
+                read(stage, 1);
 #pragma unroll
-                for (int phase = 0; phase < 3; ++phase) {
-                    read(stage, phase + 1);
+                for (int m = 0; m < kProducts; ++m) multiply(0, m);
+                spread<kProducts, kReadsA + kReadsB>();
+                read(stage, 2);
 #pragma unroll
-                    for (int m = 0; m < kProducts; ++m) multiply(phase, m);
-                    if (phase == 1) spread<kProducts, kReadsA + kReadsB>();
-                    else spread<kProducts, kReadsA>();
+                for (int m = 0; m < kProducts; ++m) multiply(1, m);
+                spread<kProducts, kReadsA>();
+                __syncthreads();
+                read(stage, 3);
+#pragma unroll
+                for (int m = 0; m < kProducts; ++m) {
+#pragma unroll
+                    for (int n = m * kEarly / kProducts; n < (m + 1) * kEarly / kProducts; ++n) issue(stage, n);
+                    multiply(2, m);
                 }
-                arrive();
+                arrive<kEarly>();
                 read(stage ^ 1, 0);
 #pragma unroll
                 for (int m = 0; m < kProducts; ++m) {
-                    issue(stage, m * kLoads / kProducts, (m + 1) * kLoads / kProducts);
+                    constexpr int kLate = kLoads - kEarly;
+#pragma unroll
+                    for (int n = m * kLate / kProducts; n < (m + 1) * kLate / kProducts; ++n) issue(stage, kEarly + n);
                     multiply(3, m);
                 }
                 stage ^= 1;
