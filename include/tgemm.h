@@ -362,8 +362,8 @@ int64_t tgemm_sgemm_host_workspace_size(int64_t M, int64_t N, int64_t K, int64_t
  *             gradients.  Products of 16-bit values are exact and summed in
  *             float32.  A float32 operand is split into three bf16 planes (24
  *             bits) and the six products of planes that reach 2^-24 of the
- *             largest are summed in float32; in X and W an infinity gives NaN
- *             there.  Row statistics, losses and the sums over pieces are
+ *             largest are summed in float32; an infinity there, or a value
+ *             above 3.39e38, gives NaN or infinity.  Row statistics, losses and the sums over pieces are
  *             float32.  The logits' gradient is rounded to the operands' type
  *             (float32: to three planes) before the two gradient products.
  * Sizes       0 <= T < 2^24, 1 <= V <= 2^24, 1 <= D <= 2^22, 1 <= K <= 1024,

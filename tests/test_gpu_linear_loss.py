@@ -17,7 +17,8 @@ TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
 # tiles, and enough rows or words for several tiles each way
 SIZES = [(1, 1, 1), (1, 257, 64), (2, 31, 7), (5, 300, 40), (20, 129, 1000), (33, 1000, 128), (64, 512, 64),
          (65, 513, 72), (130, 777, 200), (257, 2049, 64), (256, 1024, 256), (300, 5003, 320), (1, 20011, 192),
-         (700, 130, 65), (2100, 100, 64), (1500, 600, 512)]
+         (700, 130, 65), (2100, 100, 64), (1500, 600, 512),
+         (16, 4001, 136), (17, 130, 520), (32, 1000, 8), (3, 70, 384)]
 
 
 @pytest.fixture(scope="module", autouse=True)

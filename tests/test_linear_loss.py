@@ -121,10 +121,12 @@ def test_workspace_sizes():
     for refused in (dict(T=0), dict(T=-1), dict(V=0), dict(dtype=7), dict(ldx=3), dict(V=1 << 25)):
         assert size(**refused) == 0 and size(**refused, backward=1) == 0
     # a copy of W is laid out only where the matrix cores cannot read it as it is stored
-    stored = size(V=100000)
+    stored = size(T=64, V=100000)
     for copied in (dict(W=W_ + 2), dict(ldw=68), dict(dtype=0)):
-        assert size(V=100000, **copied) >= stored + 100000 * 64 * 2
-    assert size(V=100000, D=60) >= stored + 100000 * 64 * 2
+        assert size(T=64, V=100000, **copied) >= stored + 100000 * 64 * 2
+    assert size(T=64, V=100000, D=60) >= stored + 100000 * 64 * 2
+    # a few rows take W as it is, in float32 too
+    assert size(T=32, V=100000, dtype=0) < 100000 * 64
     # the pieces of the logits' gradient are far smaller than the logits
     T, V = 16384, 131072
     assert size(T=T, V=V, backward=1) < T * V * 2 // 8

@@ -152,7 +152,8 @@ struct Plan {
     int64_t total = 0;
     int64_t x = -1, w = -1, xs = -1;  // operands laid out for the matrix cores
     // forward
-    int stat_tile = 0, groups = 0;
+    bool few = false;
+    int stat_tile = 0, groups = 0, group_columns = 0;
     int64_t part = -1, picked = -1, counted = -1, starts = -1, list = -1;
     // backward
     int64_t piece = 0, pieces = 0, ldg = 0;
@@ -193,9 +194,20 @@ bool fits(int64_t M, int64_t N, int tile, int64_t splits)
 
 bool plan_forward(Plan &p, const Head &h, int64_t teacher_k)
 {
-    plan_operands(p, h, false);
-    p.stat_tile = choose_tile(h.T, h.V, p.Dp / kStepK * p.segments).tile;
-    p.groups = (int)ceil_div(h.V, tile_shape(p.stat_tile).stat_columns);
+    // The rows of X come from the caches once for every 16 words, which is as
+    // much again as W from 16 rows on: tiles take more than 8 rows sooner
+    // where they need no copy of W (17×32000×2048 bf16 31 against 40 µs, one
+    // row 58 against 47; float32 341 against 90).
+    const bool stored = as_stored(h.X, h.ldx, h) && as_stored(h.W, h.ldw, h);
+    p.few = h.T <= (stored ? 8 : kFewRows) && h.D % 8 == 0 && rows16(h.X, h.ldx, h.dtype) && rows16(h.W, h.ldw, h.dtype);
+    if (p.few) {
+        p.group_columns = kFewColumns;
+    } else {
+        plan_operands(p, h, false);
+        p.stat_tile = choose_tile(h.T, h.V, p.Dp / kStepK * p.segments).tile;
+        p.group_columns = tile_shape(p.stat_tile).stat_columns;
+    }
+    p.groups = (int)ceil_div(h.V, p.group_columns);
     p.part = p.take(h.T * p.groups * 8);
     if (teacher_k > 0) {
         p.starts = p.take(h.T * (p.groups + 1) * 2);
@@ -204,7 +216,7 @@ bool plan_forward(Plan &p, const Head &h, int64_t teacher_k)
         p.picked = p.take(h.T * 4);
     }
     p.counted = p.take(h.T * 4);
-    return fits(h.T, h.V, p.stat_tile, 1);
+    return p.few || fits(h.T, h.V, p.stat_tile, 1);
 }
 
 bool plan_backward(Plan &p, const Head &h)
@@ -328,7 +340,7 @@ tgemm_status_t forward(const Plan &p, const Head &h, const Labels &l, float *los
     s.target = l.target;
     s.picked = in<float>(ws, p.picked);
     if (l.teacher != nullptr) {
-        const SortArgs k{h.T, h.V, p.groups, tile_shape(p.stat_tile).stat_columns, *l.teacher, in<uint16_t>(ws, p.starts),
+        const SortArgs k{h.T, h.V, p.groups, p.group_columns, *l.teacher, in<uint16_t>(ws, p.starts),
                          in<uint32_t>(ws, p.list), student};
         e = launch_sort(k, stream);
         if (e != hipSuccess) return from_hip(e);
@@ -337,7 +349,7 @@ tgemm_status_t forward(const Plan &p, const Head &h, const Labels &l, float *los
         s.K = l.teacher->K;
         s.student = student;
     }
-    e = launch_stats(p.half, p.stat_tile, s, stream);
+    e = p.few ? launch_stats_few(s, h.dtype, (int)h.D, stream) : launch_stats(p.half, p.stat_tile, s, stream);
     if (e != hipSuccess) return from_hip(e);
     JoinArgs j{h.T, h.V, p.groups, s.part, l.target, l.ignore, s.picked, l.teacher, student, loss, lse, summary,
                in<int>(ws, p.counted)};

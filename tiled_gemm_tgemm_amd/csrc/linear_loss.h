@@ -49,6 +49,12 @@ struct StatsArgs {
 };
 hipError_t launch_stats(bool half, int tile, const StatsArgs &a, hipStream_t stream);
 
+// launch_stats for at most kFewRows rows, on operands as they are stored (rows
+// 16-byte aligned, D a multiple of 8); column groups of kFewColumns.
+constexpr int64_t kFewRows = 32;
+constexpr int kFewColumns = 64;
+hipError_t launch_stats_few(const StatsArgs &a, tgemm_dtype_t dtype, int D, hipStream_t stream);
+
 // A piece of the logits' gradient: G[t][v - v0] = coef[t]·(exp(s·z - lse[t]) -
 // [v = target[t]]), zero past the ends, 16-bit or three bf16 planes.
 struct GradArgs {

@@ -34,16 +34,6 @@ __device__ __forceinline__ float wave_sum(float v)
     return v;
 }
 
-// The high part of a float32 as bf16.  A finite value that would round to
-// infinity keeps the largest bf16, so that the rest can hold what is missing.
-__device__ __forceinline__ __bf16 plane_of(float x)
-{
-    const __bf16 h = (__bf16)x;
-    if (__builtin_isinf((float)h) && !__builtin_isinf(x))
-        return __builtin_bit_cast(__bf16, (uint16_t)(0x7F7F | (__builtin_bit_cast(uint32_t, x) >> 16 & 0x8000)));
-    return h;
-}
-
 __device__ __forceinline__ uint16_t bits(__bf16 v) { return __builtin_bit_cast(uint16_t, v); }
 __device__ __forceinline__ uint16_t bits(_Float16 v) { return __builtin_bit_cast(uint16_t, v); }
 
@@ -114,14 +104,11 @@ __global__ __launch_bounds__(256) void linear_copy_kernel(CopyArgs a, CoefArgs m
             const float *from = (const float *)a.src + row * a.ld + col;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float x = e < left ? from[e] : 0.0f;
-                const __bf16 h = plane_of(x);
-                const bool finite = !__builtin_isinf(x) && !__builtin_isnan(x);
-                const float r = finite ? x - (float)h : 0.0f;
-                const __bf16 m = (__bf16)r;
+                __bf16 h, m, l;
+                m16::split(e < left ? from[e] : 0.0f, h, m, l);
                 v[0][e] = bits(h);
                 v[1][e] = bits(m);
-                v[2][e] = bits((__bf16)(r - (float)m));
+                v[2][e] = bits(l);
             }
         } else if (counts) {
             const uint16_t *from = (const uint16_t *)a.src + row * a.ld + col;

@@ -65,6 +65,17 @@ struct Operands {
 constexpr int kPairsA = (1 << 0) | (0 << 2) | (2 << 4) | (0 << 6) | (1 << 8) | (0 << 10);
 constexpr int kPairsB = (1 << 0) | (2 << 2) | (0 << 4) | (1 << 6) | (0 << 8) | (0 << 10);
 
+// x = high + middle + low.  An infinity or NaN is all in the high part, and so
+// is a value above 3.39e38, which rounds to infinity there.
+__device__ __forceinline__ void split(float x, __bf16 &high, __bf16 &middle, __bf16 &low)
+{
+    high = (__bf16)x;
+    float rest = x - (float)high;
+    if (__builtin_isinf(rest) || __builtin_isnan(rest)) rest = 0.0f;
+    middle = (__bf16)rest;
+    low = (__bf16)(rest - (float)middle);
+}
+
 template <class E>
 struct Frag;
 template <>
