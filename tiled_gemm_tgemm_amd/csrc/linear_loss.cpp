@@ -93,11 +93,13 @@ tgemm_status_t check_head(const Head &h)
 }
 
 // The matrix cores take an operand as it is stored if it is 16-bit, its rows
-// are whole steps of K and start 16-byte aligned, and a tile's offsets fit 32
-// bits; otherwise the call lays a copy out first.
-bool as_stored(const void *p, int64_t ld, const Head &h)
+// start 16-byte aligned and hold whole pieces of 16 bytes, and a tile's
+// offsets fit 32 bits; otherwise the call lays a copy out first.  X has to
+// end in whole steps of K besides, so that what stands in for W's last step
+// meets zeros.
+bool as_stored(const void *p, int64_t ld, const Head &h, int64_t whole = 8)
 {
-    return h.dtype != TGEMM_F32 && h.D % kStepK == 0 && ld % 8 == 0 && ld <= kMaxD &&
+    return h.dtype != TGEMM_F32 && h.D % whole == 0 && ld % 8 == 0 && ld <= kMaxD &&
            reinterpret_cast<uintptr_t>(p) % 16 == 0;
 }
 
@@ -180,7 +182,7 @@ void plan_operands(Plan &p, const Head &h, bool backward)
     if (p.copy_w) p.w = p.take(h.V * p.Dp * 2 * p.planes);
     // the backward pass holds X with its rows that do not count cleared (`xs`);
     // only fp16, where `xs` is scaled too, may need another copy
-    p.copy_x = !as_stored(h.X, h.ldx, h) && (!backward || p.half);
+    p.copy_x = !as_stored(h.X, h.ldx, h, kStepK) && (!backward || p.half);
     if (p.copy_x) p.x = p.take(h.T * p.Dp * 2 * p.planes);
     if (backward) p.xs = p.take(p.Tp * p.Dp * 2 * p.planes);
 }
@@ -198,7 +200,7 @@ bool plan_forward(Plan &p, const Head &h, int64_t teacher_k)
     // much again as W from 16 rows on: tiles take more than 8 rows sooner
     // where they need no copy of W (17×32000×2048 bf16 31 against 40 µs, one
     // row 58 against 47; float32 341 against 90).
-    const bool stored = as_stored(h.X, h.ldx, h) && as_stored(h.W, h.ldw, h);
+    const bool stored = as_stored(h.X, h.ldx, h, kStepK) && as_stored(h.W, h.ldw, h);
     p.few = h.T <= (stored ? 8 : kFewRows) && h.D % 8 == 0 && rows16(h.X, h.ldx, h.dtype) && rows16(h.W, h.ldw, h.dtype);
     if (p.few) {
         p.group_columns = kFewColumns;
@@ -334,6 +336,7 @@ tgemm_status_t forward(const Plan &p, const Head &h, const Labels &l, float *los
     s.op.ldb = w.ld;
     s.op.plane_b = w.plane;
     s.op.mn_b = (int)h.V;
+    s.op.k_b = (int)(p.copy_w ? p.Dp : h.D);
     s.scale = l.teacher ? l.teacher->scale : 1.0f;
     s.part = in<float2>(ws, p.part);
     s.groups = p.groups;
@@ -428,6 +431,7 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
         a.op.ldb = w.ld;
         a.op.plane_b = w.plane;
         a.op.mn_b = (int)(h.V - v0);
+        a.op.k_b = (int)(p.copy_w ? p.Dp : h.D);
         a.scale = scale;
         a.lse = lse;
         a.coef = c.coef;
@@ -458,7 +462,7 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
             o.op.B = wn;
             o.op.ldb = w.ld;
             o.op.plane_b = w.plane;
-            o.op.mn_b = (int)p.Dp;
+            o.op.mn_b = (int)(p.copy_w ? p.Dp : h.D);
             o.op.k_b = (int)(h.V - v0);
             if (p.dx_direct) {
                 o.out = dX;

@@ -54,7 +54,7 @@ struct Operands {
     int steps;                 // steps of 64 along K
     int steps_per_split;       // part y of the sum takes steps [y·this, (y+1)·this)
     int mn_a, mn_b;            // KC: rows of A / B; MC: columns that may be read, a multiple of 8
-    int k_a, k_b;              // MC: rows (values of k) of A / B
+    int k_a, k_b;              // values of k of A / B; a multiple of 8 for a KC operand, of 64 for A
     int tiles_m, tiles_n, splits;
 };
 
@@ -149,8 +149,10 @@ struct Loader {
     uint32_t off[kRounds];
 
     // mn_last: the last row (KC) or the last 8-aligned column (MC) of the
-    // operand, relative to the tile; k_last: the last row of an MC operand,
-    // relative to the step.
+    // operand, relative to the tile; k_last: the last row of an MC operand or
+    // the last 8-aligned column of a KC one, relative to the step.  Past it an
+    // MC operand's last row stands in, and a KC operand's first columns of the
+    // step: they meet zeros of the other operand.
     __device__ __forceinline__ void place(int64_t ld, int mn_last, int k_last)
     {
         const int thread = thread_anew();
@@ -166,7 +168,8 @@ struct Loader {
                     const int in = row % (16 * F), b = in / 16, q = in / 4 % 4;
                     mn = row - in + 4 * F * q + 4 * b + in % 4;
                 }
-                off[r] = ((uint32_t)min(mn, mn_last) * (uint32_t)ld + (uint32_t)((slot ^ swizzle(row)) * 8)) * 2u;
+                const int k = (slot ^ swizzle(row)) * 8;
+                off[r] = ((uint32_t)min(mn, mn_last) * (uint32_t)ld + (uint32_t)(k <= k_last ? k : 0)) * 2u;
             }
         }
     }
@@ -313,8 +316,8 @@ struct TileProduct {
             const int a0 = min(m0, a_end), b0 = min(n0, b_end);
             a_last = a_end - a0;
             b_last = b_end - b0;
-            la.place(p.lda, a_last, A_MC ? p.k_a - 1 - start(first, p.k_a) : 0);
-            lb.place(p.ldb, b_last, B_MC ? p.k_b - 1 - start(first, p.k_b) : 0);
+            la.place(p.lda, a_last, A_MC ? p.k_a - 1 - start(first, p.k_a) : BK);
+            lb.place(p.ldb, b_last, B_MC ? p.k_b - 1 - start(first, p.k_b) : p.k_b - 8 - first * BK);
             A = (const char *)p.A + (A_MC ? (int64_t)a0 : (int64_t)a0 * p.lda) * 2;
             B = (const char *)p.B + (B_MC ? (int64_t)b0 : (int64_t)b0 * p.ldb) * 2;
             seg = 0;
@@ -336,9 +339,9 @@ struct TileProduct {
                 from_a += ((kPairsA >> (2 * seg)) & 3) * p.plane_a * 2;
                 from_b += ((kPairsB >> (2 * seg)) & 3) * p.plane_b * 2;
             }
-            // an MC operand may end inside its last step; the next segment has whole ones again
+            // an operand may end inside its last step; the next segment has whole ones again
             if (A_MC && ((k + 1) * BK > p.k_a || (p.segments > 1 && k == first))) la.place(p.lda, a_last, p.k_a - 1 - start_a);
-            if (B_MC && ((k + 1) * BK > p.k_b || (p.segments > 1 && k == first))) lb.place(p.ldb, b_last, p.k_b - 1 - start_b);
+            if ((k + 1) * BK > p.k_b || (B_MC && p.segments > 1 && k == first)) lb.place(p.ldb, b_last, p.k_b - (B_MC ? 1 : 8) - start_b);
             ++k;
         };
         // A round of a KC operand may be just the rows that the wavefronts'
