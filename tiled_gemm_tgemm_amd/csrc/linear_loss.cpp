@@ -119,8 +119,8 @@ Choice choose_tile(int64_t M, int64_t N, int64_t steps, bool split = false)
     static const double rate[] = {1.0, 0.83, 0.375};
     Choice best;
     double least = -1;
-    for (int i = 0; i < tile_count(); ++i) {
-        const TileShape &s = tile_shape(i);
+    for (int i = 0; i < kTileCount; ++i) {
+        const TileShape &s = kTiles[i];
         const int64_t tiles = ceil_div(M, s.bm) * ceil_div(N, s.bn);
         for (int64_t parts = 1; parts == 1 || (split && parts <= 64 && steps / parts >= 4); ++parts) {
             const int64_t on_one = ceil_div(tiles * parts, 256);
@@ -190,7 +190,7 @@ void plan_operands(Plan &p, const Head &h, bool backward)
 // False where a launch would have too many threads.
 bool fits(int64_t M, int64_t N, int tile, int64_t splits)
 {
-    const TileShape &s = tile_shape(tile);
+    const TileShape &s = kTiles[tile];
     return ceil_div(M, s.bm) * ceil_div(N, s.bn) * 512 <= kMaxThreads / splits;
 }
 
@@ -207,7 +207,7 @@ bool plan_forward(Plan &p, const Head &h, int64_t teacher_k)
     } else {
         plan_operands(p, h, false);
         p.stat_tile = choose_tile(h.T, h.V, p.Dp / kStepK * p.segments).tile;
-        p.group_columns = tile_shape(p.stat_tile).stat_columns;
+        p.group_columns = kTiles[p.stat_tile].stat_columns;
     }
     p.groups = (int)ceil_div(h.V, p.group_columns);
     p.part = p.take(h.T * p.groups * 8);
@@ -255,7 +255,7 @@ bool plan_backward(Plan &p, const Head &h)
 
 Operands operands(const Plan &p, int64_t M, int64_t N, int64_t steps, int tile)
 {
-    const TileShape &s = tile_shape(tile);
+    const TileShape &s = kTiles[tile];
     Operands o{};
     o.segments = p.segments;
     o.M = (int)M;
@@ -422,7 +422,7 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
 
         GradArgs a{};
         a.op = operands(p, h.T, cols, p.Dp / kStepK, p.grad_tile);
-        a.op.tiles_m = (int)ceil_div(p.Tp, tile_shape(p.grad_tile).bm);
+        a.op.tiles_m = (int)ceil_div(p.Tp, kTiles[p.grad_tile].bm);
         a.op.A = x.p;
         a.op.lda = x.ld;
         a.op.plane_a = x.plane;

@@ -7,8 +7,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "mfma16.h"
 #include "tgemm.h"
+#include "tile_walk.h"
 
 namespace tgemm {
 namespace loss {
@@ -19,14 +19,15 @@ constexpr int kHalfShift = 15;
 
 // ---- the products ----------------------------------------------------------
 
-// Tile configurations, by index (linear_loss_product.hip).
+// Tile configurations: index, rows and columns, wavefronts along them.
+#define TGEMM_TILES(X) X(0, 256, 256, 2, 4) X(1, 128, 128, 2, 2) X(2, 32, 128, 1, 4)
 struct TileShape {
     int bm, bn;
     int wg_per_cu;
     int stat_columns;  // columns a wavefront's partial (maximum, sum) covers
 };
-int tile_count();
-const TileShape &tile_shape(int index);
+constexpr TileShape kTiles[] = {{256, 256, 1, 64}, {128, 128, 2, 64}, {32, 128, 3, 32}};
+constexpr int kTileCount = 3;
 
 // Partial softmax statistics of s·X·Wᵀ: part[t][g] = (maximum, sum of
 // exp2(· - maximum)) of row t's columns of group g, in units of log2;

@@ -9,6 +9,7 @@
 // itself.  The rows of X come from the caches.  A float32 operand is split
 // into its bf16 planes in registers, which spares a copy of W in planes.
 #include "linear_loss.h"
+#include "mfma16.h"
 
 namespace tgemm {
 namespace loss {

@@ -2,6 +2,7 @@
 // piece of the logits' gradient, and the two gradients.  See mfma16.h for the
 // tiles.
 #include "linear_loss.h"
+#include "mfma16.h"
 
 namespace tgemm {
 namespace loss {
@@ -260,14 +261,6 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_out_kernel(OutArgs a)
     });
 }
 
-constexpr TileShape kTiles[] = {
-    {256, 256, 1, 64},
-    {128, 128, 2, 64},
-    {32, 128, 3, 32},
-};
-
-#define TGEMM_TILES(X) X(0, 256, 256, 2, 4) X(1, 128, 128, 2, 2) X(2, 32, 128, 1, 4)
-
 // As many work-groups as the GPU holds at once (a multiple of 8, so that a
 // work-group's tiles stay on its XCD).
 template <class Args>
@@ -279,9 +272,6 @@ unsigned grid_of(const Args &a, int tile)
 }
 
 }  // namespace
-
-int tile_count() { return (int)(sizeof(kTiles) / sizeof(kTiles[0])); }
-const TileShape &tile_shape(int index) { return kTiles[index]; }
 
 hipError_t launch_stats(bool half, int tile, const StatsArgs &a, hipStream_t stream)
 {

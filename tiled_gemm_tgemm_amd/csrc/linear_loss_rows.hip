@@ -3,6 +3,7 @@
 // rows' gradient factors and the sum of partial gradients.  Each touches its
 // data once and is bound by device memory (or, on few rows, by its launch).
 #include "linear_loss.h"
+#include "mfma16.h"
 
 namespace tgemm {
 namespace loss {
