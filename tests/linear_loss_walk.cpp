@@ -192,16 +192,15 @@ void check_coef(const CoefArgs &a)
     if (a.target) rows(a.target, a.T, 1, 1, 8, false, "targets");
     if (a.teacher) read_teacher(*a.teacher, a.T);
     rows(a.coef, a.T, 1, 1, 4, true, "coef");
-    if (a.half) {
-        rows(a.row_scale, a.T, 1, 1, 4, true, "row scales");
-        rows(a.exps, a.T, 1, 1, 4, true, "exponents");
-    }
+    if (a.half || a.grad_step == 0) rows(a.row_scale, a.T, 1, 1, 4, true, "row scales");
+    if (a.grad_step == 0) touch(a.all_scale, 4, true, "scale");
+    else if (a.half) rows(a.exps, a.T, 1, 1, 4, true, "exponents");
 }
 
 hipError_t launch_coef(const CoefArgs &a, hipStream_t)
 {
     check_coef(a);
-    if (a.half) rows(a.block_max, coef_blocks(a.T, a.teacher != nullptr), 1, 1, 4, true, "largest exponents");
+    if (a.half && a.grad_step != 0) rows(a.block_max, coef_blocks(a.T, a.teacher != nullptr), 1, 1, 4, true, "largest exponents");
     return hipSuccess;
 }
 
@@ -218,7 +217,7 @@ hipError_t launch_copy(const CopyArgs &a, hipStream_t)
         rows(a.exps, a.rows, 1, 1, 4, false, "exponents");
         rows(a.block_max, a.blocks, 1, 1, 4, false, "largest exponents");
     }
-    if (a.exps || (a.make && a.make->half)) touch(a.all_scale, 4, true, "scale");
+    if (a.exps) touch(a.all_scale, 4, true, "scale");
     return hipSuccess;
 }
 

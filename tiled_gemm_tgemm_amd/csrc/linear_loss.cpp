@@ -240,11 +240,11 @@ bool plan_backward(Plan &p, const Head &h)
     p.dx_splits = parts_of(ceil_div(h.V < p.piece ? h.V : p.piece, kStepK), dx.splits);
     p.dx_direct = p.pieces == 1 && p.dx_splits == 1;
     p.coef = p.take(h.T * 4);
+    p.row_scale = p.take(h.T * 4);
+    p.all_scale = p.take(4);
     if (p.half) {
-        p.row_scale = p.take(h.T * 4);
         p.exps = p.take(h.T * 4);
         p.block_max = p.take(coef_blocks(h.T, true) * 4);
-        p.all_scale = p.take(4);
     }
     p.g = p.take(p.Tp * p.ldg * 2 * p.planes);
     if (!p.dx_direct) p.dx_part = p.take(p.dx_splits * h.T * p.Dp * 4);
@@ -377,7 +377,11 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
     c.teacher = l.teacher;
     c.half = p.half;
     c.coef = in<float>(ws, p.coef);
-    c.row_scale = in<float>(ws, p.row_scale);
+    const bool scaled = p.half || grad_step == 0;
+    float *row_scale = scaled ? in<float>(ws, p.row_scale) : nullptr;
+    float *all_scale = scaled ? in<float>(ws, p.all_scale) : nullptr;
+    c.row_scale = row_scale;
+    c.all_scale = all_scale;
     c.exps = in<int>(ws, p.exps);
     c.block_max = in<int>(ws, p.block_max);
     hipError_t e = coef_in_copy(c) ? hipSuccess : launch_coef(c, stream);
@@ -387,14 +391,16 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
     // would meet a zero of the logits' gradient.
     void *xs = in<void>(ws, p.xs);
     CopyArgs clear = copy_of(p, h, h.X, h.ldx, h.T, xs, p.Tp);
-    clear.all_scale = in<float>(ws, p.all_scale);
     if (coef_in_copy(c)) {
         clear.make = &c;
     } else {
         clear.coef = c.coef;
-        clear.exps = c.exps;
-        clear.block_max = c.block_max;
-        clear.blocks = (int)coef_blocks(h.T, l.teacher != nullptr);
+        if (p.half && grad_step != 0) {
+            clear.exps = c.exps;
+            clear.block_max = c.block_max;
+            clear.blocks = (int)coef_blocks(h.T, l.teacher != nullptr);
+            clear.all_scale = all_scale;
+        }
     }
     e = launch_copy(clear, stream);
     if (e != hipSuccess) return from_hip(e);
@@ -469,7 +475,7 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
                 o.ldo = lddx;
                 o.dtype = h.dtype;
                 o.vec = rows16(dX, lddx, h.dtype);
-                o.row_scale = in<float>(ws, p.row_scale);
+                o.row_scale = row_scale;
             } else {
                 o.out = in<float>(ws, p.dx_part);
                 o.ldo = p.Dp;
@@ -500,7 +506,7 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
                 o.ldo = lddw;
                 o.dtype = h.dtype;
                 o.vec = rows16(dW, lddw, h.dtype);
-                o.all_scale = in<float>(ws, p.all_scale);
+                o.all_scale = all_scale;
             } else {
                 o.op.splits = p.dw_splits;
                 o.op.steps_per_split = (int)ceil_div(p.Tp / kStepK, p.dw_splits);
@@ -514,14 +520,14 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
             if (e != hipSuccess) return from_hip(e);
             if (p.dw_splits > 1) {
                 SumArgs s{cols, h.D, in<float>(ws, p.dw_part), p.Dp, o.split_stride, p.dw_splits, nullptr,
-                          in<float>(ws, p.all_scale), to, lddw, h.dtype, rows16(dW, lddw, h.dtype)};
+                          all_scale, to, lddw, h.dtype, rows16(dW, lddw, h.dtype)};
                 e = launch_sum(s, stream);
                 if (e != hipSuccess) return from_hip(e);
             }
         }
     }
     if (dX != nullptr && !p.dx_direct) {
-        SumArgs s{h.T, h.D, in<float>(ws, p.dx_part), p.Dp, dx_stride, p.dx_splits, in<float>(ws, p.row_scale), nullptr,
+        SumArgs s{h.T, h.D, in<float>(ws, p.dx_part), p.Dp, dx_stride, p.dx_splits, row_scale, nullptr,
                   dX, lddx, h.dtype, rows16(dX, lddx, h.dtype)};
         e = launch_sum(s, stream);
         if (e != hipSuccess) return from_hip(e);

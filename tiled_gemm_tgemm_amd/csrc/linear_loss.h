@@ -80,8 +80,7 @@ struct OutArgs {
     bool vec;                // out and its rows 16-byte aligned
     bool add;                // float32 out: add to what is there
     int64_t split_stride;    // elements between the outputs of the sum's parts
-    const float *row_scale;  // or NULL
-    const float *all_scale;  // or NULL
+    const float *row_scale, *all_scale;  // as SumArgs
 };
 hipError_t launch_dx(bool half, int tile, const OutArgs &a, hipStream_t stream);
 hipError_t launch_dw(bool half, int tile, const OutArgs &a, hipStream_t stream);
@@ -129,11 +128,17 @@ hipError_t launch_join(const JoinArgs &a, hipStream_t stream);
 // The summary of no rows.
 hipError_t launch_summary_none(float *summary, hipStream_t stream);
 
-// The factor of a row's gradient, coef[t] = grad[t·grad_step]·factor·*weight, 0 for rows that do
-// not count, NaN for rows with an index out of range; for fp16 its fraction
-// times 2^kHalfShift, with row_scale[t] = 2^(exponent - kHalfShift), exps[t]
-// the exponent, and block_max[b] the largest of a work-group's rows (256, or
-// 16 where each has a teacher's entries).
+// The factor c_t = grad[t·grad_step]·factor·*weight of a row's gradient, in two
+// parts: coef[t] multiplies the logits' gradient before it is rounded (0 for
+// rows that do not count, NaN for rows with an index out of range), the scales
+// multiply the results.
+// * One value for all rows (grad_step 0): coef is 1 (fp16: 2^kHalfShift), and
+//   row_scale[t] and all_scale[0] hold the rest, so that its rounding is not
+//   that of every element.
+// * Otherwise coef is c_t; for fp16 its fraction times 2^kHalfShift, with
+//   row_scale[t] = 2^(exponent - kHalfShift), exps[t] the exponent, and
+//   block_max[b] the largest of a work-group's rows (256, or 16 where each has
+//   a teacher's entries); launch_copy writes all_scale.
 inline int64_t coef_blocks(int64_t T, bool teacher) { return teacher ? (T + 15) / 16 : (T + 255) / 256; }
 struct CoefArgs {
     int64_t T, V;
@@ -145,13 +150,13 @@ struct CoefArgs {
     int64_t ignore;
     const Teacher *teacher;
     bool half;
-    float *coef, *row_scale;
+    float *coef, *row_scale, *all_scale;
     int *exps, *block_max;
 };
 hipError_t launch_coef(const CoefArgs &a, hipStream_t stream);
 
-// Cross entropy's factors need no pass of their own where a row's power of two
-// is known without the others': in fp16, where one value serves all rows.
+// Cross entropy's factors need no pass of their own, but for fp16 with a factor
+// a row, where the largest exponent has to be known first.
 inline bool coef_in_copy(const CoefArgs &a) { return a.teacher == nullptr && (!a.half || a.grad_step == 0); }
 
 // dst (planes of rows_out×ld_out 16-bit elements, zero past the ends) = src
@@ -187,8 +192,8 @@ struct ScatterArgs {
 };
 hipError_t launch_scatter(const ScatterArgs &a, hipStream_t stream);
 
-// out[t][d] = row_scale[t]·all_scale·(part_0 + part_1 + ...)[t][d], part_s at
-// part + s·stride; either scale may be NULL.
+// out[t][d] = scale·(part_0 + part_1 + ...)[t][d], part_s at part + s·stride,
+// the scale row_scale[t], or all_scale[0], or 1 where both are NULL.
 struct SumArgs {
     int64_t T, D;
     const float *part;

@@ -15,14 +15,6 @@ using m16::TileProduct;
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// a·b, where 0 times anything, NaN and infinity too, is 0.
-__device__ __forceinline__ float mul_zero(float a, float b)
-{
-    float r;
-    asm("v_mul_legacy_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
-    return r;
-}
-
 // A row's adjacent columns that a lane holds.
 template <class Tile>
 constexpr int kHeld = 4 * Tile::FN;
@@ -187,7 +179,7 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_grad_kernel(GradArgs a)
             // 0 times anything is 0 here: a row that does not count is zero
             // whatever its logits are
 #pragma unroll
-            for (int e = 0; e < H; ++e) g[e] = mul_zero(c, g[e]);
+            for (int e = 0; e < H; ++e) g[e] = m16::mul_zero(c, g[e]);
             E *to = (E *)a.G + (int64_t)row * a.ldg + col;
             if (a.planes == 1) {
                 store_packed<E, H>(to, g);
@@ -232,6 +224,7 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_out_kernel(OutArgs a)
     typedef TileProduct<E, BM, BN, WM, WN, A_MC, true> Tile;
     constexpr int H = kHeld<Tile>;
     __shared__ __align__(1024) char lds[Tile::kLds];
+    const bool scaled = a.row_scale != nullptr || a.all_scale != nullptr;
     const float all = a.all_scale != nullptr ? *a.all_scale : 1.0f;
     Tile::run(a.op, (lds_char *)lds, [&](typename Tile::Acc &acc, int row0, int col0, int split) {
         const int lane = m16::thread_anew() & 63, l16 = lane & 15, quarter = lane >> 4;
@@ -241,10 +234,14 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_out_kernel(OutArgs a)
         for (int i = 0; i < Tile::FM; ++i) {
             const int row = row0 + i * 16 + l16;
             if (row >= a.op.M) continue;
-            const float s = a.row_scale != nullptr ? a.row_scale[row] * all : all;
             float v[H];
 #pragma unroll
-            for (int e = 0; e < H; ++e) v[e] = acc[i][e / 4][e % 4] * s;
+            for (int e = 0; e < H; ++e) v[e] = acc[i][e / 4][e % 4];
+            if (scaled) {
+                const float s = a.row_scale != nullptr ? a.row_scale[row] : all;
+#pragma unroll
+                for (int e = 0; e < H; ++e) v[e] = m16::mul_zero(s, v[e]);
+            }
             const int64_t at = (int64_t)row * a.ldo + col + (int64_t)split * a.split_stride;
             if (a.dtype == TGEMM_F32) {
                 float *to = (float *)a.out + at;

@@ -44,36 +44,43 @@ __device__ __forceinline__ float grad_of(const CoefArgs &a, int64_t row)
     return a.weight != nullptr ? g * *a.weight : g;
 }
 
-__device__ __forceinline__ void put_coef(const CoefArgs &a, int64_t row, float c, int &exponent)
+enum RowKind { kNotCounted, kCounted, kBad };
+
+// Also returns the exponent of an fp16 row's own factor, kNoExponent where there is none.
+__device__ __forceinline__ int put_coef(const CoefArgs &a, int64_t row, RowKind kind)
 {
-    exponent = kNoExponent;
-    if (a.half) {
-        int e = 0;
-        if (c != 0.0f && !__builtin_isinf(c) && !__builtin_isnan(c)) {
-            c = ldexpf(frexpf(c, &e), kHalfShift);
-            exponent = e;
+    float coef = kind == kBad ? NAN : 0.0f;
+    int exponent = kNoExponent;
+    if (a.grad_step == 0) {
+        const float shift = a.half ? ldexpf(1.0f, kHalfShift) : 1.0f;
+        if (kind == kCounted) coef = shift;
+        a.row_scale[row] = kind == kNotCounted ? 0.0f : kind == kBad ? NAN : grad_of(a, 0) / shift;
+        if (row == 0) *a.all_scale = grad_of(a, 0) / shift;
+    } else {
+        if (kind == kCounted) coef = grad_of(a, row);
+        if (a.half) {
+            int e = 0;
+            if (coef != 0.0f && !__builtin_isinf(coef) && !__builtin_isnan(coef)) {
+                coef = ldexpf(frexpf(coef, &e), kHalfShift);
+                exponent = e;
+            }
+            a.row_scale[row] = ldexpf(1.0f, e - kHalfShift);
+            a.exps[row] = e;
         }
-        a.row_scale[row] = ldexpf(1.0f, e - kHalfShift);
-        a.exps[row] = e;
     }
-    a.coef[row] = c;
+    a.coef[row] = coef;
+    return exponent;
 }
 
-__device__ __forceinline__ float ce_factor(const CoefArgs &a, int64_t row)
+__device__ __forceinline__ RowKind ce_kind(const CoefArgs &a, int64_t row)
 {
     const int64_t y = a.target[row];
-    return y == a.ignore ? 0.0f : y < 0 || y >= a.V ? NAN : grad_of(a, row);
+    return y == a.ignore ? kNotCounted : y < 0 || y >= a.V ? kBad : kCounted;
 }
 
 __global__ __launch_bounds__(256) void linear_copy_kernel(CopyArgs a, CoefArgs make, bool making)
 {
     int top = 0;
-    if (making && make.half) {
-        // every row that counts has the same factor: its power of two is the largest
-        const float c = grad_of(make, 0);
-        if (c != 0.0f && !__builtin_isinf(c) && !__builtin_isnan(c)) frexpf(c, &top);
-        if (blockIdx.x == 0 && threadIdx.x == 0) *a.all_scale = ldexpf(1.0f, top - kHalfShift);
-    }
     if (a.exps != nullptr) {
         __shared__ int best[4];
         int m = kNoExponent;
@@ -93,10 +100,9 @@ __global__ __launch_bounds__(256) void linear_copy_kernel(CopyArgs a, CoefArgs m
         uint16_t *to = (uint16_t *)a.dst + row * a.ld_out + col;
         bool counts = left > 0;
         if (making && row < a.rows) {
-            const float c = ce_factor(make, row);
-            int exponent;
-            if (col == 0) put_coef(make, row, c, exponent);
-            counts = counts && c != 0.0f;
+            const RowKind kind = ce_kind(make, row);
+            if (col == 0) put_coef(make, row, kind);
+            counts = counts && kind != kNotCounted;
         } else if (a.coef != nullptr && row < a.rows) {
             counts = counts && a.coef[row] != 0.0f;
         }
@@ -316,7 +322,7 @@ __global__ __launch_bounds__(1024) void linear_summary_kernel(int64_t T, const f
 template <int WAVES>
 __device__ __forceinline__ void put_block_max(const CoefArgs &a, int64_t block, int exponent)
 {
-    if (!a.half) return;
+    if (!a.half || a.grad_step == 0) return;
     __shared__ int best[WAVES];
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) exponent = max(exponent, __shfl_xor(exponent, d));
@@ -333,7 +339,7 @@ __global__ __launch_bounds__(256) void linear_ce_coef_kernel(CoefArgs a)
     const int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x;
     int exponent = kNoExponent;
     if (row < a.T) {
-        put_coef(a, row, ce_factor(a, row), exponent);
+        exponent = put_coef(a, row, ce_kind(a, row));
     }
     put_block_max<4>(a, blockIdx.x, exponent);
 }
@@ -354,7 +360,7 @@ __global__ __launch_bounds__(1024) void linear_kd_coef_kernel(CoefArgs a, Teache
         }
         any = __any(any);
         bad = __any(bad);
-        if (lane == 0) put_coef(a, row, !any ? 0.0f : bad ? NAN : grad_of(a, row), exponent);
+        if (lane == 0) exponent = put_coef(a, row, !any ? kNotCounted : bad ? kBad : kCounted);
     }
     put_block_max<16>(a, blockIdx.x, exponent);
 }
@@ -414,9 +420,9 @@ __global__ __launch_bounds__(256) void linear_sum_kernel(SumArgs a)
         const float *part = a.part + row * a.ld + col;
         m16::f32x4 v = *(const m16::f32x4 *)part;
         for (int s = 1; s < a.count; ++s) v += *(const m16::f32x4 *)(part + s * a.stride);
-        float scale = a.row_scale != nullptr ? a.row_scale[row] : 1.0f;
-        if (a.all_scale != nullptr) scale *= *a.all_scale;
-        v *= scale;
+        const float scale = a.row_scale != nullptr ? a.row_scale[row] : a.all_scale != nullptr ? *a.all_scale : 1.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = m16::mul_zero(scale, v[e]);
         const int64_t at = row * a.ldo + col;
         if (a.vec && col + 4 <= a.D) {
             if (a.dtype == TGEMM_F32) {

@@ -44,6 +44,14 @@ __device__ __forceinline__ void split(float x, __bf16 &high, __bf16 &middle, __b
     low = (__bf16)(rest - (float)middle);
 }
 
+// a·b, where 0 times anything, NaN and infinity too, is 0.
+__device__ __forceinline__ float mul_zero(float a, float b)
+{
+    float r;
+    asm("v_mul_legacy_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
+}
+
 template <class E>
 struct Frag;
 template <>
