@@ -25,10 +25,15 @@ from ._lib import TgemmError
 REDUCTIONS = ("mean", "sum", "none")
 
 
-def _dtype(t):
+@functools.lru_cache(maxsize=None)
+def _types():
     import torch
 
-    return {torch.float32: _lib.TGEMM_F32, torch.bfloat16: _lib.TGEMM_BF16, torch.float16: _lib.TGEMM_F16}.get(t.dtype)
+    return {torch.float32: _lib.TGEMM_F32, torch.bfloat16: _lib.TGEMM_BF16, torch.float16: _lib.TGEMM_F16}
+
+
+def _dtype(t):
+    return _types().get(t.dtype)
 
 
 def _rows(t, name, shape=None, device=None, like=None):
@@ -44,9 +49,10 @@ def _rows(t, name, shape=None, device=None, like=None):
     if shape is not None and tuple(t.shape) != shape:
         raise ValueError(f"{name} must be {shape[0]}x{shape[1]}")
     rows, cols = t.shape
-    if cols > 1 and rows > 0 and t.stride(1) != 1 or rows > 1 and t.stride(0) < cols:
+    down, across = t.stride()
+    if cols > 1 and rows > 0 and across != 1 or rows > 1 and down < cols:
         raise ValueError(f"{name} must be row-major")
-    return max(t.stride(0), cols, 1) if rows > 1 else max(cols, 1)
+    return max(down, cols, 1) if rows > 1 else max(cols, 1)
 
 
 def _ids(t, name, shape, device):
@@ -85,15 +91,17 @@ class _Call:
         self.T, self.D = X.shape
         self.V = W.shape[0]
         self.head = (_dtype(X), self.T, self.V, self.D, X.data_ptr(), ldx, W.data_ptr(), ldw)
-        self.stream = torch.cuda.current_stream(X.device).cuda_stream if stream is None else stream
+        self.stream, self.elsewhere = stream, stream is not None
+        if stream is None:
+            self.stream = torch.cuda.current_stream(X.device).cuda_stream
         self.made = []
 
     def again(self, X, W):
-        """This call for the backward pass: the same tensors (checked before), wherever they are now."""
+        """This call for the backward pass: the same tensors, wherever and however they are stored by now."""
         import torch
 
         c = copy.copy(self)
-        c.head = (*self.head[:4], X.data_ptr(), self.head[5], W.data_ptr(), self.head[7])
+        c.head = (*self.head[:4], X.data_ptr(), _rows(X, "X"), W.data_ptr(), _rows(W, "W"))
         c.stream = torch.cuda.current_stream(self.device).cuda_stream
         return c
 
@@ -142,30 +150,32 @@ class _Call:
     def queue(self, entry, *args):
         import torch
 
-        from . import _hold_for_stream
+        if self.elsewhere:
+            from . import _hold_for_stream
 
-        _hold_for_stream(self.stream, self.device, *self.made)
+            _hold_for_stream(self.stream, self.device, *self.made)
         self.made = []  # the call may be kept for the backward pass, its workspace not
+        entry_point = getattr(_lib.library(), entry)
         if torch.cuda.current_device() == self.device.index:
-            st = getattr(_lib, entry)(*self.head, *args, self.stream)
+            st = entry_point(*self.head, *args, self.stream)
         else:
             with torch.cuda.device(self.device):
-                st = getattr(_lib, entry)(*self.head, *args, self.stream)
+                st = entry_point(*self.head, *args, self.stream)
         if st != _lib.TGEMM_SUCCESS:
             raise TgemmError(st, entry)
+
+    def rows_and_summary(self):
+        """Room for what a differentiable forward pass keeps, in one tensor: the summary (3 floats, the fourth is
+        free), lse and loss; and the addresses of loss, lse and summary."""
+        import torch
+
+        kept = torch.empty(4 + 2 * self.T, dtype=torch.float32, device=self.device)
+        at = kept.data_ptr()
+        return kept, (at + 16 + 4 * self.T, at + 16, at)
 
 
 def _ptr(t):
     return 0 if t is None else t.data_ptr()
-
-
-def _ce_forward(c, target, ignore_index, loss, lse, summary, workspace):
-    """(loss, lse, summary or None); target checked."""
-    loss, lse = c.floats(loss, "loss", (c.T,)), c.floats(lse, "lse", (c.T,))
-    summary = c.floats(None, "summary", (3,)) if summary else None
-    c.queue("tgemm_linear_ce_forward", target.data_ptr(), int(ignore_index), loss.data_ptr(), lse.data_ptr(),
-            _ptr(summary), *c.room(workspace, 0, 0))
-    return loss, lse, summary
 
 
 def linear_cross_entropy_forward(X, W, target, *, ignore_index=-100, loss=None, lse=None, workspace=None, stream=None):
@@ -174,7 +184,11 @@ def linear_cross_entropy_forward(X, W, target, *, ignore_index=-100, loss=None, 
     and lse: float32 tensors of T to write to; workspace: a CUDA uint8 tensor of at least
     tgemm_linear_loss_workspace_size bytes (allocated if omitted; two calls in flight at once need two)."""
     c = _Call(X, W, stream)
-    return _ce_forward(c, _ids(target, "target", (c.T,), c.device), ignore_index, loss, lse, False, workspace)[:2]
+    target = _ids(target, "target", (c.T,), c.device)
+    loss, lse = c.floats(loss, "loss", (c.T,)), c.floats(lse, "lse", (c.T,))
+    c.queue("tgemm_linear_ce_forward", target.data_ptr(), int(ignore_index), loss.data_ptr(), lse.data_ptr(), 0,
+            *c.room(workspace, 0, 0))
+    return loss, lse
 
 
 def _gradients(c, dX, dW, need):
@@ -195,10 +209,10 @@ def _grad_loss(c, grad):
 
 
 def _ce_backward(c, grad_loss, weight, target, lse, ignore_index, dX, dW, need, workspace):
-    """target and lse checked"""
+    """target checked; weight and lse: addresses"""
     dX, dW, outs = _gradients(c, dX, dW, need)
-    c.queue("tgemm_linear_ce_backward", target.data_ptr(), int(ignore_index), lse.data_ptr(), *_grad_loss(c, grad_loss),
-            _ptr(weight), *outs, *c.room(workspace, 0, 1))
+    c.queue("tgemm_linear_ce_backward", target.data_ptr(), int(ignore_index), lse, *_grad_loss(c, grad_loss), weight, *outs,
+            *c.room(workspace, 0, 1))
     return dX, dW
 
 
@@ -209,18 +223,8 @@ def linear_cross_entropy_backward(grad_loss, X, W, target, lse, *, ignore_index=
     tensors to write to; need: which of the two are computed (None is returned for the other)."""
     c = _Call(X, W, stream)
     target = _ids(target, "target", (c.T,), c.device)
-    return _ce_backward(c, grad_loss, None, target, _floats(lse, "lse", (c.T,), c.device), ignore_index, dX, dW, need,
-                        workspace)
-
-
-def _kd_forward(c, teacher, loss, lse, student, summary, workspace):
-    """(loss, lse, student, summary or None); teacher as _Call.teacher gave it"""
-    loss, lse = c.floats(loss, "loss", (c.T,)), c.floats(lse, "lse", (c.T,))
-    student = c.floats(student, "student", (c.T, c.K))
-    summary = c.floats(None, "summary", (3,)) if summary else None
-    c.queue("tgemm_linear_kd_forward", *teacher, loss.data_ptr(), lse.data_ptr(), student.data_ptr(), _ptr(summary),
-            *c.room(workspace, c.K, 0))
-    return loss, lse, student, summary
+    lse = _floats(lse, "lse", (c.T,), c.device)
+    return _ce_backward(c, grad_loss, 0, target, lse.data_ptr(), ignore_index, dX, dW, need, workspace)
 
 
 def linear_distillation_forward(X, W, teacher_ids, teacher_logits, *, temperature=1.0, loss=None, lse=None,
@@ -232,14 +236,18 @@ def linear_distillation_forward(X, W, teacher_ids, teacher_logits, *, temperatur
     where an entry's id is outside the vocabulary.  student: z at the teacher's ids (0 where absent)."""
     c = _Call(X, W, stream)
     teacher = c.teacher(teacher_ids, teacher_logits, temperature)
-    return _kd_forward(c, teacher, loss, lse, student, False, workspace)[:3]
+    loss, lse = c.floats(loss, "loss", (c.T,)), c.floats(lse, "lse", (c.T,))
+    student = c.floats(student, "student", (c.T, c.K))
+    c.queue("tgemm_linear_kd_forward", *teacher, loss.data_ptr(), lse.data_ptr(), student.data_ptr(), 0,
+            *c.room(workspace, c.K, 0))
+    return loss, lse, student
 
 
 def _kd_backward(c, grad_loss, weight, teacher, lse, student, dX, dW, need, workspace):
-    """teacher as _Call.teacher gave it; lse and student checked"""
+    """teacher as _Call.teacher gave it; weight, lse and student: addresses"""
     dX, dW, outs = _gradients(c, dX, dW, need)
-    c.queue("tgemm_linear_kd_backward", *teacher, lse.data_ptr(), student.data_ptr(), *_grad_loss(c, grad_loss),
-            _ptr(weight), *outs, *c.room(workspace, c.K, 1))
+    c.queue("tgemm_linear_kd_backward", *teacher, lse, student, *_grad_loss(c, grad_loss), weight, *outs,
+            *c.room(workspace, c.K, 1))
     return dX, dW
 
 
@@ -251,7 +259,7 @@ def linear_distillation_backward(grad_loss, X, W, teacher_ids, teacher_logits, l
     teacher = c.teacher(teacher_ids, teacher_logits, temperature)
     lse = _floats(lse, "lse", (c.T,), c.device)
     student = _floats(student, "student", (c.T, c.K), c.device)
-    return _kd_backward(c, grad_loss, None, teacher, lse, student, dX, dW, need, workspace)
+    return _kd_backward(c, grad_loss, 0, teacher, lse.data_ptr(), student.data_ptr(), dX, dW, need, workspace)
 
 
 @functools.lru_cache(maxsize=None)
@@ -260,26 +268,34 @@ def _functions():
     import torch
     from torch.autograd.function import once_differentiable
 
-    def reduced(reduction, loss, summary):
-        # a copy of one element: an output that is a view could not be changed in place by the caller
-        return loss if reduction == "none" else summary[0 if reduction == "sum" else 1].clone()
+    def result(c, reduction, kept):
+        # tensors of their own on `kept`, not views of it: a caller may change them in place
+        place, shape = {"mean": (1, ()), "sum": (0, ()), "none": (4 + c.T, (c.T,))}[reduction]
+        return torch.empty(0, dtype=torch.float32, device=c.device).set_(kept.untyped_storage(), place, shape)
+
+    def addresses(reduction, kept):
+        """The mean's weight, or none, and lse."""
+        at = kept.data_ptr()
+        return at + 8 if reduction == "mean" else 0, at + 16
 
     class CrossEntropy(torch.autograd.Function):
         @staticmethod
         def forward(ctx, X, W, target, ignore_index, reduction):
             c = _Call(X, W, None)
             target = _ids(target, "target", (c.T,), c.device)
-            loss, lse, summary = _ce_forward(c, target, ignore_index, None, None, reduction != "none", None)
-            ctx.save_for_backward(X, W, target, lse, summary if reduction == "mean" else None)
-            ctx.call, ctx.ignore_index = c, ignore_index
-            return reduced(reduction, loss, summary)
+            kept, at = c.rows_and_summary()
+            c.queue("tgemm_linear_ce_forward", target.data_ptr(), int(ignore_index), *at, *c.room(None, 0, 0))
+            ctx.save_for_backward(X, W, target, kept)
+            ctx.call, ctx.ignore_index, ctx.reduction = c, ignore_index, reduction
+            return result(c, reduction, kept)
 
         @staticmethod
         @once_differentiable
         def backward(ctx, grad):
-            X, W, target, lse, summary = ctx.saved_tensors
-            dX, dW = _ce_backward(ctx.call.again(X, W), grad, None if summary is None else summary[2:], target, lse,
-                                  ctx.ignore_index, None, None, ctx.needs_input_grad, None)
+            X, W, target, kept = ctx.saved_tensors
+            weight, lse = addresses(ctx.reduction, kept)
+            dX, dW = _ce_backward(ctx.call.again(X, W), grad, weight, target, lse, ctx.ignore_index, None, None,
+                                  ctx.needs_input_grad, None)
             return dX, dW, None, None, None
 
     class Distillation(torch.autograd.Function):
@@ -287,20 +303,21 @@ def _functions():
         def forward(ctx, X, W, teacher_ids, teacher_logits, temperature, reduction):
             c = _Call(X, W, None)
             teacher = c.teacher(teacher_ids, teacher_logits, temperature)
-            loss, lse, student, summary = _kd_forward(c, teacher, None, None, None, reduction != "none", None)
-            ctx.save_for_backward(X, W, teacher_ids, teacher_logits, lse, student,
-                                  summary if reduction == "mean" else None)
-            ctx.call, ctx.temperature = c, temperature
-            return reduced(reduction, loss, summary)
+            kept, at = c.rows_and_summary()
+            student = torch.empty((c.T, c.K), dtype=torch.float32, device=c.device)
+            c.queue("tgemm_linear_kd_forward", *teacher, *at[:2], student.data_ptr(), at[2], *c.room(None, c.K, 0))
+            ctx.save_for_backward(X, W, teacher_ids, teacher_logits, kept, student)
+            ctx.call, ctx.temperature, ctx.reduction = c, temperature, reduction
+            return result(c, reduction, kept)
 
         @staticmethod
         @once_differentiable
         def backward(ctx, grad):
-            X, W, ids, logits, lse, student, summary = ctx.saved_tensors
+            X, W, ids, logits, kept, student = ctx.saved_tensors
             c = ctx.call.again(X, W)
-            dX, dW = _kd_backward(c, grad, None if summary is None else summary[2:],
-                                  c.teacher(ids, logits, ctx.temperature), lse, student, None, None,
-                                  ctx.needs_input_grad, None)
+            weight, lse = addresses(ctx.reduction, kept)
+            dX, dW = _kd_backward(c, grad, weight, c.teacher(ids, logits, ctx.temperature), lse, student.data_ptr(), None,
+                                  None, ctx.needs_input_grad, None)
             return dX, dW, None, None, None, None
 
     return CrossEntropy, Distillation
