@@ -399,6 +399,95 @@ def test_on_another_stream():
     assert torch.equal(got[0], want[0])
 
 
+@pytest.mark.parametrize("kind,teacher", [("bf16", "fp32"), ("fp32", "bf16"), ("fp16", "fp32"), ("bf16", "fp16")])
+def test_a_teacher_of_another_type(kind, teacher):
+    T, V, D, K = 70, 900, 128, 17
+    X, W, g = head(T, V, D, TYPES[kind], 17)
+    ids, logits = entries(T, V, 2 * K, TYPES[teacher], g)
+    ids, logits = ids[:, :K], logits[:, 3:K + 3]  # rows apart
+    logits[(ids < 0) | (ids >= V)] = float("-inf")
+    grad = row_grads(T, g)
+    loss, lse, student = tg.linear_distillation_forward(X, W, ids, logits, temperature=2.5)
+    dX, dW = tg.linear_distillation_backward(grad, X, W, ids, logits, lse, student, temperature=2.5)
+    torch.cuda.synchronize()
+    ref = Reference(X, W, ids=ids, logits=logits, temperature=2.5)
+    ref.check_rows(loss, lse, student)
+    ref.check_gradients(grad.double(), dX, dW)
+
+
+@pytest.mark.parametrize("kind", TYPES)
+def test_strided_targets_and_factors(kind):
+    """A target and factors that are every second element of others, on another stream."""
+    T, V, D = 90, 500, 64
+    X, W, g = head(T, V, D, TYPES[kind], 18)
+    y2, grad2 = targets(2 * T, V, g), row_grads(2 * T, g)
+    y, grad = y2[::2], grad2[::2]
+    want = tg.linear_cross_entropy_forward(X, W, y.clone())
+    want += tg.linear_cross_entropy_backward(grad.clone(), X, W, y.clone(), want[1])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    loss, lse = tg.linear_cross_entropy_forward(X, W, y, stream=side.cuda_stream)
+    got = (loss, lse, *tg.linear_cross_entropy_backward(grad, X, W, y, lse, stream=side.cuda_stream))
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_two_streams_at_once():
+    T, V, D = 300, 4000, 256
+    X, W, g = head(T, V, D, torch.bfloat16, 19)
+    y = [targets(T, V, g) for _ in range(2)]
+    grad = row_grads(T, g)
+    want = []
+    for t in y:
+        loss, lse = tg.linear_cross_entropy_forward(X, W, t)
+        want.append((loss, lse, *tg.linear_cross_entropy_backward(grad, X, W, t, lse)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                loss, lse = tg.linear_cross_entropy_forward(X, W, y[i])
+                got[i].append((loss, lse, *tg.linear_cross_entropy_backward(grad, X, W, y[i], lse)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+def test_saved_tensors_may_be_stored_elsewhere(kind):
+    """torch's hooks on what the backward pass keeps: rows that were apart come back together."""
+    T, V, D = 40, 300, 64
+    X, W, g = head(T, V, D, TYPES[kind], 20, pad=16)
+    y = targets(T, V, g)
+    X.requires_grad_()
+    W.requires_grad_()
+    want = torch.autograd.grad(tg.linear_cross_entropy(X, W, y), (X, W))
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: t.cpu(), lambda t: t.cuda()):
+        loss = tg.linear_cross_entropy(X, W, y)
+    loss_before = float(loss.detach())
+    got = torch.autograd.grad(loss, (X, W), retain_graph=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    again = torch.autograd.grad(loss, (X, W))
+    assert all(torch.equal(a, b) for a, b in zip(again, want)) and float(loss.detach()) == loss_before
+
+
+def test_a_loss_may_be_changed_in_place():
+    T, V, D = 40, 300, 64
+    X, W, g = head(T, V, D, torch.bfloat16, 21)
+    y = targets(T, V, g)
+    X.requires_grad_()
+    W.requires_grad_()
+    for reduction in ("mean", "sum", "none"):
+        loss = tg.linear_cross_entropy(X, W, y, reduction=reduction)
+        half = tg.linear_cross_entropy(X, W, y, reduction=reduction) * 0.5
+        loss *= 0.5
+        a = torch.autograd.grad(loss.sum(), (X, W))
+        b = torch.autograd.grad(half.sum(), (X, W))
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
 def test_trained_together():
     """A student's steps on both losses with one weight: the gradients of their sum, accumulated over two parts of a
     batch, against the formulas."""

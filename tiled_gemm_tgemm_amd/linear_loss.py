@@ -62,7 +62,7 @@ def _ids(t, name, shape, device):
         raise TypeError(f"{name} must be an int64 torch tensor of {'x'.join(map(str, shape))}")
     if t.device != device:
         raise TypeError(f"{name} must live on {device}")
-    return t.contiguous() if t.dim() == 1 else t
+    return t
 
 
 def _floats(t, name, shape, device):
@@ -117,6 +117,13 @@ class _Call:
         ld = _rows(logits, "teacher_logits", (self.T, self.K), self.device)
         ld_ids = max(ids.stride(0), self.K) if self.T > 1 else self.K
         return (self.K, ids.data_ptr(), ld_ids, _dtype(logits), logits.data_ptr(), ld, float(temperature))
+
+    def target(self, t):
+        t = _ids(t, "target", (self.T,), self.device)
+        if not t.is_contiguous():
+            t = t.contiguous()
+            self.made.append(t)
+        return t
 
     def new(self, shape, dtype):
         import torch
@@ -184,7 +191,7 @@ def linear_cross_entropy_forward(X, W, target, *, ignore_index=-100, loss=None, 
     and lse: float32 tensors of T to write to; workspace: a CUDA uint8 tensor of at least
     tgemm_linear_loss_workspace_size bytes (allocated if omitted; two calls in flight at once need two)."""
     c = _Call(X, W, stream)
-    target = _ids(target, "target", (c.T,), c.device)
+    target = c.target(target)
     loss, lse = c.floats(loss, "loss", (c.T,)), c.floats(lse, "lse", (c.T,))
     c.queue("tgemm_linear_ce_forward", target.data_ptr(), int(ignore_index), loss.data_ptr(), lse.data_ptr(), 0,
             *c.room(workspace, 0, 0))
@@ -222,7 +229,7 @@ def linear_cross_entropy_backward(grad_loss, X, W, target, lse, *, ignore_index=
     value a row or one of no dimension for all; lse as linear_cross_entropy_forward gave it.  dX, dW: row-major
     tensors to write to; need: which of the two are computed (None is returned for the other)."""
     c = _Call(X, W, stream)
-    target = _ids(target, "target", (c.T,), c.device)
+    target = c.target(target)
     lse = _floats(lse, "lse", (c.T,), c.device)
     return _ce_backward(c, grad_loss, 0, target, lse.data_ptr(), ignore_index, dX, dW, need, workspace)
 
@@ -282,7 +289,7 @@ def _functions():
         @staticmethod
         def forward(ctx, X, W, target, ignore_index, reduction):
             c = _Call(X, W, None)
-            target = _ids(target, "target", (c.T,), c.device)
+            target = c.target(target)
             kept, at = c.rows_and_summary()
             c.queue("tgemm_linear_ce_forward", target.data_ptr(), int(ignore_index), *at, *c.room(None, 0, 0))
             ctx.save_for_backward(X, W, target, kept)
