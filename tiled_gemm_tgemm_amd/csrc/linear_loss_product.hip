@@ -29,7 +29,30 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_stats_kernel(StatsArgs a)
     constexpr int H = kHeld<Tile>;
     __shared__ __align__(1024) char lds[Tile::kLds];
     const float scale2 = a.scale * kLog2e;
-    Tile::run(a.op, (lds_char *)lds, [&](typename Tile::Acc &acc, int row0, int col0, int) {
+    // a row's target, as this lane's column (negative: another's), or where its
+    // entries in this column group start (low half) and end
+    struct Ahead {
+        int what[Tile::FM];
+    };
+    auto prologue = [&](int row0, int col0) {
+        const int lane = m16::thread_anew() & 63, l16 = lane & 15, quarter = lane >> 4;
+        Ahead ahead;
+        const int group = col0 / (Tile::FN * 16);
+#pragma unroll
+        for (int i = 0; i < Tile::FM; ++i) {
+            const int64_t row = min(row0 + i * 16 + l16, a.op.M - 1);
+            ahead.what[i] = 0;
+            if (a.target != nullptr) {
+                const int64_t y = a.target[row];
+                ahead.what[i] = y >= 0 && y < a.op.N ? (int)y - (col0 + H * quarter) : -1;
+            } else if (group < a.groups) {
+                const uint16_t *from = a.starts + row * (a.groups + 1) + group;
+                ahead.what[i] = from[0] | (int)from[1] << 16;
+            }
+        }
+        return ahead;
+    };
+    Tile::run(a.op, (lds_char *)lds, prologue, [&](typename Tile::Acc &acc, int row0, int col0, int, const Ahead &ahead) {
         const int lane = m16::thread_anew() & 63, l16 = lane & 15, quarter = lane >> 4;
         const int left = a.op.N - (col0 + H * quarter);  // this lane's columns that exist
         if (a.op.N - col0 < Tile::FN * 16) {
@@ -39,43 +62,32 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_stats_kernel(StatsArgs a)
                 for (int e = 0; e < H; ++e)
                     if (e >= left) acc[i][e / 4][e % 4] = -INFINITY;
         }
+        const int group = col0 / (Tile::FN * 16);
         if (a.target != nullptr) {
 #pragma unroll
             for (int i = 0; i < Tile::FM; ++i) {
-                const int row = row0 + i * 16 + l16;
-                if (row >= a.op.M) continue;
-                const int64_t want = a.target[row] - (col0 + H * quarter);
-                if (want < 0 || want >= min(left, H)) continue;
+                const int row = row0 + i * 16 + l16, want = ahead.what[i];
+                if (row >= a.op.M || want < 0 || want >= H) continue;
                 float z = 0.0f;
 #pragma unroll
                 for (int e = 0; e < H; ++e) z = want == e ? acc[i][e / 4][e % 4] : z;
                 a.picked[row] = z * a.scale;
             }
-        }
-        const int group = col0 / (Tile::FN * 16);
-        if (a.starts != nullptr && group < a.groups) {
-            // a row's first entry here, for all rows at once: most have one or none
-            int at[Tile::FM], n[Tile::FM];
+        } else if (group < a.groups) {
+            // the first entry of every row at once: most have one or none
             uint32_t entry[Tile::FM];
 #pragma unroll
             for (int i = 0; i < Tile::FM; ++i) {
-                const int64_t row = min(row0 + i * 16 + l16, a.op.M - 1);
-                const uint16_t *from = a.starts + row * (a.groups + 1) + group;
-                at[i] = from[0];
-                n[i] = from[1];
-            }
-#pragma unroll
-            for (int i = 0; i < Tile::FM; ++i) {
-                const int row = row0 + i * 16 + l16;
-                n[i] = row < a.op.M ? n[i] - at[i] : 0;
+                const int row = row0 + i * 16 + l16, from = ahead.what[i] & 0xFFFF, to = ahead.what[i] >> 16;
                 entry[i] = 0;
-                if (n[i] > 0) entry[i] = a.list[(int64_t)row * a.K + at[i]];
+                if (row < a.op.M && from < to) entry[i] = a.list[(int64_t)row * a.K + from];
             }
 #pragma unroll
             for (int i = 0; i < Tile::FM; ++i) {
-                const int64_t base = (int64_t)(row0 + i * 16 + l16) * a.K;
-                for (int c = 0; c < n[i]; ++c) {
-                    const uint32_t what = c == 0 ? entry[i] : a.list[base + at[i] + c];
+                const int row = row0 + i * 16 + l16, from = ahead.what[i] & 0xFFFF, to = row < a.op.M ? ahead.what[i] >> 16 : 0;
+                const int64_t base = (int64_t)row * a.K;
+                for (int c = from; c < to; ++c) {
+                    const uint32_t what = c == from ? entry[i] : a.list[base + c];
                     const int e = (int)(what & 255) - H * quarter;
                     if (e < 0 || e >= H) continue;
                     float z = 0.0f;
@@ -146,7 +158,29 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_grad_kernel(GradArgs a)
     typedef TileProduct<E, BM, BN, WM, WN, false, false> Tile;
     constexpr int H = kHeld<Tile>;
     __shared__ __align__(1024) char lds[Tile::kLds];
-    Tile::run(a.op, (lds_char *)lds, [&](typename Tile::Acc &acc, int row0, int col0, int) {
+    // a row's factor, its logarithm of the sum, and its target as this lane's
+    // column (negative: another's)
+    struct Ahead {
+        float coef[Tile::FM], lse[Tile::FM];
+        int want[Tile::FM];
+    };
+    auto prologue = [&](int row0, int col0) {
+        const int lane = m16::thread_anew() & 63, l16 = lane & 15, quarter = lane >> 4;
+        Ahead ahead;
+#pragma unroll
+        for (int i = 0; i < Tile::FM; ++i) {
+            const int row = min(row0 + i * 16 + l16, a.op.M - 1);
+            ahead.coef[i] = a.coef[row];
+            ahead.lse[i] = a.lse[row];
+            ahead.want[i] = -1;
+            if (a.target != nullptr) {
+                const int64_t y = a.target[row] - a.v0;
+                if (y >= 0 && y < a.op.N) ahead.want[i] = (int)y - (col0 + H * quarter);
+            }
+        }
+        return ahead;
+    };
+    Tile::run(a.op, (lds_char *)lds, prologue, [&](typename Tile::Acc &acc, int row0, int col0, int, const Ahead &ahead) {
         const int lane = m16::thread_anew() & 63, l16 = lane & 15, quarter = lane >> 4;
         const int col = col0 + H * quarter;
         if (col >= a.ldg) return;
@@ -155,9 +189,9 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_grad_kernel(GradArgs a)
             const int row = row0 + i * 16 + l16;
             if (row >= a.rows) continue;
             const bool real = row < a.op.M;
-            const float c = real ? a.coef[row] : 0.0f;
-            const float lse = !real ? 0.0f : c == c ? a.lse[row] : c;
-            const int64_t want = real && a.target != nullptr ? a.target[row] - a.v0 - col : -1;
+            const float c = real ? ahead.coef[i] : 0.0f;
+            const float lse = !real ? 0.0f : c == c ? ahead.lse[i] : c;
+            const int want = ahead.want[i];
             float g[H];
             // in 16 bits the exponent's argument may be rounded once more
             if (a.planes == 1) {
@@ -226,7 +260,9 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_out_kernel(OutArgs a)
     __shared__ __align__(1024) char lds[Tile::kLds];
     const bool scaled = a.row_scale != nullptr || a.all_scale != nullptr;
     const float all = a.all_scale != nullptr ? *a.all_scale : 1.0f;
-    Tile::run(a.op, (lds_char *)lds, [&](typename Tile::Acc &acc, int row0, int col0, int split) {
+    struct Ahead {};
+    Tile::run(a.op, (lds_char *)lds, [](int, int) { return Ahead{}; },
+              [&](typename Tile::Acc &acc, int row0, int col0, int split, Ahead) {
         const int lane = m16::thread_anew() & 63, l16 = lane & 15, quarter = lane >> 4;
         const int col = col0 + H * quarter, left = a.op.N - col;
         if (left <= 0) return;

@@ -183,10 +183,12 @@ __device__ __forceinline__ void spread()
 }
 
 // The tiles of C that a work-group computes: blockIdx.x, blockIdx.x +
-// gridDim.x, ...  For each, `epilogue(acc, row0, col0, split)` is called when
-// the lane holds in acc[i][j][r] row row0 + 16·i + lane % 16, column col0 +
+// gridDim.x, ...  For each, `epilogue(acc, row0, col0, split, ahead)` is called
+// when the lane holds in acc[i][j][r] row row0 + 16·i + lane % 16, column col0 +
 // 4·FN·(lane / 16) + 4·j + r.  The loads run two steps ahead without regard to
-// where a tile ends, so the next tile's are under way by then.
+// where a tile ends, so the next tile's are under way by then; as loads come
+// back in order, the epilogue would wait for those with its own.  What it needs
+// for its rows is what `prologue(row0, col0)` returned before the products.
 template <class E, int BM, int BN, int WM, int WN, bool A_MC, bool B_MC>
 struct TileProduct {
     static constexpr int kThreads = 64 * WM * WN;
@@ -196,8 +198,8 @@ struct TileProduct {
     static constexpr int kLds = 2 * kStage;
     typedef f32x4 Acc[FM][FN];
 
-    template <class Epilogue>
-    static __device__ __forceinline__ void run(const Operands &p, lds_char *lds, Epilogue epilogue)
+    template <class Prologue, class Epilogue>
+    static __device__ __forceinline__ void run(const Operands &p, lds_char *lds, Prologue prologue, Epilogue epilogue)
     {
         const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
         const int wm = wave / WN, wn = wave % WN;
@@ -273,6 +275,8 @@ struct TileProduct {
                     for (int r = 0; r < 4; ++r) acc[i][j][r] = 0.0f;
             int m0, n0, split, from, to;
             tile_at<BM, BN>(p, id, m0, n0, split, from, to);
+            const int row0 = m0 + wm * (FM * 16), col0 = n0 + wn * (FN * 16);
+            const auto ahead = prologue(row0, col0);
             for (int n = (to - from) * p.segments; n > 0; --n) {
                 // A step on the slices of `stage`, its first fragments read.
                 // The first barrier stands after the phases that read B and
@@ -309,7 +313,7 @@ struct TileProduct {
                 }
                 stage ^= 1;
             }
-            epilogue(acc, m0 + wm * (FM * 16), n0 + wn * (FN * 16), split);
+            epilogue(acc, row0, col0, split, ahead);
         }
         __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no load into LDS outlives the work-group
     }
