@@ -98,7 +98,7 @@ struct Teacher {
     float scale;  // 1 / temperature
 };
 
-// Sorts each row's entries by column for launch_stats, and sets student to 0
+// Sorts each row's entries by column group for launch_stats, and sets student to 0
 // where an entry is absent and NaN where its id is out of range.
 struct SortArgs {
     int64_t T, V;
