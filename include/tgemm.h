@@ -365,7 +365,8 @@ int64_t tgemm_sgemm_host_workspace_size(int64_t M, int64_t N, int64_t K, int64_t
  *             largest are summed in float32; an infinity there, or a value
  *             above 3.39e38, gives NaN or infinity.  Row statistics, losses and the sums over pieces are
  *             float32.  The logits' gradient is rounded to the operands' type
- *             (float32: to three planes) before the two gradient products.
+ *             (float32: to three planes; up to 128 rows: to two numbers of the
+ *             type that add up to it) before the two gradient products.
  * Sizes       0 <= T < 2^24, 1 <= V <= 2^24, 1 <= D <= 2^22, 1 <= K <= 1024,
  *             leading dimensions up to 2^40; larger ones, and an unknown
  *             dtype: TGEMM_ERROR_NOT_SUPPORTED.  T = 0: nothing but `summary`

@@ -27,6 +27,16 @@ constexpr int64_t kMaxThreads = ((int64_t)1 << 32) - 1;
 constexpr int64_t kPieceBytes = (int64_t)256 << 20;
 constexpr int64_t kMinPiece = 2048, kMaxPiece = (int64_t)1 << 22;
 
+// Up to this many rows the logits' gradient is held as two 16-bit planes.  One
+// plane's roundings are as large as those of the results, so the two together
+// are sqrt(2) times the latter, which a sum over many rows' entries comes close
+// to; a few rows' gradients hang on a few entries, whose rounding may be the
+// largest there is (3 rows of distillation 1.8 times the results' own rounding,
+// 128 rows 1.47).  A second plane takes little time while W's way from memory
+// is what takes it (distillation backward at 32000×2048 with 8, 33 and 128
+// rows 115 -> 113, 114 -> 122 and 138 -> 159 µs; 512 rows would be 244 -> 350).
+constexpr int64_t kTwoPlaneRows = 128;
+
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t size_of(tgemm_dtype_t t) { return t == TGEMM_F32 ? 4 : 2; }
@@ -148,7 +158,10 @@ int parts_of(int64_t steps, int64_t most) { return (int)ceil_div(steps, ceil_div
 // Where a call's buffers lie in its workspace.
 struct Plan {
     bool half = false;
-    int planes = 1, segments = 1;
+    int planes = 1, segments = 1;      // of X and W, and of their product
+    int g_planes = 1;                  // of the logits' gradient
+    int dw_segments = 1;
+    int64_t dx_rows = 0;
     int64_t Tp = 0, Dp = 0;
     bool copy_x = false, copy_w = false;
     int64_t total = 0;
@@ -224,21 +237,25 @@ bool plan_forward(Plan &p, const Head &h, int64_t teacher_k)
 bool plan_backward(Plan &p, const Head &h)
 {
     plan_operands(p, h, true);
-    int64_t cols = kPieceBytes / (p.Tp * 2 * p.planes) / 256 * 256;
+    p.g_planes = h.dtype == TGEMM_F32 ? 3 : h.T <= kTwoPlaneRows ? 2 : 1;
+    // dW meets both of two planes one after the other; dX has them as rows, so
+    // that W is read once, and adds the two rows' sums up with the parts'
+    p.dw_segments = h.dtype == TGEMM_F32 ? 6 : p.g_planes;
+    p.dx_rows = p.g_planes == 2 ? 2 * p.Tp : h.T;
+    int64_t cols = kPieceBytes / (p.Tp * 2 * p.g_planes) / 256 * 256;
     cols = cols < kMinPiece ? kMinPiece : cols > kMaxPiece ? kMaxPiece : cols;
     p.pieces = ceil_div(h.V, cols);
     p.piece = round_up(ceil_div(h.V, p.pieces), 256);
     p.pieces = ceil_div(h.V, p.piece);
     p.ldg = p.piece + 128;
-    const int64_t seg = p.segments;
-    p.grad_tile = choose_tile(p.Tp, p.piece, p.Dp / kStepK * seg).tile;
-    const Choice dw = choose_tile(p.piece, h.D, p.Tp / kStepK * seg, true);
+    p.grad_tile = choose_tile(p.Tp, p.piece, p.Dp / kStepK * p.segments).tile;
+    const Choice dw = choose_tile(p.piece, h.D, p.Tp / kStepK * p.dw_segments, true);
     p.dw_tile = dw.tile;
     p.dw_splits = parts_of(p.Tp / kStepK, dw.splits);
-    const Choice dx = choose_tile(h.T, h.D, p.piece / kStepK * seg, true);
+    const Choice dx = choose_tile(p.dx_rows, h.D, p.piece / kStepK * p.segments, true);
     p.dx_tile = dx.tile;
     p.dx_splits = parts_of(ceil_div(h.V < p.piece ? h.V : p.piece, kStepK), dx.splits);
-    p.dx_direct = p.pieces == 1 && p.dx_splits == 1;
+    p.dx_direct = p.pieces == 1 && p.dx_splits == 1 && p.dx_rows == h.T;
     p.coef = p.take(h.T * 4);
     p.row_scale = p.take(h.T * 4);
     p.all_scale = p.take(4);
@@ -246,18 +263,18 @@ bool plan_backward(Plan &p, const Head &h)
         p.exps = p.take(h.T * 4);
         p.block_max = p.take(coef_blocks(h.T, true) * 4);
     }
-    p.g = p.take(p.Tp * p.ldg * 2 * p.planes);
-    if (!p.dx_direct) p.dx_part = p.take(p.dx_splits * h.T * p.Dp * 4);
+    p.g = p.take(p.Tp * p.ldg * 2 * p.g_planes);
+    if (!p.dx_direct) p.dx_part = p.take(p.dx_splits * p.dx_rows * p.Dp * 4);
     if (p.dw_splits > 1) p.dw_part = p.take(p.dw_splits * p.piece * p.Dp * 4);
     return fits(p.Tp, p.piece, p.grad_tile, 1) && fits(p.piece, h.D, p.dw_tile, p.dw_splits) &&
-           fits(h.T, h.D, p.dx_tile, p.dx_splits);
+           fits(p.dx_rows, h.D, p.dx_tile, p.dx_splits);
 }
 
-Operands operands(const Plan &p, int64_t M, int64_t N, int64_t steps, int tile)
+Operands operands(int segments, int64_t M, int64_t N, int64_t steps, int tile)
 {
     const TileShape &s = kTiles[tile];
     Operands o{};
-    o.segments = p.segments;
+    o.segments = segments;
     o.M = (int)M;
     o.N = (int)N;
     o.steps = o.steps_per_split = (int)steps;
@@ -305,7 +322,8 @@ struct Labels {
     const Teacher *teacher = nullptr;
 };
 
-// An operand of the head's product as the matrix cores read it.
+// An operand of the head's product as the matrix cores read it.  plane: 0 if
+// it is not split, so that its only plane meets both of the logits' gradient.
 struct Stored {
     const void *p;
     int64_t ld, plane;
@@ -322,12 +340,12 @@ tgemm_status_t forward(const Plan &p, const Head &h, const Labels &l, float *los
         if (e != hipSuccess) return from_hip(e);
     }
     if (p.copy_w) {
-        w = Stored{in<void>(ws, p.w), p.Dp, h.V * p.Dp};
+        w = Stored{in<void>(ws, p.w), p.Dp, p.planes > 1 ? h.V * p.Dp : 0};
         e = launch_copy(copy_of(p, h, h.W, h.ldw, h.V, in<void>(ws, p.w), h.V), stream);
         if (e != hipSuccess) return from_hip(e);
     }
     StatsArgs s{};
-    s.op = operands(p, h.T, h.V, p.Dp / kStepK, p.stat_tile);
+    s.op = operands(p.segments, h.T, h.V, p.Dp / kStepK, p.stat_tile);
     s.op.A = x.p;
     s.op.lda = x.ld;
     s.op.plane_a = x.plane;
@@ -404,7 +422,7 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
     }
     e = launch_copy(clear, stream);
     if (e != hipSuccess) return from_hip(e);
-    const Stored cleared{xs, p.Dp, p.Tp * p.Dp};
+    const Stored cleared{xs, p.Dp, p.planes > 1 ? p.Tp * p.Dp : 0};
     Stored x = cleared, w{h.W, h.ldw, 0};
     if (p.half) x = Stored{h.X, h.ldx, 0};
     if (p.copy_x) {
@@ -413,21 +431,20 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
         if (e != hipSuccess) return from_hip(e);
     }
     if (p.copy_w) {
-        w = Stored{in<void>(ws, p.w), p.Dp, h.V * p.Dp};
+        w = Stored{in<void>(ws, p.w), p.Dp, p.planes > 1 ? h.V * p.Dp : 0};
         e = launch_copy(copy_of(p, h, h.W, h.ldw, h.V, in<void>(ws, p.w), h.V), stream);
         if (e != hipSuccess) return from_hip(e);
     }
 
     void *g = in<void>(ws, p.g);
     const int64_t plane_g = p.Tp * p.ldg;
-    const int64_t dx_stride = h.T * p.Dp;
     for (int64_t n = 0; n < p.pieces; ++n) {
         const int64_t v0 = n * p.piece, cols = h.V - v0 < p.piece ? h.V - v0 : p.piece;
         const int64_t cols_steps = ceil_div(cols, kStepK);
         const char *wn = (const char *)w.p + v0 * w.ld * 2;
 
         GradArgs a{};
-        a.op = operands(p, h.T, cols, p.Dp / kStepK, p.grad_tile);
+        a.op = operands(p.segments, h.T, cols, p.Dp / kStepK, p.grad_tile);
         a.op.tiles_m = (int)ceil_div(p.Tp, kTiles[p.grad_tile].bm);
         a.op.A = x.p;
         a.op.lda = x.ld;
@@ -447,24 +464,24 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
         a.G = g;
         a.ldg = p.ldg;
         a.plane = plane_g;
-        a.planes = p.planes;
+        a.planes = p.g_planes;
         e = launch_grad(p.half, p.grad_tile, a, stream);
         if (e != hipSuccess) return from_hip(e);
         if (l.teacher != nullptr) {
-            ScatterArgs s{h.T, v0, cols, *l.teacher, student, lse, c.coef, g, p.ldg, plane_g, p.planes, p.half};
+            ScatterArgs s{h.T, v0, cols, *l.teacher, student, lse, c.coef, g, p.ldg, plane_g, p.g_planes, p.half};
             e = launch_scatter(s, stream);
             if (e != hipSuccess) return from_hip(e);
         }
         if (dX != nullptr) {
             OutArgs o{};
-            o.op = operands(p, h.T, h.D, cols_steps, p.dx_tile);
+            o.op = operands(p.segments, p.dx_rows, h.D, cols_steps, p.dx_tile);
             // the last piece may take fewer parts; the others' sums stand
             o.op.splits = parts_of(cols_steps, p.dx_splits);
             o.op.steps_per_split = (int)ceil_div(cols_steps, o.op.splits);
             o.op.A = g;
             o.op.lda = p.ldg;
             o.op.plane_a = plane_g;
-            o.op.mn_a = (int)p.Tp;
+            o.op.mn_a = (int)(p.dx_rows > p.Tp ? p.dx_rows : p.Tp);
             o.op.B = wn;
             o.op.ldb = w.ld;
             o.op.plane_b = w.plane;
@@ -482,14 +499,18 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
                 o.dtype = TGEMM_F32;
                 o.vec = true;
                 o.add = n > 0;
-                o.split_stride = dx_stride;
+                o.split_stride = p.dx_rows * p.Dp;
+                if (p.dx_rows > p.Tp) {  // two planes' rows
+                    o.period = (int)p.Tp;
+                    o.kept = (int)h.T;
+                }
             }
             e = launch_dx(p.half, p.dx_tile, o, stream);
             if (e != hipSuccess) return from_hip(e);
         }
         if (dW != nullptr) {
             OutArgs o{};
-            o.op = operands(p, cols, h.D, p.Tp / kStepK, p.dw_tile);
+            o.op = operands(p.dw_segments, cols, h.D, p.Tp / kStepK, p.dw_tile);
             o.op.A = g;
             o.op.lda = p.ldg;
             o.op.plane_a = plane_g;
@@ -527,7 +548,8 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
         }
     }
     if (dX != nullptr && !p.dx_direct) {
-        SumArgs s{h.T, h.D, in<float>(ws, p.dx_part), p.Dp, dx_stride, p.dx_splits, row_scale, nullptr,
+        const int planes = p.dx_rows > p.Tp ? 2 : 1;
+        SumArgs s{h.T, h.D, in<float>(ws, p.dx_part), p.Dp, p.dx_rows / planes * p.Dp, p.dx_splits * planes, row_scale, nullptr,
                   dX, lddx, h.dtype, rows16(dX, lddx, h.dtype)};
         e = launch_sum(s, stream);
         if (e != hipSuccess) return from_hip(e);

@@ -57,7 +57,8 @@ constexpr int kFewColumns = 64;
 hipError_t launch_stats_few(const StatsArgs &a, tgemm_dtype_t dtype, int D, hipStream_t stream);
 
 // A piece of the logits' gradient: G[t][v - v0] = coef[t]·(exp(s·z - lse[t]) -
-// [v = target[t]]), zero past the ends, 16-bit or three bf16 planes.
+// [v = target[t]]), zero past the ends, 16-bit: one plane, or two or three that
+// add up to it.
 struct GradArgs {
     m16::Operands op;
     float scale;
@@ -80,6 +81,7 @@ struct OutArgs {
     bool vec;                // out and its rows 16-byte aligned
     bool add;                // float32 out: add to what is there
     int64_t split_stride;    // elements between the outputs of the sum's parts
+    int period = 0, kept = INT32_MAX;  // of every `period` rows (a power of two; 0: one run) the first `kept` are stored
     const float *row_scale, *all_scale;  // as SumArgs
 };
 hipError_t launch_dx(bool half, int tile, const OutArgs &a, hipStream_t stream);

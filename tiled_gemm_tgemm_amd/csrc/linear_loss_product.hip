@@ -220,6 +220,7 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_grad_kernel(GradArgs a)
             } else {
 #pragma unroll
                 for (int q = 0; q < 3; ++q) {
+                    if (q == a.planes) break;
                     store_packed<E, H>(to + q * a.plane, g);
 #pragma unroll
                     for (int e = 0; e < H; ++e) g[e] -= (float)(E)g[e];
@@ -269,7 +270,7 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_out_kernel(OutArgs a)
 #pragma unroll
         for (int i = 0; i < Tile::FM; ++i) {
             const int row = row0 + i * 16 + l16;
-            if (row >= a.op.M) continue;
+            if (row >= a.op.M || (row & (a.period - 1)) >= a.kept) continue;
             float v[H];
 #pragma unroll
             for (int e = 0; e < H; ++e) v[e] = acc[i][e / 4][e % 4];

@@ -37,7 +37,7 @@ struct Operands {
     const void *A, *B;
     int64_t lda, ldb;          // elements
     int64_t plane_a, plane_b;  // elements between the planes of a split operand
-    int segments;              // 1, or 6: the plane pairs of kPairs
+    int segments;              // 1; 6: the plane pairs of kPairs; 2: the first two, with plane_b = 0
     int M, N;
     int steps;                 // steps of 64 along K
     int steps_per_split;       // part y of the sum takes steps [y·this, (y+1)·this)
@@ -49,7 +49,8 @@ struct Operands {
 // A float32 operand is the sum of three bf16 planes (high, middle, low: 24
 // bits).  Of the nine products of planes the six that reach 2^-24 of the
 // largest are summed, small ones first: (mid,mid), (high,low), (low,high),
-// (high,mid), (mid,high), (high,high); two bits a plane.
+// (high,mid), (mid,high), (high,high); two bits a plane.  The first two also
+// serve an A of two planes and a B of one: (low of the two, B), (high, B).
 constexpr int kPairsA = (1 << 0) | (0 << 2) | (2 << 4) | (0 << 6) | (1 << 8) | (0 << 10);
 constexpr int kPairsB = (1 << 0) | (2 << 2) | (0 << 4) | (1 << 6) | (0 << 8) | (0 << 10);
 
