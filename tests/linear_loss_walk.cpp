@@ -139,8 +139,7 @@ hipError_t launch_stats(bool, int tile, const StatsArgs &a, hipStream_t)
 hipError_t launch_stats_few(const StatsArgs &a, tgemm_dtype_t dtype, int D, hipStream_t)
 {
     const size_t size = size_of(dtype);
-    if (a.op.M > kFewRows || D % 8 || (uintptr_t)a.op.A % 16 || (uintptr_t)a.op.B % 16 || a.op.lda * size % 16 || a.op.ldb * size % 16)
-        fail("rows that are not 16-byte aligned", 0, 0);
+    if (a.op.M > kFewRows) fail("too many rows", 0, 0);
     rows(a.op.A, a.op.M, D, a.op.lda, size, false, "X");
     rows(a.op.B, a.op.N, D, a.op.ldb, size, false, "W");
     check_stats(a, kFewColumns);
@@ -164,7 +163,6 @@ hipError_t launch_grad(bool, int tile, const GradArgs &a, hipStream_t)
 void check_out(const OutArgs &a)
 {
     const size_t size = size_of(a.dtype);
-    if (a.vec && ((uintptr_t)a.out % 16 || a.ldo * size % 16 || a.split_stride * size % 16)) fail("a misaligned store", 0, 0);
     for (int s = 0; s < a.op.splits; ++s)
         rows((char *)a.out + s * a.split_stride * size, a.op.M, a.op.N, a.ldo, size, true, "gradient");
     if (a.row_scale) rows(a.row_scale, a.op.M, 1, 1, 4, false, "row scales");
@@ -207,7 +205,6 @@ hipError_t launch_coef(const CoefArgs &a, hipStream_t)
 hipError_t launch_copy(const CopyArgs &a, hipStream_t)
 {
     rows(a.src, a.rows, a.cols, a.ld, size_of(a.dtype), false, "an operand to copy");
-    if (a.vec && ((uintptr_t)a.src % 16 || a.ld * size_of(a.dtype) % 16)) fail("a misaligned read", 0, 0);
     if ((uintptr_t)a.dst % 16 || a.ld_out % 8) fail("a misaligned copy", 0, 0);
     for (int q = 0; q < a.planes; ++q)
         rows((char *)a.dst + q * a.plane * 2, a.rows_out, a.ld_out, a.ld_out, 2, true, "a copy");
@@ -270,7 +267,6 @@ hipError_t launch_sum(const SumArgs &a, hipStream_t)
     const int64_t padded = (a.D + 3) / 4 * 4;
     for (int s = 0; s < a.count; ++s) rows(a.part + s * a.stride, a.T, padded, a.ld, 4, false, "parts of a sum");
     if ((uintptr_t)a.part % 16 || a.ld % 4 || a.stride % 4) fail("a misaligned read", 0, 0);
-    if (a.vec && ((uintptr_t)a.out % 16 || a.ldo * size_of(a.dtype) % 16)) fail("a misaligned store", 0, 0);
     rows(a.out, a.T, a.D, a.ldo, size_of(a.dtype), true, "gradient");
     if (a.row_scale) rows(a.row_scale, a.T, 1, 1, 4, false, "row scales");
     if (a.all_scale) touch(a.all_scale, 4, false, "scale");

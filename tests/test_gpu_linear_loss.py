@@ -138,6 +138,27 @@ def test_strides_and_alignment(kind, D, pad, shift):
         assert bool((room[:, :shift] == 7).all()) and bool((room[:, shift + D:] == 7).all())
 
 
+# a few rows are read as they are stored, wherever that is
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("T", [1, 7, 20, 32])
+@pytest.mark.parametrize("D,pad,shift", [(1, 0, 0), (7, 2, 1), (33, 0, 0), (64, 1, 1), (100, 3, 5), (257, 0, 3), (1003, 2, 0)])
+def test_few_rows_anywhere(kind, T, D, pad, shift):
+    log(f"few rows {kind} T={T} D={D} pad={pad} shift={shift}")
+    X, W, g = head(T, 150, D, TYPES[kind], 13, pad, shift)
+    y, grad = targets(T, 150, g), row_grads(T, g)
+    loss, lse = tg.linear_cross_entropy_forward(X, W, y)
+    ref = Reference(X, W, y)
+    ref.check_rows(loss, lse)
+    room_x = torch.full((T, D + pad + shift), 7.0, dtype=X.dtype, device="cuda")
+    room_w = torch.full((150, D + pad + shift), 7.0, dtype=X.dtype, device="cuda")
+    dX, dW = room_x[:, shift:shift + D], room_w[:, shift:shift + D]
+    tg.linear_cross_entropy_backward(grad, X, W, y, lse, dX=dX, dW=dW)
+    torch.cuda.synchronize()
+    ref.check_gradients(grad.double(), dX, dW)
+    for room in (room_x, room_w):
+        assert bool((room[:, :shift] == 7).all()) and bool((room[:, shift + D:] == 7).all())
+
+
 @pytest.mark.parametrize("kind", ["bf16", "fp32"])
 def test_vocabulary_in_pieces(kind):
     T, V, D = (8192, 20003, 64) if kind == "bf16" else (4096, 13001, 64)

@@ -42,12 +42,6 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t size_of(tgemm_dtype_t t) { return t == TGEMM_F32 ? 4 : 2; }
 bool known(tgemm_dtype_t t) { return t == TGEMM_F32 || t == TGEMM_BF16 || t == TGEMM_F16; }
 
-// Rows start 16-byte aligned.
-bool rows16(const void *p, int64_t ld, tgemm_dtype_t dtype)
-{
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * (int64_t)size_of(dtype) % 16 == 0;
-}
-
 tgemm_status_t from_hip(hipError_t e) { return e == hipSuccess ? TGEMM_SUCCESS : TGEMM_ERROR_HIP; }
 
 // A byte range that a call reads or writes.
@@ -212,9 +206,10 @@ bool plan_forward(Plan &p, const Head &h, int64_t teacher_k)
     // The rows of X come from the caches once for every 16 words, which is as
     // much again as W from 16 rows on: tiles take more than 8 rows sooner
     // where they need no copy of W (17×32000×2048 bf16 31 against 40 µs, one
-    // row 58 against 47; float32 341 against 90).
+    // row 58 against 47), and fewer rows or none where they do (20×32000×1001
+    // bf16 55 against 45 µs, 32 rows 55 against 55; float32 341 against 90).
     const bool stored = as_stored(h.X, h.ldx, h, kStepK) && as_stored(h.W, h.ldw, h);
-    p.few = h.T <= (stored ? 8 : kFewRows) && h.D % 8 == 0 && rows16(h.X, h.ldx, h.dtype) && rows16(h.W, h.ldw, h.dtype);
+    p.few = h.T <= (stored ? 8 : kFewRows);
     if (p.few) {
         p.group_columns = kFewColumns;
     } else {
@@ -312,7 +307,6 @@ CopyArgs copy_of(const Plan &p, const Head &h, const void *src, int64_t ld, int6
     c.ld_out = p.Dp;
     c.plane = rows_out * p.Dp;
     c.planes = p.planes;
-    c.vec = rows16(src, ld, h.dtype);
     return c;
 }
 
@@ -491,13 +485,11 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
                 o.out = dX;
                 o.ldo = lddx;
                 o.dtype = h.dtype;
-                o.vec = rows16(dX, lddx, h.dtype);
                 o.row_scale = row_scale;
             } else {
                 o.out = in<float>(ws, p.dx_part);
                 o.ldo = p.Dp;
                 o.dtype = TGEMM_F32;
-                o.vec = true;
                 o.add = n > 0;
                 o.split_stride = p.dx_rows * p.Dp;
                 if (p.dx_rows > p.Tp) {  // two planes' rows
@@ -526,7 +518,6 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
                 o.out = to;
                 o.ldo = lddw;
                 o.dtype = h.dtype;
-                o.vec = rows16(dW, lddw, h.dtype);
                 o.all_scale = all_scale;
             } else {
                 o.op.splits = p.dw_splits;
@@ -534,14 +525,13 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
                 o.out = in<float>(ws, p.dw_part);
                 o.ldo = p.Dp;
                 o.dtype = TGEMM_F32;
-                o.vec = true;
                 o.split_stride = p.piece * p.Dp;
             }
             e = launch_dw(p.half, p.dw_tile, o, stream);
             if (e != hipSuccess) return from_hip(e);
             if (p.dw_splits > 1) {
                 SumArgs s{cols, h.D, in<float>(ws, p.dw_part), p.Dp, o.split_stride, p.dw_splits, nullptr,
-                          all_scale, to, lddw, h.dtype, rows16(dW, lddw, h.dtype)};
+                          all_scale, to, lddw, h.dtype};
                 e = launch_sum(s, stream);
                 if (e != hipSuccess) return from_hip(e);
             }
@@ -550,7 +540,7 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
     if (dX != nullptr && !p.dx_direct) {
         const int planes = p.dx_rows > p.Tp ? 2 : 1;
         SumArgs s{h.T, h.D, in<float>(ws, p.dx_part), p.Dp, p.dx_rows / planes * p.Dp, p.dx_splits * planes, row_scale, nullptr,
-                  dX, lddx, h.dtype, rows16(dX, lddx, h.dtype)};
+                  dX, lddx, h.dtype};
         e = launch_sum(s, stream);
         if (e != hipSuccess) return from_hip(e);
     }

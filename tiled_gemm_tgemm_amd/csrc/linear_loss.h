@@ -50,8 +50,8 @@ struct StatsArgs {
 };
 hipError_t launch_stats(bool half, int tile, const StatsArgs &a, hipStream_t stream);
 
-// launch_stats for at most kFewRows rows, on operands as they are stored (rows
-// 16-byte aligned, D a multiple of 8); column groups of kFewColumns.
+// launch_stats for at most kFewRows rows, on operands however they are stored;
+// column groups of kFewColumns.
 constexpr int64_t kFewRows = 32;
 constexpr int kFewColumns = 64;
 hipError_t launch_stats_few(const StatsArgs &a, tgemm_dtype_t dtype, int D, hipStream_t stream);
@@ -78,7 +78,6 @@ struct OutArgs {
     void *out;
     int64_t ldo;
     tgemm_dtype_t dtype;
-    bool vec;                // out and its rows 16-byte aligned
     bool add;                // float32 out: add to what is there
     int64_t split_stride;    // elements between the outputs of the sum's parts
     int period = 0, kept = INT32_MAX;  // of every `period` rows (a power of two; 0: one run) the first `kept` are stored
@@ -173,7 +172,6 @@ struct CopyArgs {
     void *dst;
     int64_t rows_out, ld_out, plane;
     int planes;
-    bool vec;  // 16-byte loads
     const float *coef;
     const int *exps, *block_max;
     int blocks;
@@ -205,7 +203,6 @@ struct SumArgs {
     void *out;
     int64_t ldo;
     tgemm_dtype_t dtype;
-    bool vec;  // out and its rows 16-byte aligned
 };
 hipError_t launch_sum(const SumArgs &a, hipStream_t stream);
 

@@ -7,7 +7,14 @@
 // are under way while these are multiplied: there is no LDS stage and no
 // barrier, so each wavefront keeps 4 (float32: 8) KB of W on its way by
 // itself.  The rows of X come from the caches.  A float32 operand is split
-// into its bf16 planes in registers, which spares a copy of W in planes.
+// into its bf16 planes in registers, which spares a copy of W in planes, and
+// rows may lie anywhere and have any length, which spares a copy of W in rows
+// of whole steps.
+//
+// One row of 32000×4096 bf16 takes 40 µs, one of 131072×2048 100 µs (5.4
+// TB/s), and 4 of 56852×2752 float32 184 µs (3.4 TB/s), with the join.  Rows
+// that start at odd multiples of 2 bytes cost their 16-byte loads twice the
+// time: one row of 32000×4097 109 µs (a copy and the tiles take 200).
 #include "linear_loss.h"
 #include "mfma16.h"
 
@@ -20,13 +27,16 @@ using m16::Frag;
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// Eight values of an operand as they are stored, and as fragments.
+// Eight values of an operand as they are stored (device memory takes 16-byte
+// loads at any address), and as fragments.
 template <class In>
 struct Eight {
     typedef typename Frag<In>::type Raw;
+    typedef Raw Anywhere __attribute__((aligned(2)));
     static constexpr int kPlanes = 1;
     typedef In Element;
-    static __device__ __forceinline__ Raw load(const In *p) { return *(const Raw *)p; }
+    static __device__ __forceinline__ Raw load(const In *p) { return *(const Anywhere *)p; }
+    static __device__ __forceinline__ void set(Raw &raw, int e, In v) { raw[e] = v; }
     static __device__ __forceinline__ void planes(const Raw &raw, typename Frag<In>::type (&out)[1]) { out[0] = raw; }
 };
 template <>
@@ -34,9 +44,11 @@ struct Eight<float> {
     struct Raw {
         f32x4 lo, hi;
     };
+    typedef f32x4 Anywhere __attribute__((aligned(4)));
     static constexpr int kPlanes = 3;
     typedef __bf16 Element;
-    static __device__ __forceinline__ Raw load(const float *p) { return Raw{((const f32x4 *)p)[0], ((const f32x4 *)p)[1]}; }
+    static __device__ __forceinline__ Raw load(const float *p) { return Raw{((const Anywhere *)p)[0], ((const Anywhere *)p)[1]}; }
+    static __device__ __forceinline__ void set(Raw &raw, int e, float v) { (e < 4 ? raw.lo : raw.hi)[e & 3] = v; }
     static __device__ __forceinline__ void planes(const Raw &raw, m16::bf16x8 (&out)[3])
     {
 #pragma unroll
@@ -116,10 +128,19 @@ __global__ __launch_bounds__(256) void linear_few_kernel(StatsArgs a, int D)
     }
     for (int k = whole * 32 * U; k < D; k += 32) {
         Raw zw{}, zx[R] = {};
-        if (k + 8 * quarter < D) {  // D is a multiple of 8
+        const int left = D - (k + 8 * quarter);
+        if (left >= 8) {
             zw = X8::load(w + k);
 #pragma unroll
             for (int i = 0; i < R; ++i) zx[i] = X8::load(x[i] + k);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < left) {
+                    X8::set(zw, e, w[k + e]);
+#pragma unroll
+                    for (int i = 0; i < R; ++i) X8::set(zx[i], e, x[i][k + e]);
+                }
         }
         multiply(zw, zx);
     }

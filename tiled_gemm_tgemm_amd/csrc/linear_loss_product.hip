@@ -139,7 +139,11 @@ __device__ __forceinline__ uint32_t pack(_Float16 a, _Float16 b)
     return (uint32_t)__builtin_bit_cast(uint16_t, a) | (uint32_t)__builtin_bit_cast(uint16_t, b) << 16;
 }
 
-// N (a multiple of 8) adjacent values as 16-bit numbers, 16-byte aligned.
+// Device memory takes 16-byte stores at any address.
+typedef uint32_t u32x4_anywhere __attribute__((ext_vector_type(4), aligned(2)));
+typedef f32x4 f32x4_anywhere __attribute__((aligned(4)));
+
+// N (a multiple of 8) adjacent values as 16-bit numbers.
 template <class E, int N>
 __device__ __forceinline__ void store_packed(E *to, const float (&v)[N])
 {
@@ -148,7 +152,7 @@ __device__ __forceinline__ void store_packed(E *to, const float (&v)[N])
         uint32_t w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[e] = pack((E)v[8 * q + 2 * e], (E)v[8 * q + 2 * e + 1]);
-        reinterpret_cast<uint4 *>(to)[q] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<u32x4_anywhere *>(to)[q] = u32x4_anywhere{w[0], w[1], w[2], w[3]};
     }
 }
 
@@ -232,9 +236,9 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_grad_kernel(GradArgs a)
 
 // N adjacent values of a row of the result, `left` of them inside it.
 template <class T, int N>
-__device__ __forceinline__ void store_row(T *to, const float (&v)[N], int left, bool vec)
+__device__ __forceinline__ void store_row(T *to, const float (&v)[N], int left)
 {
-    if (vec && left >= N) {
+    if (left >= N) {
         if constexpr (sizeof(T) == 2) {
             store_packed<T, N>(to, v);
         } else {
@@ -243,7 +247,7 @@ __device__ __forceinline__ void store_row(T *to, const float (&v)[N], int left, 
                 f32x4 w;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w[e] = v[4 * q + e];
-                reinterpret_cast<f32x4 *>(to)[q] = w;
+                reinterpret_cast<f32x4_anywhere *>(to)[q] = w;
             }
         }
     } else {
@@ -287,9 +291,9 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_out_kernel(OutArgs a)
                     for (int e = 0; e < H; ++e)
                         if (e < left) v[e] += to[e];
                 }
-                store_row<float, H>(to, v, left, a.vec);
+                store_row<float, H>(to, v, left);
             } else {
-                store_row<E, H>((E *)a.out + at, v, left, a.vec);
+                store_row<E, H>((E *)a.out + at, v, left);
             }
         }
     });

@@ -10,6 +10,12 @@ namespace loss {
 namespace {
 
 typedef unsigned short u16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+// device memory takes 16-byte loads and stores at any address
+typedef u16x8 u16x8_anywhere __attribute__((aligned(2)));
+typedef f32x8 f32x8_anywhere __attribute__((aligned(4)));
+typedef m16::f32x4 f32x4_anywhere __attribute__((aligned(4)));
+typedef uint32_t u32x2_anywhere __attribute__((ext_vector_type(2), aligned(2)));
 
 // No factor of a float32 row can be as low: the largest exponent of rows that all do not count.
 constexpr int kNoExponent = -100000;
@@ -109,18 +115,25 @@ __global__ __launch_bounds__(256) void linear_copy_kernel(CopyArgs a, CoefArgs m
         u16x8 v[3] = {};
         if (counts && a.dtype == TGEMM_F32) {
             const float *from = (const float *)a.src + row * a.ld + col;
+            f32x8 f{};
+            if (left == 8) {
+                f = *(const f32x8_anywhere *)from;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = e < left ? from[e] : 0.0f;
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 __bf16 h, m, l;
-                m16::split(e < left ? from[e] : 0.0f, h, m, l);
+                m16::split(f[e], h, m, l);
                 v[0][e] = bits(h);
                 v[1][e] = bits(m);
                 v[2][e] = bits(l);
             }
         } else if (counts) {
             const uint16_t *from = (const uint16_t *)a.src + row * a.ld + col;
-            if (a.vec && left == 8) {
-                v[0] = *(const u16x8 *)from;
+            if (left == 8) {
+                v[0] = *(const u16x8_anywhere *)from;
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[0][e] = e < left ? from[e] : (uint16_t)0;
@@ -462,14 +475,14 @@ __global__ __launch_bounds__(256) void linear_sum_kernel(SumArgs a)
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = m16::mul_zero(scale, v[e]);
         const int64_t at = row * a.ldo + col;
-        if (a.vec && col + 4 <= a.D) {
+        if (col + 4 <= a.D) {
             if (a.dtype == TGEMM_F32) {
-                *(m16::f32x4 *)((float *)a.out + at) = v;
+                *(f32x4_anywhere *)((float *)a.out + at) = v;
             } else {
                 uint16_t w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w[e] = a.dtype == TGEMM_BF16 ? bits((__bf16)v[e]) : bits((_Float16)v[e]);
-                *(uint2 *)((uint16_t *)a.out + at) = make_uint2(w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16);
+                *(u32x2_anywhere *)((uint16_t *)a.out + at) = u32x2_anywhere{w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16};
             }
         } else {
 #pragma unroll
