@@ -136,13 +136,13 @@ hipError_t launch_stats(bool, int tile, const StatsArgs &a, hipStream_t)
     return hipSuccess;
 }
 
-hipError_t launch_stats_few(const StatsArgs &a, tgemm_dtype_t dtype, int D, hipStream_t)
+hipError_t launch_stats_few(const StatsArgs &a, tgemm_dtype_t dtype, int columns, int D, hipStream_t)
 {
     const size_t size = size_of(dtype);
     if (a.op.M > kFewRows) fail("too many rows", 0, 0);
     rows(a.op.A, a.op.M, D, a.op.lda, size, false, "X");
     rows(a.op.B, a.op.N, D, a.op.ldb, size, false, "W");
-    check_stats(a, kFewColumns);
+    check_stats(a, columns);
     return hipSuccess;
 }
 

@@ -101,7 +101,8 @@ def test_cross_entropy(kind, T, V, D):
                                                  (130, 777, 200, 33, 3.0), (257, 2049, 64, 64, 0.5),
                                                  (300, 5003, 320, 100, 2.0), (8, 4000, 64, 1024, 1.5),
                                                  (5, 262144, 8, 90, 1.0), (40, 262145, 8, 33, 2.0),
-                                                 (9, 600007, 16, 200, 1.0)])
+                                                 (9, 600007, 16, 200, 1.0), (20, 16383, 24, 50, 1.0),
+                                                 (7, 16384, 200, 128, 2.0)])
 def test_distillation(kind, T, V, D, K, temperature):
     log(f"distillation {kind} {T}x{V}x{D} K={K} temperature={temperature}")
     X, W, g = head(T, V, D, TYPES[kind], 2)

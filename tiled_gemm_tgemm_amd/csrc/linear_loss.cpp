@@ -211,7 +211,7 @@ bool plan_forward(Plan &p, const Head &h, int64_t teacher_k)
     const bool stored = as_stored(h.X, h.ldx, h, kStepK) && as_stored(h.W, h.ldw, h);
     p.few = h.T <= (stored ? 8 : kFewRows);
     if (p.few) {
-        p.group_columns = kFewColumns;
+        p.group_columns = few_columns(h.V);
     } else {
         plan_operands(p, h, false);
         p.stat_tile = choose_tile(h.T, h.V, p.Dp / kStepK * p.segments).tile;
@@ -364,7 +364,7 @@ tgemm_status_t forward(const Plan &p, const Head &h, const Labels &l, float *los
         s.K = l.teacher->K;
         s.student = student;
     }
-    e = p.few ? launch_stats_few(s, h.dtype, (int)h.D, stream) : launch_stats(p.half, p.stat_tile, s, stream);
+    e = p.few ? launch_stats_few(s, h.dtype, p.group_columns, (int)h.D, stream) : launch_stats(p.half, p.stat_tile, s, stream);
     if (e != hipSuccess) return from_hip(e);
     JoinArgs j{h.T, h.V, p.groups, s.part, l.target, l.ignore, s.picked, l.teacher, student, loss, lse, summary,
                in<int>(ws, p.counted)};

@@ -51,10 +51,14 @@ struct StatsArgs {
 hipError_t launch_stats(bool half, int tile, const StatsArgs &a, hipStream_t stream);
 
 // launch_stats for at most kFewRows rows, on operands however they are stored;
-// column groups of kFewColumns.
-constexpr int64_t kFewRows = 32;
-constexpr int kFewColumns = 64;
-hipError_t launch_stats_few(const StatsArgs &a, tgemm_dtype_t dtype, int D, hipStream_t stream);
+// column groups of 16 or 64 (few_columns).  A compute unit gets no more than
+// about 22 GB/s of W from memory however many wavefronts ask for it, so words
+// are dealt 16 at a time where 64 at a time leave compute units without any:
+// one row of 4000×4096 bf16 11 against 25 µs, of 16000×4096 26 against 28, of
+// 32000×4096 46 against 44, of 65536×1024 29 against 26.
+constexpr int64_t kFewRows = 32, kFewBelow = 16384;
+inline int few_columns(int64_t V) { return V < kFewBelow ? 16 : 64; }
+hipError_t launch_stats_few(const StatsArgs &a, tgemm_dtype_t dtype, int columns, int D, hipStream_t stream);
 
 // A piece of the logits' gradient: G[t][v - v0] = coef[t]·(exp(s·z - lse[t]) -
 // [v = target[t]]), zero past the ends, 16-bit: one plane, or two or three that

@@ -2,19 +2,21 @@
 // served): bound by reading W once.
 //
 // A wavefront takes 16 words (rows of W) and R blocks of 16 rows of X, a
-// work-group 64 words.  Fragments come straight from device memory into
-// registers, eight values a lane, and the loads of the next 128 values of k
-// are under way while these are multiplied: there is no LDS stage and no
-// barrier, so each wavefront keeps 4 (float32: 8) KB of W on its way by
-// itself.  The rows of X come from the caches.  A float32 operand is split
-// into its bf16 planes in registers, which spares a copy of W in planes, and
-// rows may lie anywhere and have any length, which spares a copy of W in rows
-// of whole steps.
+// work-group 64 words, or 16 with four wavefronts along k.  Fragments come
+// straight from device memory into registers, eight values a lane, and the
+// loads of the next 128 values of k are under way while these are multiplied:
+// there is no LDS stage and no barrier, so each wavefront keeps 4 (float32: 8)
+// KB of W on its way by itself.  The rows of X come from the caches.  A float32
+// operand is split into its bf16 planes in registers, which spares a copy of W
+// in planes, and rows may lie anywhere and have any length, which spares a copy
+// of W in rows of whole steps.
 //
-// One row of 32000×4096 bf16 takes 40 µs, one of 131072×2048 100 µs (5.4
-// TB/s), and 4 of 56852×2752 float32 184 µs (3.4 TB/s), with the join.  Rows
-// that start at odd multiples of 2 bytes cost their 16-byte loads twice the
-// time: one row of 32000×4097 109 µs (a copy and the tiles take 200).
+// With the join: one row of 32000×4096 bf16 44 µs, one of 131072×2048 106 µs
+// (5.1 TB/s), 4 of 56852×2752 float32 155 µs (4.0 TB/s; 185 with one wavefront
+// along k, whose splitting of the operands the loads then wait for; two blocks
+// of rows 52 against 55 at 32×32768×1024, so those keep one).  Rows that start
+// at odd multiples of 2 bytes cost their 16-byte loads twice the time: one row
+// of 32000×4097 109 µs (a copy and the tiles take 200).
 #include "linear_loss.h"
 #include "mfma16.h"
 
@@ -62,14 +64,19 @@ struct Eight<float> {
     }
 };
 
-template <class In, int R>
-__global__ __launch_bounds__(256) void linear_few_kernel(StatsArgs a, int D)
+// C: the blocks of 16 words; S: the parts of the sum over k, each with
+// wavefronts of its own, which are added through LDS.
+template <class In, int R, int C, int S>
+__global__ __launch_bounds__(64 * C * S) void linear_few_kernel(StatsArgs a, int D)
 {
     typedef Eight<In> X8;
     typedef typename X8::Raw Raw;
-    constexpr int U = sizeof(In) == 4 && R == 2 ? 2 : 4;  // 32 values of k each; two blocks of float32 rows fill the registers sooner
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, quarter = lane >> 4;
-    const int group = blockIdx.x, col0 = group * kFewColumns + wave * 16;
+    // 32 values of k each; two blocks of float32 rows fill the registers sooner,
+    // as do 16 wavefronts
+    constexpr int U = sizeof(In) == 4 && (R == 2 || C * S == 16) ? 2 : 4;
+    const int lane = threadIdx.x & 63, wave = (threadIdx.x >> 6) % C, part = (threadIdx.x >> 6) / C;
+    const int l16 = lane & 15, quarter = lane >> 4;
+    const int group = blockIdx.x, col0 = (group * C + wave) * 16;
     // words and rows past the last are read from it and do not count
     const In *w = (const In *)a.op.B + (int64_t)min(col0 + l16, a.op.N - 1) * a.op.ldb + 8 * quarter;
     const In *x[R];
@@ -108,11 +115,11 @@ __global__ __launch_bounds__(256) void linear_few_kernel(StatsArgs a, int D)
 #pragma unroll
         for (int u = 0; u < U; ++u) multiply(rw[set][u], rx[set][u]);
     };
-    const int whole = D / (32 * U);
-    if (whole > 0) {
-        load(0, 0);
-        int n = 1;
-        for (; n + 1 < whole; n += 2) {
+    const int each = (D / (32 * U) + S - 1) / S, whole = min(D / (32 * U), (part + 1) * each);
+    int n = part * each;
+    if (n < whole) {
+        load(0, n * 32 * U);
+        for (++n; n + 1 < whole; n += 2) {
             load(1, n * 32 * U);
             use(0);
             load(0, (n + 1) * 32 * U);
@@ -126,7 +133,7 @@ __global__ __launch_bounds__(256) void linear_few_kernel(StatsArgs a, int D)
             use(0);
         }
     }
-    for (int k = whole * 32 * U; k < D; k += 32) {
+    for (int k = D / (32 * U) * 32 * U; k < D && part == S - 1; k += 32) {
         Raw zw{}, zx[R] = {};
         const int left = D - (k + 8 * quarter);
         if (left >= 8) {
@@ -145,14 +152,29 @@ __global__ __launch_bounds__(256) void linear_few_kernel(StatsArgs a, int D)
         multiply(zw, zx);
     }
 
+    if constexpr (S > 1) {
+        __shared__ f32x4 sums[S - 1][C][R][64];
+        if (part > 0) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) sums[part - 1][wave][i][lane] = acc[i];
+        }
+        __syncthreads();
+        if (part == 0) {
+#pragma unroll
+            for (int q = 0; q < S - 1; ++q)
+#pragma unroll
+                for (int i = 0; i < R; ++i) acc[i] += sums[q][wave][i][lane];
+        }
+    }
+
     // acc[i][r]: row 16·i + l16, column col0 + 4·quarter + r
     const int left = a.op.N - (col0 + 4 * quarter);
     const float scale2 = a.scale * kLog2e;
-    __shared__ float2 parts[4][16 * R];
+    __shared__ float2 parts[C][16 * R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const int row = 16 * i + l16;
-        if (row < a.op.M) {
+        if (row < a.op.M && part == 0) {
             if (a.target != nullptr) {
                 const int64_t want = a.target[row] - (col0 + 4 * quarter);
 #pragma unroll
@@ -184,35 +206,43 @@ __global__ __launch_bounds__(256) void linear_few_kernel(StatsArgs a, int D)
         for (int r = 0; r < 4; ++r) sum += __builtin_amdgcn_exp2f(fmaf(acc[i][r], scale2, -from));
         sum += __shfl_xor(sum, 16);
         sum += __shfl_xor(sum, 32);
-        if (quarter == 0) parts[wave][row] = make_float2(high, sum);
+        if (quarter == 0 && part == 0) parts[wave][row] = make_float2(high, sum);
     }
     __syncthreads();
     const int row = threadIdx.x;
     if (row < 16 * R && row < a.op.M) {
         float high = -INFINITY, sum = 0.0f;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) high = fmaxf(high, parts[v][row].x);
+        for (int v = 0; v < C; ++v) high = fmaxf(high, parts[v][row].x);
         const float from = high == -INFINITY ? 0.0f : high;
 #pragma unroll
-        for (int v = 0; v < 4; ++v) sum += parts[v][row].y * __builtin_amdgcn_exp2f(parts[v][row].x - from);
+        for (int v = 0; v < C; ++v) sum += parts[v][row].y * __builtin_amdgcn_exp2f(parts[v][row].x - from);
         a.part[(int64_t)row * a.groups + group] = make_float2(high, sum);
     }
 }
 
-template <class In>
-void launch(const StatsArgs &a, int D, hipStream_t stream)
+template <class In, int R>
+void launch(const StatsArgs &a, int columns, int D, hipStream_t stream)
 {
-    if (a.op.M <= 16) linear_few_kernel<In, 1><<<(unsigned)a.groups, 256, 0, stream>>>(a, D);
-    else linear_few_kernel<In, 2><<<(unsigned)a.groups, 256, 0, stream>>>(a, D);
+    const unsigned groups = (unsigned)a.groups;
+    if (columns == 16) linear_few_kernel<In, R, 1, 4><<<groups, 256, 0, stream>>>(a, D);
+    else if (sizeof(In) == 4 && R == 1) linear_few_kernel<In, R, 4, 4><<<groups, 1024, 0, stream>>>(a, D);
+    else linear_few_kernel<In, R, 4, 1><<<groups, 256, 0, stream>>>(a, D);
+}
+template <class In>
+void launch(const StatsArgs &a, int columns, int D, hipStream_t stream)
+{
+    if (a.op.M <= 16) launch<In, 1>(a, columns, D, stream);
+    else launch<In, 2>(a, columns, D, stream);
 }
 
 }  // namespace
 
-hipError_t launch_stats_few(const StatsArgs &a, tgemm_dtype_t dtype, int D, hipStream_t stream)
+hipError_t launch_stats_few(const StatsArgs &a, tgemm_dtype_t dtype, int columns, int D, hipStream_t stream)
 {
-    if (dtype == TGEMM_F32) launch<float>(a, D, stream);
-    else if (dtype == TGEMM_BF16) launch<__bf16>(a, D, stream);
-    else launch<_Float16>(a, D, stream);
+    if (dtype == TGEMM_F32) launch<float>(a, columns, D, stream);
+    else if (dtype == TGEMM_BF16) launch<__bf16>(a, columns, D, stream);
+    else launch<_Float16>(a, columns, D, stream);
     return hipGetLastError();
 }
 
