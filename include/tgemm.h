@@ -413,14 +413,14 @@ tgemm_status_t tgemm_linear_ce_forward(tgemm_dtype_t dtype, int64_t T, int64_t V
                                        const void *X, int64_t ldx,
                                        const void *W, int64_t ldw,
                                        const int64_t *target, int64_t ignore_index,
-                                       float *loss, float *lse, float *summary,
+                                       float *loss, float *lse, float *logits, int64_t ldz, float *summary,
                                        void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 tgemm_status_t tgemm_linear_ce_backward(tgemm_dtype_t dtype, int64_t T, int64_t V, int64_t D,
                                         const void *X, int64_t ldx,
                                         const void *W, int64_t ldw,
                                         const int64_t *target, int64_t ignore_index,
-                                        const float *lse,
+                                        const float *lse, const float *logits, int64_t ldz,
                                         const float *grad_loss, int64_t grad_step, const float *grad_weight,
                                         void *dX, int64_t lddx, void *dW, int64_t lddw,
                                         void *workspace, size_t workspace_bytes, hipStream_t stream);
@@ -442,7 +442,8 @@ tgemm_status_t tgemm_linear_kd_forward(tgemm_dtype_t dtype, int64_t T, int64_t V
                                        int64_t K, const int64_t *teacher_ids, int64_t ld_ids,
                                        tgemm_dtype_t teacher_dtype, const void *teacher_logits, int64_t ld_logits,
                                        float temperature,
-                                       float *loss, float *lse, float *student, float *summary,
+                                       float *loss, float *lse, float *student,
+                                       float *logits, int64_t ldz, float *summary,
                                        void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 tgemm_status_t tgemm_linear_kd_backward(tgemm_dtype_t dtype, int64_t T, int64_t V, int64_t D,
@@ -451,7 +452,7 @@ tgemm_status_t tgemm_linear_kd_backward(tgemm_dtype_t dtype, int64_t T, int64_t 
                                         int64_t K, const int64_t *teacher_ids, int64_t ld_ids,
                                         tgemm_dtype_t teacher_dtype, const void *teacher_logits, int64_t ld_logits,
                                         float temperature,
-                                        const float *lse, const float *student,
+                                        const float *lse, const float *student, const float *logits, int64_t ldz,
                                         const float *grad_loss, int64_t grad_step, const float *grad_weight,
                                         void *dX, int64_t lddx, void *dW, int64_t lddw,
                                         void *workspace, size_t workspace_bytes, hipStream_t stream);

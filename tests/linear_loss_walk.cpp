@@ -129,10 +129,16 @@ void check_stats(const StatsArgs &a, int columns)
     }
 }
 
+void check_kept(const StatsArgs &a)
+{
+    if (a.logits) rows(a.logits, a.op.M, a.op.N, a.ldz, 4, true, "kept logits");
+}
+
 hipError_t launch_stats(bool, int tile, const StatsArgs &a, hipStream_t)
 {
     walk_tile<false, false>(tile, a.op);
     check_stats(a, kTiles[tile].stat_columns);
+    check_kept(a);
     return hipSuccess;
 }
 
@@ -143,6 +149,7 @@ hipError_t launch_stats_few(const StatsArgs &a, tgemm_dtype_t dtype, int columns
     rows(a.op.A, a.op.M, D, a.op.lda, size, false, "X");
     rows(a.op.B, a.op.N, D, a.op.ldb, size, false, "W");
     check_stats(a, columns);
+    check_kept(a);
     return hipSuccess;
 }
 
@@ -153,6 +160,18 @@ hipError_t launch_grad(bool, int tile, const GradArgs &a, hipStream_t)
     if (a.op.tiles_m * s.bm < a.rows || a.op.tiles_n * s.bn < (a.op.N + 63) / 64 * 64) fail("rows or columns left out", 0, 0);
     const int64_t cols = std::min<int64_t>(a.ldg, (int64_t)a.op.tiles_n * s.bn);
     if ((uintptr_t)a.G % 16 || a.ldg % 16) fail("rows that are not 16-byte aligned", 0, 0);
+    for (int q = 0; q < a.planes; ++q) rows((char *)a.G + q * a.plane * 2, a.rows, cols, a.ldg, 2, true, "G");
+    rows(a.coef, a.op.M, 1, 1, 4, false, "coef");
+    rows(a.lse, a.op.M, 1, 1, 4, false, "lse");
+    if (a.target) rows(a.target, a.op.M, 1, 1, 8, false, "targets");
+    return hipSuccess;
+}
+
+hipError_t launch_grad_kept(bool, const GradArgs &a, const float *logits, int64_t ldz, hipStream_t)
+{
+    rows(logits, a.op.M, a.op.N, ldz, 4, false, "kept logits");
+    const int64_t cols = (a.op.N + 63) / 64 * 64;
+    if (cols > a.ldg || (uintptr_t)a.G % 16 || a.ldg % 16) fail("rows that are not 16-byte aligned", 0, 0);
     for (int q = 0; q < a.planes; ++q) rows((char *)a.G + q * a.plane * 2, a.rows, cols, a.ldg, 2, true, "G");
     rows(a.coef, a.op.M, 1, 1, 4, false, "coef");
     rows(a.lse, a.op.M, 1, 1, 4, false, "lse");
@@ -312,21 +331,23 @@ int main()
         float *summary = (float *)give("summary", 12, !pass), *grad = (float *)matrix("grad", T, 1, nx ? 0 : 1, 4, false);
         void *dX = nx ? matrix("dX", T, D, lddx, size, true, sx * size) : nullptr;
         void *dW = nw ? matrix("dW", V, D, lddw, size, true, sw * size) : nullptr;
+        const int64_t ldz = V + 3;
+        float *z = (T + V) % 2 ? (float *)matrix("kept logits", T, V, ldz, 4, !pass) : nullptr;
         const size_t need = tgemm_linear_loss_workspace_size(dtype, T, V, D, X, ldx, W, ldw, op ? K : 0, (int)pass);
         void *ws = give("workspace", need, true);
         tgemm_status_t st;
         const int64_t step = nx ? 0 : 1;
         if (!op && !pass)
-            st = tgemm_linear_ce_forward(dtype, T, V, D, X, ldx, W, ldw, target, -100, loss, lse, summary, ws, need, nullptr);
+            st = tgemm_linear_ce_forward(dtype, T, V, D, X, ldx, W, ldw, target, -100, loss, lse, z, ldz, summary, ws, need, nullptr);
         else if (!op)
-            st = tgemm_linear_ce_backward(dtype, T, V, D, X, ldx, W, ldw, target, -100, lse, grad, step, summary + 2, dX, lddx, dW,
+            st = tgemm_linear_ce_backward(dtype, T, V, D, X, ldx, W, ldw, target, -100, lse, z, ldz, grad, step, summary + 2, dX, lddx, dW,
                                           lddw, ws, need, nullptr);
         else if (!pass)
             st = tgemm_linear_kd_forward(dtype, T, V, D, X, ldx, W, ldw, K, ids, K + 1, dtype, logits, K + 3, 2.0f, loss, lse,
-                                         student, summary, ws, need, nullptr);
+                                         student, z, ldz, summary, ws, need, nullptr);
         else
             st = tgemm_linear_kd_backward(dtype, T, V, D, X, ldx, W, ldw, K, ids, K + 1, dtype, logits, K + 3, 2.0f, lse, student,
-                                          grad, step, nullptr, dX, lddx, dW, lddw, ws, need, nullptr);
+                                          z, ldz, grad, step, nullptr, dX, lddx, dW, lddw, ws, need, nullptr);
         if (st != TGEMM_SUCCESS) {
             std::printf("status %d for: %s", (int)st, line);
             return 1;

@@ -539,3 +539,122 @@ def test_trained_together():
         assert bool(((weight.grad.double() - want_w).abs() <= off_w).all())
         assert float((hidden.grad.double() - want_x).norm() / want_x.norm()) < 2.0 ** -16
         opt.step()
+
+
+# the products kept for the backward pass: by the tiles of each size, by the few rows' kernel, in rows that start
+# anywhere, with nothing written between them
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("T,V,D,pad", [(1, 1, 1, 0), (5, 301, 40, 2), (20, 1000, 72, 0), (33, 1001, 128, 1), (64, 30000, 64, 0),
+                                       (130, 777, 200, 3), (300, 5003, 65, 0), (700, 4099, 320, 5)])
+def test_kept_logits(kind, T, V, D, pad):
+    log(f"kept {kind} {T}x{V}x{D} pad={pad}")
+    X, W, g = head(T, V, D, TYPES[kind], 14)
+    y, grad = targets(T, V, g), row_grads(T, g)
+    room = torch.full((T, V + pad), 7.0, device="cuda")
+    Z = room[:, :V]
+    for distill in (False, True):
+        if distill:
+            ids, top = entries(T, V, min(V, 9), TYPES[kind], g)
+            loss, lse, student = tg.linear_distillation_forward(X, W, ids, top, temperature=2.0, logits=Z)
+            ref = Reference(X, W, ids=ids, logits=top, temperature=2.0)
+            ref.check_rows(loss, lse, student)
+            dX, dW = tg.linear_distillation_backward(grad, X, W, ids, top, lse, student, temperature=2.0, logits=Z)
+        else:
+            loss, lse = tg.linear_cross_entropy_forward(X, W, y, logits=Z)
+            ref = Reference(X, W, y)
+            ref.check_rows(loss, lse)
+            dX, dW = tg.linear_cross_entropy_backward(grad, X, W, y, lse, logits=Z)
+        torch.cuda.synchronize()
+        # the reference's tolerance counts the products of rows that count (the others are cleared in it)
+        assert bool(((Z.double() - ref.z * ref.tau).abs() <= ref.z_off * ref.tau)[ref.counts].all())
+        assert bool((room[:, V:] == 7).all())
+        ref.check_gradients(grad.double(), dX, dW)
+        if not distill:  # for one of the gradients only
+            only = tg.linear_cross_entropy_backward(grad, X, W, y, lse, logits=Z, need=(False, True))
+            assert only[0] is None and torch.equal(only[1], dW)
+            only = tg.linear_cross_entropy_backward(grad, X, W, y, lse, logits=Z, need=(True, False))
+            assert only[1] is None and torch.equal(only[0], dX)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+def test_kept_logits_in_pieces(kind):
+    T, V, D = (8192, 20003, 64) if kind == "bf16" else (4096, 13001, 64)
+    log(f"kept in pieces {kind}")
+    X, W, g = head(T, V, D, TYPES[kind], 15)
+    y, grad = targets(T, V, g), row_grads(T, g)
+    Z = torch.empty((T, V), device="cuda")
+    loss, lse = tg.linear_cross_entropy_forward(X, W, y, logits=Z)
+    kept = tg.linear_cross_entropy_backward(grad, X, W, y, lse, logits=Z)
+    again = tg.linear_cross_entropy_backward(grad, X, W, y, lse)
+    torch.cuda.synchronize()
+    # the same products, the same arithmetic on them
+    assert torch.equal(kept[0], again[0]) and torch.equal(kept[1], again[1])
+
+
+@pytest.mark.parametrize("kind", TYPES)
+@pytest.mark.parametrize("T,V,D", [(12, 900, 64), (200, 900, 256), (40, 300, 1032)])
+def test_differentiable_with_kept_logits(kind, T, V, D):
+    log(f"differentiable, kept {kind} {T}x{V}x{D}")
+    X, W, g = head(T, V, D, TYPES[kind], 16)
+    X, W = X.contiguous().requires_grad_(), W.contiguous().requires_grad_()
+    y = targets(T, V, g)
+    X.data[2] = float("nan")  # a row that does not count
+    ref = Reference(X.detach(), W.detach(), y)
+    one = torch.full((T,), 1.0 / int(ref.counts.sum()), dtype=torch.float64, device="cuda")
+    for keep in (True, False, None):
+        loss = tg.linear_cross_entropy(X, W, y, keep_logits=keep)
+        first = torch.autograd.grad(loss, (X, W), retain_graph=True)
+        second = torch.autograd.grad(loss, (X, W))
+        torch.cuda.synchronize()
+        ref.check_gradients(one, *first)
+        assert torch.equal(first[0], second[0]) and torch.equal(first[1], second[1])
+    ids, top = entries(T, V, 7, TYPES[kind], g)
+    X.data[2] = 0.5
+    ref = Reference(X.detach(), W.detach(), ids=ids, logits=top, temperature=1.5)
+    for keep in (True, False):
+        loss = tg.linear_distillation(X, W, ids, top, temperature=1.5, reduction="sum", keep_logits=keep)
+        ref.check_gradients(torch.ones(T, dtype=torch.float64, device="cuda"), *torch.autograd.grad(loss, (X, W)))
+
+
+def test_kept_logits_and_an_index_out_of_range():
+    X, W, g = head(40, 100, 64, torch.bfloat16, 17)
+    y = torch.randint(0, 100, (40,), generator=g, device="cuda")
+    y[7] = 100
+    Z = torch.empty((40, 100), device="cuda")
+    loss, lse = tg.linear_cross_entropy_forward(X, W, y, logits=Z)
+    dX, dW = tg.linear_cross_entropy_backward(torch.ones(40, device="cuda"), X, W, y, lse, logits=Z)
+    torch.cuda.synchronize()
+    bad = torch.arange(40, device="cuda") == 7
+    assert bool(torch.isnan(loss[bad]).all()) and bool(torch.isnan(dX[bad]).all()) and bool(torch.isnan(dW).all())
+    assert bool(torch.isfinite(loss[~bad]).all()) and bool(torch.isfinite(dX[~bad]).all())
+
+
+def test_a_step_with_kept_logits_captured_and_replayed():
+    log("kept, captured")
+    T, V, D = 150, 2000, 1024
+    X, W, g = head(T, V, D, torch.bfloat16, 18)
+    y, grad = targets(T, V, g), row_grads(T, g)
+    Z = torch.empty((T, V), device="cuda")
+    loss, lse = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    dX, dW = torch.empty_like(X), torch.empty_like(W)
+
+    def step():
+        tg.linear_cross_entropy_forward(X, W, y, loss=loss, lse=lse, logits=Z)
+        tg.linear_cross_entropy_backward(grad, X, W, y, lse, logits=Z, dX=dX, dW=dW)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for n in range(3):
+        X.copy_(torch.randn((T, D), generator=g, device="cuda"))
+        step()
+        torch.cuda.synchronize()
+        want = [t.clone() for t in (loss, lse, dX, dW)]
+        for t in (loss, lse, dX, dW, Z):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for have, t in zip((loss, lse, dX, dW), want):
+            assert torch.equal(have, t)

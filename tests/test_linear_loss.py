@@ -150,3 +150,32 @@ def test_torch_calls_refuse():
         tg.linear_cross_entropy(X, W, y, reduction="average")
     with pytest.raises(ValueError):
         tg.linear_distillation(X, W, y[:, None], X[:, :1], reduction=None)
+    with pytest.raises(ValueError):
+        tg.linear_cross_entropy(X, W, y, keep_logits="yes")
+
+
+KEPT = 1 << 40
+
+
+@pytest.mark.parametrize("entry", EVERY)
+@pytest.mark.parametrize("logits,ldz,status", [(KEPT, 9, INVALID), (KEPT, 0, INVALID), (KEPT, (1 << 40) + 1, UNSUPPORTED),
+                                               (KEPT + 2, 10, INVALID), ((1 << 64) - 64, 10, INVALID), (WS + 256, 10, INVALID)])
+def test_refusals_of_kept_logits(entry, logits, ldz, status, monkeypatch):
+    import functools
+
+    name = f"tgemm_linear_{entry}"
+    monkeypatch.setattr(tg, name, functools.partial(getattr(tg, name), logits=logits, ldz=ldz))
+    assert EVERY[entry]() == status
+
+
+@pytest.mark.parametrize("entry,overlaps", [("ce_forward", (X_, W_, Y_, LOSS, LSE, SUM)), ("ce_backward", (DX, DW)),
+                                            ("kd_forward", (X_, W_, IDS, LOGITS, STUDENT, LOSS, LSE, SUM)),
+                                            ("kd_backward", (DX, DW))])
+def test_kept_logits_overlap_nothing(entry, overlaps, monkeypatch):
+    import functools
+
+    name = f"tgemm_linear_{entry}"
+    call = getattr(tg, name)
+    for at in overlaps:
+        monkeypatch.setattr(tg, name, functools.partial(call, logits=at, ldz=10))
+        assert EVERY[entry]() == INVALID

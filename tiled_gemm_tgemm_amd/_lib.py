@@ -40,6 +40,7 @@ TGEMM_F16 = 2
 _HEAD = [ctypes.c_int, _i64, _i64, _i64, _ptr, _i64, _ptr, _i64]  # dtype, T, V, D, X, ldx, W, ldw
 _TEACHER = [_i64, _ptr, _i64, ctypes.c_int, _ptr, _i64, ctypes.c_float]
 _GRADS = [_ptr, _i64, _ptr, _ptr, _i64, _ptr, _i64]  # grad_loss, grad_step, grad_weight, dX, lddx, dW, lddw
+_KEPT = [_ptr, _i64]  # logits, ldz
 _ROOM = [_ptr, ctypes.c_size_t, _ptr]  # workspace, its bytes, stream
 
 SIGNATURES = {
@@ -64,10 +65,10 @@ SIGNATURES = {
     "tgemm_sgemm_splitk_workspace_size": (ctypes.c_size_t, [_i64, _i64, _i64, ctypes.c_int]),
     "tgemm_sgemm_splitk_choose": (ctypes.c_int, [_i64, _i64, _i64]),
     "tgemm_linear_loss_workspace_size": (ctypes.c_size_t, _HEAD + [_i64, ctypes.c_int]),
-    "tgemm_linear_ce_forward": (ctypes.c_int, _HEAD + [_ptr, _i64] + [_ptr] * 3 + _ROOM),
-    "tgemm_linear_ce_backward": (ctypes.c_int, _HEAD + [_ptr, _i64, _ptr] + _GRADS + _ROOM),
-    "tgemm_linear_kd_forward": (ctypes.c_int, _HEAD + _TEACHER + [_ptr] * 4 + _ROOM),
-    "tgemm_linear_kd_backward": (ctypes.c_int, _HEAD + _TEACHER + [_ptr] * 2 + _GRADS + _ROOM),
+    "tgemm_linear_ce_forward": (ctypes.c_int, _HEAD + [_ptr, _i64] + [_ptr] * 2 + _KEPT + [_ptr] + _ROOM),
+    "tgemm_linear_ce_backward": (ctypes.c_int, _HEAD + [_ptr, _i64, _ptr] + _KEPT + _GRADS + _ROOM),
+    "tgemm_linear_kd_forward": (ctypes.c_int, _HEAD + _TEACHER + [_ptr] * 3 + _KEPT + [_ptr] + _ROOM),
+    "tgemm_linear_kd_backward": (ctypes.c_int, _HEAD + _TEACHER + [_ptr] * 2 + _KEPT + _GRADS + _ROOM),
     "tgemm_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "tgemm_version": (ctypes.c_int, []),
 }
@@ -174,33 +175,34 @@ def tgemm_linear_loss_workspace_size(dtype, T, V, D, X, ldx, W, ldw, teacher_k=0
 
 
 def tgemm_linear_ce_forward(dtype, T, V, D, X, ldx, W, ldw, target, ignore_index, loss, lse, summary, workspace,
-                            workspace_bytes, stream=None) -> int:
-    return library().tgemm_linear_ce_forward(dtype, T, V, D, X, ldx, W, ldw, target, ignore_index, loss, lse, summary,
-                                             workspace, workspace_bytes, stream)
+                            workspace_bytes, stream=None, logits=0, ldz=0) -> int:
+    return library().tgemm_linear_ce_forward(dtype, T, V, D, X, ldx, W, ldw, target, ignore_index, loss, lse, logits,
+                                             ldz, summary, workspace, workspace_bytes, stream)
 
 
 def tgemm_linear_ce_backward(dtype, T, V, D, X, ldx, W, ldw, target, ignore_index, lse, grad_loss, grad_step,
-                             grad_weight, dX, lddx, dW, lddw, workspace, workspace_bytes, stream=None) -> int:
-    return library().tgemm_linear_ce_backward(dtype, T, V, D, X, ldx, W, ldw, target, ignore_index, lse, grad_loss,
-                                              grad_step, grad_weight, dX, lddx, dW, lddw, workspace, workspace_bytes,
-                                              stream)
+                             grad_weight, dX, lddx, dW, lddw, workspace, workspace_bytes, stream=None, logits=0,
+                             ldz=0) -> int:
+    return library().tgemm_linear_ce_backward(dtype, T, V, D, X, ldx, W, ldw, target, ignore_index, lse, logits, ldz,
+                                              grad_loss, grad_step, grad_weight, dX, lddx, dW, lddw, workspace,
+                                              workspace_bytes, stream)
 
 
 def tgemm_linear_kd_forward(dtype, T, V, D, X, ldx, W, ldw, K, teacher_ids, ld_ids, teacher_dtype, teacher_logits,
                             ld_logits, temperature, loss, lse, student, summary, workspace, workspace_bytes,
-                            stream=None) -> int:
+                            stream=None, logits=0, ldz=0) -> int:
     return library().tgemm_linear_kd_forward(dtype, T, V, D, X, ldx, W, ldw, K, teacher_ids, ld_ids, teacher_dtype,
-                                             teacher_logits, ld_logits, temperature, loss, lse, student, summary,
-                                             workspace, workspace_bytes, stream)
+                                             teacher_logits, ld_logits, temperature, loss, lse, student, logits, ldz,
+                                             summary, workspace, workspace_bytes, stream)
 
 
 def tgemm_linear_kd_backward(dtype, T, V, D, X, ldx, W, ldw, K, teacher_ids, ld_ids, teacher_dtype, teacher_logits,
                              ld_logits, temperature, lse, student, grad_loss, grad_step, grad_weight, dX, lddx, dW,
-                             lddw, workspace, workspace_bytes, stream=None) -> int:
+                             lddw, workspace, workspace_bytes, stream=None, logits=0, ldz=0) -> int:
     return library().tgemm_linear_kd_backward(dtype, T, V, D, X, ldx, W, ldw, K, teacher_ids, ld_ids, teacher_dtype,
-                                              teacher_logits, ld_logits, temperature, lse, student, grad_loss,
-                                              grad_step, grad_weight, dX, lddx, dW, lddw, workspace, workspace_bytes,
-                                              stream)
+                                              teacher_logits, ld_logits, temperature, lse, student, logits, ldz,
+                                              grad_loss, grad_step, grad_weight, dX, lddx, dW, lddw, workspace,
+                                              workspace_bytes, stream)
 
 
 def tgemm_mfma_variant_count() -> int:

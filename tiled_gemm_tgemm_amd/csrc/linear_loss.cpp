@@ -310,6 +310,12 @@ CopyArgs copy_of(const Plan &p, const Head &h, const void *src, int64_t ld, int6
     return c;
 }
 
+// The products that the forward pass may leave for the backward pass.
+struct Logits {
+    float *p = nullptr;
+    int64_t ld = 0;
+};
+
 struct Labels {
     const int64_t *target = nullptr;
     int64_t ignore = 0;
@@ -324,7 +330,7 @@ struct Stored {
 };
 
 tgemm_status_t forward(const Plan &p, const Head &h, const Labels &l, float *loss, float *lse, float *student,
-                       float *summary, void *ws, hipStream_t stream)
+                       const Logits &z, float *summary, void *ws, hipStream_t stream)
 {
     hipError_t e = hipSuccess;
     Stored x{h.X, h.ldx, 0}, w{h.W, h.ldw, 0};
@@ -354,6 +360,8 @@ tgemm_status_t forward(const Plan &p, const Head &h, const Labels &l, float *los
     s.groups = p.groups;
     s.target = l.target;
     s.picked = in<float>(ws, p.picked);
+    s.logits = z.p;
+    s.ldz = z.ld;
     if (l.teacher != nullptr) {
         const SortArgs k{h.T, h.V, p.groups, p.group_columns, *l.teacher, in<uint16_t>(ws, p.starts),
                          in<uint32_t>(ws, p.list), student};
@@ -372,8 +380,8 @@ tgemm_status_t forward(const Plan &p, const Head &h, const Labels &l, float *los
 }
 
 tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const float *grad, int64_t grad_step,
-                        const float *weight, const float *lse, const float *student, void *dX, int64_t lddx, void *dW, int64_t lddw, void *ws,
-                        hipStream_t stream)
+                        const float *weight, const float *lse, const float *student, const Logits &z, void *dX, int64_t lddx,
+                        void *dW, int64_t lddw, void *ws, hipStream_t stream)
 {
     // d loss / d (x·w) = grad·(1/τ)·τ² (p - q) for distillation
     const float scale = l.teacher ? l.teacher->scale : 1.0f;
@@ -419,12 +427,12 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
     const Stored cleared{xs, p.Dp, p.planes > 1 ? p.Tp * p.Dp : 0};
     Stored x = cleared, w{h.W, h.ldw, 0};
     if (p.half) x = Stored{h.X, h.ldx, 0};
-    if (p.copy_x) {
+    if (p.copy_x && z.p == nullptr) {
         x = Stored{in<void>(ws, p.x), p.Dp, h.T * p.Dp};
         e = launch_copy(copy_of(p, h, h.X, h.ldx, h.T, in<void>(ws, p.x), h.T), stream);
         if (e != hipSuccess) return from_hip(e);
     }
-    if (p.copy_w) {
+    if (p.copy_w && (z.p == nullptr || dX != nullptr)) {
         w = Stored{in<void>(ws, p.w), p.Dp, p.planes > 1 ? h.V * p.Dp : 0};
         e = launch_copy(copy_of(p, h, h.W, h.ldw, h.V, in<void>(ws, p.w), h.V), stream);
         if (e != hipSuccess) return from_hip(e);
@@ -459,7 +467,7 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
         a.ldg = p.ldg;
         a.plane = plane_g;
         a.planes = p.g_planes;
-        e = launch_grad(p.half, p.grad_tile, a, stream);
+        e = z.p ? launch_grad_kept(p.half, a, z.p + v0, z.ld, stream) : launch_grad(p.half, p.grad_tile, a, stream);
         if (e != hipSuccess) return from_hip(e);
         if (l.teacher != nullptr) {
             ScatterArgs s{h.T, v0, cols, *l.teacher, student, lse, c.coef, g, p.ldg, plane_g, p.g_planes, p.half};
@@ -547,6 +555,13 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
     return TGEMM_SUCCESS;
 }
 
+// The kept products' rows.
+tgemm_status_t check_kept(const Head &h, const float *logits, int64_t ldz)
+{
+    if (logits == nullptr) return TGEMM_SUCCESS;
+    return ldz < h.V ? TGEMM_ERROR_INVALID_VALUE : ldz > kMaxLd ? TGEMM_ERROR_NOT_SUPPORTED : TGEMM_SUCCESS;
+}
+
 tgemm_status_t no_rows(float *summary, hipStream_t stream)
 {
     Range r;
@@ -580,97 +595,109 @@ size_t tgemm_linear_loss_workspace_size(tgemm_dtype_t dtype, int64_t T, int64_t 
 
 tgemm_status_t tgemm_linear_ce_forward(tgemm_dtype_t dtype, int64_t T, int64_t V, int64_t D, const void *X, int64_t ldx,
                                        const void *W, int64_t ldw, const int64_t *target, int64_t ignore_index,
-                                       float *loss, float *lse, float *summary, void *workspace, size_t workspace_bytes,
-                                       hipStream_t stream)
+                                       float *loss, float *lse, float *logits, int64_t ldz, float *summary,
+                                       void *workspace, size_t workspace_bytes, hipStream_t stream)
 {
     const Head h{dtype, T, V, D, X, ldx, W, ldw};
-    const tgemm_status_t st = check_head(h);
+    tgemm_status_t st = check_head(h);
+    if (st == TGEMM_SUCCESS) st = check_kept(h, logits, ldz);
     if (st != TGEMM_SUCCESS) return st;
     if (T == 0) return no_rows(summary, stream);
     Plan p;
     if (!plan_forward(p, h, 0)) return TGEMM_ERROR_NOT_SUPPORTED;
-    Range r[3], w[4];
+    const Logits z{logits, ldz};
+    Range r[3], w[5];
     if (!at(X, T, D, ldx, size_of(dtype), r[0]) || !at(W, V, D, ldw, size_of(dtype), r[1]) ||
         !at(target, T, 1, 1, 8, r[2]) || !at(loss, T, 1, 1, 4, w[0]) || !at(lse, T, 1, 1, 4, w[1]) ||
-        !at(summary, summary ? 1 : 0, 3, 3, 4, w[2]) || !room_at(workspace, workspace_bytes, p, w[3]) || !disjoint(w, 4, r, 3))
+        !at(summary, summary ? 1 : 0, 3, 3, 4, w[2]) || !room_at(workspace, workspace_bytes, p, w[3]) ||
+        !at(logits, logits ? T : 0, V, ldz, 4, w[4]) || !disjoint(w, 5, r, 3))
         return TGEMM_ERROR_INVALID_VALUE;
-    return forward(p, h, Labels{target, ignore_index, nullptr}, loss, lse, nullptr, summary, workspace, stream);
+    return forward(p, h, Labels{target, ignore_index, nullptr}, loss, lse, nullptr, z, summary, workspace, stream);
 }
 
 tgemm_status_t tgemm_linear_ce_backward(tgemm_dtype_t dtype, int64_t T, int64_t V, int64_t D, const void *X, int64_t ldx,
                                         const void *W, int64_t ldw, const int64_t *target, int64_t ignore_index,
-                                        const float *lse, const float *grad_loss, int64_t grad_step, const float *grad_weight,
-                                        void *dX, int64_t lddx, void *dW, int64_t lddw, void *workspace, size_t workspace_bytes, hipStream_t stream)
+                                        const float *lse, const float *logits, int64_t ldz,
+                                        const float *grad_loss, int64_t grad_step, const float *grad_weight,
+                                        void *dX, int64_t lddx, void *dW, int64_t lddw,
+                                        void *workspace, size_t workspace_bytes, hipStream_t stream)
 {
     const Head h{dtype, T, V, D, X, ldx, W, ldw};
     tgemm_status_t st = check_head(h);
+    if (st == TGEMM_SUCCESS) st = check_kept(h, logits, ldz);
     if (st != TGEMM_SUCCESS) return st;
     if (grad_step < 0 || (dX != nullptr && lddx < D) || (dW != nullptr && lddw < D)) return TGEMM_ERROR_INVALID_VALUE;
     if (lddx > kMaxLd || lddw > kMaxLd || grad_step > kMaxLd) return TGEMM_ERROR_NOT_SUPPORTED;
     if (dX == nullptr && dW == nullptr) return TGEMM_SUCCESS;
     Plan p;
     if (T > 0 && !plan_backward(p, h)) return TGEMM_ERROR_NOT_SUPPORTED;
-    Range r[6], w[3];
+    const Logits z{const_cast<float *>(logits), ldz};
+    Range r[7], w[3];
     if (!at(X, T, D, ldx, size_of(dtype), r[0]) || !at(W, T == 0 ? 0 : V, D, ldw, size_of(dtype), r[1]) ||
         !at(target, T, 1, 1, 8, r[2]) || !at(lse, T, 1, 1, 4, r[3]) || !at(grad_loss, T, 1, grad_step, 4, r[4]) || !at(grad_weight, T && grad_weight ? 1 : 0, 1, 1, 4, r[5]) ||
         !at(dX, dX ? T : 0, D, lddx, size_of(dtype), w[0]) || !at(dW, dW ? V : 0, D, lddw, size_of(dtype), w[1]) ||
-        !room_at(workspace, workspace_bytes, p, w[2]) || !disjoint(w, 3, r, 6))
+        !room_at(workspace, workspace_bytes, p, w[2]) || !at(logits, logits ? T : 0, V, ldz, 4, r[6]) || !disjoint(w, 3, r, 7))
         return TGEMM_ERROR_INVALID_VALUE;
     if (T == 0) return dW ? from_hip(launch_zero(dW, lddw, dtype, V, D, stream)) : TGEMM_SUCCESS;
-    return backward(p, h, Labels{target, ignore_index, nullptr}, grad_loss, grad_step, grad_weight, lse, nullptr, dX, lddx, dW, lddw, workspace,
-                    stream);
+    return backward(p, h, Labels{target, ignore_index, nullptr}, grad_loss, grad_step, grad_weight, lse, nullptr, z, dX, lddx, dW, lddw,
+                    workspace, stream);
 }
 
 tgemm_status_t tgemm_linear_kd_forward(tgemm_dtype_t dtype, int64_t T, int64_t V, int64_t D, const void *X, int64_t ldx,
                                        const void *W, int64_t ldw, int64_t K, const int64_t *teacher_ids,
                                        int64_t ld_ids, tgemm_dtype_t teacher_dtype, const void *teacher_logits,
                                        int64_t ld_logits, float temperature, float *loss, float *lse, float *student,
-                                       float *summary, void *workspace, size_t workspace_bytes, hipStream_t stream)
+                                       float *logits, int64_t ldz, float *summary, void *workspace, size_t workspace_bytes, hipStream_t stream)
 {
     const Head h{dtype, T, V, D, X, ldx, W, ldw};
     tgemm_status_t st = check_head(h);
     if (st == TGEMM_SUCCESS) st = check_teacher(h, K, ld_ids, teacher_dtype, ld_logits, temperature);
+    if (st == TGEMM_SUCCESS) st = check_kept(h, logits, ldz);
     if (st != TGEMM_SUCCESS) return st;
     if (T == 0) return no_rows(summary, stream);
     Plan p;
     if (!plan_forward(p, h, K)) return TGEMM_ERROR_NOT_SUPPORTED;
-    Range r[4], w[5];
+    const Logits z{logits, ldz};
+    Range r[4], w[6];
     if (!at(X, T, D, ldx, size_of(dtype), r[0]) || !at(W, V, D, ldw, size_of(dtype), r[1]) ||
         !at(teacher_ids, T, K, ld_ids, 8, r[2]) || !at(teacher_logits, T, K, ld_logits, size_of(teacher_dtype), r[3]) ||
         !at(loss, T, 1, 1, 4, w[0]) || !at(lse, T, 1, 1, 4, w[1]) || !at(student, T, K, K, 4, w[2]) ||
-        !at(summary, summary ? 1 : 0, 3, 3, 4, w[3]) || !room_at(workspace, workspace_bytes, p, w[4]) || !disjoint(w, 5, r, 4))
+        !at(summary, summary ? 1 : 0, 3, 3, 4, w[3]) || !room_at(workspace, workspace_bytes, p, w[4]) ||
+        !at(logits, logits ? T : 0, V, ldz, 4, w[5]) || !disjoint(w, 6, r, 4))
         return TGEMM_ERROR_INVALID_VALUE;
     const Teacher t{(int)K, teacher_ids, ld_ids, teacher_logits, ld_logits, teacher_dtype, 1.0f / temperature};
-    return forward(p, h, Labels{nullptr, 0, &t}, loss, lse, student, summary, workspace, stream);
+    return forward(p, h, Labels{nullptr, 0, &t}, loss, lse, student, z, summary, workspace, stream);
 }
 
 tgemm_status_t tgemm_linear_kd_backward(tgemm_dtype_t dtype, int64_t T, int64_t V, int64_t D, const void *X, int64_t ldx,
                                         const void *W, int64_t ldw, int64_t K, const int64_t *teacher_ids,
                                         int64_t ld_ids, tgemm_dtype_t teacher_dtype, const void *teacher_logits,
                                         int64_t ld_logits, float temperature, const float *lse, const float *student,
-                                        const float *grad_loss, int64_t grad_step, const float *grad_weight, void *dX,
+                                        const float *logits, int64_t ldz, const float *grad_loss, int64_t grad_step, const float *grad_weight, void *dX,
                                         int64_t lddx, void *dW, int64_t lddw,
                                         void *workspace, size_t workspace_bytes, hipStream_t stream)
 {
     const Head h{dtype, T, V, D, X, ldx, W, ldw};
     tgemm_status_t st = check_head(h);
     if (st == TGEMM_SUCCESS) st = check_teacher(h, K, ld_ids, teacher_dtype, ld_logits, temperature);
+    if (st == TGEMM_SUCCESS) st = check_kept(h, logits, ldz);
     if (st != TGEMM_SUCCESS) return st;
     if (grad_step < 0 || (dX != nullptr && lddx < D) || (dW != nullptr && lddw < D)) return TGEMM_ERROR_INVALID_VALUE;
     if (lddx > kMaxLd || lddw > kMaxLd || grad_step > kMaxLd) return TGEMM_ERROR_NOT_SUPPORTED;
     if (dX == nullptr && dW == nullptr) return TGEMM_SUCCESS;
     Plan p;
     if (T > 0 && !plan_backward(p, h)) return TGEMM_ERROR_NOT_SUPPORTED;
-    Range r[8], w[3];
+    const Logits z{const_cast<float *>(logits), ldz};
+    Range r[9], w[3];
     if (!at(X, T, D, ldx, size_of(dtype), r[0]) || !at(W, T == 0 ? 0 : V, D, ldw, size_of(dtype), r[1]) ||
         !at(teacher_ids, T, K, ld_ids, 8, r[2]) || !at(teacher_logits, T, K, ld_logits, size_of(teacher_dtype), r[3]) ||
         !at(lse, T, 1, 1, 4, r[4]) || !at(student, T, K, K, 4, r[5]) || !at(grad_loss, T, 1, grad_step, 4, r[6]) || !at(grad_weight, T && grad_weight ? 1 : 0, 1, 1, 4, r[7]) ||
         !at(dX, dX ? T : 0, D, lddx, size_of(dtype), w[0]) || !at(dW, dW ? V : 0, D, lddw, size_of(dtype), w[1]) ||
-        !room_at(workspace, workspace_bytes, p, w[2]) || !disjoint(w, 3, r, 8))
+        !room_at(workspace, workspace_bytes, p, w[2]) || !at(logits, logits ? T : 0, V, ldz, 4, r[8]) || !disjoint(w, 3, r, 9))
         return TGEMM_ERROR_INVALID_VALUE;
     if (T == 0) return dW ? from_hip(launch_zero(dW, lddw, dtype, V, D, stream)) : TGEMM_SUCCESS;
     const Teacher t{(int)K, teacher_ids, ld_ids, teacher_logits, ld_logits, teacher_dtype, 1.0f / temperature};
-    return backward(p, h, Labels{nullptr, 0, &t}, grad_loss, grad_step, grad_weight, lse, student, dX, lddx, dW, lddw, workspace, stream);
+    return backward(p, h, Labels{nullptr, 0, &t}, grad_loss, grad_step, grad_weight, lse, student, z, dX, lddx, dW, lddw, workspace, stream);
 }
 
 }  // extern "C"

@@ -47,6 +47,8 @@ struct StatsArgs {
     const uint32_t *list;
     int K;
     float *student;
+    float *logits;  // or NULL: the products, before the scale, rows ldz apart
+    int64_t ldz;
 };
 hipError_t launch_stats(bool half, int tile, const StatsArgs &a, hipStream_t stream);
 
@@ -75,6 +77,10 @@ struct GradArgs {
     int planes;
 };
 hipError_t launch_grad(bool half, int tile, const GradArgs &a, hipStream_t stream);
+
+// The same from the products that launch_stats kept: a.op is not used but for
+// M (T) and N (columns), and a.rows rows of whole 64 columns are written.
+hipError_t launch_grad_kept(bool half, const GradArgs &a, const float *logits, int64_t ldz, hipStream_t stream);
 
 // C = A·B with A = G as stored (dX) or transposed (dW), B MN-contiguous.
 struct OutArgs {

@@ -175,6 +175,12 @@ __global__ __launch_bounds__(64 * C * S) void linear_few_kernel(StatsArgs a, int
     for (int i = 0; i < R; ++i) {
         const int row = 16 * i + l16;
         if (row < a.op.M && part == 0) {
+            if (a.logits != nullptr) {
+                float *to = a.logits + (int64_t)row * a.ldz + col0 + 4 * quarter;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (r < left) to[r] = acc[i][r];
+            }
             if (a.target != nullptr) {
                 const int64_t want = a.target[row] - (col0 + 4 * quarter);
 #pragma unroll

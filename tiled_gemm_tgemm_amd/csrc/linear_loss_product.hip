@@ -19,6 +19,79 @@ constexpr float kLog2e = 1.44269504088896340736f;
 template <class Tile>
 constexpr int kHeld = 4 * Tile::FN;
 
+__device__ __forceinline__ uint32_t pack(__bf16 a, __bf16 b)
+{
+    return (uint32_t)__builtin_bit_cast(uint16_t, a) | (uint32_t)__builtin_bit_cast(uint16_t, b) << 16;
+}
+__device__ __forceinline__ uint32_t pack(_Float16 a, _Float16 b)
+{
+    return (uint32_t)__builtin_bit_cast(uint16_t, a) | (uint32_t)__builtin_bit_cast(uint16_t, b) << 16;
+}
+
+// Device memory takes 16-byte stores at any address.
+typedef uint32_t u32x4_anywhere __attribute__((ext_vector_type(4), aligned(2)));
+typedef f32x4 f32x4_anywhere __attribute__((aligned(4)));
+
+// N (a multiple of 8) adjacent values as 16-bit numbers.
+template <class E, int N>
+__device__ __forceinline__ void store_packed(E *to, const float (&v)[N])
+{
+#pragma unroll
+    for (int q = 0; q < N / 8; ++q) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = pack((E)v[8 * q + 2 * e], (E)v[8 * q + 2 * e + 1]);
+        reinterpret_cast<u32x4_anywhere *>(to)[q] = u32x4_anywhere{w[0], w[1], w[2], w[3]};
+    }
+}
+
+// N adjacent values of a row of the result, `left` of them inside it.
+template <class T, int N>
+__device__ __forceinline__ void store_row(T *to, const float (&v)[N], int left)
+{
+    if (left >= N) {
+        if constexpr (sizeof(T) == 2) {
+            store_packed<T, N>(to, v);
+        } else {
+#pragma unroll
+            for (int q = 0; q < N / 4; ++q) {
+                f32x4 w;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = v[4 * q + e];
+                reinterpret_cast<f32x4_anywhere *>(to)[q] = w;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (e < left) to[e] = (T)v[e];
+    }
+}
+
+// The four lanes that share a row (16 apart) exchange their four times four
+// columns, so that what they store at once lies side by side: lane q's v[j]
+// becomes lane j's v[q].
+__device__ __forceinline__ void turn(f32x4 (&v)[4])
+{
+    auto word = [](float f) { return __builtin_bit_cast(uint32_t, f); };
+    auto value = [](uint32_t w) { return __builtin_bit_cast(float, w); };
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {  // lanes 2, 3 of one and 0, 1 of the other
+            const auto r = __builtin_amdgcn_permlane32_swap(word(v[j][e]), word(v[j + 2][e]), false, false);
+            v[j][e] = value(r[0]);
+            v[j + 2][e] = value(r[1]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {  // lanes 1, 3 of one and 0, 2 of the other
+            const auto r = __builtin_amdgcn_permlane16_swap(word(v[j][e]), word(v[j + 1][e]), false, false);
+            v[j][e] = value(r[0]);
+            v[j + 1][e] = value(r[1]);
+        }
+    }
+}
+
 // Columns past the last of the vocabulary do not count.  A row's maximum and
 // sum take the lane's own values and two exchanges with the three lanes that
 // hold the rest of the row.
@@ -55,6 +128,23 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_stats_kernel(StatsArgs a)
     Tile::run(a.op, (lds_char *)lds, prologue, [&](typename Tile::Acc &acc, int row0, int col0, int, const Ahead &ahead) {
         const int lane = m16::thread_anew() & 63, l16 = lane & 15, quarter = lane >> 4;
         const int left = a.op.N - (col0 + H * quarter);  // this lane's columns that exist
+        if (a.logits != nullptr) {
+#pragma unroll
+            for (int i = 0; i < Tile::FM; ++i) {
+                const int row = row0 + i * 16 + l16;
+                f32x4 v[Tile::FN];
+#pragma unroll
+                for (int j = 0; j < Tile::FN; ++j) v[j] = acc[i][j];
+                if constexpr (Tile::FN == 4) turn(v);
+                if (row >= a.op.M) continue;
+#pragma unroll
+                for (int j = 0; j < Tile::FN; ++j) {
+                    const int col = col0 + (Tile::FN == 4 ? 16 * j + 4 * quarter : H * quarter + 4 * j);
+                    const float one[4] = {v[j][0], v[j][1], v[j][2], v[j][3]};
+                    store_row<float, 4>(a.logits + (int64_t)row * a.ldz + col, one, a.op.N - col);
+                }
+            }
+        }
         if (a.op.N - col0 < Tile::FN * 16) {
 #pragma unroll
             for (int i = 0; i < Tile::FM; ++i)
@@ -128,32 +218,6 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_stats_kernel(StatsArgs a)
             }
         }
     });
-}
-
-__device__ __forceinline__ uint32_t pack(__bf16 a, __bf16 b)
-{
-    return (uint32_t)__builtin_bit_cast(uint16_t, a) | (uint32_t)__builtin_bit_cast(uint16_t, b) << 16;
-}
-__device__ __forceinline__ uint32_t pack(_Float16 a, _Float16 b)
-{
-    return (uint32_t)__builtin_bit_cast(uint16_t, a) | (uint32_t)__builtin_bit_cast(uint16_t, b) << 16;
-}
-
-// Device memory takes 16-byte stores at any address.
-typedef uint32_t u32x4_anywhere __attribute__((ext_vector_type(4), aligned(2)));
-typedef f32x4 f32x4_anywhere __attribute__((aligned(4)));
-
-// N (a multiple of 8) adjacent values as 16-bit numbers.
-template <class E, int N>
-__device__ __forceinline__ void store_packed(E *to, const float (&v)[N])
-{
-#pragma unroll
-    for (int q = 0; q < N / 8; ++q) {
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = pack((E)v[8 * q + 2 * e], (E)v[8 * q + 2 * e + 1]);
-        reinterpret_cast<u32x4_anywhere *>(to)[q] = u32x4_anywhere{w[0], w[1], w[2], w[3]};
-    }
 }
 
 template <class E, int BM, int BN, int WM, int WN>
@@ -234,29 +298,6 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_grad_kernel(GradArgs a)
     });
 }
 
-// N adjacent values of a row of the result, `left` of them inside it.
-template <class T, int N>
-__device__ __forceinline__ void store_row(T *to, const float (&v)[N], int left)
-{
-    if (left >= N) {
-        if constexpr (sizeof(T) == 2) {
-            store_packed<T, N>(to, v);
-        } else {
-#pragma unroll
-            for (int q = 0; q < N / 4; ++q) {
-                f32x4 w;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = v[4 * q + e];
-                reinterpret_cast<f32x4_anywhere *>(to)[q] = w;
-            }
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-            if (e < left) to[e] = (T)v[e];
-    }
-}
-
 template <class E, int BM, int BN, int WM, int WN, bool A_MC>
 __global__ __launch_bounds__(64 * WM * WN) void linear_out_kernel(OutArgs a)
 {
@@ -299,6 +340,48 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_out_kernel(OutArgs a)
     });
 }
 
+// Eight columns a thread; a work-group stays in a row.
+template <class E>
+__global__ __launch_bounds__(256) void linear_grad_kept_kernel(GradArgs a, const float *logits, int64_t ldz, int64_t blocks, int per_row)
+{
+    typedef float f32x8 __attribute__((ext_vector_type(8)));
+    typedef f32x8 f32x8_anywhere __attribute__((aligned(4)));
+    const int whole = (a.op.N + 63) / 64 * 64;
+    const float scale2 = a.scale * kLog2e;
+    for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
+        const int row = (int)(b / per_row), col = (int)(b % per_row) * 2048 + threadIdx.x * 8;
+        if (col >= whole) continue;
+        const float c = row < a.op.M ? a.coef[row] : 0.0f;
+        float g[8] = {};
+        if (c != 0.0f) {  // a row that does not count is zero whatever its logits are
+            const float lse = c == c ? a.lse[row] : c, lse2 = lse * kLog2e;
+            const int64_t y = a.target != nullptr ? a.target[row] - a.v0 - col : -1;
+            const float *from = logits + row * ldz + col;
+            f32x8 z{};
+            if (col + 8 <= a.op.N) {
+                z = *(const f32x8_anywhere *)from;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (col + e < a.op.N) z[e] = from[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float x = a.planes == 1 ? fmaf(z[e], scale2, -lse2) : fmaf(z[e], a.scale, -lse) * kLog2e;
+                float p = __builtin_amdgcn_exp2f(x);
+                if (e == y) p -= 1.0f;
+                g[e] = col + e < a.op.N ? m16::mul_zero(c, p) : 0.0f;
+            }
+        }
+        E *to = (E *)a.G + (int64_t)row * a.ldg + col;
+        for (int q = 0; q < a.planes; ++q) {
+            store_packed<E, 8>(to + q * a.plane, g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] -= (float)(E)g[e];
+        }
+    }
+}
+
 // As many work-groups as the GPU holds at once (a multiple of 8, so that a
 // work-group's tiles stay on its XCD).
 template <class Args>
@@ -336,6 +419,16 @@ hipError_t launch_grad(bool half, int tile, const GradArgs &a, hipStream_t strea
         TGEMM_TILES(X)
 #undef X
     }
+    return hipGetLastError();
+}
+
+hipError_t launch_grad_kept(bool half, const GradArgs &a, const float *logits, int64_t ldz, hipStream_t stream)
+{
+    const int per_row = (a.op.N + 2047) / 2048;
+    const int64_t blocks = (int64_t)a.rows * per_row;
+    const unsigned grid = (unsigned)(blocks < (1 << 20) ? blocks : 1 << 20);
+    if (half) linear_grad_kept_kernel<_Float16><<<grid, 256, 0, stream>>>(a, logits, ldz, blocks, per_row);
+    else linear_grad_kept_kernel<__bf16><<<grid, 256, 0, stream>>>(a, logits, ldz, blocks, per_row);
     return hipGetLastError();
 }
 

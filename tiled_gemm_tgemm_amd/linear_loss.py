@@ -24,6 +24,16 @@ from ._lib import TgemmError
 
 REDUCTIONS = ("mean", "sum", "none")
 
+# The differentiable calls keep the logits for the backward pass, in float32, up to KEPT_BYTES of them.  Writing and
+# reading them takes longer than forming them again (six times the products for float32 operands) below an inner size
+# of about KEPT_WIDTH: a bf16 step of 4096×32768 takes 614 µs (formed again) against 737 (kept) with 512, 1030 against
+# 1006 with 1024, 1778 against 1579 with 2048 and 3289 against 2722 with 4096; a float32 one 1225 against 1321 with 128
+# and 1774 against 1692 with 200.  A few that stay in the caches are always worth keeping (KEPT_ALWAYS): 45 against 41
+# µs for 33×8192 and 43 against 41 for 261×1855, both with 64.
+KEPT_BYTES = 8 << 30
+KEPT_ALWAYS = 4 << 20
+KEPT_WIDTH = 1024
+
 
 @functools.lru_cache(maxsize=None)
 def _types():
@@ -137,6 +147,21 @@ class _Call:
 
         return self.new(shape, torch.float32) if t is None else _floats(t, name, shape, self.device)
 
+    def logits(self, t):
+        """The address and leading dimension of the logits' room, or none."""
+        import torch
+
+        return (0, 0) if t is None else (t.data_ptr(), _rows(t, "logits", (self.T, self.V), self.device, torch.float32))
+
+    def keep(self, keep):
+        """Room for the logits between the two passes of a differentiable call; None to have them formed again."""
+        import torch
+
+        if keep is None:
+            size, width = 4 * self.T * self.V, self.D * (6 if self.dtype == torch.float32 else 1)
+            keep = size <= (KEPT_BYTES if width >= KEPT_WIDTH else KEPT_ALWAYS)
+        return torch.empty((self.T, self.V), dtype=torch.float32, device=self.device) if keep else None
+
     def gradient(self, t, name, shape):
         if t is None:
             return self.new(shape, self.dtype), shape[1]
@@ -185,16 +210,18 @@ def _ptr(t):
     return 0 if t is None else t.data_ptr()
 
 
-def linear_cross_entropy_forward(X, W, target, *, ignore_index=-100, loss=None, lse=None, workspace=None, stream=None):
+def linear_cross_entropy_forward(X, W, target, *, ignore_index=-100, loss=None, lse=None, logits=None, workspace=None,
+                                 stream=None):
     """(loss, lse) of the rows (tgemm_linear_ce_forward): lse_t = log sum_v exp(x_t·w_v), loss_t = lse_t - x_t·w_y
     with y = target_t (int64), 0 where y is ignore_index and NaN where y is outside the vocabulary otherwise.  loss
-    and lse: float32 tensors of T to write to; workspace: a CUDA uint8 tensor of at least
+    and lse: float32 tensors of T to write to; logits: a row-major float32 tensor of T×V to leave the logits in, for
+    the backward call (not written if omitted); workspace: a CUDA uint8 tensor of at least
     tgemm_linear_loss_workspace_size bytes (allocated if omitted; two calls in flight at once need two)."""
     c = _Call(X, W, stream)
     target = c.target(target)
     loss, lse = c.floats(loss, "loss", (c.T,)), c.floats(lse, "lse", (c.T,))
-    c.queue("tgemm_linear_ce_forward", target.data_ptr(), int(ignore_index), loss.data_ptr(), lse.data_ptr(), 0,
-            *c.room(workspace, 0, 0))
+    c.queue("tgemm_linear_ce_forward", target.data_ptr(), int(ignore_index), loss.data_ptr(), lse.data_ptr(),
+            *c.logits(logits), 0, *c.room(workspace, 0, 0))
     return loss, lse
 
 
@@ -215,58 +242,61 @@ def _grad_loss(c, grad):
     return grad.data_ptr(), grad.stride(0) if grad.dim() and c.T > 1 else 0
 
 
-def _ce_backward(c, grad_loss, weight, target, lse, ignore_index, dX, dW, need, workspace):
-    """target checked; weight and lse: addresses"""
+def _ce_backward(c, grad_loss, weight, target, lse, logits, ignore_index, dX, dW, need, workspace):
+    """target checked; weight and lse: addresses; logits as _Call.logits gave it"""
     dX, dW, outs = _gradients(c, dX, dW, need)
-    c.queue("tgemm_linear_ce_backward", target.data_ptr(), int(ignore_index), lse, *_grad_loss(c, grad_loss), weight, *outs,
+    c.queue("tgemm_linear_ce_backward", target.data_ptr(), int(ignore_index), lse, *logits,
+            *_grad_loss(c, grad_loss), weight, *outs,
             *c.room(workspace, 0, 1))
     return dX, dW
 
 
-def linear_cross_entropy_backward(grad_loss, X, W, target, lse, *, ignore_index=-100, dX=None, dW=None,
+def linear_cross_entropy_backward(grad_loss, X, W, target, lse, *, ignore_index=-100, logits=None, dX=None, dW=None,
                                   need=(True, True), workspace=None, stream=None):
     """(dX, dW) = the gradients of sum_t grad_loss_t·loss_t (tgemm_linear_ce_backward).  grad_loss: float32, one
-    value a row or one of no dimension for all; lse as linear_cross_entropy_forward gave it.  dX, dW: row-major
-    tensors to write to; need: which of the two are computed (None is returned for the other)."""
+    value a row or one of no dimension for all; lse, and logits if it left them, as linear_cross_entropy_forward gave
+    them (without logits they are formed again).  dX, dW: row-major tensors to write to; need: which of the two are computed (None is returned for the other)."""
     c = _Call(X, W, stream)
     target = c.target(target)
     lse = _floats(lse, "lse", (c.T,), c.device)
-    return _ce_backward(c, grad_loss, 0, target, lse.data_ptr(), ignore_index, dX, dW, need, workspace)
+    return _ce_backward(c, grad_loss, 0, target, lse.data_ptr(), c.logits(logits), ignore_index, dX, dW, need, workspace)
 
 
 def linear_distillation_forward(X, W, teacher_ids, teacher_logits, *, temperature=1.0, loss=None, lse=None,
-                                student=None, workspace=None, stream=None):
+                                student=None, logits=None, workspace=None, stream=None):
     """(loss, lse, student) of the rows (tgemm_linear_kd_forward) for a teacher's top logits: teacher_ids (T×K,
     int64) the words and teacher_logits (T×K, float32, bfloat16 or float16) their logits; an entry with the logit
     -inf is absent.  With q the softmax of a row's logits / temperature over its entries and z the student's logits
     / temperature, loss_t = temperature²·sum_k q_k·(log q_k - (z_k - lse_t)), 0 for a row without entries and NaN
-    where an entry's id is outside the vocabulary.  student: z at the teacher's ids (0 where absent)."""
+    where an entry's id is outside the vocabulary.  student: z at the teacher's ids (0 where absent).  logits: as
+    linear_cross_entropy_forward's, before the division by the temperature."""
     c = _Call(X, W, stream)
     teacher = c.teacher(teacher_ids, teacher_logits, temperature)
     loss, lse = c.floats(loss, "loss", (c.T,)), c.floats(lse, "lse", (c.T,))
     student = c.floats(student, "student", (c.T, c.K))
-    c.queue("tgemm_linear_kd_forward", *teacher, loss.data_ptr(), lse.data_ptr(), student.data_ptr(), 0,
-            *c.room(workspace, c.K, 0))
+    c.queue("tgemm_linear_kd_forward", *teacher, loss.data_ptr(), lse.data_ptr(), student.data_ptr(),
+            *c.logits(logits), 0, *c.room(workspace, c.K, 0))
     return loss, lse, student
 
 
-def _kd_backward(c, grad_loss, weight, teacher, lse, student, dX, dW, need, workspace):
-    """teacher as _Call.teacher gave it; weight, lse and student: addresses"""
+def _kd_backward(c, grad_loss, weight, teacher, lse, student, logits, dX, dW, need, workspace):
+    """teacher and logits as _Call's functions gave them; weight, lse and student: addresses"""
     dX, dW, outs = _gradients(c, dX, dW, need)
-    c.queue("tgemm_linear_kd_backward", *teacher, lse, student, *_grad_loss(c, grad_loss), weight, *outs,
+    c.queue("tgemm_linear_kd_backward", *teacher, lse, student, *logits, *_grad_loss(c, grad_loss), weight, *outs,
             *c.room(workspace, c.K, 1))
     return dX, dW
 
 
 def linear_distillation_backward(grad_loss, X, W, teacher_ids, teacher_logits, lse, student, *, temperature=1.0,
-                                 dX=None, dW=None, need=(True, True), workspace=None, stream=None):
-    """(dX, dW) = the gradients of sum_t grad_loss_t·loss_t (tgemm_linear_kd_backward); lse and student as
-    linear_distillation_forward gave them, the rest as linear_cross_entropy_backward."""
+                                 logits=None, dX=None, dW=None, need=(True, True), workspace=None, stream=None):
+    """(dX, dW) = the gradients of sum_t grad_loss_t·loss_t (tgemm_linear_kd_backward); lse, student and, if it left
+    them, logits as linear_distillation_forward gave them, the rest as linear_cross_entropy_backward."""
     c = _Call(X, W, stream)
     teacher = c.teacher(teacher_ids, teacher_logits, temperature)
     lse = _floats(lse, "lse", (c.T,), c.device)
     student = _floats(student, "student", (c.T, c.K), c.device)
-    return _kd_backward(c, grad_loss, 0, teacher, lse.data_ptr(), student.data_ptr(), dX, dW, need, workspace)
+    return _kd_backward(c, grad_loss, 0, teacher, lse.data_ptr(), student.data_ptr(), c.logits(logits), dX, dW, need,
+                        workspace)
 
 
 @functools.lru_cache(maxsize=None)
@@ -287,65 +317,74 @@ def _functions():
 
     class CrossEntropy(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, X, W, target, ignore_index, reduction):
+        def forward(ctx, X, W, target, ignore_index, reduction, keep):
             c = _Call(X, W, None)
             target = c.target(target)
             kept, at = c.rows_and_summary()
-            c.queue("tgemm_linear_ce_forward", target.data_ptr(), int(ignore_index), *at, *c.room(None, 0, 0))
-            ctx.save_for_backward(X, W, target, kept)
+            logits = c.keep(keep) if any(ctx.needs_input_grad) else None
+            c.queue("tgemm_linear_ce_forward", target.data_ptr(), int(ignore_index), *at[:2], *c.logits(logits), at[2],
+                    *c.room(None, 0, 0))
+            ctx.save_for_backward(X, W, target, kept, logits)
             ctx.call, ctx.ignore_index, ctx.reduction = c, ignore_index, reduction
             return result(c, reduction, kept)
 
         @staticmethod
         @once_differentiable
         def backward(ctx, grad):
-            X, W, target, kept = ctx.saved_tensors
+            X, W, target, kept, logits = ctx.saved_tensors
             weight, lse = addresses(ctx.reduction, kept)
-            dX, dW = _ce_backward(ctx.call.again(X, W), grad, weight, target, lse, ctx.ignore_index, None, None,
+            c = ctx.call.again(X, W)
+            dX, dW = _ce_backward(c, grad, weight, target, lse, c.logits(logits), ctx.ignore_index, None, None,
                                   ctx.needs_input_grad, None)
-            return dX, dW, None, None, None
+            return dX, dW, None, None, None, None
 
     class Distillation(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, X, W, teacher_ids, teacher_logits, temperature, reduction):
+        def forward(ctx, X, W, teacher_ids, teacher_logits, temperature, reduction, keep):
             c = _Call(X, W, None)
             teacher = c.teacher(teacher_ids, teacher_logits, temperature)
             kept, at = c.rows_and_summary()
             student = torch.empty((c.T, c.K), dtype=torch.float32, device=c.device)
-            c.queue("tgemm_linear_kd_forward", *teacher, *at[:2], student.data_ptr(), at[2], *c.room(None, c.K, 0))
-            ctx.save_for_backward(X, W, teacher_ids, teacher_logits, kept, student)
+            logits = c.keep(keep) if any(ctx.needs_input_grad) else None
+            c.queue("tgemm_linear_kd_forward", *teacher, *at[:2], student.data_ptr(), *c.logits(logits), at[2],
+                    *c.room(None, c.K, 0))
+            ctx.save_for_backward(X, W, teacher_ids, teacher_logits, kept, student, logits)
             ctx.call, ctx.temperature, ctx.reduction = c, temperature, reduction
             return result(c, reduction, kept)
 
         @staticmethod
         @once_differentiable
         def backward(ctx, grad):
-            X, W, ids, logits, kept, student = ctx.saved_tensors
+            X, W, ids, top, kept, student, logits = ctx.saved_tensors
             c = ctx.call.again(X, W)
             weight, lse = addresses(ctx.reduction, kept)
-            dX, dW = _kd_backward(c, grad, weight, c.teacher(ids, logits, ctx.temperature), lse, student.data_ptr(), None,
-                                  None, ctx.needs_input_grad, None)
-            return dX, dW, None, None, None, None
+            dX, dW = _kd_backward(c, grad, weight, c.teacher(ids, top, ctx.temperature), lse, student.data_ptr(),
+                                  c.logits(logits), None, None, ctx.needs_input_grad, None)
+            return dX, dW, None, None, None, None, None
 
     return CrossEntropy, Distillation
 
 
-def _check_reduction(reduction):
+def _check_choices(reduction, keep_logits):
     if reduction not in REDUCTIONS:
         raise ValueError(f"reduction must be one of {REDUCTIONS}")
+    if keep_logits not in (None, True, False):
+        raise ValueError("keep_logits must be None, True or False")
 
 
-def linear_cross_entropy(X, W, target, *, ignore_index=-100, reduction="mean"):
-    """The softmax cross entropy of the logits X·Wᵀ against `target`, differentiable in X and W; the logits are never
-    held.  reduction: "mean" over the rows whose target is not ignore_index (0 if there is none), "sum", or "none"
-    for the losses of the rows.  Losses are float32; gradients have the type of X and W."""
-    _check_reduction(reduction)
-    return _functions()[0].apply(X, W, target, ignore_index, reduction)
+def linear_cross_entropy(X, W, target, *, ignore_index=-100, reduction="mean", keep_logits=None):
+    """The softmax cross entropy of the logits X·Wᵀ against `target`, differentiable in X and W.  reduction: "mean"
+    over the rows whose target is not ignore_index (0 if there is none), "sum", or "none" for the losses of the rows.
+    Losses are float32; gradients have the type of X and W.  keep_logits: whether the logits (T×V float32) are held
+    until the backward pass or formed again there; None: held where that is faster and takes at most KEPT_BYTES.
+    Without a gradient to compute they are never held."""
+    _check_choices(reduction, keep_logits)
+    return _functions()[0].apply(X, W, target, ignore_index, reduction, keep_logits)
 
 
-def linear_distillation(X, W, teacher_ids, teacher_logits, *, temperature=1.0, reduction="mean"):
+def linear_distillation(X, W, teacher_ids, teacher_logits, *, temperature=1.0, reduction="mean", keep_logits=None):
     """The distillation loss of the logits X·Wᵀ against a teacher's top logits (linear_distillation_forward),
     differentiable in X and W (the teacher's logits get no gradient).  reduction: "mean" over the rows that have an
-    entry (0 if none has), "sum" or "none"."""
-    _check_reduction(reduction)
-    return _functions()[1].apply(X, W, teacher_ids, teacher_logits, temperature, reduction)
+    entry (0 if none has), "sum" or "none"; keep_logits as linear_cross_entropy's."""
+    _check_choices(reduction, keep_logits)
+    return _functions()[1].apply(X, W, teacher_ids, teacher_logits, temperature, reduction, keep_logits)
