@@ -349,14 +349,17 @@ tgemm_status_t tgemm_sgemm_host(int64_t M, int64_t N, int64_t K,
 int64_t tgemm_sgemm_host_workspace_size(int64_t M, int64_t N, int64_t K, int64_t panel_rows);
 
 /*
- * Losses on the product Z = X·Wᵀ of an output head, without Z
- * -----------------------------------------------------------
+ * Losses on the product Z = X·Wᵀ of an output head
+ * ------------------------------------------------
  * X is T×D (a row a token's hidden state), W is V×D (a row a word of the
  * vocabulary), both row-major with leading dimensions ldx, ldw >= D in
  * elements, of type `dtype` (both the same).  Z is T×V and read by nothing but
- * the loss; it is formed tile by tile in registers, reduced there to a maximum
- * and a sum of exponentials a row, and formed again in the backward pass, a
- * piece of the vocabulary at a time.
+ * the loss; it is formed tile by tile in registers and reduced there to a
+ * maximum and a sum of exponentials a row.  Its memory is the caller's choice:
+ * without `logits` (NULL) it is nowhere held, and formed again in the backward
+ * pass, a piece of the vocabulary at a time; with `logits` (T×V float32, ldz >=
+ * V) the forward call leaves it there, and the backward call reads it from
+ * there (the same array and ldz, unchanged).
  *
  * Types       dtype float32, bf16 or fp16: the type of X, W and their
  *             gradients.  Products of 16-bit values are exact and summed in
@@ -430,8 +433,8 @@ tgemm_status_t tgemm_linear_ce_backward(tgemm_dtype_t dtype, int64_t T, int64_t 
  * dimension ld_ids >= K) and teacher_logits (T×K of teacher_dtype, ld_logits
  * >= K) hold a row's K words and the teacher's logits of them; an entry with
  * the logit -infinity is absent, whatever its id.  With q_t the softmax of the
- * row's logits / temperature over its entries (an id that comes twice holds
- * the sum of both), and z the student's logits / temperature,
+ * row's logits / temperature over its entries (an id that comes twice is
+ * two entries), and z the student's logits / temperature,
  *   loss[t] = temperature²·sum_k q_tk·(log q_tk - (z_t,id - lse[t])),
  * the Kullback-Leibler divergence from the student's whole vocabulary to q.
  * student[t·K + k] receives z_t,id (0 for an absent entry).

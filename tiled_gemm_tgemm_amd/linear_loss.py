@@ -24,15 +24,14 @@ from ._lib import TgemmError
 
 REDUCTIONS = ("mean", "sum", "none")
 
-# The differentiable calls keep the logits for the backward pass, in float32, up to KEPT_BYTES of them.  Writing and
-# reading them takes longer than forming them again (six times the products for float32 operands) below an inner size
-# of about KEPT_WIDTH: a bf16 step of 4096×32768 takes 614 µs (formed again) against 737 (kept) with 512, 1030 against
-# 1006 with 1024, 1778 against 1579 with 2048 and 3289 against 2722 with 4096; a float32 one 1225 against 1321 with 128
-# and 1774 against 1692 with 200.  A few that stay in the caches are always worth keeping (KEPT_ALWAYS): 45 against 41
-# µs for 33×8192 and 43 against 41 for 261×1855, both with 64.
-KEPT_BYTES = 8 << 30
-KEPT_ALWAYS = 4 << 20
-KEPT_WIDTH = 1024
+# Unless told otherwise the differentiable calls form the logits again in the backward pass, and hold them (float32)
+# only where all of them take no more than a piece of their gradient does (256 MiB, which the backward pass holds
+# anyway) and that is faster.  Writing and reading them costs about as much as forming them again does at an inner size
+# (a sixth of it for float32 operands, which take six products) that depends on where they stay meanwhile: (bytes,
+# inner size), one line that both meet is enough.  Formed again against held, µs, a step: 33×8192 with 64 45, 41;
+# 777×20011 with 512 159, 148, with 1000 219, 188; 2048×32000 with 512 306, 368, with 1000 525, 525.  Larger ones, for
+# those who ask for it: 4096×32768 with 2048 1778, 1579, with 4096 3289, 2722.
+KEPT = ((4 << 20, 0), (64 << 20, 512), (256 << 20, 1024))
 
 
 @functools.lru_cache(maxsize=None)
@@ -158,8 +157,8 @@ class _Call:
         import torch
 
         if keep is None:
-            size, width = 4 * self.T * self.V, self.D * (6 if self.dtype == torch.float32 else 1)
-            keep = size <= (KEPT_BYTES if width >= KEPT_WIDTH else KEPT_ALWAYS)
+            size, inner = 4 * self.T * self.V, self.D * (6 if self.dtype == torch.float32 else 1)
+            keep = any(size <= room and inner >= least for room, least in KEPT)
         return torch.empty((self.T, self.V), dtype=torch.float32, device=self.device) if keep else None
 
     def gradient(self, t, name, shape):
@@ -375,9 +374,10 @@ def _check_choices(reduction, keep_logits):
 def linear_cross_entropy(X, W, target, *, ignore_index=-100, reduction="mean", keep_logits=None):
     """The softmax cross entropy of the logits X·Wᵀ against `target`, differentiable in X and W.  reduction: "mean"
     over the rows whose target is not ignore_index (0 if there is none), "sum", or "none" for the losses of the rows.
-    Losses are float32; gradients have the type of X and W.  keep_logits: whether the logits (T×V float32) are held
-    until the backward pass or formed again there; None: held where that is faster and takes at most KEPT_BYTES.
-    Without a gradient to compute they are never held."""
+    Losses are float32; gradients have the type of X and W.  keep_logits: False: the logits are held nowhere and formed
+    again in the backward pass; True: they are held until then (T×V float32), which is faster by up to a fifth where
+    the inner size is large; None: held where that is faster and takes no more than 256 MiB.  Without a gradient to
+    compute they are never held."""
     _check_choices(reduction, keep_logits)
     return _functions()[0].apply(X, W, target, ignore_index, reduction, keep_logits)
 
