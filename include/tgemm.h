@@ -1,5 +1,6 @@
 /*
- * libtgemm — single-precision C = A·B on one AMD Instinct MI355X (gfx950).
+ * libtgemm — single-precision C = A·B on one AMD Instinct MI355X (gfx950), and
+ * two losses on such a product of an output head (declared last).
  *
  * The operation is the dense product of page 1 ("[Multi-Core & GPU
  * Programming] CUDA - Matrix Multiplication", section [Matrix

@@ -3,7 +3,9 @@
 The compute lives in the C-ABI library libtgemm.so (sources in csrc/,
 declarations in include/tgemm.h).  ``_lib`` exposes the C entry points under
 their own names; ``sgemm`` and ``transpose`` below are the same calls for
-torch tensors, with torch used for device memory and the current stream only.
+torch tensors, with torch used for device memory and the current stream only,
+and ``linear_cross_entropy`` and ``linear_distillation`` the losses on an output
+head's product, with their gradients.
 
 Nothing here loads the library at import time; the first call does, and it
 raises if libtgemm.so has not been built (``python -m
