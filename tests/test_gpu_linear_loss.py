@@ -658,3 +658,38 @@ def test_a_step_with_kept_logits_captured_and_replayed():
         torch.cuda.synchronize()
         for have, t in zip((loss, lse, dX, dW), want):
             assert torch.equal(have, t)
+
+
+def peak(call):
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    call()
+    torch.cuda.synchronize()
+    return torch.cuda.max_memory_allocated() - before
+
+
+def test_logits_are_held_only_where_a_gradient_can_come():
+    log("what is held")
+    T, V, D = 1000, 20000, 1024
+    X, W, g = head(T, V, D, torch.bfloat16, 19)
+    X, W = X.contiguous().requires_grad_(), W.contiguous().requires_grad_()
+    y = targets(T, V, g)
+    ids, top = entries(T, V, 4, torch.bfloat16, g)
+    logits = 4 * T * V
+    for call in (lambda **k: tg.linear_cross_entropy(X, W, y, **k), lambda **k: tg.linear_distillation(X, W, ids, top, **k)):
+        assert peak(lambda: call()) > logits
+        assert peak(lambda: call(keep_logits=False)) < logits // 4
+        with torch.no_grad():
+            for keep in (None, True):
+                assert peak(lambda: call(keep_logits=keep)) < logits // 4
+
+
+def test_a_step_holds_a_small_part_of_large_logits():
+    log("peak of a step")
+    T, V, D = 8192, 131072, 64
+    X, W, g = head(T, V, D, torch.bfloat16, 20)
+    X, W = X.contiguous().requires_grad_(), W.contiguous().requires_grad_()
+    y = targets(T, V, g)
+    # a piece of the logits' gradient (256 MiB and a row's padding), sums in float32, statistics
+    assert peak(lambda: torch.autograd.grad(tg.linear_cross_entropy(X, W, y), (X, W))) < 4 * T * V // 8

@@ -364,11 +364,15 @@ def _functions():
     return CrossEntropy, Distillation
 
 
-def _check_choices(reduction, keep_logits):
+def _choices(reduction, keep_logits):
+    """The two, checked; nothing is kept where no backward pass can come (autograd is off within a Function)."""
+    import torch
+
     if reduction not in REDUCTIONS:
         raise ValueError(f"reduction must be one of {REDUCTIONS}")
     if keep_logits not in (None, True, False):
         raise ValueError("keep_logits must be None, True or False")
+    return reduction, keep_logits if torch.is_grad_enabled() else False
 
 
 def linear_cross_entropy(X, W, target, *, ignore_index=-100, reduction="mean", keep_logits=None):
@@ -378,13 +382,11 @@ def linear_cross_entropy(X, W, target, *, ignore_index=-100, reduction="mean", k
     again in the backward pass; True: they are held until then (T×V float32), which is faster by up to a fifth where
     the inner size is large; None: held where that is faster and takes no more than 256 MiB.  Without a gradient to
     compute they are never held."""
-    _check_choices(reduction, keep_logits)
-    return _functions()[0].apply(X, W, target, ignore_index, reduction, keep_logits)
+    return _functions()[0].apply(X, W, target, ignore_index, *_choices(reduction, keep_logits))
 
 
 def linear_distillation(X, W, teacher_ids, teacher_logits, *, temperature=1.0, reduction="mean", keep_logits=None):
     """The distillation loss of the logits X·Wᵀ against a teacher's top logits (linear_distillation_forward),
     differentiable in X and W (the teacher's logits get no gradient).  reduction: "mean" over the rows that have an
     entry (0 if none has), "sum" or "none"; keep_logits as linear_cross_entropy's."""
-    _check_choices(reduction, keep_logits)
-    return _functions()[1].apply(X, W, teacher_ids, teacher_logits, temperature, reduction, keep_logits)
+    return _functions()[1].apply(X, W, teacher_ids, teacher_logits, temperature, *_choices(reduction, keep_logits))
