@@ -205,11 +205,12 @@ bool plan_forward(Plan &p, const Head &h, int64_t teacher_k)
 {
     // The rows of X come from the caches once for every 16 words, which is as
     // much again as W from 16 rows on: tiles take more than 8 rows sooner
-    // where they need no copy of W (17×32000×2048 bf16 31 against 40 µs, one
-    // row 58 against 47), and fewer rows or none where they do (20×32000×1001
-    // bf16 55 against 45 µs, 32 rows 55 against 55; float32 341 against 90).
+    // where they need no copy of W and the vocabulary gives every compute unit
+    // one (µs, tiles against few rows' kernel: 16×32000×2048 bf16 28, 35 and
+    // 16×128256×1024 50, 65; 16×16384×2048 25, 21, 32×8192×512 13, 10 and
+    // 32×5000×4096 39, 28; with a copy 20×32000×1001 55, 45, 32 of them 55, 55).
     const bool stored = as_stored(h.X, h.ldx, h, kStepK) && as_stored(h.W, h.ldw, h);
-    p.few = h.T <= (stored ? 8 : kFewRows);
+    p.few = h.T <= (stored && h.V > kFewBelow ? 8 : kFewRows);
     if (p.few) {
         p.group_columns = few_columns(h.V);
     } else {
@@ -634,20 +635,22 @@ tgemm_status_t tgemm_linear_ce_backward(tgemm_dtype_t dtype, int64_t T, int64_t 
     const Logits z{const_cast<float *>(logits), ldz};
     Range r[7], w[3];
     if (!at(X, T, D, ldx, size_of(dtype), r[0]) || !at(W, T == 0 ? 0 : V, D, ldw, size_of(dtype), r[1]) ||
-        !at(target, T, 1, 1, 8, r[2]) || !at(lse, T, 1, 1, 4, r[3]) || !at(grad_loss, T, 1, grad_step, 4, r[4]) || !at(grad_weight, T && grad_weight ? 1 : 0, 1, 1, 4, r[5]) ||
+        !at(target, T, 1, 1, 8, r[2]) || !at(lse, T, 1, 1, 4, r[3]) ||
+        !at(grad_loss, T, 1, grad_step, 4, r[4]) || !at(grad_weight, T && grad_weight ? 1 : 0, 1, 1, 4, r[5]) ||
         !at(dX, dX ? T : 0, D, lddx, size_of(dtype), w[0]) || !at(dW, dW ? V : 0, D, lddw, size_of(dtype), w[1]) ||
         !room_at(workspace, workspace_bytes, p, w[2]) || !at(logits, logits ? T : 0, V, ldz, 4, r[6]) || !disjoint(w, 3, r, 7))
         return TGEMM_ERROR_INVALID_VALUE;
     if (T == 0) return dW ? from_hip(launch_zero(dW, lddw, dtype, V, D, stream)) : TGEMM_SUCCESS;
-    return backward(p, h, Labels{target, ignore_index, nullptr}, grad_loss, grad_step, grad_weight, lse, nullptr, z, dX, lddx, dW, lddw,
-                    workspace, stream);
+    return backward(p, h, Labels{target, ignore_index, nullptr}, grad_loss, grad_step, grad_weight, lse, nullptr, z, dX,
+                    lddx, dW, lddw, workspace, stream);
 }
 
 tgemm_status_t tgemm_linear_kd_forward(tgemm_dtype_t dtype, int64_t T, int64_t V, int64_t D, const void *X, int64_t ldx,
                                        const void *W, int64_t ldw, int64_t K, const int64_t *teacher_ids,
                                        int64_t ld_ids, tgemm_dtype_t teacher_dtype, const void *teacher_logits,
                                        int64_t ld_logits, float temperature, float *loss, float *lse, float *student,
-                                       float *logits, int64_t ldz, float *summary, void *workspace, size_t workspace_bytes, hipStream_t stream)
+                                       float *logits, int64_t ldz, float *summary, void *workspace,
+                                       size_t workspace_bytes, hipStream_t stream)
 {
     const Head h{dtype, T, V, D, X, ldx, W, ldw};
     tgemm_status_t st = check_head(h);
@@ -673,7 +676,8 @@ tgemm_status_t tgemm_linear_kd_backward(tgemm_dtype_t dtype, int64_t T, int64_t 
                                         const void *W, int64_t ldw, int64_t K, const int64_t *teacher_ids,
                                         int64_t ld_ids, tgemm_dtype_t teacher_dtype, const void *teacher_logits,
                                         int64_t ld_logits, float temperature, const float *lse, const float *student,
-                                        const float *logits, int64_t ldz, const float *grad_loss, int64_t grad_step, const float *grad_weight, void *dX,
+                                        const float *logits, int64_t ldz, const float *grad_loss, int64_t grad_step,
+                                        const float *grad_weight, void *dX,
                                         int64_t lddx, void *dW, int64_t lddw,
                                         void *workspace, size_t workspace_bytes, hipStream_t stream)
 {
@@ -691,13 +695,15 @@ tgemm_status_t tgemm_linear_kd_backward(tgemm_dtype_t dtype, int64_t T, int64_t 
     Range r[9], w[3];
     if (!at(X, T, D, ldx, size_of(dtype), r[0]) || !at(W, T == 0 ? 0 : V, D, ldw, size_of(dtype), r[1]) ||
         !at(teacher_ids, T, K, ld_ids, 8, r[2]) || !at(teacher_logits, T, K, ld_logits, size_of(teacher_dtype), r[3]) ||
-        !at(lse, T, 1, 1, 4, r[4]) || !at(student, T, K, K, 4, r[5]) || !at(grad_loss, T, 1, grad_step, 4, r[6]) || !at(grad_weight, T && grad_weight ? 1 : 0, 1, 1, 4, r[7]) ||
+        !at(lse, T, 1, 1, 4, r[4]) || !at(student, T, K, K, 4, r[5]) ||
+        !at(grad_loss, T, 1, grad_step, 4, r[6]) || !at(grad_weight, T && grad_weight ? 1 : 0, 1, 1, 4, r[7]) ||
         !at(dX, dX ? T : 0, D, lddx, size_of(dtype), w[0]) || !at(dW, dW ? V : 0, D, lddw, size_of(dtype), w[1]) ||
         !room_at(workspace, workspace_bytes, p, w[2]) || !at(logits, logits ? T : 0, V, ldz, 4, r[8]) || !disjoint(w, 3, r, 9))
         return TGEMM_ERROR_INVALID_VALUE;
     if (T == 0) return dW ? from_hip(launch_zero(dW, lddw, dtype, V, D, stream)) : TGEMM_SUCCESS;
     const Teacher t{(int)K, teacher_ids, ld_ids, teacher_logits, ld_logits, teacher_dtype, 1.0f / temperature};
-    return backward(p, h, Labels{nullptr, 0, &t}, grad_loss, grad_step, grad_weight, lse, student, z, dX, lddx, dW, lddw, workspace, stream);
+    return backward(p, h, Labels{nullptr, 0, &t}, grad_loss, grad_step, grad_weight, lse, student, z, dX,
+                    lddx, dW, lddw, workspace, stream);
 }
 
 }  // extern "C"

@@ -97,7 +97,8 @@ __global__ __launch_bounds__(64 * C * S) void linear_few_kernel(StatsArgs a, int
             } else {
 #pragma unroll
                 for (int pair = 0; pair < 6; ++pair)
-                    acc[i] = Frag<__bf16>::mfma(fw[(m16::kPairsB >> (2 * pair)) & 3], fx[(m16::kPairsA >> (2 * pair)) & 3], acc[i]);
+                    acc[i] = Frag<__bf16>::mfma(fw[(m16::kPairsB >> (2 * pair)) & 3], fx[(m16::kPairsA >> (2 * pair)) & 3],
+                                                acc[i]);
             }
         }
     };

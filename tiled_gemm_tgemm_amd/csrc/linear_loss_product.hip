@@ -360,7 +360,8 @@ __global__ __launch_bounds__(64 * WM * WN) void linear_out_kernel(OutArgs a)
 // work-group stays in a row.  Bound by memory: 4096×32768 bf16 reads 537 MB and
 // writes 268 in 152 µs (5.3 TB/s).
 template <class E>
-__global__ __launch_bounds__(256) void linear_grad_kept_kernel(GradArgs a, const float *logits, int64_t ldz, int64_t blocks, int per_row)
+__global__ __launch_bounds__(256) void linear_grad_kept_kernel(GradArgs a, const float *logits, int64_t ldz,
+                                                               int64_t blocks, int per_row)
 {
     typedef float f32x8 __attribute__((ext_vector_type(8)));
     typedef f32x8 f32x8_anywhere __attribute__((aligned(4)));

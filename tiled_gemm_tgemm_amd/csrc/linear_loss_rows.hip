@@ -484,7 +484,8 @@ __global__ __launch_bounds__(256) void linear_sum_kernel(SumArgs a)
                 uint16_t w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w[e] = a.dtype == TGEMM_BF16 ? bits((__bf16)v[e]) : bits((_Float16)v[e]);
-                *(u32x2_anywhere *)((uint16_t *)a.out + at) = u32x2_anywhere{w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16};
+                *(u32x2_anywhere *)((uint16_t *)a.out + at) =
+                    u32x2_anywhere{w[0] | (uint32_t)w[1] << 16, w[2] | (uint32_t)w[3] << 16};
             }
         } else {
 #pragma unroll
