@@ -693,3 +693,23 @@ def test_a_step_holds_a_small_part_of_large_logits():
     y = targets(T, V, g)
     # a piece of the logits' gradient (256 MiB and a row's padding), sums in float32, statistics
     assert peak(lambda: torch.autograd.grad(tg.linear_cross_entropy(X, W, y), (X, W))) < 4 * T * V // 8
+
+
+@pytest.mark.parametrize("keep", [False, True])
+def test_differentiable_on_a_side_stream(keep):
+    log(f"side stream, kept {keep}")
+    T, V, D = 200, 3000, 256
+    X, W, g = head(T, V, D, torch.bfloat16, 21)
+    X, W = X.contiguous().requires_grad_(), W.contiguous().requires_grad_()
+    y = targets(T, V, g)
+    want = torch.autograd.grad(tg.linear_cross_entropy(X, W, y, keep_logits=keep), (X, W))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            loss = tg.linear_cross_entropy(X, W, y, keep_logits=keep)
+        junk = [torch.full((T, V), 3.0, device="cuda") for _ in range(4)]  # would land on memory handed back too soon
+        have = torch.autograd.grad(loss, (X, W))  # torch runs it on `side`, and this stream waits for it
+        torch.cuda.synchronize()
+        assert torch.equal(have[0], want[0]) and torch.equal(have[1], want[1])
+        del junk

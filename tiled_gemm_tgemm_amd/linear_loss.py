@@ -45,10 +45,10 @@ def _dtype(t):
 
 
 def _rows(t, name, shape=None, device=None, like=None):
-    """A row-major matrix of a supported type, and its leading dimension."""
+    """The leading dimension of a row-major matrix of a supported type."""
     import torch
 
-    if not isinstance(t, torch.Tensor) or t.dim() != 2 or _dtype(t) is None:
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype not in _types():
         raise TypeError(f"{name} must be a 2-D float32, bfloat16 or float16 torch tensor")
     if not t.is_cuda or (device is not None and t.device != device):
         raise TypeError(f"{name} must live on {'a GPU' if device is None else device}")
@@ -57,6 +57,8 @@ def _rows(t, name, shape=None, device=None, like=None):
     if shape is not None and tuple(t.shape) != shape:
         raise ValueError(f"{name} must be {shape[0]}x{shape[1]}")
     rows, cols = t.shape
+    if rows > 1 and t.is_contiguous():
+        return cols or 1
     down, across = t.stride()
     if cols > 1 and rows > 0 and across != 1 or rows > 1 and down < cols:
         raise ValueError(f"{name} must be row-major")
@@ -90,29 +92,24 @@ class _Call:
         import torch
 
         ldx = _rows(X, "X")
-        ldw = _rows(W, "W", device=X.device, like=X.dtype)
-        if X.shape[1] != W.shape[1]:
+        device, dtype = X.device, X.dtype
+        ldw = _rows(W, "W", device=device, like=dtype)
+        (T, D), (V, inner) = X.shape, W.shape
+        if D != inner:
             raise ValueError(f"inner sizes differ: X is {tuple(X.shape)}, W is {tuple(W.shape)}")
-        if W.shape[0] < 1 or W.shape[1] < 1:
+        if V < 1 or D < 1:
             raise ValueError("W must have a row and a column")
-        self.device, self.dtype = X.device, X.dtype
-        self.T, self.D = X.shape
-        self.V = W.shape[0]
-        self.head = (_dtype(X), self.T, self.V, self.D, X.data_ptr(), ldx, W.data_ptr(), ldw)
-        self.stream, self.elsewhere = stream, stream is not None
-        if stream is None:
-            self.stream = torch.cuda.current_stream(X.device).cuda_stream
+        self.device, self.dtype, self.T, self.V, self.D = device, dtype, T, V, D
+        self.head = (_types()[dtype], T, V, D, X.data_ptr(), ldx, W.data_ptr(), ldw)
+        self.elsewhere = stream is not None
+        self.stream = stream if self.elsewhere else torch.cuda.current_stream(device).cuda_stream
         self.made = []
 
     def again(self, X, W):
-        """This call for the backward pass: the same tensors, wherever and however they are stored by now."""
-        import torch
-
-        c = object.__new__(_Call)
-        c.__dict__.update(self.__dict__)
-        c.head = (*self.head[:4], X.data_ptr(), _rows(X, "X"), W.data_ptr(), _rows(W, "W"))
-        c.stream = torch.cuda.current_stream(self.device).cuda_stream
-        return c
+        """For the backward pass, which torch runs on the forward pass's stream: the same tensors, wherever and
+        however they are stored by now (the call may be kept for another backward pass)."""
+        self.head = (*self.head[:4], X.data_ptr(), _rows(X, "X"), W.data_ptr(), _rows(W, "W"))
+        return self
 
     def teacher(self, ids, logits, temperature):
         import torch
@@ -169,10 +166,12 @@ class _Call:
     def room(self, workspace, k, backward):
         import torch
 
-        need = _lib.tgemm_linear_loss_workspace_size(*self.head, k, backward)
         if workspace is None:
-            workspace = self.new(max(need, 1), torch.uint8)
-        elif not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8:
+            need = _lib.library().tgemm_linear_loss_workspace_size(*self.head, k, backward)
+            workspace = torch.empty(need or 1, dtype=torch.uint8, device=self.device)
+            self.made.append(workspace)
+            return workspace.data_ptr(), need or 1
+        if not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8:
             raise TypeError("workspace must be a CUDA uint8 tensor")
         elif workspace.device != self.device or not workspace.is_contiguous():
             raise TypeError(f"workspace must be contiguous and live on {self.device}")
@@ -185,7 +184,7 @@ class _Call:
             from . import _hold_for_stream
 
             _hold_for_stream(self.stream, self.device, *self.made)
-        self.made = []  # the call may be kept for the backward pass, its workspace not
+        self.made.clear()  # the call may be kept for the backward pass, its workspace not
         entry_point = getattr(_lib.library(), entry)
         if torch.cuda.current_device() == self.device.index:
             st = entry_point(*self.head, *args, self.stream)
@@ -241,15 +240,6 @@ def _grad_loss(c, grad):
     return grad.data_ptr(), grad.stride(0) if grad.dim() and c.T > 1 else 0
 
 
-def _ce_backward(c, grad_loss, weight, target, lse, logits, ignore_index, dX, dW, need, workspace):
-    """target checked; weight and lse: addresses; logits as _Call.logits gave it"""
-    dX, dW, outs = _gradients(c, dX, dW, need)
-    c.queue("tgemm_linear_ce_backward", target.data_ptr(), int(ignore_index), lse, *logits,
-            *_grad_loss(c, grad_loss), weight, *outs,
-            *c.room(workspace, 0, 1))
-    return dX, dW
-
-
 def linear_cross_entropy_backward(grad_loss, X, W, target, lse, *, ignore_index=-100, logits=None, dX=None, dW=None,
                                   need=(True, True), workspace=None, stream=None):
     """(dX, dW) = the gradients of sum_t grad_loss_t·loss_t (tgemm_linear_ce_backward).  grad_loss: float32, one
@@ -258,7 +248,10 @@ def linear_cross_entropy_backward(grad_loss, X, W, target, lse, *, ignore_index=
     c = _Call(X, W, stream)
     target = c.target(target)
     lse = _floats(lse, "lse", (c.T,), c.device)
-    return _ce_backward(c, grad_loss, 0, target, lse.data_ptr(), c.logits(logits), ignore_index, dX, dW, need, workspace)
+    dX, dW, outs = _gradients(c, dX, dW, need)
+    c.queue("tgemm_linear_ce_backward", target.data_ptr(), int(ignore_index), lse.data_ptr(), *c.logits(logits),
+            *_grad_loss(c, grad_loss), 0, *outs, *c.room(workspace, 0, 1))
+    return dX, dW
 
 
 def linear_distillation_forward(X, W, teacher_ids, teacher_logits, *, temperature=1.0, loss=None, lse=None,
@@ -278,14 +271,6 @@ def linear_distillation_forward(X, W, teacher_ids, teacher_logits, *, temperatur
     return loss, lse, student
 
 
-def _kd_backward(c, grad_loss, weight, teacher, lse, student, logits, dX, dW, need, workspace):
-    """teacher and logits as _Call's functions gave them; weight, lse and student: addresses"""
-    dX, dW, outs = _gradients(c, dX, dW, need)
-    c.queue("tgemm_linear_kd_backward", *teacher, lse, student, *logits, *_grad_loss(c, grad_loss), weight, *outs,
-            *c.room(workspace, c.K, 1))
-    return dX, dW
-
-
 def linear_distillation_backward(grad_loss, X, W, teacher_ids, teacher_logits, lse, student, *, temperature=1.0,
                                  logits=None, dX=None, dW=None, need=(True, True), workspace=None, stream=None):
     """(dX, dW) = the gradients of sum_t grad_loss_t·loss_t (tgemm_linear_kd_backward); lse, student and, if it left
@@ -294,8 +279,10 @@ def linear_distillation_backward(grad_loss, X, W, teacher_ids, teacher_logits, l
     teacher = c.teacher(teacher_ids, teacher_logits, temperature)
     lse = _floats(lse, "lse", (c.T,), c.device)
     student = _floats(student, "student", (c.T, c.K), c.device)
-    return _kd_backward(c, grad_loss, 0, teacher, lse.data_ptr(), student.data_ptr(), c.logits(logits), dX, dW, need,
-                        workspace)
+    dX, dW, outs = _gradients(c, dX, dW, need)
+    c.queue("tgemm_linear_kd_backward", *teacher, lse.data_ptr(), student.data_ptr(), *c.logits(logits),
+            *_grad_loss(c, grad_loss), 0, *outs, *c.room(workspace, c.K, 1))
+    return dX, dW
 
 
 @functools.lru_cache(maxsize=None)
@@ -306,13 +293,17 @@ def _functions():
 
     def result(c, reduction, kept):
         # tensors of their own on `kept`, not views of it: a caller may change them in place
-        place, shape = {"mean": (1, ()), "sum": (0, ()), "none": (4 + c.T, (c.T,))}[reduction]
+        place, shape = (4 + c.T, (c.T,)) if reduction == "none" else (1 if reduction == "mean" else 0, ())
         return torch.empty(0, dtype=torch.float32, device=c.device).set_(kept.untyped_storage(), place, shape)
 
-    def addresses(reduction, kept):
-        """The mean's weight, or none, and lse."""
+    def gradients(ctx, grad, c, kept):
+        """What _gradients and _grad_loss give, for what torch hands over; and the address of lse."""
+        need_x, need_w = ctx.needs_input_grad[:2]
+        dX = torch.empty((c.T, c.D), dtype=c.dtype, device=c.device) if need_x else None
+        dW = torch.empty((c.V, c.D), dtype=c.dtype, device=c.device) if need_w else None
         at = kept.data_ptr()
-        return at + 8 if reduction == "mean" else 0, at + 16
+        return dX, dW, (grad.data_ptr(), grad.stride(0) if c.T > 1 and grad.dim() else 0,
+                        at + 8 if ctx.reduction == "mean" else 0, _ptr(dX), c.D, _ptr(dW), c.D), at + 16
 
     class CrossEntropy(torch.autograd.Function):
         @staticmethod
@@ -324,17 +315,17 @@ def _functions():
             c.queue("tgemm_linear_ce_forward", target.data_ptr(), int(ignore_index), *at[:2], *c.logits(logits), at[2],
                     *c.room(None, 0, 0))
             ctx.save_for_backward(X, W, target, kept, logits)
-            ctx.call, ctx.ignore_index, ctx.reduction = c, ignore_index, reduction
+            ctx.call, ctx.ignore_index, ctx.reduction = c, int(ignore_index), reduction
             return result(c, reduction, kept)
 
         @staticmethod
         @once_differentiable
         def backward(ctx, grad):
             X, W, target, kept, logits = ctx.saved_tensors
-            weight, lse = addresses(ctx.reduction, kept)
             c = ctx.call.again(X, W)
-            dX, dW = _ce_backward(c, grad, weight, target, lse, c.logits(logits), ctx.ignore_index, None, None,
-                                  ctx.needs_input_grad, None)
+            dX, dW, rest, lse = gradients(ctx, grad, c, kept)
+            c.queue("tgemm_linear_ce_backward", target.data_ptr(), ctx.ignore_index, lse, *c.logits(logits), *rest,
+                    *c.room(None, 0, 1))
             return dX, dW, None, None, None, None
 
     class Distillation(torch.autograd.Function):
@@ -356,9 +347,9 @@ def _functions():
         def backward(ctx, grad):
             X, W, ids, top, kept, student, logits = ctx.saved_tensors
             c = ctx.call.again(X, W)
-            weight, lse = addresses(ctx.reduction, kept)
-            dX, dW = _kd_backward(c, grad, weight, c.teacher(ids, top, ctx.temperature), lse, student.data_ptr(),
-                                  c.logits(logits), None, None, ctx.needs_input_grad, None)
+            dX, dW, rest, lse = gradients(ctx, grad, c, kept)
+            c.queue("tgemm_linear_kd_backward", *c.teacher(ids, top, ctx.temperature), lse, student.data_ptr(),
+                    *c.logits(logits), *rest, *c.room(None, c.K, 1))
             return dX, dW, None, None, None, None, None
 
     return CrossEntropy, Distillation
