@@ -184,13 +184,17 @@ class _Call:
             from . import _hold_for_stream
 
             _hold_for_stream(self.stream, self.device, *self.made)
-        self.made.clear()  # the call may be kept for the backward pass, its workspace not
         entry_point = getattr(_lib.library(), entry)
-        if torch.cuda.current_device() == self.device.index:
-            st = entry_point(*self.head, *args, self.stream)
-        else:
-            with torch.cuda.device(self.device):
+        try:
+            if torch.cuda.current_device() == self.device.index:
                 st = entry_point(*self.head, *args, self.stream)
+            else:
+                with torch.cuda.device(self.device):
+                    st = entry_point(*self.head, *args, self.stream)
+        finally:
+            # only now: what is released after the launches is handed out again behind them.  The call may be kept for
+            # the backward pass, its workspace not.
+            self.made.clear()
         if st != _lib.TGEMM_SUCCESS:
             raise TgemmError(st, entry)
 
