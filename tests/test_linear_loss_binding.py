@@ -21,28 +21,35 @@ class Host:
 
     def __init__(self):
         self.stream = 1 << 44
-        self.memory = []  # (address, bytes, reference) of everything allocated, in order
+        self.memory = []  # (memory, address, reference to who has it) of everything allocated; no address comes twice
         self.calls = []   # (entry, arguments)
-        self.entered = []  # called at the next entries, one each
+        self.allocating = []  # called at the next allocations, one each
 
-    def watch(self, t):
+    def empty(self, shape, dtype=torch.float32, device=None):
+        """As torch.empty."""
+        if self.allocating:
+            self.allocating.pop(0)()
+        return self.room(shape, dtype)
+
+    def room(self, shape, dtype):
         from torch.multiprocessing.reductions import StorageWeakRef
 
-        room = t.untyped_storage()
-        if room.nbytes():
-            self.memory.append((room.data_ptr(), room.nbytes(), StorageWeakRef(room)))
+        memory = bytearray(torch.Size([shape] if isinstance(shape, int) else shape).numel() * dtype.itemsize + 64)
+        t = torch.frombuffer(memory, dtype=dtype)[:(len(memory) - 64) // dtype.itemsize].view(shape)
+        self.memory.append((memory, t.data_ptr(), StorageWeakRef(t.untyped_storage())))
         return t
 
+    def copy(self, t):
+        return self.room(t.shape, t.dtype).copy_(t.detach())
+
     def at(self, address):
-        """The last allocation that has this address, or None."""
-        for lo, size, ref in reversed(self.memory):
-            if lo <= address < lo + size:
+        """Who has, or had, this address, or None."""
+        for memory, lo, ref in self.memory:
+            if lo <= address < lo + len(memory):
                 return ref
         return None
 
     def entry(self, name, args):
-        if self.entered:
-            self.entered.pop(0)()
         for a in args:
             ref = self.at(a) if isinstance(a, int) else None
             assert ref is None or not ref.expired(), f"{name} is handed memory that was released"
@@ -61,9 +68,8 @@ class Host:
 @pytest.fixture
 def host(monkeypatch):
     h = Host()
-    empty = torch.empty
     monkeypatch.setattr(_lib, "library", lambda: h)
-    monkeypatch.setattr(torch, "empty", lambda *a, **k: h.watch(empty(*a, **k)))
+    monkeypatch.setattr(torch, "empty", h.empty)
     monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: True), raising=False)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: types.SimpleNamespace(cuda_stream=h.stream))
@@ -114,3 +120,28 @@ def test_a_workspace_is_released_after_the_call(host):
     loss = losses()["ce"](X, W)
     torch.autograd.grad(loss, (X, W), retain_graph=True)
     assert all(host.at(args[-3]).expired() for _, args in host.calls)
+
+
+@pytest.mark.parametrize("op", ["ce", "kd"])
+@pytest.mark.parametrize("turn", [0, 1, 2])
+def test_backward_passes_through_one_node_do_not_meet(host, op, turn):
+    """Another pass comes in where the first one allocates its `turn`-th tensor, as another thread's may, and each has
+    saved tensors of its own, as hooks make them."""
+    X, W = (t.requires_grad_() for t in head())
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: t, lambda t: host.copy(t)):
+        loss = losses()[op](X, W)
+    host.allocating = [lambda: None] * turn + [lambda: torch.autograd.grad(loss, (X, W), retain_graph=True)]
+    torch.autograd.grad(loss, (X, W), retain_graph=True)
+    assert [name for name, _ in host.calls] == [f"tgemm_linear_{op}_forward"] + 2 * [f"tgemm_linear_{op}_backward"]
+    inner, outer = host.calls[1][1], host.calls[2][1]
+    assert inner[4] != outer[4] and inner[6] != outer[6] and inner[-3] != outer[-3]
+
+
+def test_a_saved_tensor_that_changed_its_size_is_refused(host):
+    X, W = (t.requires_grad_() for t in head())
+    for change in (lambda t: t[:2], lambda t: t.double()):
+        with torch.autograd.graph.saved_tensors_hooks(lambda t: t, lambda t: change(t.detach()) if t.dim() == 2 else t):
+            loss = losses()["ce"](X, W, keep_logits=False)
+        with pytest.raises((TypeError, ValueError)):
+            torch.autograd.grad(loss, (X, W))
+    assert all(name.endswith("forward") for name, _ in host.calls)

@@ -16,6 +16,7 @@ return without waiting.  include/tgemm.h states the arithmetic.
 
 from __future__ import annotations
 
+import copy
 import functools
 
 from . import _lib
@@ -106,10 +107,13 @@ class _Call:
         self.made = []
 
     def again(self, X, W):
-        """For the backward pass, which torch runs on the forward pass's stream: the same tensors, wherever and
-        however they are stored by now (the call may be kept for another backward pass)."""
-        self.head = (*self.head[:4], X.data_ptr(), _rows(X, "X"), W.data_ptr(), _rows(W, "W"))
-        return self
+        """The call of a backward pass, which torch runs on the forward pass's stream: the same tensors, wherever and
+        however they are stored by now.  It is the pass's own: others may go through the same node meanwhile."""
+        c = copy.copy(self)
+        ldx = _rows(X, "X", (c.T, c.D), c.device, c.dtype)
+        c.head = (*c.head[:4], X.data_ptr(), ldx, W.data_ptr(), _rows(W, "W", (c.V, c.D), c.device, c.dtype))
+        c.made = []
+        return c
 
     def teacher(self, ids, logits, temperature):
         import torch
@@ -192,8 +196,8 @@ class _Call:
                 with torch.cuda.device(self.device):
                     st = entry_point(*self.head, *args, self.stream)
         finally:
-            # only now: what is released after the launches is handed out again behind them.  The call may be kept for
-            # the backward pass, its workspace not.
+            # only now: what is released after the launches is handed out again behind them.  The call is kept for the
+            # backward pass, its workspace not.
             self.made.clear()
         if st != _lib.TGEMM_SUCCESS:
             raise TgemmError(st, entry)
