@@ -78,3 +78,22 @@ def test_two_late_streams_of_one_thread():
     for a, b in zip(got, want):
         assert all(torch.equal(p, q) for p, q in zip(a, b))
     del held
+
+
+@pytest.mark.parametrize("keep", [False, True])
+def test_a_node_called_under_a_late_stream(keep):
+    X, W, g = head(T, V, D, torch.bfloat16, 33)
+    X, W = X.contiguous().requires_grad_(), W.contiguous().requires_grad_()
+    y = targets(T, V, g)
+    loss = tg.linear_cross_entropy(X, W, y, keep_logits=keep)
+    one = torch.ones((), device="cuda")
+    want = torch.autograd.grad(loss, (X, W), one, retain_graph=True)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    held = later(side)
+    with torch.cuda.stream(side):
+        got = loss.grad_fn.apply(one)[:2]
+    junk = take(X, W, 0, 1)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    del junk, held

@@ -145,3 +145,24 @@ def test_a_saved_tensor_that_changed_its_size_is_refused(host):
         with pytest.raises((TypeError, ValueError)):
             torch.autograd.grad(loss, (X, W))
     assert all(name.endswith("forward") for name, _ in host.calls)
+
+
+@pytest.mark.parametrize("op", ["ce", "kd"])
+@pytest.mark.parametrize("keep", [False, True])
+def test_a_node_called_under_another_stream_runs_there(host, op, keep, monkeypatch):
+    recorded = []
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append((t.data_ptr(), s.cuda_stream)),
+                        raising=False)
+    X, W = (t.requires_grad_() for t in head())
+    loss = losses()[op](X, W, keep_logits=keep)
+    first = host.stream
+    torch.autograd.grad(loss, (X, W), retain_graph=True)
+    assert host.calls[-1][1][-1] == first and not recorded
+    host.stream = 1 << 46
+    loss.grad_fn.apply(torch.ones(()))
+    name, args = host.calls[-1]
+    assert name.endswith("backward") and args[-1] == host.stream
+    # what the forward pass allocated on its own stream is known to be in use on this one
+    assert len(recorded) == 1 + keep + (op == "kd") and {s for _, s in recorded} == {host.stream}
+    torch.autograd.grad(loss, (X, W))
+    assert len(host.calls) == 4

@@ -106,10 +106,20 @@ class _Call:
         self.stream = stream if self.elsewhere else torch.cuda.current_stream(device).cuda_stream
         self.made = []
 
-    def again(self, X, W):
-        """The call of a backward pass, which torch runs on the forward pass's stream: the same tensors, wherever and
-        however they are stored by now.  It is the pass's own: others may go through the same node meanwhile."""
+    def again(self, X, W, *kept):
+        """The call of a backward pass: the same tensors, wherever and however they are stored by now, on the stream
+        that is torch's current one (its engine makes that the forward pass's; a node that is called by hand runs where
+        its caller is).  It is the pass's own: others may go through the same node meanwhile.  kept: what the forward
+        pass allocated."""
+        import torch
+
         c = copy.copy(self)
+        current = torch.cuda.current_stream(c.device)
+        if current.cuda_stream != c.stream:
+            c.stream = current.cuda_stream
+            for t in kept:
+                if t is not None:
+                    t.record_stream(current)
         ldx = _rows(X, "X", (c.T, c.D), c.device, c.dtype)
         c.head = (*c.head[:4], X.data_ptr(), ldx, W.data_ptr(), _rows(W, "W", (c.V, c.D), c.device, c.dtype))
         c.made = []
@@ -330,7 +340,7 @@ def _functions():
         @once_differentiable
         def backward(ctx, grad):
             X, W, target, kept, logits = ctx.saved_tensors
-            c = ctx.call.again(X, W)
+            c = ctx.call.again(X, W, kept, logits)
             dX, dW, rest, lse = gradients(ctx, grad, c, kept)
             c.queue("tgemm_linear_ce_backward", target.data_ptr(), ctx.ignore_index, lse, *c.logits(logits), *rest,
                     *c.room(None, 0, 1))
@@ -354,7 +364,7 @@ def _functions():
         @once_differentiable
         def backward(ctx, grad):
             X, W, ids, top, kept, student, logits = ctx.saved_tensors
-            c = ctx.call.again(X, W)
+            c = ctx.call.again(X, W, kept, student, logits)
             dX, dW, rest, lse = gradients(ctx, grad, c, kept)
             c.queue("tgemm_linear_kd_backward", *c.teacher(ids, top, ctx.temperature), lse, student.data_ptr(),
                     *c.logits(logits), *rest, *c.room(None, c.K, 1))
