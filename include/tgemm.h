@@ -371,6 +371,9 @@ int64_t tgemm_sgemm_host_workspace_size(int64_t M, int64_t N, int64_t K, int64_t
  *             float32.  The logits' gradient is rounded to the operands' type
  *             (float32: to three planes; up to 128 rows: to two numbers of the
  *             type that add up to it) before the two gradient products.
+ *             fp16 rows with factors of their own share a range of 40 binary
+ *             places in dW: a row's part is rounded by up to 2^-38 of the
+ *             largest product of a factor and a state besides.
  * Sizes       0 <= T < 2^24, 1 <= V <= 2^24, 1 <= D <= 2^22, 1 <= K <= 1024,
  *             leading dimensions up to 2^40; larger ones, and an unknown
  *             dtype: TGEMM_ERROR_NOT_SUPPORTED.  T = 0: nothing but `summary`

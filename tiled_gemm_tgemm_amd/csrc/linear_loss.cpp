@@ -397,6 +397,9 @@ tgemm_status_t backward(const Plan &p, const Head &h, const Labels &l, const flo
     c.ignore = l.ignore;
     c.teacher = l.teacher;
     c.half = p.half;
+    c.X = h.X;
+    c.ldx = h.ldx;
+    c.D = h.D;
     c.coef = in<float>(ws, p.coef);
     const bool scaled = p.half || grad_step == 0;
     float *row_scale = scaled ? in<float>(ws, p.row_scale) : nullptr;

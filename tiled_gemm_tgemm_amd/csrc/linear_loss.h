@@ -148,9 +148,18 @@ hipError_t launch_summary_none(float *summary, hipStream_t stream);
 //   that of every element.
 // * Otherwise coef is c_t; for fp16 its fraction times 2^kHalfShift, with
 //   row_scale[t] = 2^(exponent - kHalfShift), exps[t] the exponent, and
-//   block_max[b] the largest of a work-group's rows (256, or 16 where each has
-//   a teacher's entries); launch_copy writes all_scale.
-inline int64_t coef_blocks(int64_t T, bool teacher) { return teacher ? (T + 15) / 16 : (T + 255) / 256; }
+//   block_max[b] the largest over a work-group's kCoefRows rows of exponent +
+//   that of the row's largest finite state (X, fp16).  launch_copy scales dW's
+//   rows of X by their factors' powers of two, such that the largest product of
+//   the two lies just below 2^kHalfShift, and writes all_scale: a row whose
+//   factor is 2^-28 of the largest keeps the bits of its states.  (Scaled by
+//   their factors relative to the largest, without regard to the states, rows
+//   of N(0,1) lost bits from 2^-14 on and were 29% off at 2^-24.)
+constexpr int kCoefRows = 16;
+inline int64_t coef_blocks(int64_t T, bool /* a row of either loss takes a wavefront */)
+{
+    return (T + kCoefRows - 1) / kCoefRows;
+}
 struct CoefArgs {
     int64_t T, V;
     const float *grad;
@@ -163,6 +172,8 @@ struct CoefArgs {
     bool half;
     float *coef, *row_scale, *all_scale;
     int *exps, *block_max;
+    const void *X;  // T×D, rows ldx apart
+    int64_t ldx, D;
 };
 hipError_t launch_coef(const CoefArgs &a, hipStream_t stream);
 
@@ -172,8 +183,8 @@ inline bool coef_in_copy(const CoefArgs &a) { return a.teacher == nullptr && (!a
 
 // dst (planes of rows_out×ld_out 16-bit elements, zero past the ends) = src
 // (rows×cols).  coef: rows with coef 0 become zero.  exps: row t is scaled by
-// 2^(exps[t] - the largest of block_max), and all_scale receives
-// 2^(that - kHalfShift).
+// 2^(kHalfShift + exps[t] - the largest of block_max), if it has an exponent,
+// and all_scale receives 2^(that - 2·kHalfShift).
 struct CopyArgs {
     const void *src;
     int64_t ld;

@@ -17,7 +17,8 @@ typedef f32x8 f32x8_anywhere __attribute__((aligned(4)));
 typedef m16::f32x4 f32x4_anywhere __attribute__((aligned(4)));
 typedef uint32_t u32x2_anywhere __attribute__((ext_vector_type(2), aligned(2)));
 
-// No factor of a float32 row can be as low: the largest exponent of rows that all do not count.
+// The exponent of nothing: a row without a factor of its own, or without a
+// state that is neither zero nor infinite.  Lower than any other.
 constexpr int kNoExponent = -100000;
 
 __device__ __forceinline__ float load_as_float(const void *p, int64_t at, tgemm_dtype_t dtype)
@@ -71,7 +72,7 @@ __device__ __forceinline__ int put_coef(const CoefArgs &a, int64_t row, RowKind 
                 exponent = e;
             }
             a.row_scale[row] = ldexpf(1.0f, e - kHalfShift);
-            a.exps[row] = e;
+            a.exps[row] = exponent;
         }
     }
     a.coef[row] = coef;
@@ -97,7 +98,8 @@ __global__ __launch_bounds__(256) void linear_copy_kernel(CopyArgs a, CoefArgs m
         __syncthreads();
         top = max(max(best[0], best[1]), max(best[2], best[3]));
         if (top == kNoExponent) top = 0;
-        if (blockIdx.x == 0 && threadIdx.x == 0) *a.all_scale = ldexpf(1.0f, top - kHalfShift);
+        // no less than float32 holds, so that a NaN in the sums stays one; the least fp16 is far above
+        if (blockIdx.x == 0 && threadIdx.x == 0) *a.all_scale = ldexpf(1.0f, max(top - 2 * kHalfShift, -126));
     }
     const int64_t per_row = a.ld_out / 8, total = a.rows_out * per_row;
     for (int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x; p < total; p += (int64_t)gridDim.x * 256) {
@@ -139,7 +141,7 @@ __global__ __launch_bounds__(256) void linear_copy_kernel(CopyArgs a, CoefArgs m
                 for (int e = 0; e < 8; ++e) v[0][e] = e < left ? from[e] : (uint16_t)0;
             }
             if (a.exps != nullptr) {
-                const int shift = a.exps[row] - top;
+                const int e = a.exps[row], shift = e == kNoExponent ? 0 : kHalfShift + e - top;
                 if (shift != 0) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
@@ -376,35 +378,62 @@ __device__ __forceinline__ void put_block_max(const CoefArgs &a, int64_t block, 
     }
 }
 
-__global__ __launch_bounds__(256) void linear_ce_coef_kernel(CoefArgs a)
+// The exponent of a row's largest finite fp16 state, kNoExponent where all are zero.
+__device__ __forceinline__ int state_exponent(const CoefArgs &a, int64_t row, int lane)
 {
-    const int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    int exponent = kNoExponent;
-    if (row < a.T) {
-        exponent = put_coef(a, row, ce_kind(a, row));
+    const uint16_t *x = (const uint16_t *)a.X + row * a.ldx;
+    uint32_t most = 0;
+    auto take = [&](uint16_t v) {
+        const uint32_t size = v & 0x7FFF;
+        if (size < 0x7C00 && size > most) most = size;
+    };
+    for (int64_t col = lane * 8; col < a.D; col += 512) {
+        if (col + 8 <= a.D) {
+            const u16x8 v = *(const u16x8_anywhere *)(x + col);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) take(v[e]);
+        } else {
+            for (int64_t e = col; e < a.D; ++e) take(x[e]);
+        }
     }
-    put_block_max<4>(a, blockIdx.x, exponent);
+    const float high = wave_max((float)__builtin_bit_cast(_Float16, (uint16_t)most));
+    int exponent = kNoExponent;
+    if (high != 0.0f) frexpf(high, &exponent);
+    return exponent;
 }
 
-// A wavefront a row.
-__global__ __launch_bounds__(1024) void linear_kd_coef_kernel(CoefArgs a, Teacher t)
+// A wavefront a row: its factor, and where that is an fp16 row's own, the
+// exponent of the largest product of factor and state.
+__global__ __launch_bounds__(1024) void linear_coef_kernel(CoefArgs a, Teacher t, bool distill)
 {
-    const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 6);
+    const int64_t row = (int64_t)blockIdx.x * kCoefRows + (threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
     int exponent = kNoExponent;
     if (row < a.T) {
-        bool any = false, bad = false;
-        for (int k = lane; k < t.K; k += 64) {
-            const int64_t id = t.ids[row * t.ld_ids + k];
-            if (load_as_float(t.logits, row * t.ld_logits + k, t.dtype) == -INFINITY) continue;
-            any = true;
-            bad |= id < 0 || id >= a.V;
+        RowKind kind;
+        if (distill) {
+            bool any = false, bad = false;
+            for (int k = lane; k < t.K; k += 64) {
+                const int64_t id = t.ids[row * t.ld_ids + k];
+                if (load_as_float(t.logits, row * t.ld_logits + k, t.dtype) == -INFINITY) continue;
+                any = true;
+                bad |= id < 0 || id >= a.V;
+            }
+            any = __any(any);
+            bad = __any(bad);
+            kind = !any ? kNotCounted : bad ? kBad : kCounted;
+        } else {
+            kind = ce_kind(a, row);
         }
-        any = __any(any);
-        bad = __any(bad);
-        if (lane == 0) exponent = put_coef(a, row, !any ? kNotCounted : bad ? kBad : kCounted);
+        int own = kNoExponent;
+        if (lane == 0) own = put_coef(a, row, kind);
+        own = __shfl(own, 0);
+        if (own != kNoExponent) {
+            const int state = state_exponent(a, row, lane);
+            if (state != kNoExponent) exponent = own + state;
+        }
     }
-    put_block_max<16>(a, blockIdx.x, exponent);
+    put_block_max<kCoefRows>(a, blockIdx.x, exponent);
 }
 
 // A wavefront a row.  An id that comes twice holds the sum of its entries in
@@ -558,8 +587,7 @@ hipError_t launch_sort(const SortArgs &a, hipStream_t stream)
 hipError_t launch_coef(const CoefArgs &a, hipStream_t stream)
 {
     const unsigned blocks = (unsigned)coef_blocks(a.T, a.teacher != nullptr);
-    if (a.teacher == nullptr) linear_ce_coef_kernel<<<blocks, 256, 0, stream>>>(a);
-    else linear_kd_coef_kernel<<<blocks, 1024, 0, stream>>>(a, *a.teacher);
+    linear_coef_kernel<<<blocks, 64 * kCoefRows, 0, stream>>>(a, a.teacher ? *a.teacher : Teacher{}, a.teacher != nullptr);
     return hipGetLastError();
 }
 
