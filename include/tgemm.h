@@ -375,8 +375,10 @@ int64_t tgemm_sgemm_host_workspace_size(int64_t M, int64_t N, int64_t K, int64_t
  *             places in dW: a row's part is rounded by up to 2^-38 of the
  *             largest product of a factor and a state besides.
  * Sizes       0 <= T < 2^24, 1 <= V <= 2^24, 1 <= D <= 2^22, 1 <= K <= 1024,
- *             leading dimensions up to 2^40; larger ones, and an unknown
- *             dtype: TGEMM_ERROR_NOT_SUPPORTED.  T = 0: nothing but `summary`
+ *             leading dimensions up to 2^40; larger ones, a product of 2^31
+ *             tiles and more (T·V from about 2^47 on; a tile has up to
+ *             256×256 entries), and an unknown dtype:
+ *             TGEMM_ERROR_NOT_SUPPORTED.  T = 0: nothing but `summary`
  *             and a zero dW is written.
  * Workspace   Device memory of the caller, 16-byte aligned, at least
  *             tgemm_linear_loss_workspace_size(...) bytes for the same

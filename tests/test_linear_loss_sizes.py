@@ -1,0 +1,39 @@
+"""Which sizes the loss operators take, and what they plan for them."""
+
+import os
+import shutil
+import subprocess
+
+import pytest
+
+import tiled_gemm_tgemm_amd as tg
+from test_linear_loss import BIG, ce_forward, kd_forward, lib, size  # noqa: F401
+from test_linear_loss_walk import CSRC
+
+
+@pytest.mark.parametrize("T,V,D", [(1 << 22, 131072, 64), (1 << 20, 1 << 20, 64), ((1 << 24) - 1, 1 << 22, 8), (1 << 20, 131072, 4096)])
+@pytest.mark.parametrize("dtype", [0, 1, 2])
+def test_many_tiles_are_taken(T, V, D, dtype):
+    for K in (0, 5):
+        assert size(dtype=dtype, T=T, V=V, D=D, ldx=D, ldw=D, K=K) > T * V // 8  # a pair of floats a row and 64 words
+        assert size(dtype=dtype, T=T, V=V, D=D, ldx=D, ldw=D, K=K, backward=1) > 0
+
+
+@pytest.mark.parametrize("call", [ce_forward, kd_forward])
+def test_too_many_tiles_are_refused(call):
+    # 2^16 by 2^15 tiles of 256×256 and one row of tiles fewer; the latter is taken but for its workspace
+    T, V = (1 << 24) - 1, 1 << 23
+    assert call(T=T, V=V) == tg.TGEMM_ERROR_NOT_SUPPORTED and size(T=T, V=V) == 0
+    assert size(T=T - 256, V=V) > BIG and call(T=T - 256, V=V) == tg.TGEMM_ERROR_INVALID_VALUE
+
+
+def test_a_tiles_place(tmp_path):
+    if not shutil.which("g++"):
+        pytest.skip("g++ is needed")
+    out = str(tmp_path / "place")
+    subprocess.run(["g++", "-O1", "-std=c++17", "-Wall", "-Werror", "-fsanitize=undefined", "-fno-sanitize-recover=all", f"-I{CSRC}",
+                    os.path.join(os.path.dirname(__file__), "tile_place.cpp"), "-o", out], check=True)
+    products = [(1, 1, 1), (1, 9, 3), (8, 8, 1), (9, 7, 5), (65535, 32768, 1), (16384, 512, 1), (32768, 65535, 1),
+                (1024, 32767, 64), (46340, 46340, 1)]
+    r = subprocess.run([out], input="".join("%d %d %d\n" % p for p in products), capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout == f"{len(products)} products\n", (r.returncode, r.stderr[-500:])

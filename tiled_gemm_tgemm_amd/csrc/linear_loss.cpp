@@ -18,7 +18,9 @@ constexpr int64_t kMaxV = (int64_t)1 << 24;
 constexpr int64_t kMaxD = (int64_t)1 << 22;   // 256 rows of 16-bit values stay within 32-bit offsets
 constexpr int64_t kMaxK = 1024;
 constexpr int64_t kMaxLd = (int64_t)1 << 40;
-constexpr int64_t kMaxThreads = ((int64_t)1 << 32) - 1;
+// A launch has as many work-groups as the GPU holds at most; they count their
+// tiles in 32 bits, and a tile's number plus a step of the grid has to fit.
+constexpr int64_t kMaxTiles = INT32_MAX - 1024;
 
 // Bytes of one piece of the logits' gradient: large enough that the products
 // of a piece fill the GPU for several rounds, small enough to stay near the
@@ -194,11 +196,11 @@ void plan_operands(Plan &p, const Head &h, bool backward)
     if (backward) p.xs = p.take(p.Tp * p.Dp * 2 * p.planes);
 }
 
-// False where a launch would have too many threads.
+// False where a product would have too many tiles.
 bool fits(int64_t M, int64_t N, int tile, int64_t splits)
 {
     const TileShape &s = kTiles[tile];
-    return ceil_div(M, s.bm) * ceil_div(N, s.bn) * 512 <= kMaxThreads / splits;
+    return ceil_div(M, s.bm) * ceil_div(N, s.bn) <= kMaxTiles / splits;
 }
 
 bool plan_forward(Plan &p, const Head &h, int64_t teacher_k)
