@@ -385,6 +385,11 @@ int64_t tgemm_sgemm_host_workspace_size(int64_t M, int64_t N, int64_t K, int64_t
  *             arguments, overlapping none of the others.  Its contents on
  *             entry do not matter and on return are unspecified.  Two calls in
  *             flight at once need two.
+ *             A backward call's holds a piece of the logits' gradient: 256
+ *             MiB of it or, where that is more, 2048 words of all rows (2
+ *             bytes each, float32 6, up to 128 rows 4), but no more words than
+ *             there are; besides it X as the products read it and sums of dX
+ *             and dW in float32.
  * Errors      As above, before anything is queued; also
  *             TGEMM_ERROR_INVALID_VALUE for a missing, misaligned, overlapping
  *             or too small workspace, an output that overlaps an input or

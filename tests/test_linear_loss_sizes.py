@@ -37,3 +37,22 @@ def test_a_tiles_place(tmp_path):
                 (1024, 32767, 64), (46340, 46340, 1)]
     r = subprocess.run([out], input="".join("%d %d %d\n" % p for p in products), capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout == f"{len(products)} products\n", (r.returncode, r.stderr[-500:])
+
+
+@pytest.mark.parametrize("dtype,value", [(0, 6), (1, 2), (2, 2)])
+@pytest.mark.parametrize("T", [1000, 21000, 65536, 100000, 262144, 1 << 20])
+@pytest.mark.parametrize("V,D", [(131072, 64), (32768, 1024), (1000, 256)])
+def test_what_a_backward_call_holds(dtype, value, T, V, D):
+    """A piece of the logits' gradient as tgemm.h bounds it (a row of it is up to 128 words longer than its words, a
+    multiple of 256), X, and the sums of dX and dW in up to 64 parts each where they are split."""
+    piece = max(256 << 20, 2048 * T * value, 256 * T * value)
+    piece = min(piece, (V + 255) // 256 * 256 * T * value) + 128 * (T + 64) * value
+    x = (T + 64) * D * (6 if dtype == 0 else 2)
+    w = V * D * 6 if dtype == 0 else 0
+    need = size(dtype=dtype, T=T, V=V, D=D, ldx=D, ldw=D, backward=1)
+    sums = need - (piece + x + w + 12 * (T + 64) + 4096)
+    # in parts only where the tiles are fewer than the GPU holds, 256 of 256×256
+    split = 256 * 256 * 256 * 4 * 2
+    assert sums <= max(4 * (T + 64) * D, split) + split
+    if T >= 262144 and dtype:
+        assert need >= min(V, 2048) * T * value

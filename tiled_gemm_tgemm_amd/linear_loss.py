@@ -25,8 +25,8 @@ from ._lib import TgemmError
 REDUCTIONS = ("mean", "sum", "none")
 
 # Unless told otherwise the differentiable calls form the logits again in the backward pass, and hold them (float32)
-# only where all of them take no more than a piece of their gradient does (256 MiB, which the backward pass holds
-# anyway) and that is faster.  Writing and reading them costs about as much as forming them again does at an inner size
+# only where all of them take no more than the 256 MiB that a piece of their gradient is meant to take, and that
+# is faster.  Writing and reading them costs about as much as forming them again does at an inner size
 # (a sixth of it for float32 operands, which take six products) that depends on where they stay meanwhile: (bytes,
 # inner size), one line that both meet is enough.  Formed again against held, µs, a step: 33×8192 with 64 45, 41;
 # 777×20011 with 512 159, 148, with 1000 219, 188; 2048×32000 with 512 306, 368, with 1000 525, 525.  Larger ones, for
