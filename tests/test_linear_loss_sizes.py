@@ -44,15 +44,27 @@ def test_a_tiles_place(tmp_path):
 @pytest.mark.parametrize("V,D", [(131072, 64), (32768, 1024), (1000, 256)])
 def test_what_a_backward_call_holds(dtype, value, T, V, D):
     """A piece of the logits' gradient as tgemm.h bounds it (a row of it is up to 128 words longer than its words, a
-    multiple of 256), X, and the sums of dX and dW in up to 64 parts each where they are split."""
+    multiple of 256), X, and the sums of dX and dW, which are taken in parts where their tiles are few."""
     piece = max(256 << 20, 2048 * T * value, 256 * T * value)
     piece = min(piece, (V + 255) // 256 * 256 * T * value) + 128 * (T + 64) * value
     x = (T + 64) * D * (6 if dtype == 0 else 2)
     w = V * D * 6 if dtype == 0 else 0
     need = size(dtype=dtype, T=T, V=V, D=D, ldx=D, ldw=D, backward=1)
     sums = need - (piece + x + w + 12 * (T + 64) + 4096)
-    # in parts only where the tiles are fewer than the GPU holds, 256 of 256×256
-    split = 256 * 256 * 256 * 4 * 2
-    assert sums <= max(4 * (T + 64) * D, split) + split
+    # in parts only up to a few rounds of the 256 tiles of 256×256 that the GPU holds
+    rounds = 4 * 256 * 256 * 256 * 4
+    assert sums <= max(4 * (T + 64) * D, rounds) + rounds
     if T >= 262144 and dtype:
         assert need >= min(V, 2048) * T * value
+
+
+@pytest.mark.parametrize("V,D", [(5000, 1000), (131072, 4096)])
+def test_what_operands_take(V, D):
+    """tgemm.h: float32 in planes, 16-bit ones that lie apart in a copy, others and few rows nothing."""
+    T, planes = 64, 6 * V * D
+    at = dict(T=T, V=V, D=D, ldx=D, ldw=D)
+    apart = dict(at, ldw=D + 1)
+    for backward in (0, 1):
+        stored, copied, float32 = (size(**a, backward=backward) for a in (at, apart, dict(at, dtype=0)))
+        assert 2 * V * D <= copied - stored <= 2 * V * (D + 64) and planes <= float32
+    assert size(**dict(at, T=32, dtype=0)) < planes // 6
