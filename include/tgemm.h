@@ -390,6 +390,12 @@ int64_t tgemm_sgemm_host_workspace_size(int64_t M, int64_t N, int64_t K, int64_t
  *             bytes each, float32 6, up to 128 rows 4), but no more words than
  *             there are; besides it X as the products read it and sums of dX
  *             and dW in float32.
+ *             float32 operands take their planes in either call: 6·V·D bytes
+ *             for W, more than W itself, and 6·T·D for X (up to 32 rows of a
+ *             forward call none).  16-bit ones are read as they are stored
+ *             where D and the leading dimension are multiples of 8 (forward
+ *             calls and fp16: X's D one of 64) and the rows start 16-byte
+ *             aligned, and copied otherwise: 2·V·D.
  * Errors      As above, before anything is queued; also
  *             TGEMM_ERROR_INVALID_VALUE for a missing, misaligned, overlapping
  *             or too small workspace, an output that overlaps an input or
