@@ -13,6 +13,7 @@ import tiled_gemm_tgemm_amd as tg  # noqa: E402
 from tiled_gemm_tgemm_amd import _lib  # noqa: E402
 
 T, V, D, K = 6, 11, 8, 3
+REAL_EMPTY = torch.empty
 ROOM = 1 << 12
 
 
@@ -21,7 +22,7 @@ class Host:
 
     def __init__(self):
         self.stream = 1 << 44
-        self.memory = []  # (memory, address, reference to who has it) of everything allocated; no address comes twice
+        self.memory = []  # (memory, address, reference to who has it) of everything allocated
         self.calls = []   # (entry, arguments)
         self.allocating = []  # called at the next allocations, one each
 
@@ -34,10 +35,14 @@ class Host:
     def room(self, shape, dtype):
         from torch.multiprocessing.reductions import StorageWeakRef
 
-        memory = bytearray(torch.Size([shape] if isinstance(shape, int) else shape).numel() * dtype.itemsize + 64)
-        t = torch.frombuffer(memory, dtype=dtype)[:(len(memory) - 64) // dtype.itemsize].view(shape)
-        self.memory.append((memory, t.data_ptr(), StorageWeakRef(t.untyped_storage())))
-        return t
+        shape = torch.Size([shape] if isinstance(shape, int) else shape)
+        t = REAL_EMPTY((0,), dtype=dtype)
+        if shape.numel():
+            memory = bytearray(shape.numel() * dtype.itemsize + 64)  # stays: no address comes twice
+            room = torch.frombuffer(memory, dtype=dtype, count=shape.numel()).untyped_storage()
+            self.memory.append((memory, room.data_ptr(), StorageWeakRef(room)))
+            t.set_(room, 0, shape)
+        return t if t.shape == shape else t.view(shape)
 
     def copy(self, t):
         return self.room(t.shape, t.dtype).copy_(t.detach())
@@ -163,6 +168,20 @@ def test_a_node_called_under_another_stream_runs_there(host, op, keep, monkeypat
     name, args = host.calls[-1]
     assert name.endswith("backward") and args[-1] == host.stream
     # what the forward pass allocated on its own stream is known to be in use on this one
-    assert len(recorded) == 1 + keep + (op == "kd") and {s for _, s in recorded} == {host.stream}
+    assert len(recorded) == 2 + keep + (op == "kd") and {s for _, s in recorded} == {host.stream}
     torch.autograd.grad(loss, (X, W))
     assert len(host.calls) == 4
+
+
+@pytest.mark.parametrize("op", ["ce", "kd"])
+@pytest.mark.parametrize("reduction,size", [("mean", 12), ("sum", 12), ("none", 4 * T)])
+def test_a_loss_that_is_kept_holds_no_more_than_itself(host, op, reduction, size):
+    X, W = (t.requires_grad_() for t in head())
+    loss = losses()[op](X, W, reduction=reduction)
+    assert loss.shape == ((T,) if reduction == "none" else ()) and not loss._is_view()
+    assert loss.detach().untyped_storage().nbytes() <= size
+    torch.autograd.grad(loss.sum(), (X, W))
+    forward, backward = (args for _, args in host.calls)
+    # lse is the forward call's, and only a mean's gradient has its third number as a factor
+    assert backward[15 if op == "kd" else 10] == forward[16 if op == "kd" else 11]
+    assert backward[21 if op == "kd" else 15] == (forward[-4] + 8 if reduction == "mean" else 0)

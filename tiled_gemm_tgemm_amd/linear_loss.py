@@ -16,7 +16,6 @@ return without waiting.  include/tgemm.h states the arithmetic.
 
 from __future__ import annotations
 
-import copy
 import functools
 
 from . import _lib
@@ -113,7 +112,8 @@ class _Call:
         pass allocated."""
         import torch
 
-        c = copy.copy(self)
+        c = _Call.__new__(_Call)
+        c.__dict__.update(self.__dict__)
         current = torch.cuda.current_stream(c.device)
         if current.cuda_stream != c.stream:
             c.stream = current.cuda_stream
@@ -212,14 +212,22 @@ class _Call:
         if st != _lib.TGEMM_SUCCESS:
             raise TgemmError(st, entry)
 
-    def rows_and_summary(self):
-        """Room for what a differentiable forward pass keeps, in one tensor: the summary (3 floats, the fourth is
-        free), lse and loss; and the addresses of loss, lse and summary."""
+    def results(self, reduction):
+        """What a differentiable forward pass writes to: the tensor that is returned, what is kept for the backward
+        pass (lse first, and the summary, whose third number is the mean's factor), and the addresses of loss, lse and
+        summary.  The returned tensor shares no memory with what grows with the rows."""
         import torch
 
-        kept = torch.empty(4 + 2 * self.T, dtype=torch.float32, device=self.device)
-        at = kept.data_ptr()
-        return kept, (at + 16 + 4 * self.T, at + 16, at)
+        if reduction == "none":
+            loss = torch.empty((self.T,), dtype=torch.float32, device=self.device)
+            lse = torch.empty((self.T,), dtype=torch.float32, device=self.device)
+            return loss, (lse, None), (loss.data_ptr(), lse.data_ptr(), 0)
+        rows = torch.empty((2 * self.T,), dtype=torch.float32, device=self.device)
+        summary = torch.empty((3,), dtype=torch.float32, device=self.device)
+        # `data`: not a view of the summary to torch, so a caller may change it in place
+        loss = summary.as_strided((), (), 1 if reduction == "mean" else 0).data
+        at = rows.data_ptr()
+        return loss, (rows, summary if reduction == "mean" else None), (at + 4 * self.T, at, summary.data_ptr())
 
 
 def _ptr(t):
@@ -309,41 +317,35 @@ def _functions():
     import torch
     from torch.autograd.function import once_differentiable
 
-    def result(c, reduction, kept):
-        # tensors of their own on `kept`, not views of it: a caller may change them in place
-        place, shape = (4 + c.T, (c.T,)) if reduction == "none" else (1 if reduction == "mean" else 0, ())
-        return torch.empty(0, dtype=torch.float32, device=c.device).set_(kept.untyped_storage(), place, shape)
-
-    def gradients(ctx, grad, c, kept):
-        """What _gradients and _grad_loss give, for what torch hands over; and the address of lse."""
+    def gradients(ctx, grad, c, summary):
+        """What _gradients and _grad_loss give, for what torch hands over."""
         need_x, need_w = ctx.needs_input_grad[:2]
         dX = torch.empty((c.T, c.D), dtype=c.dtype, device=c.device) if need_x else None
         dW = torch.empty((c.V, c.D), dtype=c.dtype, device=c.device) if need_w else None
-        at = kept.data_ptr()
         return dX, dW, (grad.data_ptr(), grad.stride(0) if c.T > 1 and grad.dim() else 0,
-                        at + 8 if ctx.reduction == "mean" else 0, _ptr(dX), c.D, _ptr(dW), c.D), at + 16
+                        0 if summary is None else summary.data_ptr() + 8, _ptr(dX), c.D, _ptr(dW), c.D)
 
     class CrossEntropy(torch.autograd.Function):
         @staticmethod
         def forward(ctx, X, W, target, ignore_index, reduction, keep):
             c = _Call(X, W, None)
             target = c.target(target)
-            kept, at = c.rows_and_summary()
+            loss, kept, at = c.results(reduction)
             logits = c.keep(keep) if any(ctx.needs_input_grad) else None
             c.queue("tgemm_linear_ce_forward", target.data_ptr(), int(ignore_index), *at[:2], *c.logits(logits), at[2],
                     *c.room(None, 0, 0))
-            ctx.save_for_backward(X, W, target, kept, logits)
-            ctx.call, ctx.ignore_index, ctx.reduction = c, int(ignore_index), reduction
-            return result(c, reduction, kept)
+            ctx.save_for_backward(X, W, target, *kept, logits)
+            ctx.call, ctx.ignore_index = c, int(ignore_index)
+            return loss
 
         @staticmethod
         @once_differentiable
         def backward(ctx, grad):
-            X, W, target, kept, logits = ctx.saved_tensors
-            c = ctx.call.again(X, W, kept, logits)
-            dX, dW, rest, lse = gradients(ctx, grad, c, kept)
-            c.queue("tgemm_linear_ce_backward", target.data_ptr(), ctx.ignore_index, lse, *c.logits(logits), *rest,
-                    *c.room(None, 0, 1))
+            X, W, target, lse, summary, logits = ctx.saved_tensors
+            c = ctx.call.again(X, W, lse, summary, logits)
+            dX, dW, rest = gradients(ctx, grad, c, summary)
+            c.queue("tgemm_linear_ce_backward", target.data_ptr(), ctx.ignore_index, lse.data_ptr(), *c.logits(logits),
+                    *rest, *c.room(None, 0, 1))
             return dX, dW, None, None, None, None
 
     class Distillation(torch.autograd.Function):
@@ -351,22 +353,22 @@ def _functions():
         def forward(ctx, X, W, teacher_ids, teacher_logits, temperature, reduction, keep):
             c = _Call(X, W, None)
             teacher = c.teacher(teacher_ids, teacher_logits, temperature)
-            kept, at = c.rows_and_summary()
+            loss, kept, at = c.results(reduction)
             student = torch.empty((c.T, c.K), dtype=torch.float32, device=c.device)
             logits = c.keep(keep) if any(ctx.needs_input_grad) else None
             c.queue("tgemm_linear_kd_forward", *teacher, *at[:2], student.data_ptr(), *c.logits(logits), at[2],
                     *c.room(None, c.K, 0))
-            ctx.save_for_backward(X, W, teacher_ids, teacher_logits, kept, student, logits)
-            ctx.call, ctx.temperature, ctx.reduction = c, temperature, reduction
-            return result(c, reduction, kept)
+            ctx.save_for_backward(X, W, teacher_ids, teacher_logits, *kept, student, logits)
+            ctx.call, ctx.temperature = c, temperature
+            return loss
 
         @staticmethod
         @once_differentiable
         def backward(ctx, grad):
-            X, W, ids, top, kept, student, logits = ctx.saved_tensors
-            c = ctx.call.again(X, W, kept, student, logits)
-            dX, dW, rest, lse = gradients(ctx, grad, c, kept)
-            c.queue("tgemm_linear_kd_backward", *c.teacher(ids, top, ctx.temperature), lse, student.data_ptr(),
+            X, W, ids, top, lse, summary, student, logits = ctx.saved_tensors
+            c = ctx.call.again(X, W, lse, summary, student, logits)
+            dX, dW, rest = gradients(ctx, grad, c, summary)
+            c.queue("tgemm_linear_kd_backward", *c.teacher(ids, top, ctx.temperature), lse.data_ptr(), student.data_ptr(),
                     *c.logits(logits), *rest, *c.room(None, c.K, 1))
             return dX, dW, None, None, None, None, None
 
