@@ -25,12 +25,21 @@ REDUCTIONS = ("mean", "sum", "none")
 
 # Unless told otherwise the differentiable calls form the logits again in the backward pass, and hold them (float32)
 # only where all of them take no more than the 256 MiB that a piece of their gradient is meant to take, and that
-# is faster.  Writing and reading them costs about as much as forming them again does at an inner size
-# (a sixth of it for float32 operands, which take six products) that depends on where they stay meanwhile: (bytes,
-# inner size), one line that both meet is enough.  Formed again against held, µs, a step: 33×8192 with 64 45, 41;
-# 777×20011 with 512 159, 148, with 1000 219, 188; 2048×32000 with 512 306, 368, with 1000 525, 525.  Larger ones, for
-# those who ask for it: 4096×32768 with 2048 1778, 1579, with 4096 3289, 2722.
-KEPT = ((4 << 20, 0), (64 << 20, 512), (256 << 20, 1024))
+# is faster.  Writing and reading them costs about as much as forming them again does at an inner size (a sixth of it
+# for float32 operands, which take six products) that depends on where they stay meanwhile: (bytes, inner size), one
+# line that both meet is enough.  A step with them held, of its time with them formed again (cross entropy bf16;
+# distillation up to 0.03 more, float32 at a sixth of the inner size up to 0.12 less), at inner sizes of 64, 256, 512, 768, 1024 and 2048:
+#     1 MiB (33×8192)       0.93  0.91  0.88  0.86  0.84  0.79
+#     8 MiB (128×16384)     0.96  0.93  0.90  0.90  0.89  0.86
+#    32 MiB (512×16384)     1.07  1.02  0.98  0.96  0.93  0.88
+#    59 MiB (777×20011)     1.06  1.00  0.95  0.92  0.88  0.86
+#    80 MiB (1024×20480)    1.13  1.04  0.98  0.94  0.91  0.89
+#    98 MiB (512×50001)     1.14  1.07  1.01  0.99  0.94  0.87
+#   128 MiB (2048×16384)    1.17  1.11  1.04  0.99  0.98  0.90
+#   183 MiB (1500×32000)    1.42  1.26  1.17  1.06  0.99  0.90
+#   250 MiB (2048×32000)    1.55  1.41  1.20  1.05  0.99  0.91
+# Larger ones, for those who ask for it: 4096×32768 (512 MiB) with 2048 0.89, with 4096 0.83.
+KEPT = ((4 << 20, 0), (96 << 20, 512), (256 << 20, 1024))
 
 
 @functools.lru_cache(maxsize=None)
