@@ -214,7 +214,8 @@ bool plan_forward(Plan &p, const Head &h, int64_t teacher_k)
     // where they need no copy of W and the vocabulary gives every compute unit
     // one (µs, tiles against few rows' kernel: 16×32000×2048 bf16 28, 35 and
     // 16×128256×1024 50, 65; 16×16384×2048 25, 21, 32×8192×512 13, 10 and
-    // 32×5000×4096 39, 28; with a copy 20×32000×1001 55, 45, 32 of them 55, 55).
+    // 32×5000×4096 39, 28; with a copy 20×32000×1001 55, 45, 32 of them 55, 55;
+    // the same W call after call, part of which stays in the last-level cache).
     const bool stored = as_stored(h.X, h.ldx, h, kStepK) && as_stored(h.W, h.ldw, h);
     p.few = h.T <= (stored && h.V > kFewBelow ? 8 : kFewRows);
     if (p.few) {

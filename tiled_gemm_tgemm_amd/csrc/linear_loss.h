@@ -57,7 +57,8 @@ hipError_t launch_stats(bool half, int tile, const StatsArgs &a, hipStream_t str
 // about 22 GB/s of W from memory however many wavefronts ask for it, so words
 // are dealt 16 at a time where 64 at a time leave compute units without any:
 // one row of 4000×4096 bf16 11 against 25 µs, of 16000×4096 26 against 28, of
-// 32000×4096 46 against 44, of 65536×1024 29 against 26.
+// 32000×4096 46 against 44, of 65536×1024 29 against 26 (the same W call after
+// call; on others in turn the one that is taken needs 13, 31, 57 and 31).
 constexpr int64_t kFewRows = 32, kFewBelow = 16384;
 inline int few_columns(int64_t V) { return V < kFewBelow ? 16 : 64; }
 hipError_t launch_stats_few(const StatsArgs &a, tgemm_dtype_t dtype, int columns, int D, hipStream_t stream);

@@ -11,12 +11,15 @@
 // in planes, and rows may lie anywhere and have any length, which spares a copy
 // of W in rows of whole steps.
 //
-// With the join: one row of 32000×4096 bf16 44 µs, one of 131072×2048 106 µs
-// (5.1 TB/s), 4 of 56852×2752 float32 155 µs (4.0 TB/s; 185 with one wavefront
-// along k, whose splitting of the operands the loads then wait for; two blocks
-// of rows 52 against 55 at 32×32768×1024, so those keep one).  Rows that start
-// at odd multiples of 2 bytes cost their 16-byte loads twice the time: one row
-// of 32000×4097 109 µs (a copy and the tiles take 200).
+// With the join, on Ws of 1 GiB together in turn: one row of 32000×4096 bf16 57
+// µs (4.6 TB/s), one of 131072×2048 108 (5.0 TB/s), 4 of 56852×2752 float32 161
+// (3.9 TB/s).  The same W call after call stays in the last-level cache in
+// part, and the first takes 45.  So measured: 4×56852×2752 float32 155 against
+// 185 with one wavefront along k, whose splitting of the operands the loads
+// then wait for; 32×32768×1024 with one block of rows 52, with two 55, so
+// those keep one.  Rows that start at odd multiples of 2 bytes cost their
+// 16-byte loads twice the time: one row of 32000×4097 112 µs on Ws in turn (a
+// copy and the tiles take 200).
 #include "linear_loss.h"
 #include "mfma16.h"
 
