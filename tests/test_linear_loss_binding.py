@@ -185,3 +185,22 @@ def test_a_loss_that_is_kept_holds_no_more_than_itself(host, op, reduction, size
     # lse is the forward call's, and only a mean's gradient has its third number as a factor
     assert backward[15 if op == "kd" else 10] == forward[16 if op == "kd" else 11]
     assert backward[21 if op == "kd" else 15] == (forward[-4] + 8 if reduction == "mean" else 0)
+
+
+@pytest.mark.parametrize("op", ["ce", "kd"])
+@pytest.mark.parametrize("kind,other", [(torch.bfloat16, torch.float32), (torch.float32, torch.float16),
+                                        (torch.float16, torch.bfloat16)])
+def test_operands_of_two_types_are_refused(host, op, kind, other):
+    X, W = head()
+    with torch.autocast("cpu", dtype=torch.bfloat16):
+        for autograd in (False, True):
+            x, w = X.to(kind).requires_grad_(autograd), W.to(other).requires_grad_(autograd)
+            with pytest.raises(TypeError, match=f"W must be {kind}"):
+                losses()[op](x, w)
+    with pytest.raises(TypeError, match=f"W must be {kind}"):
+        tg.linear_cross_entropy_forward(X.to(kind), W.to(other), Y)
+    assert not host.calls
+    w = W.to(other).requires_grad_()
+    loss = losses()[op](X.to(kind), w.to(kind))  # as the module says
+    (dW,) = torch.autograd.grad(loss, (w,))
+    assert dW.dtype == other and len(host.calls) == 2

@@ -2,6 +2,9 @@
 
 X (T×D) holds the tokens' hidden states and W (V×D) the head's weight, both
 float32, bfloat16 or float16 on one GPU, row-major with any leading dimension.
+Both have the same type, and gradients have it too: float32 weights beside
+16-bit states (torch.autocast does not reach these calls) raise TypeError;
+`W.to(X.dtype)` there, or `X.to(W.dtype)`, is differentiable.
 
 * ``linear_cross_entropy`` and ``linear_distillation`` are differentiable in X
   and W and reduce over the rows;
