@@ -204,3 +204,23 @@ def test_operands_of_two_types_are_refused(host, op, kind, other):
     loss = losses()[op](X.to(kind), w.to(kind))  # as the module says
     (dW,) = torch.autograd.grad(loss, (w,))
     assert dW.dtype == other and len(host.calls) == 2
+
+
+@pytest.mark.parametrize("name", ["ce_forward", "ce_backward", "kd_forward", "kd_backward"])
+def test_arguments_reach_their_place_in_the_c_call(name, monkeypatch):
+    """Each by its name in the header; those that come last here, and only those, stand elsewhere there."""
+    import inspect
+    import os
+    import re
+
+    with open(os.path.join(os.path.dirname(os.path.dirname(__file__)), "include", "tgemm.h")) as f:
+        declared = re.search(rf"tgemm_linear_{name}\((.*?)\);", f.read(), re.S).group(1)
+    order = [re.search(r"(\w+)$", p.strip()).group(1) for p in declared.split(",")]
+    seen = []
+    monkeypatch.setattr(_lib, "library", lambda: types.SimpleNamespace(
+        **{f"tgemm_linear_{name}": lambda *args: seen.append(args) or 0}))
+    call = getattr(tg, f"tgemm_linear_{name}")
+    here = list(inspect.signature(call).parameters)
+    call(**{p: f"<{p}>" for p in here})
+    assert seen == [tuple(f"<{p}>" for p in order)]
+    assert here[-2:] == ["logits", "ldz"] and here[:-2] == [p for p in order if p not in ("logits", "ldz")]

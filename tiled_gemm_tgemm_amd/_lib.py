@@ -99,6 +99,7 @@ def library():
 
 
 # ---- the C entry points, same names and argument order ---------------------
+# (but the loss operators' `logits` and `ldz`: optional here, they come last)
 
 def tgemm_sgemm(M, N, K, A, lda, B, ldb, C, ldc, stream=None) -> int:
     return library().tgemm_sgemm(M, N, K, A, lda, B, ldb, C, ldc, stream)
