@@ -97,3 +97,39 @@ def test_a_node_called_under_a_late_stream(keep):
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     del junk, held
+
+
+@pytest.mark.parametrize("distill", [False, True])
+@pytest.mark.parametrize("reduction,keep", [("mean", True), ("mean", False), ("none", None)])
+def test_a_differentiable_step_captured_and_replayed(distill, reduction, keep):
+    """Both passes in one graph, on inputs that change between its replays, with eager steps between them."""
+    X, W, g = head(T, V, D, torch.bfloat16, 34)
+    y, (ids, top) = targets(T, V, g), entries(T, V, K, torch.bfloat16, g)
+    up = torch.rand((T,) if reduction == "none" else (), generator=g, device="cuda")
+
+    def step(x, w):
+        loss = (tg.linear_distillation(x, w, ids, top, reduction=reduction, keep_logits=keep) if distill
+                else tg.linear_cross_entropy(x, w, y, reduction=reduction, keep_logits=keep))
+        return (loss.detach(), *torch.autograd.grad(loss, (x, w), up))
+
+    def leaves():  # of each step's own
+        return X.detach().requires_grad_(), W.detach().requires_grad_()
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(*leaves())
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    x, w = leaves()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(x, w)
+    for seed in range(3):
+        X.copy_(torch.randn((T, D), generator=g, device="cuda"))
+        want = [t.clone() for t in step(*leaves())]
+        for t in out:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), f"replay {seed}"
