@@ -68,3 +68,12 @@ def test_what_operands_take(V, D):
         stored, copied, float32 = (size(**a, backward=backward) for a in (at, apart, dict(at, dtype=0)))
         assert 2 * V * D <= copied - stored <= 2 * V * (D + 64) and planes <= float32
     assert size(**dict(at, T=32, dtype=0)) < planes // 6
+
+
+def test_outputs_between_an_inputs_rows_are_refused():
+    """tgemm.h: arrays are taken with what lies between their rows."""
+    from test_linear_loss import DX, X_, ce_backward
+
+    assert ce_backward(ldx=128, dX=X_ + 128, lddx=128) == tg.TGEMM_ERROR_INVALID_VALUE
+    assert ce_backward(dX=DX, lddx=128, dW=DX + 128, lddw=128) == tg.TGEMM_ERROR_INVALID_VALUE
+
