@@ -400,8 +400,9 @@ int64_t tgemm_sgemm_host_workspace_size(int64_t M, int64_t N, int64_t K, int64_t
  *             TGEMM_ERROR_INVALID_VALUE for a missing, misaligned, overlapping
  *             or too small workspace, an output that overlaps an input or
  *             another output (each taken from its first element to its last,
- *             with what lies between its rows), a misaligned or missing array, a negative
- *             grad_step, a temperature that is not positive and finite.
+ *             with what lies between its rows), a misaligned or missing array,
+ *             a negative grad_step, a temperature that is not positive and
+ *             finite.
  * Indices     An index out of [0, V) is never used as an address: its row's
  *             loss is NaN, and so are its row of dX and all of dW.
  * Rows        A row that does not count (its target is ignore_index, or all of

@@ -224,3 +224,17 @@ def test_arguments_reach_their_place_in_the_c_call(name, monkeypatch):
     call(**{p: f"<{p}>" for p in here})
     assert seen == [tuple(f"<{p}>" for p in order)]
     assert here[-2:] == ["logits", "ldz"] and here[:-2] == [p for p in order if p not in ("logits", "ldz")]
+
+
+@pytest.mark.parametrize("op", ["ce", "kd"])
+@pytest.mark.parametrize("reduction", ["mean", "sum", "none"])
+def test_without_autograd_nothing_is_kept(host, op, reduction):
+    X, W = (t.requires_grad_() for t in head())
+    for without in (torch.no_grad, torch.inference_mode):
+        with without():
+            loss = losses()[op](X, W, reduction=reduction, keep_logits=True)
+            loss += 1.0
+        assert not loss.requires_grad and loss.shape == ((T,) if reduction == "none" else ())
+    assert all(args[18 if op == "kd" else 12] == 0 for _, args in host.calls)
+    del loss
+    assert all(ref.expired() for _, _, ref in host.memory)

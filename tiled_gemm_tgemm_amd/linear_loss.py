@@ -31,7 +31,8 @@ REDUCTIONS = ("mean", "sum", "none")
 # is faster.  Writing and reading them costs about as much as forming them again does at an inner size (a sixth of it
 # for float32 operands, which take six products) that depends on where they stay meanwhile: (bytes, inner size), one
 # line that both meet is enough.  A step with them held, of its time with them formed again (cross entropy bf16;
-# distillation up to 0.03 more, float32 at a sixth of the inner size up to 0.12 less), at inner sizes of 64, 256, 512, 768, 1024 and 2048:
+# distillation up to 0.03 more, float32 at a sixth of the inner size up to 0.12 less), at inner sizes of 64, 256, 512,
+# 768, 1024 and 2048:
 #     1 MiB (33×8192)       0.93  0.91  0.88  0.86  0.84  0.79
 #     8 MiB (128×16384)     0.96  0.93  0.90  0.90  0.89  0.86
 #    32 MiB (512×16384)     1.07  1.02  0.98  0.96  0.93  0.88
