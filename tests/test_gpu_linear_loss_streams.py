@@ -133,3 +133,40 @@ def test_a_differentiable_step_captured_and_replayed(distill, reduction, keep):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want)), f"replay {seed}"
+
+
+def test_steps_of_several_threads_at_once():
+    """Threads share torch's current stream by default, and torch's backward thread."""
+    import concurrent.futures
+
+    X, W, g = head(T, V, D, torch.bfloat16, 35)
+    ys, (ids, top) = [targets(T, V, g) for _ in range(4)], entries(T, V, K, torch.bfloat16, g)
+
+    def step(y, distill):
+        x, w = X.detach().requires_grad_(), W.detach().requires_grad_()
+        loss = tg.linear_distillation(x, w, ids, top) if distill else tg.linear_cross_entropy(x, w, y)
+        first = torch.autograd.grad(loss, (x, w), retain_graph=True)
+        return (loss.detach(), *first, *torch.autograd.grad(loss, (x, w)))
+
+    calls = [(y, distill) for y in ys for distill in (False, True)]
+    want = [step(*c) for c in calls]
+    torch.cuda.synchronize()
+    with concurrent.futures.ThreadPoolExecutor(4) as pool:
+        for _ in range(5):
+            got = list(pool.map(lambda c: step(*c), calls))
+            torch.cuda.synchronize()
+            for a, b in zip(got, want):
+                assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_two_threads_through_one_graph():
+    import concurrent.futures
+
+    X, W, g = head(T, V, D, torch.bfloat16, 36)
+    x, w = X.detach().requires_grad_(), W.detach().requires_grad_()
+    y = targets(T, V, g)
+    loss = tg.linear_cross_entropy(x, w, y)
+    want = torch.autograd.grad(loss, (x, w), retain_graph=True)
+    with concurrent.futures.ThreadPoolExecutor(4) as pool:
+        for got in pool.map(lambda n: torch.autograd.grad(loss, (x, w), retain_graph=True), range(24)):
+            assert all(torch.equal(p, q) for p, q in zip(got, want))
