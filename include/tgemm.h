@@ -61,7 +61,7 @@ typedef enum tgemm_op {
     TGEMM_OP_T = 1  /* op(X) = Xᵀ */
 } tgemm_op_t;
 
-/* Element types of the loss operators' operands. */
+/* Element types of the operators on 16-bit tiles: losses, adapters, orthogonalised updates. */
 typedef enum tgemm_dtype {
     TGEMM_F32 = 0,
     TGEMM_BF16 = 1,
@@ -478,6 +478,58 @@ tgemm_status_t tgemm_linear_kd_backward(tgemm_dtype_t dtype, int64_t T, int64_t 
                                         const float *grad_loss, int64_t grad_step, const float *grad_weight,
                                         void *dX, int64_t lddx, void *dW, int64_t lddw,
                                         void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * An update made orthogonal by Newton-Schulz products
+ * ---------------------------------------------------
+ * For each of `batch` matrices G (M×N, rows ldg >= N apart, stride_g >= 0
+ * elements from one matrix to the next), in place of G the result of
+ *   X = G / (|G| + eps),                       |G| the root of the sum of squares
+ *   steps times:  S = X·Xᵀ,  X <- a·X + (b·S + c·S·S)·X
+ * is written to out (rows ldo >= N apart, matrices stride_out apart, which do
+ * not overlap).  Where M > N, S = Xᵀ·X stands on the other side, which is the
+ * same on the transpose.  With the coefficients 3.4445, -4.7750, 2.0315 five
+ * steps bring the singular values of G to between 0.7 and 1.2 and leave its
+ * singular vectors as they are, as the Muon optimiser takes its updates.
+ *
+ * Types       float32, bf16 or fp16, G and out alike.
+ * Arithmetic  Where the smaller side is at most 64 the iteration runs on G·Gᵀ in
+ *             float64.  Otherwise X, S and b·S + c·S·S are held in two fp16
+ *             planes (22 bits, and no finer than 2^-35 of 1), products are
+ *             summed in float32, and |G| in float64.  bf16 results take fewer
+ *             products of planes: their error is that of their own rounding
+ *             and up to half as much besides; float32 ones are as close as a
+ *             chain of float32 products.  Entries of X, S or b·S + c·S·S
+ *             beyond 60 overflow there, which coefficients that let singular
+ *             values grow can come to.
+ * coefficients  3·steps floats in host memory: a, b, c of each step.
+ * Sizes       0 <= batch <= 65535, M and N up to 2^20, 1 <= steps <= 32,
+ *             leading dimensions and strides up to 2^40; larger ones, batches
+ *             of 2^31 tiles and more, and an unknown dtype:
+ *             TGEMM_ERROR_NOT_SUPPORTED.  Nothing is written if batch, M or N
+ *             is 0.
+ * Workspace   Device memory of the caller, 16-byte aligned, at least
+ *             tgemm_orthogonalize_workspace_size(...) bytes (up to 64 on the
+ *             smaller side little, otherwise about 16·M·N + 8·min(M,N)² a matrix
+ *             with M and N in whole 64s), overlapping neither G nor out.  Its contents on entry do not matter.
+ *             Two calls in flight at once need two.
+ * Errors      As above, before anything is queued; also
+ *             TGEMM_ERROR_INVALID_VALUE for an eps that is negative or not
+ *             finite, missing coefficients, and an out that overlaps G or
+ *             whose matrices overlap one another.
+ * Values      A matrix of zeros gives zeros (NaN with an eps of 0); one that
+ *             holds an infinity or NaN gives NaN everywhere.
+ * Order       Sums are taken in a fixed order: the same call gives the same
+ *             bits.  Every call can be captured into a graph.
+ */
+tgemm_status_t tgemm_orthogonalize(tgemm_dtype_t dtype, int64_t batch, int64_t M, int64_t N,
+                                   const void *G, int64_t ldg, int64_t stride_g,
+                                   int steps, const float *coefficients, float eps,
+                                   void *out, int64_t ldo, int64_t stride_out,
+                                   void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace of that call; 0 if batch, M or N is 0 or the arguments are refused. */
+size_t tgemm_orthogonalize_workspace_size(tgemm_dtype_t dtype, int64_t batch, int64_t M, int64_t N, int steps);
 
 /* Static, human-readable text for a status code. */
 const char *tgemm_status_string(tgemm_status_t status);

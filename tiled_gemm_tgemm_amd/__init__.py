@@ -4,8 +4,9 @@ The compute lives in the C-ABI library libtgemm.so (sources in csrc/,
 declarations in include/tgemm.h).  ``_lib`` exposes the C entry points under
 their own names; ``sgemm`` and ``transpose`` below are the same calls for
 torch tensors, with torch used for device memory and the current stream only,
-and ``linear_cross_entropy`` and ``linear_distillation`` the losses on an output
-head's product, with their gradients.
+``linear_cross_entropy`` and ``linear_distillation`` the losses on an output
+head's product, with their gradients, and ``orthogonalize`` an update made orthogonal
+by Newton-Schulz products.
 
 Nothing here loads the library at import time; the first call does, and it
 raises if libtgemm.so has not been built (``python -m
@@ -44,6 +45,8 @@ from ._lib import (  # noqa: F401
     tgemm_linear_kd_backward,
     tgemm_linear_kd_forward,
     tgemm_linear_loss_workspace_size,
+    tgemm_orthogonalize,
+    tgemm_orthogonalize_workspace_size,
     TGEMM_BF16,
     TGEMM_F16,
     TGEMM_F32,
@@ -67,6 +70,8 @@ from .linear_loss import (  # noqa: F401
     linear_distillation_backward,
     linear_distillation_forward,
 )
+
+from .orthogonalize import orthogonalize  # noqa: F401
 
 KERNELS = ("auto", "mfma", "naive", "lds", "simt")
 

@@ -69,6 +69,9 @@ SIGNATURES = {
     "tgemm_linear_ce_backward": (ctypes.c_int, _HEAD + [_ptr, _i64, _ptr] + _KEPT + _GRADS + _ROOM),
     "tgemm_linear_kd_forward": (ctypes.c_int, _HEAD + _TEACHER + [_ptr] * 3 + _KEPT + [_ptr] + _ROOM),
     "tgemm_linear_kd_backward": (ctypes.c_int, _HEAD + _TEACHER + [_ptr] * 2 + _KEPT + _GRADS + _ROOM),
+    "tgemm_orthogonalize": (ctypes.c_int, [ctypes.c_int, _i64, _i64, _i64, _ptr, _i64, _i64, ctypes.c_int, _ptr,
+                                           ctypes.c_float, _ptr, _i64, _i64] + _ROOM),
+    "tgemm_orthogonalize_workspace_size": (ctypes.c_size_t, [ctypes.c_int, _i64, _i64, _i64, ctypes.c_int]),
     "tgemm_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "tgemm_version": (ctypes.c_int, []),
 }
@@ -204,6 +207,17 @@ def tgemm_linear_kd_backward(dtype, T, V, D, X, ldx, W, ldw, K, teacher_ids, ld_
                                               teacher_logits, ld_logits, temperature, lse, student, logits, ldz,
                                               grad_loss, grad_step, grad_weight, dX, lddx, dW, lddw, workspace,
                                               workspace_bytes, stream)
+
+
+def tgemm_orthogonalize(dtype, batch, M, N, G, ldg, stride_g, steps, coefficients, eps, out, ldo, stride_out, workspace,
+                        workspace_bytes, stream=None) -> int:
+    """coefficients: the address of 3·steps floats in host memory, or a ctypes array of them."""
+    return library().tgemm_orthogonalize(dtype, batch, M, N, G, ldg, stride_g, steps, coefficients, eps, out, ldo,
+                                         stride_out, workspace, workspace_bytes, stream)
+
+
+def tgemm_orthogonalize_workspace_size(dtype, batch, M, N, steps) -> int:
+    return library().tgemm_orthogonalize_workspace_size(dtype, batch, M, N, steps)
 
 
 def tgemm_mfma_variant_count() -> int:

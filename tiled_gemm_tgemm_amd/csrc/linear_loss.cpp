@@ -2,6 +2,7 @@
 // checks, the plan of a call (operand copies, pieces of the vocabulary, tiles,
 // workspace) and its launches on the caller's stream.  The declarations, with
 // the meaning of every argument, are in tgemm.h.
+#include "entry.h"
 #include "linear_loss.h"
 
 #include <hip/hip_runtime.h>
@@ -9,6 +10,7 @@
 
 namespace {
 
+using namespace tgemm::entry;
 using namespace tgemm::loss;
 using tgemm::m16::kStepK;
 using tgemm::m16::Operands;
@@ -42,48 +44,6 @@ constexpr int64_t kMinPiece = 2048, kMaxPiece = (int64_t)1 << 22;
 // is what takes it (distillation backward at 32000×2048 with 8, 33 and 128
 // rows 115 -> 113, 114 -> 122 and 138 -> 159 µs; 512 rows would be 244 -> 350).
 constexpr int64_t kTwoPlaneRows = 128;
-
-int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-size_t size_of(tgemm_dtype_t t) { return t == TGEMM_F32 ? 4 : 2; }
-bool known(tgemm_dtype_t t) { return t == TGEMM_F32 || t == TGEMM_BF16 || t == TGEMM_F16; }
-
-tgemm_status_t from_hip(hipError_t e) { return e == hipSuccess ? TGEMM_SUCCESS : TGEMM_ERROR_HIP; }
-
-// A byte range that a call reads or writes.
-struct Range {
-    uintptr_t lo = 0, hi = 0;
-};
-
-// False if `rows` rows of `cols` elements, `ld` apart, are not at p: null,
-// misaligned or past the end of the address space.  Nothing is at an empty one.
-bool at(const void *p, int64_t rows, int64_t cols, int64_t ld, size_t size, Range &r)
-{
-    r = Range();
-    if (rows == 0 || cols == 0) return true;
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    if (p == nullptr || lo % size) return false;
-    const unsigned __int128 end =
-        (unsigned __int128)lo + ((unsigned __int128)(rows - 1) * (uint64_t)ld + (uint64_t)cols) * size;
-    if (end > (unsigned __int128)UINTPTR_MAX) return false;
-    r.lo = lo;
-    r.hi = (uintptr_t)end;
-    return true;
-}
-
-bool apart(const Range &a, const Range &b) { return a.lo >= b.hi || b.lo >= a.hi; }
-
-// What is written overlaps nothing else.
-bool disjoint(const Range *written, int n_written, const Range *read, int n_read)
-{
-    for (int i = 0; i < n_written; ++i) {
-        for (int j = i + 1; j < n_written; ++j)
-            if (!apart(written[i], written[j])) return false;
-        for (int j = 0; j < n_read; ++j)
-            if (!apart(written[i], read[j])) return false;
-    }
-    return true;
-}
 
 struct Head {
     tgemm_dtype_t dtype;
@@ -286,20 +246,6 @@ Operands operands(int segments, int64_t M, int64_t N, int64_t steps, int tile)
     o.splits = 1;
     return o;
 }
-
-// The workspace's bytes and range; false if it is missing, misaligned or small.
-bool room_at(void *workspace, size_t bytes, const Plan &p, Range &r)
-{
-    if (p.total == 0) return true;
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(workspace);
-    if (workspace == nullptr || lo % 16 || bytes < (size_t)p.total || bytes > UINTPTR_MAX - lo) return false;
-    r.lo = lo;
-    r.hi = lo + (size_t)p.total;
-    return true;
-}
-
-template <class T>
-T *in(void *workspace, int64_t offset) { return offset < 0 ? nullptr : (T *)((char *)workspace + offset); }
 
 // Lays out `rows` rows of an operand at dst.
 CopyArgs copy_of(const Plan &p, const Head &h, const void *src, int64_t ld, int64_t rows, void *dst, int64_t rows_out)
@@ -620,7 +566,7 @@ tgemm_status_t tgemm_linear_ce_forward(tgemm_dtype_t dtype, int64_t T, int64_t V
     Range r[3], w[5];
     if (!at(X, T, D, ldx, size_of(dtype), r[0]) || !at(W, V, D, ldw, size_of(dtype), r[1]) ||
         !at(target, T, 1, 1, 8, r[2]) || !at(loss, T, 1, 1, 4, w[0]) || !at(lse, T, 1, 1, 4, w[1]) ||
-        !at(summary, summary ? 1 : 0, 3, 3, 4, w[2]) || !room_at(workspace, workspace_bytes, p, w[3]) ||
+        !at(summary, summary ? 1 : 0, 3, 3, 4, w[2]) || !room_at(workspace, workspace_bytes, p.total, w[3]) ||
         !at(logits, logits ? T : 0, V, ldz, 4, w[4]) || !disjoint(w, 5, r, 3))
         return TGEMM_ERROR_INVALID_VALUE;
     return forward(p, h, Labels{target, ignore_index, nullptr}, loss, lse, nullptr, z, summary, workspace, stream);
@@ -648,7 +594,7 @@ tgemm_status_t tgemm_linear_ce_backward(tgemm_dtype_t dtype, int64_t T, int64_t 
         !at(target, T, 1, 1, 8, r[2]) || !at(lse, T, 1, 1, 4, r[3]) ||
         !at(grad_loss, T, 1, grad_step, 4, r[4]) || !at(grad_weight, T && grad_weight ? 1 : 0, 1, 1, 4, r[5]) ||
         !at(dX, dX ? T : 0, D, lddx, size_of(dtype), w[0]) || !at(dW, dW ? V : 0, D, lddw, size_of(dtype), w[1]) ||
-        !room_at(workspace, workspace_bytes, p, w[2]) || !at(logits, logits ? T : 0, V, ldz, 4, r[6]) || !disjoint(w, 3, r, 7))
+        !room_at(workspace, workspace_bytes, p.total, w[2]) || !at(logits, logits ? T : 0, V, ldz, 4, r[6]) || !disjoint(w, 3, r, 7))
         return TGEMM_ERROR_INVALID_VALUE;
     if (T == 0) return dW ? from_hip(launch_zero(dW, lddw, dtype, V, D, stream)) : TGEMM_SUCCESS;
     return backward(p, h, Labels{target, ignore_index, nullptr}, grad_loss, grad_step, grad_weight, lse, nullptr, z, dX,
@@ -675,7 +621,7 @@ tgemm_status_t tgemm_linear_kd_forward(tgemm_dtype_t dtype, int64_t T, int64_t V
     if (!at(X, T, D, ldx, size_of(dtype), r[0]) || !at(W, V, D, ldw, size_of(dtype), r[1]) ||
         !at(teacher_ids, T, K, ld_ids, 8, r[2]) || !at(teacher_logits, T, K, ld_logits, size_of(teacher_dtype), r[3]) ||
         !at(loss, T, 1, 1, 4, w[0]) || !at(lse, T, 1, 1, 4, w[1]) || !at(student, T, K, K, 4, w[2]) ||
-        !at(summary, summary ? 1 : 0, 3, 3, 4, w[3]) || !room_at(workspace, workspace_bytes, p, w[4]) ||
+        !at(summary, summary ? 1 : 0, 3, 3, 4, w[3]) || !room_at(workspace, workspace_bytes, p.total, w[4]) ||
         !at(logits, logits ? T : 0, V, ldz, 4, w[5]) || !disjoint(w, 6, r, 4))
         return TGEMM_ERROR_INVALID_VALUE;
     const Teacher t{(int)K, teacher_ids, ld_ids, teacher_logits, ld_logits, teacher_dtype, 1.0f / temperature};
@@ -708,7 +654,7 @@ tgemm_status_t tgemm_linear_kd_backward(tgemm_dtype_t dtype, int64_t T, int64_t 
         !at(lse, T, 1, 1, 4, r[4]) || !at(student, T, K, K, 4, r[5]) ||
         !at(grad_loss, T, 1, grad_step, 4, r[6]) || !at(grad_weight, T && grad_weight ? 1 : 0, 1, 1, 4, r[7]) ||
         !at(dX, dX ? T : 0, D, lddx, size_of(dtype), w[0]) || !at(dW, dW ? V : 0, D, lddw, size_of(dtype), w[1]) ||
-        !room_at(workspace, workspace_bytes, p, w[2]) || !at(logits, logits ? T : 0, V, ldz, 4, r[8]) || !disjoint(w, 3, r, 9))
+        !room_at(workspace, workspace_bytes, p.total, w[2]) || !at(logits, logits ? T : 0, V, ldz, 4, r[8]) || !disjoint(w, 3, r, 9))
         return TGEMM_ERROR_INVALID_VALUE;
     if (T == 0) return dW ? from_hip(launch_zero(dW, lddw, dtype, V, D, stream)) : TGEMM_SUCCESS;
     const Teacher t{(int)K, teacher_ids, ld_ids, teacher_logits, ld_logits, teacher_dtype, 1.0f / temperature};

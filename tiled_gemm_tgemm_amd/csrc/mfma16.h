@@ -189,7 +189,7 @@ __device__ __forceinline__ void spread()
 // where a tile ends, so the next tile's are under way by then; as loads come
 // back in order, the epilogue would wait for those with its own.  What it needs
 // for its rows is what `prologue(row0, col0)` returned before the products.
-template <class E, int BM, int BN, int WM, int WN, bool A_MC, bool B_MC>
+template <class E, int BM, int BN, int WM, int WN, bool A_MC, bool B_MC, class Op = Operands>
 struct TileProduct {
     static constexpr int kThreads = 64 * WM * WN;
     static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
@@ -199,11 +199,11 @@ struct TileProduct {
     typedef f32x4 Acc[FM][FN];
 
     template <class Prologue, class Epilogue>
-    static __device__ __forceinline__ void run(const Operands &p, lds_char *lds, Prologue prologue, Epilogue epilogue)
+    static __device__ __forceinline__ void run(const Op &p, lds_char *lds, Prologue prologue, Epilogue epilogue)
     {
         const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
         const int wm = wave / WN, wn = wave % WN;
-        const int tiles = p.tiles_m * p.tiles_n * p.splits;
+        const int tiles = p.ids();
         typedef Slice<BM, FM, kThreads, A_MC, false> SliceA;
         typedef Slice<BN, FN, kThreads, B_MC, true> SliceB;
         Loader<SliceA> la;
@@ -216,7 +216,7 @@ struct TileProduct {
         constexpr int kReadsA = FM / 2 * (A_MC ? 2 : 1), kReadsB = FN * (B_MC ? 2 : 1);
 
         // the loads' way through the tiles
-        Walk<BM, BN, A_MC, B_MC> walk;
+        Walk<BM, BN, A_MC, B_MC, Op> walk;
         walk.begin(p, blockIdx.x);
         auto seek = [&]() {
             const auto moved = walk.seek(p, gridDim.x);

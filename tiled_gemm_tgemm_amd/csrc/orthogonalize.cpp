@@ -1,0 +1,326 @@
+// C entry points of the Newton-Schulz operator: argument checks, the plan of a
+// call and its launches on the caller's stream.  The declarations, with the
+// meaning of every argument, are in tgemm.h.
+#include "entry.h"
+#include "orthogonalize.h"
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace {
+
+using namespace tgemm::entry;
+using namespace tgemm::ortho;
+using tgemm::m16::kStepK;
+
+constexpr int64_t kMaxSide = (int64_t)1 << 20;   // a tile's offsets fit 32 bits
+constexpr int64_t kMaxBatch = 65535;             // a launch's y
+constexpr int64_t kMaxLd = (int64_t)1 << 40;
+constexpr int64_t kMaxTiles = INT32_MAX - 1024;
+
+struct Stack {
+    tgemm_dtype_t dtype;
+    int64_t batch, M, N;
+    int steps;
+};
+
+// How many products of planes the three products of step `step` take.
+//
+// X is held in two planes throughout.  While the singular values are small, the
+// first steps change X by little more than its factor, and what one plane
+// leaves out of the products does not show.  A bf16 result is rounded by 1.7e-3
+// (norms over norm); with one plane everywhere X's would carry 0.4e-3 to
+// 2.6e-3 besides (0.04 where X itself is held in one, on a matrix of rank 16
+// with noise of a hundredth), with the choice here 0.2e-3 to 0.6e-3.  One
+// plane in the first step alone is still too few for fp16 results (2.1e-4),
+// which it takes to 2.9e-4 on a matrix of rank 4 with noise.
+struct Segments {
+    int s, q, x;
+};
+Segments segments_of(tgemm_dtype_t dtype, int step)
+{
+    if (dtype == TGEMM_BF16) return step < 2 ? Segments{1, 1, 1} : Segments{1, 3, 3};
+    return Segments{3, 3, 3};
+}
+
+// The tile for `batch` M×N products of `steps` steps, and whether only the
+// tiles on and below the diagonal are formed: the least estimated time, in µs.
+struct Choice {
+    int tile = -1;
+    bool lower = false;
+};
+Choice choose(int64_t M, int64_t N, int64_t steps, int64_t batch, bool symmetric)
+{
+    static const double rate[] = {1.0, 0.83, 0.45}, across[] = {12.0, 6.0, 2.0};
+    Choice best;
+    double least = -1;
+    for (int i = 0; i < kTileCount; ++i) {
+        const TileShape &s = kTiles[i];
+        const int64_t m = ceil_div(M, s.side), n = ceil_div(N, s.side);
+        for (int lower = 0; lower <= (symmetric ? 1 : 0); ++lower) {
+            const int64_t tiles = (lower ? m * (m + 1) / 2 : m * n);
+            if (tiles > kMaxTiles / batch) continue;
+            const int64_t on_one = ceil_div(tiles * batch, 256);
+            auto round = [&](int64_t held) {
+                const double step = (double)held * s.side * s.side / 65536.0 / rate[i] * 1.5;
+                return (double)steps * (step > 0.5 ? step : 0.5) + 4.0 + (lower ? across[i] : 0.0);
+            };
+            double time = (double)(on_one / s.wg_per_cu) * round(s.wg_per_cu);
+            if (on_one % s.wg_per_cu != 0) time += round(on_one % s.wg_per_cu);
+            if (least < 0 || time < least) {
+                least = time;
+                best.tile = i;
+                best.lower = lower != 0;
+            }
+        }
+    }
+    return best;
+}
+
+// Where a call's buffers lie in its workspace, and the sizes of its matrices.
+struct Plan {
+    bool small = false, tall = false;
+    int64_t side = 0, length = 0;              // the smaller and the larger of M and N
+    int64_t side_p = 0, length_p = 0;          // in whole steps of K
+    int64_t total = 0;
+    // the chain
+    int parts = 0;
+    int64_t x_rows = 0, x_ld = 0;
+    int64_t squares = -1, x[2] = {-1, -1}, s = -1, q = -1;
+    // the small side's
+    int64_t part_length = 0, grams = -1, factor = -1;
+
+    int64_t take(int64_t bytes)
+    {
+        const int64_t at = total;
+        total += round_up(bytes, 256);
+        return at;
+    }
+};
+
+bool make_plan(Plan &p, const Stack &g)
+{
+    p.tall = g.M > g.N;
+    p.side = p.tall ? g.N : g.M;
+    p.length = p.tall ? g.M : g.N;
+    p.side_p = round_up(p.side, kStepK);
+    p.length_p = round_up(p.length, kStepK);
+    p.small = p.side <= kSmallSide;
+    if (p.small) {
+        const int64_t blocks = blocks_of((int)p.side), most = blocks == 4 ? 16 : 32;
+        p.part_length = round_up(ceil_div(p.length, most), 128);
+        if (p.part_length < 256) p.part_length = 256;
+        p.parts = (int)ceil_div(p.length, p.part_length);
+        p.grams = p.take(g.batch * p.parts * (blocks * (blocks + 1) / 2) * 256 * 8);
+        p.factor = p.take(g.batch * 256 * blocks * blocks * 8);
+        return true;
+    }
+    const int64_t pieces = g.M * ceil_div(g.N, 8);
+    p.parts = (int)(pieces / 1024 + 1 < kMaxSquares ? pieces / 1024 + 1 : kMaxSquares);
+    // S = Xᵀ·X of a tall X sums over its rows, in whole steps
+    p.x_rows = p.tall ? p.length_p : p.side;
+    p.x_ld = p.tall ? p.side_p : p.length_p;
+    p.squares = p.take(g.batch * p.parts * 8);
+    const int64_t x = g.batch * 2 * p.x_rows * p.x_ld * 2, s = g.batch * 2 * p.side * p.side_p * 2;
+    p.x[0] = p.take(x);
+    if (g.steps > 1) p.x[1] = p.take(x);
+    p.s = p.take(s);
+    p.q = p.take(s);
+    return choose(p.side, p.side, 1, g.batch, false).tile >= 0 && choose(g.M, g.N, 1, g.batch, false).tile >= 0;
+}
+
+tgemm_status_t check(const Stack &g, float eps)
+{
+    if (g.batch < 0 || g.M < 0 || g.N < 0 || g.steps < 1 || !(eps >= 0.0f) || __builtin_isinf(eps))
+        return TGEMM_ERROR_INVALID_VALUE;
+    if (!known(g.dtype) || g.batch > kMaxBatch || g.M > kMaxSide || g.N > kMaxSide || g.steps > kMaxSteps)
+        return TGEMM_ERROR_NOT_SUPPORTED;
+    return TGEMM_SUCCESS;
+}
+
+Chain product(int64_t M, int64_t N, int64_t steps, int segments, int64_t batch, Choice c)
+{
+    Chain o{};
+    o.segments = segments;
+    o.M = (int)M;
+    o.N = (int)N;
+    o.steps = o.steps_per_split = (int)steps;
+    o.tiles_m = (int)ceil_div(M, kTiles[c.tile].side);
+    o.tiles_n = (int)ceil_div(N, kTiles[c.tile].side);
+    o.splits = (int)batch;
+    o.lower = c.lower;
+    return o;
+}
+
+tgemm_status_t run_small(const Plan &p, const Stack &g, const void *G, int64_t ldg, int64_t batch_g, const float *coefficients,
+                         float eps, void *out, int64_t ldo, int64_t batch_o, void *ws, hipStream_t stream)
+{
+    SmallArgs a{};
+    a.G = G;
+    a.ld = ldg;
+    a.batch_g = batch_g;
+    a.dtype = g.dtype;
+    a.batch = (int)g.batch;
+    a.side = (int)p.side;
+    a.length = p.length;
+    a.tall = p.tall;
+    a.grams = in<double>(ws, p.grams);
+    a.part_length = p.part_length;
+    a.parts = p.parts;
+    a.steps = g.steps;
+    for (int n = 0; n < 3 * g.steps; ++n) a.coefficients[n] = coefficients[n];
+    a.eps = eps;
+    a.factor = in<double>(ws, p.factor);
+    a.out = out;
+    a.ldo = ldo;
+    a.batch_o = batch_o;
+    hipError_t e = launch_grams(a, stream);
+    if (e == hipSuccess) e = launch_iterate(a, stream);
+    if (e == hipSuccess) e = launch_apply(a, stream);
+    return from_hip(e);
+}
+
+tgemm_status_t run_chain(const Plan &p, const Stack &g, const void *G, int64_t ldg, int64_t batch_g, const float *coefficients,
+                         float eps, void *out, int64_t ldo, int64_t batch_o, void *ws, hipStream_t stream)
+{
+    const int64_t x_plane = p.x_rows * p.x_ld, s_plane = p.side * p.side_p;
+    SplitArgs c{};
+    c.G = G;
+    c.ld = ldg;
+    c.batch_g = batch_g;
+    c.dtype = g.dtype;
+    c.batch = (int)g.batch;
+    c.rows = g.M;
+    c.cols = g.N;
+    c.squares = in<double>(ws, p.squares);
+    c.parts = p.parts;
+    c.eps = eps;
+    c.planes = in<void>(ws, p.x[0]);
+    c.rows_out = p.x_rows;
+    c.ldo = p.x_ld;
+    c.plane = x_plane;
+    c.batch_out = 2 * x_plane;
+    hipError_t e = launch_squares(c, stream);
+    if (e == hipSuccess) e = launch_split(c, stream);
+    if (e != hipSuccess) return from_hip(e);
+
+    const float one = 1.0f / (1 << kShift);
+    void *s = in<void>(ws, p.s), *q = in<void>(ws, p.q);
+    for (int step = 0; step < g.steps; ++step) {
+        const Segments n = segments_of(g.dtype, step);
+        const float *k = coefficients + 3 * step;
+        void *x = in<void>(ws, p.x[step & 1]);
+
+        const int64_t s_steps = p.length_p / kStepK, q_steps = p.side_p / kStepK;
+        Choice tile = choose(p.side, p.side, s_steps * n.s, g.batch, true);
+        ChainArgs a{};
+        a.op = product(p.side, p.side, s_steps, n.s, g.batch, tile);
+        a.op.A = a.op.B = x;
+        a.op.lda = a.op.ldb = p.x_ld;
+        a.op.plane_a = a.op.plane_b = x_plane;
+        a.op.batch_a = a.op.batch_b = 2 * x_plane;
+        a.op.mn_a = a.op.mn_b = (int)(p.tall ? p.x_ld : p.side);
+        a.op.k_a = a.op.k_b = (int)p.length_p;
+        a.beta = one;
+        a.planes = s;
+        a.ldo = p.side_p;
+        a.plane_out = s_plane;
+        a.batch_out = 2 * s_plane;
+        a.rows = (int)p.side;
+        e = launch_chain(p.tall ? kColumns : kRows, tile.tile, a, stream);
+        if (e != hipSuccess) return from_hip(e);
+
+        tile = choose(p.side, p.side, q_steps * n.q, g.batch, true);
+        a.op = product(p.side, p.side, q_steps, n.q, g.batch, tile);
+        a.op.A = a.op.B = s;
+        a.op.lda = a.op.ldb = p.side_p;
+        a.op.plane_a = a.op.plane_b = s_plane;
+        a.op.batch_a = a.op.batch_b = 2 * s_plane;
+        a.op.mn_a = a.op.mn_b = (int)p.side;
+        a.op.k_a = a.op.k_b = (int)p.side_p;
+        a.add = s;
+        a.ld_add = p.side_p;
+        a.plane_add = s_plane;
+        a.batch_add = 2 * s_plane;
+        a.alpha = k[1];
+        a.beta = k[2] * one;
+        a.planes = q;
+        e = launch_chain(kRows, tile.tile, a, stream);
+        if (e != hipSuccess) return from_hip(e);
+
+        tile = choose(g.M, g.N, q_steps * n.x, g.batch, false);
+        a.op = product(g.M, g.N, q_steps, n.x, g.batch, tile);
+        a.op.A = p.tall ? x : q;
+        a.op.lda = p.tall ? p.x_ld : p.side_p;
+        a.op.plane_a = p.tall ? x_plane : s_plane;
+        a.op.batch_a = 2 * a.op.plane_a;
+        a.op.mn_a = (int)g.M;
+        a.op.k_a = (int)p.side_p;
+        a.op.B = p.tall ? q : x;
+        a.op.ldb = p.tall ? p.side_p : p.x_ld;
+        a.op.plane_b = p.tall ? s_plane : x_plane;
+        a.op.batch_b = 2 * a.op.plane_b;
+        a.op.mn_b = (int)(p.tall ? p.side : p.x_ld);
+        a.op.k_b = (int)(p.tall ? p.side_p : p.side);
+        a.add = x;
+        a.ld_add = p.x_ld;
+        a.plane_add = x_plane;
+        a.batch_add = 2 * x_plane;
+        a.alpha = k[0];
+        a.beta = one;
+        if (step + 1 < g.steps) {
+            a.planes = in<void>(ws, p.x[(step + 1) & 1]);
+            a.ldo = p.x_ld;
+            a.plane_out = x_plane;
+            a.batch_out = 2 * x_plane;
+            a.rows = (int)p.x_rows;
+        } else {
+            a.planes = nullptr;
+            a.result = out;
+            a.ldr = ldo;
+            a.batch_r = batch_o;
+            a.dtype = g.dtype;
+        }
+        e = launch_chain(p.tall ? kRows : kMixed, tile.tile, a, stream);
+        if (e != hipSuccess) return from_hip(e);
+    }
+    return TGEMM_SUCCESS;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t tgemm_orthogonalize_workspace_size(tgemm_dtype_t dtype, int64_t batch, int64_t M, int64_t N, int steps)
+{
+    const Stack g{dtype, batch, M, N, steps};
+    Plan p;
+    if (check(g, 0.0f) != TGEMM_SUCCESS || batch == 0 || M == 0 || N == 0 || !make_plan(p, g)) return 0;
+    return (size_t)p.total;
+}
+
+tgemm_status_t tgemm_orthogonalize(tgemm_dtype_t dtype, int64_t batch, int64_t M, int64_t N,
+                                   const void *G, int64_t ldg, int64_t stride_g,
+                                   int steps, const float *coefficients, float eps,
+                                   void *out, int64_t ldo, int64_t stride_out,
+                                   void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    const Stack g{dtype, batch, M, N, steps};
+    const tgemm_status_t st = check(g, eps);
+    if (st != TGEMM_SUCCESS) return st;
+    if (coefficients == nullptr || ldg < N || ldo < N || stride_g < 0 || stride_out < 0) return TGEMM_ERROR_INVALID_VALUE;
+    if (ldg > kMaxLd || ldo > kMaxLd || stride_g > kMaxLd || stride_out > kMaxLd) return TGEMM_ERROR_NOT_SUPPORTED;
+    if (batch == 0 || M == 0 || N == 0) return TGEMM_SUCCESS;
+    Plan p;
+    if (!make_plan(p, g)) return TGEMM_ERROR_NOT_SUPPORTED;
+    // a matrix's elements, from its first to its last
+    const int64_t span_g = (M - 1) * ldg + N, span_out = (M - 1) * ldo + N;
+    Range r[1], w[2];
+    if ((batch > 1 && stride_out < span_out) || !at(G, batch, span_g, stride_g, size_of(dtype), r[0]) ||
+        !at(out, batch, span_out, stride_out, size_of(dtype), w[0]) || !room_at(workspace, workspace_bytes, p.total, w[1]) ||
+        !disjoint(w, 2, r, 1))
+        return TGEMM_ERROR_INVALID_VALUE;
+    return (p.small ? run_small : run_chain)(p, g, G, ldg, stride_g, coefficients, eps, out, ldo, stride_out, workspace, stream);
+}
+
+}  // extern "C"

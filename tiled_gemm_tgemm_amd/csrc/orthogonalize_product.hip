@@ -1,0 +1,106 @@
+// The products of the Newton-Schulz operator on 16-bit tiles (mfma16.h): S =
+// X·Xᵀ, Q = b·S + c·S·S and a·X + Q·X, each with its sum and the split into
+// planes in the epilogue.
+#include "mfma16.h"
+#include "mfma16_store.h"
+#include "orthogonalize.h"
+
+namespace tgemm {
+namespace ortho {
+namespace {
+
+using m16::f32x4;
+using m16::kHeld;
+using m16::lds_char;
+using m16::store_packed;
+using m16::store_row;
+using m16::TileProduct;
+
+typedef _Float16 f16x8_anywhere __attribute__((ext_vector_type(8), aligned(2)));
+
+// Bound by the matrix cores.  S and Q are symmetric: where that takes fewer
+// rounds, only the tiles on and below the diagonal are formed and each is
+// stored a second time across it.
+template <int BM, int BN, int WM, int WN, bool A_MC, bool B_MC>
+__global__ __launch_bounds__(64 * WM * WN) void chain_kernel(ChainArgs a)
+{
+    typedef TileProduct<_Float16, BM, BN, WM, WN, A_MC, B_MC, Chain> Tile;
+    constexpr int H = kHeld<Tile>;
+    __shared__ __align__(1024) char lds[Tile::kLds];
+    struct Ahead {};
+    Tile::run(a.op, (lds_char *)lds, [](int, int) { return Ahead{}; },
+              [&](typename Tile::Acc &acc, int row0, int col0, int matrix, Ahead) {
+        const int lane = m16::thread_anew() & 63, l16 = lane & 15, quarter = lane >> 4;
+        const int col = col0 + H * quarter;
+        const bool mirrored = a.op.lower && row0 / BM != col0 / BN;
+#pragma unroll
+        for (int i = 0; i < Tile::FM; ++i) {
+            const int row = row0 + i * 16 + l16;
+            float v[H];
+#pragma unroll
+            for (int e = 0; e < H; ++e) v[e] = a.beta * acc[i][e / 4][e % 4];
+            if (a.add != nullptr && row < a.op.M && col < a.ld_add) {
+                const _Float16 *from = (const _Float16 *)a.add + matrix * a.batch_add + (int64_t)row * a.ld_add + col;
+#pragma unroll
+                for (int q = 0; q < H / 8; ++q) {
+                    const f16x8_anywhere high = ((const f16x8_anywhere *)from)[q];
+                    const f16x8_anywhere low = ((const f16x8_anywhere *)(from + a.plane_add))[q];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[8 * q + e] = fmaf(a.alpha, (float)high[e] + (float)low[e], v[8 * q + e]);
+                }
+            }
+            if (a.planes == nullptr) {
+                if (row >= a.op.M) continue;
+#pragma unroll
+                for (int e = 0; e < H; ++e) v[e] *= 1.0f / (1 << kShift);
+                const int64_t at = matrix * a.batch_r + (int64_t)row * a.ldr + col;
+                if (a.dtype == TGEMM_F32) store_row<float, H>((float *)a.result + at, v, a.op.N - col);
+                else if (a.dtype == TGEMM_BF16) store_row<__bf16, H>((__bf16 *)a.result + at, v, a.op.N - col);
+                else store_row<_Float16, H>((_Float16 *)a.result + at, v, a.op.N - col);
+                continue;
+            }
+#pragma unroll
+            for (int e = 0; e < H; ++e) v[e] = row < a.op.M && col + e < a.op.N ? v[e] : 0.0f;
+            _Float16 *to = (_Float16 *)a.planes + matrix * a.batch_out;
+            float low[H];
+#pragma unroll
+            for (int e = 0; e < H; ++e) low[e] = v[e] - (float)(_Float16)v[e];
+            if (row < a.rows && col < a.ldo) {
+                store_packed<_Float16, H>(to + (int64_t)row * a.ldo + col, v);
+                store_packed<_Float16, H>(to + a.plane_out + (int64_t)row * a.ldo + col, low);
+            }
+            if (mirrored && row < a.ldo) {
+#pragma unroll
+                for (int e = 0; e < H; ++e) {
+                    if (col + e < a.rows) {
+                        _Float16 *across = to + (int64_t)(col + e) * a.ldo + row;
+                        across[0] = (_Float16)v[e];
+                        across[a.plane_out] = (_Float16)low[e];
+                    }
+                }
+            }
+        }
+    });
+}
+
+}  // namespace
+
+hipError_t launch_chain(Order order, int tile, const ChainArgs &a, hipStream_t stream)
+{
+    const int64_t ids = a.op.ids(), most = (int64_t)256 * kTiles[tile].wg_per_cu;
+    const unsigned grid = (unsigned)(ids < most ? ids : most);
+    switch (tile) {
+#define X(I, BM, BN, WM, WN)                                                                                        \
+    case I:                                                                                                         \
+        if (order == kRows) chain_kernel<BM, BN, WM, WN, false, false><<<grid, 64 * WM * WN, 0, stream>>>(a);       \
+        else if (order == kColumns) chain_kernel<BM, BN, WM, WN, true, true><<<grid, 64 * WM * WN, 0, stream>>>(a); \
+        else chain_kernel<BM, BN, WM, WN, false, true><<<grid, 64 * WM * WN, 0, stream>>>(a);                       \
+        break;
+        TGEMM_CHAIN_TILES(X)
+#undef X
+    }
+    return hipGetLastError();
+}
+
+}  // namespace ortho
+}  // namespace tgemm

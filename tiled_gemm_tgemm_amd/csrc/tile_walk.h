@@ -31,21 +31,6 @@ constexpr int kXcds = 8;
 
 TGEMM_BOTH constexpr int least(int a, int b) { return a < b ? a : b; }
 
-// The operands of a product.  Rows and columns past the ends are read from
-// the last one that exists (their products are not stored, or meet zeros).
-struct Operands {
-    const void *A, *B;
-    int64_t lda, ldb;          // elements
-    int64_t plane_a, plane_b;  // elements between the planes of a split operand
-    int segments;              // 1; 6: the plane pairs of kPairs; 2: the first two, with plane_b = 0
-    int M, N;
-    int steps;                 // steps of 64 along K
-    int steps_per_split;       // part y of the sum takes steps [y·this, (y+1)·this)
-    int mn_a, mn_b;            // KC: rows of A / B; MC: columns that may be read, a multiple of 8
-    int k_a, k_b;              // values of k of A / B; a multiple of 8 for a KC operand, of 64 for A
-    int tiles_m, tiles_n, splits;
-};
-
 // A float32 operand is the sum of three bf16 planes (high, middle, low: 24
 // bits).  Of the nine products of planes the six that reach 2^-24 of the
 // largest are summed, small ones first: (mid,mid), (high,low), (low,high),
@@ -64,7 +49,7 @@ template <int MN, int F, bool PERMUTE>
 TGEMM_BOTH constexpr int flip(int k)
 {
     const int j = k & 3, h = (k >> 3) & 1;
-    if (PERMUTE) return F == 4 ? (j & 1) | (j >> 1) << 3 : 4 * j;
+    if (PERMUTE) return F == 4 ? (j & 1) | (j >> 1) << 3 : 4 * (MN >= 128 ? j : j & 1);
     return MN >= 128 ? 2 * j + 8 * h : 0;
 }
 
@@ -101,17 +86,23 @@ struct Slice {
     }
 };
 
-// Tile `id` of `ids`.  The hardware deals work-groups, and a grid that is a
-// multiple of 8 its tiles, round-robin to eight XCDs with an L2 each; XCD x
-// takes the x-th run of logical ids.  Ids walk the tiles of one part of the
+// Work-group `id` of `ids` in the order of the tiles.  The hardware deals
+// work-groups, and a grid that is a multiple of 8 its tiles, round-robin to
+// eight XCDs with an L2 each; XCD x takes the x-th run of logical ids.
+TGEMM_BOTH int deal(int id, int ids)
+{
+    const int q = ids / kXcds, r = ids % kXcds;
+    const int x = id % kXcds;
+    return id / kXcds + x * q + least(x, r);
+}
+
+// Tile `id` of `ids`.  Logical ids walk the tiles of one part of the
 // sum, then those of the next (parts share nothing), and within a part groups
 // of 8 tile rows column by column, so that the work-groups of an XCD share
 // rows of A and columns of B.
 TGEMM_BOTH void place_tile(int id, int ids, int tiles_m, int tiles_n, int &tm, int &tn, int &split)
 {
-    const int q = ids / kXcds, r = ids % kXcds;
-    const int x = id % kXcds;
-    const int logical = id / kXcds + x * q + least(x, r);
+    const int logical = deal(id, ids);
     const int tiles = tiles_m * tiles_n;
     split = logical / tiles;
     const int tile = logical - split * tiles, per_group = 8 * tiles_n;
@@ -121,27 +112,56 @@ TGEMM_BOTH void place_tile(int id, int ids, int tiles_m, int tiles_n, int &tm, i
     tn = in_group / rows;
 }
 
-// The place of tile `id` and its steps [first, last).
-template <int BM, int BN>
-TGEMM_BOTH void tile_at(const Operands &p, int id, int &m0, int &n0, int &split, int &first, int &last)
+// The operands of a product.  Rows and columns past the ends are read from
+// the last one that exists (their products are not stored, or meet zeros).
+// What a product with another order of tiles, other plane pairs or many
+// matrices does otherwise is in the members that a derived type hides.
+struct Operands {
+    const void *A, *B;
+    int64_t lda, ldb;          // elements
+    int64_t plane_a, plane_b;  // elements between the planes of a split operand
+    int segments;              // 1; 6: the plane pairs of kPairs; 2: the first two, with plane_b = 0
+    int M, N;
+    int steps;                 // steps of 64 along K
+    int steps_per_split;       // part y of the sum takes steps [y·this, (y+1)·this)
+    int mn_a, mn_b;            // KC: rows of A / B; MC: columns that may be read, a multiple of 8
+    int k_a, k_b;              // values of k of A / B; a multiple of 8 for a KC operand, of 64 for A
+    int tiles_m, tiles_n, splits;
+
+    TGEMM_BOTH int ids() const { return tiles_m * tiles_n * splits; }
+    // The place of tile `id` and its steps [first, last).
+    template <int BM, int BN>
+    TGEMM_BOTH void tile(int id, int &m0, int &n0, int &split, int &first, int &last) const
+    {
+        int tm, tn;
+        place_tile(id, ids(), tiles_m, tiles_n, tm, tn, split);
+        m0 = tm * BM;
+        n0 = tn * BN;
+        first = split * steps_per_split;
+        last = least(steps, first + steps_per_split);
+    }
+    // elements from the operands' start to the planes of segment `seg`, and to what part `split` reads
+    TGEMM_BOTH int64_t plane_at_a(int seg) const { return ((kPairsA >> (2 * seg)) & 3) * plane_a; }
+    TGEMM_BOTH int64_t plane_at_b(int seg) const { return ((kPairsB >> (2 * seg)) & 3) * plane_b; }
+    TGEMM_BOTH int64_t start_a(int) const { return 0; }
+    TGEMM_BOTH int64_t start_b(int) const { return 0; }
+};
+
+template <int BM, int BN, class Op>
+TGEMM_BOTH void tile_at(const Op &p, int id, int &m0, int &n0, int &split, int &first, int &last)
 {
-    int tm, tn;
-    place_tile(id, p.tiles_m * p.tiles_n * p.splits, p.tiles_m, p.tiles_n, tm, tn, split);
-    m0 = tm * BM;
-    n0 = tn * BN;
-    first = split * p.steps_per_split;
-    last = least(p.steps, first + p.steps_per_split);
+    p.template tile<BM, BN>(id, m0, n0, split, first, last);
 }
 
 // Which tile, segment and step the loads are at, and where from.
-template <int BM, int BN, bool A_MC, bool B_MC>
+template <int BM, int BN, bool A_MC, bool B_MC, class Op = Operands>
 struct Walk {
     int id, seg, k, first, last;  // k: the step to come
     int a_last, b_last, a_k_last, b_k_last;  // as Slice::offset takes them
     const char *a, *b;                       // the tile's first rows (KC) or columns (MC)
     const char *from_a, *from_b;             // the step's slices
 
-    TGEMM_BOTH void open(const Operands &p)
+    TGEMM_BOTH void open(const Op &p)
     {
         int m0, n0, split;
         tile_at<BM, BN>(p, id, m0, n0, split, first, last);
@@ -150,14 +170,14 @@ struct Walk {
         const int a0 = least(m0, a_end), b0 = least(n0, b_end);
         a_last = a_end - a0;
         b_last = b_end - b0;
-        a = (const char *)p.A + (A_MC ? (int64_t)a0 : (int64_t)a0 * p.lda) * 2;
-        b = (const char *)p.B + (B_MC ? (int64_t)b0 : (int64_t)b0 * p.ldb) * 2;
+        a = (const char *)p.A + (p.start_a(split) + (A_MC ? (int64_t)a0 : (int64_t)a0 * p.lda)) * 2;
+        b = (const char *)p.B + (p.start_b(split) + (B_MC ? (int64_t)b0 : (int64_t)b0 * p.ldb)) * 2;
         seg = 0;
         k = first;
         fresh = true;
     }
 
-    TGEMM_BOTH void begin(const Operands &p, int first_id)
+    TGEMM_BOTH void begin(const Op &p, int first_id)
     {
         id = first_id;
         open(p);
@@ -169,13 +189,13 @@ struct Walk {
     struct Moved {
         bool a, b;
     };
-    TGEMM_BOTH Moved seek(const Operands &p, int stride)
+    TGEMM_BOTH Moved seek(const Op &p, int stride)
     {
         if (k == last) {
             k = first;
             if (++seg == p.segments) {
                 // after the last tile its first steps are loaded again, for nobody
-                if (id + stride < p.tiles_m * p.tiles_n * p.splits) id += stride;
+                if (id + stride < p.ids()) id += stride;
                 open(p);
             }
         }
@@ -184,8 +204,8 @@ struct Walk {
         from_a = a + (A_MC ? start_a * p.lda : (int64_t)start_a) * 2;
         from_b = b + (B_MC ? start_b * p.ldb : (int64_t)start_b) * 2;
         if (p.segments > 1) {
-            from_a += ((kPairsA >> (2 * seg)) & 3) * p.plane_a * 2;
-            from_b += ((kPairsB >> (2 * seg)) & 3) * p.plane_b * 2;
+            from_a += p.plane_at_a(seg) * 2;
+            from_b += p.plane_at_b(seg) * 2;
         }
         a_k_last = A_MC ? p.k_a - 1 - start_a : kStepK;  // a KC A has whole steps
         b_k_last = p.k_b - (B_MC ? 1 : 8) - start_b;
