@@ -480,6 +480,83 @@ tgemm_status_t tgemm_linear_kd_backward(tgemm_dtype_t dtype, int64_t T, int64_t 
                                         void *workspace, size_t workspace_bytes, hipStream_t stream);
 
 /*
+ * Low-rank adapters of many requests beside a shared projection
+ * -------------------------------------------------------------
+ *   y_t = x_t·Wᵀ + scales[i]·(x_t·A_iᵀ)·B_iᵀ,   i = ids[t]
+ * X (T×D) holds a row a token, W (N×D) the shared weight, A (`count` matrices
+ * of rank×D, rows lda >= D apart, stride_a elements from one to the next) and B
+ * (count × N×rank, ldb >= rank, stride_b) the adapters, ids (T) each token's
+ * adapter, -1 for none, in any order, and scales (count floats, or NULL for 1)
+ * their factors.  Y is T×N, ldy >= N.
+ *
+ * Types       float32, bf16 or fp16: X, W, A, B, Y and the gradients alike.
+ *             Products of 16-bit values are exact and summed in float32, those
+ *             of float32 ones by the planes of the loss operators (few rows and
+ *             the adapters' part: in float32).  x·Aᵀ is float32; where it meets
+ *             16-bit matrices it is held in two bf16 numbers (17 bits).  A
+ *             result is rounded once.
+ * Sizes       0 <= T < 2^24, 1 <= N, D <= 2^22, 1 <= count <= 2^15, 1 <= rank <=
+ *             1024, lda up to 2^26, the other leading dimensions and strides up
+ *             to 2^40; larger ones, a product of 2^31 tiles and more, and an
+ *             unknown dtype: TGEMM_ERROR_NOT_SUPPORTED.
+ * hidden      T×rank floats, or NULL: the forward call leaves x_t·A_iᵀ there
+ *             (rows without an adapter are not written) for the backward call,
+ *             which takes NULL to form it again.
+ * Workspace   As the loss operators'; tgemm_linear_adapters_workspace_size for
+ *             the same arguments: need 0 for a forward call, otherwise the sum
+ *             of 1 (dX), 2 (dW), 4 (dA) and 8 (dB) of a backward call, with its
+ *             dY.  Up to 64 rows of a forward call take little; float32
+ *             operands take their planes, 16-bit ones a copy where they cannot
+ *             be read as they are stored.
+ * Errors      As above, before anything is queued; also
+ *             TGEMM_ERROR_INVALID_VALUE for an output that overlaps an input or
+ *             another output, or whose matrices overlap one another.
+ * Indices     An id other than -1 outside [0, count) is never used as an
+ *             address: its row of Y and of dX is NaN, and dA and dB have
+ *             nothing of it.
+ * Rows        What one adapter holds, infinities and NaN too, reaches the rows
+ *             of its own tokens alone.
+ * Order       Sums are taken in a fixed order: the same call gives the same
+ *             bits.  Every call can be captured into a graph.
+ *
+ * Backward: for the gradient dY of Y (T×N, lddy >= N), with h_t = x_t·A_iᵀ and
+ * u_t = dy_t·B_i,
+ *   dx_t = dy_t·W + scales[i]·u_t·A_i        dW = dYᵀ·X
+ *   dA_i = scales[i]·sum u_tᵀ·x_t            dB_i = scales[i]·sum dy_tᵀ·h_t
+ * over the adapter's tokens; an adapter without tokens gets zeros.  Any of the
+ * four may be NULL and is then not computed.  u_t is float32, held as above for
+ * dX and in two bf16 numbers for dA, as h_t for dB.
+ */
+tgemm_status_t tgemm_linear_adapters_forward(tgemm_dtype_t dtype, int64_t T, int64_t N, int64_t D,
+                                             const void *X, int64_t ldx,
+                                             const void *W, int64_t ldw,
+                                             int64_t count, int64_t rank,
+                                             const void *A, int64_t lda, int64_t stride_a,
+                                             const void *B, int64_t ldb, int64_t stride_b,
+                                             const int64_t *ids, const float *scales,
+                                             void *Y, int64_t ldy, float *hidden,
+                                             void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+tgemm_status_t tgemm_linear_adapters_backward(tgemm_dtype_t dtype, int64_t T, int64_t N, int64_t D,
+                                              const void *X, int64_t ldx,
+                                              const void *W, int64_t ldw,
+                                              int64_t count, int64_t rank,
+                                              const void *A, int64_t lda, int64_t stride_a,
+                                              const void *B, int64_t ldb, int64_t stride_b,
+                                              const int64_t *ids, const float *scales,
+                                              const float *hidden, const void *dY, int64_t lddy,
+                                              void *dX, int64_t lddx, void *dW, int64_t lddw,
+                                              void *dA, int64_t ldda, int64_t stride_da,
+                                              void *dB, int64_t lddb, int64_t stride_db,
+                                              void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+size_t tgemm_linear_adapters_workspace_size(tgemm_dtype_t dtype, int64_t T, int64_t N, int64_t D,
+                                            const void *X, int64_t ldx,
+                                            const void *W, int64_t ldw,
+                                            int64_t count, int64_t rank,
+                                            const void *dY, int64_t lddy, int need);
+
+/*
  * An update made orthogonal by Newton-Schulz products
  * ---------------------------------------------------
  * For each of `batch` matrices G (M×N, rows ldg >= N apart, stride_g >= 0

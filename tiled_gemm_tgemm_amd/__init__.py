@@ -5,7 +5,8 @@ declarations in include/tgemm.h).  ``_lib`` exposes the C entry points under
 their own names; ``sgemm`` and ``transpose`` below are the same calls for
 torch tensors, with torch used for device memory and the current stream only,
 ``linear_cross_entropy`` and ``linear_distillation`` the losses on an output
-head's product, with their gradients, and ``orthogonalize`` an update made orthogonal
+head's product, with their gradients, ``linear_adapters`` a projection with
+low-rank adapters beside it, and ``orthogonalize`` an update made orthogonal
 by Newton-Schulz products.
 
 Nothing here loads the library at import time; the first call does, and it
@@ -45,6 +46,9 @@ from ._lib import (  # noqa: F401
     tgemm_linear_kd_backward,
     tgemm_linear_kd_forward,
     tgemm_linear_loss_workspace_size,
+    tgemm_linear_adapters_backward,
+    tgemm_linear_adapters_forward,
+    tgemm_linear_adapters_workspace_size,
     tgemm_orthogonalize,
     tgemm_orthogonalize_workspace_size,
     TGEMM_BF16,
@@ -71,6 +75,7 @@ from .linear_loss import (  # noqa: F401
     linear_distillation_forward,
 )
 
+from .linear_adapters import linear_adapters, linear_adapters_backward, linear_adapters_forward  # noqa: F401
 from .orthogonalize import orthogonalize  # noqa: F401
 
 KERNELS = ("auto", "mfma", "naive", "lds", "simt")

@@ -41,6 +41,7 @@ _HEAD = [ctypes.c_int, _i64, _i64, _i64, _ptr, _i64, _ptr, _i64]  # dtype, T, V,
 _TEACHER = [_i64, _ptr, _i64, ctypes.c_int, _ptr, _i64, ctypes.c_float]
 _GRADS = [_ptr, _i64, _ptr, _ptr, _i64, _ptr, _i64]  # grad_loss, grad_step, grad_weight, dX, lddx, dW, lddw
 _KEPT = [_ptr, _i64]  # logits, ldz
+_ADAPTERS = [_i64, _i64] + [_ptr, _i64, _i64] * 2 + [_ptr, _ptr]  # count, rank, A, lda, stride_a, B, ldb, stride_b, ids, scales
 _ROOM = [_ptr, ctypes.c_size_t, _ptr]  # workspace, its bytes, stream
 
 SIGNATURES = {
@@ -69,6 +70,10 @@ SIGNATURES = {
     "tgemm_linear_ce_backward": (ctypes.c_int, _HEAD + [_ptr, _i64, _ptr] + _KEPT + _GRADS + _ROOM),
     "tgemm_linear_kd_forward": (ctypes.c_int, _HEAD + _TEACHER + [_ptr] * 3 + _KEPT + [_ptr] + _ROOM),
     "tgemm_linear_kd_backward": (ctypes.c_int, _HEAD + _TEACHER + [_ptr] * 2 + _KEPT + _GRADS + _ROOM),
+    "tgemm_linear_adapters_forward": (ctypes.c_int, _HEAD + _ADAPTERS + [_ptr, _i64, _ptr] + _ROOM),
+    "tgemm_linear_adapters_backward": (ctypes.c_int, _HEAD + _ADAPTERS + [_ptr, _ptr, _i64] + [_ptr, _i64] * 2
+                                       + [_ptr, _i64, _i64] * 2 + _ROOM),
+    "tgemm_linear_adapters_workspace_size": (ctypes.c_size_t, _HEAD + [_i64, _i64, _ptr, _i64, ctypes.c_int]),
     "tgemm_orthogonalize": (ctypes.c_int, [ctypes.c_int, _i64, _i64, _i64, _ptr, _i64, _i64, ctypes.c_int, _ptr,
                                            ctypes.c_float, _ptr, _i64, _i64] + _ROOM),
     "tgemm_orthogonalize_workspace_size": (ctypes.c_size_t, [ctypes.c_int, _i64, _i64, _i64, ctypes.c_int]),
@@ -207,6 +212,26 @@ def tgemm_linear_kd_backward(dtype, T, V, D, X, ldx, W, ldw, K, teacher_ids, ld_
                                               teacher_logits, ld_logits, temperature, lse, student, logits, ldz,
                                               grad_loss, grad_step, grad_weight, dX, lddx, dW, lddw, workspace,
                                               workspace_bytes, stream)
+
+
+def tgemm_linear_adapters_forward(dtype, T, N, D, X, ldx, W, ldw, count, rank, A, lda, stride_a, B, ldb, stride_b, ids,
+                                  scales, Y, ldy, hidden, workspace, workspace_bytes, stream=None) -> int:
+    return library().tgemm_linear_adapters_forward(dtype, T, N, D, X, ldx, W, ldw, count, rank, A, lda, stride_a, B, ldb,
+                                                   stride_b, ids, scales, Y, ldy, hidden, workspace, workspace_bytes,
+                                                   stream)
+
+
+def tgemm_linear_adapters_backward(dtype, T, N, D, X, ldx, W, ldw, count, rank, A, lda, stride_a, B, ldb, stride_b, ids,
+                                   scales, hidden, dY, lddy, dX, lddx, dW, lddw, dA, ldda, stride_da, dB, lddb,
+                                   stride_db, workspace, workspace_bytes, stream=None) -> int:
+    return library().tgemm_linear_adapters_backward(dtype, T, N, D, X, ldx, W, ldw, count, rank, A, lda, stride_a, B,
+                                                    ldb, stride_b, ids, scales, hidden, dY, lddy, dX, lddx, dW, lddw,
+                                                    dA, ldda, stride_da, dB, lddb, stride_db, workspace,
+                                                    workspace_bytes, stream)
+
+
+def tgemm_linear_adapters_workspace_size(dtype, T, N, D, X, ldx, W, ldw, count, rank, dY=0, lddy=0, need=0) -> int:
+    return library().tgemm_linear_adapters_workspace_size(dtype, T, N, D, X, ldx, W, ldw, count, rank, dY, lddy, need)
 
 
 def tgemm_orthogonalize(dtype, batch, M, N, G, ldg, stride_g, steps, coefficients, eps, out, ldo, stride_out, workspace,

@@ -27,7 +27,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["api.cpp", "host_pipeline.cpp", "naive.hip", "lds_tiled.hip", "simt_tiled.hip", "transpose.hip", "splitk_sum.hip",
            "mfma_sgemm.hip", "mfma_sgemm_flat.hip", "linear_loss.cpp", "linear_loss_rows.hip", "linear_loss_product.hip",
-           "linear_loss_few.hip", "orthogonalize.cpp", "orthogonalize_product.hip", "orthogonalize_small.hip"]
+           "linear_loss_few.hip", "linear_adapters.cpp", "linear_adapters_product.hip", "linear_adapters_rows.hip",
+           "orthogonalize.cpp", "orthogonalize_product.hip", "orthogonalize_small.hip"]
 
 ARCH = "gfx950"
 COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall", "-Wextra",

@@ -1,0 +1,535 @@
+// C entry points of the projection with low-rank adapters: argument checks, the
+// plan of a call (operand copies, tiles, parts, workspace) and its launches on
+// the caller's stream.  The declarations, with the meaning of every argument,
+// are in tgemm.h.
+#include "linear_adapters.h"
+#include "entry.h"
+#include "product_plan.h"
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace {
+
+using namespace tgemm::entry;
+using namespace tgemm::adapters;
+using tgemm::loss::Choice;
+using tgemm::loss::choose_tile;
+using tgemm::loss::CopyArgs;
+using tgemm::loss::fits;
+using tgemm::loss::kTiles;
+using tgemm::loss::launch_copy;
+using tgemm::loss::launch_dw;
+using tgemm::loss::launch_sum;
+using tgemm::loss::launch_zero;
+using tgemm::loss::OutArgs;
+using tgemm::loss::parts_of;
+using tgemm::loss::SumArgs;
+using tgemm::m16::kStepK;
+
+constexpr int64_t kMaxT = ((int64_t)1 << 24) - 1;
+constexpr int64_t kMaxSide = (int64_t)1 << 22;  // 256 rows of 16-bit values stay within 32-bit offsets
+constexpr int64_t kMaxRank = 1024, kMaxCount = (int64_t)1 << 15;
+constexpr int64_t kMaxLd = (int64_t)1 << 40;
+constexpr int64_t kMaxLdA = (int64_t)1 << 26;   // 32 ranks of float32 stay within 32-bit offsets
+
+struct Layer {
+    tgemm_dtype_t dtype;
+    int64_t T, N, D;
+    const void *X;
+    int64_t ldx;
+    const void *W;
+    int64_t ldw;
+    int64_t count, rank;
+    const void *A;
+    int64_t lda, stride_a;
+    const void *B;
+    int64_t ldb, stride_b;
+    const int64_t *ids;
+    const float *scales;
+};
+
+tgemm_status_t check(const Layer &l)
+{
+    if (l.T < 0 || l.N < 1 || l.D < 1 || l.count < 1 || l.rank < 1 || l.ldx < l.D || l.ldw < l.D || l.lda < l.D ||
+        l.ldb < l.rank || l.stride_a < 0 || l.stride_b < 0)
+        return TGEMM_ERROR_INVALID_VALUE;
+    if (!known(l.dtype) || l.T > kMaxT || l.N > kMaxSide || l.D > kMaxSide || l.count > kMaxCount || l.rank > kMaxRank ||
+        l.ldx > kMaxLd || l.ldw > kMaxLd || l.lda > kMaxLdA || l.ldb > kMaxLd || l.stride_a > kMaxLd || l.stride_b > kMaxLd)
+        return TGEMM_ERROR_NOT_SUPPORTED;
+    return TGEMM_SUCCESS;
+}
+
+// What every call reads of the adapters lies in memory.
+bool there(const Layer &l, Range *r)
+{
+    const size_t size = size_of(l.dtype);
+    return at(l.X, l.T, l.D, l.ldx, size, r[0]) && at(l.W, l.N, l.D, l.ldw, size, r[1]) &&
+           at(l.A, l.count, (l.rank - 1) * l.lda + l.D, l.stride_a, size, r[2]) &&
+           at(l.B, l.count, (l.N - 1) * l.ldb + l.rank, l.stride_b, size, r[3]) && at(l.ids, l.T, 1, 1, 8, r[4]) &&
+           at(l.scales, l.scales ? l.count : 0, 1, 1, 4, r[5]);
+}
+constexpr int kRead = 6;
+
+// The matrix cores take a 16-bit operand as it is stored if its rows start
+// 16-byte aligned and hold whole pieces of 16 bytes (an operand that comes
+// first and lies along K: whole steps) and a tile's offsets fit 32 bits.
+bool as_stored(tgemm_dtype_t dtype, const void *p, int64_t ld, int64_t cols, int64_t whole)
+{
+    return dtype != TGEMM_F32 && cols % whole == 0 && ld % 8 == 0 && ld <= kMaxSide && reinterpret_cast<uintptr_t>(p) % 16 == 0;
+}
+
+// How a sum over K of one token's values is cut: a work-group's share is 16
+// rows and the adapter's ranks, of which a compute unit takes about 20 GB/s
+// where few of them are at work, so the sum is cut while they are few.
+struct Shrink {
+    int64_t part_k = 0;
+    int parts = 1, slots = 1;
+};
+Shrink shrink_of(int64_t T, int64_t K, int64_t count, bool few)
+{
+    Shrink s;
+    const int64_t blocks = ceil_div(T, 16);
+    int64_t parts = few ? 8 : 512 / blocks;
+    if (parts > ceil_div(K, 512)) parts = ceil_div(K, 512);
+    if (parts > 8) parts = 8;
+    if (parts < 1) parts = 1;
+    s.part_k = round_up(ceil_div(K, parts), 128);
+    s.parts = (int)ceil_div(K, s.part_k);
+    s.slots = T <= 1024 ? 16 : 4;
+    if (s.slots > count) s.slots = (int)count;
+    return s;
+}
+
+// Where a call's buffers lie in its workspace.
+struct Plan {
+    bool half = false;
+    int planes = 1, segments = 1;
+    int64_t Tp = 0, Np = 0, Dp = 0;
+    int64_t total = 0;
+    int64_t x = -1, w = -1, dy = -1;         // operands laid out for the matrix cores
+    int64_t parts = -1, hidden_planes = -1;  // of the hidden values
+    Shrink shrink;
+    // forward
+    bool few = false;
+    Choice tile;
+    int64_t out_part = -1;
+    // backward
+    Shrink shrink_x;
+    int64_t u = -1, hidden = -1, parts_x = -1;
+    Choice dw;
+    int64_t dw_part = -1;
+    int64_t order = -1, starts = -1, chunks[2] = {-1, -1}, joins[2] = {-1, -1}, counts = -1, sums = -1;
+    int cut[2] = {64, 64}, most_chunks[2] = {0, 0};
+
+    int64_t take(int64_t bytes)
+    {
+        const int64_t at = total;
+        total += round_up(bytes, 256);
+        return at;
+    }
+};
+
+void plan_types(Plan &p, const Layer &l)
+{
+    p.half = l.dtype == TGEMM_F16;
+    p.planes = l.dtype == TGEMM_F32 ? 3 : 1;
+    p.segments = l.dtype == TGEMM_F32 ? 6 : 1;
+    p.Tp = round_up(l.T, kStepK);
+    p.Np = round_up(l.N, kStepK);
+    p.Dp = round_up(l.D, kStepK);
+}
+
+int64_t planes_bytes(const Layer &l) { return l.T * planes_rank(l.rank) * 4; }
+
+bool plan_forward(Plan &p, const Layer &l)
+{
+    plan_types(p, l);
+    p.few = l.T <= kFewRows;
+    p.shrink = shrink_of(l.T, l.D, l.count, p.few);
+    if (p.few || p.shrink.parts > 1) p.parts = p.take(p.shrink.parts * l.T * l.rank * 4);
+    if (p.few) return true;
+    p.hidden_planes = p.take(planes_bytes(l));
+    if (!as_stored(l.dtype, l.X, l.ldx, l.D, kStepK)) p.x = p.take(l.T * p.Dp * 2 * p.planes);
+    if (!as_stored(l.dtype, l.W, l.ldw, l.D, 8)) p.w = p.take(l.N * p.Dp * 2 * p.planes);
+    p.tile = choose_tile(l.T, l.N, p.Dp / kStepK * p.segments, true);
+    p.tile.splits = parts_of(p.Dp / kStepK, p.tile.splits);
+    if (p.tile.splits > 1) p.out_part = p.take(p.tile.splits * l.T * p.Np * 4);
+    return fits(l.T, l.N, p.tile.tile, p.tile.splits);
+}
+
+struct Need {
+    bool x, w, a, b;
+};
+
+bool plan_backward(Plan &p, const Layer &l, const void *dY, int64_t lddy, Need need, bool have_hidden)
+{
+    plan_types(p, l);
+    if (need.a || need.b) {
+        const int64_t C[2] = {l.D, l.N}, most_adapters = l.count < l.T ? l.count : l.T;
+        int64_t sums = 0;
+        p.order = p.take(l.T * 4);
+        p.starts = p.take((l.count + 1) * 4);
+        p.counts = p.take(8);
+        for (int n = 0; n < 2; ++n) {
+            // 512 work-groups or more, of 64 tokens or more
+            const int64_t columns = ceil_div(C[n], kOuterColumns);
+            int64_t tokens = round_up(ceil_div(l.T * columns, 512), 64);
+            if (tokens < 64) tokens = 64;
+            p.cut[n] = (int)tokens;
+            p.most_chunks[n] = (int)(l.T / tokens + most_adapters);
+            p.chunks[n] = p.take(((int64_t)p.most_chunks[n] + 1) * (int64_t)sizeof(Chunk));
+            p.joins[n] = p.take(l.count * 8);
+            // an adapter of several chunks has more than `tokens` tokens, and at most twice as many chunks as whole ones
+            const int64_t bytes = 2 * (l.T / tokens) * C[n] * l.rank * 4;
+            if ((n == 0 ? need.a : need.b) && bytes > sums) sums = bytes;
+        }
+        p.sums = p.take(sums);
+    }
+    if (l.T == 0) return true;
+    if (need.x || need.a) {
+        p.shrink = shrink_of(l.T, l.N, l.count, false);
+        if (p.shrink.parts > 1) p.parts = p.take(p.shrink.parts * l.T * l.rank * 4);
+        if (need.a) p.u = p.take(l.T * l.rank * 4);
+        if (need.x) p.hidden_planes = p.take(planes_bytes(l));
+    }
+    if (need.b && !have_hidden) {
+        p.shrink_x = shrink_of(l.T, l.D, l.count, false);
+        if (p.shrink_x.parts > 1) p.parts_x = p.take(p.shrink_x.parts * l.T * l.rank * 4);
+        p.hidden = p.take(l.T * l.rank * 4);
+    }
+    // dY comes first in either product: along K for dX, across for dW, whose sum has whole steps of tokens
+    if ((need.x && !as_stored(l.dtype, dY, lddy, l.N, kStepK)) ||
+        (need.w && (!as_stored(l.dtype, dY, lddy, l.N, 8) || l.T % kStepK != 0)))
+        p.dy = p.take(p.Tp * p.Np * 2 * p.planes);
+    bool fit = true;
+    if (need.x) {
+        if (!as_stored(l.dtype, l.W, l.ldw, l.D, 8)) p.w = p.take(l.N * p.Dp * 2 * p.planes);
+        p.tile = choose_tile(l.T, l.D, p.Np / kStepK * p.segments, true);
+        p.tile.splits = parts_of(p.Np / kStepK, p.tile.splits);
+        if (p.tile.splits > 1) p.out_part = p.take(p.tile.splits * l.T * p.Dp * 4);
+        fit = fits(l.T, l.D, p.tile.tile, p.tile.splits);
+    }
+    if (need.w) {
+        if (!as_stored(l.dtype, l.X, l.ldx, l.D, 8)) p.x = p.take(l.T * p.Dp * 2 * p.planes);
+        p.dw = choose_tile(l.N, l.D, p.Tp / kStepK * p.segments, true);
+        p.dw.splits = parts_of(p.Tp / kStepK, p.dw.splits);
+        if (p.dw.splits > 1) p.dw_part = p.take(p.dw.splits * l.N * p.Dp * 4);
+        fit = fit && fits(l.N, l.D, p.dw.tile, p.dw.splits);
+    }
+    return fit;
+}
+
+// An operand as the matrix cores read it.
+struct Stored {
+    const void *p;
+    int64_t ld, plane;
+};
+
+// The operand as stored, or copied to `room` (offset -1: as stored).
+hipError_t lay_out(const Plan &p, const Layer &l, const void *src, int64_t ld, int64_t rows, int64_t cols, int64_t room,
+                   int64_t rows_out, void *ws, Stored &s, hipStream_t stream)
+{
+    s = Stored{src, ld, 0};
+    if (room < 0) return hipSuccess;
+    CopyArgs c{};
+    c.src = src;
+    c.ld = ld;
+    c.dtype = l.dtype;
+    c.rows = rows;
+    c.cols = cols;
+    c.dst = in<void>(ws, room);
+    c.rows_out = rows_out;
+    c.ld_out = round_up(cols, kStepK);
+    c.plane = rows_out * c.ld_out;
+    c.planes = p.planes;
+    s = Stored{c.dst, c.ld_out, c.plane};
+    return launch_copy(c, stream);
+}
+
+ShrinkArgs shrink_args(const Layer &l, const Shrink &s, const void *rows, int64_t ld, int64_t K, const Stack &c)
+{
+    ShrinkArgs a{};
+    a.dtype = l.dtype;
+    a.T = l.T;
+    a.K = K;
+    a.rows = rows;
+    a.ld = ld;
+    a.c = c;
+    a.ids = l.ids;
+    a.scales = l.scales;
+    a.part_k = s.part_k;
+    a.parts = s.parts;
+    a.slots = s.slots;
+    return a;
+}
+
+// Hidden values to `hidden` and `planes`, either of which may be NULL.
+hipError_t make_hidden(ShrinkArgs a, float *parts, float *hidden, void *planes, hipStream_t stream)
+{
+    if (a.parts == 1) {
+        a.part = hidden;
+        a.planes = planes;
+        return launch_shrink(a, stream);
+    }
+    a.part = parts;
+    const hipError_t e = launch_shrink(a, stream);
+    return e != hipSuccess ? e : launch_finish(a, hidden, planes, stream);
+}
+
+Stack stack_a(const Layer &l) { return Stack{l.A, l.lda, l.stride_a, false, (int)l.count, (int)l.rank}; }
+Stack stack_b(const Layer &l) { return Stack{l.B, l.ldb, l.stride_b, true, (int)l.count, (int)l.rank}; }
+
+// The product, its adapters' part and the sum over its parts.
+hipError_t run_product(const Plan &p, const Layer &l, ProductArgs a, bool b_mc, int64_t steps, int64_t ld_part, void *out,
+                       int64_t ldo, void *ws, hipStream_t stream)
+{
+    a.stored = l.dtype;
+    a.out = out;
+    a.ldo = ldo;
+    a.dtype = l.dtype;
+    if (p.tile.splits > 1) {
+        a.op.splits = p.tile.splits;
+        a.op.steps_per_split = (int)ceil_div(steps, p.tile.splits);
+        a.out = in<float>(ws, p.out_part);
+        a.ldo = ld_part;
+        a.dtype = TGEMM_F32;
+        a.split_stride = l.T * ld_part;
+    }
+    hipError_t e = launch_product(p.half, b_mc, p.tile.tile, a, stream);
+    if (e != hipSuccess || p.tile.splits == 1) return e;
+    const SumArgs s{l.T, a.op.N, in<float>(ws, p.out_part), ld_part, a.split_stride, p.tile.splits, nullptr, nullptr, out, ldo, l.dtype};
+    return launch_sum(s, stream);
+}
+
+tgemm_status_t forward(const Plan &p, const Layer &l, void *Y, int64_t ldy, float *hidden, void *ws, hipStream_t stream)
+{
+    ShrinkArgs s = shrink_args(l, p.shrink, l.X, l.ldx, l.D, stack_a(l));
+    if (p.few) {
+        s.part = in<float>(ws, p.parts);
+        hipError_t e = launch_shrink(s, stream);
+        if (e == hipSuccess && hidden != nullptr) e = launch_finish(s, hidden, nullptr, stream);
+        if (e != hipSuccess) return from_hip(e);
+        const FewArgs f{l.dtype, (int)l.T, (int)l.N, (int)l.D, l.X, l.ldx, l.W, l.ldw, Y, ldy,
+                        Expand{l.ids, l.scales, s.part, l.T * l.rank, s.parts, nullptr, stack_b(l)}};
+        return from_hip(launch_few(f, stream));
+    }
+    void *planes = in<void>(ws, p.hidden_planes);
+    hipError_t e = make_hidden(s, in<float>(ws, p.parts), hidden, planes, stream);
+    Stored x, w;
+    if (e == hipSuccess) e = lay_out(p, l, l.X, l.ldx, l.T, l.D, p.x, l.T, ws, x, stream);
+    if (e == hipSuccess) e = lay_out(p, l, l.W, l.ldw, l.N, l.D, p.w, l.N, ws, w, stream);
+    if (e != hipSuccess) return from_hip(e);
+    ProductArgs a{};
+    const int64_t steps = p.Dp / kStepK;
+    a.op = tgemm::loss::operands(p.segments, l.T, l.N, steps, p.tile.tile);
+    a.op.A = x.p;
+    a.op.lda = x.ld;
+    a.op.plane_a = x.plane;
+    a.op.mn_a = (int)l.T;
+    a.op.B = w.p;
+    a.op.ldb = w.ld;
+    a.op.plane_b = w.plane;
+    a.op.mn_b = (int)l.N;
+    a.op.k_b = (int)(p.w >= 0 ? p.Dp : l.D);
+    a.e = Expand{l.ids, l.scales, nullptr, 0, 1, planes, stack_b(l)};
+    return from_hip(run_product(p, l, a, false, steps, p.Np, Y, ldy, ws, stream));
+}
+
+struct Gradients {
+    void *dX;
+    int64_t lddx;
+    void *dW;
+    int64_t lddw;
+    void *dA;
+    int64_t ldda, stride_da;
+    void *dB;
+    int64_t lddb, stride_db;
+};
+
+tgemm_status_t backward(const Plan &p, const Layer &l, const void *dY, int64_t lddy, const float *hidden, const Gradients &g,
+                        void *ws, hipStream_t stream)
+{
+    hipError_t e = hipSuccess;
+    GroupArgs o{};
+    if (g.dA != nullptr || g.dB != nullptr) {
+        o.ids = l.ids;
+        o.T = (int)l.T;
+        o.count = (int)l.count;
+        o.order = in<int>(ws, p.order);
+        o.starts = in<int>(ws, p.starts);
+        for (int n = 0; n < 2; ++n)
+            o.cuts[n] = Cut{p.cut[n], in<Chunk>(ws, p.chunks[n]), in<int2>(ws, p.joins[n]), in<int>(ws, p.counts) + n};
+        e = launch_group(o, stream);
+        if (e != hipSuccess) return from_hip(e);
+    }
+    float *u = in<float>(ws, p.u);
+    void *planes = in<void>(ws, p.hidden_planes);
+    if (l.T > 0 && (g.dX != nullptr || g.dA != nullptr))
+        e = make_hidden(shrink_args(l, p.shrink, dY, lddy, l.N, stack_b(l)), in<float>(ws, p.parts), u, planes, stream);
+    if (e == hipSuccess && p.hidden >= 0) {
+        hidden = in<float>(ws, p.hidden);
+        e = make_hidden(shrink_args(l, p.shrink_x, l.X, l.ldx, l.D, stack_a(l)), in<float>(ws, p.parts_x),
+                        in<float>(ws, p.hidden), nullptr, stream);
+    }
+    if (e != hipSuccess) return from_hip(e);
+
+    OuterArgs r{};
+    r.dtype = l.dtype;
+    r.scales = l.scales;
+    r.order = o.order;
+    r.part = in<float>(ws, p.sums);
+    r.count = (int)l.count;
+    r.rank = (int)l.rank;
+    for (int n = 0; n < 2; ++n) {
+        void *out = n == 0 ? g.dA : g.dB;
+        if (out == nullptr) continue;
+        r.C = (int)(n == 0 ? l.D : l.N);
+        r.rows = n == 0 ? l.X : dY;
+        r.ld = n == 0 ? l.ldx : lddy;
+        r.small = n == 0 ? u : hidden;
+        r.cut = o.cuts[n];
+        r.most_chunks = p.most_chunks[n];
+        r.out = out;
+        r.ldo = n == 0 ? g.ldda : g.lddb;
+        r.stride_out = n == 0 ? g.stride_da : g.stride_db;
+        r.rank_inner = n == 1;
+        if (l.T > 0) e = launch_outer(r, stream);
+        if (e == hipSuccess) e = launch_join(r, stream);
+        if (e != hipSuccess) return from_hip(e);
+    }
+    if (l.T == 0) return g.dW ? from_hip(launch_zero(g.dW, g.lddw, l.dtype, l.N, l.D, stream)) : TGEMM_SUCCESS;
+
+    Stored dy, w, x;
+    if (g.dX != nullptr || g.dW != nullptr) e = lay_out(p, l, dY, lddy, l.T, l.N, p.dy, p.Tp, ws, dy, stream);
+    if (e == hipSuccess && g.dX != nullptr) {
+        e = lay_out(p, l, l.W, l.ldw, l.N, l.D, p.w, l.N, ws, w, stream);
+        if (e != hipSuccess) return from_hip(e);
+        ProductArgs a{};
+        const int64_t steps = p.Np / kStepK;
+        a.op = tgemm::loss::operands(p.segments, l.T, l.D, steps, p.tile.tile);
+        a.op.A = dy.p;
+        a.op.lda = dy.ld;
+        a.op.plane_a = dy.plane;
+        a.op.mn_a = (int)l.T;
+        a.op.B = w.p;
+        a.op.ldb = w.ld;
+        a.op.plane_b = w.plane;
+        a.op.mn_b = (int)(p.w >= 0 ? p.Dp : l.D);
+        a.op.k_b = (int)l.N;
+        a.e = Expand{l.ids, l.scales, nullptr, 0, 1, planes, stack_a(l)};
+        e = run_product(p, l, a, true, steps, p.Dp, g.dX, g.lddx, ws, stream);
+    }
+    if (e == hipSuccess && g.dW != nullptr) {
+        e = lay_out(p, l, l.X, l.ldx, l.T, l.D, p.x, l.T, ws, x, stream);
+        if (e != hipSuccess) return from_hip(e);
+        OutArgs d{};
+        const int64_t steps = p.Tp / kStepK;
+        d.op = tgemm::loss::operands(p.segments, l.N, l.D, steps, p.dw.tile);
+        d.op.A = dy.p;
+        d.op.lda = dy.ld;
+        d.op.plane_a = dy.plane;
+        d.op.mn_a = (int)(p.dy >= 0 ? p.Np : l.N);
+        d.op.k_a = (int)p.Tp;
+        d.op.B = x.p;
+        d.op.ldb = x.ld;
+        d.op.plane_b = x.plane;
+        d.op.mn_b = (int)(p.x >= 0 ? p.Dp : l.D);
+        d.op.k_b = (int)l.T;
+        d.out = g.dW;
+        d.ldo = g.lddw;
+        d.dtype = l.dtype;
+        if (p.dw.splits > 1) {
+            d.op.splits = p.dw.splits;
+            d.op.steps_per_split = (int)ceil_div(steps, p.dw.splits);
+            d.out = in<float>(ws, p.dw_part);
+            d.ldo = p.Dp;
+            d.dtype = TGEMM_F32;
+            d.split_stride = l.N * p.Dp;
+        }
+        e = launch_dw(p.half, p.dw.tile, d, stream);
+        if (e == hipSuccess && p.dw.splits > 1) {
+            const SumArgs s{l.N, l.D, in<float>(ws, p.dw_part), p.Dp, d.split_stride, p.dw.splits, nullptr, nullptr, g.dW, g.lddw, l.dtype};
+            e = launch_sum(s, stream);
+        }
+    }
+    return from_hip(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t tgemm_linear_adapters_workspace_size(tgemm_dtype_t dtype, int64_t T, int64_t N, int64_t D, const void *X, int64_t ldx,
+                                            const void *W, int64_t ldw, int64_t count, int64_t rank, const void *dY, int64_t lddy,
+                                            int need)
+{
+    const Layer l{dtype, T, N, D, X, ldx, W, ldw, count, rank, nullptr, D, 0, nullptr, rank, 0, nullptr, nullptr};
+    if (check(l) != TGEMM_SUCCESS || need < 0 || need > 15) return 0;
+    Plan p;
+    if (need == 0) return T > 0 && plan_forward(p, l) ? (size_t)p.total : 0;
+    if (lddy < N || lddy > kMaxLd) return 0;
+    const Need n{(need & 1) != 0, (need & 2) != 0, (need & 4) != 0, (need & 8) != 0};
+    return plan_backward(p, l, dY, lddy, n, false) ? (size_t)p.total : 0;
+}
+
+tgemm_status_t tgemm_linear_adapters_forward(tgemm_dtype_t dtype, int64_t T, int64_t N, int64_t D, const void *X, int64_t ldx,
+                                             const void *W, int64_t ldw, int64_t count, int64_t rank,
+                                             const void *A, int64_t lda, int64_t stride_a,
+                                             const void *B, int64_t ldb, int64_t stride_b,
+                                             const int64_t *ids, const float *scales,
+                                             void *Y, int64_t ldy, float *hidden,
+                                             void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    const Layer l{dtype, T, N, D, X, ldx, W, ldw, count, rank, A, lda, stride_a, B, ldb, stride_b, ids, scales};
+    const tgemm_status_t st = check(l);
+    if (st != TGEMM_SUCCESS) return st;
+    if (ldy < N) return TGEMM_ERROR_INVALID_VALUE;
+    if (ldy > kMaxLd) return TGEMM_ERROR_NOT_SUPPORTED;
+    if (T == 0) return TGEMM_SUCCESS;
+    Plan p;
+    if (!plan_forward(p, l)) return TGEMM_ERROR_NOT_SUPPORTED;
+    Range r[kRead], w[3];
+    if (!there(l, r) || !at(Y, T, N, ldy, size_of(dtype), w[0]) || !at(hidden, hidden ? T : 0, rank, rank, 4, w[1]) ||
+        !room_at(workspace, workspace_bytes, p.total, w[2]) || !disjoint(w, 3, r, kRead))
+        return TGEMM_ERROR_INVALID_VALUE;
+    return forward(p, l, Y, ldy, hidden, workspace, stream);
+}
+
+tgemm_status_t tgemm_linear_adapters_backward(tgemm_dtype_t dtype, int64_t T, int64_t N, int64_t D, const void *X, int64_t ldx,
+                                              const void *W, int64_t ldw, int64_t count, int64_t rank,
+                                              const void *A, int64_t lda, int64_t stride_a,
+                                              const void *B, int64_t ldb, int64_t stride_b,
+                                              const int64_t *ids, const float *scales,
+                                              const float *hidden, const void *dY, int64_t lddy,
+                                              void *dX, int64_t lddx, void *dW, int64_t lddw,
+                                              void *dA, int64_t ldda, int64_t stride_da,
+                                              void *dB, int64_t lddb, int64_t stride_db,
+                                              void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    const Layer l{dtype, T, N, D, X, ldx, W, ldw, count, rank, A, lda, stride_a, B, ldb, stride_b, ids, scales};
+    const tgemm_status_t st = check(l);
+    if (st != TGEMM_SUCCESS) return st;
+    if (lddy < N || (dX && lddx < D) || (dW && lddw < D) || (dA && (ldda < D || stride_da < 0)) ||
+        (dB && (lddb < rank || stride_db < 0)))
+        return TGEMM_ERROR_INVALID_VALUE;
+    if (lddy > kMaxLd || lddx > kMaxLd || lddw > kMaxLd || ldda > kMaxLd || stride_da > kMaxLd || lddb > kMaxLd || stride_db > kMaxLd)
+        return TGEMM_ERROR_NOT_SUPPORTED;
+    const Need need{dX != nullptr && T > 0, dW != nullptr, dA != nullptr, dB != nullptr};
+    if (!need.x && !need.w && !need.a && !need.b) return TGEMM_SUCCESS;
+    Plan p;
+    if (!plan_backward(p, l, dY, lddy, need, hidden != nullptr)) return TGEMM_ERROR_NOT_SUPPORTED;
+    const size_t size = size_of(dtype);
+    const int64_t span_a = (rank - 1) * ldda + D, span_b = (N - 1) * lddb + rank;
+    Range r[kRead + 2], w[5];
+    if (!there(l, r) || !at(hidden, hidden ? T : 0, rank, rank, 4, r[kRead]) || !at(dY, T, N, lddy, size, r[kRead + 1]) ||
+        !at(dX, dX ? T : 0, D, lddx, size, w[0]) || !at(dW, dW ? N : 0, D, lddw, size, w[1]) ||
+        (dA && count > 1 && stride_da < span_a) || !at(dA, dA ? count : 0, span_a, stride_da, size, w[2]) ||
+        (dB && count > 1 && stride_db < span_b) || !at(dB, dB ? count : 0, span_b, stride_db, size, w[3]) ||
+        !room_at(workspace, workspace_bytes, p.total, w[4]) || !disjoint(w, 5, r, kRead + 2))
+        return TGEMM_ERROR_INVALID_VALUE;
+    const Gradients g{need.x ? dX : nullptr, lddx, dW, lddw, dA, ldda, stride_da, dB, lddb, stride_db};
+    return backward(p, l, dY, lddy, hidden, g, workspace, stream);
+}
+
+}  // extern "C"

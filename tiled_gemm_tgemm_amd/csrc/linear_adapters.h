@@ -1,0 +1,141 @@
+// Internal interface of the projection with low-rank adapters
+// (linear_adapters.cpp: entry points; linear_adapters_product.hip: the products
+// with the weight; linear_adapters_rows.hip: the adapters' own sums).  Every
+// launcher takes validated arguments and returns the launch's hipError_t.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "linear_loss.h"
+#include "tgemm.h"
+#include "tile_walk.h"
+
+namespace tgemm {
+namespace adapters {
+
+// One of a stack of adapter matrices, as a product of few columns reads it:
+// element (outer, rank) of adapter i lies at i·stride + outer·ld + rank
+// (rank_inner, B's layout) or at i·stride + rank·ld + outer (A's layout).
+struct Stack {
+    const void *p;
+    int64_t ld, stride;
+    bool rank_inner;
+    int count, rank;
+};
+
+// What the products read of a token's hidden values: scaled, and zero up to a
+// rank of whole 32s; 16-bit operands: two bf16 planes one after the other (17
+// bits), float32 ones: float32.
+TGEMM_BOTH constexpr int64_t planes_rank(int64_t rank) { return (rank + 31) / 32 * 32; }
+
+// hidden(t, rank) = sum over k of rows(t, k)·C_i(k, rank), i = ids[t], in `parts`
+// parts of the sum (part p to part + p·T·rank).  One part is the whole: it goes
+// to `part` if that is not NULL, and times scales[i] (NULL: 1) to `planes` if
+// that is not.  Rows whose id is outside [0, count) are not written.
+struct ShrinkArgs {
+    tgemm_dtype_t dtype;
+    int64_t T, K;
+    const void *rows;
+    int64_t ld;
+    Stack c;
+    const int64_t *ids;
+    const float *scales;
+    float *part;
+    void *planes;
+    int64_t part_k;  // values of k a part, a multiple of 32
+    int parts, slots;
+};
+hipError_t launch_shrink(const ShrinkArgs &a, hipStream_t stream);
+// Adds the parts up to `hidden` and `planes` (either may be NULL), for every row whose id is in range.
+hipError_t launch_finish(const ShrinkArgs &a, float *hidden, void *planes, hipStream_t stream);
+
+// What the products with the weight add to row t: scales[i]·hidden(t)·C_i.  A
+// row whose id is neither -1 nor in range becomes NaN.  The few rows' kernel
+// reads the parts of hidden, the tiles the planes.
+struct Expand {
+    const int64_t *ids;
+    const float *scales;
+    const float *hidden;
+    int64_t part_stride;
+    int parts;
+    const void *planes;
+    Stack c;
+};
+
+// C = A·B + the adapters' part, A as stored along K, B along K (forward) or not (dX).
+struct ProductArgs {
+    m16::Operands op;
+    void *out;
+    int64_t ldo;
+    tgemm_dtype_t dtype;        // of out, or float32 where the sum is split
+    tgemm_dtype_t stored;       // of the adapters
+    int64_t split_stride;
+    Expand e;
+};
+hipError_t launch_product(bool half, bool b_mc, int tile, const ProductArgs &a, hipStream_t stream);
+
+// The same for at most kFewRows rows, forward, on operands however they are stored.
+constexpr int64_t kFewRows = 64;
+struct FewArgs {
+    tgemm_dtype_t dtype;
+    int T, N, D;
+    const void *X;
+    int64_t ldx;
+    const void *W;
+    int64_t ldw;
+    void *Y;
+    int64_t ldy;
+    Expand e;
+};
+hipError_t launch_few(const FewArgs &a, hipStream_t stream);
+
+// ---- the adapters' gradients -----------------------------------------------
+
+// Tokens in the order of their adapters: order[starts[i] ... starts[i + 1]) are
+// adapter i's, ascending.  Then cut in chunks of at most `tokens`, once for
+// each gradient: chunks[n] = {adapter, first place in order, tokens, slot}, the
+// slot -1 where the adapter has one chunk; joins[i] = {first slot, chunks};
+// *chunk_count of them.
+struct Chunk {
+    int adapter, first, tokens, slot;
+};
+struct Cut {
+    int tokens;  // a multiple of 64
+    Chunk *chunks;
+    int2 *joins;
+    int *chunk_count;
+};
+struct GroupArgs {
+    const int64_t *ids;
+    int T, count;
+    int *order, *starts;
+    Cut cuts[2];
+};
+hipError_t launch_group(const GroupArgs &a, hipStream_t stream);
+
+// out_i = scales[i]·sum over adapter i's tokens of rows(t, :)ᵀ·small(t, :), laid
+// out as the stack: out(outer, rank).  Adapters of several chunks leave those
+// in part (slots × C × rank, as out but packed) for launch_join.
+struct OuterArgs {
+    tgemm_dtype_t dtype;
+    int C;                    // columns of rows
+    const void *rows;
+    int64_t ld;
+    const float *small;       // T × rank
+    const float *scales;
+    const int *order;
+    Cut cut;
+    int most_chunks;          // a launch's y
+    float *part;
+    void *out;
+    int64_t ldo, stride_out;
+    bool rank_inner;
+    int count, rank;
+};
+constexpr int kOuterColumns = 128, kOuterTokens = 64;
+hipError_t launch_outer(const OuterArgs &a, hipStream_t stream);
+hipError_t launch_join(const OuterArgs &a, hipStream_t stream);
+
+}  // namespace adapters
+}  // namespace tgemm

@@ -1,0 +1,375 @@
+// The products with a projection's weight and, in their epilogue, the
+// adapters' part: X·Wᵀ + s·H·Bᵀ forward, dY·W + s·U·A backward.
+#include "linear_adapters.h"
+#include "mfma16.h"
+#include "mfma16_store.h"
+#include "some.h"
+
+namespace tgemm {
+namespace adapters {
+namespace {
+
+using m16::bf16x8;
+using m16::f32x4;
+using m16::Frag;
+using m16::kHeld;
+using m16::lds_char;
+using m16::load_some;
+using m16::store_row;
+using m16::TileProduct;
+
+// Sums over ranks on the matrix cores, 32 ranks (8 a lane) at a time: the hidden
+// values in two bf16 planes (a rounding to 2^-17) with B as it is (bf16) or in
+// two bf16 planes (fp16, whose range bf16 holds); float32 in float32.
+struct TwoPlanes {
+    bf16x8 high, low;
+};
+struct EightFloats {
+    f32x4 v[2];
+};
+// lane's eight ranks from k on of a row's planes
+__device__ __forceinline__ void read_planes(const void *planes, int64_t row, int k, int padded, TwoPlanes &h)
+{
+    const __bf16 *from = (const __bf16 *)planes + row * 2 * padded + k;
+    h.high = *(const bf16x8 *)from;
+    h.low = *(const bf16x8 *)(from + padded);
+}
+__device__ __forceinline__ void read_planes(const void *planes, int64_t row, int k, int padded, EightFloats &h)
+{
+    const f32x4 *from = (const f32x4 *)((const float *)planes + row * padded + k);
+    h.v[0] = from[0];
+    h.v[1] = from[1];
+}
+template <class C>
+struct Ranks;
+template <>
+struct Ranks<__bf16> {
+    typedef TwoPlanes H;
+    typedef bf16x8 F;
+    static __device__ __forceinline__ F stored(const __bf16 (&v)[8])
+    {
+        F f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = v[e];
+        return f;
+    }
+    static __device__ __forceinline__ f32x4 add(const F &c, const H &h, f32x4 acc)
+    {
+        return Frag<__bf16>::mfma(c, h.high, Frag<__bf16>::mfma(c, h.low, acc));
+    }
+};
+template <>
+struct Ranks<_Float16> {
+    typedef TwoPlanes H;
+    typedef TwoPlanes F;
+    static __device__ __forceinline__ F stored(const _Float16 (&v)[8])
+    {
+        F f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float x = (float)v[e], high = (float)(__bf16)x;
+            f.high[e] = (__bf16)x;
+            f.low[e] = (__bf16)(__builtin_isinf(x) || __builtin_isnan(x) ? 0.0f : x - high);
+        }
+        return f;
+    }
+    static __device__ __forceinline__ f32x4 add(const F &c, const H &h, f32x4 acc)
+    {
+        return Frag<__bf16>::mfma(c.high, h.high, Frag<__bf16>::mfma(c.high, h.low, Frag<__bf16>::mfma(c.low, h.high, acc)));
+    }
+};
+template <>
+struct Ranks<float> {
+    typedef EightFloats H;
+    typedef EightFloats F;
+    static __device__ __forceinline__ F stored(const float (&v)[8])
+    {
+        F f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f.v[e / 4][e % 4] = v[e];
+        return f;
+    }
+    static __device__ __forceinline__ f32x4 add(const F &c, const H &h, f32x4 acc)
+    {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(c.v[e / 4][e % 4], h.v[e / 4][e % 4], acc, 0, 0, 0);
+        return acc;
+    }
+};
+
+// Eight ranks of a row's hidden values, from rank k on.
+__device__ __forceinline__ void load_hidden(const Expand &e, int64_t row, int k, float (&v)[8])
+{
+    const float *from = e.hidden + row * e.c.rank + k;
+    load_some<float, 8>(from, e.c.rank - k, v);
+    for (int p = 1; p < e.parts; ++p) {
+        float more[8];
+        load_some<float, 8>(from + p * e.part_stride, e.c.rank - k, more);
+#pragma unroll
+        for (int n = 0; n < 8; ++n) v[n] += more[n];
+    }
+}
+
+// A row's adapter: -1 for none, -2 for an id out of range.
+__device__ __forceinline__ int id_of(const Expand &e, int64_t row, int64_t rows)
+{
+    if (row >= rows) return -1;
+    const int64_t id = e.ids[row];
+    return id >= 0 && id < e.c.count ? (int)id : id == -1 ? -1 : -2;
+}
+
+// E: the tiles' type; C: the adapters'.  The wavefront's rows are taken adapter
+// by adapter, the others' hidden values zero: tokens of a sequence share
+// theirs.  Bound by the matrix cores, as the product alone is.
+template <class E, class C, int BM, int BN, int WM, int WN, bool B_MC>
+__global__ __launch_bounds__(64 * WM * WN) void adapted_kernel(ProductArgs a)
+{
+    typedef TileProduct<E, BM, BN, WM, WN, false, B_MC, m16::Operands, true> Tile;
+    constexpr int H = kHeld<Tile>;
+    __shared__ __align__(1024) char lds[Tile::kLds];
+    struct Ahead {};
+    Tile::run(a.op, (lds_char *)lds, [](int, int) { return Ahead{}; },
+              [&](typename Tile::Acc &acc, int row0, int col0, int split, Ahead) {
+        const int lane = m16::thread_anew() & 63, l16 = lane & 15, quarter = lane >> 4;
+        // 32 rows at a time, which leaves the other accumulators where they are;
+        // the first part of a split sum adds it
+        const int padded = (int)planes_rank(a.e.c.rank);
+#pragma unroll
+        for (int i0 = 0; i0 < Tile::FM; i0 += 2) {
+            int id[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) id[i] = split == 0 ? id_of(a.e, row0 + (i0 + i) * 16 + l16, a.op.M) : -1;
+            uint64_t left = (__ballot(id[0] >= 0) & 0xFFFF) | __ballot(id[1] >= 0) << 16;
+            left &= 0xFFFFFFFF;
+            while (left != 0) {
+                const int at = __builtin_ctzll(left), now = __builtin_amdgcn_readlane(at < 16 ? id[0] : id[1], at & 15);
+                left &= ~((__ballot(id[0] == now) & 0xFFFF) | __ballot(id[1] == now) << 16);
+                const C *c = (const C *)a.e.c.p + now * a.e.c.stride;
+                // summed apart and added to its own rows alone: what another
+                // adapter holds, infinities and NaN too, does not reach them
+                f32x4 more[2][Tile::FN] = {};
+                for (int k0 = 0; k0 < padded; k0 += 32) {
+                    // worked out anew, not kept in registers over the loop
+                    const int lane = m16::thread_anew() & 63, l16 = lane & 15, quarter = lane >> 4;
+                    const int k = k0 + 8 * quarter;
+                    typename Ranks<C>::H h[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) read_planes(a.e.planes, min(row0 + (i0 + i) * 16 + l16, a.op.M - 1), k, padded, h[i]);
+#pragma unroll
+                    for (int j = 0; j < Tile::FN; ++j) {
+                        // (the registers hold no more than one block's loads)
+                        if (Tile::FM == 8 && sizeof(C) == 2) asm volatile("" ::: "memory");
+                        // the column at index l16 of block j (mfma16.h)
+                        const int col = min(col0 + 4 * Tile::FN * (l16 >> 2) + 4 * j + (l16 & 3), a.op.N - 1);
+                        C v[8];
+                        if constexpr (B_MC) {
+                            const C *from = c + k0 * a.e.c.ld;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const int r = min(8 * quarter + e, a.e.c.rank - 1 - k0);  // ranks past the last meet zeros
+                                const C x = from[(uint32_t)r * (uint32_t)a.e.c.ld + (uint32_t)col];
+                                v[e] = k + e < a.e.c.rank ? x : (C)0.0f;
+                            }
+                        } else {
+                            load_some<C, 8>(c + col * a.e.c.ld + k, a.e.c.rank - k, v);
+                        }
+                        const typename Ranks<C>::F f = Ranks<C>::stored(v);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) more[i][j] = Ranks<C>::add(f, h[i], more[i][j]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (id[i] == now) {
+#pragma unroll
+                        for (int j = 0; j < Tile::FN; ++j) acc[i0 + i][j] += more[i][j];
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (id[i] == -2) {
+#pragma unroll
+                    for (int j = 0; j < Tile::FN; ++j) acc[i0 + i][j] = f32x4{NAN, NAN, NAN, NAN};
+                }
+        }
+        const int col = col0 + H * quarter, left = a.op.N - col;
+        if (left <= 0) return;
+#pragma unroll
+        for (int i = 0; i < Tile::FM; ++i) {
+            const int row = row0 + i * 16 + l16;
+            if (row >= a.op.M) continue;
+            float v[H];
+#pragma unroll
+            for (int e = 0; e < H; ++e) v[e] = acc[i][e / 4][e % 4];
+            const int64_t at = (int64_t)row * a.ldo + col + (int64_t)split * a.split_stride;
+            if (a.dtype == TGEMM_F32) store_row<float, H>((float *)a.out + at, v, left);
+            else store_row<E, H>((E *)a.out + at, v, left);
+        }
+    });
+}
+
+// ---- a few rows ------------------------------------------------------------
+
+// Fragments straight from device memory, no LDS stage and no barrier, as the
+// loss operators take a few rows: a wavefront takes 16 columns of the result
+// and R blocks of 16 rows, four wavefronts a quarter of the sum each.  Then each
+// lane adds its own rows' adapters on the vector units: there may be as many as
+// rows, and their matrices' loads do not wait for one another.
+template <class In, int R>
+__global__ __launch_bounds__(256) void adapted_few_kernel(FewArgs a)
+{
+    constexpr int S = 4, U = sizeof(In) == 4 ? 2 : R == 4 ? 2 : 4;
+    __shared__ f32x4 sums[S][R][64];
+    const int lane = threadIdx.x & 63, part = threadIdx.x >> 6, l16 = lane & 15, quarter = lane >> 4;
+    const int col0 = blockIdx.x * 16;
+    const In *w = (const In *)a.W + (int64_t)min(col0 + l16, a.N - 1) * a.ldw + 8 * quarter;
+    const In *x[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) x[i] = (const In *)a.X + (int64_t)min(16 * i + l16, a.T - 1) * a.ldx + 8 * quarter;
+    f32x4 acc[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) acc[i] = f32x4{0, 0, 0, 0};
+    auto multiply = [&](const In (&vw)[8], const In (&vx)[R][8]) {
+        if constexpr (sizeof(In) == 2) {
+            typename Frag<In>::type fw;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) fw[e] = vw[e];
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                typename Frag<In>::type fx;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) fx[e] = vx[i][e];
+                acc[i] = Frag<In>::mfma(fw, fx, acc[i]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+#pragma unroll
+                for (int i = 0; i < R; ++i) acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(vw[e], vx[i][e], acc[i], 0, 0, 0);
+        }
+    };
+    In vw[2][U][8], vx[2][U][R][8];
+    auto load = [&](int set, int k) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            load_some<In, 8>(w + k + 32 * u, 8, vw[set][u]);
+#pragma unroll
+            for (int i = 0; i < R; ++i) load_some<In, 8>(x[i] + k + 32 * u, 8, vx[set][u][i]);
+        }
+    };
+    auto use = [&](int set) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) multiply(vw[set][u], vx[set][u]);
+    };
+    const int all = a.D / (32 * U), each = (all + S - 1) / S, whole = min(all, (part + 1) * each);
+    int n = part * each;
+    if (n < whole) {
+        load(0, n * 32 * U);
+        for (++n; n + 1 < whole; n += 2) {
+            load(1, n * 32 * U);
+            use(0);
+            load(0, (n + 1) * 32 * U);
+            use(1);
+        }
+        if (n < whole) {
+            load(1, n * 32 * U);
+            use(0);
+            use(1);
+        } else {
+            use(0);
+        }
+    }
+    if (part == S - 1) {
+        for (int k = all * 32 * U; k < a.D; k += 32) {
+            const int left = a.D - (k + 8 * quarter);
+            In zw[8], zx[R][8];
+            load_some<In, 8>(w + k, left, zw);
+#pragma unroll
+            for (int i = 0; i < R; ++i) load_some<In, 8>(x[i] + k, left, zx[i]);
+            multiply(zw, zx);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) sums[part][i][lane] = acc[i];
+    __syncthreads();
+    // wavefront `part` finishes the blocks of rows part, part + 4, ...: row l16, columns col0 + 4·quarter + r
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        if (i % S != part) continue;
+        f32x4 v = sums[0][i][lane] + sums[1][i][lane] + sums[2][i][lane] + sums[3][i][lane];
+        const int row = 16 * i + l16, col = col0 + 4 * quarter;
+        if (row >= a.T) continue;
+        const int id = id_of(a.e, row, a.T);
+        if (id >= 0) {
+            const In *c[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) c[r] = (const In *)a.e.c.p + id * a.e.c.stride + (int64_t)min(col + r, a.N - 1) * a.e.c.ld;
+            f32x4 more{0, 0, 0, 0};
+            for (int k = 0; k < a.e.c.rank; k += 8) {
+                In b[4][8];
+                float h[8];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) load_some<In, 8>(c[r] + k, a.e.c.rank - k, b[r]);
+                load_hidden(a.e, row, k, h);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) more[r] = fmaf(h[e], (float)b[r][e], more[r]);
+            }
+            const float factor = a.e.scales != nullptr ? a.e.scales[id] : 1.0f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = fmaf(factor, more[r], v[r]);
+        } else if (id == -2) {
+            v = f32x4{NAN, NAN, NAN, NAN};
+        }
+        In *to = (In *)a.Y + row * a.ldy + col;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (col + r < a.N) to[r] = (In)v[r];
+    }
+}
+
+template <class In>
+void few(const FewArgs &a, hipStream_t stream)
+{
+    const unsigned grid = (unsigned)((a.N + 15) / 16);
+    if (a.T <= 16) adapted_few_kernel<In, 1><<<grid, 256, 0, stream>>>(a);
+    else if (a.T <= 32) adapted_few_kernel<In, 2><<<grid, 256, 0, stream>>>(a);
+    else adapted_few_kernel<In, 4><<<grid, 256, 0, stream>>>(a);
+}
+
+template <bool B_MC>
+hipError_t product(bool half, int tile, const ProductArgs &a, hipStream_t stream)
+{
+    const int64_t ids = a.op.ids(), most = (int64_t)256 * loss::kTiles[tile].wg_per_cu;
+    const unsigned grid = (unsigned)(ids < most ? ids : most);
+    switch (tile) {
+#define X(I, BM, BN, WM, WN)                                                                                             \
+    case I:                                                                                                              \
+        if (a.stored == TGEMM_F32) adapted_kernel<__bf16, float, BM, BN, WM, WN, B_MC><<<grid, 64 * WM * WN, 0, stream>>>(a); \
+        else if (half) adapted_kernel<_Float16, _Float16, BM, BN, WM, WN, B_MC><<<grid, 64 * WM * WN, 0, stream>>>(a);   \
+        else adapted_kernel<__bf16, __bf16, BM, BN, WM, WN, B_MC><<<grid, 64 * WM * WN, 0, stream>>>(a);                 \
+        break;
+        TGEMM_TILES(X)
+#undef X
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_product(bool half, bool b_mc, int tile, const ProductArgs &a, hipStream_t stream)
+{
+    return b_mc ? product<true>(half, tile, a, stream) : product<false>(half, tile, a, stream);
+}
+
+hipError_t launch_few(const FewArgs &a, hipStream_t stream)
+{
+    if (a.dtype == TGEMM_F32) few<float>(a, stream);
+    else if (a.dtype == TGEMM_BF16) few<__bf16>(a, stream);
+    else few<_Float16>(a, stream);
+    return hipGetLastError();
+}
+
+}  // namespace adapters
+}  // namespace tgemm

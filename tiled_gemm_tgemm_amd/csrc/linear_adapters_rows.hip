@@ -1,0 +1,546 @@
+// The sums of few columns that low-rank adapters take: a token's product with
+// its adapter's first matrix, the tokens in the order of their adapters, and
+// the gradients of both matrices.
+#include "linear_adapters.h"
+#include "mfma16.h"
+#include "some.h"
+
+namespace tgemm {
+namespace adapters {
+namespace {
+
+using m16::bf16x8;
+using m16::f32x4;
+using m16::Frag;
+using m16::load_some;
+
+// Eight values of k with eight values of k of 16 rows each, added to acc: one
+// instruction for 16-bit values, eight of four k's for float32.
+template <class In>
+struct Step {
+    typedef typename Frag<In>::type type;
+    static __device__ __forceinline__ type make(const In (&v)[8])
+    {
+        type f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = v[e];
+        return f;
+    }
+    static __device__ __forceinline__ f32x4 add(const In (&a)[8], const In (&b)[8], f32x4 acc) { return Frag<In>::mfma(make(a), make(b), acc); }
+};
+template <>
+struct Step<float> {
+    static __device__ __forceinline__ f32x4 add(const float (&a)[8], const float (&b)[8], f32x4 acc)
+    {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], acc, 0, 0, 0);
+        return acc;
+    }
+};
+
+// x = high + low to 2^-17 of itself.
+__device__ __forceinline__ void halves(float x, __bf16 &high, __bf16 &low)
+{
+    high = (__bf16)x;
+    float rest = x - (float)high;
+    if (__builtin_isinf(rest) || __builtin_isnan(rest)) rest = 0.0f;  // all in the high part
+    low = (__bf16)rest;
+}
+
+// Four hidden values of a row, from rank `at` on, as the products read them.
+template <bool WHOLE>
+__device__ __forceinline__ void put_planes(void *planes, int64_t row, int at, int rank, const f32x4 &v, float factor)
+{
+    const int padded = (int)planes_rank(rank);
+    if (at >= padded) return;
+    float x[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) x[r] = at + r < rank ? v[r] * factor : 0.0f;
+    if constexpr (WHOLE) {
+        *(f32x4 *)((float *)planes + row * padded + at) = f32x4{x[0], x[1], x[2], x[3]};
+    } else {
+        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+        bf16x4 high, low;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            __bf16 h, l;
+            halves(x[r], h, l);
+            high[r] = h;
+            low[r] = l;
+        }
+        __bf16 *to = (__bf16 *)planes + row * 2 * padded + at;
+        *(bf16x4 *)to = high;
+        *(bf16x4 *)(to + padded) = low;
+    }
+}
+
+// A work-group takes 16 rows and a part of the sum, its four wavefronts the
+// part's steps of 32 in turn; for each adapter that the rows have (the
+// `slots` work-groups of a block of rows share them) 16·BLOCKS ranks at a
+// time.  Rows are read where they lie and once for every adapter among the 16:
+// tokens of a sequence share theirs.
+template <class In, int BLOCKS, bool RANK_INNER>
+__global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a)
+{
+    __shared__ f32x4 sums[3][BLOCKS][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, quarter = lane >> 4;
+    const int64_t row = (int64_t)blockIdx.x * 16 + l16;
+    int id = -1;
+    if (row < a.T) {
+        const int64_t i = a.ids[row];
+        if (i >= 0 && i < a.c.count) id = (int)i;
+    }
+    const In *x = (const In *)a.rows + (row < a.T ? row : a.T - 1) * a.ld;
+    const int64_t first = blockIdx.z * a.part_k, last = min(first + a.part_k, a.K);
+    uint32_t left = (uint32_t)__ballot(id >= 0) & 0xFFFF;
+    for (int n = 0; left != 0; ++n) {
+        const int now = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
+        left &= ~(uint32_t)__ballot(id == now);
+        if (n % a.slots != (int)blockIdx.y) continue;
+        const In *c = (const In *)a.c.p + now * a.c.stride;
+        // (with one block of 16 the padding to 32 is a second turn's)
+        for (int rank0 = 0; rank0 < (a.planes != nullptr ? (int)planes_rank(a.c.rank) : a.c.rank); rank0 += 16 * BLOCKS) {
+            f32x4 acc[BLOCKS];
+#pragma unroll
+            for (int b = 0; b < BLOCKS; ++b) acc[b] = f32x4{0, 0, 0, 0};
+            auto load = [&](int64_t k, In (&vx)[8], In (&vc)[BLOCKS][8]) {
+                const int64_t at = k + 8 * quarter;
+                load_some<In, 8>(x + at, last - at, vx);
+#pragma unroll
+                for (int b = 0; b < BLOCKS; ++b) {
+                    const int rank = min(rank0 + 16 * b + l16, a.c.rank - 1);  // past the last: not stored
+                    if constexpr (RANK_INNER) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) vc[b][e] = at + e < last ? c[(at + e) * a.c.ld + rank] : (In)0.0f;
+                    } else {
+                        load_some<In, 8>(c + rank * a.c.ld + at, last - at, vc[b]);
+                    }
+                }
+            };
+            constexpr int U = sizeof(In) == 4 || BLOCKS == 4 ? 2 : 4;
+            int64_t k = first + 32 * wave;
+            for (; k + 128 * (U - 1) + 32 <= last; k += 128 * U) {
+                In vx[U][8], vc[U][BLOCKS][8];
+#pragma unroll
+                for (int u = 0; u < U; ++u) load(k + 128 * u, vx[u], vc[u]);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int b = 0; b < BLOCKS; ++b) acc[b] = Step<In>::add(vc[u][b], vx[u], acc[b]);
+            }
+            for (; k < last; k += 128) {
+                In vx[8], vc[BLOCKS][8];
+                load(k, vx, vc);
+#pragma unroll
+                for (int b = 0; b < BLOCKS; ++b) acc[b] = Step<In>::add(vc[b], vx, acc[b]);
+            }
+            if (wave > 0) {
+#pragma unroll
+                for (int b = 0; b < BLOCKS; ++b) sums[wave - 1][b][lane] = acc[b];
+            }
+            __syncthreads();
+            if (wave == 0 && id == now) {
+                const float factor = a.scales != nullptr ? a.scales[now] : 1.0f;
+#pragma unroll
+                for (int b = 0; b < BLOCKS; ++b) {
+                    const f32x4 v = acc[b] + sums[0][b][lane] + sums[1][b][lane] + sums[2][b][lane];
+                    const int rank = rank0 + 16 * b + 4 * quarter;
+                    if (a.part != nullptr) {
+                        float *to = a.part + ((int64_t)blockIdx.z * a.T + row) * a.c.rank + rank;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (rank + r < a.c.rank) to[r] = v[r];
+                    }
+                    if (a.planes != nullptr) put_planes<sizeof(In) == 4>(a.planes, row, rank, a.c.rank, v, factor);
+                }
+            }
+            __syncthreads();
+        }
+    }
+}
+
+template <bool WHOLE>
+__global__ __launch_bounds__(256) void finish_kernel(ShrinkArgs a, float *hidden, void *planes)
+{
+    const int per_row = (int)planes_rank(a.c.rank) / 4;
+    const int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x, row = n / per_row;
+    if (row >= a.T) return;
+    const int at = (int)(n % per_row) * 4;
+    const int64_t id = a.ids[row];
+    if (id < 0 || id >= a.c.count) return;
+    f32x4 v{0, 0, 0, 0};
+    for (int p = 0; p < a.parts; ++p) {
+        const float *from = a.part + (p * a.T + row) * a.c.rank + at;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (at + r < a.c.rank) v[r] += from[r];
+    }
+    if (hidden != nullptr) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (at + r < a.c.rank) hidden[row * a.c.rank + at + r] = v[r];
+    }
+    if (planes != nullptr) put_planes<WHOLE>(planes, row, at, a.c.rank, v, a.scales != nullptr ? a.scales[id] : 1.0f);
+}
+
+template <class In, int BLOCKS>
+void shrink(const ShrinkArgs &a, hipStream_t stream)
+{
+    const dim3 grid((unsigned)((a.T + 15) / 16), a.slots, a.parts);
+    if (a.c.rank_inner) shrink_kernel<In, BLOCKS, true><<<grid, 256, 0, stream>>>(a);
+    else shrink_kernel<In, BLOCKS, false><<<grid, 256, 0, stream>>>(a);
+}
+template <class In>
+void shrink(const ShrinkArgs &a, hipStream_t stream)
+{
+    if (a.c.rank <= 16) shrink<In, 1>(a, stream);
+    else if (a.c.rank <= 32) shrink<In, 2>(a, stream);
+    else shrink<In, 4>(a, stream);
+}
+
+// ---- grouping --------------------------------------------------------------
+
+// The sums over the work-group's threads before this one, and over all.
+__device__ __forceinline__ int before(int v, int *room, int &all)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+    int sum = v;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int other = __shfl_up(sum, d);
+        if (lane >= d) sum += other;
+    }
+    if (lane == 63) room[wave] = sum;
+    __syncthreads();
+    int base = 0;
+    all = 0;
+    for (int w = 0; w < waves; ++w) {
+        base += w < wave ? room[w] : 0;
+        all += room[w];
+    }
+    __syncthreads();
+    return base + sum - v;
+}
+
+// Work-group i counts the tokens of smaller adapters and lists its own in
+// their order: the ids are read twice by each adapter's, and nothing is
+// counted with atomics.
+__global__ __launch_bounds__(1024) void group_kernel(GroupArgs a)
+{
+    __shared__ int room[16];
+    const int mine = blockIdx.x;
+    int smaller = 0, own = 0;
+    for (int t = threadIdx.x; t < a.T; t += 1024) {
+        const int64_t id = a.ids[t];
+        smaller += id >= 0 && id < mine;
+        own += id == mine;
+    }
+    int start, total;
+    before(smaller, room, start);
+    before(own, room, total);
+    if (threadIdx.x == 0) {
+        a.starts[mine] = start;
+        if (mine == a.count - 1) a.starts[a.count] = start + total;
+    }
+    constexpr int kEach = 8;
+    for (int t0 = 0; t0 < a.T && total > 0; t0 += 1024 * kEach) {
+        const int t = t0 + threadIdx.x * kEach;
+        uint32_t is = 0;
+#pragma unroll
+        for (int e = 0; e < kEach; ++e)
+            if (t + e < a.T && a.ids[t + e] == mine) is |= 1u << e;
+        int found;
+        int at = start + before(__popc(is), room, found);
+#pragma unroll
+        for (int e = 0; e < kEach; ++e)
+            if (is >> e & 1) a.order[at++] = t + e;
+        start += found;
+    }
+}
+
+__global__ __launch_bounds__(1024) void chunks_kernel(GroupArgs a)
+{
+    __shared__ int room[16];
+    const Cut cut = a.cuts[blockIdx.x];
+    int chunk0 = 0, slot0 = 0;
+    for (int i0 = 0; i0 < a.count; i0 += 1024) {
+        const int i = i0 + threadIdx.x;
+        const int from = i < a.count ? a.starts[i] : 0, tokens = i < a.count ? a.starts[i + 1] - from : 0;
+        const int chunks = (tokens + cut.tokens - 1) / cut.tokens, slots = chunks > 1 ? chunks : 0;
+        int all_chunks, all_slots;
+        const int chunk = chunk0 + before(chunks, room, all_chunks), slot = slot0 + before(slots, room, all_slots);
+        if (i < a.count) {
+            cut.joins[i] = make_int2(slot, chunks);
+            // an adapter's tokens are dealt evenly, in whole 64s
+            const int each = chunks ? ((tokens + chunks - 1) / chunks + 63) / 64 * 64 : 0;
+            for (int n = 0; n < chunks; ++n)
+                cut.chunks[chunk + n] = Chunk{i, from + n * each, min(each, tokens - n * each), slots ? slot + n : -1};
+        }
+        chunk0 += all_chunks;
+        slot0 += all_slots;
+    }
+    if (threadIdx.x == 0) *cut.chunk_count = chunk0;
+}
+
+// ---- gradients -------------------------------------------------------------
+
+// The sum over 32 tokens (8 a lane) of z·v: bf16 values are taken as they are
+// and fp16 ones, which bf16's range holds, as two bf16 planes; v in two planes;
+// float32 in float32.
+template <class In>
+struct Outer;
+template <>
+struct Outer<float> {
+    typedef float Z;
+    struct F {
+        float v[8];
+    };
+    typedef F Zf;
+    typedef F Vf;
+    static __device__ __forceinline__ Zf z_of(const float (&v)[8]) { Zf f; 
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f.v[e] = v[e];
+        return f; }
+    static __device__ __forceinline__ Vf v_of(const float (&v)[8]) { return z_of(v); }
+    template <bool Z_FIRST>
+    static __device__ __forceinline__ f32x4 add(const Zf &z, const Vf &v, f32x4 acc)
+    {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (Z_FIRST) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(z.v[e], v.v[e], acc, 0, 0, 0);
+            else acc = __builtin_amdgcn_mfma_f32_16x16x4f32(v.v[e], z.v[e], acc, 0, 0, 0);
+        }
+        return acc;
+    }
+};
+struct OuterPlanes {
+    struct Vf {
+        bf16x8 high, low;
+    };
+    static __device__ __forceinline__ Vf v_of(const float (&v)[8])
+    {
+        Vf f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            __bf16 h, l;
+            halves(v[e], h, l);
+            f.high[e] = h;
+            f.low[e] = l;
+        }
+        return f;
+    }
+    template <bool Z_FIRST>
+    static __device__ __forceinline__ f32x4 one(const bf16x8 &z, const bf16x8 &v, f32x4 acc)
+    {
+        return Z_FIRST ? Frag<__bf16>::mfma(z, v, acc) : Frag<__bf16>::mfma(v, z, acc);
+    }
+};
+template <>
+struct Outer<__bf16> : OuterPlanes {
+    typedef bf16x8 Zf;
+    static __device__ __forceinline__ Zf z_of(const __bf16 (&v)[8])
+    {
+        Zf f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = v[e];
+        return f;
+    }
+    template <bool Z_FIRST>
+    static __device__ __forceinline__ f32x4 add(const Zf &z, const Vf &v, f32x4 acc)
+    {
+        return one<Z_FIRST>(z, v.high, one<Z_FIRST>(z, v.low, acc));
+    }
+};
+template <>
+struct Outer<_Float16> : OuterPlanes {
+    typedef Vf Zf;
+    static __device__ __forceinline__ Zf z_of(const _Float16 (&v)[8])
+    {
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = (float)v[e];
+        return v_of(f);
+    }
+    template <bool Z_FIRST>
+    static __device__ __forceinline__ f32x4 add(const Zf &z, const Vf &v, f32x4 acc)
+    {
+        return one<Z_FIRST>(z.high, v.high, one<Z_FIRST>(z.high, v.low, one<Z_FIRST>(z.low, v.high, acc)));
+    }
+};
+
+// A work-group takes 128 columns of the rows, 16·BLOCKS ranks and a chunk of an
+// adapter's tokens, 64 at a time through LDS; the loads of the next 64 are
+// under way while these are multiplied.  A wavefront takes 32 columns.  Bound by
+// reading the rows once.
+template <class In, int BLOCKS, bool RANK_INNER>
+__global__ __launch_bounds__(256) void outer_kernel(OuterArgs a)
+{
+    constexpr int kCols = kOuterColumns, kTokens = kOuterTokens, kRanks = 16 * BLOCKS;
+    constexpr int kPiece = 16 / sizeof(In), kPieces = kCols / kPiece * kTokens / 256;
+    constexpr int kVals = kRanks * kTokens / 256;
+    constexpr int kLdZ = kCols + 16 / sizeof(In), kLdV = kRanks + 1;
+    __shared__ __align__(16) In zs[kTokens * kLdZ];
+    __shared__ float vs[kTokens * kLdV];
+    if ((int)blockIdx.y >= *a.cut.chunk_count) return;
+    const Chunk chunk = a.cut.chunks[blockIdx.y];
+    const int thread = threadIdx.x, lane = thread & 63, wave = thread >> 6, l16 = lane & 15, quarter = lane >> 4;
+    const int col0 = blockIdx.x * kCols, rank0 = blockIdx.z * kRanks;
+    const int *order = a.order + chunk.first;
+    f32x4 acc[2][BLOCKS];
+#pragma unroll
+    for (int b = 0; b < BLOCKS; ++b) acc[0][b] = acc[1][b] = f32x4{0, 0, 0, 0};
+
+    In z[kPieces][kPiece];
+    float v[kVals];
+    auto load = [&](int t0) {
+#pragma unroll
+        for (int n = 0; n < kPieces; ++n) {
+            const int piece = n * 256 + thread, t = t0 + piece / (kCols / kPiece), col = col0 + piece % (kCols / kPiece) * kPiece;
+            const bool there = t < chunk.tokens && col < a.C;
+            load_some<In, kPiece>((const In *)a.rows + (there ? order[t] * a.ld + col : 0), there ? a.C - col : 0, z[n]);
+        }
+#pragma unroll
+        for (int n = 0; n < kVals; ++n) {
+            const int at = n * 256 + thread, t = t0 + at / kRanks, rank = rank0 + at % kRanks;
+            v[n] = t < chunk.tokens && rank < a.rank ? a.small[(int64_t)order[t] * a.rank + rank] : 0.0f;
+        }
+    };
+    load(0);
+    for (int t0 = 0; t0 < chunk.tokens; t0 += kTokens) {
+#pragma unroll
+        for (int n = 0; n < kPieces; ++n) {
+            const int piece = n * 256 + thread, t = piece / (kCols / kPiece), col = piece % (kCols / kPiece) * kPiece;
+            typedef In piece_t __attribute__((ext_vector_type(kPiece)));
+            piece_t p;
+#pragma unroll
+            for (int e = 0; e < kPiece; ++e) p[e] = z[n][e];
+            *(piece_t *)(zs + t * kLdZ + col) = p;
+        }
+#pragma unroll
+        for (int n = 0; n < kVals; ++n) {
+            const int at = n * 256 + thread;
+            vs[at / kRanks * kLdV + at % kRanks] = v[n];
+        }
+        __syncthreads();
+        if (t0 + kTokens < chunk.tokens) load(t0 + kTokens);
+#pragma unroll
+        for (int s = 0; s < kTokens / 32; ++s) {
+            typename Outer<In>::Zf zf[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                In e8[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) e8[e] = zs[(32 * s + 8 * quarter + e) * kLdZ + 32 * wave + 16 * j + l16];
+                zf[j] = Outer<In>::z_of(e8);
+            }
+#pragma unroll
+            for (int b = 0; b < BLOCKS; ++b) {
+                float e8[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) e8[e] = vs[(32 * s + 8 * quarter + e) * kLdV + 16 * b + l16];
+                const typename Outer<In>::Vf vf = Outer<In>::v_of(e8);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[j][b] = Outer<In>::template add<!RANK_INNER>(zf[j], vf, acc[j][b]);
+            }
+        }
+        __syncthreads();
+    }
+
+    // RANK_INNER: a lane holds column l16, ranks 4·quarter + r; otherwise rank l16, columns 4·quarter + r
+    const bool joined = chunk.slot >= 0;
+    const float scale = a.scales != nullptr ? a.scales[chunk.adapter] : 1.0f;
+    const int64_t ld = joined ? (RANK_INNER ? a.rank : a.C) : a.ldo;
+    const int64_t base = joined ? (int64_t)chunk.slot * a.C * a.rank : chunk.adapter * a.stride_out;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int col = col0 + 32 * wave + 16 * j + (RANK_INNER ? l16 : 4 * quarter + r);
+                const int rank = rank0 + 16 * b + (RANK_INNER ? 4 * quarter + r : l16);
+                if (col >= a.C || rank >= a.rank) continue;
+                const int64_t at = base + (RANK_INNER ? col * ld + rank : rank * ld + col);
+                if (joined) a.part[at] = acc[j][b][r];
+                else ((In *)a.out)[at] = (In)(acc[j][b][r] * scale);
+            }
+}
+
+// Adapters without tokens get zeros, those of several chunks their sum.
+template <class In>
+__global__ __launch_bounds__(256) void join_kernel(OuterArgs a)
+{
+    const int adapter = blockIdx.y;
+    const int2 join = a.cut.joins[adapter];
+    if (join.y == 1) return;
+    const float scale = a.scales != nullptr ? a.scales[adapter] : 1.0f;
+    const int64_t inner = a.rank_inner ? a.rank : a.C, outer = a.rank_inner ? a.C : a.rank, size = inner * outer;
+    for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < size; n += (int64_t)gridDim.x * 256) {
+        float sum = 0;
+        for (int c = 0; c < join.y; ++c) sum += a.part[(join.x + c) * size + n];
+        ((In *)a.out)[adapter * a.stride_out + n / inner * a.ldo + n % inner] = (In)(join.y ? sum * scale : 0.0f);
+    }
+}
+
+template <class In, int BLOCKS>
+void outer(const OuterArgs &a, hipStream_t stream)
+{
+    const dim3 grid((unsigned)((a.C + kOuterColumns - 1) / kOuterColumns), a.most_chunks, (a.rank + 16 * BLOCKS - 1) / (16 * BLOCKS));
+    if (a.rank_inner) outer_kernel<In, BLOCKS, true><<<grid, 256, 0, stream>>>(a);
+    else outer_kernel<In, BLOCKS, false><<<grid, 256, 0, stream>>>(a);
+}
+template <class In>
+void outer(const OuterArgs &a, hipStream_t stream)
+{
+    if (a.rank <= 16) outer<In, 1>(a, stream);
+    else if (a.rank <= 32) outer<In, 2>(a, stream);
+    else outer<In, 4>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_shrink(const ShrinkArgs &a, hipStream_t stream)
+{
+    if (a.dtype == TGEMM_F32) shrink<float>(a, stream);
+    else if (a.dtype == TGEMM_BF16) shrink<__bf16>(a, stream);
+    else shrink<_Float16>(a, stream);
+    return hipGetLastError();
+}
+
+hipError_t launch_finish(const ShrinkArgs &a, float *hidden, void *planes, hipStream_t stream)
+{
+    const unsigned grid = (unsigned)((a.T * (planes_rank(a.c.rank) / 4) + 255) / 256);
+    if (a.dtype == TGEMM_F32) finish_kernel<true><<<grid, 256, 0, stream>>>(a, hidden, planes);
+    else finish_kernel<false><<<grid, 256, 0, stream>>>(a, hidden, planes);
+    return hipGetLastError();
+}
+
+hipError_t launch_group(const GroupArgs &a, hipStream_t stream)
+{
+    group_kernel<<<a.count, 1024, 0, stream>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    chunks_kernel<<<2, 1024, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_outer(const OuterArgs &a, hipStream_t stream)
+{
+    if (a.dtype == TGEMM_F32) outer<float>(a, stream);
+    else if (a.dtype == TGEMM_BF16) outer<__bf16>(a, stream);
+    else outer<_Float16>(a, stream);
+    return hipGetLastError();
+}
+
+hipError_t launch_join(const OuterArgs &a, hipStream_t stream)
+{
+    const int64_t blocks = ((int64_t)a.C * a.rank + 1023) / 1024;
+    const dim3 grid((unsigned)(blocks < 1024 ? blocks : 1024), a.count);
+    if (a.dtype == TGEMM_F32) join_kernel<float><<<grid, 256, 0, stream>>>(a);
+    else if (a.dtype == TGEMM_BF16) join_kernel<__bf16><<<grid, 256, 0, stream>>>(a);
+    else join_kernel<_Float16><<<grid, 256, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace adapters
+}  // namespace tgemm

@@ -4,6 +4,7 @@
 // the meaning of every argument, are in tgemm.h.
 #include "entry.h"
 #include "linear_loss.h"
+#include "product_plan.h"
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -20,10 +21,6 @@ constexpr int64_t kMaxV = (int64_t)1 << 24;
 constexpr int64_t kMaxD = (int64_t)1 << 22;   // 256 rows of 16-bit values stay within 32-bit offsets
 constexpr int64_t kMaxK = 1024;
 constexpr int64_t kMaxLd = (int64_t)1 << 40;
-// A launch has as many work-groups as the GPU holds at most; they count their
-// tiles in 32 bits, and a tile's number plus a step of the grid has to fit.
-constexpr int64_t kMaxTiles = INT32_MAX - 1024;
-
 // Bytes of one piece of the logits' gradient: large enough that the products
 // of a piece fill the GPU for several rounds, small enough to stay near the
 // 256 MiB last-level cache between the product that writes it and the two
@@ -73,48 +70,6 @@ bool as_stored(const void *p, int64_t ld, const Head &h, int64_t whole = 8)
            reinterpret_cast<uintptr_t>(p) % 16 == 0;
 }
 
-// The tile for an M×N product of `steps` steps, and into how many parts its
-// sum is split (1 where `split` is false): the least estimated time, in µs.  A
-// compute unit holds up to wg_per_cu tiles at once; their step takes as long
-// as their area at the rate that the shape sustains (a 256×256 tile 1.5 µs,
-// 1.37 PFLOP/s on 256 compute units), but not less than the loads' way there
-// and back, and a tile takes 4 µs to begin and to end.  Measured at 32 steps
-// with 256, 128 and 32 rows a tile: 512×16384 40, 29 and 58 µs; 64×32000 43,
-// 23 and 22; 4096×32768 with 8 steps 127, 162 and 275.
-struct Choice {
-    int tile = 0, splits = 1;
-};
-Choice choose_tile(int64_t M, int64_t N, int64_t steps, bool split = false)
-{
-    static const double rate[] = {1.0, 0.83, 0.375};
-    Choice best;
-    double least = -1;
-    for (int i = 0; i < kTileCount; ++i) {
-        const TileShape &s = kTiles[i];
-        const int64_t tiles = ceil_div(M, s.bm) * ceil_div(N, s.bn);
-        for (int64_t parts = 1; parts == 1 || (split && parts <= 64 && steps / parts >= 4); ++parts) {
-            const int64_t on_one = ceil_div(tiles * parts, 256);
-            auto round = [&](int64_t held) {
-                const double step = (double)held * s.bm * s.bn / 65536.0 / rate[i] * 1.5;
-                return (double)ceil_div(steps, parts) * (step > 0.75 ? step : 0.75) + 4.0;
-            };
-            double time = (double)(on_one / s.wg_per_cu) * round(s.wg_per_cu);
-            if (on_one % s.wg_per_cu != 0) time += round(on_one % s.wg_per_cu);
-            // the parts are written and read once more, by another launch
-            if (parts > 1) time += 6.0 + (double)M * (double)N * 8.0 * (double)parts / 5e6;
-            if (least < 0 || time < least) {
-                least = time;
-                best.tile = i;
-                best.splits = (int)parts;
-            }
-        }
-    }
-    return best;
-}
-
-// The parts of a sum of `steps` steps, at most `most`, none of them empty.
-int parts_of(int64_t steps, int64_t most) { return (int)ceil_div(steps, ceil_div(steps, most)); }
-
 // Where a call's buffers lie in its workspace.
 struct Plan {
     bool half = false;
@@ -158,13 +113,6 @@ void plan_operands(Plan &p, const Head &h, bool backward)
     p.copy_x = !as_stored(h.X, h.ldx, h, kStepK) && (!backward || p.half);
     if (p.copy_x) p.x = p.take(h.T * p.Dp * 2 * p.planes);
     if (backward) p.xs = p.take(p.Tp * p.Dp * 2 * p.planes);
-}
-
-// False where a product would have too many tiles.
-bool fits(int64_t M, int64_t N, int tile, int64_t splits)
-{
-    const TileShape &s = kTiles[tile];
-    return ceil_div(M, s.bm) * ceil_div(N, s.bn) <= kMaxTiles / splits;
 }
 
 bool plan_forward(Plan &p, const Head &h, int64_t teacher_k)
@@ -231,20 +179,6 @@ bool plan_backward(Plan &p, const Head &h)
     if (p.dw_splits > 1) p.dw_part = p.take(p.dw_splits * p.piece * p.Dp * 4);
     return fits(p.Tp, p.piece, p.grad_tile, 1) && fits(p.piece, h.D, p.dw_tile, p.dw_splits) &&
            fits(p.dx_rows, h.D, p.dx_tile, p.dx_splits);
-}
-
-Operands operands(int segments, int64_t M, int64_t N, int64_t steps, int tile)
-{
-    const TileShape &s = kTiles[tile];
-    Operands o{};
-    o.segments = segments;
-    o.M = (int)M;
-    o.N = (int)N;
-    o.steps = o.steps_per_split = (int)steps;
-    o.tiles_m = (int)ceil_div(M, s.bm);
-    o.tiles_n = (int)ceil_div(N, s.bn);
-    o.splits = 1;
-    return o;
 }
 
 // Lays out `rows` rows of an operand at dst.

@@ -189,7 +189,9 @@ __device__ __forceinline__ void spread()
 // where a tile ends, so the next tile's are under way by then; as loads come
 // back in order, the epilogue would wait for those with its own.  What it needs
 // for its rows is what `prologue(row0, col0)` returned before the products.
-template <class E, int BM, int BN, int WM, int WN, bool A_MC, bool B_MC, class Op = Operands>
+// ANEW: a tile's first fragments are read once more where it begins, so that
+// the epilogue before it has their registers.
+template <class E, int BM, int BN, int WM, int WN, bool A_MC, bool B_MC, class Op = Operands, bool ANEW = false>
 struct TileProduct {
     static constexpr int kThreads = 64 * WM * WN;
     static constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
@@ -277,6 +279,7 @@ struct TileProduct {
             tile_at<BM, BN>(p, id, m0, n0, split, from, to);
             const int row0 = m0 + wm * (FM * 16), col0 = n0 + wn * (FN * 16);
             const auto ahead = prologue(row0, col0);
+            if constexpr (ANEW) read(stage, 0);
             for (int n = (to - from) * p.segments; n > 0; --n) {
                 // A step on the slices of `stage`, its first fragments read.
                 // The first barrier stands after the phases that read B and

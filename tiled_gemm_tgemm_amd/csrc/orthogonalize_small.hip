@@ -1,6 +1,7 @@
 // Passes over the rows of G for the Newton-Schulz operator: its norm, its
 // planes, and the whole iteration in float64 where one side is small.
 #include "orthogonalize.h"
+#include "some.h"
 
 #include <math.h>
 
@@ -8,26 +9,10 @@ namespace tgemm {
 namespace ortho {
 namespace {
 
+using m16::load_some;
+using m16::Some;
+
 typedef double f64x4 __attribute__((ext_vector_type(4)));
-
-template <class In, int N>
-struct Some {
-    typedef In type __attribute__((ext_vector_type(N), aligned(sizeof(In))));
-};
-
-// N adjacent values, `left` of them there, zero past those.
-template <class In, int N>
-__device__ __forceinline__ void load_some(const In *p, int64_t left, In (&v)[N])
-{
-    if (left >= N) {
-        const typename Some<In, N>::type got = *(const typename Some<In, N>::type *)p;
-#pragma unroll
-        for (int e = 0; e < N; ++e) v[e] = got[e];
-    } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e) v[e] = e < left ? p[e] : (In)0.0f;
-    }
-}
 
 // The work-group's sum, in every thread, in a fixed order.
 __device__ __forceinline__ double sum_of_group(double v, double *room)
