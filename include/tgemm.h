@@ -495,7 +495,7 @@ tgemm_status_t tgemm_linear_kd_backward(tgemm_dtype_t dtype, int64_t T, int64_t 
  *             the adapters' part: in float32).  x·Aᵀ is float32; where it meets
  *             16-bit matrices it is held in two bf16 numbers (17 bits).  A
  *             result is rounded once.
- * Sizes       0 <= T < 2^24, 1 <= N, D <= 2^22, 1 <= count <= 2^15, 1 <= rank <=
+ * Sizes       0 <= T < 2^24, 1 <= N, D <= 2^22, 1 <= count < 2^15, 1 <= rank <=
  *             1024, lda up to 2^26, the other leading dimensions and strides up
  *             to 2^40; larger ones, a product of 2^31 tiles and more, and an
  *             unknown dtype: TGEMM_ERROR_NOT_SUPPORTED.

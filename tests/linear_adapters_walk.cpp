@@ -179,7 +179,7 @@ hipError_t launch_product(bool, bool b_mc, int tile, const ProductArgs &a, hipSt
     out(a.out, a.op.M, a.op.N, a.ldo, a.dtype, a.op.splits, a.split_stride);
     rows(a.e.planes, a.op.M, planes_rank(a.e.c.rank), planes_rank(a.e.c.rank), 4, false, "hidden planes");
     stack(a.e.c, a.op.N, size_of(a.stored), "the product's adapters");
-    if (a.e.c.rank_inner == b_mc) fail("adapters the other way", 0, 0);
+    if (!a.e.c.rank_inner && !b_mc) fail("adapters the other way", 0, 0);
     return hipSuccess;
 }
 hipError_t launch_few(const FewArgs &a, hipStream_t)
@@ -212,17 +212,48 @@ void check_outer(const OuterArgs &a)
     for (int64_t i : {(int64_t)0, (int64_t)a.count - 1})
         rows((char *)a.out + i * a.stride_out * (int64_t)size_of(a.dtype), a.rank_inner ? a.C : a.rank, a.rank_inner ? a.rank : a.C, a.ldo,
              size_of(a.dtype), true, "an adapter's gradient");
+    if (a.most_chunks > 65535) fail("a grid", 0, a.most_chunks);
+}
+int64_t tokens;  // of the call
+hipError_t launch_arrange(const OuterArgs &a, const OuterArgs &b, hipStream_t)
+{
+    for (const OuterArgs *o : {&a, &b}) {
+        if (o->out == nullptr || o->arranged == nullptr) continue;
+        rows(o->small, tokens, o->rank, o->rank, 4, false, "small");
+        if (o->arranged_plane % 64) fail("planes that are not aligned", 0, 0);
+        // whole 64s of every chunk
+        if (o->arranged_plane < (tokens + 64 * ((int64_t)tokens / o->cut.tokens + std::min<int64_t>(o->count, tokens))) / 64 * 64 * o->rank)
+            fail("arranged values' room", 0, 0);
+        rows(o->arranged, 2, o->arranged_plane, o->arranged_plane, 2, true, "arranged");
+    }
+    return hipSuccess;
 }
 hipError_t launch_outer(const OuterArgs &a, hipStream_t)
 {
     check_outer(a);
-    if (a.most_chunks > 65535) fail("a grid", 0, a.most_chunks);
-    rows(a.small, 1, a.rank, a.rank, 4, false, "small");
+    rows(a.rows, tokens, a.C, a.ld, size_of(a.dtype), false, "rows");
+    rows(a.small, tokens, a.rank, a.rank, 4, false, "small");
+    if (a.cut.tokens > kMostTokens) fail("tokens of a chunk", 0, 0);
+    if (a.arranged && (a.dtype == TGEMM_F32 || a.C % 8 || a.ld % 8 || (uintptr_t)a.rows % 16)) fail("rows that are not whole pieces", 0, 0);
+    rows(a.part, 2 * (tokens / a.cut.tokens), (int64_t)a.C * a.rank, (int64_t)a.C * a.rank, 4, true, "sums of chunks");
     return hipSuccess;
 }
-hipError_t launch_join(const OuterArgs &a, hipStream_t)
+hipError_t launch_join(const OuterArgs &a, const OuterArgs &b, hipStream_t)
 {
-    check_outer(a);
+    for (const OuterArgs *o : {&a, &b})
+        if (o->out) check_outer(*o);
+    return hipSuccess;
+}
+hipError_t launch_turn(const TurnArgs &a, const TurnArgs &b, hipStream_t)
+{
+    if (a.from.count + b.from.count > 65535) fail("a grid", 0, 0);
+    for (const TurnArgs *t : {&a, &b}) {
+        if (t->to == nullptr) continue;
+        stack(t->from, t->outer, size_of(t->dtype), "turn's adapters");
+        const int64_t n = t->from.rank_inner ? t->from.rank : t->outer, cols = t->from.rank_inner ? t->outer : t->from.rank;
+        for (int64_t i : {(int64_t)0, (int64_t)t->from.count - 1})
+            rows((char *)t->to + i * t->to_stride * (int64_t)size_of(t->dtype), n, cols, t->to_ld, size_of(t->dtype), true, "turned");
+    }
     return hipSuccess;
 }
 
@@ -248,6 +279,7 @@ int main()
             next += 0x40000000000ull;
             return (void *)at;
         };
+        tgemm::adapters::tokens = T;
         const long long ldx = D + px, ldw = D + pw, ldy = N + py, lda = D + pa, ldb = r + pb, sa = r * lda + pa, sb = N * ldb + pb;
         void *X = place((T ? (T - 1) * ldx + D : 0) * s, false, "X", true), *W = place(((N - 1) * ldw + D) * s, false, "W", true);
         void *A = place(((L - 1) * sa + (r - 1) * lda + D) * s, false, "A"), *B = place(((L - 1) * sb + (N - 1) * ldb + r) * s, false, "B", true);

@@ -29,7 +29,7 @@ using tgemm::m16::kStepK;
 
 constexpr int64_t kMaxT = ((int64_t)1 << 24) - 1;
 constexpr int64_t kMaxSide = (int64_t)1 << 22;  // 256 rows of 16-bit values stay within 32-bit offsets
-constexpr int64_t kMaxRank = 1024, kMaxCount = (int64_t)1 << 15;
+constexpr int64_t kMaxRank = 1024, kMaxCount = ((int64_t)1 << 15) - 1;  // twice that is a launch's z
 constexpr int64_t kMaxLd = (int64_t)1 << 40;
 constexpr int64_t kMaxLdA = (int64_t)1 << 26;   // 32 ranks of float32 stay within 32-bit offsets
 
@@ -79,24 +79,24 @@ bool as_stored(tgemm_dtype_t dtype, const void *p, int64_t ld, int64_t cols, int
     return dtype != TGEMM_F32 && cols % whole == 0 && ld % 8 == 0 && ld <= kMaxSide && reinterpret_cast<uintptr_t>(p) % 16 == 0;
 }
 
-// How a sum over K of one token's values is cut: a work-group's share is 16
-// rows and the adapter's ranks, of which a compute unit takes about 20 GB/s
-// where few of them are at work, so the sum is cut while they are few.
+// How the sums over K of the tokens' hidden values are cut: in parts while there
+// are fewer wavefronts than keep the memory busy.
 struct Shrink {
     int64_t part_k = 0;
-    int parts = 1, slots = 1;
+    int parts = 1, slots = 1, rows_each = 16;
 };
-Shrink shrink_of(int64_t T, int64_t K, int64_t count, bool few)
+Shrink shrink_of(int64_t T, int64_t K, int64_t count)
 {
     Shrink s;
-    const int64_t blocks = ceil_div(T, 16);
-    int64_t parts = few ? 8 : 512 / blocks;
+    s.rows_each = T <= 1024 ? 16 : T < 4096 ? 64 : 128;
+    const int64_t wavefronts = 4 * ceil_div(T, s.rows_each);
+    int64_t parts = 2048 / wavefronts;
     if (parts > ceil_div(K, 512)) parts = ceil_div(K, 512);
     if (parts > 8) parts = 8;
     if (parts < 1) parts = 1;
     s.part_k = round_up(ceil_div(K, parts), 128);
     s.parts = (int)ceil_div(K, s.part_k);
-    s.slots = T <= 1024 ? 16 : 4;
+    s.slots = T <= 1024 ? 16 : 1;
     if (s.slots > count) s.slots = (int)count;
     return s;
 }
@@ -119,7 +119,10 @@ struct Plan {
     int64_t u = -1, hidden = -1, parts_x = -1;
     Choice dw;
     int64_t dw_part = -1;
-    int64_t order = -1, starts = -1, chunks[2] = {-1, -1}, joins[2] = {-1, -1}, counts = -1, sums = -1;
+    int64_t order = -1, starts = -1, chunks[2] = {-1, -1}, joins[2] = {-1, -1}, counts = -1, sums[2] = {-1, -1};
+    int64_t arranged[2] = {-1, -1}, arranged_plane[2] = {0, 0};
+    // the adapters the other way round
+    int64_t turned_a = -1, turned_b = -1;
     int cut[2] = {64, 64}, most_chunks[2] = {0, 0};
 
     int64_t take(int64_t bytes)
@@ -146,7 +149,7 @@ bool plan_forward(Plan &p, const Layer &l)
 {
     plan_types(p, l);
     p.few = l.T <= kFewRows;
-    p.shrink = shrink_of(l.T, l.D, l.count, p.few);
+    p.shrink = shrink_of(l.T, l.D, l.count);
     if (p.few || p.shrink.parts > 1) p.parts = p.take(p.shrink.parts * l.T * l.rank * 4);
     if (p.few) return true;
     p.hidden_planes = p.take(planes_bytes(l));
@@ -167,7 +170,6 @@ bool plan_backward(Plan &p, const Layer &l, const void *dY, int64_t lddy, Need n
     plan_types(p, l);
     if (need.a || need.b) {
         const int64_t C[2] = {l.D, l.N}, most_adapters = l.count < l.T ? l.count : l.T;
-        int64_t sums = 0;
         p.order = p.take(l.T * 4);
         p.starts = p.take((l.count + 1) * 4);
         p.counts = p.take(8);
@@ -176,25 +178,38 @@ bool plan_backward(Plan &p, const Layer &l, const void *dY, int64_t lddy, Need n
             const int64_t columns = ceil_div(C[n], kOuterColumns);
             int64_t tokens = round_up(ceil_div(l.T * columns, 512), 64);
             if (tokens < 64) tokens = 64;
+            if (tokens > kMostTokens) tokens = kMostTokens;
             p.cut[n] = (int)tokens;
             p.most_chunks[n] = (int)(l.T / tokens + most_adapters);
             p.chunks[n] = p.take(((int64_t)p.most_chunks[n] + 1) * (int64_t)sizeof(Chunk));
             p.joins[n] = p.take(l.count * 8);
+            if (!(n == 0 ? need.a : need.b)) continue;
             // an adapter of several chunks has more than `tokens` tokens, and at most twice as many chunks as whole ones
-            const int64_t bytes = 2 * (l.T / tokens) * C[n] * l.rank * 4;
-            if ((n == 0 ? need.a : need.b) && bytes > sums) sums = bytes;
+            p.sums[n] = p.take(2 * (l.T / tokens) * C[n] * l.rank * 4);
+            // a chunk's small values are whole 64s
+            const bool direct = n == 0 ? as_stored(l.dtype, l.X, l.ldx, l.D, 8) : as_stored(l.dtype, dY, lddy, l.N, 8);
+            if (direct) {
+                p.arranged_plane[n] = (l.T + 64 * (l.T / tokens + most_adapters)) / 64 * 64 * l.rank;
+                p.arranged[n] = p.take(2 * p.arranged_plane[n] * 2);
+            }
         }
-        p.sums = p.take(sums);
     }
     if (l.T == 0) return true;
+    // A copy of the adapters the other way round is read 16 bytes at a time; it costs less than it spares where they
+    // have fewer ranks together than there are tokens (B for the hidden values of 8192×16384 with 8 of 32 53 µs against
+    // 280 as they lie).
+    if ((need.x || need.a) && 4 * l.count * l.rank <= l.T) {
+        p.turned_b = p.take(l.count * l.rank * round_up(l.N, 8) * (int64_t)size_of(l.dtype));
+        if (need.x) p.turned_a = p.take(l.count * l.D * round_up(l.rank, 8) * (int64_t)size_of(l.dtype));
+    }
     if (need.x || need.a) {
-        p.shrink = shrink_of(l.T, l.N, l.count, false);
+        p.shrink = shrink_of(l.T, l.N, l.count);
         if (p.shrink.parts > 1) p.parts = p.take(p.shrink.parts * l.T * l.rank * 4);
         if (need.a) p.u = p.take(l.T * l.rank * 4);
         if (need.x) p.hidden_planes = p.take(planes_bytes(l));
     }
     if (need.b && !have_hidden) {
-        p.shrink_x = shrink_of(l.T, l.D, l.count, false);
+        p.shrink_x = shrink_of(l.T, l.D, l.count);
         if (p.shrink_x.parts > 1) p.parts_x = p.take(p.shrink_x.parts * l.T * l.rank * 4);
         p.hidden = p.take(l.T * l.rank * 4);
     }
@@ -261,6 +276,7 @@ ShrinkArgs shrink_args(const Layer &l, const Shrink &s, const void *rows, int64_
     a.part_k = s.part_k;
     a.parts = s.parts;
     a.slots = s.slots;
+    a.rows_each = s.rows_each;
     return a;
 }
 
@@ -363,10 +379,20 @@ tgemm_status_t backward(const Plan &p, const Layer &l, const void *dY, int64_t l
         e = launch_group(o, stream);
         if (e != hipSuccess) return from_hip(e);
     }
+    Stack a_stack = stack_a(l), b_stack = stack_b(l);
+    if (p.turned_b >= 0) {
+        const int64_t ld_a = round_up(l.rank, 8), ld_b = round_up(l.N, 8);
+        const TurnArgs b{l.dtype, b_stack, l.N, in<void>(ws, p.turned_b), ld_b, l.rank * ld_b};
+        const TurnArgs a{l.dtype, a_stack, l.D, in<void>(ws, p.turned_a), ld_a, l.D * ld_a};
+        e = launch_turn(b, a, stream);
+        if (e != hipSuccess) return from_hip(e);
+        b_stack = Stack{b.to, ld_b, b.to_stride, false, (int)l.count, (int)l.rank};
+        if (a.to != nullptr) a_stack = Stack{a.to, ld_a, a.to_stride, true, (int)l.count, (int)l.rank};
+    }
     float *u = in<float>(ws, p.u);
     void *planes = in<void>(ws, p.hidden_planes);
     if (l.T > 0 && (g.dX != nullptr || g.dA != nullptr))
-        e = make_hidden(shrink_args(l, p.shrink, dY, lddy, l.N, stack_b(l)), in<float>(ws, p.parts), u, planes, stream);
+        e = make_hidden(shrink_args(l, p.shrink, dY, lddy, l.N, b_stack), in<float>(ws, p.parts), u, planes, stream);
     if (e == hipSuccess && p.hidden >= 0) {
         hidden = in<float>(ws, p.hidden);
         e = make_hidden(shrink_args(l, p.shrink_x, l.X, l.ldx, l.D, stack_a(l)), in<float>(ws, p.parts_x),
@@ -374,28 +400,32 @@ tgemm_status_t backward(const Plan &p, const Layer &l, const void *dY, int64_t l
     }
     if (e != hipSuccess) return from_hip(e);
 
-    OuterArgs r{};
-    r.dtype = l.dtype;
-    r.scales = l.scales;
-    r.order = o.order;
-    r.part = in<float>(ws, p.sums);
-    r.count = (int)l.count;
-    r.rank = (int)l.rank;
-    for (int n = 0; n < 2; ++n) {
-        void *out = n == 0 ? g.dA : g.dB;
-        if (out == nullptr) continue;
-        r.C = (int)(n == 0 ? l.D : l.N);
-        r.rows = n == 0 ? l.X : dY;
-        r.ld = n == 0 ? l.ldx : lddy;
-        r.small = n == 0 ? u : hidden;
-        r.cut = o.cuts[n];
-        r.most_chunks = p.most_chunks[n];
-        r.out = out;
-        r.ldo = n == 0 ? g.ldda : g.lddb;
-        r.stride_out = n == 0 ? g.stride_da : g.stride_db;
-        r.rank_inner = n == 1;
-        if (l.T > 0) e = launch_outer(r, stream);
-        if (e == hipSuccess) e = launch_join(r, stream);
+    if (g.dA != nullptr || g.dB != nullptr) {
+        OuterArgs r[2] = {};
+        for (int n = 0; n < 2; ++n) {
+            r[n].dtype = l.dtype;
+            r[n].scales = l.scales;
+            r[n].order = o.order;
+            r[n].part = in<float>(ws, p.sums[n]);
+            r[n].count = (int)l.count;
+            r[n].rank = (int)l.rank;
+            r[n].C = (int)(n == 0 ? l.D : l.N);
+            r[n].rows = n == 0 ? l.X : dY;
+            r[n].ld = n == 0 ? l.ldx : lddy;
+            r[n].small = n == 0 ? u : hidden;
+            r[n].arranged = in<void>(ws, p.arranged[n]);
+            r[n].arranged_plane = p.arranged_plane[n];
+            r[n].cut = o.cuts[n];
+            r[n].most_chunks = p.most_chunks[n];
+            r[n].out = n == 0 ? g.dA : g.dB;
+            r[n].ldo = n == 0 ? g.ldda : g.lddb;
+            r[n].stride_out = n == 0 ? g.stride_da : g.stride_db;
+            r[n].rank_inner = n == 1;
+        }
+        if (l.T > 0 && (r[0].arranged != nullptr || r[1].arranged != nullptr)) e = launch_arrange(r[0], r[1], stream);
+        for (int n = 0; n < 2; ++n)
+            if (e == hipSuccess && l.T > 0 && r[n].out != nullptr) e = launch_outer(r[n], stream);
+        if (e == hipSuccess) e = launch_join(r[0], r[1], stream);
         if (e != hipSuccess) return from_hip(e);
     }
     if (l.T == 0) return g.dW ? from_hip(launch_zero(g.dW, g.lddw, l.dtype, l.N, l.D, stream)) : TGEMM_SUCCESS;
@@ -417,7 +447,7 @@ tgemm_status_t backward(const Plan &p, const Layer &l, const void *dY, int64_t l
         a.op.plane_b = w.plane;
         a.op.mn_b = (int)(p.w >= 0 ? p.Dp : l.D);
         a.op.k_b = (int)l.N;
-        a.e = Expand{l.ids, l.scales, nullptr, 0, 1, planes, stack_a(l)};
+        a.e = Expand{l.ids, l.scales, nullptr, 0, 1, planes, a_stack};
         e = run_product(p, l, a, true, steps, p.Dp, g.dX, g.lddx, ws, stream);
     }
     if (e == hipSuccess && g.dW != nullptr) {

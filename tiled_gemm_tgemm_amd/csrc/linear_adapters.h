@@ -43,8 +43,9 @@ struct ShrinkArgs {
     const float *scales;
     float *part;
     void *planes;
-    int64_t part_k;  // values of k a part, a multiple of 32
+    int64_t part_k;  // values of k a part, a multiple of 128
     int parts, slots;
+    int rows_each;   // 16: a work-group's wavefronts share 16 rows' sums; 64, 128: they take 16, 32 rows each
 };
 hipError_t launch_shrink(const ShrinkArgs &a, hipStream_t stream);
 // Adds the parts up to `hidden` and `planes` (either may be NULL), for every row whose id is in range.
@@ -63,7 +64,8 @@ struct Expand {
     Stack c;
 };
 
-// C = A·B + the adapters' part, A as stored along K, B along K (forward) or not (dX).
+// C = A·B + the adapters' part, A as stored along K, B along K (forward, with
+// the adapters' ranks the inner ones) or not (dX).
 struct ProductArgs {
     m16::Operands op;
     void *out;
@@ -97,11 +99,14 @@ hipError_t launch_few(const FewArgs &a, hipStream_t stream);
 // each gradient: chunks[n] = {adapter, first place in order, tokens, slot}, the
 // slot -1 where the adapter has one chunk; joins[i] = {first slot, chunks};
 // *chunk_count of them.
+// place: where the chunk's small values lie among the arranged ones, whole 64s.
 struct Chunk {
     int adapter, first, tokens, slot;
+    int64_t place;
 };
+constexpr int kMostTokens = 2048;  // of a chunk
 struct Cut {
-    int tokens;  // a multiple of 64
+    int tokens;  // a multiple of 64, at most kMostTokens
     Chunk *chunks;
     int2 *joins;
     int *chunk_count;
@@ -123,6 +128,11 @@ struct OuterArgs {
     const void *rows;
     int64_t ld;
     const float *small;       // T × rank
+    // small in the order of the chunks, or NULL: for each chunk rank rows of its
+    // tokens in whole 64s, zero past them, high and low bf16 planes apart;
+    // rows are then 16-bit, 16-byte aligned and of whole 8s
+    void *arranged;
+    int64_t arranged_plane;
     const float *scales;
     const int *order;
     Cut cut;
@@ -134,8 +144,22 @@ struct OuterArgs {
     int count, rank;
 };
 constexpr int kOuterColumns = 128, kOuterTokens = 64;
+// Both gradients' small values at once (either `out` may be NULL).
+hipError_t launch_arrange(const OuterArgs &a, const OuterArgs &b, hipStream_t stream);
 hipError_t launch_outer(const OuterArgs &a, hipStream_t stream);
-hipError_t launch_join(const OuterArgs &a, hipStream_t stream);
+hipError_t launch_join(const OuterArgs &a, const OuterArgs &b, hipStream_t stream);
+
+// Stacks the other way round: element (outer, rank) of adapter i, at i·to_stride
+// + rank·to_ld + outer if the stack's ranks are the inner ones, otherwise at
+// i·to_stride + outer·to_ld + rank.
+struct TurnArgs {
+    tgemm_dtype_t dtype;
+    Stack from;
+    int64_t outer;
+    void *to;                 // or NULL: nothing to do
+    int64_t to_ld, to_stride;
+};
+hipError_t launch_turn(const TurnArgs &a, const TurnArgs &b, hipStream_t stream);
 
 }  // namespace adapters
 }  // namespace tgemm

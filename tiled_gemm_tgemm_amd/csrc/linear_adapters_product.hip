@@ -5,6 +5,8 @@
 #include "mfma16_store.h"
 #include "some.h"
 
+#include <type_traits>
+
 namespace tgemm {
 namespace adapters {
 namespace {
@@ -118,18 +120,77 @@ __device__ __forceinline__ int id_of(const Expand &e, int64_t row, int64_t rows)
     return id >= 0 && id < e.c.count ? (int)id : id == -1 ? -1 : -2;
 }
 
+// A lane's row of hidden values.
+__device__ __forceinline__ float hidden_at(const __bf16 *planes, int64_t row, int k, int padded)
+{
+    const __bf16 *from = planes + row * 2 * padded + k;
+    return (float)from[0] + (float)from[padded];
+}
+__device__ __forceinline__ float hidden_at(const float *planes, int64_t row, int k, int padded) { return planes[row * padded + k]; }
+
+// The adapters' part of a lane's row and H adjacent columns on the vector units:
+// every lane reads its own adapter.
+template <class C, int H, bool RANK_INNER, class Acc>
+__device__ __forceinline__ void add_lanes(const Expand &e, int id, int64_t row, int col, int columns, Acc &acc)
+{
+    typedef typename std::conditional<sizeof(C) == 4, float, __bf16>::type P;
+    const int padded = (int)planes_rank(e.c.rank);
+    const C *c = (const C *)e.c.p + id * e.c.stride;
+    const int left = columns - col;
+    if constexpr (RANK_INNER) {
+        for (int k = 0; k < e.c.rank; k += 8) {
+            int first = col;  // addresses are worked out anew, not kept in registers over the loop
+            asm volatile("" : "+v"(first));
+            float h[8];
+#pragma unroll
+            for (int n = 0; n < 8; ++n) h[n] = hidden_at((const P *)e.planes, row, k + n, padded);
+#pragma unroll
+            for (int j = 0; j < H / 4; ++j) {
+                C v[4][8];
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    load_some<C, 8>(c + (int64_t)min(first + 4 * j + x, columns - 1) * e.c.ld + k, e.c.rank - k, v[x]);
+#pragma unroll
+                for (int n = 0; n < 8; ++n)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) acc[j][x] = fmaf(h[n], (float)v[x][n], acc[j][x]);
+            }
+        }
+    } else {
+        for (int k = 0; k < e.c.rank; ++k) {
+            const float h = hidden_at((const P *)e.planes, row, k, padded);
+            C v[H];
+            load_some<C, H>(c + k * e.c.ld + min(col, columns - 1), left, v);
+#pragma unroll
+            for (int x = 0; x < H; ++x) acc[x / 4][x % 4] = fmaf(h, (float)v[x], acc[x / 4][x % 4]);
+        }
+    }
+}
+
 // E: the tiles' type; C: the adapters'.  The wavefront's rows are taken adapter
-// by adapter, the others' hidden values zero: tokens of a sequence share
-// theirs.  Bound by the matrix cores, as the product alone is.
-template <class E, class C, int BM, int BN, int WM, int WN, bool B_MC>
-__global__ __launch_bounds__(64 * WM * WN) void adapted_kernel(ProductArgs a)
+// by adapter: tokens of a sequence share theirs.  Where 32 rows have more than
+// kMixed, each lane reads its own instead, which takes the vector units as long
+// as about three adapters take the loads' way there and back (in a 256×256
+// tile, whose registers do not hold that, they are taken one by one all the
+// same).  The bound on registers is that of kTiles' work-groups a compute unit.  Bound by the matrix cores, as the product alone is.
+constexpr int kMixed = 3;
+template <class E, class C, int BM, int BN, int WM, int WN, bool B_MC, bool RANK_INNER>
+__global__ __launch_bounds__(64 * WM * WN, BM == 32 ? 3 : 2) void adapted_kernel(ProductArgs a)
 {
     typedef TileProduct<E, BM, BN, WM, WN, false, B_MC, m16::Operands, true> Tile;
     constexpr int H = kHeld<Tile>;
     __shared__ __align__(1024) char lds[Tile::kLds];
-    struct Ahead {};
-    Tile::run(a.op, (lds_char *)lds, [](int, int) { return Ahead{}; },
-              [&](typename Tile::Acc &acc, int row0, int col0, int split, Ahead) {
+    struct Ahead {
+        int id[Tile::FM];
+    };
+    auto prologue = [&](int row0, int) {
+        const int l16 = m16::thread_anew() & 15;
+        Ahead ahead;
+#pragma unroll
+        for (int i = 0; i < Tile::FM; ++i) ahead.id[i] = id_of(a.e, row0 + i * 16 + l16, a.op.M);
+        return ahead;
+    };
+    Tile::run(a.op, (lds_char *)lds, prologue, [&](typename Tile::Acc &acc, int row0, int col0, int split, const Ahead &ahead) {
         const int lane = m16::thread_anew() & 63, l16 = lane & 15, quarter = lane >> 4;
         // 32 rows at a time, which leaves the other accumulators where they are;
         // the first part of a split sum adds it
@@ -138,12 +199,30 @@ __global__ __launch_bounds__(64 * WM * WN) void adapted_kernel(ProductArgs a)
         for (int i0 = 0; i0 < Tile::FM; i0 += 2) {
             int id[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) id[i] = split == 0 ? id_of(a.e, row0 + (i0 + i) * 16 + l16, a.op.M) : -1;
+            for (int i = 0; i < 2; ++i) id[i] = split == 0 ? ahead.id[i0 + i] : -1;
             uint64_t left = (__ballot(id[0] >= 0) & 0xFFFF) | __ballot(id[1] >= 0) << 16;
             left &= 0xFFFFFFFF;
-            while (left != 0) {
+            auto next = [&]() {
                 const int at = __builtin_ctzll(left), now = __builtin_amdgcn_readlane(at < 16 ? id[0] : id[1], at & 15);
                 left &= ~((__ballot(id[0] == now) & 0xFFFF) | __ballot(id[1] == now) << 16);
+                return now;
+            };
+            const uint64_t rows = left;
+            int adapters = 0;
+            while (left != 0) {
+                next();
+                ++adapters;
+            }
+            if (Tile::FM < 8 && adapters > kMixed) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (id[i] >= 0) add_lanes<C, H, RANK_INNER>(a.e, id[i], row0 + (i0 + i) * 16 + l16, col0 + H * quarter, a.op.N, acc[i0 + i]);
+                left = 0;
+            } else {
+                left = rows;
+            }
+            while (left != 0) {
+                const int now = next();
                 const C *c = (const C *)a.e.c.p + now * a.e.c.stride;
                 // summed apart and added to its own rows alone: what another
                 // adapter holds, infinities and NaN too, does not reach them
@@ -158,11 +237,11 @@ __global__ __launch_bounds__(64 * WM * WN) void adapted_kernel(ProductArgs a)
 #pragma unroll
                     for (int j = 0; j < Tile::FN; ++j) {
                         // (the registers hold no more than one block's loads)
-                        if (Tile::FM == 8 && sizeof(C) == 2) asm volatile("" ::: "memory");
+                        if (Tile::FM == 8 && sizeof(C) == 2 && !RANK_INNER) asm volatile("" ::: "memory");
                         // the column at index l16 of block j (mfma16.h)
                         const int col = min(col0 + 4 * Tile::FN * (l16 >> 2) + 4 * j + (l16 & 3), a.op.N - 1);
                         C v[8];
-                        if constexpr (B_MC) {
+                        if constexpr (!RANK_INNER) {
                             const C *from = c + k0 * a.e.c.ld;
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
@@ -211,48 +290,59 @@ __global__ __launch_bounds__(64 * WM * WN) void adapted_kernel(ProductArgs a)
 // ---- a few rows ------------------------------------------------------------
 
 // Fragments straight from device memory, no LDS stage and no barrier, as the
-// loss operators take a few rows: a wavefront takes 16 columns of the result
-// and R blocks of 16 rows, four wavefronts a quarter of the sum each.  Then each
+// loss operators take a few rows: a wavefront takes COLS blocks of 16 columns of
+// the result, R blocks of 16 rows and an eighth of the sum.  Then each
 // lane adds its own rows' adapters on the vector units: there may be as many as
 // rows, and their matrices' loads do not wait for one another.
-template <class In, int R>
-__global__ __launch_bounds__(256) void adapted_few_kernel(FewArgs a)
+constexpr int kFewParts = 8;
+template <class In, int R, int COLS>
+__global__ __launch_bounds__(64 * kFewParts) void adapted_few_kernel(FewArgs a)
 {
-    constexpr int S = 4, U = sizeof(In) == 4 ? 2 : R == 4 ? 2 : 4;
-    __shared__ f32x4 sums[S][R][64];
+    constexpr int S = kFewParts, kHeld = (R + COLS) * (sizeof(In) == 4 ? 2 : 1), U = kHeld <= 3 ? 4 : kHeld <= 6 ? 2 : 1;
+    __shared__ f32x4 sums[S][R][COLS][64];
     const int lane = threadIdx.x & 63, part = threadIdx.x >> 6, l16 = lane & 15, quarter = lane >> 4;
-    const int col0 = blockIdx.x * 16;
-    const In *w = (const In *)a.W + (int64_t)min(col0 + l16, a.N - 1) * a.ldw + 8 * quarter;
-    const In *x[R];
+    const int col0 = blockIdx.x * (16 * COLS);
+    const In *w[COLS], *x[R];
+#pragma unroll
+    for (int j = 0; j < COLS; ++j) w[j] = (const In *)a.W + (int64_t)min(col0 + 16 * j + l16, a.N - 1) * a.ldw + 8 * quarter;
 #pragma unroll
     for (int i = 0; i < R; ++i) x[i] = (const In *)a.X + (int64_t)min(16 * i + l16, a.T - 1) * a.ldx + 8 * quarter;
-    f32x4 acc[R];
+    f32x4 acc[R][COLS];
 #pragma unroll
-    for (int i = 0; i < R; ++i) acc[i] = f32x4{0, 0, 0, 0};
-    auto multiply = [&](const In (&vw)[8], const In (&vx)[R][8]) {
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < COLS; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    auto multiply = [&](const In (&vw)[COLS][8], const In (&vx)[R][8]) {
         if constexpr (sizeof(In) == 2) {
-            typename Frag<In>::type fw;
+            typename Frag<In>::type fw[COLS], fx[R];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) fw[e] = vw[e];
+            for (int j = 0; j < COLS; ++j)
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                typename Frag<In>::type fx;
+                for (int e = 0; e < 8; ++e) fw[j][e] = vw[j][e];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) fx[e] = vx[i][e];
-                acc[i] = Frag<In>::mfma(fw, fx, acc[i]);
-            }
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) fx[i][e] = vx[i][e];
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int j = 0; j < COLS; ++j) acc[i][j] = Frag<In>::mfma(fw[j], fx[i], acc[i][j]);
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
 #pragma unroll
-                for (int i = 0; i < R; ++i) acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(vw[e], vx[i][e], acc[i], 0, 0, 0);
+                for (int i = 0; i < R; ++i)
+#pragma unroll
+                    for (int j = 0; j < COLS; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(vw[j][e], vx[i][e], acc[i][j], 0, 0, 0);
         }
     };
-    In vw[2][U][8], vx[2][U][R][8];
+    In vw[2][U][COLS][8], vx[2][U][R][8];
     auto load = [&](int set, int k) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            load_some<In, 8>(w + k + 32 * u, 8, vw[set][u]);
+#pragma unroll
+            for (int j = 0; j < COLS; ++j) load_some<In, 8>(w[j] + k + 32 * u, 8, vw[set][u][j]);
 #pragma unroll
             for (int i = 0; i < R; ++i) load_some<In, 8>(x[i] + k + 32 * u, 8, vx[set][u][i]);
         }
@@ -282,22 +372,26 @@ __global__ __launch_bounds__(256) void adapted_few_kernel(FewArgs a)
     if (part == S - 1) {
         for (int k = all * 32 * U; k < a.D; k += 32) {
             const int left = a.D - (k + 8 * quarter);
-            In zw[8], zx[R][8];
-            load_some<In, 8>(w + k, left, zw);
+            In zw[COLS][8], zx[R][8];
+#pragma unroll
+            for (int j = 0; j < COLS; ++j) load_some<In, 8>(w[j] + k, left, zw[j]);
 #pragma unroll
             for (int i = 0; i < R; ++i) load_some<In, 8>(x[i] + k, left, zx[i]);
             multiply(zw, zx);
         }
     }
 #pragma unroll
-    for (int i = 0; i < R; ++i) sums[part][i][lane] = acc[i];
-    __syncthreads();
-    // wavefront `part` finishes the blocks of rows part, part + 4, ...: row l16, columns col0 + 4·quarter + r
+    for (int i = 0; i < R; ++i)
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-        if (i % S != part) continue;
-        f32x4 v = sums[0][i][lane] + sums[1][i][lane] + sums[2][i][lane] + sums[3][i][lane];
-        const int row = 16 * i + l16, col = col0 + 4 * quarter;
+        for (int j = 0; j < COLS; ++j) sums[part][i][j][lane] = acc[i][j];
+    __syncthreads();
+    // wavefront n finishes the n-th blocks: row l16, columns 4·quarter + r
+    for (int n = part; n < R * COLS; n += S) {
+        const int i = n / COLS, j = n % COLS;
+        f32x4 v = sums[0][i][j][lane];
+#pragma unroll
+        for (int s = 1; s < S; ++s) v += sums[s][i][j][lane];
+        const int row = 16 * i + l16, col = col0 + 16 * j + 4 * quarter;
         if (row >= a.T) continue;
         const int id = id_of(a.e, row, a.T);
         if (id >= 0) {
@@ -329,26 +423,36 @@ __global__ __launch_bounds__(256) void adapted_few_kernel(FewArgs a)
     }
 }
 
+template <class In, int COLS>
+void few(const FewArgs &a, hipStream_t stream)
+{
+    const unsigned grid = (unsigned)((a.N + 16 * COLS - 1) / (16 * COLS));
+    if (a.T <= 16) adapted_few_kernel<In, 1, COLS><<<grid, 64 * kFewParts, 0, stream>>>(a);
+    else if (a.T <= 32) adapted_few_kernel<In, 2, COLS><<<grid, 64 * kFewParts, 0, stream>>>(a);
+    else if (a.T <= 48) adapted_few_kernel<In, 3, COLS><<<grid, 64 * kFewParts, 0, stream>>>(a);
+    else adapted_few_kernel<In, 4, COLS><<<grid, 64 * kFewParts, 0, stream>>>(a);
+}
+// Two blocks of columns halve the rows' way from the caches, where they leave
+// no compute unit without any.
 template <class In>
 void few(const FewArgs &a, hipStream_t stream)
 {
-    const unsigned grid = (unsigned)((a.N + 15) / 16);
-    if (a.T <= 16) adapted_few_kernel<In, 1><<<grid, 256, 0, stream>>>(a);
-    else if (a.T <= 32) adapted_few_kernel<In, 2><<<grid, 256, 0, stream>>>(a);
-    else adapted_few_kernel<In, 4><<<grid, 256, 0, stream>>>(a);
+    if (a.N >= 8192 && a.T > 16) few<In, 2>(a, stream);
+    else few<In, 1>(a, stream);
 }
 
-template <bool B_MC>
+template <bool B_MC, bool RANK_INNER>
 hipError_t product(bool half, int tile, const ProductArgs &a, hipStream_t stream)
 {
     const int64_t ids = a.op.ids(), most = (int64_t)256 * loss::kTiles[tile].wg_per_cu;
     const unsigned grid = (unsigned)(ids < most ? ids : most);
     switch (tile) {
-#define X(I, BM, BN, WM, WN)                                                                                             \
-    case I:                                                                                                              \
-        if (a.stored == TGEMM_F32) adapted_kernel<__bf16, float, BM, BN, WM, WN, B_MC><<<grid, 64 * WM * WN, 0, stream>>>(a); \
-        else if (half) adapted_kernel<_Float16, _Float16, BM, BN, WM, WN, B_MC><<<grid, 64 * WM * WN, 0, stream>>>(a);   \
-        else adapted_kernel<__bf16, __bf16, BM, BN, WM, WN, B_MC><<<grid, 64 * WM * WN, 0, stream>>>(a);                 \
+#define X(I, BM, BN, WM, WN)                                                                                                     \
+    case I:                                                                                                                      \
+        if (a.stored == TGEMM_F32)                                                                                               \
+            adapted_kernel<__bf16, float, BM, BN, WM, WN, B_MC, RANK_INNER><<<grid, 64 * WM * WN, 0, stream>>>(a);               \
+        else if (half) adapted_kernel<_Float16, _Float16, BM, BN, WM, WN, B_MC, RANK_INNER><<<grid, 64 * WM * WN, 0, stream>>>(a); \
+        else adapted_kernel<__bf16, __bf16, BM, BN, WM, WN, B_MC, RANK_INNER><<<grid, 64 * WM * WN, 0, stream>>>(a);             \
         break;
         TGEMM_TILES(X)
 #undef X
@@ -360,7 +464,8 @@ hipError_t product(bool half, int tile, const ProductArgs &a, hipStream_t stream
 
 hipError_t launch_product(bool half, bool b_mc, int tile, const ProductArgs &a, hipStream_t stream)
 {
-    return b_mc ? product<true>(half, tile, a, stream) : product<false>(half, tile, a, stream);
+    if (!b_mc) return product<false, true>(half, tile, a, stream);
+    return a.e.c.rank_inner ? product<true, true>(half, tile, a, stream) : product<true, false>(half, tile, a, stream);
 }
 
 hipError_t launch_few(const FewArgs &a, hipStream_t stream)

@@ -74,87 +74,121 @@ __device__ __forceinline__ void put_planes(void *planes, int64_t row, int at, in
     }
 }
 
-// A work-group takes 16 rows and a part of the sum, its four wavefronts the
-// part's steps of 32 in turn; for each adapter that the rows have (the
-// `slots` work-groups of a block of rows share them) 16·BLOCKS ranks at a
-// time.  Rows are read where they lie and once for every adapter among the 16:
-// tokens of a sequence share theirs.
-template <class In, int BLOCKS, bool RANK_INNER>
+// A wavefront takes 16·ROWS rows and, for each adapter that they have, 16·BLOCKS
+// ranks at a time: tokens of a sequence share theirs.  Rows are read where they
+// lie, once for every adapter among them, and the adapters' matrices from the
+// caches.  SHARED, for a few rows: the four wavefronts of a work-group take the
+// same 16 rows and every fourth step of the sum each.  Either way `slots`
+// work-groups share the adapters among the rows.
+template <class In, int BLOCKS, int ROWS, bool RANK_INNER, bool SHARED>
 __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a)
 {
-    __shared__ f32x4 sums[3][BLOCKS][64];
+    __shared__ f32x4 sums[SHARED ? 3 : 1][SHARED ? BLOCKS : 1][SHARED ? 64 : 1];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, quarter = lane >> 4;
-    const int64_t row = (int64_t)blockIdx.x * 16 + l16;
-    int id = -1;
-    if (row < a.T) {
-        const int64_t i = a.ids[row];
-        if (i >= 0 && i < a.c.count) id = (int)i;
+    const int64_t row0 = ((int64_t)blockIdx.x * (SHARED ? 1 : 4) + (SHARED ? 0 : wave)) * (16 * ROWS);
+    int id[ROWS];
+    const In *x[ROWS];
+    uint32_t left[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int64_t row = row0 + 16 * i + l16;
+        id[i] = -1;
+        if (row < a.T) {
+            const int64_t n = a.ids[row];
+            if (n >= 0 && n < a.c.count) id[i] = (int)n;
+        }
+        x[i] = (const In *)a.rows + (row < a.T ? row : a.T - 1) * a.ld + 8 * quarter;
+        left[i] = (uint32_t)__ballot(id[i] >= 0) & 0xFFFF;
     }
-    const In *x = (const In *)a.rows + (row < a.T ? row : a.T - 1) * a.ld;
-    const int64_t first = blockIdx.z * a.part_k, last = min(first + a.part_k, a.K);
-    uint32_t left = (uint32_t)__ballot(id >= 0) & 0xFFFF;
-    for (int n = 0; left != 0; ++n) {
-        const int now = __builtin_amdgcn_readlane(id, __builtin_ctz(left));
-        left &= ~(uint32_t)__ballot(id == now);
+    constexpr int kStep = SHARED ? 128 : 32;
+    const int64_t from = blockIdx.z * a.part_k, last = min(from + a.part_k, a.K), first = from + (SHARED ? 32 * wave : 0);
+    for (int n = 0;; ++n) {
+        int now = -1;
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+            if (now < 0 && left[i] != 0) now = __builtin_amdgcn_readlane(id[i], __builtin_ctz(left[i]));
+        if (now < 0) break;
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) left[i] &= ~(uint32_t)__ballot(id[i] == now);
         if (n % a.slots != (int)blockIdx.y) continue;
         const In *c = (const In *)a.c.p + now * a.c.stride;
         // (with one block of 16 the padding to 32 is a second turn's)
         for (int rank0 = 0; rank0 < (a.planes != nullptr ? (int)planes_rank(a.c.rank) : a.c.rank); rank0 += 16 * BLOCKS) {
-            f32x4 acc[BLOCKS];
+            f32x4 acc[ROWS][BLOCKS];
 #pragma unroll
-            for (int b = 0; b < BLOCKS; ++b) acc[b] = f32x4{0, 0, 0, 0};
-            auto load = [&](int64_t k, In (&vx)[8], In (&vc)[BLOCKS][8]) {
-                const int64_t at = k + 8 * quarter;
-                load_some<In, 8>(x + at, last - at, vx);
+            for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+                for (int b = 0; b < BLOCKS; ++b) acc[i][b] = f32x4{0, 0, 0, 0};
+            const In *cr[BLOCKS];  // past the last rank the last stands in, and is not stored
+#pragma unroll
+            for (int b = 0; b < BLOCKS; ++b) {
+                const int rank = min(rank0 + 16 * b + l16, a.c.rank - 1);
+                cr[b] = c + (RANK_INNER ? 8 * quarter * a.c.ld + rank : rank * a.c.ld + 8 * quarter);
+            }
+            auto step = [&](int64_t k, In (&vx)[ROWS][8], In (&vc)[BLOCKS][8], int64_t there) {
+#pragma unroll
+                for (int i = 0; i < ROWS; ++i) load_some<In, 8>(x[i] + k, there, vx[i]);
 #pragma unroll
                 for (int b = 0; b < BLOCKS; ++b) {
-                    const int rank = min(rank0 + 16 * b + l16, a.c.rank - 1);  // past the last: not stored
                     if constexpr (RANK_INNER) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) vc[b][e] = at + e < last ? c[(at + e) * a.c.ld + rank] : (In)0.0f;
+                        for (int e = 0; e < 8; ++e) vc[b][e] = e < there ? cr[b][(k + e) * a.c.ld] : (In)0.0f;
                     } else {
-                        load_some<In, 8>(c + rank * a.c.ld + at, last - at, vc[b]);
+                        load_some<In, 8>(cr[b] + k, there, vc[b]);
                     }
                 }
             };
-            constexpr int U = sizeof(In) == 4 || BLOCKS == 4 ? 2 : 4;
-            int64_t k = first + 32 * wave;
-            for (; k + 128 * (U - 1) + 32 <= last; k += 128 * U) {
-                In vx[U][8], vc[U][BLOCKS][8];
+            auto multiply = [&](const In (&vx)[ROWS][8], const In (&vc)[BLOCKS][8]) {
 #pragma unroll
-                for (int u = 0; u < U; ++u) load(k + 128 * u, vx[u], vc[u]);
+                for (int i = 0; i < ROWS; ++i)
 #pragma unroll
-                for (int u = 0; u < U; ++u)
+                    for (int b = 0; b < BLOCKS; ++b) acc[i][b] = Step<In>::add(vc[b], vx[i], acc[i][b]);
+            };
+            constexpr int kHeld = (ROWS + (RANK_INNER ? 4 : 1) * BLOCKS) * (sizeof(In) == 4 ? 2 : 1);
+            constexpr int U = kHeld <= 4 ? 4 : kHeld <= 8 ? 2 : 1;
+            int64_t k = first;
+            for (; k + kStep * (U - 1) + 32 <= last; k += kStep * U) {
+                In vx[U][ROWS][8], vc[U][BLOCKS][8];
 #pragma unroll
-                    for (int b = 0; b < BLOCKS; ++b) acc[b] = Step<In>::add(vc[u][b], vx[u], acc[b]);
+                for (int u = 0; u < U; ++u) step(k + kStep * u, vx[u], vc[u], 8);
+#pragma unroll
+                for (int u = 0; u < U; ++u) multiply(vx[u], vc[u]);
             }
-            for (; k < last; k += 128) {
-                In vx[8], vc[BLOCKS][8];
-                load(k, vx, vc);
-#pragma unroll
-                for (int b = 0; b < BLOCKS; ++b) acc[b] = Step<In>::add(vc[b], vx, acc[b]);
+            for (; k < last; k += kStep) {
+                In vx[ROWS][8], vc[BLOCKS][8];
+                step(k, vx, vc, last - (k + 8 * quarter));
+                multiply(vx, vc);
             }
-            if (wave > 0) {
+            if constexpr (SHARED) {
+                if (wave > 0) {
 #pragma unroll
-                for (int b = 0; b < BLOCKS; ++b) sums[wave - 1][b][lane] = acc[b];
+                    for (int b = 0; b < BLOCKS; ++b) sums[wave - 1][b][lane] = acc[0][b];
+                }
+                __syncthreads();
+                if (wave == 0) {
+#pragma unroll
+                    for (int b = 0; b < BLOCKS; ++b) acc[0][b] += sums[0][b][lane] + sums[1][b][lane] + sums[2][b][lane];
+                }
+                __syncthreads();
+                if (wave > 0) continue;
             }
-            __syncthreads();
-            if (wave == 0 && id == now) {
-                const float factor = a.scales != nullptr ? a.scales[now] : 1.0f;
+            const float factor = a.scales != nullptr ? a.scales[now] : 1.0f;
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) {
+                if (id[i] != now) continue;
+                const int64_t row = row0 + 16 * i + l16;
 #pragma unroll
                 for (int b = 0; b < BLOCKS; ++b) {
-                    const f32x4 v = acc[b] + sums[0][b][lane] + sums[1][b][lane] + sums[2][b][lane];
                     const int rank = rank0 + 16 * b + 4 * quarter;
                     if (a.part != nullptr) {
                         float *to = a.part + ((int64_t)blockIdx.z * a.T + row) * a.c.rank + rank;
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
-                            if (rank + r < a.c.rank) to[r] = v[r];
+                            if (rank + r < a.c.rank) to[r] = acc[i][b][r];
                     }
-                    if (a.planes != nullptr) put_planes<sizeof(In) == 4>(a.planes, row, rank, a.c.rank, v, factor);
+                    if (a.planes != nullptr) put_planes<sizeof(In) == 4>(a.planes, row, rank, a.c.rank, acc[i][b], factor);
                 }
             }
-            __syncthreads();
         }
     }
 }
@@ -186,9 +220,17 @@ __global__ __launch_bounds__(256) void finish_kernel(ShrinkArgs a, float *hidden
 template <class In, int BLOCKS>
 void shrink(const ShrinkArgs &a, hipStream_t stream)
 {
-    const dim3 grid((unsigned)((a.T + 15) / 16), a.slots, a.parts);
-    if (a.c.rank_inner) shrink_kernel<In, BLOCKS, true><<<grid, 256, 0, stream>>>(a);
-    else shrink_kernel<In, BLOCKS, false><<<grid, 256, 0, stream>>>(a);
+    const dim3 grid((unsigned)((a.T + a.rows_each - 1) / a.rows_each), a.slots, a.parts);
+    if (a.rows_each == 16) {
+        if (a.c.rank_inner) shrink_kernel<In, BLOCKS, 1, true, true><<<grid, 256, 0, stream>>>(a);
+        else shrink_kernel<In, BLOCKS, 1, false, true><<<grid, 256, 0, stream>>>(a);
+    } else if (a.rows_each == 64) {
+        if (a.c.rank_inner) shrink_kernel<In, BLOCKS, 1, true, false><<<grid, 256, 0, stream>>>(a);
+        else shrink_kernel<In, BLOCKS, 1, false, false><<<grid, 256, 0, stream>>>(a);
+    } else {
+        if (a.c.rank_inner) shrink_kernel<In, BLOCKS, 2, true, false><<<grid, 256, 0, stream>>>(a);
+        else shrink_kernel<In, BLOCKS, 2, false, false><<<grid, 256, 0, stream>>>(a);
+    }
 }
 template <class In>
 void shrink(const ShrinkArgs &a, hipStream_t stream)
@@ -263,21 +305,26 @@ __global__ __launch_bounds__(1024) void chunks_kernel(GroupArgs a)
     __shared__ int room[16];
     const Cut cut = a.cuts[blockIdx.x];
     int chunk0 = 0, slot0 = 0;
+    int64_t place0 = 0;
     for (int i0 = 0; i0 < a.count; i0 += 1024) {
         const int i = i0 + threadIdx.x;
         const int from = i < a.count ? a.starts[i] : 0, tokens = i < a.count ? a.starts[i + 1] - from : 0;
         const int chunks = (tokens + cut.tokens - 1) / cut.tokens, slots = chunks > 1 ? chunks : 0;
         int all_chunks, all_slots;
         const int chunk = chunk0 + before(chunks, room, all_chunks), slot = slot0 + before(slots, room, all_slots);
+        // in whole 64s; 1024 adapters have 2^24 tokens at most, and 64 more each
+        int all_places;
+        const int64_t place = place0 + 64 * (int64_t)before((tokens + 63) / 64, room, all_places);
         if (i < a.count) {
             cut.joins[i] = make_int2(slot, chunks);
             // an adapter's tokens are dealt evenly, in whole 64s
             const int each = chunks ? ((tokens + chunks - 1) / chunks + 63) / 64 * 64 : 0;
             for (int n = 0; n < chunks; ++n)
-                cut.chunks[chunk + n] = Chunk{i, from + n * each, min(each, tokens - n * each), slots ? slot + n : -1};
+                cut.chunks[chunk + n] = Chunk{i, from + n * each, min(each, tokens - n * each), slots ? slot + n : -1, place + (int64_t)n * each};
         }
         chunk0 += all_chunks;
         slot0 += all_slots;
+        place0 += 64 * (int64_t)all_places;
     }
     if (threadIdx.x == 0) *cut.chunk_count = chunk0;
 }
@@ -345,6 +392,7 @@ struct Outer<__bf16> : OuterPlanes {
         for (int e = 0; e < 8; ++e) f[e] = v[e];
         return f;
     }
+    static __device__ __forceinline__ Zf z_of(const bf16x8 &v) { return v; }
     template <bool Z_FIRST>
     static __device__ __forceinline__ f32x4 add(const Zf &z, const Vf &v, f32x4 acc)
     {
@@ -361,6 +409,13 @@ struct Outer<_Float16> : OuterPlanes {
         for (int e = 0; e < 8; ++e) f[e] = (float)v[e];
         return v_of(f);
     }
+    static __device__ __forceinline__ Zf z_of(const m16::f16x8 &v)
+    {
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = (float)v[e];
+        return v_of(f);
+    }
     template <bool Z_FIRST>
     static __device__ __forceinline__ f32x4 add(const Zf &z, const Vf &v, f32x4 acc)
     {
@@ -368,12 +423,156 @@ struct Outer<_Float16> : OuterPlanes {
     }
 };
 
+// RANK_INNER: a lane holds column l16, ranks 4·quarter + r; otherwise rank l16,
+// columns 4·quarter + r.
+template <class In, int BLOCKS, bool RANK_INNER>
+__device__ __forceinline__ void put_outer(const OuterArgs &a, const Chunk &chunk, int col0, int rank0, const f32x4 (&acc)[2][BLOCKS])
+{
+    const int lane = threadIdx.x & 63, l16 = lane & 15, quarter = lane >> 4;
+    const bool joined = chunk.slot >= 0;
+    const float scale = a.scales != nullptr ? a.scales[chunk.adapter] : 1.0f;
+    const int64_t ld = joined ? (RANK_INNER ? a.rank : a.C) : a.ldo;
+    const int64_t base = joined ? (int64_t)chunk.slot * a.C * a.rank : chunk.adapter * a.stride_out;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int b = 0; b < BLOCKS; ++b)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int col = col0 + 16 * j + (RANK_INNER ? l16 : 4 * quarter + r);
+                const int rank = rank0 + 16 * b + (RANK_INNER ? 4 * quarter + r : l16);
+                if (col >= a.C || rank >= a.rank) continue;
+                const int64_t at = base + (RANK_INNER ? col * ld + rank : rank * ld + col);
+                if (joined) a.part[at] = acc[j][b][r];
+                else ((In *)a.out)[at] = (In)(acc[j][b][r] * scale);
+            }
+}
+
+// Small values of the chunks' tokens, rank by rank, in two bf16 planes: as the
+// matrix cores read a first operand along its sum.
+constexpr int kArranged = 64;  // tokens a work-group
+__global__ __launch_bounds__(256) void arrange_kernel(OuterArgs first, OuterArgs second)
+{
+    const OuterArgs &a = blockIdx.z == 0 ? first : second;
+    if (a.out == nullptr || a.arranged == nullptr || (int)blockIdx.x >= *a.cut.chunk_count) return;
+    const Chunk chunk = a.cut.chunks[blockIdx.x];
+    const int whole = (chunk.tokens + 63) / 64 * 64, t0 = blockIdx.y * kArranged;
+    __bf16 *to = (__bf16 *)a.arranged + chunk.place * a.rank;
+    // a thread takes two tokens of a rank, a wavefront 16 adjacent ranks of eight tokens' rows
+    const int pairs = min(whole - t0, kArranged) / 2, blocks = (a.rank + 15) / 16;
+    for (int n = threadIdx.x; n < pairs * 16 * blocks; n += 256) {
+        const int block = n / (pairs * 16), in = n - block * (pairs * 16), rank = 16 * block + in % 16, t = t0 + in / 16 * 2;
+        if (rank >= a.rank) continue;
+        uint32_t high = 0, low = 0;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if (t + e >= chunk.tokens) continue;
+            __bf16 h, l;
+            halves(a.small[(int64_t)a.order[chunk.first + t + e] * a.rank + rank], h, l);
+            high |= (uint32_t)__builtin_bit_cast(uint16_t, h) << (16 * e);
+            low |= (uint32_t)__builtin_bit_cast(uint16_t, l) << (16 * e);
+        }
+        *(uint32_t *)(to + (int64_t)rank * whole + t) = high;
+        *(uint32_t *)(to + a.arranged_plane + (int64_t)rank * whole + t) = low;
+    }
+}
+
+// 16 bytes a lane from an address of its own to 16 adjacent bytes a lane from
+// `to` (as load_lds, which reaches 4 GiB from one base).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void gather_lds(const void *from, m16::lds_char *to)
+{
+    const uint32_t at = (uint32_t)(uintptr_t)to;
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(at)), "v"((uint64_t)(uintptr_t)from)
+                 : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
 // A work-group takes 128 columns of the rows, 16·BLOCKS ranks and a chunk of an
-// adapter's tokens, 64 at a time through LDS; the loads of the next 64 are
-// under way while these are multiplied.  A wavefront takes 32 columns.  Bound by
-// reading the rows once.
+// adapter's tokens, 64 at a time: the rows' and the arranged values' slices go
+// straight into one of two LDS stages, and the loads of the next 64 are under
+// way while these are multiplied.  The rows' fragments come from the transposing
+// LDS read.  A wavefront takes 32 columns.  Bound by reading the rows once.
 template <class In, int BLOCKS, bool RANK_INNER>
 __global__ __launch_bounds__(256) void outer_kernel(OuterArgs a)
+{
+    constexpr int kCols = kOuterColumns, kTokens = kOuterTokens, kRanks = 16 * BLOCKS;
+    typedef m16::Slice<kCols, 2, 256, true, false> SliceZ;
+    typedef m16::Slice<kRanks, BLOCKS, 128 * BLOCKS, false, false> SliceV;  // one round a plane
+    constexpr int kBytesV = SliceV::kBytes, kStage = SliceZ::kBytes + 2 * kBytesV;
+    static_assert(SliceZ::kRounds == 4 && SliceV::kRounds == 1, "rounds");
+    __shared__ __align__(1024) char lds[2 * kStage];
+    __shared__ int order[kMostTokens];
+    if ((int)blockIdx.y >= *a.cut.chunk_count) return;
+    const Chunk chunk = a.cut.chunks[blockIdx.y];
+    const int thread = threadIdx.x, lane = thread & 63, wave = __builtin_amdgcn_readfirstlane(thread >> 6);
+    const int col0 = blockIdx.x * kCols, rank0 = blockIdx.z * kRanks;
+    const int whole = (chunk.tokens + 63) / 64 * 64;
+    // tokens past the last meet zeros: the last stands in
+    for (int t = thread; t < whole; t += 256) order[t] = a.order[chunk.first + min(t, chunk.tokens - 1)];
+    const In *rows = (const In *)a.rows + col0;
+    const int last_col = a.C - 8 - col0;
+    const __bf16 *small = (const __bf16 *)a.arranged + chunk.place * a.rank + (int64_t)min(rank0, a.rank - 1) * whole;
+    const int last_rank = a.rank - 1 - min(rank0, a.rank - 1);
+    // the pieces of both planes of V: 2·128·BLOCKS, 256 at a time
+    auto issue = [&](int stage, int t0) {
+        m16::lds_char *to = (m16::lds_char *)lds + stage * kStage;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int position = r * 256 + thread, row = position / SliceZ::kRowPieces, slot = position % SliceZ::kRowPieces;
+            const int col = min((slot ^ m16::flip<kCols, 2, false>(row)) * 8, last_col);
+            gather_lds(rows + order[t0 + row] * a.ld + col, to + (r * 256 + wave * 64) * 16);
+        }
+#pragma unroll
+        for (int r = 0; r < BLOCKS; ++r) {
+            const int position = r * 256 + thread, plane = position / (128 * BLOCKS), in = position % (128 * BLOCKS);
+            gather_lds((const char *)(small + plane * a.arranged_plane + t0) + SliceV::offset(in, whole, last_rank, kTokens),
+                       to + SliceZ::kBytes + (r * 256 + wave * 64) * 16);
+        }
+    };
+    m16::Reader<kCols, 2, true, false> rz;
+    m16::Reader<kRanks, BLOCKS, false, false> rv;
+    rz.place(wave * 32, lane);
+    rv.place(0, lane);
+    f32x4 acc[2][BLOCKS];
+#pragma unroll
+    for (int b = 0; b < BLOCKS; ++b) acc[0][b] = acc[1][b] = f32x4{0, 0, 0, 0};
+    __syncthreads();  // the order
+    issue(0, 0);
+    if (kTokens < whole) issue(1, kTokens);
+    int stage = 0;
+    for (int t0 = 0; t0 < whole; t0 += kTokens) {
+        if (t0 + kTokens < whole) m16::arrive<4 + BLOCKS>();
+        else m16::arrive<0>();
+        m16::lds_char *z = (m16::lds_char *)lds + stage * kStage, *v = z + SliceZ::kBytes;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            typename Outer<In>::Zf zf[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) zf[j] = Outer<In>::z_of(rz.template read<In>(z, j, s));
+#pragma unroll
+            for (int b = 0; b < BLOCKS; ++b) {
+                OuterPlanes::Vf vf;
+                vf.high = rv.template read<__bf16>(v, b, s);
+                vf.low = rv.template read<__bf16>(v + kBytesV, b, s);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[j][b] = Outer<In>::template add<!RANK_INNER>(zf[j], vf, acc[j][b]);
+            }
+        }
+        __syncthreads();
+        if (t0 + 2 * kTokens < whole) issue(stage, t0 + 2 * kTokens);
+        stage ^= 1;
+    }
+    put_outer<In, BLOCKS, RANK_INNER>(a, chunk, col0 + 32 * wave, rank0, acc);
+}
+
+// The same for float32 rows and rows that start anywhere: through registers into
+// LDS, and out of it value by value.
+template <class In, int BLOCKS, bool RANK_INNER>
+__global__ __launch_bounds__(256) void outer_any_kernel(OuterArgs a)
 {
     constexpr int kCols = kOuterColumns, kTokens = kOuterTokens, kRanks = 16 * BLOCKS;
     constexpr int kPiece = 16 / sizeof(In), kPieces = kCols / kPiece * kTokens / 256;
@@ -446,39 +645,56 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs a)
         __syncthreads();
     }
 
-    // RANK_INNER: a lane holds column l16, ranks 4·quarter + r; otherwise rank l16, columns 4·quarter + r
-    const bool joined = chunk.slot >= 0;
-    const float scale = a.scales != nullptr ? a.scales[chunk.adapter] : 1.0f;
-    const int64_t ld = joined ? (RANK_INNER ? a.rank : a.C) : a.ldo;
-    const int64_t base = joined ? (int64_t)chunk.slot * a.C * a.rank : chunk.adapter * a.stride_out;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int b = 0; b < BLOCKS; ++b)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int col = col0 + 32 * wave + 16 * j + (RANK_INNER ? l16 : 4 * quarter + r);
-                const int rank = rank0 + 16 * b + (RANK_INNER ? 4 * quarter + r : l16);
-                if (col >= a.C || rank >= a.rank) continue;
-                const int64_t at = base + (RANK_INNER ? col * ld + rank : rank * ld + col);
-                if (joined) a.part[at] = acc[j][b][r];
-                else ((In *)a.out)[at] = (In)(acc[j][b][r] * scale);
-            }
+    put_outer<In, BLOCKS, RANK_INNER>(a, chunk, col0 + 32 * wave, rank0, acc);
 }
 
-// Adapters without tokens get zeros, those of several chunks their sum.
+// Adapters without tokens get zeros, those of several chunks their sum, eight
+// loads at a time.
 template <class In>
-__global__ __launch_bounds__(256) void join_kernel(OuterArgs a)
+__global__ __launch_bounds__(256) void join_kernel(OuterArgs first, OuterArgs second)
 {
+    const OuterArgs &a = blockIdx.z == 0 ? first : second;
+    if (a.out == nullptr) return;
     const int adapter = blockIdx.y;
     const int2 join = a.cut.joins[adapter];
     if (join.y == 1) return;
     const float scale = a.scales != nullptr ? a.scales[adapter] : 1.0f;
     const int64_t inner = a.rank_inner ? a.rank : a.C, outer = a.rank_inner ? a.C : a.rank, size = inner * outer;
     for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < size; n += (int64_t)gridDim.x * 256) {
+        const float *from = a.part + join.x * size + n;
         float sum = 0;
-        for (int c = 0; c < join.y; ++c) sum += a.part[(join.x + c) * size + n];
+        for (int c = 0; c < join.y; c += 8) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = c + e < join.y ? from[(c + e) * size] : 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum += v[e];
+        }
         ((In *)a.out)[adapter * a.stride_out + n / inner * a.ldo + n % inner] = (In)(join.y ? sum * scale : 0.0f);
+    }
+}
+
+// 64×64 elements at a time through LDS.
+template <class In>
+__global__ __launch_bounds__(256) void turn_kernel(TurnArgs first, TurnArgs second)
+{
+    __shared__ In tile[64][65];
+    const bool other = blockIdx.z >= (unsigned)first.from.count;
+    const TurnArgs &a = other ? second : first;
+    if (a.to == nullptr) return;
+    const int64_t adapter = other ? blockIdx.z - first.from.count : blockIdx.z;
+    const int64_t rows = a.from.rank_inner ? a.outer : a.from.rank, cols = a.from.rank_inner ? a.from.rank : a.outer;
+    const int64_t across = (cols + 63) / 64, tiles = (rows + 63) / 64 * across;
+    const In *from = (const In *)a.from.p + adapter * a.from.stride;
+    In *to = (In *)a.to + adapter * a.to_stride;
+    for (int64_t n = blockIdx.x; n < tiles; n += gridDim.x) {
+        const int64_t r0 = n / across * 64, c0 = n % across * 64;
+        for (int e = threadIdx.x; e < 4096; e += 256)
+            if (r0 + e / 64 < rows && c0 + e % 64 < cols) tile[e / 64][e % 64] = from[(r0 + e / 64) * a.from.ld + c0 + e % 64];
+        __syncthreads();
+        for (int e = threadIdx.x; e < 4096; e += 256)
+            if (c0 + e / 64 < cols && r0 + e % 64 < rows) to[(c0 + e / 64) * a.to_ld + r0 + e % 64] = tile[e % 64][e / 64];
+        __syncthreads();
     }
 }
 
@@ -486,8 +702,15 @@ template <class In, int BLOCKS>
 void outer(const OuterArgs &a, hipStream_t stream)
 {
     const dim3 grid((unsigned)((a.C + kOuterColumns - 1) / kOuterColumns), a.most_chunks, (a.rank + 16 * BLOCKS - 1) / (16 * BLOCKS));
-    if (a.rank_inner) outer_kernel<In, BLOCKS, true><<<grid, 256, 0, stream>>>(a);
-    else outer_kernel<In, BLOCKS, false><<<grid, 256, 0, stream>>>(a);
+    if constexpr (sizeof(In) == 2) {
+        if (a.arranged != nullptr) {
+            if (a.rank_inner) outer_kernel<In, BLOCKS, true><<<grid, 256, 0, stream>>>(a);
+            else outer_kernel<In, BLOCKS, false><<<grid, 256, 0, stream>>>(a);
+            return;
+        }
+    }
+    if (a.rank_inner) outer_any_kernel<In, BLOCKS, true><<<grid, 256, 0, stream>>>(a);
+    else outer_any_kernel<In, BLOCKS, false><<<grid, 256, 0, stream>>>(a);
 }
 template <class In>
 void outer(const OuterArgs &a, hipStream_t stream)
@@ -532,13 +755,30 @@ hipError_t launch_outer(const OuterArgs &a, hipStream_t stream)
     return hipGetLastError();
 }
 
-hipError_t launch_join(const OuterArgs &a, hipStream_t stream)
+hipError_t launch_arrange(const OuterArgs &a, const OuterArgs &b, hipStream_t stream)
 {
-    const int64_t blocks = ((int64_t)a.C * a.rank + 1023) / 1024;
-    const dim3 grid((unsigned)(blocks < 1024 ? blocks : 1024), a.count);
-    if (a.dtype == TGEMM_F32) join_kernel<float><<<grid, 256, 0, stream>>>(a);
-    else if (a.dtype == TGEMM_BF16) join_kernel<__bf16><<<grid, 256, 0, stream>>>(a);
-    else join_kernel<_Float16><<<grid, 256, 0, stream>>>(a);
+    const int most = a.most_chunks > b.most_chunks ? a.most_chunks : b.most_chunks;
+    const int tokens = a.cut.tokens > b.cut.tokens ? a.cut.tokens : b.cut.tokens;
+    arrange_kernel<<<dim3(most, (tokens + kArranged - 1) / kArranged, 2), 256, 0, stream>>>(a, b);
+    return hipGetLastError();
+}
+
+hipError_t launch_join(const OuterArgs &a, const OuterArgs &b, hipStream_t stream)
+{
+    const int64_t C = a.C > b.C ? a.C : b.C, blocks = (C * a.rank + 255) / 256;
+    const dim3 grid((unsigned)(blocks < 1024 ? blocks : 1024), a.count, 2);
+    if (a.dtype == TGEMM_F32) join_kernel<float><<<grid, 256, 0, stream>>>(a, b);
+    else if (a.dtype == TGEMM_BF16) join_kernel<__bf16><<<grid, 256, 0, stream>>>(a, b);
+    else join_kernel<_Float16><<<grid, 256, 0, stream>>>(a, b);
+    return hipGetLastError();
+}
+
+hipError_t launch_turn(const TurnArgs &a, const TurnArgs &b, hipStream_t stream)
+{
+    const int64_t outer = a.outer > b.outer ? a.outer : b.outer, tiles = (outer + 63) / 64 * ((a.from.rank + 63) / 64);
+    const dim3 grid((unsigned)(tiles < 1024 ? tiles : 1024), 1, a.from.count + b.from.count);
+    if (a.dtype == TGEMM_F32) turn_kernel<float><<<grid, 256, 0, stream>>>(a, b);
+    else turn_kernel<uint16_t><<<grid, 256, 0, stream>>>(a, b);
     return hipGetLastError();
 }
 
