@@ -154,7 +154,7 @@ namespace adapters {
 
 hipError_t launch_shrink(const ShrinkArgs &a, hipStream_t)
 {
-    if (a.parts < 1 || a.slots < 1 || a.part_k % 128 || a.parts * a.part_k < a.K || (a.parts - 1) * a.part_k >= a.K) fail("parts", 0, 0);
+    if (a.parts < 1 || a.slots < 1 || a.part_k % 256 || a.parts * a.part_k < a.K || (a.parts - 1) * a.part_k >= a.K) fail("parts", 0, 0);
     if (a.parts > 1 && (!a.part || a.planes)) fail("parts without room", 0, 0);
     if (!a.part && !a.planes) fail("hidden values for nobody", 0, 0);
     rows(a.rows, a.T, a.K, a.ld, size_of(a.dtype), false, "shrink's rows");
@@ -177,9 +177,19 @@ hipError_t launch_product(bool, bool b_mc, int tile, const ProductArgs &a, hipSt
     if (b_mc) walk_tile<false, true>(tile, a.op);
     else walk_tile<false, false>(tile, a.op);
     out(a.out, a.op.M, a.op.N, a.ldo, a.dtype, a.op.splits, a.split_stride);
+    if ((a.e.ids == nullptr) != (a.op.splits > 1)) fail("adapters of a split sum", 0, 0);
+    if (a.e.ids == nullptr) return hipSuccess;
     rows(a.e.planes, a.op.M, planes_rank(a.e.c.rank), planes_rank(a.e.c.rank), 4, false, "hidden planes");
     stack(a.e.c, a.op.N, size_of(a.stored), "the product's adapters");
     if (!a.e.c.rank_inner && !b_mc) fail("adapters the other way", 0, 0);
+    return hipSuccess;
+}
+hipError_t launch_add(const AddArgs &a, hipStream_t)
+{
+    for (int p : {0, a.count - 1}) rows(a.part + p * a.stride, a.T, a.N, a.ld, 4, false, "parts of a sum");
+    rows(a.out, a.T, a.N, a.ldo, size_of(a.dtype), true, "a sum");
+    rows(a.e.planes, a.T, planes_rank(a.e.c.rank), planes_rank(a.e.c.rank), 4, false, "hidden planes");
+    stack(a.e.c, a.N, size_of(a.dtype), "the sum's adapters");
     return hipSuccess;
 }
 hipError_t launch_few(const FewArgs &a, hipStream_t)
@@ -259,6 +269,21 @@ hipError_t launch_turn(const TurnArgs &a, const TurnArgs &b, hipStream_t)
 
 }  // namespace adapters
 }  // namespace tgemm
+
+extern "C" {
+int tgemm_sgemm_splitk_choose(int64_t M, int64_t N, int64_t K) { return M * N < 512 * 512 && K > 512 ? 4 : 1; }
+size_t tgemm_sgemm_splitk_workspace_size(int64_t M, int64_t N, int64_t, int splits) { return splits > 1 ? (size_t)M * N * splits * 4 : 0; }
+tgemm_status_t tgemm_sgemm_splitk_ex(tgemm_op_t op_a, tgemm_op_t op_b, int64_t M, int64_t N, int64_t K, const float *A, int64_t lda,
+                                     const float *B, int64_t ldb, float *C, int64_t ldc, int splits, void *room, size_t bytes, hipStream_t)
+{
+    rows(A, op_a ? K : M, op_a ? M : K, lda, 4, false, "A");
+    rows(B, op_b ? N : K, op_b ? K : N, ldb, 4, false, "B");
+    rows(C, M, N, ldc, 4, true, "C");
+    if (bytes != tgemm_sgemm_splitk_workspace_size(M, N, K, splits)) fail("a workspace", 0, bytes);
+    touch(room, bytes, true, "the product's workspace");
+    return TGEMM_SUCCESS;
+}
+}
 
 int main()
 {

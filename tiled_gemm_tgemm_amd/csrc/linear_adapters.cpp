@@ -90,15 +90,39 @@ Shrink shrink_of(int64_t T, int64_t K, int64_t count)
     Shrink s;
     s.rows_each = T <= 1024 ? 16 : T < 4096 ? 64 : 128;
     const int64_t wavefronts = 4 * ceil_div(T, s.rows_each);
-    int64_t parts = 2048 / wavefronts;
+    int64_t parts = 4096 / wavefronts;
     if (parts > ceil_div(K, 512)) parts = ceil_div(K, 512);
-    if (parts > 8) parts = 8;
+    if (parts > (T <= 1024 ? 8 : 16)) parts = T <= 1024 ? 8 : 16;
     if (parts < 1) parts = 1;
-    s.part_k = round_up(ceil_div(K, parts), 128);
+    s.part_k = round_up(ceil_div(K, parts), 256);
     s.parts = (int)ceil_div(K, s.part_k);
     s.slots = T <= 1024 ? 16 : 1;
     if (s.slots > count) s.slots = (int)count;
     return s;
+}
+
+// How a product with the weight is taken: on the tiles, or, float32 ones, on the
+// library's float32 product, which needs no planes.  Six products of planes are
+// 1.4 times faster than one in float32 where there are many tiles; with few of
+// them, or short sums, the planes' copies and the steps' own time take that
+// back.
+struct Route {
+    bool plain = false;
+    Choice tile;
+    int splits = 1;  // of the plain product
+};
+Route route_of(tgemm_dtype_t dtype, int64_t M, int64_t N, int64_t K, int64_t k_steps, int64_t copied, int64_t most_ld)
+{
+    Route r;
+    r.tile = choose_tile(M, N, k_steps * (dtype == TGEMM_F32 ? 6 : 1), true);
+    r.tile.splits = parts_of(k_steps, r.tile.splits);
+    if (dtype != TGEMM_F32 || most_ld >= (int64_t)1 << 21) return r;
+    // the planes are read and written once, 10 bytes a value, by launches of their own
+    const double planes = r.tile.time + 10.0 + (double)copied * 10.0 / 4e6;
+    const double plain = 10.0 + 2.0 * (double)M * (double)N * (double)K / 125e6;
+    r.plain = plain < planes;
+    if (r.plain) r.splits = tgemm_sgemm_splitk_choose(M, N, K);
+    return r;
 }
 
 // Where a call's buffers lie in its workspace.
@@ -112,12 +136,12 @@ struct Plan {
     Shrink shrink;
     // forward
     bool few = false;
-    Choice tile;
+    Route main;
     int64_t out_part = -1;
     // backward
     Shrink shrink_x;
     int64_t u = -1, hidden = -1, parts_x = -1;
-    Choice dw;
+    Route dw;
     int64_t dw_part = -1;
     int64_t order = -1, starts = -1, chunks[2] = {-1, -1}, joins[2] = {-1, -1}, counts = -1, sums[2] = {-1, -1};
     int64_t arranged[2] = {-1, -1}, arranged_plane[2] = {0, 0};
@@ -153,12 +177,15 @@ bool plan_forward(Plan &p, const Layer &l)
     if (p.few || p.shrink.parts > 1) p.parts = p.take(p.shrink.parts * l.T * l.rank * 4);
     if (p.few) return true;
     p.hidden_planes = p.take(planes_bytes(l));
+    p.main = route_of(l.dtype, l.T, l.N, l.D, p.Dp / kStepK, (l.T + l.N) * l.D, l.ldx > l.ldw ? l.ldx : l.ldw);
+    if (p.main.plain) {
+        p.out_part = p.take((int64_t)tgemm_sgemm_splitk_workspace_size(l.T, l.N, l.D, p.main.splits));
+        return true;
+    }
     if (!as_stored(l.dtype, l.X, l.ldx, l.D, kStepK)) p.x = p.take(l.T * p.Dp * 2 * p.planes);
     if (!as_stored(l.dtype, l.W, l.ldw, l.D, 8)) p.w = p.take(l.N * p.Dp * 2 * p.planes);
-    p.tile = choose_tile(l.T, l.N, p.Dp / kStepK * p.segments, true);
-    p.tile.splits = parts_of(p.Dp / kStepK, p.tile.splits);
-    if (p.tile.splits > 1) p.out_part = p.take(p.tile.splits * l.T * p.Np * 4);
-    return fits(l.T, l.N, p.tile.tile, p.tile.splits);
+    if (p.main.tile.splits > 1) p.out_part = p.take(p.main.tile.splits * l.T * p.Np * 4);
+    return fits(l.T, l.N, p.main.tile.tile, p.main.tile.splits);
 }
 
 struct Need {
@@ -213,24 +240,27 @@ bool plan_backward(Plan &p, const Layer &l, const void *dY, int64_t lddy, Need n
         if (p.shrink_x.parts > 1) p.parts_x = p.take(p.shrink_x.parts * l.T * l.rank * 4);
         p.hidden = p.take(l.T * l.rank * 4);
     }
+    const int64_t widest = l.ldx > lddy ? l.ldx > l.ldw ? l.ldx : l.ldw : lddy > l.ldw ? lddy : l.ldw;
+    if (need.x) p.main = route_of(l.dtype, l.T, l.D, l.N, p.Np / kStepK, (l.T + l.D) * l.N, widest);
+    if (need.w) p.dw = route_of(l.dtype, l.N, l.D, l.T, p.Tp / kStepK, (l.N + l.D) * l.T, widest);
     // dY comes first in either product: along K for dX, across for dW, whose sum has whole steps of tokens
-    if ((need.x && !as_stored(l.dtype, dY, lddy, l.N, kStepK)) ||
-        (need.w && (!as_stored(l.dtype, dY, lddy, l.N, 8) || l.T % kStepK != 0)))
+    if ((need.x && !p.main.plain && !as_stored(l.dtype, dY, lddy, l.N, kStepK)) ||
+        (need.w && !p.dw.plain && (!as_stored(l.dtype, dY, lddy, l.N, 8) || l.T % kStepK != 0)))
         p.dy = p.take(p.Tp * p.Np * 2 * p.planes);
     bool fit = true;
-    if (need.x) {
+    if (need.x && p.main.plain) {
+        p.out_part = p.take((int64_t)tgemm_sgemm_splitk_workspace_size(l.T, l.D, l.N, p.main.splits));
+    } else if (need.x) {
         if (!as_stored(l.dtype, l.W, l.ldw, l.D, 8)) p.w = p.take(l.N * p.Dp * 2 * p.planes);
-        p.tile = choose_tile(l.T, l.D, p.Np / kStepK * p.segments, true);
-        p.tile.splits = parts_of(p.Np / kStepK, p.tile.splits);
-        if (p.tile.splits > 1) p.out_part = p.take(p.tile.splits * l.T * p.Dp * 4);
-        fit = fits(l.T, l.D, p.tile.tile, p.tile.splits);
+        if (p.main.tile.splits > 1) p.out_part = p.take(p.main.tile.splits * l.T * p.Dp * 4);
+        fit = fits(l.T, l.D, p.main.tile.tile, p.main.tile.splits);
     }
-    if (need.w) {
+    if (need.w && p.dw.plain) {
+        p.dw_part = p.take((int64_t)tgemm_sgemm_splitk_workspace_size(l.N, l.D, l.T, p.dw.splits));
+    } else if (need.w) {
         if (!as_stored(l.dtype, l.X, l.ldx, l.D, 8)) p.x = p.take(l.T * p.Dp * 2 * p.planes);
-        p.dw = choose_tile(l.N, l.D, p.Tp / kStepK * p.segments, true);
-        p.dw.splits = parts_of(p.Tp / kStepK, p.dw.splits);
-        if (p.dw.splits > 1) p.dw_part = p.take(p.dw.splits * l.N * p.Dp * 4);
-        fit = fit && fits(l.N, l.D, p.dw.tile, p.dw.splits);
+        if (p.dw.tile.splits > 1) p.dw_part = p.take(p.dw.tile.splits * l.N * p.Dp * 4);
+        fit = fit && fits(l.N, l.D, p.dw.tile.tile, p.dw.tile.splits);
     }
     return fit;
 }
@@ -296,26 +326,35 @@ hipError_t make_hidden(ShrinkArgs a, float *parts, float *hidden, void *planes, 
 Stack stack_a(const Layer &l) { return Stack{l.A, l.lda, l.stride_a, false, (int)l.count, (int)l.rank}; }
 Stack stack_b(const Layer &l) { return Stack{l.B, l.ldb, l.stride_b, true, (int)l.count, (int)l.rank}; }
 
-// The product, its adapters' part and the sum over its parts.
+// The product on the tiles with its adapters' part.
 hipError_t run_product(const Plan &p, const Layer &l, ProductArgs a, bool b_mc, int64_t steps, int64_t ld_part, void *out,
                        int64_t ldo, void *ws, hipStream_t stream)
 {
+    const Choice &tile = p.main.tile;
+    const Expand e = a.e;
     a.stored = l.dtype;
     a.out = out;
     a.ldo = ldo;
     a.dtype = l.dtype;
-    if (p.tile.splits > 1) {
-        a.op.splits = p.tile.splits;
-        a.op.steps_per_split = (int)ceil_div(steps, p.tile.splits);
-        a.out = in<float>(ws, p.out_part);
-        a.ldo = ld_part;
-        a.dtype = TGEMM_F32;
-        a.split_stride = l.T * ld_part;
-    }
-    hipError_t e = launch_product(p.half, b_mc, p.tile.tile, a, stream);
-    if (e != hipSuccess || p.tile.splits == 1) return e;
-    const SumArgs s{l.T, a.op.N, in<float>(ws, p.out_part), ld_part, a.split_stride, p.tile.splits, nullptr, nullptr, out, ldo, l.dtype};
-    return launch_sum(s, stream);
+    if (tile.splits == 1) return launch_product(p.half, b_mc, tile.tile, a, stream);
+    a.op.splits = tile.splits;
+    a.op.steps_per_split = (int)ceil_div(steps, tile.splits);
+    a.out = in<float>(ws, p.out_part);
+    a.ldo = ld_part;
+    a.dtype = TGEMM_F32;
+    a.split_stride = l.T * ld_part;
+    a.e.ids = nullptr;
+    const hipError_t st = launch_product(p.half, b_mc, tile.tile, a, stream);
+    if (st != hipSuccess) return st;
+    return launch_add(AddArgs{l.T, a.op.N, in<float>(ws, p.out_part), ld_part, a.split_stride, tile.splits, out, ldo, l.dtype, e}, stream);
+}
+
+// A float32 product as it is.
+tgemm_status_t run_plain(const Route &r, tgemm_op_t op_a, tgemm_op_t op_b, int64_t M, int64_t N, int64_t K, const void *A, int64_t lda,
+                         const void *B, int64_t ldb, void *C, int64_t ldc, void *room, hipStream_t stream)
+{
+    return tgemm_sgemm_splitk_ex(op_a, op_b, M, N, K, (const float *)A, lda, (const float *)B, ldb, (float *)C, ldc, r.splits, room,
+                                 tgemm_sgemm_splitk_workspace_size(M, N, K, r.splits), stream);
 }
 
 tgemm_status_t forward(const Plan &p, const Layer &l, void *Y, int64_t ldy, float *hidden, void *ws, hipStream_t stream)
@@ -332,13 +371,21 @@ tgemm_status_t forward(const Plan &p, const Layer &l, void *Y, int64_t ldy, floa
     }
     void *planes = in<void>(ws, p.hidden_planes);
     hipError_t e = make_hidden(s, in<float>(ws, p.parts), hidden, planes, stream);
+    const Expand expand{l.ids, l.scales, nullptr, 0, 1, planes, stack_b(l)};
+    if (p.main.plain) {
+        if (e != hipSuccess) return from_hip(e);
+        const tgemm_status_t st = run_plain(p.main, TGEMM_OP_N, TGEMM_OP_T, l.T, l.N, l.D, l.X, l.ldx, l.W, l.ldw, Y, ldy,
+                                            in<void>(ws, p.out_part), stream);
+        if (st != TGEMM_SUCCESS) return st;
+        return from_hip(launch_add(AddArgs{l.T, l.N, (const float *)Y, ldy, 0, 1, Y, ldy, l.dtype, expand}, stream));
+    }
     Stored x, w;
     if (e == hipSuccess) e = lay_out(p, l, l.X, l.ldx, l.T, l.D, p.x, l.T, ws, x, stream);
     if (e == hipSuccess) e = lay_out(p, l, l.W, l.ldw, l.N, l.D, p.w, l.N, ws, w, stream);
     if (e != hipSuccess) return from_hip(e);
     ProductArgs a{};
     const int64_t steps = p.Dp / kStepK;
-    a.op = tgemm::loss::operands(p.segments, l.T, l.N, steps, p.tile.tile);
+    a.op = tgemm::loss::operands(p.segments, l.T, l.N, steps, p.main.tile.tile);
     a.op.A = x.p;
     a.op.lda = x.ld;
     a.op.plane_a = x.plane;
@@ -348,7 +395,7 @@ tgemm_status_t forward(const Plan &p, const Layer &l, void *Y, int64_t ldy, floa
     a.op.plane_b = w.plane;
     a.op.mn_b = (int)l.N;
     a.op.k_b = (int)(p.w >= 0 ? p.Dp : l.D);
-    a.e = Expand{l.ids, l.scales, nullptr, 0, 1, planes, stack_b(l)};
+    a.e = expand;
     return from_hip(run_product(p, l, a, false, steps, p.Np, Y, ldy, ws, stream));
 }
 
@@ -430,14 +477,28 @@ tgemm_status_t backward(const Plan &p, const Layer &l, const void *dY, int64_t l
     }
     if (l.T == 0) return g.dW ? from_hip(launch_zero(g.dW, g.lddw, l.dtype, l.N, l.D, stream)) : TGEMM_SUCCESS;
 
+    const Expand expand{l.ids, l.scales, nullptr, 0, 1, planes, a_stack};
+    if (g.dX != nullptr && p.main.plain) {
+        const tgemm_status_t st = run_plain(p.main, TGEMM_OP_N, TGEMM_OP_N, l.T, l.D, l.N, dY, lddy, l.W, l.ldw, g.dX, g.lddx,
+                                            in<void>(ws, p.out_part), stream);
+        if (st != TGEMM_SUCCESS) return st;
+        e = launch_add(AddArgs{l.T, l.D, (const float *)g.dX, g.lddx, 0, 1, g.dX, g.lddx, l.dtype, expand}, stream);
+        if (e != hipSuccess) return from_hip(e);
+    }
+    if (g.dW != nullptr && p.dw.plain) {
+        const tgemm_status_t st = run_plain(p.dw, TGEMM_OP_T, TGEMM_OP_N, l.N, l.D, l.T, dY, lddy, l.X, l.ldx, g.dW, g.lddw,
+                                            in<void>(ws, p.dw_part), stream);
+        if (st != TGEMM_SUCCESS) return st;
+    }
+    const bool tiled_x = g.dX != nullptr && !p.main.plain, tiled_w = g.dW != nullptr && !p.dw.plain;
     Stored dy, w, x;
-    if (g.dX != nullptr || g.dW != nullptr) e = lay_out(p, l, dY, lddy, l.T, l.N, p.dy, p.Tp, ws, dy, stream);
-    if (e == hipSuccess && g.dX != nullptr) {
+    if (tiled_x || tiled_w) e = lay_out(p, l, dY, lddy, l.T, l.N, p.dy, p.Tp, ws, dy, stream);
+    if (e == hipSuccess && tiled_x) {
         e = lay_out(p, l, l.W, l.ldw, l.N, l.D, p.w, l.N, ws, w, stream);
         if (e != hipSuccess) return from_hip(e);
         ProductArgs a{};
         const int64_t steps = p.Np / kStepK;
-        a.op = tgemm::loss::operands(p.segments, l.T, l.D, steps, p.tile.tile);
+        a.op = tgemm::loss::operands(p.segments, l.T, l.D, steps, p.main.tile.tile);
         a.op.A = dy.p;
         a.op.lda = dy.ld;
         a.op.plane_a = dy.plane;
@@ -447,15 +508,15 @@ tgemm_status_t backward(const Plan &p, const Layer &l, const void *dY, int64_t l
         a.op.plane_b = w.plane;
         a.op.mn_b = (int)(p.w >= 0 ? p.Dp : l.D);
         a.op.k_b = (int)l.N;
-        a.e = Expand{l.ids, l.scales, nullptr, 0, 1, planes, a_stack};
+        a.e = expand;
         e = run_product(p, l, a, true, steps, p.Dp, g.dX, g.lddx, ws, stream);
     }
-    if (e == hipSuccess && g.dW != nullptr) {
+    if (e == hipSuccess && tiled_w) {
         e = lay_out(p, l, l.X, l.ldx, l.T, l.D, p.x, l.T, ws, x, stream);
         if (e != hipSuccess) return from_hip(e);
         OutArgs d{};
         const int64_t steps = p.Tp / kStepK;
-        d.op = tgemm::loss::operands(p.segments, l.N, l.D, steps, p.dw.tile);
+        d.op = tgemm::loss::operands(p.segments, l.N, l.D, steps, p.dw.tile.tile);
         d.op.A = dy.p;
         d.op.lda = dy.ld;
         d.op.plane_a = dy.plane;
@@ -469,17 +530,17 @@ tgemm_status_t backward(const Plan &p, const Layer &l, const void *dY, int64_t l
         d.out = g.dW;
         d.ldo = g.lddw;
         d.dtype = l.dtype;
-        if (p.dw.splits > 1) {
-            d.op.splits = p.dw.splits;
-            d.op.steps_per_split = (int)ceil_div(steps, p.dw.splits);
+        if (p.dw.tile.splits > 1) {
+            d.op.splits = p.dw.tile.splits;
+            d.op.steps_per_split = (int)ceil_div(steps, p.dw.tile.splits);
             d.out = in<float>(ws, p.dw_part);
             d.ldo = p.Dp;
             d.dtype = TGEMM_F32;
             d.split_stride = l.N * p.Dp;
         }
-        e = launch_dw(p.half, p.dw.tile, d, stream);
-        if (e == hipSuccess && p.dw.splits > 1) {
-            const SumArgs s{l.N, l.D, in<float>(ws, p.dw_part), p.Dp, d.split_stride, p.dw.splits, nullptr, nullptr, g.dW, g.lddw, l.dtype};
+        e = launch_dw(p.half, p.dw.tile.tile, d, stream);
+        if (e == hipSuccess && p.dw.tile.splits > 1) {
+            const SumArgs s{l.N, l.D, in<float>(ws, p.dw_part), p.Dp, d.split_stride, p.dw.tile.splits, nullptr, nullptr, g.dW, g.lddw, l.dtype};
             e = launch_sum(s, stream);
         }
     }

@@ -43,7 +43,7 @@ struct ShrinkArgs {
     const float *scales;
     float *part;
     void *planes;
-    int64_t part_k;  // values of k a part, a multiple of 128
+    int64_t part_k;  // values of k a part, a multiple of 256
     int parts, slots;
     int rows_each;   // 16: a work-group's wavefronts share 16 rows' sums; 64, 128: they take 16, 32 rows each
 };
@@ -64,7 +64,7 @@ struct Expand {
     Stack c;
 };
 
-// C = A·B + the adapters' part, A as stored along K, B along K (forward, with
+// C = A·B + the adapters' part (without where e.ids is NULL), A as stored along K, B along K (forward, with
 // the adapters' ranks the inner ones) or not (dX).
 struct ProductArgs {
     m16::Operands op;
@@ -76,6 +76,19 @@ struct ProductArgs {
     Expand e;
 };
 hipError_t launch_product(bool half, bool b_mc, int tile, const ProductArgs &a, hipStream_t stream);
+
+// out = the sum of `count` parts + the adapters' part (with one part, out may be it).
+struct AddArgs {
+    int64_t T, N;
+    const float *part;
+    int64_t ld, stride;
+    int count;
+    void *out;
+    int64_t ldo;
+    tgemm_dtype_t dtype;
+    Expand e;
+};
+hipError_t launch_add(const AddArgs &a, hipStream_t stream);
 
 // The same for at most kFewRows rows, forward, on operands however they are stored.
 constexpr int64_t kFewRows = 64;

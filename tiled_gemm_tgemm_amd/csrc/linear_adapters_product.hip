@@ -99,34 +99,46 @@ struct Ranks<float> {
     }
 };
 
-// Eight ranks of a row's hidden values, from rank k on.
+// Eight ranks of a row's hidden values, from rank k on, four parts' loads at once.
 __device__ __forceinline__ void load_hidden(const Expand &e, int64_t row, int k, float (&v)[8])
 {
     const float *from = e.hidden + row * e.c.rank + k;
-    load_some<float, 8>(from, e.c.rank - k, v);
-    for (int p = 1; p < e.parts; ++p) {
-        float more[8];
-        load_some<float, 8>(from + p * e.part_stride, e.c.rank - k, more);
 #pragma unroll
-        for (int n = 0; n < 8; ++n) v[n] += more[n];
+    for (int n = 0; n < 8; ++n) v[n] = 0.0f;
+    for (int p = 0; p < e.parts; p += 4) {
+        float next[4][8];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) load_some<float, 8>(from + (p + u) * e.part_stride, p + u < e.parts ? e.c.rank - k : 0, next[u]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int n = 0; n < 8; ++n) v[n] += next[u][n];
     }
 }
 
 // A row's adapter: -1 for none, -2 for an id out of range.
 __device__ __forceinline__ int id_of(const Expand &e, int64_t row, int64_t rows)
 {
-    if (row >= rows) return -1;
+    if (row >= rows || e.ids == nullptr) return -1;
     const int64_t id = e.ids[row];
     return id >= 0 && id < e.c.count ? (int)id : id == -1 ? -1 : -2;
 }
 
-// A lane's row of hidden values.
-__device__ __forceinline__ float hidden_at(const __bf16 *planes, int64_t row, int k, int padded)
+// Eight hidden values of a row.
+__device__ __forceinline__ void eight_hidden(const __bf16 *planes, int64_t row, int k, int padded, float (&h)[8])
 {
-    const __bf16 *from = planes + row * 2 * padded + k;
-    return (float)from[0] + (float)from[padded];
+    TwoPlanes both;
+    read_planes(planes, row, k, padded, both);
+#pragma unroll
+    for (int n = 0; n < 8; ++n) h[n] = (float)both.high[n] + (float)both.low[n];
 }
-__device__ __forceinline__ float hidden_at(const float *planes, int64_t row, int k, int padded) { return planes[row * padded + k]; }
+__device__ __forceinline__ void eight_hidden(const float *planes, int64_t row, int k, int padded, float (&h)[8])
+{
+    EightFloats all;
+    read_planes(planes, row, k, padded, all);
+#pragma unroll
+    for (int n = 0; n < 8; ++n) h[n] = all.v[n / 4][n % 4];
+}
 
 // The adapters' part of a lane's row and H adjacent columns on the vector units:
 // every lane reads its own adapter.
@@ -142,8 +154,7 @@ __device__ __forceinline__ void add_lanes(const Expand &e, int id, int64_t row, 
             int first = col;  // addresses are worked out anew, not kept in registers over the loop
             asm volatile("" : "+v"(first));
             float h[8];
-#pragma unroll
-            for (int n = 0; n < 8; ++n) h[n] = hidden_at((const P *)e.planes, row, k + n, padded);
+            eight_hidden((const P *)e.planes, row, k, padded, h);
 #pragma unroll
             for (int j = 0; j < H / 4; ++j) {
                 C v[4][8];
@@ -157,12 +168,16 @@ __device__ __forceinline__ void add_lanes(const Expand &e, int id, int64_t row, 
             }
         }
     } else {
-        for (int k = 0; k < e.c.rank; ++k) {
-            const float h = hidden_at((const P *)e.planes, row, k, padded);
-            C v[H];
-            load_some<C, H>(c + k * e.c.ld + min(col, columns - 1), left, v);
+        for (int k = 0; k < e.c.rank; k += 8) {
+            float h[8];
+            eight_hidden((const P *)e.planes, row, k, padded, h);
 #pragma unroll
-            for (int x = 0; x < H; ++x) acc[x / 4][x % 4] = fmaf(h, (float)v[x], acc[x / 4][x % 4]);
+            for (int n = 0; n < 8; ++n) {
+                C v[H];
+                load_some<C, H>(c + (k + n) * e.c.ld + min(col, columns - 1), k + n < e.c.rank ? left : 0, v);
+#pragma unroll
+                for (int x = 0; x < H; ++x) acc[x / 4][x % 4] = fmaf(h[n], (float)v[x], acc[x / 4][x % 4]);
+            }
         }
     }
 }
@@ -192,14 +207,13 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 32 ? 3 : 2) void adapted_kernel
     };
     Tile::run(a.op, (lds_char *)lds, prologue, [&](typename Tile::Acc &acc, int row0, int col0, int split, const Ahead &ahead) {
         const int lane = m16::thread_anew() & 63, l16 = lane & 15, quarter = lane >> 4;
-        // 32 rows at a time, which leaves the other accumulators where they are;
-        // the first part of a split sum adds it
+        // 32 rows at a time, which leaves the other accumulators where they are
         const int padded = (int)planes_rank(a.e.c.rank);
 #pragma unroll
         for (int i0 = 0; i0 < Tile::FM; i0 += 2) {
             int id[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) id[i] = split == 0 ? ahead.id[i0 + i] : -1;
+            for (int i = 0; i < 2; ++i) id[i] = ahead.id[i0 + i];
             uint64_t left = (__ballot(id[0] >= 0) & 0xFFFF) | __ballot(id[1] >= 0) << 16;
             left &= 0xFFFFFFFF;
             auto next = [&]() {
@@ -287,26 +301,98 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 32 ? 3 : 2) void adapted_kernel
     });
 }
 
+// The sum over parts and the adapters' part, four columns a thread: a wavefront
+// has 256 columns of a row.  (In the tiles of a split sum, which are few and
+// short, the adapters' loads would be waited for: 256×4096×4096 with 32 adapters
+// 49 µs and 5 for the sum.)
+template <class C, bool RANK_INNER>
+__global__ __launch_bounds__(256) void adapted_sum_kernel(AddArgs a)
+{
+    typedef typename std::conditional<sizeof(C) == 4, float, __bf16>::type P;
+    const int64_t per_row = (a.N + 255) / 256 * 64, total = a.T * per_row;
+    const int padded = (int)planes_rank(a.e.c.rank);
+    for (int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x; p < total; p += (int64_t)gridDim.x * 256) {
+        const int64_t row = p / per_row, col = p % per_row * 4, left = a.N - col;
+        if (left <= 0) continue;
+        float v[4];
+        load_some<float, 4>(a.part + row * a.ld + col, left, v);
+        for (int s = 1; s < a.count; s += 8) {  // eight parts on their way at once
+            float next[8][4];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) load_some<float, 4>(a.part + row * a.ld + col + (s + u) * a.stride, s + u < a.count ? left : 0, next[u]);
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] += next[u][e];
+        }
+        const int id = id_of(a.e, row, a.T);
+        if (id >= 0) {
+            const C *c = (const C *)a.e.c.p + id * a.e.c.stride;
+            if constexpr (RANK_INNER) {
+                for (int k = 0; k < a.e.c.rank; k += 8) {
+                    C w[4][8];
+                    float h[8];
+                    eight_hidden((const P *)a.e.planes, row, k, padded, h);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) load_some<C, 8>(c + (col + (x < left ? x : 0)) * a.e.c.ld + k, a.e.c.rank - k, w[x]);
+#pragma unroll
+                    for (int n = 0; n < 8; ++n)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) v[x] = fmaf(h[n], (float)w[x][n], v[x]);
+                }
+            } else {
+                for (int k = 0; k < a.e.c.rank; k += 8) {
+                    C w[8][4];
+                    float h[8];
+                    eight_hidden((const P *)a.e.planes, row, k, padded, h);
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) load_some<C, 4>(c + (k + n) * a.e.c.ld + col, k + n < a.e.c.rank ? left : 0, w[n]);
+#pragma unroll
+                    for (int n = 0; n < 8; ++n)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) v[x] = fmaf(h[n], (float)w[n][x], v[x]);
+                }
+            }
+        } else if (id == -2) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) v[x] = NAN;
+        }
+        C *to = (C *)a.out + row * a.ldo + col;
+        if (left >= 4) {
+            typename m16::Some<C, 4>::type w;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) w[x] = (C)v[x];
+            *(typename m16::Some<C, 4>::type *)to = w;
+        } else {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                if (x < left) to[x] = (C)v[x];
+        }
+    }
+}
+
 // ---- a few rows ------------------------------------------------------------
 
 // Fragments straight from device memory, no LDS stage and no barrier, as the
 // loss operators take a few rows: a wavefront takes COLS blocks of 16 columns of
-// the result, R blocks of 16 rows and an eighth of the sum.  Then each
+// the result, R blocks of 16 rows and an eighth of the sum, in steps of 64
+// values of k of which a lane takes 16 adjacent ones in two fragments: a row's
+// loads are whole cache lines.  Then each
 // lane adds its own rows' adapters on the vector units: there may be as many as
 // rows, and their matrices' loads do not wait for one another.
 constexpr int kFewParts = 8;
 template <class In, int R, int COLS>
 __global__ __launch_bounds__(64 * kFewParts) void adapted_few_kernel(FewArgs a)
 {
-    constexpr int S = kFewParts, kHeld = (R + COLS) * (sizeof(In) == 4 ? 2 : 1), U = kHeld <= 3 ? 4 : kHeld <= 6 ? 2 : 1;
+    constexpr int S = kFewParts, kHeld = (R + COLS) * (sizeof(In) == 4 ? 2 : 1), U = kHeld <= 3 ? 4 : 2;
     __shared__ f32x4 sums[S][R][COLS][64];
     const int lane = threadIdx.x & 63, part = threadIdx.x >> 6, l16 = lane & 15, quarter = lane >> 4;
     const int col0 = blockIdx.x * (16 * COLS);
     const In *w[COLS], *x[R];
 #pragma unroll
-    for (int j = 0; j < COLS; ++j) w[j] = (const In *)a.W + (int64_t)min(col0 + 16 * j + l16, a.N - 1) * a.ldw + 8 * quarter;
+    for (int j = 0; j < COLS; ++j) w[j] = (const In *)a.W + (int64_t)min(col0 + 16 * j + l16, a.N - 1) * a.ldw + 16 * quarter;
 #pragma unroll
-    for (int i = 0; i < R; ++i) x[i] = (const In *)a.X + (int64_t)min(16 * i + l16, a.T - 1) * a.ldx + 8 * quarter;
+    for (int i = 0; i < R; ++i) x[i] = (const In *)a.X + (int64_t)min(16 * i + l16, a.T - 1) * a.ldx + 16 * quarter;
     f32x4 acc[R][COLS];
 #pragma unroll
     for (int i = 0; i < R; ++i)
@@ -342,9 +428,9 @@ __global__ __launch_bounds__(64 * kFewParts) void adapted_few_kernel(FewArgs a)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
 #pragma unroll
-            for (int j = 0; j < COLS; ++j) load_some<In, 8>(w[j] + k + 32 * u, 8, vw[set][u][j]);
+            for (int j = 0; j < COLS; ++j) load_some<In, 8>(w[j] + k + 64 * (u / 2) + 8 * (u % 2), 8, vw[set][u][j]);
 #pragma unroll
-            for (int i = 0; i < R; ++i) load_some<In, 8>(x[i] + k + 32 * u, 8, vx[set][u][i]);
+            for (int i = 0; i < R; ++i) load_some<In, 8>(x[i] + k + 64 * (u / 2) + 8 * (u % 2), 8, vx[set][u][i]);
         }
     };
     auto use = [&](int set) {
@@ -370,14 +456,17 @@ __global__ __launch_bounds__(64 * kFewParts) void adapted_few_kernel(FewArgs a)
         }
     }
     if (part == S - 1) {
-        for (int k = all * 32 * U; k < a.D; k += 32) {
-            const int left = a.D - (k + 8 * quarter);
-            In zw[COLS][8], zx[R][8];
+        for (int k = all * 32 * U; k < a.D; k += 64) {
 #pragma unroll
-            for (int j = 0; j < COLS; ++j) load_some<In, 8>(w[j] + k, left, zw[j]);
+            for (int h = 0; h < 2; ++h) {
+                const int left = a.D - (k + 16 * quarter + 8 * h);
+                In zw[COLS][8], zx[R][8];
 #pragma unroll
-            for (int i = 0; i < R; ++i) load_some<In, 8>(x[i] + k, left, zx[i]);
-            multiply(zw, zx);
+                for (int j = 0; j < COLS; ++j) load_some<In, 8>(w[j] + k + 8 * h, left, zw[j]);
+#pragma unroll
+                for (int i = 0; i < R; ++i) load_some<In, 8>(x[i] + k + 8 * h, left, zx[i]);
+                multiply(zw, zx);
+            }
         }
     }
 #pragma unroll
@@ -466,6 +555,24 @@ hipError_t launch_product(bool half, bool b_mc, int tile, const ProductArgs &a, 
 {
     if (!b_mc) return product<false, true>(half, tile, a, stream);
     return a.e.c.rank_inner ? product<true, true>(half, tile, a, stream) : product<true, false>(half, tile, a, stream);
+}
+
+hipError_t launch_add(const AddArgs &a, hipStream_t stream)
+{
+    const int64_t blocks = (a.T * ((a.N + 255) / 256 * 64) + 255) / 256;
+    const unsigned grid = (unsigned)(blocks < (1 << 20) ? blocks : 1 << 20);
+    const bool inner = a.e.c.rank_inner;
+    if (a.dtype == TGEMM_F32) {
+        if (inner) adapted_sum_kernel<float, true><<<grid, 256, 0, stream>>>(a);
+        else adapted_sum_kernel<float, false><<<grid, 256, 0, stream>>>(a);
+    } else if (a.dtype == TGEMM_BF16) {
+        if (inner) adapted_sum_kernel<__bf16, true><<<grid, 256, 0, stream>>>(a);
+        else adapted_sum_kernel<__bf16, false><<<grid, 256, 0, stream>>>(a);
+    } else {
+        if (inner) adapted_sum_kernel<_Float16, true><<<grid, 256, 0, stream>>>(a);
+        else adapted_sum_kernel<_Float16, false><<<grid, 256, 0, stream>>>(a);
+    }
+    return hipGetLastError();
 }
 
 hipError_t launch_few(const FewArgs &a, hipStream_t stream)

@@ -97,11 +97,14 @@ __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a)
             const int64_t n = a.ids[row];
             if (n >= 0 && n < a.c.count) id[i] = (int)n;
         }
-        x[i] = (const In *)a.rows + (row < a.T ? row : a.T - 1) * a.ld + 8 * quarter;
+        x[i] = (const In *)a.rows + (row < a.T ? row : a.T - 1) * a.ld + 16 * quarter;
         left[i] = (uint32_t)__ballot(id[i] >= 0) & 0xFFFF;
     }
-    constexpr int kStep = SHARED ? 128 : 32;
-    const int64_t from = blockIdx.z * a.part_k, last = min(from + a.part_k, a.K), first = from + (SHARED ? 32 * wave : 0);
+    // Steps of 64 values of k, of which a lane takes 16 adjacent ones in two
+    // fragments (both operands alike, so their order is free): a row's loads are
+    // whole cache lines.
+    constexpr int kStep = SHARED ? 256 : 64;
+    const int64_t from = blockIdx.z * a.part_k, last = min(from + a.part_k, a.K), first = from + (SHARED ? 64 * wave : 0);
     for (int n = 0;; ++n) {
         int now = -1;
 #pragma unroll
@@ -123,7 +126,7 @@ __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a)
 #pragma unroll
             for (int b = 0; b < BLOCKS; ++b) {
                 const int rank = min(rank0 + 16 * b + l16, a.c.rank - 1);
-                cr[b] = c + (RANK_INNER ? 8 * quarter * a.c.ld + rank : rank * a.c.ld + 8 * quarter);
+                cr[b] = c + (RANK_INNER ? 16 * quarter * a.c.ld + rank : rank * a.c.ld + 16 * quarter);
             }
             auto step = [&](int64_t k, In (&vx)[ROWS][8], In (&vc)[BLOCKS][8], int64_t there) {
 #pragma unroll
@@ -144,20 +147,43 @@ __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a)
 #pragma unroll
                     for (int b = 0; b < BLOCKS; ++b) acc[i][b] = Step<In>::add(vc[b], vx[i], acc[i][b]);
             };
+            // two sets of steps: the loads of one are under way while the other is multiplied
             constexpr int kHeld = (ROWS + (RANK_INNER ? 4 : 1) * BLOCKS) * (sizeof(In) == 4 ? 2 : 1);
-            constexpr int U = kHeld <= 4 ? 4 : kHeld <= 8 ? 2 : 1;
+            constexpr int U = kHeld <= 3 ? 2 : 1;
+            In vx[2][2 * U][ROWS][8], vc[2][2 * U][BLOCKS][8];
+            auto load = [&](int set, int64_t k) {
+#pragma unroll
+                for (int u = 0; u < 2 * U; ++u) step(k + kStep * (u / 2) + 8 * (u % 2), vx[set][u], vc[set][u], 8);
+            };
+            auto use = [&](int set) {
+#pragma unroll
+                for (int u = 0; u < 2 * U; ++u) multiply(vx[set][u], vc[set][u]);
+            };
             int64_t k = first;
-            for (; k + kStep * (U - 1) + 32 <= last; k += kStep * U) {
-                In vx[U][ROWS][8], vc[U][BLOCKS][8];
-#pragma unroll
-                for (int u = 0; u < U; ++u) step(k + kStep * u, vx[u], vc[u], 8);
-#pragma unroll
-                for (int u = 0; u < U; ++u) multiply(vx[u], vc[u]);
+            auto whole = [&](int64_t k) { return k + kStep * (U - 1) + 64 <= last; };
+            if (whole(k)) {
+                load(0, k);
+                for (k += kStep * U; whole(k + kStep * U); k += 2 * kStep * U) {
+                    load(1, k);
+                    use(0);
+                    load(0, k + kStep * U);
+                    use(1);
+                }
+                if (whole(k)) {
+                    load(1, k);
+                    use(0);
+                    use(1);
+                    k += kStep * U;
+                } else {
+                    use(0);
+                }
             }
             for (; k < last; k += kStep) {
-                In vx[ROWS][8], vc[BLOCKS][8];
-                step(k, vx, vc, last - (k + 8 * quarter));
-                multiply(vx, vc);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    step(k + 8 * h, vx[0][h], vc[0][h], last - (k + 16 * quarter + 8 * h));
+                    multiply(vx[0][h], vc[0][h]);
+                }
             }
             if constexpr (SHARED) {
                 if (wave > 0) {

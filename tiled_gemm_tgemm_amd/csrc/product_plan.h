@@ -26,6 +26,7 @@ constexpr int64_t kMaxTiles = INT32_MAX - 1024;
 // 23 and 22; 4096×32768 with 8 steps 127, 162 and 275.
 struct Choice {
     int tile = 0, splits = 1;
+    double time = 0;
 };
 inline Choice choose_tile(int64_t M, int64_t N, int64_t steps, bool split = false)
 {
@@ -49,6 +50,7 @@ inline Choice choose_tile(int64_t M, int64_t N, int64_t steps, bool split = fals
                 least = time;
                 best.tile = i;
                 best.splits = (int)parts;
+                best.time = time;
             }
         }
     }
