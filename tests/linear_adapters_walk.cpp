@@ -158,6 +158,23 @@ hipError_t launch_shrink(const ShrinkArgs &a, hipStream_t)
     if (a.parts > 1 && (!a.part || a.planes)) fail("parts without room", 0, 0);
     if (!a.part && !a.planes) fail("hidden values for nobody", 0, 0);
     rows(a.rows, a.T, a.K, a.ld, size_of(a.dtype), false, "shrink's rows");
+    if (a.through_lds) {
+        if (a.dtype == TGEMM_F32 || a.K % 64 || a.ld % 8 || a.c.ld % 8 || a.c.stride % 8 || (uintptr_t)a.rows % 16 || (uintptr_t)a.c.p % 16 ||
+            a.c.rank_inner || a.rows_each != 64 || a.slots != 1 || a.ld > (1 << 22) || a.c.ld > (1 << 22))
+            fail("rows through LDS", 0, 0);
+        // the offsets of a part's steps, of the first and the last rows and ranks
+        typedef Slice<64, 1, 256, false, false> X;
+        typedef Slice<64, 4, 512, false, false> C;
+        for (int64_t part : {(int64_t)0, (int64_t)a.parts - 1}) {
+            const int64_t from = part * a.part_k, last = std::min(from + a.part_k, a.K);
+            for (int64_t k : {from, std::min(from + 64, last - 64), last - 64}) {
+                for (int64_t row0 : {(int64_t)0, (a.T - 1) / 64 * 64})
+                    slice<X>((const char *)a.rows + (row0 * a.ld + k) * 2, a.ld, (int)std::min<int64_t>(63, a.T - 1 - row0), 64, "X");
+                for (int64_t i : {(int64_t)0, (int64_t)a.c.count - 1})
+                    slice<C>((const char *)a.c.p + (i * a.c.stride + k) * 2, a.c.ld, a.c.rank - 1, 64, "adapters");
+            }
+        }
+    }
     stack(a.c, a.K, size_of(a.dtype), "shrink's adapters");
     rows(a.ids, a.T, 1, 1, 8, false, "ids");
     rows(a.scales, a.scales ? a.c.count : 0, 1, 1, 4, false, "scales");

@@ -22,6 +22,7 @@ struct Range {
 };
 std::vector<Range> ranges;
 long loads = 0;
+int64_t matrices = 0;  // of the call
 char line[256];
 
 void fail(const char *what, uintptr_t a, size_t n)
@@ -69,25 +70,40 @@ void walk(const Chain &p, int wg_per_cu)
     typedef Slice<BM, BM / WM / 16, 64 * WM * WN, A_MC, false> A;
     typedef Slice<BN, BN / WN / 16, 64 * WM * WN, B_MC, true> B;
     const int tiles = p.ids(), grid = std::min(tiles, 256 * wg_per_cu);
-    if (tiles <= 4096) {  // every tile of every matrix once
-        std::vector<int> seen((size_t)p.tiles_m * p.tiles_n * p.splits, 0);
+    if (tiles <= 4096) {  // every part of every tile of the launch once
+        std::vector<int> seen((size_t)tiles, 0), where((size_t)p.tiles_m * p.tiles_n, -1);
         for (int id = 0; id < tiles; ++id) {
             int m0, n0, split, first, last;
             p.tile<BM, BN>(id, m0, n0, split, first, last);
-            if (m0 % BM || n0 % BN || m0 / BM >= p.tiles_m || n0 / BN >= p.tiles_n || split < 0 || split >= p.splits || m0 < 0 || n0 < 0)
+            const int at = split - p.from * p.splits;
+            if (m0 % BM || n0 % BN || m0 / BM >= p.tiles_m || n0 / BN >= p.tiles_n || m0 < 0 || n0 < 0 || at < 0 || at >= tiles)
                 fail("a tile outside", 0, 0);
+            if (first >= last || first != split % p.splits * p.steps_per_split) fail("a tile's steps", 0, 0);
             if (p.lower && n0 > m0) fail("a tile above the diagonal", 0, 0);
-            ++seen[((size_t)split * p.tiles_m + m0 / BM) * p.tiles_n + n0 / BN];
+            ++seen[at];
+            // numbers and places of a matrix's tiles go together
+            int &place = where[(size_t)(m0 / BM) * p.tiles_n + n0 / BN];
+            const int number = split / p.splits % p.tiles();
+            if (place >= 0 && place != number) fail("a tile in two places", 0, 0);
+            place = number;
         }
-        for (size_t n = 0; n < seen.size(); ++n) {
-            const bool wanted = !p.lower || n % p.tiles_n <= n / p.tiles_n % p.tiles_m;
-            if (seen[n] != (wanted ? 1 : 0)) fail("a tile that is not taken once", n, seen[n]);
-        }
+        for (int n : seen)
+            if (n != 1) fail("a tile that is not taken once", 0, n);
+        std::vector<int> numbers;
+        for (int n : where)
+            if (n >= 0) numbers.push_back(n);
+        std::sort(numbers.begin(), numbers.end());
+        for (size_t n = 1; n < numbers.size(); ++n)
+            if (numbers[n] == numbers[n - 1]) fail("two tiles in a place", 0, 0);
     }
     for (int group : {0, 1, 7, 8, grid / 2, grid - 9, grid - 2, grid - 1}) {
         if (group < 0 || group >= grid) continue;
         int steps = 2;
-        for (int id = group; id < tiles; id += grid) steps += p.steps * p.segments;
+        for (int id = group; id < tiles; id += grid) {
+            int m0, n0, split, first, last;
+            p.tile<BM, BN>(id, m0, n0, split, first, last);
+            steps += (last - first) * p.segments;
+        }
         tgemm::m16::Walk<BM, BN, A_MC, B_MC, Chain> w;
         w.begin(p, group);
         int a_last = 0, a_k = 0, b_last = 0, b_k = 0;
@@ -107,25 +123,9 @@ void walk(const Chain &p, int wg_per_cu)
 namespace tgemm {
 namespace ortho {
 
-hipError_t launch_chain(Order order, int tile, const ChainArgs &a, hipStream_t)
+int64_t covered = 0;  // tiles of the product that is being launched
+void check_rest(const ChainArgs &a, int64_t batch)
 {
-    if (a.op.lower && (a.op.tiles_m != a.op.tiles_n || a.op.M != a.op.N)) fail("a triangle that is not square", 0, 0);
-    switch (tile) {
-#define X(I, BM, BN, WM, WN)                                                                                      \
-    case I:                                                                                                       \
-        if ((int64_t)a.op.tiles_m * BM < a.op.M || (int64_t)a.op.tiles_n * BN < a.op.N) fail("tiles", 0, 0);      \
-        if (a.planes && (int64_t)a.op.tiles_n * BN < a.ldo) fail("columns that no tile clears", 0, 0);            \
-        if (a.planes && !a.op.lower && (int64_t)a.op.tiles_m * BM < a.rows) fail("rows that no tile clears", 0, 0); \
-        if (order == kRows) walk<BM, BN, WM, WN, false, false>(a.op, kTiles[I].wg_per_cu);                        \
-        else if (order == kColumns) walk<BM, BN, WM, WN, true, true>(a.op, kTiles[I].wg_per_cu);                  \
-        else walk<BM, BN, WM, WN, false, true>(a.op, kTiles[I].wg_per_cu);                                        \
-        break;
-        TGEMM_CHAIN_TILES(X)
-#undef X
-    default:
-        fail("an unknown tile", 0, 0);
-    }
-    const int64_t batch = a.op.splits;
     if (a.add)
         for (int q = 0; q < 2; ++q)
             span((const char *)a.add + q * a.plane_add * 2, batch, a.batch_add, a.op.M, a.ld_add, a.ld_add, 2, false, "add");
@@ -136,6 +136,40 @@ hipError_t launch_chain(Order order, int tile, const ChainArgs &a, hipStream_t)
     } else {
         span(a.result, batch, a.batch_r, a.op.M, a.op.N, a.ldr, size_of(a.dtype), true, "result");
     }
+}
+hipError_t launch_chain(Order order, int tile, const ChainArgs &a, hipStream_t)
+{
+    if (a.op.lower && (a.op.tiles_m != a.op.tiles_n || a.op.M != a.op.N)) fail("a triangle that is not square", 0, 0);
+    const int64_t batch = (a.op.from + a.op.count - 1) / a.op.tiles() + 1;
+    if (a.op.from != covered) fail("tiles that were left out", 0, covered);
+    covered = a.op.from + a.op.count;
+    if (a.op.splits > 1 || covered == (int64_t)a.op.tiles() * matrices) {
+        if (covered != (int64_t)a.op.tiles() * matrices) fail("tiles that were left out", 0, covered);
+        covered = 0;
+    }
+    switch (tile) {
+#define X(I, BM, BN, WM, WN)                                                                                      \
+    case I:                                                                                                       \
+        if ((int64_t)a.op.tiles_m * BM < a.op.M || (int64_t)a.op.tiles_n * BN < a.op.N) fail("tiles", 0, 0);      \
+        if (a.planes && (int64_t)a.op.tiles_n * BN < a.ldo) fail("columns that no tile clears", 0, 0);            \
+        if (a.planes && !a.op.lower && (int64_t)a.op.tiles_m * BM < a.rows) fail("rows that no tile clears", 0, 0); \
+        if (order == kRows) walk<BM, BN, WM, WN, false, false>(a.op, kTiles[I].wg_per_cu);                        \
+        else if (order == kColumns) walk<BM, BN, WM, WN, true, true>(a.op, kTiles[I].wg_per_cu);                  \
+        else walk<BM, BN, WM, WN, false, true>(a.op, kTiles[I].wg_per_cu);                                        \
+        if (a.op.splits > 1) touch(a.parts, (size_t)a.op.count * a.op.splits * BM * BN * 4, true, "parts");       \
+        break;
+        TGEMM_CHAIN_TILES(X)
+#undef X
+    default:
+        fail("an unknown tile", 0, 0);
+    }
+    if (a.op.splits == 1) check_rest(a, batch);
+    return hipSuccess;
+}
+hipError_t launch_join(int, const ChainArgs &a, hipStream_t)
+{
+    if (a.op.splits < 2) fail("a join of nothing", 0, 0);
+    check_rest(a, (a.op.from + a.op.count - 1) / a.op.tiles() + 1);
     return hipSuccess;
 }
 
@@ -190,6 +224,7 @@ int main()
         if (std::sscanf(line, "%d %lld %lld %lld %d %lld %lld %lld %lld %lld", &dtype, &batch, &M, &N, &steps, &ldg, &sg, &shift, &ldo, &so) != 10) return 2;
         const tgemm_dtype_t t = (tgemm_dtype_t)dtype;
         const size_t size = size_of(t);
+        matrices = batch;
         const uintptr_t G = 0x100000000000ull + shift * size, O = 0x300000000000ull, W = 0x500000000000ull;
         const size_t ws = tgemm_orthogonalize_workspace_size(t, batch, M, N, steps);
         ranges = {{G, G + ((batch - 1) * sg + (M - 1) * ldg + N) * size, false, "G"},

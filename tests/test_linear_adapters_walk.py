@@ -62,5 +62,6 @@ def test_no_rows(walker):
 
 def test_large_sizes(walker):
     sizes = [(1, 4096, 4096, 8, 16), (48, 8192, 2048, 32, 16), (8192, 16384, 4096, 8, 32), (8192, 64, 16384, 1, 1024), (65, 200000, 64, 4, 4),
-             (100000, 300, 64, 32767, 1), (131100, 300, 64, 32767, 1), (20000, 5000, 1000, 1000, 16), (513, 72, 1 << 18, 2, 128)]
+             (100000, 300, 64, 32767, 1), (131100, 300, 64, 32767, 1), (20000, 5000, 1000, 1000, 16), (513, 72, 1 << 18, 2, 128),
+             (2048, 1024, 1024, 2, 8), (4100, 320, 448, 3, 40), (1025, 64, 64, 1, 16)]
     follow(walker, [call(need, dtype, *s) for need in (0, 15) for dtype in (0, 1) for s in sizes])

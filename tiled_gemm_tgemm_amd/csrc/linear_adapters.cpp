@@ -79,20 +79,33 @@ bool as_stored(tgemm_dtype_t dtype, const void *p, int64_t ld, int64_t cols, int
     return dtype != TGEMM_F32 && cols % whole == 0 && ld % 8 == 0 && ld <= kMaxSide && reinterpret_cast<uintptr_t>(p) % 16 == 0;
 }
 
+Stack stack_a(const Layer &l) { return Stack{l.A, l.lda, l.stride_a, false, (int)l.count, (int)l.rank}; }
+Stack stack_b(const Layer &l) { return Stack{l.B, l.ldb, l.stride_b, true, (int)l.count, (int)l.rank}; }
+
+// Whether the rows and the adapters' sums over them go through LDS as they lie.
+bool along_k(const Layer &l, const void *rows, int64_t ld, int64_t K, const Stack &c)
+{
+    return as_stored(l.dtype, rows, ld, K, kStepK) && !c.rank_inner && c.ld % 8 == 0 && c.ld <= kMaxSide && c.stride % 8 == 0 &&
+           reinterpret_cast<uintptr_t>(c.p) % 16 == 0;
+}
+
 // How the sums over K of the tokens' hidden values are cut: in parts while there
 // are fewer wavefronts than keep the memory busy.
 struct Shrink {
     int64_t part_k = 0;
     int parts = 1, slots = 1, rows_each = 16;
+    bool through_lds = false;
 };
-Shrink shrink_of(int64_t T, int64_t K, int64_t count)
+Shrink shrink_of(int64_t T, int64_t K, int64_t count, bool through_lds)
 {
     Shrink s;
-    s.rows_each = T <= 1024 ? 16 : T < 4096 ? 64 : 128;
-    const int64_t wavefronts = 4 * ceil_div(T, s.rows_each);
+    s.through_lds = through_lds && T > 1024;
+    s.rows_each = T <= 1024 ? 16 : T < 4096 || s.through_lds ? 64 : 128;
+    // (the workspace does not depend on how the adapters lie)
+    const int64_t wavefronts = 4 * ceil_div(T, T <= 1024 ? 16 : T < 4096 ? 64 : 128), most = T <= 1024 ? 8 : 16;
     int64_t parts = 4096 / wavefronts;
     if (parts > ceil_div(K, 512)) parts = ceil_div(K, 512);
-    if (parts > (T <= 1024 ? 8 : 16)) parts = T <= 1024 ? 8 : 16;
+    if (parts > most) parts = most;
     if (parts < 1) parts = 1;
     s.part_k = round_up(ceil_div(K, parts), 256);
     s.parts = (int)ceil_div(K, s.part_k);
@@ -173,7 +186,7 @@ bool plan_forward(Plan &p, const Layer &l)
 {
     plan_types(p, l);
     p.few = l.T <= kFewRows;
-    p.shrink = shrink_of(l.T, l.D, l.count);
+    p.shrink = shrink_of(l.T, l.D, l.count, along_k(l, l.X, l.ldx, l.D, stack_a(l)));
     if (p.few || p.shrink.parts > 1) p.parts = p.take(p.shrink.parts * l.T * l.rank * 4);
     if (p.few) return true;
     p.hidden_planes = p.take(planes_bytes(l));
@@ -230,13 +243,15 @@ bool plan_backward(Plan &p, const Layer &l, const void *dY, int64_t lddy, Need n
         if (need.x) p.turned_a = p.take(l.count * l.D * round_up(l.rank, 8) * (int64_t)size_of(l.dtype));
     }
     if (need.x || need.a) {
-        p.shrink = shrink_of(l.T, l.N, l.count);
+        // (turned, B lies along the sum)
+        const Stack b{nullptr, round_up(l.N, 8), 0, false, (int)l.count, (int)l.rank};
+        p.shrink = shrink_of(l.T, l.N, l.count, p.turned_b >= 0 && along_k(l, dY, lddy, l.N, b));
         if (p.shrink.parts > 1) p.parts = p.take(p.shrink.parts * l.T * l.rank * 4);
         if (need.a) p.u = p.take(l.T * l.rank * 4);
         if (need.x) p.hidden_planes = p.take(planes_bytes(l));
     }
     if (need.b && !have_hidden) {
-        p.shrink_x = shrink_of(l.T, l.D, l.count);
+        p.shrink_x = shrink_of(l.T, l.D, l.count, along_k(l, l.X, l.ldx, l.D, stack_a(l)));
         if (p.shrink_x.parts > 1) p.parts_x = p.take(p.shrink_x.parts * l.T * l.rank * 4);
         p.hidden = p.take(l.T * l.rank * 4);
     }
@@ -307,6 +322,7 @@ ShrinkArgs shrink_args(const Layer &l, const Shrink &s, const void *rows, int64_
     a.parts = s.parts;
     a.slots = s.slots;
     a.rows_each = s.rows_each;
+    a.through_lds = s.through_lds;
     return a;
 }
 
@@ -322,9 +338,6 @@ hipError_t make_hidden(ShrinkArgs a, float *parts, float *hidden, void *planes, 
     const hipError_t e = launch_shrink(a, stream);
     return e != hipSuccess ? e : launch_finish(a, hidden, planes, stream);
 }
-
-Stack stack_a(const Layer &l) { return Stack{l.A, l.lda, l.stride_a, false, (int)l.count, (int)l.rank}; }
-Stack stack_b(const Layer &l) { return Stack{l.B, l.ldb, l.stride_b, true, (int)l.count, (int)l.rank}; }
 
 // The product on the tiles with its adapters' part.
 hipError_t run_product(const Plan &p, const Layer &l, ProductArgs a, bool b_mc, int64_t steps, int64_t ld_part, void *out,

@@ -46,6 +46,9 @@ struct ShrinkArgs {
     int64_t part_k;  // values of k a part, a multiple of 256
     int parts, slots;
     int rows_each;   // 16: a work-group's wavefronts share 16 rows' sums; 64, 128: they take 16, 32 rows each
+    // 16-bit rows and adapters 16-byte aligned, K in whole 64s, leading dimensions
+    // below 2^22, the ranks not the inner ones, rows_each 64 and slots 1
+    bool through_lds;
 };
 hipError_t launch_shrink(const ShrinkArgs &a, hipStream_t stream);
 // Adds the parts up to `hidden` and `planes` (either may be NULL), for every row whose id is in range.

@@ -301,73 +301,66 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 32 ? 3 : 2) void adapted_kernel
     });
 }
 
-// The sum over parts and the adapters' part, four columns a thread: a wavefront
-// has 256 columns of a row.  (In the tiles of a split sum, which are few and
-// short, the adapters' loads would be waited for: 256×4096×4096 with 32 adapters
-// 49 µs and 5 for the sum.)
+// The sum over parts and the adapters' part, four columns a thread, 64 apart, so
+// that a wavefront's loads of an adapter lie side by side.  (In the tiles of a
+// split sum, which are few and short, the adapters' loads would be waited for:
+// 256×4096×4096 with 32 adapters 49 µs and 5 for the sum, against 22 and 13.)
 template <class C, bool RANK_INNER>
 __global__ __launch_bounds__(256) void adapted_sum_kernel(AddArgs a)
 {
     typedef typename std::conditional<sizeof(C) == 4, float, __bf16>::type P;
-    const int64_t per_row = (a.N + 255) / 256 * 64, total = a.T * per_row;
-    const int padded = (int)planes_rank(a.e.c.rank);
-    for (int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x; p < total; p += (int64_t)gridDim.x * 256) {
-        const int64_t row = p / per_row, col = p % per_row * 4, left = a.N - col;
-        if (left <= 0) continue;
+    const int64_t per_row = (a.N + 255) / 256, total = a.T * per_row;
+    const int padded = (int)planes_rank(a.e.c.rank), lane = threadIdx.x & 63;
+    for (int64_t p = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); p < total; p += (int64_t)gridDim.x * 4) {
+        const int64_t row = p / per_row, col0 = p % per_row * 256 + lane;
+        // columns past the last are read from it and not stored
+        int64_t col[4];
         float v[4];
-        load_some<float, 4>(a.part + row * a.ld + col, left, v);
-        for (int s = 1; s < a.count; s += 8) {  // eight parts on their way at once
-            float next[8][4];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) load_some<float, 4>(a.part + row * a.ld + col + (s + u) * a.stride, s + u < a.count ? left : 0, next[u]);
+        for (int x = 0; x < 4; ++x) {
+            col[x] = min(col0 + 64 * x, a.N - 1);
+            v[x] = a.part[row * a.ld + col[x]];
+        }
+        for (int s = 1; s < a.count; s += 4) {  // four parts on their way at once
+            float next[4][4];
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
+            for (int u = 0; u < 4; ++u)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] += next[u][e];
+                for (int x = 0; x < 4; ++x) next[u][x] = s + u < a.count ? a.part[row * a.ld + col[x] + (s + u) * a.stride] : 0.0f;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) v[x] += next[u][x];
         }
         const int id = id_of(a.e, row, a.T);
         if (id >= 0) {
             const C *c = (const C *)a.e.c.p + id * a.e.c.stride;
-            if constexpr (RANK_INNER) {
-                for (int k = 0; k < a.e.c.rank; k += 8) {
-                    C w[4][8];
-                    float h[8];
-                    eight_hidden((const P *)a.e.planes, row, k, padded, h);
+            for (int k = 0; k < a.e.c.rank; k += 8) {
+                float h[8];
+                eight_hidden((const P *)a.e.planes, row, k, padded, h);
+                C w[4][8];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) load_some<C, 8>(c + (col + (x < left ? x : 0)) * a.e.c.ld + k, a.e.c.rank - k, w[x]);
+                for (int x = 0; x < 4; ++x) {
+                    if constexpr (RANK_INNER) {
+                        load_some<C, 8>(c + col[x] * a.e.c.ld + k, a.e.c.rank - k, w[x]);
+                    } else {
 #pragma unroll
-                    for (int n = 0; n < 8; ++n)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) v[x] = fmaf(h[n], (float)w[x][n], v[x]);
+                        for (int n = 0; n < 8; ++n) w[x][n] = k + n < a.e.c.rank ? c[(k + n) * a.e.c.ld + col[x]] : (C)0.0f;
+                    }
                 }
-            } else {
-                for (int k = 0; k < a.e.c.rank; k += 8) {
-                    C w[8][4];
-                    float h[8];
-                    eight_hidden((const P *)a.e.planes, row, k, padded, h);
 #pragma unroll
-                    for (int n = 0; n < 8; ++n) load_some<C, 4>(c + (k + n) * a.e.c.ld + col, k + n < a.e.c.rank ? left : 0, w[n]);
+                for (int n = 0; n < 8; ++n)
 #pragma unroll
-                    for (int n = 0; n < 8; ++n)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) v[x] = fmaf(h[n], (float)w[n][x], v[x]);
-                }
+                    for (int x = 0; x < 4; ++x) v[x] = fmaf(h[n], (float)w[x][n], v[x]);
             }
         } else if (id == -2) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) v[x] = NAN;
         }
-        C *to = (C *)a.out + row * a.ldo + col;
-        if (left >= 4) {
-            typename m16::Some<C, 4>::type w;
+        C *to = (C *)a.out + row * a.ldo;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) w[x] = (C)v[x];
-            *(typename m16::Some<C, 4>::type *)to = w;
-        } else {
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                if (x < left) to[x] = (C)v[x];
-        }
+        for (int x = 0; x < 4; ++x)
+            if (col0 + 64 * x < a.N) to[col0 + 64 * x] = (C)v[x];
     }
 }
 
@@ -559,7 +552,7 @@ hipError_t launch_product(bool half, bool b_mc, int tile, const ProductArgs &a, 
 
 hipError_t launch_add(const AddArgs &a, hipStream_t stream)
 {
-    const int64_t blocks = (a.T * ((a.N + 255) / 256 * 64) + 255) / 256;
+    const int64_t blocks = (a.T * ((a.N + 255) / 256) + 3) / 4;
     const unsigned grid = (unsigned)(blocks < (1 << 20) ? blocks : 1 << 20);
     const bool inner = a.e.c.rank_inner;
     if (a.dtype == TGEMM_F32) {

@@ -219,6 +219,105 @@ __global__ __launch_bounds__(256) void shrink_kernel(ShrinkArgs a)
     }
 }
 
+// The same for many rows of 16-bit values, 16-byte aligned and of whole steps of
+// 64, with adapters that lie along the sum: a work-group takes 64 rows and goes
+// through LDS, 128 values of k at a time in one of two stages, which makes the
+// rows' loads 256 adjacent bytes, and an adapter is read once for 64 rows.  Bound by
+// reading the rows once.  (8192 rows of 16384 with 32 ranks straight from device
+// memory, where 16 rows that lie a power of two apart meet in few of the memory's channels,
+// 115 µs.)
+template <class In, int BLOCKS>
+__global__ __launch_bounds__(256) void shrink_rows_kernel(ShrinkArgs a)
+{
+    typedef m16::Slice<64, 1, 256, false, false> SliceX;
+    typedef m16::Slice<16 * BLOCKS, BLOCKS, 128 * BLOCKS, false, false> SliceC;  // one round a half
+    constexpr int kHalf = SliceX::kBytes, kHalfC = SliceC::kBytes, kStage = 2 * kHalf + 2 * kHalfC;
+    static_assert(SliceX::kRounds == 2 && SliceC::kRounds == 1, "rounds");
+    __shared__ __align__(1024) char lds[2 * kStage];
+    const int thread = threadIdx.x, lane = thread & 63, wave = __builtin_amdgcn_readfirstlane(thread >> 6);
+    const int l16 = lane & 15, quarter = lane >> 4;
+    const int64_t row0 = (int64_t)blockIdx.x * 64;
+    // every wavefront goes through the adapters of all 64 rows
+    int all = -1;
+    if (row0 + lane < a.T) {
+        const int64_t n = a.ids[row0 + lane];
+        if (n >= 0 && n < a.c.count) all = (int)n;
+    }
+    const int id = __shfl(all, wave * 16 + l16);
+    const int64_t row = row0 + wave * 16 + l16, from = blockIdx.z * a.part_k, last = min(from + a.part_k, a.K);
+    const int last_row = (int)min((int64_t)63, a.T - 1 - row0);
+    const char *x = (const char *)((const In *)a.rows + row0 * a.ld);
+    m16::Reader<64, 1, false, false> rx;
+    m16::Reader<16 * BLOCKS, BLOCKS, false, false> rc;
+    rx.place(wave * 16, lane);
+    rc.place(0, lane);
+    uint64_t left = __ballot(all >= 0);
+    while (left != 0) {
+        const int now = __builtin_amdgcn_readlane(all, __builtin_ctzll(left));
+        left &= ~__ballot(all == now);
+        const bool here = __ballot(id == now) != 0;
+        for (int rank0 = 0; rank0 < (a.planes != nullptr ? (int)planes_rank(a.c.rank) : a.c.rank); rank0 += 16 * BLOCKS) {
+            const int first_rank = min(rank0, a.c.rank - 1), last_rank = a.c.rank - 1 - first_rank;
+            const char *c = (const char *)((const In *)a.c.p + now * a.c.stride + first_rank * a.c.ld);
+            auto issue = [&](int stage, int64_t k) {
+                m16::lds_char *to = (m16::lds_char *)lds + stage * kStage;
+                const int64_t half[2] = {k, min(k + 64, last - 64)};  // past the end the last stands in, for nobody
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        m16::load_lds(x + half[h] * 2, SliceX::offset(r * 256 + thread, a.ld, last_row, 64), to + h * kHalf + (r * 256 + wave * 64) * 16);
+#pragma unroll
+                for (int r = 0; r < BLOCKS; ++r) {
+                    const int position = r * 256 + thread, h = position / (128 * BLOCKS);
+                    m16::load_lds(c, SliceC::offset(position % (128 * BLOCKS), a.c.ld, last_rank, 64) + (uint32_t)half[h] * 2,
+                                  to + 2 * kHalf + (r * 256 + wave * 64) * 16);
+                }
+            };
+            f32x4 acc[BLOCKS];
+#pragma unroll
+            for (int b = 0; b < BLOCKS; ++b) acc[b] = f32x4{0, 0, 0, 0};
+            issue(0, from);
+            if (from + 128 < last) issue(1, from + 128);
+            int stage = 0;
+            for (int64_t k = from; k < last; k += 128) {
+                if (k + 128 < last) m16::arrive<4 + BLOCKS>();
+                else m16::arrive<0>();
+                m16::lds_char *at = (m16::lds_char *)lds + stage * kStage;
+                if (here) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (h == 1 && k + 64 >= last) continue;
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            const typename Frag<In>::type fx = rx.template read<In>(at + h * kHalf, 0, s);
+#pragma unroll
+                            for (int b = 0; b < BLOCKS; ++b)
+                                acc[b] = Frag<In>::mfma(rc.template read<In>(at + 2 * kHalf + h * kHalfC, b, s), fx, acc[b]);
+                        }
+                    }
+                }
+                __syncthreads();
+                if (k + 256 < last) issue(stage, k + 256);
+                stage ^= 1;
+            }
+            if (id != now) continue;
+            const float factor = a.scales != nullptr ? a.scales[now] : 1.0f;
+#pragma unroll
+            for (int b = 0; b < BLOCKS; ++b) {
+                const int rank = rank0 + 16 * b + 4 * quarter;
+                if (a.part != nullptr) {
+                    float *to = a.part + ((int64_t)blockIdx.z * a.T + row) * a.c.rank + rank;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (rank + r < a.c.rank) to[r] = acc[b][r];
+                }
+                if (a.planes != nullptr) put_planes<false>(a.planes, row, rank, a.c.rank, acc[b], factor);
+            }
+        }
+    }
+}
+
 template <bool WHOLE>
 __global__ __launch_bounds__(256) void finish_kernel(ShrinkArgs a, float *hidden, void *planes)
 {
@@ -247,6 +346,12 @@ template <class In, int BLOCKS>
 void shrink(const ShrinkArgs &a, hipStream_t stream)
 {
     const dim3 grid((unsigned)((a.T + a.rows_each - 1) / a.rows_each), a.slots, a.parts);
+    if constexpr (sizeof(In) == 2) {
+        if (a.through_lds) {
+            shrink_rows_kernel<In, BLOCKS><<<grid, 256, 0, stream>>>(a);
+            return;
+        }
+    }
     if (a.rows_each == 16) {
         if (a.c.rank_inner) shrink_kernel<In, BLOCKS, 1, true, true><<<grid, 256, 0, stream>>>(a);
         else shrink_kernel<In, BLOCKS, 1, false, true><<<grid, 256, 0, stream>>>(a);

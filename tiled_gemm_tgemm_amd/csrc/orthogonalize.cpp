@@ -43,34 +43,62 @@ Segments segments_of(tgemm_dtype_t dtype, int step)
     return Segments{3, 3, 3};
 }
 
-// The tile for `batch` M×N products of `steps` steps, and whether only the
-// tiles on and below the diagonal are formed: the least estimated time, in µs.
+// The tile for `batch` M×N products of `steps` steps (of `segments` each),
+// whether only the tiles on and below the diagonal are formed, and into how many
+// parts the sums of the tiles are split that do not fill the GPU a last time:
+// the least estimated time, in µs.
+//
+// A compute unit that holds 1 ... 4 tiles takes kStep for a step of all of them
+// and kBegin for what comes before and after, most of which is the planes' way;
+// across the diagonal a tile's takes kAcross more.  The whole GPU multiplies no
+// more than 1.3 PFLOP/s, and runs the faster the less of it is at work (a tenth
+// of the time at that rate is added).  Parts are written and read once more, by another
+// launch.  Measured (µs; tiles of 256, 128 and 64): S and Q of 256×1024 with 16
+// and 12 steps 31 and 33, 16 and 16, 11 and 10; Q of 2048×2048, 96 steps, 135,
+// 66 and 56; of 4096×4096, 192 steps, 268 below the diagonal and 341, 288 and
+// 406; S of 3000×1000, 141 steps, 128 and below the diagonal 91, in 7 parts 34.
 struct Choice {
     int tile = -1;
     bool lower = false;
+    int whole = 0, rest = 0, splits = 1;  // tiles in whole sums, and those in parts
 };
-Choice choose(int64_t M, int64_t N, int64_t steps, int64_t batch, bool symmetric)
+constexpr double kStep[kTileCount][4] = {{1.2}, {0.57, 0.95}, {0.33, 0.45, 0.62, 0.8}};
+constexpr double kBegin[kTileCount] = {22.0, 10.0, 6.5}, kBeginPart[kTileCount] = {15.0, 8.0, 5.0}, kAcross[kTileCount] = {8.0, 1.5, 0.7};
+Choice choose(int64_t M, int64_t N, int64_t steps, int segments, int64_t batch, bool symmetric)
 {
-    static const double rate[] = {1.0, 0.83, 0.45}, across[] = {12.0, 6.0, 2.0};
     Choice best;
     double least = -1;
     for (int i = 0; i < kTileCount; ++i) {
         const TileShape &s = kTiles[i];
         const int64_t m = ceil_div(M, s.side), n = ceil_div(N, s.side);
         for (int lower = 0; lower <= (symmetric ? 1 : 0); ++lower) {
-            const int64_t tiles = (lower ? m * (m + 1) / 2 : m * n);
-            if (tiles > kMaxTiles / batch) continue;
-            const int64_t on_one = ceil_div(tiles * batch, 256);
-            auto round = [&](int64_t held) {
-                const double step = (double)held * s.side * s.side / 65536.0 / rate[i] * 1.5;
-                return (double)steps * (step > 0.5 ? step : 0.5) + 4.0 + (lower ? across[i] : 0.0);
+            if (m * n > kMaxTiles / batch / 64) continue;
+            const int64_t tiles = (lower ? m * (m + 1) / 2 : m * n) * batch, most = (int64_t)256 * s.wg_per_cu;
+            auto rounds = [&](int64_t tiles, int64_t steps, double begin) {
+                const int64_t on_one = ceil_div(tiles, 256), rest = on_one % s.wg_per_cu;
+                auto round = [&](int64_t held) { return (double)(steps * segments) * kStep[i][held - 1] + begin; };
+                const double time = (double)(on_one / s.wg_per_cu) * round(s.wg_per_cu) + (rest ? round(rest) : 0.0);
+                const double area = (double)(tiles * s.side) * s.side;
+                const double power = area * (double)(steps * segments * kStepK) * 2.0 / 1.3e9 + begin;
+                return tiles == 0 ? 0.0 : (time > power ? time : power) + 0.1 * power;
             };
-            double time = (double)(on_one / s.wg_per_cu) * round(s.wg_per_cu);
-            if (on_one % s.wg_per_cu != 0) time += round(on_one % s.wg_per_cu);
-            if (least < 0 || time < least) {
-                least = time;
-                best.tile = i;
-                best.lower = lower != 0;
+            for (int64_t whole : {tiles, tiles / most * most}) {
+                const int64_t rest = tiles - whole;
+                for (int64_t parts = rest ? 2 : 1; parts == 1 || (parts <= 32 && parts <= steps); ++parts) {
+                    double time = rounds(whole, steps, kBegin[i] + (lower ? kAcross[i] : 0.0));
+                    if (rest)
+                        time += rounds(rest * parts, ceil_div(steps, parts), kBeginPart[i]) + (whole ? 9.0 : 6.0) +
+                                (double)(rest * parts * s.side * s.side) * 8.0 / 4e6;
+                    if (least < 0 || time < least) {
+                        least = time;
+                        best.tile = i;
+                        best.lower = lower != 0;
+                        best.whole = (int)whole;
+                        best.rest = (int)rest;
+                        best.splits = (int)ceil_div(steps, ceil_div(steps, parts));
+                    }
+                    if (rest == 0) break;
+                }
             }
         }
     }
@@ -86,7 +114,7 @@ struct Plan {
     // the chain
     int parts = 0;
     int64_t x_rows = 0, x_ld = 0;
-    int64_t squares = -1, x[2] = {-1, -1}, s = -1, q = -1;
+    int64_t squares = -1, x[2] = {-1, -1}, s = -1, q = -1, parts_room = -1;
     // the small side's
     int64_t part_length = 0, grams = -1, factor = -1;
 
@@ -98,6 +126,20 @@ struct Plan {
     }
 };
 
+int64_t parts_bytes(const Choice &c) { return (int64_t)c.rest * c.splits * kTiles[c.tile].side * kTiles[c.tile].side * 4; }
+
+// The choices for a step's three products.
+struct Choices {
+    Choice s, q, x;
+};
+Choices choices(const Plan &p, const Stack &g, int step)
+{
+    const Segments n = segments_of(g.dtype, step);
+    return Choices{choose(p.side, p.side, p.length_p / kStepK, n.s, g.batch, true),
+                   choose(p.side, p.side, p.side_p / kStepK, n.q, g.batch, true),
+                   choose(g.M, g.N, p.side_p / kStepK, n.x, g.batch, false)};
+}
+
 bool make_plan(Plan &p, const Stack &g)
 {
     p.tall = g.M > g.N;
@@ -107,7 +149,7 @@ bool make_plan(Plan &p, const Stack &g)
     p.length_p = round_up(p.length, kStepK);
     p.small = p.side <= kSmallSide;
     if (p.small) {
-        const int64_t blocks = blocks_of((int)p.side), most = blocks == 4 ? 16 : 32;
+        const int64_t blocks = blocks_of((int)p.side), most = 16;
         p.part_length = round_up(ceil_div(p.length, most), 128);
         if (p.part_length < 256) p.part_length = 256;
         p.parts = (int)ceil_div(p.length, p.part_length);
@@ -126,7 +168,16 @@ bool make_plan(Plan &p, const Stack &g)
     if (g.steps > 1) p.x[1] = p.take(x);
     p.s = p.take(s);
     p.q = p.take(s);
-    return choose(p.side, p.side, 1, g.batch, false).tile >= 0 && choose(g.M, g.N, 1, g.batch, false).tile >= 0;
+    int64_t room = 0;
+    for (int step = 0; step < g.steps && step < 3; ++step) {  // no further kinds of steps
+        const Choices c = choices(p, g, step);
+        for (const Choice *one : {&c.s, &c.q, &c.x}) {
+            if (one->tile < 0) return false;
+            if (parts_bytes(*one) > room) room = parts_bytes(*one);
+        }
+    }
+    p.parts_room = p.take(room);
+    return true;
 }
 
 tgemm_status_t check(const Stack &g, float eps)
@@ -138,18 +189,36 @@ tgemm_status_t check(const Stack &g, float eps)
     return TGEMM_SUCCESS;
 }
 
-Chain product(int64_t M, int64_t N, int64_t steps, int segments, int64_t batch, Choice c)
+Chain product(int64_t M, int64_t N, int64_t steps, int segments, const Choice &c)
 {
     Chain o{};
     o.segments = segments;
     o.M = (int)M;
     o.N = (int)N;
-    o.steps = o.steps_per_split = (int)steps;
+    o.steps = (int)steps;
     o.tiles_m = (int)ceil_div(M, kTiles[c.tile].side);
     o.tiles_n = (int)ceil_div(N, kTiles[c.tile].side);
-    o.splits = (int)batch;
     o.lower = c.lower;
     return o;
+}
+
+// The tiles with whole sums, then those in parts.
+hipError_t run(Order order, const Choice &c, ChainArgs a, hipStream_t stream)
+{
+    hipError_t e = hipSuccess;
+    if (c.whole > 0) {
+        a.op.count = c.whole;
+        a.op.splits = 1;
+        a.op.steps_per_split = a.op.steps;
+        e = launch_chain(order, c.tile, a, stream);
+    }
+    if (e != hipSuccess || c.rest == 0) return e;
+    a.op.from = c.whole;
+    a.op.count = c.rest;
+    a.op.splits = c.splits;
+    a.op.steps_per_split = (int)ceil_div(a.op.steps, c.splits);
+    e = launch_chain(order, c.tile, a, stream);
+    return e != hipSuccess ? e : launch_join(c.tile, a, stream);
 }
 
 tgemm_status_t run_small(const Plan &p, const Stack &g, const void *G, int64_t ldg, int64_t batch_g, const float *coefficients,
@@ -212,9 +281,10 @@ tgemm_status_t run_chain(const Plan &p, const Stack &g, const void *G, int64_t l
         void *x = in<void>(ws, p.x[step & 1]);
 
         const int64_t s_steps = p.length_p / kStepK, q_steps = p.side_p / kStepK;
-        Choice tile = choose(p.side, p.side, s_steps * n.s, g.batch, true);
+        const Choices c = choices(p, g, step);
         ChainArgs a{};
-        a.op = product(p.side, p.side, s_steps, n.s, g.batch, tile);
+        a.parts = in<float>(ws, p.parts_room);
+        a.op = product(p.side, p.side, s_steps, n.s, c.s);
         a.op.A = a.op.B = x;
         a.op.lda = a.op.ldb = p.x_ld;
         a.op.plane_a = a.op.plane_b = x_plane;
@@ -227,11 +297,10 @@ tgemm_status_t run_chain(const Plan &p, const Stack &g, const void *G, int64_t l
         a.plane_out = s_plane;
         a.batch_out = 2 * s_plane;
         a.rows = (int)p.side;
-        e = launch_chain(p.tall ? kColumns : kRows, tile.tile, a, stream);
+        e = run(p.tall ? kColumns : kRows, c.s, a, stream);
         if (e != hipSuccess) return from_hip(e);
 
-        tile = choose(p.side, p.side, q_steps * n.q, g.batch, true);
-        a.op = product(p.side, p.side, q_steps, n.q, g.batch, tile);
+        a.op = product(p.side, p.side, q_steps, n.q, c.q);
         a.op.A = a.op.B = s;
         a.op.lda = a.op.ldb = p.side_p;
         a.op.plane_a = a.op.plane_b = s_plane;
@@ -244,12 +313,14 @@ tgemm_status_t run_chain(const Plan &p, const Stack &g, const void *G, int64_t l
         a.batch_add = 2 * s_plane;
         a.alpha = k[1];
         a.beta = k[2] * one;
+        // three products of planes hold as much of a·X as its planes do
+        const bool folded = n.x == 3;
+        a.diagonal = folded ? k[0] * (1 << kShift) : 0.0f;
         a.planes = q;
-        e = launch_chain(kRows, tile.tile, a, stream);
+        e = run(kRows, c.q, a, stream);
         if (e != hipSuccess) return from_hip(e);
 
-        tile = choose(g.M, g.N, q_steps * n.x, g.batch, false);
-        a.op = product(g.M, g.N, q_steps, n.x, g.batch, tile);
+        a.op = product(g.M, g.N, q_steps, n.x, c.x);
         a.op.A = p.tall ? x : q;
         a.op.lda = p.tall ? p.x_ld : p.side_p;
         a.op.plane_a = p.tall ? x_plane : s_plane;
@@ -262,7 +333,8 @@ tgemm_status_t run_chain(const Plan &p, const Stack &g, const void *G, int64_t l
         a.op.batch_b = 2 * a.op.plane_b;
         a.op.mn_b = (int)(p.tall ? p.side : p.x_ld);
         a.op.k_b = (int)(p.tall ? p.side_p : p.side);
-        a.add = x;
+        a.diagonal = 0.0f;
+        a.add = folded ? nullptr : x;
         a.ld_add = p.x_ld;
         a.plane_add = x_plane;
         a.batch_add = 2 * x_plane;
@@ -281,7 +353,7 @@ tgemm_status_t run_chain(const Plan &p, const Stack &g, const void *G, int64_t l
             a.batch_r = batch_o;
             a.dtype = g.dtype;
         }
-        e = launch_chain(p.tall ? kRows : kMixed, tile.tile, a, stream);
+        e = run(p.tall ? kRows : kMixed, c.x, a, stream);
         if (e != hipSuccess) return from_hip(e);
     }
     return TGEMM_SUCCESS;

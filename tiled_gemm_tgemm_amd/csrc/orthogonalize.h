@@ -22,58 +22,69 @@ namespace ortho {
 // this leaves a factor of 30 before they overflow.
 constexpr int kShift = 10;
 
-// Operands of one of a batch of products: part y is matrix y.  Two planes an
-// operand; three segments are (low, high), (high, low), (high, high), one is
-// (high, high).  lower: tiles on and below the diagonal only (square tiles).
+// Operands of a batch of products.  Two planes an operand; three segments are
+// (low, high), (high, low), (high, high), one is (high, high).  lower: tiles on
+// and below the diagonal only (square tiles).  The batch's tiles, matrix by
+// matrix, are numbered through; a launch takes `count` of them from `from` on,
+// each with its sum in `splits` parts.  What the epilogue is told as the part
+// is the tile's number times splits and its part.
 struct Chain : m16::Operands {
     int64_t batch_a, batch_b;  // elements between the matrices
     bool lower;
+    int from, count;
 
     TGEMM_BOTH int tiles() const { return lower ? tiles_m * (tiles_m + 1) / 2 : tiles_m * tiles_n; }
-    TGEMM_BOTH int ids() const { return tiles() * splits; }
-    template <int BM, int BN>
-    TGEMM_BOTH void tile(int id, int &m0, int &n0, int &split, int &first, int &last) const
+    TGEMM_BOTH int ids() const { return count * splits; }
+    // the row and column of tile `at` of a matrix
+    TGEMM_BOTH void spot(int at, int &tm, int &tn) const
     {
-        const int logical = m16::deal(id, ids()), of = tiles();
-        split = logical / of;
-        int at = logical - split * of, tm, tn;
         if (!lower) {
             const int per_group = 8 * tiles_n, group = at / per_group, in_group = at - group * per_group;
             const int rows = m16::least(tiles_m - group * 8, 8);
             tm = group * 8 + in_group % rows;
             tn = in_group / rows;
-        } else {
-            // groups of 8 rows of tiles: a rectangle, column by column, and the
-            // triangle at its end, row by row
-            int group = 0, rows = m16::least(tiles_m, 8), size = rows * (rows + 1) / 2;
-            while (at >= size) {
-                at -= size;
-                ++group;
-                rows = m16::least(tiles_m - group * 8, 8);
-                size = rows * 8 * group + rows * (rows + 1) / 2;
-            }
-            tm = 8 * group;
-            tn = 0;
-            if (at < rows * 8 * group) {
-                tm += at % rows;
-                tn = at / rows;
-            } else {
-                at -= rows * 8 * group;
-                int r = 0;
-                while (at > r) at -= ++r;
-                tm += r;
-                tn = 8 * group + at;
-            }
+            return;
         }
+        // groups of 8 rows of tiles: a rectangle, column by column, and the
+        // triangle at its end, row by row
+        int group = 0, rows = m16::least(tiles_m, 8), size = rows * (rows + 1) / 2;
+        while (at >= size) {
+            at -= size;
+            ++group;
+            rows = m16::least(tiles_m - group * 8, 8);
+            size = rows * 8 * group + rows * (rows + 1) / 2;
+        }
+        tm = 8 * group;
+        tn = 0;
+        if (at < rows * 8 * group) {
+            tm += at % rows;
+            tn = at / rows;
+        } else {
+            at -= rows * 8 * group;
+            int r = 0;
+            while (at > r) at -= ++r;
+            tm += r;
+            tn = 8 * group + at;
+        }
+    }
+    template <int BM, int BN>
+    TGEMM_BOTH void tile(int id, int &m0, int &n0, int &split, int &first, int &last) const
+    {
+        // parts of a tile share nothing; neighbours share rows and columns
+        const int logical = m16::deal(id, ids()), part = logical / count, number = from + logical - part * count;
+        int tm, tn;
+        spot(number % tiles(), tm, tn);
         m0 = tm * BM;
         n0 = tn * BN;
-        first = 0;
-        last = steps;
+        split = number * splits + part;
+        first = part * steps_per_split;
+        last = m16::least(steps, first + steps_per_split);
     }
     TGEMM_BOTH int64_t plane_at_a(int seg) const { return seg == 0 ? plane_a : 0; }
     TGEMM_BOTH int64_t plane_at_b(int seg) const { return seg == 1 ? plane_b : 0; }
-    TGEMM_BOTH int64_t start_a(int split) const { return split * batch_a; }
-    TGEMM_BOTH int64_t start_b(int split) const { return split * batch_b; }
+    TGEMM_BOTH int matrix(int split) const { return split / splits / tiles(); }
+    TGEMM_BOTH int64_t start_a(int split) const { return matrix(split) * batch_a; }
+    TGEMM_BOTH int64_t start_b(int split) const { return matrix(split) * batch_b; }
 };
 
 // Tile configurations: index, rows and columns, wavefronts along them.
@@ -84,10 +95,10 @@ struct TileShape {
 constexpr TileShape kTiles[] = {{256, 1}, {128, 2}, {64, 4}};
 constexpr int kTileCount = 3;
 
-// alpha·add + beta·(the product), entry by entry, as planes or as the result.
+// alpha·add + beta·(the product) + diagonal·I, as planes or as the result.
 struct ChainArgs {
     Chain op;
-    float alpha, beta;
+    float alpha, beta, diagonal;
     const void *add;            // planes, or NULL
     int64_t ld_add, plane_add, batch_add;
     void *planes;               // or NULL: rows × ldo of each plane are written, zero past M and N
@@ -96,10 +107,14 @@ struct ChainArgs {
     void *result;               // M×N, rows ldr apart
     int64_t ldr, batch_r;
     tgemm_dtype_t dtype;
+    // Room for the parts of split sums, tile by tile and part by part: the launch
+    // leaves the products there, and launch_join does the rest.
+    float *parts;
 };
 // How A and B lie: both with K along their rows, both along their columns, or A along its rows and B not.
 enum Order { kRows, kColumns, kMixed };
 hipError_t launch_chain(Order order, int tile, const ChainArgs &a, hipStream_t stream);
+hipError_t launch_join(int tile, const ChainArgs &a, hipStream_t stream);
 
 // ---- passes over G ---------------------------------------------------------
 

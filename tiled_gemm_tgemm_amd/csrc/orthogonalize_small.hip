@@ -146,21 +146,30 @@ __global__ __launch_bounds__(256) void gram_kernel(SmallArgs a)
     }
 }
 
-// The iteration on one matrix's S, a wavefront a block of 16×16 of the results.
-// Bound by the chain of 17 products, 4·BLOCKS instructions each.
+// The iteration on one matrix's S, a wavefront a block of 16×16 of the results
+// (with one block the other three help to add S's parts up).  Bound by the chain
+// of 17 products, 4·BLOCKS instructions each.
 template <int BLOCKS>
-__global__ __launch_bounds__(64 * BLOCKS * BLOCKS) void iterate_kernel(SmallArgs a)
+constexpr int kIterate = BLOCKS == 1 ? 256 : 64 * BLOCKS * BLOCKS;
+template <int BLOCKS>
+__global__ __launch_bounds__(kIterate<BLOCKS>) void iterate_kernel(SmallArgs a)
 {
     constexpr int N = 16 * BLOCKS, kLd = N + 2, kPairs = BLOCKS * (BLOCKS + 1) / 2;
     __shared__ double S[N * kLd], P[N * kLd], Q[N * kLd], W[N * kLd];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, quarter = lane >> 4;
-    const int bi = wave / BLOCKS, bj = wave % BLOCKS;
+    const int bi = BLOCKS == 1 ? 0 : wave / BLOCKS, bj = BLOCKS == 1 ? 0 : wave % BLOCKS;
 
     // S, both halves, from its parts; zero past the side, where the loads stood in
     const double *from = a.grams + (int64_t)blockIdx.x * a.parts * kPairs * 256;
     for (int n = threadIdx.x; n < kPairs * 256; n += blockDim.x) {
         double sum = 0;
-        for (int p = 0; p < a.parts; ++p) sum += from[(int64_t)p * kPairs * 256 + n];
+        for (int p = 0; p < a.parts; p += 8) {  // eight parts on their way at once
+            double next[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) next[u] = p + u < a.parts ? from[(int64_t)(p + u) * kPairs * 256 + n] : 0.0;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) sum += next[u];
+        }
         const int pair = n / 256, at = n / 4 % 64, r = n % 4;
         const int ib = pair == 0 ? 0 : pair < 3 ? 1 : pair < 6 ? 2 : 3, jb = pair - ib * (ib + 1) / 2;
         const int i = 16 * ib + 4 * r + at / 16, j = 16 * jb + at % 16;
@@ -169,12 +178,14 @@ __global__ __launch_bounds__(64 * BLOCKS * BLOCKS) void iterate_kernel(SmallArgs
         S[j * kLd + i] = v;
     }
     __syncthreads();
-    double trace = 0;
-    for (int i = 0; i < a.side; ++i) trace += S[i * kLd + i];
+    double trace = lane < a.side ? S[lane * kLd + lane] : 0.0;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) trace += __shfl_xor(trace, d);
     __syncthreads();
     const double scale = 1 / (sqrt(trace) + (double)a.eps);
     for (int n = threadIdx.x; n < N * N; n += blockDim.x) S[n / N * kLd + n % N] *= scale * scale;
     __syncthreads();
+    if (BLOCKS == 1 && wave > 0) return;  // one wavefront needs no barrier with the others
 
     auto multiply = [&](const double *x, const double *y) {
         f64x4 acc{0, 0, 0, 0};
@@ -188,6 +199,11 @@ __global__ __launch_bounds__(64 * BLOCKS * BLOCKS) void iterate_kernel(SmallArgs
 #pragma unroll
         for (int r = 0; r < 4; ++r) to[(16 * bi + 4 * r + quarter) * kLd + 16 * bj + l16] = v[r];
     };
+    // what the others stored is there; a wavefront's own LDS accesses come in order
+    auto settle = [&]() {
+        if constexpr (BLOCKS > 1) __syncthreads();
+        else __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    };
     f64x4 q{};
     for (int step = 0; step < a.steps; ++step) {
         const double c0 = a.coefficients[3 * step], c1 = a.coefficients[3 * step + 1], c2 = a.coefficients[3 * step + 2];
@@ -198,14 +214,14 @@ __global__ __launch_bounds__(64 * BLOCKS * BLOCKS) void iterate_kernel(SmallArgs
             p[r] = c2 * p[r] + c1 * S[i * kLd + j] + (i == j ? c0 : 0.0);
         }
         store(P, p);
-        __syncthreads();
+        settle();
         q = step == 0 ? p : multiply(P, Q);
         if (step + 1 == a.steps) break;
         store(W, multiply(S, P));
-        __syncthreads();
+        settle();
         store(Q, q);
         store(S, multiply(P, W));
-        __syncthreads();
+        settle();
     }
     double *to = a.factor + (int64_t)blockIdx.x * N * N;
 #pragma unroll
@@ -374,9 +390,9 @@ hipError_t launch_grams(const SmallArgs &a, hipStream_t stream)
 hipError_t launch_iterate(const SmallArgs &a, hipStream_t stream)
 {
     switch (blocks_of(a.side)) {
-    case 1: iterate_kernel<1><<<a.batch, 64, 0, stream>>>(a); break;
-    case 2: iterate_kernel<2><<<a.batch, 256, 0, stream>>>(a); break;
-    default: iterate_kernel<4><<<a.batch, 1024, 0, stream>>>(a); break;
+    case 1: iterate_kernel<1><<<a.batch, kIterate<1>, 0, stream>>>(a); break;
+    case 2: iterate_kernel<2><<<a.batch, kIterate<2>, 0, stream>>>(a); break;
+    default: iterate_kernel<4><<<a.batch, kIterate<4>, 0, stream>>>(a); break;
     }
     return hipGetLastError();
 }
