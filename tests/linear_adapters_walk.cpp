@@ -255,14 +255,19 @@ hipError_t launch_arrange(const OuterArgs &a, const OuterArgs &b, hipStream_t)
     }
     return hipSuccess;
 }
-hipError_t launch_outer(const OuterArgs &a, hipStream_t)
+hipError_t launch_outer(const OuterArgs &first, const OuterArgs &second, hipStream_t)
 {
-    check_outer(a);
-    rows(a.rows, tokens, a.C, a.ld, size_of(a.dtype), false, "rows");
-    rows(a.small, tokens, a.rank, a.rank, 4, false, "small");
-    if (a.cut.tokens > kMostTokens) fail("tokens of a chunk", 0, 0);
-    if (a.arranged && (a.dtype == TGEMM_F32 || a.C % 8 || a.ld % 8 || (uintptr_t)a.rows % 16)) fail("rows that are not whole pieces", 0, 0);
-    rows(a.part, 2 * (tokens / a.cut.tokens), (int64_t)a.C * a.rank, (int64_t)a.C * a.rank, 4, true, "sums of chunks");
+    if (first.rank_inner || !second.rank_inner || first.rank != second.rank) fail("which is which", 0, 0);
+    for (const OuterArgs *o : {&first, &second}) {
+        const OuterArgs &a = *o;
+        if (a.out == nullptr) continue;
+        check_outer(a);
+        rows(a.rows, tokens, a.C, a.ld, size_of(a.dtype), false, "rows");
+        rows(a.small, tokens, a.rank, a.rank, 4, false, "small");
+        if (a.cut.tokens > kMostTokens) fail("tokens of a chunk", 0, 0);
+        if (a.arranged && (a.dtype == TGEMM_F32 || a.C % 8 || a.ld % 8 || (uintptr_t)a.rows % 16)) fail("rows that are not whole pieces", 0, 0);
+        rows(a.part, 2 * (tokens / a.cut.tokens), (int64_t)a.C * a.rank, (int64_t)a.C * a.rank, 4, true, "sums of chunks");
+    }
     return hipSuccess;
 }
 hipError_t launch_join(const OuterArgs &a, const OuterArgs &b, hipStream_t)
@@ -271,8 +276,9 @@ hipError_t launch_join(const OuterArgs &a, const OuterArgs &b, hipStream_t)
         if (o->out) check_outer(*o);
     return hipSuccess;
 }
-hipError_t launch_turn(const TurnArgs &a, const TurnArgs &b, hipStream_t)
+hipError_t launch_turn(const TurnArgs &a, const TurnArgs &b, const GroupArgs *group, hipStream_t)
 {
+    if (group && launch_group(*group, nullptr) != hipSuccess) return hipErrorUnknown;
     if (a.from.count + b.from.count > 65535) fail("a grid", 0, 0);
     for (const TurnArgs *t : {&a, &b}) {
         if (t->to == nullptr) continue;

@@ -75,8 +75,8 @@ from .linear_loss import (  # noqa: F401
     linear_distillation_forward,
 )
 
-from .linear_adapters import linear_adapters, linear_adapters_backward, linear_adapters_forward  # noqa: F401
-from .orthogonalize import orthogonalize  # noqa: F401
+from .adapters import linear_adapters, linear_adapters_backward, linear_adapters_forward  # noqa: F401
+from .newton_schulz import orthogonalize  # noqa: F401
 
 KERNELS = ("auto", "mfma", "naive", "lds", "simt")
 

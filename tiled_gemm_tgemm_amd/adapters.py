@@ -80,6 +80,27 @@ class _Call:
         self.adapters = (self.L, self.r, A.data_ptr(), lda, stride_a, B.data_ptr(), ldb, stride_b, ids.data_ptr(),
                          _ptr(scales))
 
+    def again(self, X, W, A, B, ids, scales, hidden):
+        """The call of a backward pass: the same tensors, wherever and however they are stored by now, on the stream
+        that is torch's current one (its engine makes that the forward pass's; a node that is called by hand runs where
+        its caller is).  It is the pass's own: others may go through the same node meanwhile.  hidden: what the forward
+        pass allocated, or None."""
+        import torch
+
+        c = _Call.__new__(_Call)
+        c.__dict__.update(self.__dict__)
+        current = torch.cuda.current_stream(c.device)
+        if current.cuda_stream != c.stream:
+            c.stream = current.cuda_stream
+            if hidden is not None:
+                hidden.record_stream(current)
+        ldx = _rows(X, "X", (c.T, c.D), c.device, c.dtype)
+        c.head = (*c.head[:4], X.data_ptr(), ldx, W.data_ptr(), _rows(W, "W", (c.N, c.D), c.device, c.dtype))
+        c.adapters = (c.L, c.r, A.data_ptr(), *_stacked(A, "A", (c.L, c.r, c.D), c.device, c.dtype), B.data_ptr(),
+                      *_stacked(B, "B", (c.L, c.N, c.r), c.device, c.dtype), ids.data_ptr(), _ptr(scales))
+        c.made = []
+        return c
+
     def new(self, shape, dtype=None):
         import torch
 
@@ -189,22 +210,22 @@ def _function():
     class Adapters(torch.autograd.Function):
         @staticmethod
         def forward(ctx, X, W, A, B, ids, scales):
+            # (a copy that the call makes of ids stands in for it in the backward pass)
             c = _Call(X, W, A, B, ids, scales, None)
-            Y, out = c.matrix(None, "out", (c.T, c.N))
+            if c.made:
+                ids = c.made[0]
+            Y = torch.empty((c.T, c.N), dtype=c.dtype, device=c.device)
             hidden = torch.empty((c.T, c.r), dtype=torch.float32, device=c.device) if ctx.needs_input_grad[3] else None
-            c.queue("tgemm_linear_adapters_forward", *out, _ptr(hidden), *c.room(None))
+            c.queue("tgemm_linear_adapters_forward", Y.data_ptr(), c.N, _ptr(hidden), *c.room(None))
             ctx.save_for_backward(X, W, A, B, ids, scales, hidden)
-            ctx.stream = c.stream
+            ctx.call = c
             return Y
 
         @staticmethod
         @once_differentiable
         def backward(ctx, dY):
             X, W, A, B, ids, scales, hidden = ctx.saved_tensors
-            c = _Call(X, W, A, B, ids, scales, None)
-            if hidden is not None and c.stream != ctx.stream:
-                # a node that is called by hand runs where its caller is
-                hidden.record_stream(torch.cuda.current_stream(c.device))
+            c = ctx.call.again(X, W, A, B, ids, scales, hidden)
             if not dY.is_contiguous():
                 dY = dY.contiguous()
             return (*_backward(c, dY, hidden, (None,) * 4, ctx.needs_input_grad[:4], None), None, None)

@@ -105,6 +105,7 @@ Shrink shrink_of(int64_t T, int64_t K, int64_t count, bool through_lds)
     const int64_t wavefronts = 4 * ceil_div(T, T <= 1024 ? 16 : T < 4096 ? 64 : 128), most = T <= 1024 ? 8 : 16;
     int64_t parts = 4096 / wavefronts;
     if (parts > ceil_div(K, 512)) parts = ceil_div(K, 512);
+    if (K <= 1024 && T > kFewRows) parts = 1;  // not worth the launch that adds them up
     if (parts > most) parts = most;
     if (parts < 1) parts = 1;
     s.part_k = round_up(ceil_div(K, parts), 256);
@@ -428,7 +429,8 @@ tgemm_status_t backward(const Plan &p, const Layer &l, const void *dY, int64_t l
 {
     hipError_t e = hipSuccess;
     GroupArgs o{};
-    if (g.dA != nullptr || g.dB != nullptr) {
+    const bool grouped = g.dA != nullptr || g.dB != nullptr;
+    if (grouped) {
         o.ids = l.ids;
         o.T = (int)l.T;
         o.count = (int)l.count;
@@ -436,19 +438,15 @@ tgemm_status_t backward(const Plan &p, const Layer &l, const void *dY, int64_t l
         o.starts = in<int>(ws, p.starts);
         for (int n = 0; n < 2; ++n)
             o.cuts[n] = Cut{p.cut[n], in<Chunk>(ws, p.chunks[n]), in<int2>(ws, p.joins[n]), in<int>(ws, p.counts) + n};
-        e = launch_group(o, stream);
-        if (e != hipSuccess) return from_hip(e);
     }
     Stack a_stack = stack_a(l), b_stack = stack_b(l);
-    if (p.turned_b >= 0) {
-        const int64_t ld_a = round_up(l.rank, 8), ld_b = round_up(l.N, 8);
-        const TurnArgs b{l.dtype, b_stack, l.N, in<void>(ws, p.turned_b), ld_b, l.rank * ld_b};
-        const TurnArgs a{l.dtype, a_stack, l.D, in<void>(ws, p.turned_a), ld_a, l.D * ld_a};
-        e = launch_turn(b, a, stream);
-        if (e != hipSuccess) return from_hip(e);
-        b_stack = Stack{b.to, ld_b, b.to_stride, false, (int)l.count, (int)l.rank};
-        if (a.to != nullptr) a_stack = Stack{a.to, ld_a, a.to_stride, true, (int)l.count, (int)l.rank};
-    }
+    const int64_t ld_a = round_up(l.rank, 8), ld_b = round_up(l.N, 8);
+    const TurnArgs turn_b{l.dtype, b_stack, l.N, in<void>(ws, p.turned_b), ld_b, l.rank * ld_b};
+    const TurnArgs turn_a{l.dtype, a_stack, l.D, in<void>(ws, p.turned_a), ld_a, l.D * ld_a};
+    e = launch_turn(turn_b, turn_a, grouped ? &o : nullptr, stream);
+    if (e != hipSuccess) return from_hip(e);
+    if (turn_b.to != nullptr) b_stack = Stack{turn_b.to, ld_b, turn_b.to_stride, false, (int)l.count, (int)l.rank};
+    if (turn_a.to != nullptr) a_stack = Stack{turn_a.to, ld_a, turn_a.to_stride, true, (int)l.count, (int)l.rank};
     float *u = in<float>(ws, p.u);
     void *planes = in<void>(ws, p.hidden_planes);
     if (l.T > 0 && (g.dX != nullptr || g.dA != nullptr))
@@ -483,8 +481,7 @@ tgemm_status_t backward(const Plan &p, const Layer &l, const void *dY, int64_t l
             r[n].rank_inner = n == 1;
         }
         if (l.T > 0 && (r[0].arranged != nullptr || r[1].arranged != nullptr)) e = launch_arrange(r[0], r[1], stream);
-        for (int n = 0; n < 2; ++n)
-            if (e == hipSuccess && l.T > 0 && r[n].out != nullptr) e = launch_outer(r[n], stream);
+        if (e == hipSuccess && l.T > 0) e = launch_outer(r[0], r[1], stream);
         if (e == hipSuccess) e = launch_join(r[0], r[1], stream);
         if (e != hipSuccess) return from_hip(e);
     }

@@ -134,6 +134,9 @@ struct GroupArgs {
     Cut cuts[2];
 };
 hipError_t launch_group(const GroupArgs &a, hipStream_t stream);
+// Up to these one work-group does it, an adapter after the other (0.5 µs each),
+// next to the adapters' turn; the two launches that this spares take 10 µs.
+constexpr int kAloneTokens = 8192, kAloneAdapters = 16;
 
 // out_i = scales[i]·sum over adapter i's tokens of rows(t, :)ᵀ·small(t, :), laid
 // out as the stack: out(outer, rank).  Adapters of several chunks leave those
@@ -162,7 +165,8 @@ struct OuterArgs {
 constexpr int kOuterColumns = 128, kOuterTokens = 64;
 // Both gradients' small values at once (either `out` may be NULL).
 hipError_t launch_arrange(const OuterArgs &a, const OuterArgs &b, hipStream_t stream);
-hipError_t launch_outer(const OuterArgs &a, hipStream_t stream);
+// a is A's (its ranks are not the inner ones), b is B's
+hipError_t launch_outer(const OuterArgs &a, const OuterArgs &b, hipStream_t stream);
 hipError_t launch_join(const OuterArgs &a, const OuterArgs &b, hipStream_t stream);
 
 // Stacks the other way round: element (outer, rank) of adapter i, at i·to_stride
@@ -175,7 +179,8 @@ struct TurnArgs {
     void *to;                 // or NULL: nothing to do
     int64_t to_ld, to_stride;
 };
-hipError_t launch_turn(const TurnArgs &a, const TurnArgs &b, hipStream_t stream);
+// Also does launch_group's work if `group` is not NULL.
+hipError_t launch_turn(const TurnArgs &a, const TurnArgs &b, const GroupArgs *group, hipStream_t stream);
 
 }  // namespace adapters
 }  // namespace tgemm

@@ -431,10 +431,8 @@ __global__ __launch_bounds__(1024) void group_kernel(GroupArgs a)
     }
 }
 
-__global__ __launch_bounds__(1024) void chunks_kernel(GroupArgs a)
+__device__ __forceinline__ void cut_chunks(const GroupArgs &a, const Cut &cut, int *room)
 {
-    __shared__ int room[16];
-    const Cut cut = a.cuts[blockIdx.x];
     int chunk0 = 0, slot0 = 0;
     int64_t place0 = 0;
     for (int i0 = 0; i0 < a.count; i0 += 1024) {
@@ -458,6 +456,38 @@ __global__ __launch_bounds__(1024) void chunks_kernel(GroupArgs a)
         place0 += 64 * (int64_t)all_places;
     }
     if (threadIdx.x == 0) *cut.chunk_count = chunk0;
+}
+
+__global__ __launch_bounds__(1024) void chunks_kernel(GroupArgs a)
+{
+    __shared__ int room[16];
+    cut_chunks(a, a.cuts[blockIdx.x], room);
+}
+
+// All of it by one work-group for a few tokens and adapters, whose ids it keeps
+// in registers: a launch less, and the adapters' turn goes with it.
+__device__ __forceinline__ void group_alone(const GroupArgs &a, int *room)
+{
+    int64_t id[kAloneTokens / 1024];
+    const int first = threadIdx.x * (kAloneTokens / 1024);
+#pragma unroll
+    for (int e = 0; e < kAloneTokens / 1024; ++e) id[e] = first + e < a.T ? a.ids[first + e] : -1;
+    int start = 0;
+    for (int i = 0; i < a.count; ++i) {
+        int own = 0, total;
+#pragma unroll
+        for (int e = 0; e < kAloneTokens / 1024; ++e) own += id[e] == i;
+        int at = start + before(own, room, total);
+#pragma unroll
+        for (int e = 0; e < kAloneTokens / 1024; ++e)
+            if (id[e] == i) a.order[at++] = first + e;
+        if (threadIdx.x == 0) a.starts[i] = start;
+        start += total;
+    }
+    if (threadIdx.x == 0) a.starts[a.count] = start;
+    __threadfence_block();
+    __syncthreads();
+    for (int n = 0; n < 2; ++n) cut_chunks(a, a.cuts[n], room);
 }
 
 // ---- gradients -------------------------------------------------------------
@@ -622,25 +652,26 @@ __device__ __forceinline__ void gather_lds(const void *from, m16::lds_char *to)
 }
 #pragma clang diagnostic pop
 
+template <int BLOCKS>
+constexpr int kOuterLds = 2 * (kOuterColumns * 128 + 2 * 16 * BLOCKS * 128);
+
 // A work-group takes 128 columns of the rows, 16·BLOCKS ranks and a chunk of an
 // adapter's tokens, 64 at a time: the rows' and the arranged values' slices go
 // straight into one of two LDS stages, and the loads of the next 64 are under
 // way while these are multiplied.  The rows' fragments come from the transposing
 // LDS read.  A wavefront takes 32 columns.  Bound by reading the rows once.
 template <class In, int BLOCKS, bool RANK_INNER>
-__global__ __launch_bounds__(256) void outer_kernel(OuterArgs a)
+__device__ __forceinline__ void outer_of(const OuterArgs &a, int rank0, char *lds, int *order)
 {
     constexpr int kCols = kOuterColumns, kTokens = kOuterTokens, kRanks = 16 * BLOCKS;
     typedef m16::Slice<kCols, 2, 256, true, false> SliceZ;
     typedef m16::Slice<kRanks, BLOCKS, 128 * BLOCKS, false, false> SliceV;  // one round a plane
     constexpr int kBytesV = SliceV::kBytes, kStage = SliceZ::kBytes + 2 * kBytesV;
     static_assert(SliceZ::kRounds == 4 && SliceV::kRounds == 1, "rounds");
-    __shared__ __align__(1024) char lds[2 * kStage];
-    __shared__ int order[kMostTokens];
-    if ((int)blockIdx.y >= *a.cut.chunk_count) return;
+    static_assert(2 * kStage == kOuterLds<BLOCKS>, "room");
     const Chunk chunk = a.cut.chunks[blockIdx.y];
     const int thread = threadIdx.x, lane = thread & 63, wave = __builtin_amdgcn_readfirstlane(thread >> 6);
-    const int col0 = blockIdx.x * kCols, rank0 = blockIdx.z * kRanks;
+    const int col0 = blockIdx.x * kCols;
     const int whole = (chunk.tokens + 63) / 64 * 64;
     // tokens past the last meet zeros: the last stands in
     for (int t = thread; t < whole; t += 256) order[t] = a.order[chunk.first + min(t, chunk.tokens - 1)];
@@ -698,6 +729,20 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs a)
         stage ^= 1;
     }
     put_outer<In, BLOCKS, RANK_INNER>(a, chunk, col0 + 32 * wave, rank0, acc);
+}
+
+// Both gradients' in one launch: the first's ranks, then the second's, along z.
+template <class In, int BLOCKS>
+__global__ __launch_bounds__(256) void outer_kernel(OuterArgs first, OuterArgs second)
+{
+    __shared__ __align__(1024) char lds[kOuterLds<BLOCKS>];
+    __shared__ int order[kMostTokens];
+    const int blocks = (first.rank + 16 * BLOCKS - 1) / (16 * BLOCKS);
+    const bool other = (int)blockIdx.z >= blocks;
+    const OuterArgs &a = other ? second : first;
+    if (a.out == nullptr || a.arranged == nullptr || (int)blockIdx.x * kOuterColumns >= a.C || (int)blockIdx.y >= *a.cut.chunk_count) return;
+    if (other) outer_of<In, BLOCKS, true>(a, ((int)blockIdx.z - blocks) * 16 * BLOCKS, lds, order);
+    else outer_of<In, BLOCKS, false>(a, (int)blockIdx.z * 16 * BLOCKS, lds, order);
 }
 
 // The same for float32 rows and rows that start anywhere: through registers into
@@ -805,11 +850,17 @@ __global__ __launch_bounds__(256) void join_kernel(OuterArgs first, OuterArgs se
     }
 }
 
-// 64×64 elements at a time through LDS.
+// The adapters the other way round, 64×64 elements at a time through LDS; the
+// last work-group along x of the first adapter groups the tokens if `grouping`.
 template <class In>
-__global__ __launch_bounds__(256) void turn_kernel(TurnArgs first, TurnArgs second)
+__global__ __launch_bounds__(1024) void turn_kernel(TurnArgs first, TurnArgs second, GroupArgs group, bool grouping)
 {
     __shared__ In tile[64][65];
+    __shared__ int room[16];
+    if (grouping && blockIdx.x + 1 == gridDim.x) {
+        if (blockIdx.z == 0) group_alone(group, room);
+        return;
+    }
     const bool other = blockIdx.z >= (unsigned)first.from.count;
     const TurnArgs &a = other ? second : first;
     if (a.to == nullptr) return;
@@ -818,37 +869,43 @@ __global__ __launch_bounds__(256) void turn_kernel(TurnArgs first, TurnArgs seco
     const int64_t across = (cols + 63) / 64, tiles = (rows + 63) / 64 * across;
     const In *from = (const In *)a.from.p + adapter * a.from.stride;
     In *to = (In *)a.to + adapter * a.to_stride;
-    for (int64_t n = blockIdx.x; n < tiles; n += gridDim.x) {
+    for (int64_t n = blockIdx.x; n < tiles; n += gridDim.x - (grouping ? 1 : 0)) {
         const int64_t r0 = n / across * 64, c0 = n % across * 64;
-        for (int e = threadIdx.x; e < 4096; e += 256)
+#pragma unroll
+        for (int e = threadIdx.x; e < 4096; e += 1024)
             if (r0 + e / 64 < rows && c0 + e % 64 < cols) tile[e / 64][e % 64] = from[(r0 + e / 64) * a.from.ld + c0 + e % 64];
         __syncthreads();
-        for (int e = threadIdx.x; e < 4096; e += 256)
+#pragma unroll
+        for (int e = threadIdx.x; e < 4096; e += 1024)
             if (c0 + e / 64 < cols && r0 + e % 64 < rows) to[(c0 + e / 64) * a.to_ld + r0 + e % 64] = tile[e % 64][e / 64];
         __syncthreads();
     }
 }
 
 template <class In, int BLOCKS>
-void outer(const OuterArgs &a, hipStream_t stream)
+void outer(const OuterArgs &a, const OuterArgs &b, hipStream_t stream)
 {
-    const dim3 grid((unsigned)((a.C + kOuterColumns - 1) / kOuterColumns), a.most_chunks, (a.rank + 16 * BLOCKS - 1) / (16 * BLOCKS));
+    const int ranks = (a.rank + 16 * BLOCKS - 1) / (16 * BLOCKS);
     if constexpr (sizeof(In) == 2) {
-        if (a.arranged != nullptr) {
-            if (a.rank_inner) outer_kernel<In, BLOCKS, true><<<grid, 256, 0, stream>>>(a);
-            else outer_kernel<In, BLOCKS, false><<<grid, 256, 0, stream>>>(a);
-            return;
-        }
+        const bool first = a.out != nullptr && a.arranged != nullptr, second = b.out != nullptr && b.arranged != nullptr;
+        const int C = !second || (first && a.C > b.C) ? a.C : b.C;
+        const int chunks = !second || (first && a.most_chunks > b.most_chunks) ? a.most_chunks : b.most_chunks;
+        if (first || second)
+            outer_kernel<In, BLOCKS><<<dim3((C + kOuterColumns - 1) / kOuterColumns, chunks, 2 * ranks), 256, 0, stream>>>(a, b);
     }
-    if (a.rank_inner) outer_any_kernel<In, BLOCKS, true><<<grid, 256, 0, stream>>>(a);
-    else outer_any_kernel<In, BLOCKS, false><<<grid, 256, 0, stream>>>(a);
+    for (const OuterArgs *o : {&a, &b}) {
+        if (o->out == nullptr || (sizeof(In) == 2 && o->arranged != nullptr)) continue;
+        const dim3 grid((unsigned)((o->C + kOuterColumns - 1) / kOuterColumns), o->most_chunks, ranks);
+        if (o->rank_inner) outer_any_kernel<In, BLOCKS, true><<<grid, 256, 0, stream>>>(*o);
+        else outer_any_kernel<In, BLOCKS, false><<<grid, 256, 0, stream>>>(*o);
+    }
 }
 template <class In>
-void outer(const OuterArgs &a, hipStream_t stream)
+void outer(const OuterArgs &a, const OuterArgs &b, hipStream_t stream)
 {
-    if (a.rank <= 16) outer<In, 1>(a, stream);
-    else if (a.rank <= 32) outer<In, 2>(a, stream);
-    else outer<In, 4>(a, stream);
+    if (a.rank <= 16) outer<In, 1>(a, b, stream);
+    else if (a.rank <= 32) outer<In, 2>(a, b, stream);
+    else outer<In, 4>(a, b, stream);
 }
 
 }  // namespace
@@ -878,11 +935,11 @@ hipError_t launch_group(const GroupArgs &a, hipStream_t stream)
     return hipGetLastError();
 }
 
-hipError_t launch_outer(const OuterArgs &a, hipStream_t stream)
+hipError_t launch_outer(const OuterArgs &a, const OuterArgs &b, hipStream_t stream)
 {
-    if (a.dtype == TGEMM_F32) outer<float>(a, stream);
-    else if (a.dtype == TGEMM_BF16) outer<__bf16>(a, stream);
-    else outer<_Float16>(a, stream);
+    if (a.dtype == TGEMM_F32) outer<float>(a, b, stream);
+    else if (a.dtype == TGEMM_BF16) outer<__bf16>(a, b, stream);
+    else outer<_Float16>(a, b, stream);
     return hipGetLastError();
 }
 
@@ -904,12 +961,20 @@ hipError_t launch_join(const OuterArgs &a, const OuterArgs &b, hipStream_t strea
     return hipGetLastError();
 }
 
-hipError_t launch_turn(const TurnArgs &a, const TurnArgs &b, hipStream_t stream)
+hipError_t launch_turn(const TurnArgs &a, const TurnArgs &b, const GroupArgs *group, hipStream_t stream)
 {
-    const int64_t outer = a.outer > b.outer ? a.outer : b.outer, tiles = (outer + 63) / 64 * ((a.from.rank + 63) / 64);
-    const dim3 grid((unsigned)(tiles < 1024 ? tiles : 1024), 1, a.from.count + b.from.count);
-    if (a.dtype == TGEMM_F32) turn_kernel<float><<<grid, 256, 0, stream>>>(a, b);
-    else turn_kernel<uint16_t><<<grid, 256, 0, stream>>>(a, b);
+    const bool here = group != nullptr && group->T <= kAloneTokens && group->count <= kAloneAdapters;
+    if (group != nullptr && !here) {
+        const hipError_t e = launch_group(*group, stream);
+        if (e != hipSuccess) return e;
+    }
+    const bool turning = a.to != nullptr || b.to != nullptr;
+    if (!turning && !here) return hipSuccess;
+    const int64_t outer = a.outer > b.outer ? a.outer : b.outer, tiles = turning ? (outer + 63) / 64 * ((a.from.rank + 63) / 64) : 0;
+    const dim3 grid((unsigned)(tiles < 1024 ? tiles : 1024) + (here ? 1 : 0), 1, turning ? a.from.count + b.from.count : 1);
+    const GroupArgs g = here ? *group : GroupArgs{};
+    if (a.dtype == TGEMM_F32) turn_kernel<float><<<grid, 1024, 0, stream>>>(a, b, g, here);
+    else turn_kernel<uint16_t><<<grid, 1024, 0, stream>>>(a, b, g, here);
     return hipGetLastError();
 }
 
