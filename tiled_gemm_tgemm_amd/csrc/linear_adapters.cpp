@@ -236,10 +236,10 @@ bool plan_backward(Plan &p, const Layer &l, const void *dY, int64_t lddy, Need n
         }
     }
     if (l.T == 0) return true;
-    // A copy of the adapters the other way round is read 16 bytes at a time; it costs less than it spares where they
-    // have fewer ranks together than there are tokens (B for the hidden values of 8192×16384 with 8 of 32 53 µs against
-    // 280 as they lie).
-    if ((need.x || need.a) && 4 * l.count * l.rank <= l.T) {
+    // A copy of the adapters the other way round is read 16 bytes at a time (hidden values of 8192×16384 with 8 adapters
+    // of 32 ranks 75 µs, against 280 with B as it lies).  It is worth its launch, 7 to 20 µs, where the adapters have
+    // fewer ranks together than there are tokens, and those are many: from 1025 on they go through LDS.
+    if ((need.x || need.a) && l.T > 1024 && 4 * l.count * l.rank <= l.T) {
         p.turned_b = p.take(l.count * l.rank * round_up(l.N, 8) * (int64_t)size_of(l.dtype));
         if (need.x) p.turned_a = p.take(l.count * l.D * round_up(l.rank, 8) * (int64_t)size_of(l.dtype));
     }

@@ -182,6 +182,48 @@ __device__ __forceinline__ void add_lanes(const Expand &e, int id, int64_t row, 
     }
 }
 
+// Eight ranks, from k0 + 8·(lane / 16) on, of the column at index lane % 16 of
+// block j (mfma16.h), of an adapter at c.
+template <class Tile, class C, bool RANK_INNER>
+__device__ __forceinline__ typename Ranks<C>::F column_ranks(const ProductArgs &a, const C *c, int col0, int j, int k0)
+{
+    const int lane = m16::thread_anew() & 63, l16 = lane & 15, quarter = lane >> 4, k = k0 + 8 * quarter;
+    const int col = min(col0 + 4 * Tile::FN * (l16 >> 2) + 4 * j + (l16 & 3), a.op.N - 1);
+    C v[8];
+    if constexpr (!RANK_INNER) {
+        const C *from = c + k0 * a.e.c.ld;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int r = min(8 * quarter + e, a.e.c.rank - 1 - k0);  // ranks past the last meet zeros
+            const C x = from[(uint32_t)r * (uint32_t)a.e.c.ld + (uint32_t)col];
+            v[e] = k + e < a.e.c.rank ? x : (C)0.0f;
+        }
+    } else {
+        load_some<C, 8>(c + (int64_t)col * a.e.c.ld + k, a.e.c.rank - k, v);
+    }
+    return Ranks<C>::stored(v);
+}
+
+// One adapter's part of all of a wavefront's rows.
+template <class Tile, class C, bool RANK_INNER>
+__device__ __forceinline__ void add_one(const ProductArgs &a, int adapter, int row0, int col0, typename Tile::Acc &acc)
+{
+    const int padded = (int)planes_rank(a.e.c.rank);
+    const C *c = (const C *)a.e.c.p + adapter * a.e.c.stride;
+    for (int k0 = 0; k0 < padded; k0 += 32) {
+        const int lane = m16::thread_anew() & 63, l16 = lane & 15, quarter = lane >> 4;
+        typename Ranks<C>::H h[Tile::FM];
+#pragma unroll
+        for (int i = 0; i < Tile::FM; ++i) read_planes(a.e.planes, min(row0 + i * 16 + l16, a.op.M - 1), k0 + 8 * quarter, padded, h[i]);
+#pragma unroll
+        for (int j = 0; j < Tile::FN; ++j) {
+            const typename Ranks<C>::F f = column_ranks<Tile, C, RANK_INNER>(a, c, col0, j, k0);
+#pragma unroll
+            for (int i = 0; i < Tile::FM; ++i) acc[i][j] = Ranks<C>::add(f, h[i], acc[i][j]);
+        }
+    }
+}
+
 // E: the tiles' type; C: the adapters'.  The wavefront's rows are taken adapter
 // by adapter: tokens of a sequence share theirs.  Where 32 rows have more than
 // kMixed, each lane reads its own instead, which takes the vector units as long
@@ -207,13 +249,24 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 32 ? 3 : 2) void adapted_kernel
     };
     Tile::run(a.op, (lds_char *)lds, prologue, [&](typename Tile::Acc &acc, int row0, int col0, int split, const Ahead &ahead) {
         const int lane = m16::thread_anew() & 63, l16 = lane & 15, quarter = lane >> 4;
+        // One adapter for all of the wavefront's rows: everything is loaded at once.
+        int one = -1;
+#pragma unroll
+        for (int i = 0; i < Tile::FM; ++i) {
+            const uint32_t some = (uint32_t)__ballot(ahead.id[i] >= 0) & 0xFFFF;
+            if (one < 0 && some != 0) one = __builtin_amdgcn_readlane(ahead.id[i], __builtin_ctz(some));
+        }
+        bool alone = one >= 0;
+#pragma unroll
+        for (int i = 0; i < Tile::FM; ++i) alone = alone && __ballot(ahead.id[i] == one || row0 + i * 16 + l16 >= a.op.M) == ~(uint64_t)0;
+        if (alone) add_one<Tile, C, RANK_INNER>(a, one, row0, col0, acc);
         // 32 rows at a time, which leaves the other accumulators where they are
         const int padded = (int)planes_rank(a.e.c.rank);
 #pragma unroll
         for (int i0 = 0; i0 < Tile::FM; i0 += 2) {
             int id[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) id[i] = ahead.id[i0 + i];
+            for (int i = 0; i < 2; ++i) id[i] = alone ? -1 : ahead.id[i0 + i];
             uint64_t left = (__ballot(id[0] >= 0) & 0xFFFF) | __ballot(id[1] >= 0) << 16;
             left &= 0xFFFFFFFF;
             auto next = [&]() {
@@ -252,21 +305,7 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 32 ? 3 : 2) void adapted_kernel
                     for (int j = 0; j < Tile::FN; ++j) {
                         // (the registers hold no more than one block's loads)
                         if (Tile::FM == 8 && sizeof(C) == 2 && !RANK_INNER) asm volatile("" ::: "memory");
-                        // the column at index l16 of block j (mfma16.h)
-                        const int col = min(col0 + 4 * Tile::FN * (l16 >> 2) + 4 * j + (l16 & 3), a.op.N - 1);
-                        C v[8];
-                        if constexpr (!RANK_INNER) {
-                            const C *from = c + k0 * a.e.c.ld;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) {
-                                const int r = min(8 * quarter + e, a.e.c.rank - 1 - k0);  // ranks past the last meet zeros
-                                const C x = from[(uint32_t)r * (uint32_t)a.e.c.ld + (uint32_t)col];
-                                v[e] = k + e < a.e.c.rank ? x : (C)0.0f;
-                            }
-                        } else {
-                            load_some<C, 8>(c + col * a.e.c.ld + k, a.e.c.rank - k, v);
-                        }
-                        const typename Ranks<C>::F f = Ranks<C>::stored(v);
+                        const typename Ranks<C>::F f = column_ranks<Tile, C, RANK_INNER>(a, c, col0, j, k0);
 #pragma unroll
                         for (int i = 0; i < 2; ++i) more[i][j] = Ranks<C>::add(f, h[i], more[i][j]);
                     }
@@ -301,8 +340,9 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 32 ? 3 : 2) void adapted_kernel
     });
 }
 
-// The sum over parts and the adapters' part, four columns a thread, 64 apart, so
-// that a wavefront's loads of an adapter lie side by side.  (In the tiles of a
+// The sum over parts and the adapters' part, four columns a thread: adjacent
+// ones, or 64 apart where a column's ranks are, so that a wavefront's loads of
+// an adapter lie side by side.  (In the tiles of a
 // split sum, which are few and short, the adapters' loads would be waited for:
 // 256×4096×4096 with 32 adapters 49 µs and 5 for the sum, against 22 and 13.)
 template <class C, bool RANK_INNER>
@@ -312,13 +352,14 @@ __global__ __launch_bounds__(256) void adapted_sum_kernel(AddArgs a)
     const int64_t per_row = (a.N + 255) / 256, total = a.T * per_row;
     const int padded = (int)planes_rank(a.e.c.rank), lane = threadIdx.x & 63;
     for (int64_t p = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); p < total; p += (int64_t)gridDim.x * 4) {
-        const int64_t row = p / per_row, col0 = p % per_row * 256 + lane;
+        constexpr int kApart = RANK_INNER ? 64 : 1;
+        const int64_t row = p / per_row, col0 = p % per_row * 256 + (RANK_INNER ? lane : 4 * lane);
         // columns past the last are read from it and not stored
         int64_t col[4];
         float v[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            col[x] = min(col0 + 64 * x, a.N - 1);
+            col[x] = min(col0 + kApart * x, a.N - 1);
             v[x] = a.part[row * a.ld + col[x]];
         }
         for (int s = 1; s < a.count; s += 4) {  // four parts on their way at once
@@ -338,20 +379,23 @@ __global__ __launch_bounds__(256) void adapted_sum_kernel(AddArgs a)
             for (int k = 0; k < a.e.c.rank; k += 8) {
                 float h[8];
                 eight_hidden((const P *)a.e.planes, row, k, padded, h);
-                C w[4][8];
+                if constexpr (RANK_INNER) {
+                    C w[4][8];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    if constexpr (RANK_INNER) {
-                        load_some<C, 8>(c + col[x] * a.e.c.ld + k, a.e.c.rank - k, w[x]);
-                    } else {
+                    for (int x = 0; x < 4; ++x) load_some<C, 8>(c + col[x] * a.e.c.ld + k, a.e.c.rank - k, w[x]);
 #pragma unroll
-                        for (int n = 0; n < 8; ++n) w[x][n] = k + n < a.e.c.rank ? c[(k + n) * a.e.c.ld + col[x]] : (C)0.0f;
-                    }
+                    for (int n = 0; n < 8; ++n)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) v[x] = fmaf(h[n], (float)w[x][n], v[x]);
+                } else {
+                    C w[8][4];
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) load_some<C, 4>(c + (k + n) * a.e.c.ld + col[0], k + n < a.e.c.rank ? a.N - col0 : 0, w[n]);
+#pragma unroll
+                    for (int n = 0; n < 8; ++n)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) v[x] = fmaf(h[n], (float)w[n][x], v[x]);
                 }
-#pragma unroll
-                for (int n = 0; n < 8; ++n)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) v[x] = fmaf(h[n], (float)w[x][n], v[x]);
             }
         } else if (id == -2) {
 #pragma unroll
@@ -360,7 +404,7 @@ __global__ __launch_bounds__(256) void adapted_sum_kernel(AddArgs a)
         C *to = (C *)a.out + row * a.ldo;
 #pragma unroll
         for (int x = 0; x < 4; ++x)
-            if (col0 + 64 * x < a.N) to[col0 + 64 * x] = (C)v[x];
+            if (col0 + kApart * x < a.N) to[col0 + kApart * x] = (C)v[x];
     }
 }
 

@@ -385,14 +385,16 @@ __device__ __forceinline__ int before(int v, int *room, int &all)
     }
     if (lane == 63) room[wave] = sum;
     __syncthreads();
-    int base = 0;
-    all = 0;
-    for (int w = 0; w < waves; ++w) {
-        base += w < wave ? room[w] : 0;
-        all += room[w];
-    }
+    int of = lane < waves ? room[lane] : 0;  // the wavefronts' sums, in every wavefront
     __syncthreads();
-    return base + sum - v;
+#pragma unroll
+    for (int d = 1; d < 16; d <<= 1) {
+        const int other = __shfl_up(of, d);
+        if (lane >= d) of += other;
+    }
+    all = __shfl(of, waves - 1);
+    const int base = __shfl(of, wave > 0 ? wave - 1 : 0);
+    return (wave > 0 ? base : 0) + sum - v;
 }
 
 // Work-group i counts the tokens of smaller adapters and lists its own in
