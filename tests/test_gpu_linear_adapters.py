@@ -111,6 +111,27 @@ def test_larger_ones(size, ids, dtype):
     check(layer(*size, dtype, 5, ids))
 
 
+@pytest.mark.parametrize("dtype", TYPES[1:])
+@pytest.mark.parametrize("T", [1, 2, 16, 17, 32, 33, 47, 48, 49, 64])
+@pytest.mark.parametrize("N,D", [(1, 64), (50, 128), (640, 192), (100, 256), (330, 832), (48, 1024), (8193, 64), (8200, 1088)])
+def test_few_rows_of_whole_steps(T, N, D, dtype):
+    """These go through LDS: sums of fewer steps than wavefronts, of fewer and of more than there are stages."""
+    check(layer(T, N, D, 5, 24, dtype, T + N + D), (False, False, False, True))
+
+
+@pytest.mark.parametrize("dtype", TYPES[1:])
+@pytest.mark.parametrize("T", [7, 40])
+def test_few_rows_of_wider_ones(T, dtype):
+    """X and W with leading dimensions of their own, what lies between their rows not a number; Y's other columns stay."""
+    X, W, A, B, ids, scales, dY = layer(T, 200, 320, 4, 8, dtype, 8)
+    want, off = exact(X, W, A, B, ids, scales, dY)
+    wide = lambda m, more: torch.cat([m, torch.full((m.shape[0], more), float("nan"), device="cuda", dtype=dtype)], 1)[:, : m.shape[1]]
+    out = torch.full((T, 208), 3.0, device="cuda", dtype=dtype)
+    Y = tg.linear_adapters_forward(wide(X, 8), wide(W, 64), A, B, ids, scales=scales, out=out[:, :200])
+    close(Y, want[0], off[0])
+    assert bool((out[:, 200:] == 3).all())
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("T", [5, 70, 1100])
 @pytest.mark.parametrize("ids", [-1, 2])

@@ -380,7 +380,8 @@ tgemm_status_t forward(const Plan &p, const Layer &l, void *Y, int64_t ldy, floa
         if (e == hipSuccess && hidden != nullptr) e = launch_finish(s, hidden, nullptr, stream);
         if (e != hipSuccess) return from_hip(e);
         const FewArgs f{l.dtype, (int)l.T, (int)l.N, (int)l.D, l.X, l.ldx, l.W, l.ldw, Y, ldy,
-                        Expand{l.ids, l.scales, s.part, l.T * l.rank, s.parts, nullptr, stack_b(l)}};
+                        Expand{l.ids, l.scales, s.part, l.T * l.rank, s.parts, nullptr, stack_b(l)},
+                        as_stored(l.dtype, l.X, l.ldx, l.D, kStepK) && as_stored(l.dtype, l.W, l.ldw, l.D, kStepK)};
         return from_hip(launch_few(f, stream));
     }
     void *planes = in<void>(ws, p.hidden_planes);

@@ -105,6 +105,7 @@ struct FewArgs {
     void *Y;
     int64_t ldy;
     Expand e;
+    bool through_lds;  // 16-bit values, 16-byte aligned rows of whole steps of 64, ldx and ldw at most 2^22
 };
 hipError_t launch_few(const FewArgs &a, hipStream_t stream);
 

@@ -15,6 +15,7 @@ using m16::bf16x8;
 using m16::f32x4;
 using m16::Frag;
 using m16::kHeld;
+using m16::kStepK;
 using m16::lds_char;
 using m16::load_some;
 using m16::store_row;
@@ -410,6 +411,59 @@ __global__ __launch_bounds__(256) void adapted_sum_kernel(AddArgs a)
 
 // ---- a few rows ------------------------------------------------------------
 
+// The end of a few rows' products: wavefront n of S adds up the S parts of the
+// n-th blocks (row lane % 16, columns 4·(lane / 16) + r) and the adapters' part
+// on the vector units: there may be as many adapters as rows, and their loads
+// do not wait for one another.
+template <class In, int R, int COLS, int S, class Sum>
+__device__ __forceinline__ void finish_few(const FewArgs &a, int col0, int part, int lane, Sum sum)
+{
+    const int l16 = lane & 15, quarter = lane >> 4;
+    for (int n = part; n < R * COLS; n += S) {
+        const int i = n / COLS, j = n % COLS;
+        f32x4 v = sum(0, i, j);
+#pragma unroll
+        for (int s = 1; s < S; ++s) v += sum(s, i, j);
+        const int row = 16 * i + l16, col = col0 + 16 * j + 4 * quarter;
+        if (row >= a.T) continue;
+        const int id = id_of(a.e, row, a.T);
+        if (id >= 0) {
+            const In *c[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) c[r] = (const In *)a.e.c.p + id * a.e.c.stride + (int64_t)min(col + r, a.N - 1) * a.e.c.ld;
+            f32x4 more{0, 0, 0, 0};
+            for (int k = 0; k < a.e.c.rank; k += 8) {
+                In b[4][8];
+                float h[8];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) load_some<In, 8>(c[r] + k, a.e.c.rank - k, b[r]);
+                load_hidden(a.e, row, k, h);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) more[r] = fmaf(h[e], (float)b[r][e], more[r]);
+            }
+            const float factor = a.e.scales != nullptr ? a.e.scales[id] : 1.0f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = fmaf(factor, more[r], v[r]);
+        } else if (id == -2) {
+            v = f32x4{NAN, NAN, NAN, NAN};
+        }
+        In *to = (In *)a.Y + row * a.ldy + col;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (col + r < a.N) to[r] = (In)v[r];
+    }
+}
+
+// This wavefront's loads into LDS have arrived but for the last FLYING.
+template <int FLYING>
+__device__ __forceinline__ void arrived()
+{
+    static_assert(FLYING < 64, "six bits");
+    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(FLYING) : "memory");
+}
+
 // Fragments straight from device memory, no LDS stage and no barrier, as the
 // loss operators take a few rows: a wavefront takes COLS blocks of 16 columns of
 // the result, R blocks of 16 rows and an eighth of the sum, in steps of 64
@@ -417,7 +471,7 @@ __global__ __launch_bounds__(256) void adapted_sum_kernel(AddArgs a)
 // loads are whole cache lines.  Then each
 // lane adds its own rows' adapters on the vector units: there may be as many as
 // rows, and their matrices' loads do not wait for one another.
-constexpr int kFewParts = 8;
+constexpr int kFewParts = 8, kFewLdsParts = 4;
 template <class In, int R, int COLS>
 __global__ __launch_bounds__(64 * kFewParts) void adapted_few_kernel(FewArgs a)
 {
@@ -511,48 +565,116 @@ __global__ __launch_bounds__(64 * kFewParts) void adapted_few_kernel(FewArgs a)
 #pragma unroll
         for (int j = 0; j < COLS; ++j) sums[part][i][j][lane] = acc[i][j];
     __syncthreads();
-    // wavefront n finishes the n-th blocks: row l16, columns 4·quarter + r
-    for (int n = part; n < R * COLS; n += S) {
-        const int i = n / COLS, j = n % COLS;
-        f32x4 v = sums[0][i][j][lane];
+    finish_few<In, R, COLS, S>(a, col0, part, lane, [&](int s, int i, int j) { return sums[s][i][j][lane]; });
+}
+
+// The same on 16-bit operands with aligned rows of whole steps of 64.  A
+// fragment's load from device memory takes 16 bytes of 16 rows in turn and so
+// 16 bytes a clock of a compute unit: enough for W's way in once, not for X's
+// in every work-group.  Here both go straight to LDS in 128 adjacent bytes a row, into
+// `STAGES` stages of a wavefront's own, so that it waits for nobody and the loads
+// of all the stages are under way at once.  Wavefront n takes steps n, n + 4, ...
+// Bound by W's way from memory and, with more rows, by X's from the L2s.  With W
+// not in any cache (µs, T×N×D): 1×4096×4096 11.7 (2.9 TB/s), 16×4096×4096 11.6 against 14.5 straight from
+// memory, 48×8192×2048 15.9 against 17.6, 64×4096×4096 17.6 against 26.9,
+// 48×2048×8192 21.4 against 35.6; of these the adapters' part is 3 to 5.
+template <class In, int R, int COLS, int STAGES>
+__global__ __launch_bounds__(64 * kFewLdsParts) void adapted_few_lds_kernel(FewArgs a)
+{
+    constexpr int S = kFewLdsParts, kLoads = 2 * (R + COLS), kStage = kLoads * 1024;
+    typedef m16::Slice<16 * R, R, 64, false, false> SliceX;
+    typedef m16::Slice<16 * COLS, COLS, 64, false, false> SliceW;
+    static_assert(SliceX::kBytes + SliceW::kBytes == kStage && R * COLS <= kLoads * STAGES, "room");
+    __shared__ __align__(1024) char lds[S * STAGES * kStage];
+    const int lane = threadIdx.x & 63, part = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int col0 = blockIdx.x * (16 * COLS);
+    const char *x = (const char *)a.X, *w = (const char *)((const In *)a.W + col0 * a.ldw);
+    lds_char *own = (lds_char *)lds + part * STAGES * kStage;
+    m16::Loader<SliceX> lx;
+    m16::Loader<SliceW> lw;
 #pragma unroll
-        for (int s = 1; s < S; ++s) v += sums[s][i][j][lane];
-        const int row = 16 * i + l16, col = col0 + 16 * j + 4 * quarter;
-        if (row >= a.T) continue;
-        const int id = id_of(a.e, row, a.T);
-        if (id >= 0) {
-            const In *c[4];
+    for (int r = 0; r < 2 * R; ++r) lx.off[r] = SliceX::offset(r * 64 + lane, a.ldx, a.T - 1, kStepK);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) c[r] = (const In *)a.e.c.p + id * a.e.c.stride + (int64_t)min(col + r, a.N - 1) * a.e.c.ld;
-            f32x4 more{0, 0, 0, 0};
-            for (int k = 0; k < a.e.c.rank; k += 8) {
-                In b[4][8];
-                float h[8];
+    for (int r = 0; r < 2 * COLS; ++r) lw.off[r] = SliceW::offset(r * 64 + lane, a.ldw, a.N - 1 - col0, kStepK);
+    auto issue = [&](int stage, int step) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) load_some<In, 8>(c[r] + k, a.e.c.rank - k, b[r]);
-                load_hidden(a.e, row, k, h);
+        for (int r = 0; r < 2 * COLS; ++r) lw.issue_one(w + (int64_t)step * (2 * kStepK), own + stage * kStage + SliceX::kBytes, 0, r);
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
+        for (int r = 0; r < 2 * R; ++r) lx.issue_one(x + (int64_t)step * (2 * kStepK), own + stage * kStage, 0, r);
+    };
+    m16::Reader<16 * R, R, false, false> rx;
+    m16::Reader<16 * COLS, COLS, false, false> rw;
+    rx.place(0, lane);
+    rw.place(0, lane);
+    f32x4 acc[R][COLS];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) more[r] = fmaf(h[e], (float)b[r][e], more[r]);
-            }
-            const float factor = a.e.scales != nullptr ? a.e.scales[id] : 1.0f;
+    for (int i = 0; i < R; ++i)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = fmaf(factor, more[r], v[r]);
-        } else if (id == -2) {
-            v = f32x4{NAN, NAN, NAN, NAN};
+        for (int j = 0; j < COLS; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    const int steps = a.D / kStepK, count = part < steps ? (steps - part + S - 1) / S : 0;
+    // the work-groups of an XCD begin at steps apart: rows that lie a power of
+    // two apart would have them all at the same few of the L2's channels
+    int next = count > 0 ? (int)(blockIdx.x / m16::kXcds % (unsigned)count) : 0;
+    auto issue_next = [&](int stage) {
+        issue(stage, part + S * next);
+        if (++next == count) next = 0;
+    };
+#pragma unroll
+    for (int n = 0; n < STAGES; ++n)
+        if (n < count) issue_next(n);
+    int stage = 0;
+    for (int n = 0; n < count; ++n) {
+        // this stage's loads have arrived; those of the later ones may be under way
+        const int later = count - 1 - n;
+        if (later >= STAGES - 1) arrived<(STAGES - 1) * kLoads>();
+        else if (STAGES > 3 && later == 2) arrived<2 * kLoads>();
+        else if (later == 1) arrived<kLoads>();
+        else arrived<0>();
+        typename Frag<In>::type fx[2][R], fw[2][COLS];
+        lds_char *at = own + stage * kStage;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) fx[s][i] = rx.template read<In>(at, i, s);
+#pragma unroll
+            for (int j = 0; j < COLS; ++j) fw[s][j] = rw.template read<In>(at + SliceX::kBytes, j, s);
         }
-        In *to = (In *)a.Y + row * a.ldy + col;
+        // the stage has been read
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (n + STAGES < count) issue_next(stage);
+        if (++stage == STAGES) stage = 0;
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if (col + r < a.N) to[r] = (In)v[r];
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int j = 0; j < COLS; ++j) acc[i][j] = Frag<In>::mfma(fw[s][j], fx[s][i], acc[i][j]);
     }
+    // every wavefront's sums go where its stages were
+    f32x4 *sums = (f32x4 *)(lds + part * STAGES * kStage);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int j = 0; j < COLS; ++j) sums[(i * COLS + j) * 64 + lane] = acc[i][j];
+    __syncthreads();
+    finish_few<In, R, COLS, S>(a, col0, part, lane, [&](int s, int i, int j) {
+        return ((const f32x4 *)(lds + s * STAGES * kStage))[(i * COLS + j) * 64 + lane];
+    });
 }
 
 template <class In, int COLS>
 void few(const FewArgs &a, hipStream_t stream)
 {
     const unsigned grid = (unsigned)((a.N + 16 * COLS - 1) / (16 * COLS));
+    if constexpr (sizeof(In) == 2) {
+        if (a.through_lds) {
+            if (a.T <= 16) adapted_few_lds_kernel<In, 1, COLS, 4><<<grid, 64 * kFewLdsParts, 0, stream>>>(a);
+            else if (a.T <= 32) adapted_few_lds_kernel<In, 2, COLS, 4><<<grid, 64 * kFewLdsParts, 0, stream>>>(a);
+            else if (a.T <= 48) adapted_few_lds_kernel<In, 3, COLS, COLS == 1 ? 4 : 3><<<grid, 64 * kFewLdsParts, 0, stream>>>(a);
+            else adapted_few_lds_kernel<In, 4, COLS, 3><<<grid, 64 * kFewLdsParts, 0, stream>>>(a);
+            return;
+        }
+    }
     if (a.T <= 16) adapted_few_kernel<In, 1, COLS><<<grid, 64 * kFewParts, 0, stream>>>(a);
     else if (a.T <= 32) adapted_few_kernel<In, 2, COLS><<<grid, 64 * kFewParts, 0, stream>>>(a);
     else if (a.T <= 48) adapted_few_kernel<In, 3, COLS><<<grid, 64 * kFewParts, 0, stream>>>(a);
