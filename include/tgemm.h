@@ -1,6 +1,7 @@
 /*
- * libtgemm — single-precision C = A·B on one AMD Instinct MI355X (gfx950), and
- * two losses on such a product of an output head (declared last).
+ * libtgemm — single-precision C = A·B on one AMD Instinct MI355X (gfx950), and,
+ * declared last, two losses on such a product of an output head, a projection
+ * with low-rank adapters beside it, and updates made orthogonal.
  *
  * The operation is the dense product of page 1 ("[Multi-Core & GPU
  * Programming] CUDA - Matrix Multiplication", section [Matrix
@@ -491,10 +492,11 @@ tgemm_status_t tgemm_linear_kd_backward(tgemm_dtype_t dtype, int64_t T, int64_t 
  *
  * Types       float32, bf16 or fp16: X, W, A, B, Y and the gradients alike.
  *             Products of 16-bit values are exact and summed in float32, those
- *             of float32 ones by the planes of the loss operators (few rows and
- *             the adapters' part: in float32).  x·Aᵀ is float32; where it meets
- *             16-bit matrices it is held in two bf16 numbers (17 bits).  A
- *             result is rounded once.
+ *             of float32 ones by the planes of the loss operators or, where
+ *             that is faster, in float32 (few rows, few tiles, the adapters'
+ *             part).  x·Aᵀ is float32; where it meets 16-bit matrices in more
+ *             than 64 rows it is held in two bf16 numbers (17 bits).  A result
+ *             is rounded once.
  * Sizes       0 <= T < 2^24, 1 <= N, D <= 2^22, 1 <= count < 2^15, 1 <= rank <=
  *             1024, lda up to 2^26, the other leading dimensions and strides up
  *             to 2^40; larger ones, a product of 2^31 tiles and more, and an
@@ -515,7 +517,8 @@ tgemm_status_t tgemm_linear_kd_backward(tgemm_dtype_t dtype, int64_t T, int64_t 
  *             address: its row of Y and of dX is NaN, and dA and dB have
  *             nothing of it.
  * Rows        What one adapter holds, infinities and NaN too, reaches the rows
- *             of its own tokens alone.
+ *             of its own tokens alone.  An infinity may come out as NaN in the
+ *             values that it reaches.
  * Order       Sums are taken in a fixed order: the same call gives the same
  *             bits.  Every call can be captured into a graph.
  *

@@ -7,7 +7,8 @@ float32) their factors:
     y_t = x_t·Wᵀ + scales_i·(x_t·A_iᵀ)·B_iᵀ,  i = ids_t
 
 X, W, A and B have one type, float32, bfloat16 or float16, which the result and
-the gradients have too.
+the gradients have too; others, and mixed ones, raise TypeError (torch.autocast
+does not reach these calls).
 
 * ``linear_adapters`` is differentiable in X, W, A and B;
 * ``linear_adapters_forward`` and ``linear_adapters_backward`` are the same calls

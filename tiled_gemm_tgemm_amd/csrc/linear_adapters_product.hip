@@ -230,7 +230,10 @@ __device__ __forceinline__ void add_one(const ProductArgs &a, int adapter, int r
 // kMixed, each lane reads its own instead, which takes the vector units as long
 // as about three adapters take the loads' way there and back (in a 256×256
 // tile, whose registers do not hold that, they are taken one by one all the
-// same).  The bound on registers is that of kTiles' work-groups a compute unit.  Bound by the matrix cores, as the product alone is.
+// same).  The bound on registers is that of kTiles' work-groups a compute unit.
+// Bound by the matrix cores, as the product alone is: 8192×16384×4096 with 8
+// adapters of 32 ranks in runs 871 µs, 1.27 PFLOP/s (in random order 1306);
+// 2003×4096×4096 with 6 of 64 85 µs, 0.8 PFLOP/s, one round of 128×128 tiles.
 constexpr int kMixed = 3;
 template <class E, class C, int BM, int BN, int WM, int WN, bool B_MC, bool RANK_INNER>
 __global__ __launch_bounds__(64 * WM * WN, BM == 32 ? 3 : 2) void adapted_kernel(ProductArgs a)
@@ -345,7 +348,8 @@ __global__ __launch_bounds__(64 * WM * WN, BM == 32 ? 3 : 2) void adapted_kernel
 // ones, or 64 apart where a column's ranks are, so that a wavefront's loads of
 // an adapter lie side by side.  (In the tiles of a
 // split sum, which are few and short, the adapters' loads would be waited for:
-// 256×4096×4096 with 32 adapters 49 µs and 5 for the sum, against 22 and 13.)
+// 256×4096×4096 with 32 adapters 49 µs and 5 for the sum, against 23 and 7.5.)
+// Bound by the parts' and the adapters' loads (777×3000 float32 of one part with ranks of 10: 14 µs).
 template <class C, bool RANK_INNER>
 __global__ __launch_bounds__(256) void adapted_sum_kernel(AddArgs a)
 {

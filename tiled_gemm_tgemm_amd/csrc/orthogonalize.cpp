@@ -30,7 +30,7 @@ struct Stack {
 // first steps change X by little more than its factor, and what one plane
 // leaves out of the products does not show.  A bf16 result is rounded by 1.7e-3
 // (norms over norm); with one plane everywhere X's would carry 0.4e-3 to
-// 2.6e-3 besides (0.04 where X itself is held in one, on a matrix of rank 16
+// 2.6e-3 besides (23e-3 where X itself is held in one, on 256×1024 of rank 16
 // with noise of a hundredth), with the choice here 0.2e-3 to 0.6e-3.  One
 // plane in the first step alone is still too few for fp16 results (2.1e-4),
 // which it takes to 2.9e-4 on a matrix of rank 4 with noise.

