@@ -90,7 +90,9 @@ bool along_k(const Layer &l, const void *rows, int64_t ld, int64_t K, const Stac
 }
 
 // How the sums over K of the tokens' hidden values are cut: in parts while there
-// are fewer wavefronts than keep the memory busy.
+// are fewer wavefronts than keep the memory busy.  (With 8 parts at 16 to 64 row
+// blocks of 16 slots, as few rows take, 256, 512 and 1024 rows of 4096 of 32
+// adapters in random order 15, 24 and 44 µs, with 4, 2 and 2 12, 17 and 31.)
 struct Shrink {
     int64_t part_k = 0;
     int parts = 1, slots = 1, rows_each = 16;
@@ -101,17 +103,17 @@ Shrink shrink_of(int64_t T, int64_t K, int64_t count, bool through_lds)
     Shrink s;
     s.through_lds = through_lds && T > 1024;
     s.rows_each = T <= 1024 ? 16 : T < 4096 || s.through_lds ? 64 : 128;
+    s.slots = T <= 1024 ? 16 : 1;
+    if (s.slots > count) s.slots = (int)count;
     // (the workspace does not depend on how the adapters lie)
-    const int64_t wavefronts = 4 * ceil_div(T, T <= 1024 ? 16 : T < 4096 ? 64 : 128), most = T <= 1024 ? 8 : 16;
-    int64_t parts = 4096 / wavefronts;
+    int64_t parts = T <= 1024 ? 1024 / (ceil_div(T, 16) * s.slots) : 1024 / ceil_div(T, T < 4096 ? 64 : 128);
+    if (T <= 1024 && parts < 2) parts = 2;  // rows in runs leave all but one slot idle
     if (parts > ceil_div(K, 512)) parts = ceil_div(K, 512);
     if (K <= 1024 && T > kFewRows) parts = 1;  // not worth the launch that adds them up
-    if (parts > most) parts = most;
+    if (parts > (T <= 1024 ? 8 : 16)) parts = T <= 1024 ? 8 : 16;
     if (parts < 1) parts = 1;
     s.part_k = round_up(ceil_div(K, parts), 256);
     s.parts = (int)ceil_div(K, s.part_k);
-    s.slots = T <= 1024 ? 16 : 1;
-    if (s.slots > count) s.slots = (int)count;
     return s;
 }
 
