@@ -135,8 +135,8 @@ struct GroupArgs {
     Cut cuts[2];
 };
 hipError_t launch_group(const GroupArgs &a, hipStream_t stream);
-// Up to these one work-group does it, an adapter after the other (0.5 µs each),
-// next to the adapters' turn; the two launches that this spares take 10 µs.
+// Up to these one work-group does it next to the adapters' turn; the two launches
+// that this spares take 10 µs.
 constexpr int kAloneTokens = 8192, kAloneAdapters = 16;
 
 // out_i = scales[i]·sum over adapter i's tokens of rows(t, :)ᵀ·small(t, :), laid

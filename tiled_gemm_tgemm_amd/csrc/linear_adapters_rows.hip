@@ -439,7 +439,7 @@ __device__ __forceinline__ void cut_chunks(const GroupArgs &a, const Cut &cut, i
 {
     int chunk0 = 0, slot0 = 0;
     int64_t place0 = 0;
-    for (int i0 = 0; i0 < a.count; i0 += 1024) {
+    for (int i0 = 0; i0 < a.count; i0 += blockDim.x) {
         const int i = i0 + threadIdx.x;
         const int from = i < a.count ? a.starts[i] : 0, tokens = i < a.count ? a.starts[i + 1] - from : 0;
         const int chunks = (tokens + cut.tokens - 1) / cut.tokens, slots = chunks > 1 ? chunks : 0;
@@ -468,30 +468,61 @@ __global__ __launch_bounds__(1024) void chunks_kernel(GroupArgs a)
     cut_chunks(a, a.cuts[blockIdx.x], room);
 }
 
-// All of it by one work-group for a few tokens and adapters, whose ids it keeps
-// in registers: a launch less, and the adapters' turn goes with it.
-__device__ __forceinline__ void group_alone(const GroupArgs &a, int *room)
+// All of it by one work-group of THREADS for a few tokens and adapters: a launch
+// less, and the adapters' turn goes with it.  A thread takes adjacent tokens,
+// whose ids it keeps in registers, and counts them adapter by adapter; one
+// round through LDS gives it its places in each adapter's list.
+template <int THREADS>
+struct AloneRoom {
+    int place[kAloneAdapters][THREADS];
+    int waves[kAloneAdapters][THREADS / 64];
+    int scan[16];
+};
+template <int THREADS>
+__device__ __forceinline__ void group_alone(const GroupArgs &a, AloneRoom<THREADS> &room)
 {
-    int64_t id[kAloneTokens / 1024];
-    const int first = threadIdx.x * (kAloneTokens / 1024);
+    constexpr int kMost = kAloneTokens / THREADS, kWaves = THREADS / 64;
+    const int thread = threadIdx.x, lane = thread & 63, wave = thread >> 6;
+    const int each = (a.T + THREADS - 1) / THREADS, first = thread * each;
+    int id[kMost];
 #pragma unroll
-    for (int e = 0; e < kAloneTokens / 1024; ++e) id[e] = first + e < a.T ? a.ids[first + e] : -1;
+    for (int e = 0; e < kMost; ++e) {
+        const int64_t n = e < each && first + e < a.T ? a.ids[first + e] : -1;
+        id[e] = n >= 0 && n < a.count ? (int)n : -1;
+    }
+    for (int i = 0; i < a.count; ++i) {
+        int own = 0;
+#pragma unroll
+        for (int e = 0; e < kMost; ++e) own += id[e] == i;
+        int sum = own;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int other = __shfl_up(sum, d);
+            if (lane >= d) sum += other;
+        }
+        if (lane == 63) room.waves[i][wave] = sum;
+        room.place[i][thread] = sum - own;  // within the wavefront
+    }
+    __syncthreads();
     int start = 0;
     for (int i = 0; i < a.count; ++i) {
-        int own = 0, total;
+        int base = start;
 #pragma unroll
-        for (int e = 0; e < kAloneTokens / 1024; ++e) own += id[e] == i;
-        int at = start + before(own, room, total);
-#pragma unroll
-        for (int e = 0; e < kAloneTokens / 1024; ++e)
-            if (id[e] == i) a.order[at++] = first + e;
-        if (threadIdx.x == 0) a.starts[i] = start;
-        start += total;
+        for (int w = 0; w < kWaves; ++w) {
+            const int n = room.waves[i][w];
+            if (w < wave) base += n;
+            start += n;
+        }
+        if (thread == 0) a.starts[i + 1] = start;
+        room.place[i][thread] += base;
     }
-    if (threadIdx.x == 0) a.starts[a.count] = start;
+    if (thread == 0) a.starts[0] = 0;
+#pragma unroll
+    for (int e = 0; e < kMost; ++e)
+        if (id[e] >= 0) a.order[room.place[id[e]][thread]++] = first + e;
     __threadfence_block();
     __syncthreads();
-    for (int n = 0; n < 2; ++n) cut_chunks(a, a.cuts[n], room);
+    for (int n = 0; n < 2; ++n) cut_chunks(a, a.cuts[n], room.scan);
 }
 
 // ---- gradients -------------------------------------------------------------
@@ -831,42 +862,58 @@ __global__ __launch_bounds__(256) void outer_any_kernel(OuterArgs a)
     put_outer<In, BLOCKS, RANK_INNER>(a, chunk, col0 + 32 * wave, rank0, acc);
 }
 
-// Adapters without tokens get zeros, those of several chunks their sum, eight
-// loads at a time.  Bound by the start of its work-groups and the loads'
-// way there and back (8 adapters' 32×4096 in two or three chunks 17 µs).
+// Adapters without tokens get zeros, those of several chunks their sum, W
+// adjacent values a thread (whole rows of W) and eight loads at a time.
+template <class In, int W>
+__device__ __forceinline__ void join_chunks(const OuterArgs &a, int adapter, int2 join, int64_t inner, int64_t size)
+{
+    typedef float floats __attribute__((ext_vector_type(W)));
+    const float scale = a.scales != nullptr ? a.scales[adapter] : 1.0f;
+    for (int64_t n = ((int64_t)blockIdx.x * 256 + threadIdx.x) * W; n < size; n += (int64_t)gridDim.x * 256 * W) {
+        const float *from = a.part + join.x * size + n;
+        floats sum = 0;
+        for (int c = 0; c < join.y; c += 8) {
+            floats v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = c + e < join.y ? *(const floats *)(from + (c + e) * size) : (floats)0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum += v[e];
+        }
+        In *to = (In *)a.out + adapter * a.stride_out + n / inner * a.ldo + n % inner;
+        typename m16::Some<In, W>::type results;
+#pragma unroll
+        for (int e = 0; e < W; ++e) results[e] = (In)(join.y ? sum[e] * scale : 0.0f);
+        *(typename m16::Some<In, W>::type *)to = results;
+    }
+}
+
+// Bound by the start of its work-groups and the loads' way there and back (8
+// adapters' 32×4096 in two or three chunks, their 32×16384 in one: 9 µs).
 template <class In>
 __global__ __launch_bounds__(256) void join_kernel(OuterArgs first, OuterArgs second)
 {
     const OuterArgs &a = blockIdx.z == 0 ? first : second;
     if (a.out == nullptr) return;
-    const int adapter = blockIdx.y;
-    const int2 join = a.cut.joins[adapter];
+    const int2 join = a.cut.joins[blockIdx.y];
     if (join.y == 1) return;
-    const float scale = a.scales != nullptr ? a.scales[adapter] : 1.0f;
-    const int64_t inner = a.rank_inner ? a.rank : a.C, outer = a.rank_inner ? a.C : a.rank, size = inner * outer;
-    for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < size; n += (int64_t)gridDim.x * 256) {
-        const float *from = a.part + join.x * size + n;
-        float sum = 0;
-        for (int c = 0; c < join.y; c += 8) {
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = c + e < join.y ? from[(c + e) * size] : 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sum += v[e];
-        }
-        ((In *)a.out)[adapter * a.stride_out + n / inner * a.ldo + n % inner] = (In)(join.y ? sum * scale : 0.0f);
-    }
+    const int64_t inner = a.rank_inner ? a.rank : a.C, size = inner * (a.rank_inner ? a.C : a.rank);
+    if (inner % 4 == 0) join_chunks<In, 4>(a, blockIdx.y, join, inner, size);
+    else join_chunks<In, 1>(a, blockIdx.y, join, inner, size);
 }
 
-// The adapters the other way round, 64×64 elements at a time through LDS; the
-// last work-group along x of the first adapter groups the tokens if `grouping`.
+// The adapters the other way round, 64×64 elements at a time through LDS, four
+// adjacent ones a load and store; the last work-group along x of the first
+// adapter groups the tokens if `grouping`, which takes longest: 8 adapters of 32
+// ranks and 4096 and 16384 columns with 8192 tokens 25 µs, 3 with 777 tokens and
+// nothing to turn 10.5.
+constexpr int kTurn = 256;
 template <class In>
-__global__ __launch_bounds__(1024) void turn_kernel(TurnArgs first, TurnArgs second, GroupArgs group, bool grouping)
+__global__ __launch_bounds__(kTurn) void turn_kernel(TurnArgs first, TurnArgs second, GroupArgs group, bool grouping)
 {
     __shared__ In tile[64][65];
-    __shared__ int room[16];
+    __shared__ AloneRoom<kTurn> room;
     if (grouping && blockIdx.x + 1 == gridDim.x) {
-        if (blockIdx.z == 0) group_alone(group, room);
+        if (blockIdx.z == 0) group_alone<kTurn>(group, room);
         return;
     }
     const bool other = blockIdx.z >= (unsigned)first.from.count;
@@ -879,13 +926,31 @@ __global__ __launch_bounds__(1024) void turn_kernel(TurnArgs first, TurnArgs sec
     In *to = (In *)a.to + adapter * a.to_stride;
     for (int64_t n = blockIdx.x; n < tiles; n += gridDim.x - (grouping ? 1 : 0)) {
         const int64_t r0 = n / across * 64, c0 = n % across * 64;
+        In v[1024 / kTurn][4];
 #pragma unroll
-        for (int e = threadIdx.x; e < 4096; e += 1024)
-            if (r0 + e / 64 < rows && c0 + e % 64 < cols) tile[e / 64][e % 64] = from[(r0 + e / 64) * a.from.ld + c0 + e % 64];
+        for (int u = 0; u < 1024 / kTurn; ++u) {
+            const int e = u * kTurn + threadIdx.x, r = e / 16, c = e % 16 * 4;
+            const bool there = r0 + r < rows && c0 + c < cols;
+            m16::load_some<In, 4>(from + (there ? (r0 + r) * a.from.ld + c0 + c : 0), there ? cols - c0 - c : 0, v[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < 1024 / kTurn; ++u) {
+            const int e = u * kTurn + threadIdx.x, r = e / 16, c = e % 16 * 4;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) tile[r][c + x] = v[u][x];
+        }
         __syncthreads();
 #pragma unroll
-        for (int e = threadIdx.x; e < 4096; e += 1024)
-            if (c0 + e / 64 < cols && r0 + e % 64 < rows) to[(c0 + e / 64) * a.to_ld + r0 + e % 64] = tile[e % 64][e / 64];
+        for (int u = 0; u < 1024 / kTurn; ++u) {
+            const int e = u * kTurn + threadIdx.x, r = e / 16, c = e % 16 * 4;
+            if (c0 + r >= cols || r0 + c >= rows) continue;
+            In *at = to + (c0 + r) * a.to_ld + r0 + c;
+            typename m16::Some<In, 4>::type four;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) four[x] = tile[c + x][r];
+            // (rows of the copy are whole 8s; past the last of them lies nothing that is read)
+            *(typename m16::Some<In, 4>::type *)at = four;
+        }
         __syncthreads();
     }
 }
@@ -961,8 +1026,8 @@ hipError_t launch_arrange(const OuterArgs &a, const OuterArgs &b, hipStream_t st
 
 hipError_t launch_join(const OuterArgs &a, const OuterArgs &b, hipStream_t stream)
 {
-    const int64_t C = a.C > b.C ? a.C : b.C, blocks = (C * a.rank + 255) / 256;
-    const dim3 grid((unsigned)(blocks < 1024 ? blocks : 1024), a.count, 2);
+    const int64_t C = a.C > b.C ? a.C : b.C, each = a.rank % 4 == 0 && a.C % 4 == 0 ? 1024 : 256, blocks = (C * a.rank + each - 1) / each;
+    const dim3 grid((unsigned)(blocks < 256 ? blocks : 256), a.count, 2);
     if (a.dtype == TGEMM_F32) join_kernel<float><<<grid, 256, 0, stream>>>(a, b);
     else if (a.dtype == TGEMM_BF16) join_kernel<__bf16><<<grid, 256, 0, stream>>>(a, b);
     else join_kernel<_Float16><<<grid, 256, 0, stream>>>(a, b);
@@ -981,8 +1046,8 @@ hipError_t launch_turn(const TurnArgs &a, const TurnArgs &b, const GroupArgs *gr
     const int64_t outer = a.outer > b.outer ? a.outer : b.outer, tiles = turning ? (outer + 63) / 64 * ((a.from.rank + 63) / 64) : 0;
     const dim3 grid((unsigned)(tiles < 1024 ? tiles : 1024) + (here ? 1 : 0), 1, turning ? a.from.count + b.from.count : 1);
     const GroupArgs g = here ? *group : GroupArgs{};
-    if (a.dtype == TGEMM_F32) turn_kernel<float><<<grid, 1024, 0, stream>>>(a, b, g, here);
-    else turn_kernel<uint16_t><<<grid, 1024, 0, stream>>>(a, b, g, here);
+    if (a.dtype == TGEMM_F32) turn_kernel<float><<<grid, kTurn, 0, stream>>>(a, b, g, here);
+    else turn_kernel<uint16_t><<<grid, kTurn, 0, stream>>>(a, b, g, here);
     return hipGetLastError();
 }
 
