@@ -312,11 +312,21 @@ def test_gradients_against_differences(T):
 
 @pytest.mark.parametrize("T", [30, 200, 1500])
 def test_captured_and_replayed(T):
-    sizes, dtype = (T, 128, 192, 3, 8), torch.bfloat16
+    captured((T, 128, 192, 3, 8), torch.bfloat16)
+
+
+@pytest.mark.parametrize("sizes", [(50, 100, 90, 3, 8), (300, 200, 1000, 20, 6), (2100, 1000, 520, 3, 10)])
+def test_captured_and_replayed_in_float32(sizes):
+    """Few rows, the float32 product in parts, and the planes' product."""
+    captured(sizes, torch.float32)
+
+
+def captured(sizes, dtype):
+    T, N, _, _, r = sizes
     args = layer(*sizes, dtype, 13)
     X, W, A, B, ids, scales, dY = args
-    hidden = torch.empty(T, 8, device="cuda")
-    out = torch.empty(T, 128, device="cuda", dtype=dtype)
+    hidden = torch.empty(T, r, device="cuda")
+    out = torch.empty(T, N, device="cuda", dtype=dtype)
     grads = [torch.empty_like(t) for t in (X, W, A, B)]
 
     def step():
