@@ -579,9 +579,10 @@ size_t tgemm_linear_adapters_workspace_size(tgemm_dtype_t dtype, int64_t T, int6
  *             summed in float32, and |G| in float64.  bf16 results take fewer
  *             products of planes: their error is that of their own rounding
  *             and up to half as much besides; float32 ones are as close as a
- *             chain of float32 products.  Entries of X, S or b·S + c·S·S
- *             beyond 60 overflow there, which coefficients that let singular
- *             values grow can come to.
+ *             chain of float32 products.  Entries of X, S, b·S + c·S·S or, where
+ *             a lies within -16 ... 16, a·I + b·S + c·S·S beyond 60 overflow
+ *             there, which coefficients that let singular values grow can come
+ *             to (a itself may be of any size).
  * coefficients  3·steps floats in host memory: a, b, c of each step.
  * Sizes       0 <= batch <= 65535, M and N up to 2^20, 1 <= steps <= 32,
  *             leading dimensions and strides up to 2^40; larger ones, batches

@@ -17,6 +17,7 @@ constexpr int64_t kMaxSide = (int64_t)1 << 20;   // a tile's offsets fit 32 bits
 constexpr int64_t kMaxBatch = 65535;             // a launch's y
 constexpr int64_t kMaxLd = (int64_t)1 << 40;
 constexpr int64_t kMaxTiles = INT32_MAX - 1024;
+constexpr float kMostFolded = 16.0f;             // a larger a stays out of Q's planes, which hold up to 64
 
 struct Stack {
     tgemm_dtype_t dtype;
@@ -313,8 +314,8 @@ tgemm_status_t run_chain(const Plan &p, const Stack &g, const void *G, int64_t l
         a.batch_add = 2 * s_plane;
         a.alpha = k[1];
         a.beta = k[2] * one;
-        // three products of planes hold as much of a·X as its planes do
-        const bool folded = n.x == 3;
+        // three products of planes hold as much of a·X as its planes do, while a is no more than what else they hold
+        const bool folded = n.x == 3 && k[0] >= -kMostFolded && k[0] <= kMostFolded;
         a.diagonal = folded ? k[0] * (1 << kShift) : 0.0f;
         a.planes = q;
         e = run(kRows, c.q, a, stream);

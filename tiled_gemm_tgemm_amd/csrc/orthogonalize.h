@@ -16,10 +16,11 @@ namespace ortho {
 
 // ---- the chain of products -------------------------------------------------
 
-// X, S = X·Xᵀ and Q = b·S + c·S² are held as 2^kShift times their values in two
-// fp16 planes (high, low: 22 bits, down to 2^-35 of 1).  The entries of all
-// three are below 2 for coefficients that keep the singular values near 1, so
-// this leaves a factor of 30 before they overflow.
+// X, S = X·Xᵀ and Q = b·S + c·S² (+ a·I) are held as 2^kShift times their values
+// in two fp16 planes (high, low: 22 bits, down to 2^-35 of 1), which overflow
+// past 64.  With the coefficients 3.4445, -4.7750, 2.0315 singular values stay
+// below 1.21, entries of X and S thus below 1.5 and those of Q below 2.9 without
+// a·I (the polynomial's least value on [0, 1.5] is -2.81) and 3.45 with it.
 constexpr int kShift = 10;
 
 // Operands of a batch of products.  Two planes an operand; three segments are
