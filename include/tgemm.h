@@ -575,14 +575,16 @@ size_t tgemm_linear_adapters_workspace_size(tgemm_dtype_t dtype, int64_t T, int6
  * Types       float32, bf16 or fp16, G and out alike.
  * Arithmetic  Where the smaller side is at most 64 the iteration runs on G·Gᵀ in
  *             float64.  Otherwise X, S and b·S + c·S·S are held in two fp16
- *             planes (22 bits, and no finer than 2^-35 of 1), products are
- *             summed in float32, and |G| in float64.  bf16 results take fewer
- *             products of planes: their error is that of their own rounding
- *             and up to half as much besides; float32 ones are as close as a
- *             chain of float32 products.  Entries of X, S, b·S + c·S·S or, where
- *             a lies within -16 ... 16, a·I + b·S + c·S·S beyond 60 overflow
- *             there, which coefficients that let singular values grow can come
- *             to (a itself may be of any size).
+ *             planes (22 bits, and no finer than 2^-35 of 1), every product is
+ *             three of planes, summed in float32, and |G| is summed in float64:
+ *             results of all types are as close as a chain of float32 products
+ *             before their own rounding.  (Where a relative change of X changes
+ *             the result f times as much, up to about f·2^-22 besides: f is 1 to
+ *             a few hundred, but tens of thousands where coefficients without a
+ *             margin meet a singular value at the end of their range.)  Entries
+ *             of X, S, b·S + c·S·S or, where a lies within -16 ... 16, a·I + b·S +
+ *             c·S·S beyond 60 overflow there, which coefficients that let
+ *             singular values grow can come to (a itself may be of any size).
  * coefficients  3·steps floats in host memory: a, b, c of each step.
  * Sizes       0 <= batch <= 65535, M and N up to 2^20, 1 <= steps <= 32,
  *             leading dimensions and strides up to 2^40; larger ones, batches

@@ -25,27 +25,21 @@ struct Stack {
     int steps;
 };
 
-// How many products of planes the three products of step `step` take.
-//
-// X is held in two planes throughout.  While the singular values are small, the
-// first steps change X by little more than its factor, and what one plane
-// leaves out of the products does not show.  A bf16 result is rounded by 1.7e-3
-// (norms over norm); with one plane everywhere X's would carry 0.4e-3 to
-// 2.6e-3 besides (23e-3 where X itself is held in one, on 256×1024 of rank 16
-// with noise of a hundredth), with the choice here 0.2e-3 to 0.6e-3.  One
-// plane in the first step alone is still too few for fp16 results (2.1e-4),
-// which it takes to 2.9e-4 on a matrix of rank 4 with noise.
-struct Segments {
-    int s, q, x;
-};
-Segments segments_of(tgemm_dtype_t dtype, int step)
-{
-    if (dtype == TGEMM_BF16) return step < 2 ? Segments{1, 1, 1} : Segments{1, 3, 3};
-    return Segments{3, 3, 3};
-}
+// Every product takes three of planes, in every step and for every type.  A
+// bf16 result's own rounding is 1.7e-3 (norms over norm), but one plane left out
+// anywhere can show beside it: values that are alike are rounded alike, and what
+// that changes in a dominant direction the polynomial makes several times as
+// large.  Of the rounding's error, the roundings followed on the host: with one
+// plane for S alone, from the third step on, 256×1024 of one large value a row
+// 2.7 times and an orthogonal 384×384 1.4; with one in the first two steps 1 +
+// 0.001·normal values of 384×384 1.4 to 3.9, by the coefficients, and 70×300 of
+// rank 1 with noise of a thousandth up to 340; with three 1.0 in all of these.
+// Two of the three cost bf16 8192×8192 26.8 ms instead of 17.2, 8×1024×4096 2.05
+// instead of 1.40 and 256×1024 0.20 instead of 0.16.
+constexpr int kSegments = 3;
 
-// The tile for `batch` M×N products of `steps` steps (of `segments` each),
-// whether only the tiles on and below the diagonal are formed, and into how many
+// The tile for `batch` M×N products of `steps` steps (of kSegments each), whether
+// only the tiles on and below the diagonal are formed, and into how many
 // parts the sums of the tiles are split that do not fill the GPU a last time:
 // the least estimated time, in µs.
 //
@@ -65,7 +59,7 @@ struct Choice {
 };
 constexpr double kStep[kTileCount][4] = {{1.2}, {0.57, 0.95}, {0.33, 0.45, 0.62, 0.8}};
 constexpr double kBegin[kTileCount] = {22.0, 10.0, 6.5}, kBeginPart[kTileCount] = {15.0, 8.0, 5.0}, kAcross[kTileCount] = {8.0, 1.5, 0.7};
-Choice choose(int64_t M, int64_t N, int64_t steps, int segments, int64_t batch, bool symmetric)
+Choice choose(int64_t M, int64_t N, int64_t steps, int64_t batch, bool symmetric)
 {
     Choice best;
     double least = -1;
@@ -77,10 +71,10 @@ Choice choose(int64_t M, int64_t N, int64_t steps, int segments, int64_t batch, 
             const int64_t tiles = (lower ? m * (m + 1) / 2 : m * n) * batch, most = (int64_t)256 * s.wg_per_cu;
             auto rounds = [&](int64_t tiles, int64_t steps, double begin) {
                 const int64_t on_one = ceil_div(tiles, 256), rest = on_one % s.wg_per_cu;
-                auto round = [&](int64_t held) { return (double)(steps * segments) * kStep[i][held - 1] + begin; };
+                auto round = [&](int64_t held) { return (double)(steps * kSegments) * kStep[i][held - 1] + begin; };
                 const double time = (double)(on_one / s.wg_per_cu) * round(s.wg_per_cu) + (rest ? round(rest) : 0.0);
                 const double area = (double)(tiles * s.side) * s.side;
-                const double power = area * (double)(steps * segments * kStepK) * 2.0 / 1.3e9 + begin;
+                const double power = area * (double)(steps * kSegments * kStepK) * 2.0 / 1.3e9 + begin;
                 return tiles == 0 ? 0.0 : (time > power ? time : power) + 0.1 * power;
             };
             for (int64_t whole : {tiles, tiles / most * most}) {
@@ -116,6 +110,7 @@ struct Plan {
     int parts = 0;
     int64_t x_rows = 0, x_ld = 0;
     int64_t squares = -1, x[2] = {-1, -1}, s = -1, q = -1, parts_room = -1;
+    Choice product_s, product_q, product_x;  // of every step
     // the small side's
     int64_t part_length = 0, grams = -1, factor = -1;
 
@@ -128,18 +123,6 @@ struct Plan {
 };
 
 int64_t parts_bytes(const Choice &c) { return (int64_t)c.rest * c.splits * kTiles[c.tile].side * kTiles[c.tile].side * 4; }
-
-// The choices for a step's three products.
-struct Choices {
-    Choice s, q, x;
-};
-Choices choices(const Plan &p, const Stack &g, int step)
-{
-    const Segments n = segments_of(g.dtype, step);
-    return Choices{choose(p.side, p.side, p.length_p / kStepK, n.s, g.batch, true),
-                   choose(p.side, p.side, p.side_p / kStepK, n.q, g.batch, true),
-                   choose(g.M, g.N, p.side_p / kStepK, n.x, g.batch, false)};
-}
 
 bool make_plan(Plan &p, const Stack &g)
 {
@@ -169,13 +152,13 @@ bool make_plan(Plan &p, const Stack &g)
     if (g.steps > 1) p.x[1] = p.take(x);
     p.s = p.take(s);
     p.q = p.take(s);
+    p.product_s = choose(p.side, p.side, p.length_p / kStepK, g.batch, true);
+    p.product_q = choose(p.side, p.side, p.side_p / kStepK, g.batch, true);
+    p.product_x = choose(g.M, g.N, p.side_p / kStepK, g.batch, false);
     int64_t room = 0;
-    for (int step = 0; step < g.steps && step < 3; ++step) {  // no further kinds of steps
-        const Choices c = choices(p, g, step);
-        for (const Choice *one : {&c.s, &c.q, &c.x}) {
-            if (one->tile < 0) return false;
-            if (parts_bytes(*one) > room) room = parts_bytes(*one);
-        }
+    for (const Choice *one : {&p.product_s, &p.product_q, &p.product_x}) {
+        if (one->tile < 0) return false;
+        if (parts_bytes(*one) > room) room = parts_bytes(*one);
     }
     p.parts_room = p.take(room);
     return true;
@@ -190,10 +173,10 @@ tgemm_status_t check(const Stack &g, float eps)
     return TGEMM_SUCCESS;
 }
 
-Chain product(int64_t M, int64_t N, int64_t steps, int segments, const Choice &c)
+Chain product(int64_t M, int64_t N, int64_t steps, const Choice &c)
 {
     Chain o{};
-    o.segments = segments;
+    o.segments = kSegments;
     o.M = (int)M;
     o.N = (int)N;
     o.steps = (int)steps;
@@ -277,15 +260,13 @@ tgemm_status_t run_chain(const Plan &p, const Stack &g, const void *G, int64_t l
     const float one = 1.0f / (1 << kShift);
     void *s = in<void>(ws, p.s), *q = in<void>(ws, p.q);
     for (int step = 0; step < g.steps; ++step) {
-        const Segments n = segments_of(g.dtype, step);
         const float *k = coefficients + 3 * step;
         void *x = in<void>(ws, p.x[step & 1]);
 
         const int64_t s_steps = p.length_p / kStepK, q_steps = p.side_p / kStepK;
-        const Choices c = choices(p, g, step);
         ChainArgs a{};
         a.parts = in<float>(ws, p.parts_room);
-        a.op = product(p.side, p.side, s_steps, n.s, c.s);
+        a.op = product(p.side, p.side, s_steps, p.product_s);
         a.op.A = a.op.B = x;
         a.op.lda = a.op.ldb = p.x_ld;
         a.op.plane_a = a.op.plane_b = x_plane;
@@ -298,10 +279,10 @@ tgemm_status_t run_chain(const Plan &p, const Stack &g, const void *G, int64_t l
         a.plane_out = s_plane;
         a.batch_out = 2 * s_plane;
         a.rows = (int)p.side;
-        e = run(p.tall ? kColumns : kRows, c.s, a, stream);
+        e = run(p.tall ? kColumns : kRows, p.product_s, a, stream);
         if (e != hipSuccess) return from_hip(e);
 
-        a.op = product(p.side, p.side, q_steps, n.q, c.q);
+        a.op = product(p.side, p.side, q_steps, p.product_q);
         a.op.A = a.op.B = s;
         a.op.lda = a.op.ldb = p.side_p;
         a.op.plane_a = a.op.plane_b = s_plane;
@@ -314,14 +295,14 @@ tgemm_status_t run_chain(const Plan &p, const Stack &g, const void *G, int64_t l
         a.batch_add = 2 * s_plane;
         a.alpha = k[1];
         a.beta = k[2] * one;
-        // three products of planes hold as much of a·X as its planes do, while a is no more than what else they hold
-        const bool folded = n.x == 3 && k[0] >= -kMostFolded && k[0] <= kMostFolded;
+        // Q's planes hold as much of a·X as X's do, while a is no more than what else they hold
+        const bool folded = k[0] >= -kMostFolded && k[0] <= kMostFolded;
         a.diagonal = folded ? k[0] * (1 << kShift) : 0.0f;
         a.planes = q;
-        e = run(kRows, c.q, a, stream);
+        e = run(kRows, p.product_q, a, stream);
         if (e != hipSuccess) return from_hip(e);
 
-        a.op = product(g.M, g.N, q_steps, n.x, c.x);
+        a.op = product(g.M, g.N, q_steps, p.product_x);
         a.op.A = p.tall ? x : q;
         a.op.lda = p.tall ? p.x_ld : p.side_p;
         a.op.plane_a = p.tall ? x_plane : s_plane;
@@ -354,7 +335,7 @@ tgemm_status_t run_chain(const Plan &p, const Stack &g, const void *G, int64_t l
             a.batch_r = batch_o;
             a.dtype = g.dtype;
         }
-        e = run(p.tall ? kRows : kMixed, c.x, a, stream);
+        e = run(p.tall ? kRows : kMixed, p.product_x, a, stream);
         if (e != hipSuccess) return from_hip(e);
     }
     return TGEMM_SUCCESS;

@@ -23,8 +23,8 @@ namespace ortho {
 // a·I (the polynomial's least value on [0, 1.5] is -2.81) and 3.45 with it.
 constexpr int kShift = 10;
 
-// Operands of a batch of products.  Two planes an operand; three segments are
-// (low, high), (high, low), (high, high), one is (high, high).  lower: tiles on
+// Operands of a batch of products.  Two planes an operand; the three segments are
+// (low, high), (high, low), (high, high).  lower: tiles on
 // and below the diagonal only (square tiles).  The batch's tiles, matrix by
 // matrix, are numbered through; a launch takes `count` of them from `from` on,
 // each with its sum in `splits` parts.  What the epilogue is told as the part
