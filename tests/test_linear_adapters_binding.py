@@ -1,0 +1,65 @@
+"""The adapters' torch calls without a GPU, as test_linear_loss_binding has the
+losses': tensors of the host stand in for the device's, and the library's entry
+points are replaced by ones that look at what they are handed."""
+
+import types
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import tiled_gemm_tgemm_amd as tg  # noqa: E402
+from test_linear_loss_binding import Host  # noqa: E402
+from tiled_gemm_tgemm_amd import _lib  # noqa: E402
+
+T, N, D, L, R = 6, 11, 8, 3, 2
+IDS, HIDDEN = 16, 20  # where a forward call's arguments have them
+
+
+class Library(Host):
+    def __getattr__(self, name):
+        if name == "tgemm_linear_adapters_workspace_size":
+            return lambda *args: 1 << 12
+        return super().__getattr__(name)
+
+
+@pytest.fixture
+def host(monkeypatch):
+    h = Library()
+    contiguous = torch.Tensor.contiguous
+    monkeypatch.setattr(_lib, "library", lambda: h)
+    monkeypatch.setattr(torch, "empty", h.empty)
+    monkeypatch.setattr(torch.Tensor, "contiguous", lambda t: t if t.is_contiguous() else h.copy(contiguous(t)))
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: True), raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: types.SimpleNamespace(cuda_stream=h.stream))
+    monkeypatch.setattr(tg, "_hold_for_stream", lambda stream, device, *tensors: None)
+    return h
+
+
+def layer():
+    g = torch.Generator().manual_seed(1)
+    n = lambda *s: torch.randn(s, generator=g)
+    return n(T, D), n(N, D), n(L, R, D), n(L, N, R), torch.arange(T) % (L + 1) - 1
+
+
+@pytest.mark.parametrize("strided", [False, True])
+def test_a_node_called_under_another_stream_runs_there(host, strided, monkeypatch):
+    recorded = []
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append((t.data_ptr(), s.cuda_stream)), raising=False)
+    X, W, A, B, ids = layer()
+    if strided:
+        ids = ids.repeat_interleave(2)[::2]
+    Y = tg.linear_adapters(X, W, A.requires_grad_(), B.requires_grad_(), ids)
+    forward = host.calls[-1][1]
+    assert (forward[IDS] == ids.data_ptr()) != strided and forward[HIDDEN]
+    first = host.stream
+    torch.autograd.grad(Y, (A, B), torch.ones(T, N), retain_graph=True)
+    assert host.calls[-1][1][-1] == first and not recorded
+    host.stream = 1 << 46
+    Y.grad_fn.apply(torch.ones(T, N))
+    name, args = host.calls[-1]
+    assert name.endswith("backward") and args[-1] == host.stream and args[IDS] == forward[IDS]
+    # what the forward pass allocated on its own stream is known to be in use on this one, and nothing of the caller's
+    own = [forward[HIDDEN]] + [forward[IDS]] * strided
+    assert sorted(recorded) == sorted((at, host.stream) for at in own)

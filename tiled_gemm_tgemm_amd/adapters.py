@@ -81,11 +81,11 @@ class _Call:
         self.adapters = (self.L, self.r, A.data_ptr(), lda, stride_a, B.data_ptr(), ldb, stride_b, ids.data_ptr(),
                          _ptr(scales))
 
-    def again(self, X, W, A, B, ids, scales, hidden):
+    def again(self, X, W, A, B, ids, scales, *kept):
         """The call of a backward pass: the same tensors, wherever and however they are stored by now, on the stream
         that is torch's current one (its engine makes that the forward pass's; a node that is called by hand runs where
-        its caller is).  It is the pass's own: others may go through the same node meanwhile.  hidden: what the forward
-        pass allocated, or None."""
+        its caller is).  It is the pass's own: others may go through the same node meanwhile.  kept: what the forward
+        pass allocated."""
         import torch
 
         c = _Call.__new__(_Call)
@@ -93,8 +93,9 @@ class _Call:
         current = torch.cuda.current_stream(c.device)
         if current.cuda_stream != c.stream:
             c.stream = current.cuda_stream
-            if hidden is not None:
-                hidden.record_stream(current)
+            for t in kept:
+                if t is not None:
+                    t.record_stream(current)
         ldx = _rows(X, "X", (c.T, c.D), c.device, c.dtype)
         c.head = (*c.head[:4], X.data_ptr(), ldx, W.data_ptr(), _rows(W, "W", (c.N, c.D), c.device, c.dtype))
         c.adapters = (c.L, c.r, A.data_ptr(), *_stacked(A, "A", (c.L, c.r, c.D), c.device, c.dtype), B.data_ptr(),
@@ -213,7 +214,8 @@ def _function():
         def forward(ctx, X, W, A, B, ids, scales):
             # (a copy that the call makes of ids stands in for it in the backward pass)
             c = _Call(X, W, A, B, ids, scales, None)
-            if c.made:
+            ctx.copied = bool(c.made)
+            if ctx.copied:
                 ids = c.made[0]
             Y = torch.empty((c.T, c.N), dtype=c.dtype, device=c.device)
             hidden = torch.empty((c.T, c.r), dtype=torch.float32, device=c.device) if ctx.needs_input_grad[3] else None
@@ -226,7 +228,7 @@ def _function():
         @once_differentiable
         def backward(ctx, dY):
             X, W, A, B, ids, scales, hidden = ctx.saved_tensors
-            c = ctx.call.again(X, W, A, B, ids, scales, hidden)
+            c = ctx.call.again(X, W, A, B, ids, scales, hidden, ids if ctx.copied else None)
             if not dY.is_contiguous():
                 dY = dY.contiguous()
             return (*_backward(c, dY, hidden, (None,) * 4, ctx.needs_input_grad[:4], None), None, None)
