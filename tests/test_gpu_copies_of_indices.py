@@ -39,3 +39,14 @@ def test_adapters(T):
     leaves = [t.clone().requires_grad_() for t in (X, W, A, B)]
     got = backward_under_a_late_stream(lambda: tg.linear_adapters(*leaves, strided(ids), scales=scales), dY)
     assert all(torch.equal(a, b) for a, b in zip(got[:4], want))
+
+
+def test_cross_entropy():
+    T, V, D = 600, 9000, 256
+    g = torch.Generator(device="cuda").manual_seed(42)
+    X, W = (torch.randn(s, generator=g, device="cuda").bfloat16().requires_grad_() for s in ((T, D), (V, D)))
+    target = torch.randint(0, V, (T,), generator=g, device="cuda")
+    one = torch.ones((), device="cuda")
+    want = torch.autograd.grad(tg.linear_cross_entropy(X, W, target), (X, W), one)
+    got = backward_under_a_late_stream(lambda: tg.linear_cross_entropy(X, W, strided(target)), one)
+    assert all(torch.equal(a, b) for a, b in zip(got[:2], want))

@@ -343,6 +343,7 @@ def _functions():
         def forward(ctx, X, W, target, ignore_index, reduction, keep):
             c = _Call(X, W, None)
             target = c.target(target)
+            ctx.copied = bool(c.made)
             loss, kept, at = c.results(reduction)
             logits = c.keep(keep) if any(ctx.needs_input_grad) else None
             c.queue("tgemm_linear_ce_forward", target.data_ptr(), int(ignore_index), *at[:2], *c.logits(logits), at[2],
@@ -355,7 +356,7 @@ def _functions():
         @once_differentiable
         def backward(ctx, grad):
             X, W, target, lse, summary, logits = ctx.saved_tensors
-            c = ctx.call.again(X, W, lse, summary, logits)
+            c = ctx.call.again(X, W, lse, summary, logits, target if ctx.copied else None)
             dX, dW, rest = gradients(ctx, grad, c, summary)
             c.queue("tgemm_linear_ce_backward", target.data_ptr(), ctx.ignore_index, lse.data_ptr(), *c.logits(logits),
                     *rest, *c.room(None, 0, 1))
