@@ -63,3 +63,26 @@ def test_a_node_called_under_another_stream_runs_there(host, strided, monkeypatc
     # what the forward pass allocated on its own stream is known to be in use on this one, and nothing of the caller's
     own = [forward[HIDDEN]] + [forward[IDS]] * strided
     assert sorted(recorded) == sorted((at, host.stream) for at in own)
+
+
+@pytest.mark.parametrize("which", range(5))
+@pytest.mark.parametrize("others", [False, True])
+def test_a_forward_mode_derivative_is_not_dropped(host, which, others):
+    """Of any of the arguments, where no backward pass comes and where one does."""
+    from torch.autograd import forward_ad
+
+    X, W, A, B, ids = layer()
+    if others:
+        X.requires_grad_()
+    args = [X, W, A, B, torch.ones(L)]
+    with forward_ad.dual_level():
+        assert tg.linear_adapters(X, W, A, B, ids).shape == (T, N)  # none of them has one
+        args[which] = forward_ad.make_dual(args[which], torch.ones_like(args[which]))
+        calls = len(host.calls)
+        for autograd in (torch.enable_grad, torch.no_grad):
+            with autograd(), pytest.raises(NotImplementedError):
+                tg.linear_adapters(*args[:4], ids, scales=args[4])
+        assert len(host.calls) == calls
+    with pytest.raises((NotImplementedError, RuntimeError)):
+        torch.func.jvp(lambda t: tg.linear_adapters(*args[:which], t, *args[which + 1:4], ids, scales=None) if which < 4
+                       else tg.linear_adapters(*args[:4], ids, scales=t), (torch.ones_like(args[which]),), (torch.ones_like(args[which]),))

@@ -25,7 +25,7 @@ import functools
 
 from . import _lib
 from ._lib import TgemmError
-from .linear_loss import _floats, _ids, _ptr, _rows, _types
+from .linear_loss import _floats, _ids, _no_tangents, _ptr, _rows, _types
 
 
 def _stacked(t, name, shape, device, dtype):
@@ -238,9 +238,11 @@ def _function():
 
 def linear_adapters(X, W, A, B, ids, *, scales=None):
     """The projection X·Wᵀ with each token's adapter beside it, differentiable in X, W, A and B (in those of them that
-    require a gradient; scales gets none).  Without a gradient to compute it is linear_adapters_forward."""
+    require a gradient; scales gets none).  Without a gradient to compute it is linear_adapters_forward.  There is no
+    forward-mode derivative: arguments that carry one raise NotImplementedError."""
     import torch
 
+    _no_tangents("linear_adapters", X, W, A, B, scales)
     if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (X, W, A, B)):
         return _function().apply(X, W, A, B, ids, scales)
     return linear_adapters_forward(X, W, A, B, ids, scales=scales)
