@@ -86,3 +86,17 @@ def test_a_forward_mode_derivative_is_not_dropped(host, which, others):
     with pytest.raises((NotImplementedError, RuntimeError)):
         torch.func.jvp(lambda t: tg.linear_adapters(*args[:which], t, *args[which + 1:4], ids, scales=None) if which < 4
                        else tg.linear_adapters(*args[:4], ids, scales=t), (torch.ones_like(args[which]),), (torch.ones_like(args[which]),))
+
+
+@pytest.mark.parametrize("others", [False, True])
+def test_scales_that_require_a_gradient_are_refused(host, others):
+    X, W, A, B, ids = layer()
+    if others:
+        A.requires_grad_()
+    scales = torch.ones(L, requires_grad=True)
+    with pytest.raises(NotImplementedError, match="scales"):
+        tg.linear_adapters(X, W, A, B, ids, scales=scales)
+    assert not host.calls
+    assert tg.linear_adapters(X, W, A, B, ids, scales=scales.detach()).requires_grad == others
+    with torch.no_grad():
+        assert not tg.linear_adapters(X, W, A, B, ids, scales=scales).requires_grad

@@ -238,11 +238,14 @@ def _function():
 
 def linear_adapters(X, W, A, B, ids, *, scales=None):
     """The projection X·Wᵀ with each token's adapter beside it, differentiable in X, W, A and B (in those of them that
-    require a gradient; scales gets none).  Without a gradient to compute it is linear_adapters_forward.  There is no
-    forward-mode derivative: arguments that carry one raise NotImplementedError."""
+    require a gradient).  Without a gradient to compute it is linear_adapters_forward.  There is no gradient of scales
+    and no forward-mode derivative: where autograd would want either, NotImplementedError is raised."""
     import torch
 
     _no_tangents("linear_adapters", X, W, A, B, scales)
-    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in (X, W, A, B)):
-        return _function().apply(X, W, A, B, ids, scales)
+    if torch.is_grad_enabled():
+        if isinstance(scales, torch.Tensor) and scales.requires_grad:
+            raise NotImplementedError("linear_adapters has no gradient of scales: pass scales.detach()")
+        if any(isinstance(t, torch.Tensor) and t.requires_grad for t in (X, W, A, B)):
+            return _function().apply(X, W, A, B, ids, scales)
     return linear_adapters_forward(X, W, A, B, ids, scales=scales)
