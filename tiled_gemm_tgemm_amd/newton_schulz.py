@@ -14,7 +14,7 @@ import functools
 
 from . import _lib
 from ._lib import TgemmError
-from .linear_loss import _types
+from .linear_loss import _no_tangents, _types
 
 MUON = (3.4445, -4.7750, 2.0315)
 
@@ -45,13 +45,43 @@ def _stack(t, name):
     return batch, rows, cols, ld, t.stride(0) if batch > 1 and t.numel() else 0
 
 
+@functools.lru_cache(maxsize=None)
+def _function():
+    """The call as a node of a graph, which no backward pass gets through."""
+    import torch
+
+    class Orthogonalize(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, G, options):
+            return _run(G, **options)
+
+        @staticmethod
+        def backward(ctx, grad):
+            raise NotImplementedError("orthogonalize has no derivative: call it on G.detach() or under torch.no_grad()")
+
+    return Orthogonalize
+
+
 def orthogonalize(G, *, steps=5, coefficients=MUON, eps=1e-7, out=None, workspace=None, stream=None):
     """X_steps of X_0 = G / (|G| + eps) and X <- a·X + (b·S + c·S·S)·X with S = X·Xᵀ (of the transpose where G has more
     rows than columns): G with its singular values brought near 1 (tgemm_orthogonalize).  G: a row-major matrix or a
     stack of them (3-D), float32, bfloat16 or float16; the result has its type.  coefficients: (a, b, c), or a row of
     three for each step.  out: a tensor like G to write to, not G itself; workspace: a CUDA uint8 tensor of at least
     tgemm_orthogonalize_workspace_size bytes (allocated if omitted; two calls in flight at once need two).  Not
-    differentiable."""
+    differentiable: a backward pass through the result raises NotImplementedError."""
+    import torch
+
+    options = dict(steps=steps, coefficients=coefficients, eps=eps, out=out, workspace=workspace, stream=stream)
+    _no_tangents("orthogonalize", G)
+    if torch.is_grad_enabled() and isinstance(G, torch.Tensor) and G.requires_grad:
+        if out is not None:
+            raise RuntimeError("orthogonalize has no derivative, so a G that requires a gradient is not written to out: "
+                               "call it on G.detach() or under torch.no_grad()")
+        return _function().apply(G, options)
+    return _run(G, **options)
+
+
+def _run(G, *, steps, coefficients, eps, out, workspace, stream):
     import torch
 
     batch, rows, cols, ldg, stride_g = _stack(G, "G")
