@@ -19,9 +19,18 @@ from .linear_loss import _no_tangents, _types
 MUON = (3.4445, -4.7750, 2.0315)
 
 
+def _floats_of(v):
+    """A number as a float, rows of them as tuples: what is kept by its values, whatever they come in."""
+    if type(v) is tuple and set(map(type, v)) == {float}:
+        return v
+    if hasattr(v, "__iter__") and getattr(v, "ndim", 1) and not isinstance(v, str):  # (an array of no dimension is a number)
+        return tuple(_floats_of(e) for e in v)
+    return float(v)
+
+
 @functools.lru_cache(maxsize=64)
 def _coefficients(coefficients, steps):
-    """3·steps floats, and how many steps."""
+    """3·steps floats; coefficients: floats, or tuples of them."""
     rows = coefficients if coefficients and isinstance(coefficients[0], tuple) else (coefficients,) * steps
     if len(rows) != steps or any(not isinstance(r, tuple) or len(r) != 3 for r in rows):
         raise ValueError("coefficients must be three numbers, or as many rows of three as there are steps")
@@ -88,9 +97,7 @@ def _run(G, *, steps, coefficients, eps, out, workspace, stream):
     steps = int(steps)
     if steps < 1:
         raise ValueError("steps must be at least 1")
-    if not isinstance(coefficients, tuple):
-        coefficients = tuple(tuple(c) if hasattr(c, "__iter__") else float(c) for c in coefficients)
-    numbers = _coefficients(coefficients, steps)
+    numbers = _coefficients(_floats_of(coefficients), steps)
     device, made = G.device, []
     if out is None:
         out = torch.empty(G.shape, dtype=G.dtype, device=device)
