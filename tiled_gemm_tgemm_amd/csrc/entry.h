@@ -40,6 +40,13 @@ inline bool at(const void *p, int64_t rows, int64_t cols, int64_t ld, size_t siz
 
 inline bool apart(const Range &a, const Range &b) { return a.lo >= b.hi || b.lo >= a.hi; }
 
+// `count` matrices of `rows` rows of `cols` elements, the rows ld and the matrices
+// `stride` apart, that share none: one after another, or side by side.
+inline bool separate(int64_t count, int64_t rows, int64_t cols, int64_t ld, int64_t stride)
+{
+    return count < 2 || stride >= (rows - 1) * ld + cols || (stride >= cols && ld >= (count - 1) * stride + cols);
+}
+
 // What is written overlaps nothing else.
 inline bool disjoint(const Range *written, int n_written, const Range *read, int n_read)
 {

@@ -628,8 +628,8 @@ tgemm_status_t tgemm_linear_adapters_backward(tgemm_dtype_t dtype, int64_t T, in
     Range r[kRead + 2], w[5];
     if (!there(l, r) || !at(hidden, hidden ? T : 0, rank, rank, 4, r[kRead]) || !at(dY, T, N, lddy, size, r[kRead + 1]) ||
         !at(dX, dX ? T : 0, D, lddx, size, w[0]) || !at(dW, dW ? N : 0, D, lddw, size, w[1]) ||
-        (dA && count > 1 && stride_da < span_a) || !at(dA, dA ? count : 0, span_a, stride_da, size, w[2]) ||
-        (dB && count > 1 && stride_db < span_b) || !at(dB, dB ? count : 0, span_b, stride_db, size, w[3]) ||
+        (dA && !separate(count, rank, D, ldda, stride_da)) || !at(dA, dA ? count : 0, span_a, stride_da, size, w[2]) ||
+        (dB && !separate(count, N, rank, lddb, stride_db)) || !at(dB, dB ? count : 0, span_b, stride_db, size, w[3]) ||
         !room_at(workspace, workspace_bytes, p.total, w[4]) || !disjoint(w, 5, r, kRead + 2))
         return TGEMM_ERROR_INVALID_VALUE;
     const Gradients g{need.x ? dX : nullptr, lddx, dW, lddw, dA, ldda, stride_da, dB, lddb, stride_db};

@@ -370,7 +370,7 @@ tgemm_status_t tgemm_orthogonalize(tgemm_dtype_t dtype, int64_t batch, int64_t M
     // a matrix's elements, from its first to its last
     const int64_t span_g = (M - 1) * ldg + N, span_out = (M - 1) * ldo + N;
     Range r[1], w[2];
-    if ((batch > 1 && stride_out < span_out) || !at(G, batch, span_g, stride_g, size_of(dtype), r[0]) ||
+    if (!separate(batch, M, N, ldo, stride_out) || !at(G, batch, span_g, stride_g, size_of(dtype), r[0]) ||
         !at(out, batch, span_out, stride_out, size_of(dtype), w[0]) || !room_at(workspace, workspace_bytes, p.total, w[1]) ||
         !disjoint(w, 2, r, 1))
         return TGEMM_ERROR_INVALID_VALUE;
