@@ -100,3 +100,15 @@ def test_scales_that_require_a_gradient_are_refused(host, others):
     assert tg.linear_adapters(X, W, A, B, ids, scales=scales.detach()).requires_grad == others
     with torch.no_grad():
         assert not tg.linear_adapters(X, W, A, B, ids, scales=scales).requires_grad
+
+
+@pytest.mark.parametrize("change", [lambda t: t[:2], lambda t: t.double(), lambda t: t.repeat_interleave(2)[::2]])
+def test_saved_ids_and_scales_that_changed_are_refused(host, change):
+    """As hooks may hand them back: the kernels would read past their ends, or other values."""
+    X, W, A, B, ids = layer()
+    for which in (torch.int64, torch.float32):
+        with torch.autograd.graph.saved_tensors_hooks(lambda t: t, lambda t: change(t.detach()) if t.dim() == 1 and t.dtype == which else t):
+            Y = tg.linear_adapters(X, W, A.requires_grad_(), B.requires_grad_(), ids, scales=torch.ones(L))
+        with pytest.raises((TypeError, ValueError)):
+            torch.autograd.grad(Y, (A, B), torch.ones(T, N))
+    assert all(name.endswith("forward") for name, _ in host.calls)

@@ -96,6 +96,10 @@ class _Call:
             for t in kept:
                 if t is not None:
                     t.record_stream(current)
+        if not _ids(ids, "ids", (c.T,), c.device).is_contiguous():
+            raise ValueError("ids must be contiguous")
+        if scales is not None:
+            _floats(scales, "scales", (c.L,), c.device)
         ldx = _rows(X, "X", (c.T, c.D), c.device, c.dtype)
         c.head = (*c.head[:4], X.data_ptr(), ldx, W.data_ptr(), _rows(W, "W", (c.N, c.D), c.device, c.dtype))
         c.adapters = (c.L, c.r, A.data_ptr(), *_stacked(A, "A", (c.L, c.r, c.D), c.device, c.dtype), B.data_ptr(),
