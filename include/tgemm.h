@@ -592,9 +592,13 @@ size_t tgemm_linear_adapters_workspace_size(tgemm_dtype_t dtype, int64_t T, int6
  *             TGEMM_ERROR_NOT_SUPPORTED.  Nothing is written if batch, M or N
  *             is 0.
  * Workspace   Device memory of the caller, 16-byte aligned, at least
- *             tgemm_orthogonalize_workspace_size(...) bytes (up to 64 on the
- *             smaller side little, otherwise about 16·M·N + 8·min(M,N)² a matrix
- *             with M and N in whole 64s), overlapping neither G nor out.  Its contents on entry do not matter.
+ *             tgemm_orthogonalize_workspace_size(...) bytes, overlapping
+ *             neither G nor out: up to 64 on the smaller side little, otherwise
+ *             about 8·M·N + 8·min(M,N)² a matrix with M and N in whole 64s
+ *             (4·M·N for a single step) and, for the whole call, the parts of
+ *             sums that are split, which that function alone tells (up to 4 MB
+ *             for a matrix of 300×1000, 0.1 GB for many large ones).  Its
+ *             contents on entry do not matter.
  *             Two calls in flight at once need two.
  * Errors      As above, before anything is queued; also
  *             TGEMM_ERROR_INVALID_VALUE for an eps that is negative or not
