@@ -53,3 +53,17 @@ def test_the_same_bits_from_any_workspace(shape, dtype, coefficients):
         room = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
         assert torch.equal(first, tg.orthogonalize(G, workspace=room, **k))
     assert first.isfinite().all() and error(first, chain(G, **k)) < 0.02
+
+
+@pytest.mark.parametrize("dtype", TYPES[:2])
+@pytest.mark.parametrize("sizes", [(600, 256, 192, 1000, 4, 16), (1300, 200, 264, 777, 2, 80)])
+def test_updates_of_the_gradients_of_a_step(sizes, dtype):
+    """Through a projection with adapters and an output head's loss: no further off than their rounding either."""
+    from test_gpu_adapter_training import model, step
+
+    args = model(*sizes, dtype, 65)
+    args[2].requires_grad_(), args[3].requires_grad_()
+    _, dA, dB, uA, uB = step(*args)
+    for grad, got in ((dA, uA), (dB, uB)):
+        updates.check(grad)
+        assert torch.equal(got, tg.orthogonalize(grad))

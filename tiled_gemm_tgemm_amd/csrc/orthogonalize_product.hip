@@ -20,7 +20,7 @@ typedef _Float16 f16x8_anywhere __attribute__((ext_vector_type(8), aligned(2)));
 
 // Bound by the matrix cores where sums are long (Q·X of 8192×8192 in three
 // products of planes 2440 µs, 1.35 PFLOP/s), otherwise by the planes' way in
-// the epilogue besides (of 8×1024×4096 178, 0.87 PFLOP/s; 268 MB).  S and Q are
+// the epilogue besides (of 8×1024×4096 193, 1.07 PFLOP/s; 268 MB).  S and Q are
 // symmetric: where that takes fewer rounds, only the tiles on and below the
 // diagonal are formed and each is stored a second time across it.
 template <int BM, int BN, int WM, int WN, bool A_MC, bool B_MC>
