@@ -98,14 +98,21 @@ def _floats(t, name, shape, device):
     return t
 
 
-def _no_tangents(name, *tensors):
-    """Refuses tensors with a forward-mode derivative, which a call around torch's autograd would drop."""
-    import torch
+@functools.lru_cache(maxsize=None)
+def _forward_ad():
     from torch.autograd import forward_ad
 
+    return forward_ad
+
+
+def _no_tangents(name, *tensors):
+    """Refuses tensors with a forward-mode derivative, which a call around torch's autograd would drop."""
+    forward_ad = _forward_ad()
     # (outside every dual level, as nearly always, this costs a tenth of what asking five tensors does)
     if getattr(forward_ad, "_current_level", 0) < 0:
         return
+    import torch
+
     if any(isinstance(t, torch.Tensor) and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
         raise NotImplementedError(f"{name} has no forward-mode derivative")
 

@@ -61,8 +61,8 @@ def _function():
 
     class Orthogonalize(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, G, options):
-            return _run(G, **options)
+        def forward(ctx, G, steps, coefficients, eps, workspace, stream):
+            return _run(G, steps, coefficients, eps, None, workspace, stream)
 
         @staticmethod
         def backward(ctx, grad):
@@ -80,17 +80,16 @@ def orthogonalize(G, *, steps=5, coefficients=MUON, eps=1e-7, out=None, workspac
     differentiable: a backward pass through the result raises NotImplementedError."""
     import torch
 
-    options = dict(steps=steps, coefficients=coefficients, eps=eps, out=out, workspace=workspace, stream=stream)
     _no_tangents("orthogonalize", G)
     if torch.is_grad_enabled() and isinstance(G, torch.Tensor) and G.requires_grad:
         if out is not None:
             raise RuntimeError("orthogonalize has no derivative, so a G that requires a gradient is not written to out: "
                                "call it on G.detach() or under torch.no_grad()")
-        return _function().apply(G, options)
-    return _run(G, **options)
+        return _function().apply(G, steps, coefficients, eps, workspace, stream)
+    return _run(G, steps, coefficients, eps, out, workspace, stream)
 
 
-def _run(G, *, steps, coefficients, eps, out, workspace, stream):
+def _run(G, steps, coefficients, eps, out, workspace, stream):
     import torch
 
     batch, rows, cols, ldg, stride_g = _stack(G, "G")
